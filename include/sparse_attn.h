@@ -399,6 +399,164 @@ sa_status sparse_attn_kv_window_append(int32_t BH, int32_t d, int32_t chunk_toke
                                        const void* new_k, const void* new_v,
                                        int64_t* valid_tokens, sa_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the attention path: rotary positions, attention with
+ * masks / capped scores / a distance bias, and a cache that evicts by
+ * accumulated attention weight.  One step of a rolling cache is
+ *   rope (Q, K) -> K, V into the cache -> forward_masked (o, lse)
+ *   -> cache_weights -> cache_evict.
+ * The pages name the parts (DiT page, "The Architecture": 3-D rotary
+ * positions of Q and K ahead of the cache; frames generated causally over a
+ * rolling window); the formulas are written out here.
+ *
+ * Tensors of these calls are views [B, H, N, d] with element strides and a
+ * contiguous d: every row starts on 16 bytes, so [B, N, H, d] storage or a
+ * slice of a cache needs no copy.  The stride of a dimension of size 1 is
+ * free.  An output's rows must not overlap; an input may repeat a dimension
+ * (stride 0) where its line says so.
+ */
+typedef struct {
+  int64_t b, h, n; /* elements between batch entries, heads, tokens */
+} sa_strides;
+
+#define SA_ROPE_INTERLEAVED 0 /* pair i is elements (2i, 2i + 1) */
+#define SA_ROPE_HALF 1        /* pair i is elements (i, i + r/2) of the r rotated ones */
+
+/*
+ * Rotary positions along up to three axes (time, height, width).  The first
+ * r = sum of axis_dim elements of a row are r/2 pairs; the first axis_dim[0]/2
+ * pairs belong to axis 0, and so on; the other elements pass unchanged.  Pair
+ * number i of axis a turns by t = p_a * f, f = theta^(-2i / axis_dim[a]) (or
+ * inv_freq, over all pairs):
+ *   (x, y) -> (x cos t - y sin t, x sin t + y cos t);  inverse: by -t, which is
+ * also the gradient.  Angles are exact to 2^-24 of a half turn at every
+ * 32-bit position.
+ */
+typedef struct {
+  int32_t B, N, d;
+  int32_t axes;              /* 1 .. 3 */
+  int32_t axis_dim[3];       /* even, sum <= d; SA_ROPE_HALF: the sum a multiple of 16 */
+  int32_t pairing;
+  int32_t dtype;             /* SA_OUT_BF16 or SA_OUT_FP32, of every tensor */
+  int32_t inverse;
+  double theta;              /* > 0; ignored with inv_freq */
+  const double* inv_freq;    /* host, r/2 values, or NULL */
+  const int32_t* positions;  /* device int32 [B, N, axes], or NULL: the grid */
+  int64_t positions_b;       /* elements between batch entries (0: shared by all) */
+  sa_voxel_grid grid;        /* positions NULL: token n's (t, h, w), axes = 3, T*Hh*W = N */
+  int32_t voxel_order;       /* 0: raster order, 1: the order of sparse_attn_voxel_permute */
+  int64_t offset[3];         /* added to the grid's positions (frames generated so far, ...) */
+} sa_rope;
+
+/*
+ * Rotates x0 (H0 heads) into y0 and, when H1 > 0, x1 (H1 heads) into y1 with
+ * the same positions (queries and keys of a layer in one launch).  y may be
+ * the same view as its x (in place); otherwise they must not overlap.  Views
+ * of the two pairs may interleave in one buffer but must not share elements.
+ * Inputs may repeat a dimension.
+ */
+sa_status sparse_attn_rope(const sa_rope* rope, int32_t H0, const void* x0, const sa_strides* x0_strides,
+                           void* y0, const sa_strides* y0_strides, int32_t H1, const void* x1,
+                           const sa_strides* x1_strides, void* y1, const sa_strides* y1_strides,
+                           sa_stream_t stream);
+
+/*
+ * Attention with masks, capped scores and a distance bias.  Hq query heads
+ * share Hkv key heads (Hq a multiple of Hkv; query head h reads key head
+ * h / (Hq/Hkv)).  For a query row at position p and a key at position c of its
+ * document
+ *   s = cap tanh(scale q.k / cap) - slopes[h] |p - c|
+ * (cap 0: scale q.k; slopes NULL: no bias), o = softmax(s) v over the keys
+ * the row sees, lse = ln of the sum of e^s over them.  A row that sees none
+ * gets o = 0, lse = -inf.
+ *
+ *  - Documents: with ndocs > 0, document e of batch entry b is query rows
+ *    docs_q[b][e] .. docs_q[b][e+1] - 1 and keys docs_k[b][e] ..
+ *    docs_k[b][e+1] - 1 (tables [B, ndocs + 1], non-decreasing, values up to
+ *    Nq and Nk; empty documents are fine); rows of no document see nothing.
+ *    With ndocs = 0 a batch entry is one document, its keys the first
+ *    lengths[b] (NULL: all Nk).  Tables are clamped to the tensors: whatever
+ *    they hold, nothing outside is read.
+ *  - Positions: key c of a document has position c; the document's query rows
+ *    are its last positions (a new token over a cache: lengths = tokens so
+ *    far, Nq = 1).
+ *  - causal = F > 0: a row sees the keys up to the end of its own frame of F
+ *    tokens (1: token-causal); F = 0: all keys of its document.
+ *  - prefix [B, ndocs] (nullable, needs ndocs > 0): the document's first
+ *    prefix keys are seen by all its rows.
+ *
+ * q, k, v bf16; o bf16 or fp32 by out_dtype; P is rounded to bf16 for the
+ * second product (o is normalised by the sum of the rounded values), all sums
+ * are fp32.  q may repeat a dimension.  Keys and values past a row's document
+ * never reach it, whatever they hold; a NaN or an infinite V row inside the
+ * document may reach other rows of the same document that do not see it.
+ * Few rows split the keys over the GPU: the workspace (256-byte aligned, may
+ * be NULL when its size is 0) holds the partial results, and two calls that
+ * may overlap on the GPU need two workspaces.
+ */
+typedef struct {
+  int32_t B, Hq, Hkv, Nq, Nk, d;  /* d in {64, 128}; Nq, Nk <= 2^30 */
+  float scale;                    /* finite, not 0 */
+  int32_t out_dtype;              /* of o (sparse_attn_forward_masked) */
+  sa_strides q, k, v, o;          /* v and o: sparse_attn_forward_masked only */
+  float cap;                      /* >= 0 */
+  const float* slopes;            /* device fp32 [Hq] or NULL */
+  int32_t causal;
+  int32_t ndocs;
+  const int32_t* docs_q;          /* device */
+  const int32_t* docs_k;
+  const int32_t* prefix;
+  const int32_t* lengths;         /* device [B]; NULL with ndocs > 0 */
+} sa_masked;
+
+size_t sparse_attn_forward_masked_workspace_size(const sa_masked* problem);
+
+/* lse (fp32 [B, Hq, Nq]) and dev_status are nullable. */
+sa_status sparse_attn_forward_masked(const sa_masked* problem, const void* q, const void* k, const void* v,
+                                     void* o, float* lse, int32_t* dev_status, void* workspace,
+                                     size_t workspace_bytes, sa_stream_t stream);
+
+/*
+ * The attention weight every cached key received:
+ *   w_out[b][hk][j] = decay w_in[b][hk][j] + sum over the query heads of hk and
+ *   the rows i that see j of exp(s_ij - lse_i),
+ * s as above and lse as sparse_attn_forward_masked (or the dense
+ * sparse_attn_forward) wrote it for the same q and k; rows without a finite
+ * lse add nothing.  Entries at and past lengths[b] stay as they were (they are
+ * copied when w_out is another buffer).  Sums have a fixed order: the same
+ * inputs give the same bits.
+ *   lse    fp32 [B, Hq, Nq];  w_in, w_out  fp32 [B, Hkv, Nk], the same buffer
+ *          or apart; w_in may be NULL when decay = 0 (then it is not read)
+ * Hq / Hkv <= 256.
+ */
+sa_status sparse_attn_cache_weights(const sa_masked* problem, const void* q, const void* k, const float* lse,
+                                    const float* w_in, float* w_out, float decay, int32_t* dev_status,
+                                    sa_stream_t stream);
+
+/*
+ * Eviction: of the n = lengths[b] (NULL: Nk) entries of a head keep the first
+ * `sink`, the last `recent` and, of those between, the ones of largest weight
+ * (ties: the lowest index; a NaN ranks below every number), min(n, budget) in
+ * all.
+ *   kept         int32 [B, Hkv, budget]: the kept entries, ascending; -1 behind them
+ *   k_out, v_out [B, Hkv, budget, d]: their rows in that order (rows behind
+ *                the last are left as they were); k, v, k_out, v_out are all
+ *                NULL to select only
+ *   weights_out  fp32 [B, Hkv, budget] (likewise), nullable
+ * No output may overlap an input.  sink + recent <= budget; B*Hkv <= 65535.
+ * k and v may repeat a dimension.
+ */
+typedef struct {
+  int32_t B, Hkv, Nk, d;
+  int32_t budget, sink, recent;
+  const int32_t* lengths;
+  sa_strides k, v, k_out, v_out;
+} sa_evict;
+
+sa_status sparse_attn_cache_evict(const sa_evict* problem, const float* weights, const void* k, const void* v,
+                                  int32_t* kept, void* k_out, void* v_out, float* weights_out,
+                                  sa_stream_t stream);
+
 /*
  * Checks index lists without trapping: row_ptr[0] == 0, row_ptr[rows] == nnz,
  * row_ptr non-decreasing, every index in [0, Nk) and strictly ascending

@@ -1,0 +1,208 @@
+"""GPU checks of the masked forward against the 64-bit form.
+
+Tolerances.  A score is off by at most e = d 2^-23 a (a: the largest scale * sum |q k| of the row's head, fp32
+accumulation of exact products) + 2^-20 cap + 2^-22 bias terms; P is rounded to bf16 (half a step, 2^-8) and O is
+normalised by the rounded sum, so
+    |o - want| <= (2^-8 + 2 e + 2^-16) 1.01 (sum p |v| + |want|) + the output's own rounding,
+    |lse - want| <= e + 2^-20 (1 + |want|)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_ops as O
+
+pytestmark = pytest.mark.gpu
+
+
+def tensors(B, H, Hk, Nq, Nk, d, seed=0, layout="bhnd", sigma=1.5):
+    g = torch.Generator().manual_seed(seed)
+
+    def t(h, n, s):
+        x = torch.randn((B, h, n, d) if layout == "bhnd" else (B, n, h, d), generator=g).mul(s).to(torch.bfloat16).cuda()
+        return x if layout == "bhnd" else x.transpose(1, 2)
+    return t(H, Nq, sigma), t(Hk, Nk, 1.0), t(Hk, Nk, 1.0)
+
+
+def check(o, lse, q, k, v, *, scale=None, cap=0.0, slopes=None, causal=0, docs_q=None, docs_k=None, prefix=None,
+          lengths=None):
+    B, H, Nq, d = q.shape
+    Hk, Nk = k.shape[1:3]
+    scale = d ** -0.5 if scale is None else scale
+    q, k, v = (x.double().cpu().numpy() for x in (q, k, v))
+    eps = torch.finfo(o.dtype).eps / 2
+    got, glse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    row = lambda t, b: None if t is None else np.atleast_2d(t)[b % np.atleast_2d(t).shape[0]]  # noqa: E731
+    for b in range(B):
+        see, dist = O.visible(Nq, Nk, causal, row(docs_q, b), row(docs_k, b), row(prefix, b),
+                              None if lengths is None else lengths[b])
+        for h in range(H):
+            hk = h // (H // Hk)
+            sl = 0.0 if slopes is None else float(slopes[h])
+            want, wlse, pv = O.attention(q[b, h], k[b, hk], v[b, hk], scale, see, cap=cap, slope=sl, dist=dist)
+            kk = np.where(see.any(0)[:, None], k[b, hk], 0.0)
+            a = abs(scale) * float((np.abs(q[b, h]) @ np.abs(kk).T).max(initial=0.0))
+            e = d * 2.0 ** -23 * a + 2.0 ** -20 * cap + 2.0 ** -22 * abs(sl) * float(dist.max(initial=0.0))
+            tol = (2.0 ** -8 + 2 * e + 2.0 ** -16) * 1.01 * (pv + np.abs(want)) + eps * np.abs(want)
+            err = np.abs(got[b, h] - want)
+            assert (err <= tol).all(), (b, h, float((err - tol).max()), np.argwhere(~(err <= tol))[:4])
+            none = np.isinf(wlse)
+            assert np.array_equal(glse[b, h] == -np.inf, none)
+            assert (got[b, h][none] == 0).all()
+            lerr = np.abs(glse[b, h][~none] - wlse[~none])
+            assert (lerr <= (e + 2.0 ** -20 * (1 + np.abs(wlse[~none])))).all(), float(lerr.max())
+
+
+def run(q, k, v, **kw):
+    from video_dit_sparse_gb300 import binding as sa
+    dev = dict(kw)
+    for n in ("docs_q", "docs_k", "prefix", "lengths"):
+        if dev.get(n) is not None:
+            dev[n] = torch.tensor(dev[n], dtype=torch.int32, device="cuda")
+    if dev.get("slopes") is not None:
+        dev["slopes"] = torch.tensor(dev["slopes"], dtype=torch.float32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, lse = sa.sparse_attn_forward_masked(q, k, v, status=status, **dev)
+    assert int(status) == 0
+    return o, lse
+
+
+# rows per key head under, at and over one tile; one key to several tiles; odd sizes
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hk,Nq,Nk", [(1, 1, 1, 1), (2, 2, 1, 129), (2, 1, 130, 128), (3, 1, 43, 257), (8, 1, 17, 640),
+                                        (2, 2, 300, 77), (6, 2, 100, 513), (1, 1, 515, 1000)])
+@pytest.mark.parametrize("causal", [0, 1, 97])
+def test_sizes(d, H, Hk, Nq, Nk, causal):
+    q, k, v = tensors(2, H, Hk, Nq, Nk, d, seed=Nq + Nk)
+    check(*run(q, k, v, causal=causal), q, k, v, causal=causal)
+
+
+@pytest.mark.parametrize("layout", ["bhnd", "bnhd"])
+@pytest.mark.parametrize("cap,bias", [(30.0, False), (0.0, True), (5.0, True)])
+@pytest.mark.parametrize("H,Hk,Nq,Nk", [(4, 2, 1, 700), (4, 2, 200, 333), (2, 2, 257, 257)])
+def test_cap_and_bias(layout, cap, bias, H, Hk, Nq, Nk):
+    q, k, v = tensors(2, H, Hk, Nq, Nk, 128, seed=3, layout=layout, sigma=4.0)
+    kw = dict(cap=cap, slopes=[2.0 ** -i for i in range(1, H + 1)] if bias else None, causal=1)
+    check(*run(q, k, v, out_dtype=torch.float32, **kw), q, k, v, **kw)
+
+
+DOCS = [
+    ([0, 100, 100, 101, 300], [0, 250, 260, 260, 400]),
+    ([5, 100, 290], [10, 10, 390]),      # rows and keys of no document, a document without keys
+    ([0, 0, 0, 300], [0, 7, 130, 400]),  # documents without rows
+    ([0, 300], [0, 0]),                  # nothing to see
+]
+
+
+@pytest.mark.parametrize("dq,dk", DOCS)
+@pytest.mark.parametrize("causal,prefix", [(0, None), (1, None), (1, 30), (97, 200)])
+def test_documents(dq, dk, causal, prefix):
+    q, k, v = tensors(1, 3, 1, 300, 400, 64, seed=7)
+    px = None if prefix is None else [prefix] * (len(dq) - 1)
+    kw = dict(docs_q=dq, docs_k=dk, prefix=px, causal=causal)
+    check(*run(q, k, v, **kw), q, k, v, **kw)
+
+
+def test_documents_of_each_batch_entry():
+    q, k, v = tensors(2, 2, 2, 90, 160, 128, seed=8)
+    kw = dict(docs_q=[[0, 30, 90], [0, 89, 90]], docs_k=[[0, 150, 160], [0, 1, 2]], prefix=[[3, 0], [1, 1]], causal=1)
+    check(*run(q, k, v, **kw), q, k, v, **kw)
+
+
+@pytest.mark.parametrize("Nq", [1, 3, 200])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_lengths_and_what_lies_behind_them(Nq, bad):
+    lengths = [0, 1, 127, 128, 300, 400]
+    q, k, v = tensors(6, 4, 2, Nq, 400, 128, seed=9)
+    for b, n in enumerate(lengths):
+        k[b, :, n:] = bad
+        v[b, :, n:] = bad
+    kw = dict(lengths=lengths, causal=1)
+    check(*run(q, k, v, **kw), q, k, v, **kw)
+    check(*run(q, k, v, lengths=lengths), q, k, v, lengths=lengths)
+
+
+def test_non_finite_rows_of_another_document_do_not_leak():
+    q, k, v = tensors(1, 1, 1, 256, 512, 64, seed=10)
+    kw = dict(docs_q=[0, 128, 256], docs_k=[0, 100, 512])
+    o, lse = run(q, k, v, **kw)
+    v[0, 0, 100:] = float("nan")
+    k[0, 0, 100:] = float("nan")
+    q[0, 0, 128:] = float("nan")
+    o2, lse2 = run(q[:, :, :128], k, v, docs_q=[0, 128], docs_k=[0, 100])
+    assert torch.equal(o2, o[:, :, :128]) or float((o2 - o[:, :, :128]).abs().max()) < 2.0 ** -7 * 4
+    assert bool(torch.isfinite(o2).all())
+
+
+def test_late_maximum_raises_the_reference():
+    q, k, v = tensors(1, 2, 2, 200, 640, 128, seed=11)
+    k[:, :, 500:] *= 12  # scores far above those of the first tiles
+    check(*run(q, k, v, out_dtype=torch.float32), q, k, v)
+    k[:, :, :130] *= 12
+    check(*run(q, k, v, causal=1, out_dtype=torch.float32), q, k, v, causal=1)
+
+
+def test_negative_scale_and_far_bias():
+    q, k, v = tensors(1, 2, 2, 140, 300, 64, seed=12)
+    check(*run(q, k, v, scale=-0.2), q, k, v, scale=-0.2)
+    kw = dict(slopes=[50.0, -0.05], causal=0)  # nearly one-hot rows; a bias that grows with distance
+    check(*run(q, k, v, **kw), q, k, v, **kw)
+
+
+def test_strided_views_and_out():
+    from video_dit_sparse_gb300 import binding as sa
+    buf = torch.randn(2, 70, 3, 4, 64, device="cuda").to(torch.bfloat16)
+    q, k, v = (buf[:, :, i].transpose(1, 2) for i in range(3))
+    out = torch.full((2, 70, 6, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    view = out[:, :, 1:5].transpose(1, 2)
+    o, lse = sa.sparse_attn_forward_masked(q, k, v, causal=1, out=view)
+    check(o, lse, q, k, v, causal=1)
+    assert bool((out[:, :, 0] == 9).all()) and bool((out[:, :, 5] == 9).all())
+    cache = torch.randn(2, 4, 500, 64, device="cuda").to(torch.bfloat16)
+    kc, vc = cache[:, :, 20:90], cache[:, :, 200:270]
+    check(*sa.sparse_attn_forward_masked(q, kc, vc), q, kc, vc)
+
+
+def test_matches_the_dense_forward():
+    from video_dit_sparse_gb300 import binding as sa
+    q, k, v = tensors(1, 2, 2, 384, 1000, 128, seed=13)
+    o, lse = sa.sparse_attn_forward_masked(q, k, v, out_dtype=torch.float32)
+    d, dl = sa.sparse_attn_forward(q, k, v, None, None, out_dtype=torch.float32)
+    assert float((o - d).abs().max()) <= 2.0 ** -7 * 4  # two roundings of P, values within 4 or so
+    assert float((lse - dl).abs().max()) <= 2.0 ** -18 * 16
+
+
+def test_streams_graphs_and_repeatability():
+    from video_dit_sparse_gb300 import binding as sa
+    q, k, v = tensors(2, 4, 2, 1, 3000, 128, seed=14)
+    kw = dict(causal=1, lengths=torch.tensor([2999, 1234], dtype=torch.int32, device="cuda"))
+    want, wl = sa.sparse_attn_forward_masked(q, k, v, **kw)
+    for _ in range(3):
+        o, l = sa.sparse_attn_forward_masked(q, k, v, **kw)
+        assert torch.equal(o, want) and torch.equal(l, wl)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    o, l = sa.sparse_attn_forward_masked(q, k, v, stream=s, **kw)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(o, want)
+    out, lse = torch.zeros_like(want), torch.zeros_like(wl)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sa.sparse_attn_forward_masked(q, k, v, out=out, lse=lse, **kw)
+    kw["lengths"].copy_(torch.tensor([5, 3000], dtype=torch.int32))  # a replay reads the tables anew
+    g.replay()
+    want, wl = sa.sparse_attn_forward_masked(q, k, v, **kw)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+def test_tables_that_point_outside_read_nothing_outside():
+    q, k, v = tensors(1, 2, 2, 150, 200, 64, seed=15)
+    big = 2 ** 31 - 1
+    for dq, dk in (([0, 150], [-5, 10 ** 6]), ([-10 ** 9, 10 ** 9], [-10 ** 9, 10 ** 9]), ([90, 10, 150], [150, 3, 77]),
+                   ([0, 70, 150], [big, -big, big])):
+        for causal in (0, 1, big):
+            o, lse = run(q, k, v, docs_q=dq, docs_k=dk, causal=causal, prefix=[big] * (len(dq) - 1))
+            assert bool(torch.isfinite(o).all())
+    o, lse = run(q, k, v, lengths=[10 ** 9])
+    check(o, lse, q, k, v)
+    o, lse = run(q, k, v, lengths=[-4])
+    assert bool((o == 0).all()) and bool((lse == -float("inf")).all())

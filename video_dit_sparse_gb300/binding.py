@@ -51,6 +51,41 @@ class sa_voxel_grid(ctypes.Structure):
                 ("vt", ctypes.c_int32), ("vh", ctypes.c_int32), ("vw", ctypes.c_int32)]
 
 
+class sa_strides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("n", ctypes.c_int64)]
+
+
+SA_ROPE_INTERLEAVED, SA_ROPE_HALF = 0, 1
+_PAIRINGS = {"interleaved": SA_ROPE_INTERLEAVED, "half": SA_ROPE_HALF}
+
+
+class sa_rope(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("axis_dim", ctypes.c_int32 * 3),
+                ("pairing", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("theta", ctypes.c_double),
+                ("inv_freq", ctypes.POINTER(ctypes.c_double)), ("positions", ctypes.c_void_p),
+                ("positions_b", ctypes.c_int64), ("grid", sa_voxel_grid),
+                ("voxel_order", ctypes.c_int32), ("offset", ctypes.c_int64 * 3)]
+
+
+class sa_masked(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("Nq", ctypes.c_int32), ("Nk", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("out_dtype", ctypes.c_int32), ("q", sa_strides),
+                ("k", sa_strides), ("v", sa_strides), ("o", sa_strides), ("cap", ctypes.c_float),
+                ("slopes", ctypes.c_void_p), ("causal", ctypes.c_int32), ("ndocs", ctypes.c_int32),
+                ("docs_q", ctypes.c_void_p), ("docs_k", ctypes.c_void_p),
+                ("prefix", ctypes.c_void_p), ("lengths", ctypes.c_void_p)]
+
+
+class sa_evict(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("Nk", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("budget", ctypes.c_int32), ("sink", ctypes.c_int32),
+                ("recent", ctypes.c_int32), ("lengths", ctypes.c_void_p), ("k", sa_strides),
+                ("v", sa_strides), ("k_out", sa_strides), ("v_out", sa_strides)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -88,6 +123,19 @@ def _load():
                                                  ctypes.c_int32, i64, vp, vp, vp, vp,
                                                  P(ctypes.c_int64), vp]
     lib.sparse_attn_kv_window_append.restype = ctypes.c_int
+    ps = P(sa_strides)
+    lib.sparse_attn_rope.argtypes = [P(sa_rope), ctypes.c_int32, vp, ps, vp, ps, ctypes.c_int32, vp,
+                                     ps, vp, ps, vp]
+    lib.sparse_attn_rope.restype = ctypes.c_int
+    lib.sparse_attn_forward_masked_workspace_size.argtypes = [P(sa_masked)]
+    lib.sparse_attn_forward_masked_workspace_size.restype = ctypes.c_size_t
+    lib.sparse_attn_forward_masked.argtypes = [P(sa_masked), vp, vp, vp, vp, vp, vp, vp,
+                                               ctypes.c_size_t, vp]
+    lib.sparse_attn_forward_masked.restype = ctypes.c_int
+    lib.sparse_attn_cache_weights.argtypes = [P(sa_masked), vp, vp, vp, vp, vp, ctypes.c_float, vp, vp]
+    lib.sparse_attn_cache_weights.restype = ctypes.c_int
+    lib.sparse_attn_cache_evict.argtypes = [P(sa_evict), vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.sparse_attn_cache_evict.restype = ctypes.c_int
     lib.sparse_attn_validate_index.argtypes = [P(sa_problem), vp, vp, i64, vp, vp]
     lib.sparse_attn_validate_index.restype = ctypes.c_int
     lib.sparse_attn_status_string.argtypes = [ctypes.c_int]
@@ -381,6 +429,292 @@ def sparse_attn_kv_window_append(cache_k: torch.Tensor, cache_v: torch.Tensor,
     return int(valid.value)
 
 
+# ------------------------------------------------ operators around the attention path
+
+def _view(t: torch.Tensor, dtype, name: str, ref: torch.Tensor | None = None) -> sa_strides:
+    """A [B, H, N, d] view with a contiguous d: its strides."""
+    if not t.is_cuda or t.dtype != dtype or t.dim() != 4:
+        raise ValueError(f"{name} must be a CUDA tensor [B, H, N, d] of {dtype}")
+    if ref is not None and t.device != ref.device:
+        raise ValueError(f"{name} must be on {ref.device}")
+    sb, sh, sn, sd = t.stride()
+    if sd != 1 and t.shape[3] != 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    return sa_strides(sb, sh, sn)
+
+
+def _flat(t, dtype, name, ref, shape=None):
+    """A contiguous tensor on ref's device (or None), its pointer."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != ref.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {dtype} on {ref.device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+class _On:
+    """The tensor's device made current for a call, and the call's stream; tensors made for a call
+    on another stream than the current one are recorded there."""
+
+    def __init__(self, ref, stream):
+        self.guard = None
+        if ref.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(ref.device)
+        self.stream = stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        cur = torch.cuda.current_stream()
+        self.other = self.stream if self.stream is not None and self.stream != cur else None
+        return (self.stream or cur).cuda_stream
+
+    def keep(self, *tensors):
+        if self.other is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.other)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def sparse_attn_rope(q: torch.Tensor, k: torch.Tensor | None = None, *, axes=(44, 42, 42),
+                     theta: float = 10000.0, inv_freq=None, pairing: str = "interleaved",
+                     grid=None, voxel=None, offset=(0, 0, 0), positions: torch.Tensor | None = None,
+                     inverse: bool = False, out=None, stream=None):
+    """Rotary positions along up to three axes of q (and k, in the same launch): [B, H, N, d] bf16
+    or fp32 views; returns the rotated q, or (q, k) when k is given.
+
+    axes: rotated elements per axis.  positions int32 [N, A] or [B, N, A]; or grid (T, H, W) with
+    N = T*H*W, tokens in raster order, or in sparse_attn_voxel_permute's when `voxel` is given, plus
+    `offset`.  inv_freq: r/2 frequencies (radians per position) instead of theta's.  inverse rotates
+    back, which is also the gradient.  out: the output (or a pair of them); it may be the input."""
+    dtype = q.dtype
+    if dtype not in _OUT:
+        raise ValueError("q must be bfloat16 or float32")
+    qs = _view(q, dtype, "q")
+    B, H, N, d = q.shape
+    oq, ok = out if isinstance(out, (tuple, list)) else (out, None)
+    if k is not None:
+        ks = _view(k, dtype, "k", q)
+        if k.shape[0] != B or k.shape[2] != N or k.shape[3] != d:
+            raise ValueError("k must be [B, Hk, N, d] with q's B, N and d")
+    elif ok is not None:
+        raise ValueError("an output for k without k")
+    axes = tuple(int(a) for a in axes)
+    if not 1 <= len(axes) <= 3:
+        raise ValueError("one to three axes")
+    if pairing not in _PAIRINGS:
+        raise ValueError("pairing must be 'interleaved' or 'half'")
+    r = sa_rope(B, N, d, len(axes))
+    for i, a in enumerate(axes):
+        r.axis_dim[i] = a
+    r.pairing, r.dtype, r.inverse, r.theta = _PAIRINGS[pairing], _OUT[dtype], int(inverse), float(theta)
+    if inv_freq is not None:
+        f = [float(x) for x in inv_freq]
+        if len(f) != sum(axes) // 2:
+            raise ValueError("inv_freq must have one value per rotated pair")
+        r.inv_freq = (ctypes.c_double * len(f))(*f)
+    if (positions is None) == (grid is None):
+        raise ValueError("positions or grid, and not both")
+    if positions is not None:
+        if voxel is not None or any(offset):
+            raise ValueError("voxel and offset go with grid")
+        shared = positions.dim() == 2
+        r.positions = _flat(positions, torch.int32, "positions", q,
+                            (N, len(axes)) if shared else (B, N, len(axes)))
+        r.positions_b = 0 if shared else N * len(axes)
+    else:
+        r.grid = sa_voxel_grid(*grid, *(voxel if voxel is not None else (0, 0, 0)))
+        r.voxel_order = 0 if voxel is None else 1
+        for i in range(3):
+            r.offset[i] = int(offset[i])
+    on = _On(q, stream)
+    with on as s:
+        y = torch.empty_like(q) if oq is None else oq
+        ys = _view(y, dtype, "out", q)
+        if y.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        z = zs = None
+        if k is not None:
+            z = torch.empty_like(k) if ok is None else ok
+            zs = _view(z, dtype, "out of k", q)
+            if z.shape != k.shape:
+                raise ValueError("out of k must have k's shape")
+        on.keep(y, z)
+        st = lib.sparse_attn_rope(r, H, q.data_ptr(), qs, y.data_ptr(), ys,
+                                  0 if k is None else k.shape[1], _ptr(k), None if k is None else ks,
+                                  _ptr(z), zs, s)
+    if st != SA_OK:
+        raise SparseAttnError(st, "sparse_attn_rope")
+    return y if k is None else (y, z)
+
+
+def _masked(q, k, scale, cap, slopes, causal, docs_q, docs_k, prefix, lengths):
+    """sa_masked of q [B, Hq, Nq, d] and k [B, Hkv, Nk, d], without v and o."""
+    qs, ks = _view(q, torch.bfloat16, "q"), _view(k, torch.bfloat16, "k", q)
+    B, H, Nq, d = q.shape
+    Hk, Nk = k.shape[1], k.shape[2]
+    if k.shape[0] != B or k.shape[3] != d or not Hk or H % Hk:
+        raise ValueError("k must be [B, Hk, Nk, d] with q's B and d, and H a multiple of Hk")
+    p = sa_masked(B, H, Hk, Nq, Nk, d, 1.0 / math.sqrt(d) if scale is None else scale)
+    p.q, p.k, p.cap, p.causal = qs, ks, float(cap), int(causal)
+    p.slopes = _flat(slopes, torch.float32, "slopes", q, (H,))
+    if (docs_q is None) != (docs_k is None) or (prefix is not None and docs_q is None):
+        raise ValueError("docs_q and docs_k come together, prefix with them")
+    keep = None
+    if docs_q is not None:
+        n = docs_q.shape[-1] - 1
+        if n < 1:
+            raise ValueError("docs_q must hold the bounds of at least one document")
+        if docs_q.dim() == 1:
+            docs_q, docs_k = (t.expand(B, n + 1).contiguous() for t in (docs_q, docs_k))
+            prefix = None if prefix is None else prefix.expand(B, n).contiguous()
+        p.ndocs = n
+        p.docs_q = _flat(docs_q, torch.int32, "docs_q", q, (B, n + 1))
+        p.docs_k = _flat(docs_k, torch.int32, "docs_k", q, (B, n + 1))
+        p.prefix = _flat(prefix, torch.int32, "prefix", q, (B, n))
+        keep = (docs_q, docs_k, prefix)
+    p.lengths = _flat(lengths, torch.int32, "lengths", q, (B,))
+    return p, keep
+
+
+def sparse_attn_forward_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
+                               scale: float | None = None, cap: float = 0.0,
+                               slopes: torch.Tensor | None = None, causal: int = 0,
+                               docs_q: torch.Tensor | None = None,
+                               docs_k: torch.Tensor | None = None,
+                               prefix: torch.Tensor | None = None,
+                               lengths: torch.Tensor | None = None,
+                               out: torch.Tensor | None = None, out_dtype=torch.bfloat16,
+                               lse: torch.Tensor | bool = True,
+                               workspace: torch.Tensor | None = None,
+                               status: torch.Tensor | None = None, stream=None):
+    """Attention with masks, capped scores and a distance bias; bf16 views q [B, H, Nq, d],
+    k and v [B, Hk, Nk, d] (H a multiple of Hk).  Returns (o [B, H, Nq, d], lse fp32 [B, H, Nq] or
+    None).
+
+    s = cap tanh(scale q.k / cap) - slopes[h] |p - c| over the keys a row sees: its document's
+    (docs_q, docs_k int32 [n+1] or [B, n+1]; or the first lengths[b] keys), up to the end of its
+    frame when `causal` (tokens per frame, 1: per token), and the document's first `prefix` keys.  A
+    document's rows are its last positions, so one new token over a cache is Nq = 1 with lengths."""
+    p, keep = _masked(q, k, scale, cap, slopes, causal, docs_q, docs_k, prefix, lengths)
+    p.v = _view(v, torch.bfloat16, "v", q)
+    if v.shape != k.shape:
+        raise ValueError("v must have k's shape")
+    on = _On(q, stream)
+    with on as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        elif out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        if out.dtype not in _OUT:
+            raise ValueError("out must be bfloat16 or float32")
+        p.out_dtype, p.o = _OUT[out.dtype], _view(out, out.dtype, "out", q)
+        if lse is True:
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        elif lse is False:
+            lse = None
+        need = lib.sparse_attn_forward_masked_workspace_size(p)
+        if need and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        on.keep(out, lse, workspace, *(keep or ()))
+        st = lib.sparse_attn_forward_masked(
+            p, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+            _flat(lse, torch.float32, "lse", q, q.shape[:3]), _flat(status, torch.int32, "status", q),
+            _flat(workspace, torch.uint8, "workspace", q),
+            0 if workspace is None else workspace.numel(), s)
+    if st != SA_OK:
+        raise SparseAttnError(st, "sparse_attn_forward_masked")
+    return out, lse
+
+
+def sparse_attn_cache_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor,
+                              weights: torch.Tensor | None = None, *, decay: float = 1.0,
+                              scale: float | None = None, cap: float = 0.0,
+                              slopes: torch.Tensor | None = None, causal: int = 0,
+                              docs_q: torch.Tensor | None = None,
+                              docs_k: torch.Tensor | None = None,
+                              prefix: torch.Tensor | None = None,
+                              lengths: torch.Tensor | None = None,
+                              out: torch.Tensor | None = None,
+                              status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """decay * weights + the attention weight every cached key received from q's rows (summed over
+    the heads that share its key head): fp32 [B, Hk, Nk].  lse, scale and the masks as in the forward
+    that wrote lse.  weights None starts from zero; out=weights accumulates in place; entries past
+    lengths[b] stay as they were (zero when there were none)."""
+    p, keep = _masked(q, k, scale, cap, slopes, causal, docs_q, docs_k, prefix, lengths)
+    shape = k.shape[:3]
+    on = _On(q, stream)
+    with on as s:
+        if out is None:
+            make = torch.zeros if weights is None and lengths is not None else torch.empty
+            out = make(shape, dtype=torch.float32, device=q.device)
+        on.keep(out, *(keep or ()))
+        st = lib.sparse_attn_cache_weights(
+            p, q.data_ptr(), k.data_ptr(), _flat(lse, torch.float32, "lse", q, q.shape[:3]),
+            _flat(weights, torch.float32, "weights", q, shape), _flat(out, torch.float32, "out", q, shape),
+            float(decay) if weights is not None else 0.0, _flat(status, torch.int32, "status", q), s)
+    if st != SA_OK:
+        raise SparseAttnError(st, "sparse_attn_cache_weights")
+    return out
+
+
+def sparse_attn_cache_evict(weights: torch.Tensor, k: torch.Tensor | None, v: torch.Tensor | None,
+                            budget: int, *, sink: int = 0, recent: int = 0,
+                            lengths: torch.Tensor | None = None, out=None,
+                            kept: torch.Tensor | None = None, stream=None):
+    """Keeps min(n, budget) of every head's n = lengths[b] (default: all) cached entries: the first
+    `sink`, the last `recent` and the largest weights between (ties: the lowest index).
+
+    weights fp32 [B, Hk, Nk]; k, v bf16 views [B, Hk, Nk, d], or None to select only.  Returns (kept
+    int32 [B, Hk, budget], k, v [B, Hk, budget, d], weights [B, Hk, budget]): the kept entries in their
+    order; behind a shorter one kept is -1 and the rows of `out` = (k, v, weights) are left as they
+    were (zero when out is not given)."""
+    if weights.dim() != 3 or not weights.is_cuda:
+        raise ValueError("weights must be a CUDA tensor [B, Hk, Nk]")
+    B, H, N = weights.shape
+    if (k is None) != (v is None):
+        raise ValueError("k and v come together")
+    budget = int(budget)
+    p = sa_evict(B, H, N, 128 if k is None else k.shape[-1], budget, int(sink), int(recent))
+    w = _flat(weights, torch.float32, "weights", weights)
+    p.lengths = _flat(lengths, torch.int32, "lengths", weights, (B,))
+    on = _On(weights, stream)
+    with on as s:
+        make = torch.empty if lengths is None and budget <= N else torch.zeros
+        if out is None:
+            ko = vo = None
+            if k is not None and budget > 0:
+                ko, vo = (make((B, H, budget, t.shape[-1]), dtype=torch.bfloat16, device=weights.device)
+                          for t in (k, v))
+            wo = make((B, H, max(budget, 0)), dtype=torch.float32, device=weights.device)
+        else:
+            ko, vo, wo = out
+        if kept is None:
+            kept = torch.empty((B, H, max(budget, 0)), dtype=torch.int32, device=weights.device)
+        if k is not None:
+            p.k, p.v = _view(k, torch.bfloat16, "k", weights), _view(v, torch.bfloat16, "v", weights)
+            if k.shape != v.shape or tuple(k.shape[:3]) != (B, H, N):
+                raise ValueError("k and v must be [B, Hk, Nk, d] with weights' B, Hk and Nk")
+            if budget > 0:
+                p.k_out, p.v_out = (_view(t, torch.bfloat16, "out", weights) for t in (ko, vo))
+                if tuple(ko.shape) != (B, H, budget, k.shape[3]) or vo.shape != ko.shape:
+                    raise ValueError("out must hold k and v as [B, Hk, budget, d]")
+        on.keep(ko, vo, wo, kept)
+        st = lib.sparse_attn_cache_evict(
+            p, w, _ptr(k), _ptr(v), _flat(kept, torch.int32, "kept", weights, (B, H, max(budget, 0))),
+            _ptr(ko) if k is not None else None, _ptr(vo) if k is not None else None,
+            _flat(wo, torch.float32, "out", weights, (B, H, max(budget, 0))), s)
+    if st != SA_OK:
+        raise SparseAttnError(st, "sparse_attn_cache_evict")
+    return kept, ko, vo, wo
+
+
 class HostLayer:
     """One attention layer from pinned host tensors (sparse_attn_layer_from_host):
     device staging, one chunk's scratch and two copy streams, allocated once
@@ -442,3 +776,7 @@ voxel_permute = sparse_attn_voxel_permute
 index_from_bitmask = sparse_attn_index_from_bitmask
 index_from_block_mask = sparse_attn_index_from_block_mask
 kv_window_append = sparse_attn_kv_window_append
+rope = sparse_attn_rope
+forward_masked = sparse_attn_forward_masked
+cache_weights = sparse_attn_cache_weights
+cache_evict = sparse_attn_cache_evict

@@ -1,0 +1,582 @@
+// sa_cache.cu — which cached keys matter, and the eviction of the others.
+//
+//  * sa_cache_weights_kernel:  w_out[j] = decay w_in[j] + sum over the query
+//    heads that share the key head, and their rows i, of p_ij = e^(s_ij - lse_i):
+//    the attention weight key j received, in one pass over the scores.  s is
+//    the masked forward's (mask, cap, bias); a masked pair adds nothing.
+//  * sa_evict_select_kernel:  of a head's n entries keep the first `sink`, the
+//    last `recent` and the highest weights in between (ties: lowest index).
+//  * sa_evict_gather_kernel:  the kept rows of K, V and w, in their order.
+//
+// Weights.  S^T = K Q^T puts keys on the 128 TMEM lanes and query rows on the
+// columns, so an epilogue thread owns one key and sums over queries in its own
+// registers: no cross-lane reduction, no atomics, a fixed order.  A unit is one
+// 128-key tile; its K stays in shared memory while Q tiles of up to 256 packed
+// rows (query * R + head-in-group) stream by.  Two sets of four warps take
+// alternate Q tiles (one TMEM buffer each).  With many rows the bound is the one
+// exponential a pair; with one token per sequence it is the read of K.
+#include <atomic>
+#include <climits>
+
+#include "sa_device.cuh"
+#include "sa_internal.h"
+#include "sa_mask.cuh"
+#include "sa_tma.h"
+
+namespace sa {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMaxStages = 6;
+
+struct WCfg {
+  static constexpr int kEpiWarps = 8, kMmaWarp = 8;  // and one warp that loads
+  static constexpr int kThreads = 320;
+  static constexpr int kCols = 256;  // columns of a TMEM buffer
+};
+
+struct WBars {
+  uint64_t kfull[kMaxStages], kempty[kMaxStages], qfull[kMaxStages], qempty[kMaxStages];
+  uint64_t dfull[2], dempty[2], xfull[2], xempty[2], drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+// What a launch fixes: the Q tile (qn queries x R heads = rows, NR columns),
+// the rings and the shared-memory offsets.
+struct WPlan {
+  int32_t qn, rows, NR, qtiles, qst, kst, kqbytes, ktile;
+  int64_t units;
+  int32_t ktiles;
+};
+
+// Q tiles [t0, t1) with a row that sees one of the keys [k0, k0 + 128).
+__device__ __forceinline__ void tile_range(const MaskDev& m, const WPlan& p, int b, int k0, int* t0, int* t1) {
+  int a = 0, z = p.qtiles;
+  if (m.causal || m.nd || m.len) {
+    while (a < z && row_span(m, b, min((a + 1) * p.qn, m.Nq) - 1).hi <= k0) ++a;
+    if (m.nd)
+      while (z > a && row_span(m, b, (z - 1) * p.qn).lo >= k0 + 128) --z;
+  }
+  *t0 = a;
+  *t1 = z;
+}
+
+}  // namespace
+
+template <int D, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(WCfg::kThreads, 1)
+    sa_cache_weights_kernel(const WeightArgs wa, const WPlan p, const __grid_constant__ CUtensorMap tm_q,
+                            const __grid_constant__ CUtensorMap tm_k) {
+  const MaskedArgs& a = wa.m;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sK = smem;
+  uint8_t* sQ = sK + p.kst * p.ktile;
+  float* sL = reinterpret_cast<float*>(sQ + p.qst * p.kqbytes);     // [8 warps][256] lse in exp2 units
+  float* sX = sL + WCfg::kEpiWarps * WCfg::kCols;                   // [2][128] sums of set 1
+  WBars* bars = reinterpret_cast<WBars*>(sX + 2 * 128);
+  volatile int* abort = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(&bars->kfull[s], 1);
+      mbar_init(&bars->kempty[s], 1);
+      mbar_init(&bars->qfull[s], 1);
+      mbar_init(&bars->qempty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars->dfull[b], 1);
+      mbar_init(&bars->dempty[b], 128);
+      mbar_init(&bars->xfull[b], 128);
+      mbar_init(&bars->xempty[b], 128);
+    }
+    mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  // Q rows that no copy fills are zero for good (their columns count nothing,
+  // but what they hold must not be a NaN).
+  for (int i = threadIdx.x; i < p.qst * p.kqbytes / 16; i += WCfg::kThreads)
+    reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  if (warp == WCfg::kMmaWarp) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp < WCfg::kEpiWarps) {
+    // ------------------------------------------------------------ epilogue
+    const int es = warp >> 2, tid = threadIdx.x & 127;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    float* wL = sL + warp * WCfg::kCols;
+    const int nch = p.NR / 32;
+    // Column c * 32 + lane is query tile * qn + qo[c] of head ho: fixed per lane.
+    int off[8], qo[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const int r = c * 32 + lane;
+      qo[c] = r < p.rows ? r / a.R : INT_MAX / 2;
+      off[c] = r < p.rows ? (r % a.R) * a.Nq + r / a.R : 0;
+    }
+    uint32_t it = 0, xn = 0;
+    for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
+      const int bh = static_cast<int>(u / p.ktiles), k0 = static_cast<int>(u % p.ktiles) * 128;
+      const int b = bh / a.Hkv, hk = bh % a.Hkv;
+      int t0, t1;
+      tile_range(a.mask, p, b, k0, &t0, &t1);
+      const int key = k0 + tid;
+      const bool solo = t1 - t0 == 1;
+      const float* lse = wa.lse + (int64_t(b) * a.Hq + int64_t(hk) * a.R) * a.Nq;
+      const float* slopes = BIAS ? a.slopes + hk * a.R : nullptr;
+      const float sl = a.scale_log2;
+      float total = 0.f;
+      float next[8];
+      int first = t0 + ((it ^ es) & 1);
+      auto fetch = [&](int t) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          next[c] = c < nch && qo[c] < a.Nq - t * p.qn ? __ldg(lse + int64_t(t) * p.qn + off[c]) : 0.f;
+      };
+      if (first < t1) fetch(first);
+      // the entry as it was, and the keys that take part at all
+      const int len = a.mask.len ? clamp_int(__ldg(a.mask.len + b), 0, a.Nk) : a.Nk;
+      const int64_t wi = int64_t(bh) * a.Nk + key;
+      const bool mine = key < a.Nk && (solo ? ((it ^ es) & 1) == 0 : es == 0);
+      float was = 0.f;
+      if (mine && wa.w_in && (key >= len || wa.decay != 0.f)) was = wa.w_in[wi];
+      for (int t = first; t < t1; t += 2) {
+        const uint32_t n = it + (t - t0);
+        // lse of this tile's columns; a row without a finite one adds nothing
+        uint32_t dead = 0;
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          if (c < nch) {
+            const bool row = qo[c] < a.Nq - t * p.qn;
+            const bool fin = isfinite(next[c]);
+            wL[c * 32 + lane] = row && fin ? next[c] * kLog2e : INFINITY;
+            if (__any_sync(0xffffffffu, row && !fin)) dead |= 1u << c;
+          }
+        }
+        __syncwarp();
+        const int qa = t * p.qn, qz = min(qa + p.qn, a.Nq) - 1;
+        bool edge = false;
+        if (a.mask.causal || a.mask.nd || a.mask.len)
+          edge = row_span(a.mask, b, qz).lo > k0 || row_span(a.mask, b, qa).hi < min(k0 + 128, a.Nk);
+        if (t + 2 < t1) fetch(t + 2);
+        if (!mbar_wait(&bars->dfull[es], (n >> 1) & 1, abort)) goto done;
+        tc_fence_after();
+        const uint32_t sbase = tmem + lane_base + es * WCfg::kCols;
+        uint64_t acc[4] = {0, 0, 0, 0};
+        for (int c = 0; c < nch; ++c) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld32(sbase + c * 32, r);
+          tmem_ld_wait();
+          const float4* l4 = reinterpret_cast<const float4*>(wL + c * 32);
+          const bool care = edge || ((dead >> c) & 1);
+          int lo = 0, hi = INT_MAX, pos = 0;
+          float slope = 0.f;
+          if (edge || BIAS) {
+            const int rr = c * 32 + lane;
+            if (rr < p.rows && qa + rr / a.R < a.Nq) {
+              const Span sp = row_span(a.mask, b, qa + rr / a.R);
+              lo = sp.lo;
+              hi = sp.hi;
+              pos = sp.pos;
+              if (BIAS) slope = -__ldg(slopes + rr % a.R) * kLog2e;
+            }
+          }
+          const uint64_t sl2 = f2(sl, sl);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 L = l4[e];
+            const float Lf[4] = {L.x, L.y, L.z, L.w};
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              const uint64_t x = f2(__uint_as_float(r[4 * e + i]), __uint_as_float(r[4 * e + i + 1]));
+              uint64_t v;
+              if (CAP) {
+                const uint64_t ex = mul2(x, f2(a.cap_k1, a.cap_k1));
+                const uint64_t d1 = add2(f2(fast_exp2(f2lo(ex)), fast_exp2(f2hi(ex))), f2(1.f, 1.f));
+                v = fma2(f2(fast_rcp(f2lo(d1)), fast_rcp(f2hi(d1))), f2(-2.f * a.cap_log2, -2.f * a.cap_log2),
+                         f2(a.cap_log2, a.cap_log2));
+              } else if (BIAS) {
+                v = mul2(x, sl2);
+              }
+              if (BIAS) {
+                const float s0 = __shfl_sync(0xffffffffu, slope, 4 * e + i);
+                const float s1 = __shfl_sync(0xffffffffu, slope, 4 * e + i + 1);
+                const int p0 = __shfl_sync(0xffffffffu, pos, 4 * e + i);
+                const int p1 = __shfl_sync(0xffffffffu, pos, 4 * e + i + 1);
+                v = fma2(f2(s0, s1), f2(fabsf(static_cast<float>(p0 - key)), fabsf(static_cast<float>(p1 - key))), v);
+              }
+              if (CAP || BIAS)
+                v = sub2(v, f2(Lf[i], Lf[i + 1]));
+              else
+                v = fma2(x, sl2, f2(-Lf[i], -Lf[i + 1]));
+              y[i] = f2lo(v);
+              y[i + 1] = f2hi(v);
+            }
+            if (care) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int clo = __shfl_sync(0xffffffffu, lo, 4 * e + i);
+                const int chi = __shfl_sync(0xffffffffu, hi, 4 * e + i);
+                if (key < clo || key >= chi || Lf[i] == INFINITY) y[i] = -INFINITY;
+              }
+            }
+            acc[e & 3] = add2(acc[e & 3], f2(fast_exp2(y[0]), fast_exp2(y[1])));
+            acc[e & 3] = add2(acc[e & 3], f2(fast_exp2(y[2]), fast_exp2(y[3])));
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&bars->dempty[es]);
+        const uint64_t s2 = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+        total += f2lo(s2) + f2hi(s2);
+      }
+      it += t1 > t0 ? t1 - t0 : 0;
+      if (t1 - t0 > 1) {
+        // set 1 hands its sums to set 0
+        const uint32_t xb = xn & 1, xp = (xn >> 1) & 1;
+        ++xn;
+        if (es == 1) {
+          if (!mbar_wait(&bars->xempty[xb], xp ^ 1, abort)) goto done;
+          sX[xb * 128 + tid] = total;
+          mbar_arrive(&bars->xfull[xb]);
+        } else {
+          if (!mbar_wait(&bars->xfull[xb], xp, abort)) goto done;
+          total += sX[xb * 128 + tid];
+          mbar_arrive(&bars->xempty[xb]);
+        }
+      }
+      if (mine) {
+        if (key < len)
+          wa.w_out[wi] = wa.decay != 0.f ? fmaf(wa.decay, was, total) : total;
+        else if (wa.w_in && wa.w_in != wa.w_out)
+          wa.w_out[wi] = was;  // an entry past the sequence stays as it was
+      }
+    }
+  } else if (warp == WCfg::kMmaWarp) {
+    // ------------------------------------------------------------ MMA issue
+    if (lane == 0) {
+      const uint32_t base = idesc_bf16(128, p.NR, false, false);
+      const uint32_t kIdesc = a.neg_scale ? idesc_negate_b(base) : base;
+      const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sK);
+      uint32_t it = 0, un = 0;
+      bool ok = true;
+      for (int64_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
+        const int bh = static_cast<int>(u / p.ktiles), k0 = static_cast<int>(u % p.ktiles) * 128;
+        int t0, t1;
+        tile_range(a.mask, p, bh / a.Hkv, k0, &t0, &t1);
+        if (t1 <= t0) continue;
+        const uint32_t ks = un % p.kst;
+        if (!mbar_wait(&bars->kfull[ks], (un / p.kst) & 1, abort)) break;
+        for (int t = t0; t < t1; ++t, ++it) {
+          const uint32_t qs = it % p.qst, d = it & 1;
+          if (!mbar_wait(&bars->qfull[qs], (it / p.qst) & 1, abort) ||
+              !mbar_wait(&bars->dempty[d], ((it >> 1) & 1) ^ 1, abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t ka = k_addr + ks * p.ktile, qa = q_addr + qs * p.kqbytes;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + d * WCfg::kCols, sw128_desc(ka + (kk >> 2) * 128 * 128 + (kk & 3) * 32, 16, 1024),
+                   sw128_desc(qa + (kk >> 2) * p.NR * 128 + (kk & 3) * 32, 16, 1024), kIdesc, kk > 0 ? 1u : 0u);
+          mma_commit(&bars->dfull[d]);
+          mma_commit(&bars->qempty[qs]);
+          if (t == t1 - 1) mma_commit(&bars->kempty[ks]);
+        }
+        ++un;
+      }
+      mma_commit(&bars->drain);
+      const long long c0 = clock64();
+      while (!mbar_test(&bars->drain, 0) && clock64() - c0 < kWaitLimitCycles) {
+      }
+    }
+  } else if (lane == 0) {
+    // ------------------------------------------------------------ loads (TMA)
+    const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sK);
+    uint32_t it = 0, un = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
+      const int bh = static_cast<int>(u / p.ktiles), k0 = static_cast<int>(u % p.ktiles) * 128;
+      const int b = bh / a.Hkv, hk = bh % a.Hkv;
+      int t0, t1;
+      tile_range(a.mask, p, b, k0, &t0, &t1);
+      if (t1 <= t0) continue;
+      const uint32_t ks = un % p.kst;
+      if (!mbar_wait(&bars->kempty[ks], ((un / p.kst) & 1) ^ 1, abort)) break;
+      mbar_expect_tx(&bars->kfull[ks], p.ktile);
+#pragma unroll
+      for (int cb = 0; cb < D / 64; ++cb)
+        tma_load_4d(k_addr + ks * p.ktile + cb * 128 * 128, &tm_k, 64 * cb, k0, hk, b, &bars->kfull[ks]);
+      ++un;
+      for (int t = t0; t < t1; ++t, ++it) {
+        const uint32_t qs = it % p.qst;
+        if (!mbar_wait(&bars->qempty[qs], ((it / p.qst) & 1) ^ 1, abort)) {
+          ok = false;
+          break;
+        }
+        mbar_expect_tx(&bars->qfull[qs], p.rows * D * 2);
+#pragma unroll
+        for (int cb = 0; cb < D / 64; ++cb)
+          tma_load_4d(q_addr + qs * p.kqbytes + cb * p.NR * 128, &tm_q, 64 * cb, hk * a.R, t * p.qn, b,
+                      &bars->qfull[qs]);
+      }
+    }
+    // After an abort: the copies in flight land before the block ends.
+    if (*abort) {
+      for (uint32_t i = it > uint32_t(p.qst) ? it - p.qst : 0; i < it; ++i) {
+        const long long c0 = clock64();
+        while (!mbar_test(&bars->qfull[i % p.qst], (i / p.qst) & 1) && clock64() - c0 < kWaitLimitCycles) {
+        }
+      }
+      for (uint32_t i = un > uint32_t(p.kst) ? un - p.kst : 0; i < un; ++i) {
+        const long long c0 = clock64();
+        while (!mbar_test(&bars->kfull[i % p.kst], (i / p.kst) & 1) && clock64() - c0 < kWaitLimitCycles) {
+        }
+      }
+    }
+  }
+done:
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && bars->abort) report(a.status, SA_DEVERR_TIMEOUT);
+  if (warp == WCfg::kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, bool CAP, bool BIAS>
+static cudaError_t launch_w(const WeightArgs& a, const WPlan& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                            int num_sms, cudaStream_t st) {
+  auto kern = sa_cache_weights_kernel<D, CAP, BIAS>;
+  int smem = 1024 + p.kst * p.ktile + p.qst * p.kqbytes + WCfg::kEpiWarps * WCfg::kCols * 4 + 1024 +
+             static_cast<int>(sizeof(WBars)) + 64;
+  if (smem < 120 * 1024) smem = 120 * 1024;  // one block per SM owns its TMEM
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = p.units < num_sms ? p.units : num_sms;
+  kern<<<static_cast<unsigned>(grid), WCfg::kThreads, smem, st>>>(a, p, tq, tk);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_weights(const WeightArgs& a, int num_sms, cudaStream_t st) {
+  const MaskedArgs& m = a.m;
+  WPlan p;
+  p.qn = 256 / m.R < m.Nq ? 256 / m.R : m.Nq;
+  p.rows = p.qn * m.R;
+  p.NR = (p.rows + 31) / 32 * 32;
+  p.qtiles = (m.Nq + p.qn - 1) / p.qn;
+  p.ktile = 128 * m.d * 2;
+  p.kqbytes = p.NR * m.d * 2;
+  p.qst = p.NR <= 64 ? kMaxStages : 2;
+  const int room = 212 * 1024 - p.qst * p.kqbytes;
+  p.kst = room / p.ktile < kMaxStages ? room / p.ktile : kMaxStages;
+  p.ktiles = (m.Nk + 127) / 128;
+  p.units = int64_t(m.B) * m.Hkv * p.ktiles;
+  CUtensorMap tq, tk;
+  if (!make_view_map(&tq, m.q, m.d, m.Nq, m.Hq, m.B, m.qs.n, m.qs.h, m.qs.b, p.qn, m.R, true) ||
+      !make_view_map(&tk, m.k, m.d, m.Nk, m.Hkv, m.B, m.ks.n, m.ks.h, m.ks.b, 128, 1, false))
+    return cudaErrorInvalidValue;
+  const bool cap = m.cap_log2 > 0.f, bias = m.slopes != nullptr;
+  if (m.d == 128) {
+    if (cap) return bias ? launch_w<128, true, true>(a, p, tq, tk, num_sms, st) : launch_w<128, true, false>(a, p, tq, tk, num_sms, st);
+    return bias ? launch_w<128, false, true>(a, p, tq, tk, num_sms, st) : launch_w<128, false, false>(a, p, tq, tk, num_sms, st);
+  }
+  if (cap) return bias ? launch_w<64, true, true>(a, p, tq, tk, num_sms, st) : launch_w<64, true, false>(a, p, tq, tk, num_sms, st);
+  return bias ? launch_w<64, false, true>(a, p, tq, tk, num_sms, st) : launch_w<64, false, false>(a, p, tq, tk, num_sms, st);
+}
+
+// ---------------------------------------------------------------- eviction
+
+namespace {
+
+constexpr int kSelThreads = 1024;
+constexpr int kBins = 2048;
+constexpr int kCached = 48 * 1024;  // weights of a row kept in shared memory
+
+// Order of weights: larger first, -0 equal to +0, a NaN below everything.
+__device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0u : order_key(w + 0.f); }
+
+}  // namespace
+
+__global__ void __launch_bounds__(kSelThreads) sa_evict_select_kernel(const EvictArgs a) {
+  extern __shared__ uint32_t s_keys[];
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t wsum[32], weq[32];
+  __shared__ uint32_t s_digit, s_left;
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int32_t* kept = a.kept + row * a.budget;
+  const int n = a.len ? min(max(__ldg(a.len + row / a.Hkv), 0), a.Nk) : a.Nk;
+  if (n <= a.budget) {
+    for (int i = tid; i < a.budget; i += kSelThreads) kept[i] = i < n ? i : -1;
+    return;
+  }
+  const int lo = a.sink, M = n - a.recent - a.sink;
+  const uint32_t want = a.budget - a.sink - a.recent;  // of the M in between: 0 <= want < M
+  for (int i = tid; i < a.sink; i += kSelThreads) kept[i] = i;
+  for (int i = tid; i < a.recent; i += kSelThreads) kept[a.budget - a.recent + i] = n - a.recent + i;
+  if (want == 0) return;
+  const float* w = a.w + row * a.Nk + lo;
+  const bool cached = M <= kCached;
+  auto key_at = [&](int i) -> uint32_t { return cached ? s_keys[i] : weight_key(__ldg(w + i)); };
+  if (cached)
+    for (int i = tid; i < M; i += kSelThreads) s_keys[i] = weight_key(__ldg(w + i));
+
+  // Radix selection from the top: 11, 11 and 10 bits.
+  uint32_t prefix = 0, mask = 0, left = want;
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t dmask = pass == 2 ? 1023u : 2047u;
+    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < M; i += kSelThreads) {
+      const uint32_t k = key_at(i);
+      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & dmask], 1u);
+    }
+    __syncthreads();
+    // suffix sums: thread t holds bins 2047 - 2t and 2046 - 2t
+    const uint32_t h0 = hist[kBins - 1 - 2 * tid], h1 = hist[kBins - 2 - 2 * tid];
+    uint32_t inc = h0 + h1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+      uint32_t v = wsum[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+      }
+      wsum[lane] = v;
+    }
+    __syncthreads();
+    const uint32_t above = inc - h0 - h1 + (warp ? wsum[warp - 1] : 0);
+    if (above < left && left <= above + h0) {
+      s_digit = kBins - 1 - 2 * tid;
+      s_left = left - above;
+    } else if (above + h0 < left && left <= above + h0 + h1) {
+      s_digit = kBins - 2 - 2 * tid;
+      s_left = left - above - h0;
+    }
+    __syncthreads();
+    prefix |= s_digit << shift;
+    mask |= dmask << shift;
+    left = s_left;
+    __syncthreads();
+  }
+  // Keep every key above the cut, and the first `left` of those at it.  Each
+  // warp owns a run of the row; the counts of the runs before it place its own.
+  const uint32_t cut = prefix;
+  const int run = ((M + 31) / 32 + 31) / 32 * 32;
+  const int i0 = warp * run, i1 = min(i0 + run, M);
+  uint32_t gt = 0, eq = 0;
+  for (int i = i0 + lane; i < i1; i += 32) {
+    const uint32_t k = key_at(i);
+    gt += k > cut;
+    eq += k == cut;
+  }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  if (lane == 0) {
+    wsum[warp] = gt;
+    weq[warp] = eq;
+  }
+  __syncthreads();
+  uint32_t gb = 0, eb = 0;
+  for (int x = 0; x < warp; ++x) {
+    gb += wsum[x];
+    eb += weq[x];
+  }
+  const uint32_t below = (1u << lane) - 1;
+  for (int base = i0; base < i1; base += 32) {
+    const int i = base + lane;
+    const uint32_t k = i < i1 ? key_at(i) : 0;
+    const bool g = i < i1 && k > cut, e = i < i1 && k == cut;
+    const uint32_t bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
+    const uint32_t ge = gb + __popc(bg & below), ee = eb + __popc(be & below);
+    if (g || (e && ee < left)) kept[a.sink + ge + min(ee, left)] = lo + i;
+    gb += __popc(bg);
+    eb += __popc(be);
+  }
+}
+
+// PIECES 16-byte pieces per row (d / 8); U slots per thread in flight.
+template <int PIECES>
+__global__ void __launch_bounds__(256) sa_evict_gather_kernel(const EvictArgs a) {
+  constexpr int U = 4, kSlots = 256 / PIECES;
+  const int piece = threadIdx.x % PIECES;
+  const int64_t row = blockIdx.y, b = row / a.Hkv, h = row % a.Hkv;
+  const int32_t* kept = a.kept + row * a.budget;
+  const int j0 = blockIdx.x * (kSlots * U) + threadIdx.x / PIECES;
+  int idx[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int j = j0 + i * kSlots;
+    idx[i] = j < a.budget ? __ldg(kept + j) : -1;
+  }
+  if (a.k) {
+    const uint16_t* k = a.k + b * a.ks.b + h * a.ks.h + piece * 8;
+    const uint16_t* v = a.v + b * a.vs.b + h * a.vs.h + piece * 8;
+    uint16_t* ko = a.k_out + b * a.kos.b + h * a.kos.h + piece * 8;
+    uint16_t* vo = a.v_out + b * a.vos.b + h * a.vos.h + piece * 8;
+    uint4 kr[U], vr[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (idx[i] >= 0) {
+        kr[i] = __ldg(reinterpret_cast<const uint4*>(k + idx[i] * a.ks.n));
+        vr[i] = __ldg(reinterpret_cast<const uint4*>(v + idx[i] * a.vs.n));
+      }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (idx[i] >= 0) {
+        const int64_t j = j0 + i * kSlots;
+        *reinterpret_cast<uint4*>(ko + j * a.kos.n) = kr[i];
+        *reinterpret_cast<uint4*>(vo + j * a.vos.n) = vr[i];
+      }
+  }
+  if (a.w_out && piece == 0) {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (idx[i] >= 0) a.w_out[row * a.budget + j0 + i * kSlots] = __ldg(a.w + row * a.Nk + idx[i]);
+  }
+}
+
+cudaError_t launch_cache_evict(const EvictArgs& a, int num_sms, cudaStream_t st) {
+  (void)num_sms;
+  const int64_t rows = int64_t(a.B) * a.Hkv;
+  const int smem = kCached * 4;
+  cudaError_t e = cudaFuncSetAttribute(sa_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t need = int64_t(a.Nk) < kCached ? int64_t(a.Nk) * 4 : smem;
+  sa_evict_select_kernel<<<static_cast<unsigned>(rows), kSelThreads, need, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (!a.k && !a.w_out) return cudaSuccess;
+  const int slots = 4 * (256 / (a.d / 8));
+  const dim3 grid((a.budget + slots - 1) / slots, static_cast<unsigned>(rows));
+  if (a.d == 128)
+    sa_evict_gather_kernel<16><<<grid, 256, 0, st>>>(a);
+  else
+    sa_evict_gather_kernel<8><<<grid, 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace sa

@@ -149,6 +149,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x
       : "memory");
 }
 
+// 4-D tiled TMA load of one box at element coordinates (x, y, z, w).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // 3-D tiled TMA store of one box from shared memory (bulk async group).
 __device__ __forceinline__ void tma_store_3d(const void* map, uint32_t src, int x, int y, int z) {
   asm volatile(
@@ -415,6 +425,13 @@ __device__ __forceinline__ float add_bf16x2(uint32_t packed, float acc) {
       : "=f"(r)
       : "r"(packed), "f"(acc));
   return r;
+}
+
+// 1/x to about one unit in the last place (0 for an infinite x).
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ float fast_exp2(float x) {

@@ -112,6 +112,82 @@ struct FmtArgs {
 };
 cudaError_t launch_index_from_mask(const FmtArgs& a, int num_sms, cudaStream_t stream);
 
+// Which keys a query row sees (sa_mask.cuh has the rule).
+struct MaskDev {
+  const int32_t* dq;   // [B, nd + 1] first query row of each document, or null
+  const int32_t* dk;   // [B, nd + 1] first key of each document
+  const int32_t* px;   // [B, nd] prefix keys, or null
+  const int32_t* len;  // [B] keys of each batch entry, or null
+  int32_t nd;          // documents (0: one, the whole rows)
+  int32_t causal;      // 0: none, else tokens per frame
+  int32_t Nq, Nk;
+};
+
+// Masked forward and cache weights.
+struct MaskedArgs {
+  const uint16_t* q;   // bf16 views, element strides, d contiguous
+  const uint16_t* k;
+  const uint16_t* v;
+  void* o;
+  sa_strides qs, ks, vs, os;
+  float* lse;          // [B, Hq, Nq] or null
+  const float* slopes; // [Hq] or null
+  int32_t* status;
+  MaskDev mask;
+  int32_t B, Hq, Hkv, R, Nq, Nk, d;
+  int32_t out_fp32, neg_scale;
+  float scale_log2;    // |scale| log2(e)
+  float cap_log2;      // cap log2(e), 0: no cap
+  float cap_k1;        // 2 |scale| log2(e) / cap
+  int64_t rows;        // packed rows of a key head, R * Nq
+  int64_t total_rows;  // B * Hq * Nq
+  int32_t row_blocks, splits;
+  float* part_o;       // [splits, total_rows, d] partials (splits > 1)
+  float* part_lse;     // [splits, total_rows]
+};
+int masked_splits(int64_t rows, int64_t BH, int32_t Nk);
+cudaError_t launch_masked(const MaskedArgs& a, cudaStream_t stream);
+
+struct WeightArgs {
+  MaskedArgs m;        // q, k, mask, scale, cap, slopes
+  const float* lse;    // [B, Hq, Nq]
+  const float* w_in;   // [B, Hkv, Nk], or null (decay 0)
+  float* w_out;        // may be w_in
+  float decay;
+};
+cudaError_t launch_cache_weights(const WeightArgs& a, int num_sms, cudaStream_t stream);
+
+struct EvictArgs {
+  const float* w;      // [B, Hkv, Nk]
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* k_out;
+  uint16_t* v_out;
+  float* w_out;        // [B, Hkv, budget] or null
+  int32_t* kept;       // [B, Hkv, budget]
+  const int32_t* len;  // [B] or null
+  sa_strides ks, vs, kos, vos;
+  int32_t B, Hkv, Nk, d, budget, sink, recent;
+};
+cudaError_t launch_cache_evict(const EvictArgs& a, int num_sms, cudaStream_t stream);
+
+struct RopeArgs {
+  const void* x[2];
+  void* y[2];
+  sa_strides xs[2], ys[2];
+  int32_t H[2];
+  int32_t B, N, d, half, fp32, inverse;
+  int32_t rot;             // rotated elements (the first of a row)
+  int32_t axes, first[4];  // pairs first[a] .. first[a + 1] - 1 turn with axis a
+  const int32_t* pos;      // [N, axes] positions (batch stride pos_b), or null: grid
+  int64_t pos_b;
+  int32_t offset[3];
+  VoxArgs vox;             // grid and voxel shape (only these fields)
+  int32_t voxel_order;
+  uint64_t turn[64];       // turns per position of each pair, in units of 2^-64
+};
+cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream);
+
 // sparse_attn_layer_from_host splits a layer into at most this many chunks.
 constexpr int kMaxPipelineChunks = 64;
 

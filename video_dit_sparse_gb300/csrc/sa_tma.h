@@ -44,6 +44,26 @@ inline bool make_rows_map(CUtensorMap* map, const void* base, uint64_t rows, uin
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A bf16 [B, H, N, d] view with element strides (sb, sh, sn, 1) seen as boxes
+// of 64 elements x box_n rows x box_h heads, 128-byte swizzled.  `heads_first`
+// walks the heads of a token before its next token (smem row = n * box_h + h),
+// otherwise box_h is 1.  Rows past N (and heads past H) read as zeros.
+inline bool make_view_map(CUtensorMap* map, const void* base, uint32_t d, uint64_t N, uint64_t H,
+                          uint64_t B, int64_t sn, int64_t sh, int64_t sb, uint32_t box_n, uint32_t box_h,
+                          bool heads_first) {
+  const EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  const cuuint64_t n2 = static_cast<cuuint64_t>(sn) * 2, h2 = static_cast<cuuint64_t>(sh) * 2;
+  const cuuint64_t dims[4] = {d, heads_first ? H : N, heads_first ? N : H, B};
+  const cuuint64_t strides[3] = {heads_first ? h2 : n2, heads_first ? n2 : h2,
+                                 static_cast<cuuint64_t>(sb) * 2};
+  const cuuint32_t box[4] = {64, heads_first ? box_h : box_n, heads_first ? box_n : box_h, 1};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+            elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Every `stride`-th key row of each of BH heads of a [BH, Nk, d] bf16 tensor:
 // row i of head h is key i*stride (i < nkeys), seen as boxes of 64 elements x
 // 128 rows of one head, 128-byte swizzled.  Rows past nkeys read as zeros.
