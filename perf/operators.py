@@ -368,7 +368,7 @@ def _run_own(c):
         else:
             y = sa.sparse_attn_rope(c["q"], c["k"], axes=c["axes"], grid=c["grid"], voxel=c["voxel"] or None,
                                     offset=(c["offset"], 0, 0), pairing=c["pairing"], inverse=c["inverse"])
-        return [t for t in y if t is not None]
+        return [y] if c["k"] is None else list(y)
     if c["op"] == "masked":
         return sa.sparse_attn_forward_masked(c["q"], c["k"], c["v"], causal=c["causal"], cap=c["cap"], slopes=c["slopes"],
                                              docs_q=c["docs_q"], docs_k=c["docs_k"], prefix=c["prefix"])
