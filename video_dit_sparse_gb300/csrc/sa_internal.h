@@ -141,11 +141,14 @@ struct MaskedArgs {
   float cap_k1;        // 2 |scale| log2(e) / cap
   int64_t rows;        // packed rows of a key head, R * Nq
   int64_t total_rows;  // B * Hq * Nq
-  int32_t row_blocks, splits;
-  float* part_o;       // [splits, total_rows, d] partials (splits > 1)
-  float* part_lse;     // [splits, total_rows]
+  // masked_plan: a unit is unit_rows packed rows of a key head; the first
+  // full_units run whole, the other split_units in `splits` runs of keys
+  int32_t unit_rows, row_blocks, splits;
+  int64_t full_units, split_units;
+  float* part_o;       // [split_units * splits, unit_rows, d] partials
+  float* part_lse;     // [split_units * splits, unit_rows]
 };
-int masked_splits(int64_t rows, int64_t BH, int32_t Nk);
+void masked_plan(MaskedArgs* a);
 cudaError_t launch_masked(const MaskedArgs& a, cudaStream_t stream);
 
 struct WeightArgs {

@@ -97,7 +97,8 @@ sa_status check_masked(const sa_masked* p, sa::MaskedArgs* a) {
   a->cap_k1 = p->cap > 0.f ? static_cast<float>(2.0 * s * log2e / p->cap) : 0.f;
   a->rows = R * p->Nq;
   a->total_rows = int64_t(p->B) * p->Hq * p->Nq;
-  a->row_blocks = a->splits = 1;
+  a->unit_rows = a->row_blocks = a->splits = 1;
+  a->full_units = a->split_units = 0;
   a->part_o = nullptr;
   a->part_lse = nullptr;
   return SA_OK;
@@ -113,16 +114,13 @@ bool masked_tables(const sa_masked* p) {
          (!p->slopes || in_device_allocation(p->slopes, uint64_t(p->Hq) * 4));
 }
 
-// 256-byte aligned: the partial outputs, then their lse.
-size_t part_bytes(const sa::MaskedArgs& a, int splits) {
-  return (size_t(splits) * a.total_rows * a.d * 4 + 255) / 256 * 256;
+// The partial outputs, then their lse (each 256-byte aligned).
+size_t part_bytes(const sa::MaskedArgs& a) {
+  return size_t(a.split_units) * a.splits * a.unit_rows * a.d * 4;
 }
 
-int splits_of(const sa::MaskedArgs& a) { return sa::masked_splits(a.rows, int64_t(a.B) * a.Hkv, a.Nk); }
-
 size_t masked_workspace(const sa::MaskedArgs& a) {
-  const int s = splits_of(a);
-  return s == 1 ? 0 : part_bytes(a, s) + (size_t(s) * a.total_rows * 4 + 255) / 256 * 256;
+  return part_bytes(a) + (size_t(a.split_units) * a.splits * a.unit_rows * 4 + 255) / 256 * 256;
 }
 
 }  // namespace
@@ -131,7 +129,9 @@ extern "C" {
 
 size_t sparse_attn_forward_masked_workspace_size(const sa_masked* p) {
   sa::MaskedArgs a;
-  return check_masked(p, &a) == SA_OK ? masked_workspace(a) : 0;
+  if (check_masked(p, &a) != SA_OK) return 0;
+  sa::masked_plan(&a);
+  return masked_workspace(a);
 }
 
 sa_status sparse_attn_forward_masked(const sa_masked* p, const void* q, const void* k, const void* v, void* o,
@@ -147,12 +147,10 @@ sa_status sparse_attn_forward_masked(const sa_masked* p, const void* q, const vo
       !check_view(o, &a.os, p->B, p->Hq, p->Nq, p->d, a.out_fp32 ? 4 : 2, true, false, &no))
     return SA_ERR_INVALID_ARG;
   if (!aligned(lse, 4) || !aligned(dev_status, 4)) return SA_ERR_INVALID_ARG;
-  a.splits = splits_of(a);
+  sa::masked_plan(&a);
   const size_t need = masked_workspace(a);
   if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return SA_ERR_INVALID_ARG;
-  const int64_t tile = a.rows > 128 ? 256 : 128;
-  if (int64_t(p->B) * p->Hkv * ((a.rows + tile - 1) / tile) * a.splits >= (int64_t(1) << 31))
-    return SA_ERR_UNSUPPORTED;  // grid.x
+  if (a.full_units + a.split_units * a.splits >= (int64_t(1) << 31)) return SA_ERR_UNSUPPORTED;  // grid.x
   int sms = 0;
   if ((st = device_info(&sms)) != SA_OK) return st;
   if (!in_device_allocation(q, nq) || !in_device_allocation(k, nk) || !in_device_allocation(v, nv) ||
@@ -168,7 +166,7 @@ sa_status sparse_attn_forward_masked(const sa_masked* p, const void* q, const vo
   a.status = dev_status;
   if (need) {
     a.part_o = static_cast<float*>(workspace);
-    a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + part_bytes(a, a.splits));
+    a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + part_bytes(a));
   }
   sa::NvtxRange range("sparse_attn_forward_masked");
   return map_cuda(sa::launch_masked(a, reinterpret_cast<cudaStream_t>(stream)));
