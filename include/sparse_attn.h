@@ -487,7 +487,7 @@ sa_status sparse_attn_rope(const sa_rope* rope, int32_t H0, const void* x0, cons
  *
  * q, k, v bf16; o bf16 or fp32 by out_dtype; P is rounded to bf16 for the
  * second product (o is normalised by the sum of the rounded values), all sums
- * are fp32.  q may repeat a dimension.  Keys and values past a row's document
+ * are fp32.  Hq / Hkv <= 128.  Keys and values past a row's document
  * never reach it, whatever they hold; a NaN or an infinite V row inside the
  * document may reach other rows of the same document that do not see it.
  * Few rows split the keys over the GPU: the workspace (256-byte aligned, may
@@ -527,7 +527,6 @@ sa_status sparse_attn_forward_masked(const sa_masked* problem, const void* q, co
  * inputs give the same bits.
  *   lse    fp32 [B, Hq, Nq];  w_in, w_out  fp32 [B, Hkv, Nk], the same buffer
  *          or apart; w_in may be NULL when decay = 0 (then it is not read)
- * Hq / Hkv <= 256.
  */
 sa_status sparse_attn_cache_weights(const sa_masked* problem, const void* q, const void* k, const float* lse,
                                     const float* w_in, float* w_out, float decay, int32_t* dev_status,

@@ -47,6 +47,7 @@ def test_forward_masked_refusals(sa):
     for name in ("q", "k", "v", "o"):
         assert forward(sa, ok, **{name: None}) == INVALID
         assert forward(sa, ok, **{name: MIS}) == INVALID
+    assert forward(sa, masked(sa, Hq=258, q=sa.sa_strides(258 * 1024, 1024, 128), o=sa.sa_strides(258 * 1024, 1024, 128))) == UNSUPPORTED
     assert forward(sa, ok, lse=A16 + 2) == INVALID
     S = sa.sa_strides
     for bad in (dict(q=S(4096, 1024, -128)), dict(q=S(4096, 1024, 100)), dict(k=S(16384, 8192, 0)),

@@ -8,8 +8,10 @@ a missing library raises at import.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
+import struct
 
 import torch
 
@@ -430,58 +432,77 @@ def sparse_attn_kv_window_append(cache_k: torch.Tensor, cache_v: torch.Tensor,
 
 
 # ------------------------------------------------ operators around the attention path
+#
+# A call on a small problem takes the GPU a few microseconds, so what Python does per call counts:
+# problems are packed in one go (the structures above say what their fields are) and passed as bytes.
 
-def _view(t: torch.Tensor, dtype, name: str, ref: torch.Tensor | None = None) -> sa_strides:
-    """A [B, H, N, d] view with a contiguous d: its strides."""
-    if not t.is_cuda or t.dtype != dtype or t.dim() != 4:
-        raise ValueError(f"{name} must be a CUDA tensor [B, H, N, d] of {dtype}")
-    if ref is not None and t.device != ref.device:
-        raise ValueError(f"{name} must be on {ref.device}")
+_MASKED = struct.Struct("@6ifi12qfP2i4P")
+_EVICT = struct.Struct("@7iP12q")
+_ROPE = struct.Struct("@10id2Pq6ii3q")
+assert _MASKED.size == ctypes.sizeof(sa_masked) and _EVICT.size == ctypes.sizeof(sa_evict)
+assert _ROPE.size == ctypes.sizeof(sa_rope)
+_STRIDES = struct.Struct("@3q")
+
+
+def _by_bytes(name, argtypes, restype=ctypes.c_int):
+    f = lib[name]  # its own function object: the declared prototype stays as it is
+    f.argtypes, f.restype = argtypes, restype
+    return f
+
+
+_vp, _cp = ctypes.c_void_p, ctypes.c_char_p
+_c_rope = _by_bytes("sparse_attn_rope", [_cp, ctypes.c_int32, _vp, _cp, _vp, _cp, ctypes.c_int32, _vp, _cp, _vp, _cp, _vp])
+_c_masked = _by_bytes("sparse_attn_forward_masked", [_cp] + [_vp] * 7 + [ctypes.c_size_t, _vp])
+_c_masked_ws = _by_bytes("sparse_attn_forward_masked_workspace_size", [_cp], ctypes.c_size_t)
+_c_weights = _by_bytes("sparse_attn_cache_weights", [_cp] + [_vp] * 5 + [ctypes.c_float, _vp, _vp])
+_c_evict = _by_bytes("sparse_attn_cache_evict", [_cp] + [_vp] * 8)
+
+
+def _view(t: torch.Tensor, dtype, name: str, dev: int):
+    """The strides of a view [B, H, N, d] with a contiguous d on CUDA device `dev`."""
+    if t.dtype is not dtype or t.dim() != 4 or t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor [B, H, N, d] of {dtype}, on the first tensor's device")
     sb, sh, sn, sd = t.stride()
     if sd != 1 and t.shape[3] != 1:
         raise ValueError(f"{name} must have a contiguous last dimension")
-    return sa_strides(sb, sh, sn)
+    return sb, sh, sn
 
 
-def _flat(t, dtype, name, ref, shape=None):
-    """A contiguous tensor on ref's device (or None), its pointer."""
+def _flat(t, dtype, name, dev, shape=None) -> int:
+    """The address of a contiguous tensor on device `dev` (0 for None)."""
     if t is None:
-        return None
-    if t.dtype != dtype or t.device != ref.device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of {dtype} on {ref.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+        return 0
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {dtype} on the first tensor's device")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
     return t.data_ptr()
 
 
-class _On:
-    """The tensor's device made current for a call, and the call's stream; tensors made for a call
-    on another stream than the current one are recorded there."""
-
-    def __init__(self, ref, stream):
-        self.guard = None
-        if ref.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(ref.device)
-        self.stream = stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        cur = torch.cuda.current_stream()
-        self.other = self.stream if self.stream is not None and self.stream != cur else None
-        return (self.stream or cur).cuda_stream
-
-    def keep(self, *tensors):
-        if self.other is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.other)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _on_device(f):
+    """Runs f with the device of its first tensor current."""
+    @functools.wraps(f)
+    def g(first, *args, **kw):
+        dev = first.get_device()
+        if dev >= 0 and dev != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return f(first, *args, **kw)
+        return f(first, *args, **kw)
+    return g
 
 
+def _raw_stream(stream, dev: int, *made) -> int:
+    """The stream's handle.  Tensors made for a call on another stream than the current one are
+    recorded there."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    for t in made:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+@_on_device
 def sparse_attn_rope(q: torch.Tensor, k: torch.Tensor | None = None, *, axes=(44, 42, 42),
                      theta: float = 10000.0, inv_freq=None, pairing: str = "interleaved",
                      grid=None, voxel=None, offset=(0, 0, 0), positions: torch.Tensor | None = None,
@@ -493,96 +514,94 @@ def sparse_attn_rope(q: torch.Tensor, k: torch.Tensor | None = None, *, axes=(44
     N = T*H*W, tokens in raster order, or in sparse_attn_voxel_permute's when `voxel` is given, plus
     `offset`.  inv_freq: r/2 frequencies (radians per position) instead of theta's.  inverse rotates
     back, which is also the gradient.  out: the output (or a pair of them); it may be the input."""
-    dtype = q.dtype
+    dtype, dev = q.dtype, q.get_device()
     if dtype not in _OUT:
         raise ValueError("q must be bfloat16 or float32")
-    qs = _view(q, dtype, "q")
+    qs = _view(q, dtype, "q", dev)
     B, H, N, d = q.shape
     oq, ok = out if isinstance(out, (tuple, list)) else (out, None)
     if k is not None:
-        ks = _view(k, dtype, "k", q)
+        ks = _STRIDES.pack(*_view(k, dtype, "k", dev))
         if k.shape[0] != B or k.shape[2] != N or k.shape[3] != d:
             raise ValueError("k must be [B, Hk, N, d] with q's B, N and d")
     elif ok is not None:
         raise ValueError("an output for k without k")
-    axes = tuple(int(a) for a in axes)
-    if not 1 <= len(axes) <= 3:
+    na = len(axes)
+    if not 1 <= na <= 3:
         raise ValueError("one to three axes")
     if pairing not in _PAIRINGS:
         raise ValueError("pairing must be 'interleaved' or 'half'")
-    r = sa_rope(B, N, d, len(axes))
-    for i, a in enumerate(axes):
-        r.axis_dim[i] = a
-    r.pairing, r.dtype, r.inverse, r.theta = _PAIRINGS[pairing], _OUT[dtype], int(inverse), float(theta)
+    freq = 0
     if inv_freq is not None:
         f = [float(x) for x in inv_freq]
         if len(f) != sum(axes) // 2:
             raise ValueError("inv_freq must have one value per rotated pair")
-        r.inv_freq = (ctypes.c_double * len(f))(*f)
+        host = (ctypes.c_double * len(f))(*f)
+        freq = ctypes.addressof(host)
     if (positions is None) == (grid is None):
         raise ValueError("positions or grid, and not both")
+    pos = pos_b = 0
+    cells, order = (0, 0, 0, 0, 0, 0), 0
     if positions is not None:
         if voxel is not None or any(offset):
             raise ValueError("voxel and offset go with grid")
         shared = positions.dim() == 2
-        r.positions = _flat(positions, torch.int32, "positions", q,
-                            (N, len(axes)) if shared else (B, N, len(axes)))
-        r.positions_b = 0 if shared else N * len(axes)
+        pos = _flat(positions, torch.int32, "positions", dev, (N, na) if shared else (B, N, na))
+        pos_b = 0 if shared else N * na
     else:
-        r.grid = sa_voxel_grid(*grid, *(voxel if voxel is not None else (0, 0, 0)))
-        r.voxel_order = 0 if voxel is None else 1
-        for i in range(3):
-            r.offset[i] = int(offset[i])
-    on = _On(q, stream)
-    with on as s:
-        y = torch.empty_like(q) if oq is None else oq
-        ys = _view(y, dtype, "out", q)
-        if y.shape != q.shape:
-            raise ValueError("out must have q's shape")
-        z = zs = None
-        if k is not None:
-            z = torch.empty_like(k) if ok is None else ok
-            zs = _view(z, dtype, "out of k", q)
-            if z.shape != k.shape:
-                raise ValueError("out of k must have k's shape")
-        on.keep(y, z)
-        st = lib.sparse_attn_rope(r, H, q.data_ptr(), qs, y.data_ptr(), ys,
-                                  0 if k is None else k.shape[1], _ptr(k), None if k is None else ks,
-                                  _ptr(z), zs, s)
+        order = 0 if voxel is None else 1
+        cells = (*grid, *(voxel or (0, 0, 0)))
+    p = _ROPE.pack(B, N, d, na, *axes, *(0,) * (3 - na), _PAIRINGS[pairing], _OUT[dtype],
+                   1 if inverse else 0, theta, freq, pos, pos_b, *cells, order, *offset)
+    y = torch.empty_like(q) if oq is None else oq
+    if y.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    ys = _STRIDES.pack(*_view(y, dtype, "out", dev))
+    z = None
+    if k is None:
+        st = _c_rope(p, H, q.data_ptr(), _STRIDES.pack(*qs), y.data_ptr(), ys, 0, None, None, None, None,
+                     _raw_stream(stream, dev, y))
+    else:
+        z = torch.empty_like(k) if ok is None else ok
+        if z.shape != k.shape:
+            raise ValueError("out of k must have k's shape")
+        st = _c_rope(p, H, q.data_ptr(), _STRIDES.pack(*qs), y.data_ptr(), ys, k.shape[1], k.data_ptr(), ks,
+                     z.data_ptr(), _STRIDES.pack(*_view(z, dtype, "out of k", dev)),
+                     _raw_stream(stream, dev, y, z))
     if st != SA_OK:
         raise SparseAttnError(st, "sparse_attn_rope")
     return y if k is None else (y, z)
 
 
-def _masked(q, k, scale, cap, slopes, causal, docs_q, docs_k, prefix, lengths):
-    """sa_masked of q [B, Hq, Nq, d] and k [B, Hkv, Nk, d], without v and o."""
-    qs, ks = _view(q, torch.bfloat16, "q"), _view(k, torch.bfloat16, "k", q)
-    B, H, Nq, d = q.shape
-    Hk, Nk = k.shape[1], k.shape[2]
-    if k.shape[0] != B or k.shape[3] != d or not Hk or H % Hk:
+def _mask_fields(q, k, dev, slopes, docs_q, docs_k, prefix, lengths):
+    """The mask's tables: (number of documents, their addresses, tensors to keep)."""
+    B, H = q.shape[:2]
+    if k.shape[0] != B or k.shape[3] != q.shape[3] or not k.shape[1] or H % k.shape[1]:
         raise ValueError("k must be [B, Hk, Nk, d] with q's B and d, and H a multiple of Hk")
-    p = sa_masked(B, H, Hk, Nq, Nk, d, 1.0 / math.sqrt(d) if scale is None else scale)
-    p.q, p.k, p.cap, p.causal = qs, ks, float(cap), int(causal)
-    p.slopes = _flat(slopes, torch.float32, "slopes", q, (H,))
-    if (docs_q is None) != (docs_k is None) or (prefix is not None and docs_q is None):
-        raise ValueError("docs_q and docs_k come together, prefix with them")
-    keep = None
-    if docs_q is not None:
+    slopes = _flat(slopes, torch.float32, "slopes", dev, (H,))
+    n, made = 0, ()
+    if docs_q is None:
+        if docs_k is not None or prefix is not None:
+            raise ValueError("docs_q and docs_k come together, prefix with them")
+        dq = dk = px = 0
+    else:
+        if docs_k is None:
+            raise ValueError("docs_q and docs_k come together, prefix with them")
         n = docs_q.shape[-1] - 1
         if n < 1:
             raise ValueError("docs_q must hold the bounds of at least one document")
-        if docs_q.dim() == 1:
+        if docs_q.dim() == 1 and B > 1:
             docs_q, docs_k = (t.expand(B, n + 1).contiguous() for t in (docs_q, docs_k))
             prefix = None if prefix is None else prefix.expand(B, n).contiguous()
-        p.ndocs = n
-        p.docs_q = _flat(docs_q, torch.int32, "docs_q", q, (B, n + 1))
-        p.docs_k = _flat(docs_k, torch.int32, "docs_k", q, (B, n + 1))
-        p.prefix = _flat(prefix, torch.int32, "prefix", q, (B, n))
-        keep = (docs_q, docs_k, prefix)
-    p.lengths = _flat(lengths, torch.int32, "lengths", q, (B,))
-    return p, keep
+            made = (docs_q, docs_k, prefix)
+        one = docs_q.dim() == 1
+        dq = _flat(docs_q, torch.int32, "docs_q", dev, (n + 1,) if one else (B, n + 1))
+        dk = _flat(docs_k, torch.int32, "docs_k", dev, (n + 1,) if one else (B, n + 1))
+        px = _flat(prefix, torch.int32, "prefix", dev, (n,) if one else (B, n))
+    return n, slopes, dq, dk, px, _flat(lengths, torch.int32, "lengths", dev, (B,)), made
 
 
+@_on_device
 def sparse_attn_forward_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
                                scale: float | None = None, cap: float = 0.0,
                                slopes: torch.Tensor | None = None, causal: int = 0,
@@ -602,37 +621,40 @@ def sparse_attn_forward_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     (docs_q, docs_k int32 [n+1] or [B, n+1]; or the first lengths[b] keys), up to the end of its
     frame when `causal` (tokens per frame, 1: per token), and the document's first `prefix` keys.  A
     document's rows are its last positions, so one new token over a cache is Nq = 1 with lengths."""
-    p, keep = _masked(q, k, scale, cap, slopes, causal, docs_q, docs_k, prefix, lengths)
-    p.v = _view(v, torch.bfloat16, "v", q)
+    dev = q.get_device()
+    qs, ks = _view(q, torch.bfloat16, "q", dev), _view(k, torch.bfloat16, "k", dev)
+    vs = _view(v, torch.bfloat16, "v", dev)
     if v.shape != k.shape:
         raise ValueError("v must have k's shape")
-    on = _On(q, stream)
-    with on as s:
-        if out is None:
-            out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
-        elif out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-        if out.dtype not in _OUT:
-            raise ValueError("out must be bfloat16 or float32")
-        p.out_dtype, p.o = _OUT[out.dtype], _view(out, out.dtype, "out", q)
-        if lse is True:
-            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-        elif lse is False:
-            lse = None
-        need = lib.sparse_attn_forward_masked_workspace_size(p)
-        if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        on.keep(out, lse, workspace, *(keep or ()))
-        st = lib.sparse_attn_forward_masked(
-            p, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-            _flat(lse, torch.float32, "lse", q, q.shape[:3]), _flat(status, torch.int32, "status", q),
-            _flat(workspace, torch.uint8, "workspace", q),
-            0 if workspace is None else workspace.numel(), s)
+    n, sl, dq, dk, px, lens, made = _mask_fields(q, k, dev, slopes, docs_q, docs_k, prefix, lengths)
+    B, H, Nq, d = shape = q.shape
+    if out is None:
+        out = q.new_empty(shape, dtype=out_dtype)
+    elif out.shape != shape:
+        raise ValueError("out must have q's shape")
+    if out.dtype not in _OUT:
+        raise ValueError("out must be bfloat16 or float32")
+    if lse is True:
+        lse = q.new_empty(shape[:3], dtype=torch.float32)
+    elif lse is False:
+        lse = None
+    p = _MASKED.pack(B, H, k.shape[1], Nq, k.shape[2], d, 1.0 / math.sqrt(d) if scale is None else scale,
+                     _OUT[out.dtype], *qs, *ks, *vs, *_view(out, out.dtype, "out", dev), cap, sl, causal, n,
+                     dq, dk, px, lens)
+    need = _c_masked_ws(p)
+    if need and workspace is None:
+        workspace = q.new_empty(need, dtype=torch.uint8)
+    st = _c_masked(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                   _flat(lse, torch.float32, "lse", dev, shape[:3]), _flat(status, torch.int32, "status", dev),
+                   _flat(workspace, torch.uint8, "workspace", dev),
+                   0 if workspace is None else workspace.numel(),
+                   _raw_stream(stream, dev, out, lse, workspace, *made))
     if st != SA_OK:
         raise SparseAttnError(st, "sparse_attn_forward_masked")
     return out, lse
 
 
+@_on_device
 def sparse_attn_cache_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor,
                               weights: torch.Tensor | None = None, *, decay: float = 1.0,
                               scale: float | None = None, cap: float = 0.0,
@@ -647,23 +669,26 @@ def sparse_attn_cache_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tenso
     the heads that share its key head): fp32 [B, Hk, Nk].  lse, scale and the masks as in the forward
     that wrote lse.  weights None starts from zero; out=weights accumulates in place; entries past
     lengths[b] stay as they were (zero when there were none)."""
-    p, keep = _masked(q, k, scale, cap, slopes, causal, docs_q, docs_k, prefix, lengths)
+    dev = q.get_device()
+    qs, ks = _view(q, torch.bfloat16, "q", dev), _view(k, torch.bfloat16, "k", dev)
+    n, sl, dq, dk, px, lens, made = _mask_fields(q, k, dev, slopes, docs_q, docs_k, prefix, lengths)
+    B, H, Nq, d = q.shape
     shape = k.shape[:3]
-    on = _On(q, stream)
-    with on as s:
-        if out is None:
-            make = torch.zeros if weights is None and lengths is not None else torch.empty
-            out = make(shape, dtype=torch.float32, device=q.device)
-        on.keep(out, *(keep or ()))
-        st = lib.sparse_attn_cache_weights(
-            p, q.data_ptr(), k.data_ptr(), _flat(lse, torch.float32, "lse", q, q.shape[:3]),
-            _flat(weights, torch.float32, "weights", q, shape), _flat(out, torch.float32, "out", q, shape),
-            float(decay) if weights is not None else 0.0, _flat(status, torch.int32, "status", q), s)
+    if out is None:
+        make = torch.zeros if weights is None and lengths is not None else torch.empty
+        out = make(shape, dtype=torch.float32, device=q.device)
+    p = _MASKED.pack(B, H, shape[1], Nq, shape[2], d, 1.0 / math.sqrt(d) if scale is None else scale, 0,
+                     *qs, *ks, 0, 0, 0, 0, 0, 0, cap, sl, causal, n, dq, dk, px, lens)
+    st = _c_weights(p, q.data_ptr(), k.data_ptr(), _flat(lse, torch.float32, "lse", dev, (B, H, Nq)),
+                    _flat(weights, torch.float32, "weights", dev, shape),
+                    _flat(out, torch.float32, "out", dev, shape), 0.0 if weights is None else decay,
+                    _flat(status, torch.int32, "status", dev), _raw_stream(stream, dev, out, *made))
     if st != SA_OK:
         raise SparseAttnError(st, "sparse_attn_cache_weights")
     return out
 
 
+@_on_device
 def sparse_attn_cache_evict(weights: torch.Tensor, k: torch.Tensor | None, v: torch.Tensor | None,
                             budget: int, *, sink: int = 0, recent: int = 0,
                             lengths: torch.Tensor | None = None, out=None,
@@ -675,41 +700,43 @@ def sparse_attn_cache_evict(weights: torch.Tensor, k: torch.Tensor | None, v: to
     int32 [B, Hk, budget], k, v [B, Hk, budget, d], weights [B, Hk, budget]): the kept entries in their
     order; behind a shorter one kept is -1 and the rows of `out` = (k, v, weights) are left as they
     were (zero when out is not given)."""
-    if weights.dim() != 3 or not weights.is_cuda:
+    dev = weights.get_device()
+    if weights.dim() != 3 or dev < 0:
         raise ValueError("weights must be a CUDA tensor [B, Hk, Nk]")
     B, H, N = weights.shape
     if (k is None) != (v is None):
         raise ValueError("k and v come together")
-    budget = int(budget)
-    p = sa_evict(B, H, N, 128 if k is None else k.shape[-1], budget, int(sink), int(recent))
-    w = _flat(weights, torch.float32, "weights", weights)
-    p.lengths = _flat(lengths, torch.int32, "lengths", weights, (B,))
-    on = _On(weights, stream)
-    with on as s:
+    if budget < 1:
+        raise ValueError("budget must be at least 1")
+    w = _flat(weights, torch.float32, "weights", dev)
+    lens = _flat(lengths, torch.int32, "lengths", dev, (B,))
+    d = 128
+    strides = (0,) * 12
+    if k is not None:
+        ks, vs = _view(k, torch.bfloat16, "k", dev), _view(v, torch.bfloat16, "v", dev)
+        d = k.shape[3]
+        if k.shape != v.shape or k.shape[:3] != weights.shape:
+            raise ValueError("k and v must be [B, Hk, Nk, d] with weights' B, Hk and Nk")
+    if out is None:
         make = torch.empty if lengths is None and budget <= N else torch.zeros
-        if out is None:
-            ko = vo = None
-            if k is not None and budget > 0:
-                ko, vo = (make((B, H, budget, t.shape[-1]), dtype=torch.bfloat16, device=weights.device)
-                          for t in (k, v))
-            wo = make((B, H, max(budget, 0)), dtype=torch.float32, device=weights.device)
-        else:
-            ko, vo, wo = out
-        if kept is None:
-            kept = torch.empty((B, H, max(budget, 0)), dtype=torch.int32, device=weights.device)
+        ko = vo = None
         if k is not None:
-            p.k, p.v = _view(k, torch.bfloat16, "k", weights), _view(v, torch.bfloat16, "v", weights)
-            if k.shape != v.shape or tuple(k.shape[:3]) != (B, H, N):
-                raise ValueError("k and v must be [B, Hk, Nk, d] with weights' B, Hk and Nk")
-            if budget > 0:
-                p.k_out, p.v_out = (_view(t, torch.bfloat16, "out", weights) for t in (ko, vo))
-                if tuple(ko.shape) != (B, H, budget, k.shape[3]) or vo.shape != ko.shape:
-                    raise ValueError("out must hold k and v as [B, Hk, budget, d]")
-        on.keep(ko, vo, wo, kept)
-        st = lib.sparse_attn_cache_evict(
-            p, w, _ptr(k), _ptr(v), _flat(kept, torch.int32, "kept", weights, (B, H, max(budget, 0))),
-            _ptr(ko) if k is not None else None, _ptr(vo) if k is not None else None,
-            _flat(wo, torch.float32, "out", weights, (B, H, max(budget, 0))), s)
+            ko, vo = (make((B, H, budget, d), dtype=torch.bfloat16, device=weights.device) for _ in range(2))
+        wo = make((B, H, budget), dtype=torch.float32, device=weights.device)
+    else:
+        ko, vo, wo = out
+    if kept is None:
+        kept = weights.new_empty((B, H, budget), dtype=torch.int32)
+    kp = vp = kop = vop = 0
+    if k is not None:
+        if ko.shape != (B, H, budget, d) or vo.shape != ko.shape:
+            raise ValueError("out must hold k and v as [B, Hk, budget, d]")
+        strides = (*ks, *vs, *_view(ko, torch.bfloat16, "out", dev), *_view(vo, torch.bfloat16, "out", dev))
+        kp, vp, kop, vop = k.data_ptr(), v.data_ptr(), ko.data_ptr(), vo.data_ptr()
+    st = _c_evict(_EVICT.pack(B, H, N, d, budget, sink, recent, lens, *strides), w, kp, vp,
+                  _flat(kept, torch.int32, "kept", dev, (B, H, budget)), kop, vop,
+                  _flat(wo, torch.float32, "out", dev, (B, H, budget)),
+                  _raw_stream(stream, dev, ko, vo, wo, kept))
     if st != SA_OK:
         raise SparseAttnError(st, "sparse_attn_cache_evict")
     return kept, ko, vo, wo

@@ -12,9 +12,12 @@
 // columns, so an epilogue thread owns one key and sums over queries in its own
 // registers: no cross-lane reduction, no atomics, a fixed order.  A unit is one
 // 128-key tile; its K stays in shared memory while Q tiles of up to 256 packed
-// rows (query * R + head-in-group) stream by.  Two sets of four warps take
-// alternate Q tiles (one TMEM buffer each).  With many rows the bound is the one
-// exponential a pair; with one token per sequence it is the read of K.
+// rows (query * R + head-in-group) stream by.  Q tiles alternate between two
+// TMEM buffers; each buffer has its own MMA warp (its waits and commits overlap
+// the other's MMAs; they take turns, so that one buffer's sums run beside the
+// other's MMA) and two sets of four epilogue warps, one per half of the columns.
+// With many rows the bound is the tensor core (one exponential a pair is 0.8 of
+// its time on the MUFU); with one token per sequence it is the read of K.
 #include <atomic>
 #include <climits>
 
@@ -31,14 +34,15 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxStages = 6;
 
 struct WCfg {
-  static constexpr int kEpiWarps = 8, kMmaWarp = 8;  // and one warp that loads
-  static constexpr int kThreads = 320;
+  static constexpr int kEpiWarps = 16, kMmaWarp = 16, kTmaWarp = 18;
+  // 640 threads launch with 96 registers each = 61440 = 512 * 104 + 128 * 64
+  static constexpr int kThreads = 640, kRegEpi = 104, kRegOther = 64;
   static constexpr int kCols = 256;  // columns of a TMEM buffer
 };
 
 struct WBars {
   uint64_t kfull[kMaxStages], kempty[kMaxStages], qfull[kMaxStages], qempty[kMaxStages];
-  uint64_t dfull[2], dempty[2], xfull[2], xempty[2], drain;
+  uint64_t dfull[2], dempty[2], xfull[2], xempty[2], turn[2], drain[2];
   uint32_t tmem_base;
   int abort;
 };
@@ -67,32 +71,33 @@ __device__ __forceinline__ void tile_range(const MaskDev& m, const WPlan& p, int
 
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(WCfg::kThreads, 1)
-    sa_cache_weights_kernel(const WeightArgs wa, const WPlan p, const __grid_constant__ CUtensorMap tm_q,
+    sa_cache_weights_kernel(const __grid_constant__ WeightArgs wa, const __grid_constant__ WPlan p, const __grid_constant__ CUtensorMap tm_q,
                             const __grid_constant__ CUtensorMap tm_k) {
   const MaskedArgs& a = wa.m;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sK = smem;
   uint8_t* sQ = sK + p.kst * p.ktile;
-  float* sL = reinterpret_cast<float*>(sQ + p.qst * p.kqbytes);     // [8 warps][256] lse in exp2 units
-  float* sX = sL + WCfg::kEpiWarps * WCfg::kCols;                   // [2][128] sums of set 1
-  WBars* bars = reinterpret_cast<WBars*>(sX + 2 * 128);
+  float* sL = reinterpret_cast<float*>(sQ + p.qst * p.kqbytes);  // [16 warps][128] -lse in exp2 units
+  float* sX = sL + WCfg::kEpiWarps * WCfg::kCols / 2;            // [2][3][128] sums of sets 1 to 3
+  WBars* bars = reinterpret_cast<WBars*>(sX + 2 * 3 * 128);
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&bars->kfull[s], 1);
-      mbar_init(&bars->kempty[s], 1);
+      mbar_init(&bars->kempty[s], 2);
       mbar_init(&bars->qfull[s], 1);
       mbar_init(&bars->qempty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->dfull[b], 1);
-      mbar_init(&bars->dempty[b], 128);
-      mbar_init(&bars->xfull[b], 128);
+      mbar_init(&bars->dempty[b], 256);
+      mbar_init(&bars->xfull[b], 3 * 128);
       mbar_init(&bars->xempty[b], 128);
+      mbar_init(&bars->turn[b], 1);
+      mbar_init(&bars->drain[b], 1);
     }
-    mbar_init(&bars->drain, 1);
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -110,44 +115,49 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
+  if (warp < WCfg::kEpiWarps)
+    reg_alloc<WCfg::kRegEpi>();
+  else
+    reg_dealloc<WCfg::kRegOther>();
+
   if (warp < WCfg::kEpiWarps) {
     // ------------------------------------------------------------ epilogue
-    const int es = warp >> 2, tid = threadIdx.x & 127;
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    float* wL = sL + warp * WCfg::kCols;
-    const int nch = p.NR / 32;
-    // Column c * 32 + lane is query tile * qn + qo[c] of head ho: fixed per lane.
-    int off[8], qo[8];
+    // Set = warp / 4: TMEM buffer set / 2, columns' half set % 2.
+    const int set = warp >> 2, d = set >> 1, half = set & 1, tid = threadIdx.x & 127;
+    const int H = p.NR / 2, col0 = half * H;
+    const uint32_t sbase = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + d * WCfg::kCols + col0;
+    float* wL = sL + warp * (WCfg::kCols / 2);
+    // Column col0 + c * 32 + lane is query tile * qn + qo[c]: fixed per lane.
+    int off[4], qo[4];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const int r = c * 32 + lane;
-      qo[c] = r < p.rows ? r / a.R : INT_MAX / 2;
-      off[c] = r < p.rows ? (r % a.R) * a.Nq + r / a.R : 0;
+    for (int c = 0; c < 4; ++c) {
+      const int r = col0 + c * 32 + lane;
+      const bool row = c * 32 + lane < H && r < p.rows;
+      qo[c] = row ? r / a.R : INT_MAX / 2;
+      off[c] = row ? (r % a.R) * a.Nq + r / a.R : 0;
     }
+    const float sl = a.scale_log2;
     uint32_t it = 0, xn = 0;
-    for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
+    for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x, ++xn) {
       const int bh = static_cast<int>(u / p.ktiles), k0 = static_cast<int>(u % p.ktiles) * 128;
       const int b = bh / a.Hkv, hk = bh % a.Hkv;
       int t0, t1;
       tile_range(a.mask, p, b, k0, &t0, &t1);
       const int key = k0 + tid;
-      const bool solo = t1 - t0 == 1;
       const float* lse = wa.lse + (int64_t(b) * a.Hq + int64_t(hk) * a.R) * a.Nq;
       const float* slopes = BIAS ? a.slopes + hk * a.R : nullptr;
-      const float sl = a.scale_log2;
       float total = 0.f;
-      float next[8];
-      int first = t0 + ((it ^ es) & 1);
+      float next[4];
+      const int first = t0 + ((it ^ d) & 1);
       auto fetch = [&](int t) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          next[c] = c < nch && qo[c] < a.Nq - t * p.qn ? __ldg(lse + int64_t(t) * p.qn + off[c]) : 0.f;
+        for (int c = 0; c < 4; ++c) next[c] = qo[c] < a.Nq - t * p.qn ? __ldg(lse + int64_t(t) * p.qn + off[c]) : 0.f;
       };
       if (first < t1) fetch(first);
-      // the entry as it was, and the keys that take part at all
+      // set 0 writes: the entry as it was, and whether it takes part
       const int len = a.mask.len ? clamp_int(__ldg(a.mask.len + b), 0, a.Nk) : a.Nk;
       const int64_t wi = int64_t(bh) * a.Nk + key;
-      const bool mine = key < a.Nk && (solo ? ((it ^ es) & 1) == 0 : es == 0);
+      const bool mine = key < a.Nk && set == 0;
       float was = 0.f;
       if (mine && wa.w_in && (key >= len || wa.decay != 0.f)) was = wa.w_in[wi];
       for (int t = first; t < t1; t += 2) {
@@ -156,13 +166,11 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
         uint32_t dead = 0;
         __syncwarp();
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          if (c < nch) {
-            const bool row = qo[c] < a.Nq - t * p.qn;
-            const bool fin = isfinite(next[c]);
-            wL[c * 32 + lane] = row && fin ? next[c] * kLog2e : INFINITY;
-            if (__any_sync(0xffffffffu, row && !fin)) dead |= 1u << c;
-          }
+        for (int c = 0; c < 4; ++c) {
+          const bool row = qo[c] < a.Nq - t * p.qn;
+          const bool fin = isfinite(next[c]);
+          wL[c * 32 + lane] = row && fin ? -next[c] * kLog2e : -INFINITY;
+          if (__any_sync(0xffffffffu, row && !fin)) dead |= 3u << (2 * c);
         }
         __syncwarp();
         const int qa = t * p.qn, qz = min(qa + p.qn, a.Nq) - 1;
@@ -170,21 +178,50 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
         if (a.mask.causal || a.mask.nd || a.mask.len)
           edge = row_span(a.mask, b, qz).lo > k0 || row_span(a.mask, b, qa).hi < min(k0 + 128, a.Nk);
         if (t + 2 < t1) fetch(t + 2);
-        if (!mbar_wait(&bars->dfull[es], (n >> 1) & 1, abort)) goto done;
+        if (!mbar_wait(&bars->dfull[d], (n >> 1) & 1, abort)) goto done;
+        __syncwarp();
         tc_fence_after();
-        const uint32_t sbase = tmem + lane_base + es * WCfg::kCols;
-        uint64_t acc[4] = {0, 0, 0, 0};
-        for (int c = 0; c < nch; ++c) {
-          uint32_t r[32];
-          __syncwarp();
-          tmem_ld32(sbase + c * 32, r);
-          tmem_ld_wait();
-          const float4* l4 = reinterpret_cast<const float4*>(wL + c * 32);
-          const bool care = edge || ((dead >> c) & 1);
-          int lo = 0, hi = INT_MAX, pos = 0;
-          float slope = 0.f;
-          if (edge || BIAS) {
-            const int rr = c * 32 + lane;
+        uint64_t acc[2] = {0, 0};
+        // One pair's exponents from its raw products and -lse.
+        auto exponents = [&](uint64_t x, uint64_t L, int c) -> uint64_t {
+          uint64_t v = x;
+          if (CAP) {
+            const uint64_t ex = mul2(x, f2(a.cap_k1, a.cap_k1));
+            const uint64_t d1 = add2(f2(fast_exp2(f2lo(ex)), fast_exp2(f2hi(ex))), f2(1.f, 1.f));
+            v = fma2(f2(fast_rcp(f2lo(d1)), fast_rcp(f2hi(d1))), f2(-2.f * a.cap_log2, -2.f * a.cap_log2),
+                     f2(a.cap_log2, a.cap_log2));
+          }
+          return CAP ? add2(v, L) : fma2(v, f2(sl, sl), L);
+        };
+        // The plain columns of the tile: the next 16 load while 16 are summed.
+        auto plain = [&]() {
+          float buf[2][16];
+          tmem_ld16(sbase, reinterpret_cast<uint32_t*>(buf[0]));
+          auto chunk = [&](int c, float* x, float* y) {
+            tmem_ld_wait();
+            if (c + 16 < H) tmem_ld16(sbase + c + 16, reinterpret_cast<uint32_t*>(y));
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const ulonglong2 L = *reinterpret_cast<const ulonglong2*>(wL + c + e);
+              const uint64_t v0 = exponents(f2(x[e], x[e + 1]), L.x, c + e);
+              const uint64_t v1 = exponents(f2(x[e + 2], x[e + 3]), L.y, c + e + 2);
+              acc[0] = add2(acc[0], f2(fast_exp2(f2lo(v0)), fast_exp2(f2hi(v0))));
+              acc[1] = add2(acc[1], f2(fast_exp2(f2lo(v1)), fast_exp2(f2hi(v1))));
+            }
+          };
+          for (int c = 0; c < H; c += 32) {
+            chunk(c, buf[0], buf[1]);
+            if (c + 16 < H) chunk(c + 16, buf[1], buf[0]);
+          }
+        };
+        // With masked or dead columns, or a bias: each column's span, position
+        // and slope come from the lane that holds them.
+        auto careful = [&]() {
+          for (int c = 0; c < H; c += 16) {
+            float x[16];
+            int lo = 0, hi = INT_MAX, pos = 0;
+            float slope = 0.f;
+            const int rr = col0 + c + (lane & 15);
             if (rr < p.rows && qa + rr / a.R < a.Nq) {
               const Span sp = row_span(a.mask, b, qa + rr / a.R);
               lo = sp.lo;
@@ -192,70 +229,49 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
               pos = sp.pos;
               if (BIAS) slope = -__ldg(slopes + rr % a.R) * kLog2e;
             }
-          }
-          const uint64_t sl2 = f2(sl, sl);
+            __syncwarp();
+            tmem_ld16(sbase + c, reinterpret_cast<uint32_t*>(x));
+            tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 L = l4[e];
-            const float Lf[4] = {L.x, L.y, L.z, L.w};
-            float y[4];
+            for (int e = 0; e < 16; e += 2) {
+              const float2 L = *reinterpret_cast<const float2*>(wL + c + e);
+              const uint64_t v = exponents(f2(x[e], x[e + 1]), f2(L.x, L.y), c + e);
+              float y[2] = {f2lo(v), f2hi(v)};
 #pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              const uint64_t x = f2(__uint_as_float(r[4 * e + i]), __uint_as_float(r[4 * e + i + 1]));
-              uint64_t v;
-              if (CAP) {
-                const uint64_t ex = mul2(x, f2(a.cap_k1, a.cap_k1));
-                const uint64_t d1 = add2(f2(fast_exp2(f2lo(ex)), fast_exp2(f2hi(ex))), f2(1.f, 1.f));
-                v = fma2(f2(fast_rcp(f2lo(d1)), fast_rcp(f2hi(d1))), f2(-2.f * a.cap_log2, -2.f * a.cap_log2),
-                         f2(a.cap_log2, a.cap_log2));
-              } else if (BIAS) {
-                v = mul2(x, sl2);
+              for (int i = 0; i < 2; ++i) {
+                const int clo = __shfl_sync(0xffffffffu, lo, e + i), chi = __shfl_sync(0xffffffffu, hi, e + i);
+                if (BIAS) {
+                  const float s = __shfl_sync(0xffffffffu, slope, e + i);
+                  const int cp = __shfl_sync(0xffffffffu, pos, e + i);
+                  y[i] = fmaf(s, fabsf(static_cast<float>(cp - key)), y[i]);
+                }
+                if (key < clo || key >= chi || (i ? L.y : L.x) == -INFINITY) y[i] = -INFINITY;
               }
-              if (BIAS) {
-                const float s0 = __shfl_sync(0xffffffffu, slope, 4 * e + i);
-                const float s1 = __shfl_sync(0xffffffffu, slope, 4 * e + i + 1);
-                const int p0 = __shfl_sync(0xffffffffu, pos, 4 * e + i);
-                const int p1 = __shfl_sync(0xffffffffu, pos, 4 * e + i + 1);
-                v = fma2(f2(s0, s1), f2(fabsf(static_cast<float>(p0 - key)), fabsf(static_cast<float>(p1 - key))), v);
-              }
-              if (CAP || BIAS)
-                v = sub2(v, f2(Lf[i], Lf[i + 1]));
-              else
-                v = fma2(x, sl2, f2(-Lf[i], -Lf[i + 1]));
-              y[i] = f2lo(v);
-              y[i + 1] = f2hi(v);
+              acc[0] = add2(acc[0], f2(fast_exp2(y[0]), fast_exp2(y[1])));
             }
-            if (care) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int clo = __shfl_sync(0xffffffffu, lo, 4 * e + i);
-                const int chi = __shfl_sync(0xffffffffu, hi, 4 * e + i);
-                if (key < clo || key >= chi || Lf[i] == INFINITY) y[i] = -INFINITY;
-              }
-            }
-            acc[e & 3] = add2(acc[e & 3], f2(fast_exp2(y[0]), fast_exp2(y[1])));
-            acc[e & 3] = add2(acc[e & 3], f2(fast_exp2(y[2]), fast_exp2(y[3])));
           }
-        }
+        };
+        if (BIAS || edge || dead)
+          careful();
+        else
+          plain();
         tc_fence_before();
-        mbar_arrive(&bars->dempty[es]);
-        const uint64_t s2 = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+        mbar_arrive(&bars->dempty[d]);
+        const uint64_t s2 = add2(acc[0], acc[1]);
         total += f2lo(s2) + f2hi(s2);
       }
       it += t1 > t0 ? t1 - t0 : 0;
-      if (t1 - t0 > 1) {
-        // set 1 hands its sums to set 0
-        const uint32_t xb = xn & 1, xp = (xn >> 1) & 1;
-        ++xn;
-        if (es == 1) {
-          if (!mbar_wait(&bars->xempty[xb], xp ^ 1, abort)) goto done;
-          sX[xb * 128 + tid] = total;
-          mbar_arrive(&bars->xfull[xb]);
-        } else {
-          if (!mbar_wait(&bars->xfull[xb], xp, abort)) goto done;
-          total += sX[xb * 128 + tid];
-          mbar_arrive(&bars->xempty[xb]);
-        }
+      // sets 1 to 3 hand their sums to set 0
+      const uint32_t xb = xn & 1, xp = (xn >> 1) & 1;
+      float* x = sX + xb * 3 * 128 + tid;
+      if (set != 0) {
+        if (!mbar_wait(&bars->xempty[xb], xp ^ 1, abort)) goto done;
+        x[(set - 1) * 128] = total;
+        mbar_arrive(&bars->xfull[xb]);
+      } else {
+        if (!mbar_wait(&bars->xfull[xb], xp, abort)) goto done;
+        total = (total + x[0]) + (x[128] + x[256]);
+        mbar_arrive(&bars->xempty[xb]);
       }
       if (mine) {
         if (key < len)
@@ -264,12 +280,15 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
           wa.w_out[wi] = was;  // an entry past the sequence stays as it was
       }
     }
-  } else if (warp == WCfg::kMmaWarp) {
+  } else if (warp < WCfg::kTmaWarp) {
     // ------------------------------------------------------------ MMA issue
+    const int d = warp - WCfg::kMmaWarp;  // the TMEM buffer
     if (lane == 0) {
       const uint32_t base = idesc_bf16(128, p.NR, false, false);
       const uint32_t kIdesc = a.neg_scale ? idesc_negate_b(base) : base;
-      const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sK);
+      const uint64_t dq = sw128_desc(smem_u32(sQ), 16, 1024), dk = sw128_desc(smem_u32(sK), 16, 1024);
+      const uint32_t q_lo = static_cast<uint32_t>(dq), q_hi = static_cast<uint32_t>(dq >> 32);
+      const uint32_t k_lo = static_cast<uint32_t>(dk), k_hi = static_cast<uint32_t>(dk >> 32);
       uint32_t it = 0, un = 0;
       bool ok = true;
       for (int64_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
@@ -279,31 +298,40 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
         if (t1 <= t0) continue;
         const uint32_t ks = un % p.kst;
         if (!mbar_wait(&bars->kfull[ks], (un / p.kst) & 1, abort)) break;
+        bool any = false;
         for (int t = t0; t < t1; ++t, ++it) {
-          const uint32_t qs = it % p.qst, d = it & 1;
+          if ((it & 1) != static_cast<uint32_t>(d)) continue;
+          any = true;
+          const uint32_t qs = it % p.qst;
           if (!mbar_wait(&bars->qfull[qs], (it / p.qst) & 1, abort) ||
-              !mbar_wait(&bars->dempty[d], ((it >> 1) & 1) ^ 1, abort)) {
+              !mbar_wait(&bars->dempty[d], ((it >> 1) & 1) ^ 1, abort) ||
+              (it > 0 && !mbar_wait(&bars->turn[d], ((it - 1) >> 1) & 1, abort))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t ka = k_addr + ks * p.ktile, qa = q_addr + qs * p.kqbytes;
+          const uint32_t kl = k_lo + ((ks * p.ktile) >> 4), ql = q_lo + ((qs * p.kqbytes) >> 4);
+          const uint32_t qstep = (p.NR * 128) >> 4;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + d * WCfg::kCols, sw128_desc(ka + (kk >> 2) * 128 * 128 + (kk & 3) * 32, 16, 1024),
-                   sw128_desc(qa + (kk >> 2) * p.NR * 128 + (kk & 3) * 32, 16, 1024), kIdesc, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t in = ((kk & 3) * 32) >> 4;
+            mma_ss_w(tmem + d * WCfg::kCols, kl + (((kk >> 2) * 128 * 128) >> 4) + in, k_hi,
+                     ql + (kk >> 2) * qstep + in, q_hi, kIdesc, kk > 0 ? 1u : 0u);
+            if (kk == D / 16 - 2) mbar_arrive(&bars->turn[d ^ 1]);  // (an MMA covers the hand-over)
+          }
           mma_commit(&bars->dfull[d]);
           mma_commit(&bars->qempty[qs]);
-          if (t == t1 - 1) mma_commit(&bars->kempty[ks]);
+          if (t + 2 >= t1) mma_commit(&bars->kempty[ks]);
         }
+        if (ok && !any) mbar_arrive(&bars->kempty[ks]);
         ++un;
       }
-      mma_commit(&bars->drain);
+      mma_commit(&bars->drain[d]);
       const long long c0 = clock64();
-      while (!mbar_test(&bars->drain, 0) && clock64() - c0 < kWaitLimitCycles) {
+      while (!mbar_test(&bars->drain[d], 0) && clock64() - c0 < kWaitLimitCycles) {
       }
     }
-  } else if (lane == 0) {
+  } else if (warp == WCfg::kTmaWarp && lane == 0) {
     // ------------------------------------------------------------ loads (TMA)
     const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sK);
     uint32_t it = 0, un = 0;
@@ -363,9 +391,18 @@ template <int D, bool CAP, bool BIAS>
 static cudaError_t launch_w(const WeightArgs& a, const WPlan& p, const CUtensorMap& tq, const CUtensorMap& tk,
                             int num_sms, cudaStream_t st) {
   auto kern = sa_cache_weights_kernel<D, CAP, BIAS>;
-  int smem = 1024 + p.kst * p.ktile + p.qst * p.kqbytes + WCfg::kEpiWarps * WCfg::kCols * 4 + 1024 +
+  int smem = 1024 + p.kst * p.ktile + p.qst * p.kqbytes + WCfg::kEpiWarps * WCfg::kCols * 2 + 2 * 3 * 128 * 4 +
              static_cast<int>(sizeof(WBars)) + 64;
   if (smem < 120 * 1024) smem = 120 * 1024;  // one block per SM owns its TMEM
+  static std::atomic<int> regs_ok{0};  // 0 unknown, 1 enough, 2 too few
+  if (regs_ok.load() == 0) {
+    cudaFuncAttributes attr;
+    cudaError_t e = cudaFuncGetAttributes(&attr, kern);
+    if (e != cudaSuccess) return e;
+    // setmaxnreg.inc waits until the block's launch registers cover the split
+    regs_ok.store(long(attr.numRegs) * WCfg::kThreads >= 512L * WCfg::kRegEpi + 128L * WCfg::kRegOther ? 1 : 2);
+  }
+  if (regs_ok.load() != 1) return cudaErrorLaunchOutOfResources;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t grid = p.units < num_sms ? p.units : num_sms;
@@ -383,7 +420,7 @@ cudaError_t launch_cache_weights(const WeightArgs& a, int num_sms, cudaStream_t 
   p.ktile = 128 * m.d * 2;
   p.kqbytes = p.NR * m.d * 2;
   p.qst = p.NR <= 64 ? kMaxStages : 2;
-  const int room = 212 * 1024 - p.qst * p.kqbytes;
+  const int room = 212 * 1024 - p.qst * p.kqbytes;  // the rest is under 15 KB
   p.kst = room / p.ktile < kMaxStages ? room / p.ktile : kMaxStages;
   p.ktiles = (m.Nk + 127) / 128;
   p.units = int64_t(m.B) * m.Hkv * p.ktiles;

@@ -76,6 +76,11 @@ __device__ __forceinline__ void named_barrier(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
+// Arrives on it without waiting.
+__device__ __forceinline__ void named_barrier_arrive(int id, int count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 // Brings the 128-byte line holding p into L2 (no register result).
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
@@ -173,6 +178,34 @@ __device__ __forceinline__ void bulk_wait_read() {
 }
 // Waits until this thread's bulk stores are complete in global memory.
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// ---------------------------------------------------- cluster launch control
+// Asks for a block of the grid that has not started yet, to be run by this one
+// instead.  The 16-byte answer lands at `dst` and completes 16 bytes of `bar`'s
+// transaction count.  Not to be called again once an answer held no block.
+__device__ __forceinline__ void request_block(void* dst, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(dst)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// The answer's blockIdx.x, or -1 when no block was left.
+__device__ __forceinline__ int64_t answered_block(const void* src) {
+  uint32_t x, ok;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b64 lo, hi;\n\t"
+      "ld.shared.v2.b64 {lo, hi}, [%2];\n\t"
+      "mov.b128 r, {lo, hi};\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %1, 1, 0, p;\n\t"
+      "mov.u32 %0, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+      : "=r"(x), "=r"(ok)
+      : "r"(smem_u32(src))
+      : "memory");
+  return ok ? static_cast<int64_t>(x) : -1;
+}
 
 // ------------------------------------------------------------------ tcgen05
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {

@@ -139,11 +139,13 @@ struct MaskedArgs {
   float scale_log2;    // |scale| log2(e)
   float cap_log2;      // cap log2(e), 0: no cap
   float cap_k1;        // 2 |scale| log2(e) / cap
-  int64_t rows;        // packed rows of a key head, R * Nq
+  // tanh's polynomial on raw products: x (scale_log2 + w (p1 + w (p2 + w p3))), w = x^2 <= cap_limit
+  float cap_p1, cap_p2, cap_p3, cap_limit;
   int64_t total_rows;  // B * Hq * Nq
-  // masked_plan: a unit is unit_rows packed rows of a key head; the first
+  // masked_plan: a Q tile holds qn queries of R heads each, a unit unit_rows / 128
+  // tiles, a key head row_blocks units; the first
   // full_units run whole, the other split_units in `splits` runs of keys
-  int32_t unit_rows, row_blocks, splits;
+  int32_t qn, unit_rows, row_blocks, splits;
   int64_t full_units, split_units;
   float* part_o;       // [split_units * splits, unit_rows, d] partials
   float* part_lse;     // [split_units * splits, unit_rows]

@@ -8,9 +8,9 @@
 //
 // Rows of one key head are packed, row = query * R + head-in-group (R = Hq/Hkv
 // query heads share a key head), so that K and V are read once for all of
-// them.  A block takes 256 packed rows as two 128-row Q tiles (128 rows and one
-// tile when a key head has no more).  K and V stream through one ring of
-// 128-row tiles by TMA; S = Q K^T and O stay in TMEM, P (bf16) overwrites its S.
+// them.  A unit is two Q tiles of up to 128 packed rows (whole queries), or one
+// when a key head has no more.  K and V stream through one ring of 128-row
+// tiles by TMA; S = Q K^T and O stay in TMEM, P (bf16) overwrites its S.
 // The MMA thread issues PV(j) of a tile and then S(j+1) of the same tile, so
 // while one tile's softmax runs the tensor core works for the other.  TMEM is
 // full (2 S + 2 O of 128 columns), so a tile's own S cannot be a step ahead:
@@ -19,8 +19,17 @@
 // rows x 128 columns whatever else runs, so two warps share each row, 64
 // columns each (16 softmax warps for two tiles).  They keep separate sums and
 // agree on the row's reference through a pair barrier each step.
-// Only the key span that the block's rows see is read; tiles that every row
+// Tiles are taken from the last key to the first: a distance bias is strongest
+// there, so the first tile's reference holds (from the far end every tile would
+// raise it).
+// Only the key span that the unit's rows see is read; tiles that every row
 // sees whole skip the mask.
+//
+// A block starts with its own unit and then takes units of blocks that have not
+// started (cluster launch control), so the next unit's Q, K and V load and its
+// first S is computed while the last one's softmax and output finish; with one
+// unit a block, each unit paid about 10 us for its start and end.  Units differ
+// in length (causal rows, documents); taking the next free one balances them.
 //
 // Units that do not fill a last wave of SMs (all of them, for a new token over
 // a long cache) are cut into `splits` runs of key tiles; each writes a
@@ -49,7 +58,8 @@ constexpr float kRaiseLimit = 4294967296.f;
 template <int D, int T>
 struct MCfg {
   static constexpr int kSoftWarps = 8 * T;  // per Q tile two sets of four: column halves
-  static constexpr int kMmaWarp = kSoftWarps, kTmaWarp = kSoftWarps + 1;
+  static constexpr int kMmaWarp = kSoftWarps, kTmaWarp = kSoftWarps + T,  // one MMA warp a tile
+                       kTailWarp = kTmaWarp + 1;
   // whole warpgroups: setmaxnreg acts on aligned groups of four warps
   static constexpr int kThreads = 32 * (kSoftWarps + 4);
   static constexpr bool kRegSplit = T == 2;
@@ -69,21 +79,29 @@ struct MCfg {
 template <int T, int STAGES>
 struct MBars {
   uint64_t full[STAGES], empty[STAGES];
-  uint64_t qfull[T], sfull[T], pfull[T], pair[T * 4], drain;
+  uint64_t sfull[T], pfull[T], ofull[T], ofree[T];
+  uint64_t qfull, qempty, next, tail, tail_here, turn[T], ring_full[2], ring_empty[2], drain[T];
+  uint4 answer;   // of the request for the next unit
+  int4 ring[2];   // unit (-1: no more), first key, key tiles, end of the span
   int flag[T * 4][2];
   uint32_t tmem_base;
   int abort;
+};
+
+template <bool M>
+struct Masked {
+  static constexpr bool value = M;
 };
 
 }  // namespace
 
 template <int D, int T, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
-    sa_masked_kernel(const MaskedArgs a, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v) {
+    sa_masked_kernel(const __grid_constant__ MaskedArgs a, const __grid_constant__ CUtensorMap tm_q,
+                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
   using C = MCfg<D, T>;
   constexpr int S = C::kStages;
-  constexpr int W = BIAS ? 16 : 32;  // S columns in registers at a time
+  constexpr int W = 16;  // S columns a register buffer holds
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem;
@@ -93,41 +111,38 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // The block's unit: heads outermost (their K and V stay in L2), row blocks
-  // from the last (with a causal mask the longest) to the first.  Units from
-  // full_units on are split over their keys.
-  int64_t u = blockIdx.x;
-  int split = 0, splits = 1;
-  int64_t part = -1;  // partial result number
-  if (u >= a.full_units) {
-    part = u - a.full_units;
-    splits = a.splits;
-    split = static_cast<int>(part % splits);
-    u = a.full_units + part / splits;
-  }
-  const int rb = a.row_blocks - 1 - static_cast<int>(u % a.row_blocks);
-  const int bh = static_cast<int>(u / a.row_blocks);
-  const int b = bh / a.Hkv, hk = bh % a.Hkv;
-  const int64_t row0 = int64_t(rb) * (128 * T);
-  const int rows = static_cast<int>(min64(128 * T, a.rows - row0));
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&bars->full[s], 1);
-      mbar_init(&bars->empty[s], 1);
+      mbar_init(&bars->empty[s], T);
     }
     for (int i = 0; i < T; ++i) {
-      mbar_init(&bars->qfull[i], 256);
       mbar_init(&bars->sfull[i], 1);
       mbar_init(&bars->pfull[i], 256);
+      mbar_init(&bars->ofull[i], 1);
+      mbar_init(&bars->ofree[i], 256);
     }
     for (int i = 0; i < T * 4; ++i) {
-      mbar_init(&bars->pair[i], 64);
       bars->flag[i][0] = bars->flag[i][1] = 0;
     }
-    mbar_init(&bars->drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->ring_full[i], 1);
+      mbar_init(&bars->ring_empty[i], C::kSoftWarps + T + 1);
+    }
+    mbar_init(&bars->qfull, 1);
+    mbar_init(&bars->qempty, T);
+    mbar_init(&bars->next, 1);
+    mbar_init(&bars->tail, 1);
+    mbar_init(&bars->tail_here, T);
+    for (int i = 0; i < T; ++i) mbar_init(&bars->turn[i], 1);
+    for (int i = 0; i < T; ++i) mbar_init(&bars->drain[i], 1);
     bars->abort = 0;
     fence_mbar_init();
+  }
+  if (a.qn * a.R < 128) {  // Q rows that no copy fills are zero for good
+    for (int i = threadIdx.x; i < C::kQBytes / 16; i += C::kThreads)
+      reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
   }
   if (warp == C::kMmaWarp) {
     tmem_alloc(&bars->tmem_base, C::kTmemCols);
@@ -138,14 +153,6 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  // Keys that any of the block's rows sees, and this split's run of tiles.
-  const int ulo = row_span(a.mask, b, static_cast<int>(row0 / a.R)).lo;
-  const int uhi = row_span(a.mask, b, static_cast<int>((row0 + rows - 1) / a.R)).hi;
-  const int ntiles = uhi > ulo ? (uhi - ulo + BN - 1) / BN : 0;
-  const int j0 = static_cast<int>(int64_t(ntiles) * split / splits);
-  const int n = static_cast<int>(int64_t(ntiles) * (split + 1) / splits) - j0;
-  const int key0 = ulo + j0 * BN;
-
   if (C::kRegSplit) {
     if (warp < C::kSoftWarps)
       reg_alloc<C::kRegSoft>();
@@ -153,178 +160,219 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
       reg_dealloc<C::kRegOther>();
   }
 
+  // Unit number -> heads outermost (their K and V stay in L2), row blocks from
+  // the last (with a causal mask the longest) to the first; units from
+  // full_units on are split over their keys.
+  struct Unit {
+    int part, splits, split, q0, b, hk;
+  };
+  auto unit_of = [&](int g) -> Unit {
+    Unit x = {-1, 1, 0, 0, 0, 0};
+    int u = g;
+    if (g >= a.full_units) {
+      x.part = g - static_cast<int>(a.full_units);
+      x.splits = a.splits;
+      x.split = x.part % a.splits;
+      u = static_cast<int>(a.full_units) + x.part / a.splits;
+    }
+    x.q0 = (a.row_blocks - 1 - u % a.row_blocks) * (T * a.qn);
+    const int bh = u / a.row_blocks;
+    x.b = bh / a.Hkv;
+    x.hk = bh % a.Hkv;
+    return x;
+  };
+
   if (warp < C::kSoftWarps) {
     // ------------------------------------------------------------ softmax
     // Warps 8t .. 8t+3 take columns 0-63 of tile t's S (half 0), 8t+4 .. 8t+7
     // columns 64-127; warps of both halves with the same lane quarter share rows.
     const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
     constexpr int H = BN / 2;
-    const int tid = threadIdx.x & 255;                  // among the tile's 256 threads
-    const int trow = quarter * 32 + lane;               // row of the tile
+    const int trow = quarter * 32 + lane;  // row of the tile
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const int wrow0 = t * 128 + quarter * 32;           // the warp's first row in the block
-    const bool idle = wrow0 >= rows;                    // none of its rows exists
-    const bool valid = wrow0 + lane < rows;
-    const int64_t grow = row0 + wrow0 + lane;
-    const int qi = valid ? static_cast<int>(grow / a.R) : 0;
-    const int hq = hk * a.R + (valid ? static_cast<int>(grow % a.R) : 0);
-    if (n > 0) {
-      // The tile's Q rows, swizzled as the MMA reads them (missing rows zero).
-      const uint32_t q_addr = smem_u32(sQ) + t * 128 * D * 2;
-      constexpr int kCh = D / 8;  // 16-byte pieces of a row
-#pragma unroll 4
-      for (int c = 0; c < kCh / 2; ++c) {
-        const int e = c * 256 + tid, r = e / kCh, ch = e % kCh;
-        const bool ok = t * 128 + r < rows;
-        const int64_t g = row0 + t * 128 + r;
-        const int64_t q = ok ? g / a.R : 0;
-        const int64_t h = hk * a.R + (ok ? g % a.R : 0);
-        cp_async16(q_addr + sw128_offset(r, ch, 128),
-                   a.q + int64_t(b) * a.qs.b + h * a.qs.h + q * a.qs.n + ch * 8, ok ? 16u : 0u);
-      }
-      cp_async_commit();
-      cp_async_wait<0>();
-      fence_proxy_async_smem();
-      mbar_arrive(&bars->qfull[t]);
-    }
-    Span sp = {0, 0, 0};
-    if (valid) sp = row_span(a.mask, b, qi);
+    const int rq = trow / a.R, rh = trow - rq * a.R;  // its query and head in the tile
+    const bool in_tile = trow < a.qn * a.R;
     const float sl = a.scale_log2;
-    float nslope = 0.f;
-    if (BIAS && valid) nslope = -__ldg(a.slopes + hq) * kLog2e;
-    float m = -INFINITY, l = 0.f, lr = 0.f;
     const uint32_t sbase = tmem + lane_base + t * 128 + half * H;
-    uint64_t* pair = &bars->pair[t * 4 + quarter];
+    const uint32_t obase = tmem + lane_base + C::kOCol + t * D + half * (D / 2);
     volatile int* flag = bars->flag[t * 4 + quarter];
-    uint32_t xn = 0;  // pair exchanges so far
+    uint32_t xn = 0;           // pair exchanges so far
+    uint32_t tc = 0, uc = 0;   // key tiles and units with keys so far
     // Slot of exchange xn: this half's value, and the other half's.
     auto mine = [&]() -> float2* { return sX + (((xn & 1) * T + t) * 2 + half) * 128 + trow; };
     auto other = [&]() -> float2* { return sX + (((xn & 1) * T + t) * 2 + (half ^ 1)) * 128 + trow; };
+    // Meets the other half's warp.  A warp that gives up sets *abort and arrives
+    // once (below `done`), and whoever it releases gives up too.
     auto pair_sync = [&]() -> bool {
-      mbar_arrive(pair);
-      const bool ok = mbar_wait(pair, xn & 1, abort);
-      return ok;
+      named_barrier(1 + t * 4 + quarter, 64);
+      return *abort == 0;
     };
-    constexpr bool kUnits = CAP || BIAS;  // scores are brought to exp2 units first
-    for (int j = 0; j < n; ++j) {
-      if (!mbar_wait(&bars->sfull[t], j & 1, abort)) goto done;
-      if (idle) {
-        mbar_arrive(&bars->pfull[t]);
-        continue;
-      }
+    for (uint32_t i = 0;; ++i) {
+      if (!mbar_wait(&bars->ring_full[i & 1], (i >> 1) & 1, abort)) goto done;
+      const int4 e = *const_cast<const int4*>(&bars->ring[i & 1]);
       __syncwarp();
-      tc_fence_after();
-      const int c0 = key0 + j * BN + half * H;  // key of the half's first column
-      const int va = sp.lo - c0, vb = sp.hi - c0;
-      const bool edge = __any_sync(0xffffffffu, va > 0 || vb < H);
-      // W raw scores -> capped, biased and masked ones (in place)
-      auto prepare = [&](float* x, int base) {
-        if constexpr (CAP) {
-          // cap tanh(y) = cap (1 - 2 / (1 + e^2y)), in exp2 units; exact at both
-          // ends (e^2y = inf or 0), absolute error about 1e-7 cap
-          const uint64_t k1 = f2(a.cap_k1, a.cap_k1), one = f2(1.f, 1.f);
-          const uint64_t cc = f2(a.cap_log2, a.cap_log2), mc = f2(-2.f * a.cap_log2, -2.f * a.cap_log2);
-#pragma unroll
-          for (int c = 0; c < W; c += 2) {
-            const uint64_t e = mul2(f2(x[c], x[c + 1]), k1);
-            const uint64_t d1 = add2(f2(fast_exp2(f2lo(e)), fast_exp2(f2hi(e))), one);
-            const uint64_t y = fma2(f2(fast_rcp(f2lo(d1)), fast_rcp(f2hi(d1))), mc, cc);
-            x[c] = f2lo(y);
-            x[c + 1] = f2hi(y);
-          }
+      if (lane == 0) mbar_arrive(&bars->ring_empty[i & 1]);
+      if (e.x < 0) break;
+      const Unit x = unit_of(e.x);
+      const int key0 = e.y, n = e.z;
+      const int qi = x.q0 + t * a.qn + rq, hq = x.hk * a.R + rh;
+      const bool valid = in_tile && qi < a.Nq;
+      const bool idle = !__any_sync(0xffffffffu, valid);
+      Span sp = {0, 0, 0};
+      if (valid) sp = row_span(a.mask, x.b, qi);
+      float nslope = 0.f;
+      if (BIAS && valid) nslope = -__ldg(a.slopes + hq) * kLog2e;
+      float m = -INFINITY, l = 0.f, lr = 0.f;
+      for (int j = 0; j < n; ++j) {
+        if (!mbar_wait(&bars->sfull[t], (tc + j) & 1, abort)) goto done;
+        if (idle) {
+          mbar_arrive(&bars->pfull[t]);
+          continue;
         }
-        if constexpr (BIAS) {
+        __syncwarp();
+        tc_fence_after();
+        const int k0 = key0 + (n - 1 - j) * BN, c0 = k0 + half * H;  // first keys of the tile and of the half
+        const int va = sp.lo - c0, vb = sp.hi - c0;
+        const bool edge = __any_sync(0xffffffffu, valid && (va > 0 || vb < H));
+        auto load = [&](float* s, int base) { tmem_ld16(sbase + base, reinterpret_cast<uint32_t*>(s)); };
+        auto hidden = [&](int c) -> bool { return c < va || c >= vb; };
+        // cap tanh(x scale / cap) = cap (1 - 2 / (1 + e^2y)) in exp2 units; exact at
+        // both ends (e^2y = inf or 0), absolute error about 1e-7 cap
+        auto capped = [&](float s) -> float {
+          return fmaf(-2.f * a.cap_log2, fast_rcp(1.f + fast_exp2(s * a.cap_k1)), a.cap_log2);
+        };
+        // W raw scores -> scores in exp2 units with cap, bias and mask.
+        auto exact = [&](float* s, int base) {
           const float t0 = static_cast<float>(sp.pos - c0 - base);
-          const uint64_t ns2 = f2(nslope, nslope), sl2 = f2(sl, sl);
 #pragma unroll
-          for (int c = 0; c < W; c += 2) {
-            const uint64_t dist = f2(fabsf(t0 - static_cast<float>(c)), fabsf(t0 - static_cast<float>(c + 1)));
-            uint64_t y = f2(x[c], x[c + 1]);
-            if (!CAP) y = mul2(y, sl2);
-            y = fma2(ns2, dist, y);
-            x[c] = f2lo(y);
-            x[c + 1] = f2hi(y);
-          }
-        }
-        if (edge) {
-#pragma unroll
-          for (int c = 0; c < W; ++c)
-            if (base + c < va || base + c >= vb) x[c] = -INFINITY;
-        }
-      };
-      auto load = [&](float* x, int base) {
-        if constexpr (W == 32)
-          tmem_ld32(sbase + base, reinterpret_cast<uint32_t*>(x));
-        else
-          tmem_ld16(sbase + base, reinterpret_cast<uint32_t*>(x));
-      };
-      // The row's largest score so far in this tile, over both halves.
-      auto row_max = [&](float* res) -> bool {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int base = 0; base < H; base += W) {
-          float x[W];
-          load(x, base);
-          tmem_ld_wait();
-          prepare(x, base);
-#pragma unroll
-          for (int c = 0; c < W; c += 2) mx = fmax3(mx, x[c], x[c + 1]);
-        }
-        *mine() = make_float2(kUnits ? mx : sl * mx, 0.f);
-        if (!pair_sync()) return false;
-        *res = fmaxf(mine()->x, other()->x);
-        ++xn;
-        return true;
-      };
-      // P = exp2(x - mm) as bf16 pairs, its fp32 sum (for lse) and the sum of
-      // the rounded values, which normalises O (so that O stays a convex
-      // combination of V rows whatever the rounding of P to bf16).
-      uint32_t p[H / 2];
-      float ts, tr;
-      auto exps = [&](float mm) {
-        const uint64_t sl2 = f2(sl, sl), nm2 = f2(-mm, -mm);
-        uint64_t ps[2] = {0, 0};
-        float pr[2] = {0.f, 0.f};
-        auto some = [&](const float* x, uint32_t* pp) {
-#pragma unroll
-          for (int c = 0; c < W / 2; ++c) {
-            const uint64_t xx = f2(x[2 * c], x[2 * c + 1]);
-            const uint64_t y = kUnits ? add2(xx, nm2) : fma2(xx, sl2, nm2);
-            const float p0 = fast_exp2(f2lo(y)), p1 = fast_exp2(f2hi(y));
-            pp[c] = pack_bf16(p0, p1);
-            ps[c & 1] = add2(ps[c & 1], f2(p0, p1));
-            pr[c & 1] = add_bf16x2(pp[c], pr[c & 1]);
+          for (int c = 0; c < W; ++c) {
+            float y = CAP ? capped(s[c]) : s[c] * sl;
+            if (BIAS) y = fmaf(nslope, fabsf(t0 - static_cast<float>(c)), y);
+            s[c] = edge && hidden(base + c) ? -INFINITY : y;
           }
         };
+        // The row's largest score in this tile, over both halves (without a bias
+        // the largest product has the largest score).
+        auto row_max = [&](float* res) -> bool {
+          float mx = -INFINITY;
 #pragma unroll
-        for (int base = 0; base < H; base += W) {
-          float x[W];
-          load(x, base);
-          tmem_ld_wait();
-          prepare(x, base);
-          some(x, p + base / 2);
+          for (int base = 0; base < H; base += W) {
+            float s[W];
+            load(s, base);
+            tmem_ld_wait();
+            if (BIAS) {
+              exact(s, base);
+            } else if (edge) {
+#pragma unroll
+              for (int c = 0; c < W; ++c)
+                if (hidden(base + c)) s[c] = -INFINITY;
+            }
+#pragma unroll
+            for (int c = 0; c < W; c += 2) mx = fmax3(mx, s[c], s[c + 1]);
+          }
+          if (!BIAS && mx != -INFINITY) mx = CAP ? capped(mx) : sl * mx;
+          *mine() = make_float2(mx, 0.f);
+          if (!pair_sync()) return false;
+          *res = fmaxf(mx, other()->x);
+          ++xn;
+          return true;
+        };
+        // P = exp2(score - mm) as bf16 pairs, its fp32 sum (for lse) and the sum
+        // of the rounded values, which normalises O (so that O stays a convex
+        // combination of V rows whatever the rounding of P to bf16).
+        uint32_t p[H / 2];
+        uint64_t ps[2];
+        float pr[2];
+        float ts, tr;
+        auto zero = [&]() {
+          ps[0] = ps[1] = 0;
+          pr[0] = pr[1] = 0.f;
+        };
+        auto take = [&](float y0, float y1, int c) {  // a pair of exponents
+          const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+          p[c] = pack_bf16(p0, p1);
+          ps[c & 1] = add2(ps[c & 1], f2(p0, p1));
+          pr[c & 1] = add_bf16x2(p[c], pr[c & 1]);
+        };
+        // Most tiles: every visible key on one side of its row, where the bias is
+        // linear in the column.  The exponent is then one multiply-add a pair:
+        // x * f + g with g = -mm or, with a bias, a pair that steps along the
+        // columns.  With a cap, f is tanh(z)/z as a polynomial in z^2 (|z| <= 0.4,
+        // error below 1.6e-7 cap); false if a score is larger.
+        const int far = sp.pos - c0;  // distance of the half's first column
+        auto fast = [&](float mm, auto masked) -> bool {
+          zero();
+          const float ns = far > 0 ? nslope : -nslope;  // of (far - c)
+          const float g0 = BIAS ? fmaf(ns, static_cast<float>(far), -mm) : -mm;
+          uint64_t g = BIAS ? f2(g0, g0 - ns) : f2(g0, g0);
+          const uint64_t step = f2(-2.f * ns, -2.f * ns);
+          const uint64_t sl2 = f2(sl, sl), k1 = f2(a.cap_p1, a.cap_p1), k2 = f2(a.cap_p2, a.cap_p2),
+                         k3 = f2(a.cap_p3, a.cap_p3);
+          float wm = 0.f;
+          float buf[2][W];  // the next columns load while these are worked on
+          load(buf[0], 0);
+#pragma unroll
+          for (int base = 0; base < H; base += W) {
+            float* s = buf[(base / W) & 1];
+            tmem_ld_wait();
+            if (base + W < H) load(buf[(base / W + 1) & 1], base + W);
+            if (BIAS && base) g = f2(g0 - static_cast<float>(base) * ns, g0 - static_cast<float>(base + 1) * ns);
+#pragma unroll
+            for (int c = 0; c < W / 2; ++c) {
+              const uint64_t xx = f2(s[2 * c], s[2 * c + 1]);
+              uint64_t f = sl2;
+              if (CAP) {
+                const uint64_t w = mul2(xx, xx);
+                wm = fmax3(wm, f2lo(w), f2hi(w));
+                f = fma2(w, fma2(w, fma2(w, k3, k2), k1), sl2);
+              }
+              const uint64_t y = fma2(xx, f, g);
+              if (decltype(masked)::value)
+                take(hidden(base + 2 * c) ? -INFINITY : f2lo(y), hidden(base + 2 * c + 1) ? -INFINITY : f2hi(y),
+                     base / 2 + c);
+              else
+                take(f2lo(y), f2hi(y), base / 2 + c);
+              if (BIAS) g = add2(g, step);
+            }
+          }
+          return !CAP || !__any_sync(0xffffffffu, valid && !(wm <= a.cap_limit));
+        };
+        auto exps = [&](float mm) {
+          bool ok = true;
+          if (BIAS)
+            ok = __all_sync(0xffffffffu, !valid || far >= min(vb, H) - 1) ||
+                 __all_sync(0xffffffffu, !valid || far <= max(va, 0));
+          if (ok) ok = edge ? fast(mm, Masked<true>()) : fast(mm, Masked<false>());
+          if ((CAP || BIAS) && !ok) {
+            zero();
+#pragma unroll
+            for (int base = 0; base < H; base += W) {
+              float s[W];
+              load(s, base);
+              tmem_ld_wait();
+              exact(s, base);
+#pragma unroll
+              for (int c = 0; c < W / 2; ++c) take(s[2 * c] - mm, s[2 * c + 1] - mm, base / 2 + c);
+            }
+          }
+          const uint64_t s2 = add2(ps[0], ps[1]);
+          ts = f2lo(s2) + f2hi(s2);
+          tr = pr[0] + pr[1];
+        };
+        // The first tile that shows a row a key sets its reference; later tiles
+        // raise it only when needed.  (A row without one has P = 0, l = 0, O = 0.)
+        // Both warps of a pair hold the same references and spans, so they agree.
+        if (j == 0 || __any_sync(0xffffffffu, m == -INFINITY && sp.lo < k0 + BN && sp.hi > k0)) {
+          float mx;
+          if (!row_max(&mx)) goto done;
+          if (m == -INFINITY) m = mx;
         }
-        const uint64_t s2 = add2(ps[0], ps[1]);
-        ts = f2lo(s2) + f2hi(s2);
-        tr = pr[0] + pr[1];
-      };
-      // The first tile that shows a row a key sets its reference; later tiles
-      // raise it only when needed.  (A row without one has P = 0, l = 0, O = 0.)
-      // Both warps of a pair hold the same references and spans, so they agree.
-      const bool first = j == 0 || __any_sync(0xffffffffu, m == -INFINITY && sp.hi > sp.lo);
-      if (first) {
-        float mx;
-        if (!row_max(&mx)) goto done;
-        if (m == -INFINITY) m = mx;
-      }
-      exps(m == -INFINITY ? 0.f : m);
-      {
+        exps(m == -INFINITY ? 0.f : m);
         // either half's sum too large: both raise
-        const bool bad = j > 0 && __any_sync(0xffffffffu, !(ts <= kRaiseLimit));
-        if (bad && lane == 0) flag[xn & 1] = j + 1;
+        if (j > 0 && __any_sync(0xffffffffu, valid && !(ts <= kRaiseLimit)) && lane == 0) flag[xn & 1] = tc + j + 1;
         __syncwarp();
         if (!pair_sync()) goto done;
-        const bool raise = flag[xn & 1] == j + 1;
+        const bool raise = flag[xn & 1] == static_cast<int>(tc + j + 1);
         ++xn;
         if (raise) {
           float mx;
@@ -335,177 +383,260 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
           l *= alpha;
           lr *= alpha;
           // O holds PV of every earlier tile: its commit came with this S.
-          const uint32_t obase = tmem + lane_base + C::kOCol + t * D + half * (D / 2);
 #pragma unroll
           for (int c = 0; c < D / 64; ++c) {
             uint32_t r[32];
             tmem_ld32(obase + c * 32, r);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+            for (int y = 0; y < 32; ++y) r[y] = __float_as_uint(__uint_as_float(r[y]) * alpha);
             tmem_st32(obase + c * 32, r);
           }
           exps(m == -INFINITY ? 0.f : m);
         }
+        l += ts;
+        lr += tr;
+        tmem_st32(sbase, p);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bars->pfull[t]);
       }
-      l += ts;
-      lr += tr;
-      tmem_st32(sbase, p);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&bars->pfull[t]);
-    }
-    if (n > 0) {
-      if (!mbar_wait(&bars->sfull[t], n & 1, abort)) goto done;
-      __syncwarp();
-      tc_fence_after();
-    }
-    if (!idle) {
-      // both halves' sums; each half writes its half of the row
-      *mine() = make_float2(l, lr);
-      if (!pair_sync()) goto done;
-      l += other()->x;
-      lr += other()->y;
-      ++xn;
-      const float inv = l == 0.f ? 0.f : 1.f / lr;
-      if (valid && half == 0) {
-        const float lse = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
-        if (part >= 0)
-          a.part_lse[part * (128 * T) + wrow0 + lane] = lse;
-        else if (a.lse)
-          a.lse[(int64_t(b) * a.Hq + hq) * a.Nq + qi] = lse;
-      }
-      const uint32_t obase = tmem + lane_base + C::kOCol + t * D + half * (D / 2);
-      const int64_t oo = int64_t(b) * a.os.b + int64_t(hq) * a.os.h + int64_t(qi) * a.os.n + half * (D / 2);
-      float* dst32 = part >= 0 ? a.part_o + (part * (128 * T) + wrow0 + lane) * D + half * (D / 2)
-                               : static_cast<float*>(a.o) + oo;
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        float v[32];
-        if (n > 0) {
-          tmem_ld32(obase + c * 32, reinterpret_cast<uint32_t*>(v));
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = inv == 0.f ? 0.f : v[e] * inv;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0.f;
-        }
-        if (valid && (part >= 0 || a.out_fp32)) {
-          float4* dst = reinterpret_cast<float4*>(dst32 + c * 32);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-        } else if (valid) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + oo + c * 32);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
-                                pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
-        }
+      tc += n;
+      if (n > 0) {
+        if (!mbar_wait(&bars->ofull[t], uc & 1, abort)) goto done;
+        ++uc;
         __syncwarp();
+        tc_fence_after();
+      }
+      if (!idle) {
+        // both halves' sums; each half writes its half of the row
+        *mine() = make_float2(l, lr);
+        if (!pair_sync()) goto done;
+        l += other()->x;
+        lr += other()->y;
+        ++xn;
+        const float inv = l == 0.f ? 0.f : 1.f / lr;
+        const int64_t prow = int64_t(x.part) * (128 * T) + t * 128 + trow;
+        if (valid && half == 0) {
+          const float lse = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+          if (x.part >= 0)
+            a.part_lse[prow] = lse;
+          else if (a.lse)
+            a.lse[(int64_t(x.b) * a.Hq + hq) * a.Nq + qi] = lse;
+        }
+        const int64_t oo = int64_t(x.b) * a.os.b + int64_t(hq) * a.os.h + int64_t(qi) * a.os.n + half * (D / 2);
+        float* dst32 = x.part >= 0 ? a.part_o + prow * D + half * (D / 2) : static_cast<float*>(a.o) + oo;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          float v[32];
+          if (n > 0) {
+            tmem_ld32(obase + c * 32, reinterpret_cast<uint32_t*>(v));
+            tmem_ld_wait();
+            if (c == D / 64 - 1) {
+              tc_fence_before();
+              mbar_arrive(&bars->ofree[t]);
+            }
+#pragma unroll
+            for (int y = 0; y < 32; ++y) v[y] = inv == 0.f ? 0.f : v[y] * inv;
+          } else {
+#pragma unroll
+            for (int y = 0; y < 32; ++y) v[y] = 0.f;
+          }
+          if (valid && (x.part >= 0 || a.out_fp32)) {
+            float4* dst = reinterpret_cast<float4*>(dst32 + c * 32);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) dst[y] = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+          } else if (valid) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + oo + c * 32);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              dst[y] = make_uint4(pack_bf16(v[8 * y], v[8 * y + 1]), pack_bf16(v[8 * y + 2], v[8 * y + 3]),
+                                  pack_bf16(v[8 * y + 4], v[8 * y + 5]), pack_bf16(v[8 * y + 6], v[8 * y + 7]));
+          }
+          __syncwarp();
+        }
+      } else if (n > 0) {
+        mbar_arrive(&bars->ofree[t]);
       }
     }
-  } else if (warp == C::kMmaWarp) {
+  } else if (warp < C::kTmaWarp) {
     // ------------------------------------------------------------ MMA issue
+    // One warp per Q tile: issuing an MMA blocks while the tensor core is busy,
+    // so one thread for both tiles left it idle (1000 of 3600 cycles a step)
+    // whenever that thread waited for a barrier or committed.
+    const int t = warp - C::kMmaWarp;
     const uint32_t kIdescS = a.neg_scale ? idesc_negate_b(idesc_bf16(128, BN, false, false))
                                          : idesc_bf16(128, BN, false, false);
     constexpr uint32_t kIdescPV = idesc_bf16(128, D, false, true);
-    const uint32_t q_addr = smem_u32(sQ), kv_addr = smem_u32(sKV);
-    bool ok = n > 0;
-    auto ready = [&](int i) -> bool { return mbar_wait(&bars->full[i % S], (i / S) & 1, abort); };
-    auto qk = [&](int t, int i) {
-      const uint32_t ka = kv_addr + (i % S) * C::kTile, qa = q_addr + t * 128 * D * 2;
+    // Descriptor halves: stepping through a tile only adds to the low word.
+    const uint64_t dq = sw128_desc(smem_u32(sQ) + t * 128 * D * 2, 16, 1024);
+    const uint64_t dk = sw128_desc(smem_u32(sKV), 16, 1024), dv = sw128_desc(smem_u32(sKV), BN * 128, 1024);
+    const uint32_t q_lo = static_cast<uint32_t>(dq), q_hi = static_cast<uint32_t>(dq >> 32);
+    const uint32_t k_lo = static_cast<uint32_t>(dk), k_hi = static_cast<uint32_t>(dk >> 32);
+    const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
+    const uint32_t s_tmem = tmem + t * 128, o_tmem = tmem + C::kOCol + t * D;
+    auto ready = [&](uint32_t i) -> bool { return mbar_wait(&bars->full[i % S], (i / S) & 1, abort); };
+    auto pass = [&]() {  // the other tile's turn
+      if (T == 2) mbar_arrive(&bars->turn[t ^ 1]);
+    };
+    auto qk = [&](uint32_t i, bool turn) {
+      const uint32_t kl = k_lo + (((i % S) * C::kTile) >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * 128 * 128 + (kk & 3) * 32;
-        mma_ss(tmem + t * 128, sw128_desc(qa + off, 16, 1024), sw128_desc(ka + off, 16, 1024), kIdescS,
-               kk > 0 ? 1u : 0u);
+        const uint32_t off = ((kk >> 2) * 128 * 128 + (kk & 3) * 32) >> 4;
+        mma_ss_w(s_tmem, q_lo + off, q_hi, kl + off, k_hi, kIdescS, kk > 0 ? 1u : 0u);
+        if (kk == D / 16 - 3 && turn) pass();  // (two MMAs cover the hand-over)
       }
+      mma_commit(&bars->sfull[t]);
     };
-    auto pv = [&](int t, int i, bool first) {
-      const uint32_t va = kv_addr + (i % S) * C::kTile;
+    auto pv = [&](uint32_t i, bool first) {
+      const uint32_t vl = v_lo + (((i % S) * C::kTile) >> 4);
 #pragma unroll
       for (int kk = 0; kk < BN / 16; ++kk)
         // P of keys 0-63 lies in S columns 0-31, of keys 64-127 in 64-95
-        mma_ts(tmem + C::kOCol + t * D, tmem + t * 128 + (kk >> 2) * 64 + (kk & 3) * 8, sw128_desc(va + kk * 2048, BN * 128, 1024),
-               kIdescPV, (!first || kk > 0) ? 1u : 0u);
+        mma_ts_w(o_tmem, s_tmem + (kk >> 2) * 64 + (kk & 3) * 8, vl + ((kk * 2048) >> 4), v_hi, kIdescPV,
+                 (!first || kk > 0) ? 1u : 0u);
     };
-    // Ring entries: K(j) is number 2j, V(j) is 2j + 1.
-    if (ok) ok = ready(0);
-    if (ok) {
-      for (int t = 0; t < T && ok; ++t) {
-        ok = mbar_wait(&bars->qfull[t], 0, abort);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-          qk(t, 0);
-          mma_commit(&bars->sfull[t]);
-        }
-      }
-      if (ok && lane == 0) mma_commit(&bars->empty[0]);
-    }
-    for (int j = 0; j < n && ok; ++j) {
-      const bool more = j + 1 < n;
-      if (!(ok = ready(2 * j + 1)) || (more && !(ok = ready(2 * j + 2)))) break;
-      // V rows past the span (another document's, or a cache's unused rows)
-      // meet P = 0, but 0 times a NaN or an infinity would still reach O.
-      const int live = uhi - (key0 + j * BN);
-      if (live < BN) {
-        uint8_t* vt = sKV + ((2 * j + 1) % S) * C::kTile;
-        for (int e = lane; e < (BN - live) * (D / 8); e += 32) {
-          const int r = live + e / (D / 8), ch = e % (D / 8);
-          *reinterpret_cast<uint4*>(vt + (ch >> 3) * BN * 128 + r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      for (int t = 0; t < T && ok; ++t) {
-        ok = mbar_wait(&bars->pfull[t], j & 1, abort);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-          pv(t, 2 * j + 1, j == 0);
-          if (more) qk(t, 2 * j + 2);
-          mma_commit(&bars->sfull[t]);
-        }
-      }
-      if (ok && lane == 0) {
-        mma_commit(&bars->empty[(2 * j + 1) % S]);
-        if (more) mma_commit(&bars->empty[(2 * j + 2) % S]);
-      }
-      __syncwarp();
-    }
     if (lane == 0) {
-      // Every MMA issued above must finish before TMEM is released.
-      mma_commit(&bars->drain);
-      const long long t0 = clock64();
-      while (!mbar_test(&bars->drain, 0) && clock64() - t0 < kWaitLimitCycles) {
+      bool ok = true;
+      uint32_t tc = 0, uc = 0, zc = 0;  // key tiles, units with keys and cleared tails so far
+      for (uint32_t i = 0; ok; ++i) {
+        if (!mbar_wait(&bars->ring_full[i & 1], (i >> 1) & 1, abort)) break;
+        const int4 e = *const_cast<const int4*>(&bars->ring[i & 1]);
+        mbar_arrive(&bars->ring_empty[i & 1]);
+        if (e.x < 0) break;
+        const int key0 = e.y, n = e.z, uhi = e.w;
+        if (n == 0) continue;
+        // Ring entries: K(j) is number 2 (tc + j), V(j) the one behind it.
+        if (!(ok = mbar_wait(&bars->qfull, uc & 1, abort)) || !(ok = ready(2 * tc))) break;
+        tc_fence_after();
+        qk(2 * tc, false);
+        mma_commit(&bars->empty[(2 * tc) % S]);
+        if (n == 1) mma_commit(&bars->qempty);
+        for (int j = 0; j < n; ++j) {
+          const bool more = j + 1 < n;
+          const uint32_t iv = 2 * (tc + j) + 1, ik = iv + 1;
+          if (!(ok = ready(iv)) || (more && !(ok = ready(ik)))) break;
+          const bool tail = j == 0 && uhi - (key0 + (n - 1) * BN) < BN;  // to be cleared behind the span
+          if (tail) mbar_arrive(&bars->tail_here);
+          if (!(ok = mbar_wait(&bars->pfull[t], (tc + j) & 1, abort))) break;
+          if (tail && !(ok = mbar_wait(&bars->tail, zc++ & 1, abort))) break;
+          if (j == 0 && uc > 0 && !(ok = mbar_wait(&bars->ofree[t], (uc - 1) & 1, abort))) break;
+          // Turns: the tiles' steps alternate (side by side they would fall into
+          // step and leave the tensor core idle during both softmaxes).
+          if (T == 2 && tc + j + t > 0 && !(ok = mbar_wait(&bars->turn[t], (tc + j + t - 1) & 1, abort))) break;
+          tc_fence_after();
+          pv(iv, j == 0);
+          if (more)
+            qk(ik, true);
+          else
+            pass();
+          if (!more) mma_commit(&bars->ofull[t]);
+          mma_commit(&bars->empty[iv % S]);
+          if (more) mma_commit(&bars->empty[ik % S]);
+          if (j + 2 == n) mma_commit(&bars->qempty);
+        }
+        tc += n;
+        ++uc;
       }
+      // Every MMA issued above must finish before TMEM is released.
+      mma_commit(&bars->drain[t]);
+      const long long t0 = clock64();
+      while (!mbar_test(&bars->drain[t], 0) && clock64() - t0 < kWaitLimitCycles) {
+      }
+    }
+  } else if (warp == C::kTailWarp) {
+    // ------------------------------------------------------------ tails
+    // V rows past the span (another document's, or a cache's unused rows) meet
+    // P = 0, but 0 times a NaN or an infinity would still reach O: cleared.
+    // The MMA warps say when such a tile has landed.
+    uint32_t tc = 0, zc = 0;
+    for (uint32_t i = 0;; ++i) {
+      if (!mbar_wait(&bars->ring_full[i & 1], (i >> 1) & 1, abort)) break;
+      const int4 e = *const_cast<const int4*>(&bars->ring[i & 1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->ring_empty[i & 1]);
+      if (e.x < 0) break;
+      const uint32_t iv = 2 * tc + 1;  // the unit's first V: tiles come last first
+      tc += e.z;
+      const int live = e.w - (e.y + (e.z - 1) * BN);
+      if (e.z == 0 || live >= BN) continue;
+      if (!mbar_wait(&bars->tail_here, zc++ & 1, abort)) break;
+      uint8_t* vt = sKV + (iv % S) * C::kTile;
+      for (int f = lane; f < (BN - live) * (D / 8); f += 32) {
+        const int r = live + f / (D / 8), ch = f % (D / 8);
+        *reinterpret_cast<uint4*>(vt + (ch >> 3) * BN * 128 + r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->tail);
     }
   } else if (warp == C::kTmaWarp && lane == 0) {
-    // ------------------------------------------------------------ loads (TMA)
-    const uint32_t kv_addr = smem_u32(sKV);
-    int issued = 0;
-    for (int i = 0; i < 2 * n; ++i) {
-      const int s = i % S;
-      if (!mbar_wait(&bars->empty[s], ((i / S) & 1) ^ 1, abort)) break;
-      mbar_expect_tx(&bars->full[s], C::kTile);
-      const int key = key0 + (i >> 1) * BN;
-#pragma unroll
-      for (int cb = 0; cb < D / 64; ++cb)
-        tma_load_4d(kv_addr + s * C::kTile + cb * BN * 128, (i & 1) ? &tm_v : &tm_k, 64 * cb, key, hk, b,
-                    &bars->full[s]);
-      issued = i + 1;
-    }
-    // After an abort: the copies in flight land before the block ends.
-    if (*abort)
-      for (int i = issued > S ? issued - S : 0; i < issued; ++i) {
-        const long long t0 = clock64();
-        while (!mbar_test(&bars->full[i % S], (i / S) & 1) && clock64() - t0 < kWaitLimitCycles) {
-        }
+    // ------------------------------------------------------------ units and loads
+    const uint32_t q_addr = smem_u32(sQ), kv_addr = smem_u32(sKV);
+    int64_t g = blockIdx.x;
+    uint32_t it = 0, uc = 0;
+    bool ok = true;
+    uint32_t i = 0;
+    for (; ok; ++i) {
+      int key0 = 0, n = 0, uhi = 0;
+      Unit x = {};
+      if (g >= 0) {
+        mbar_expect_tx(&bars->next, 16);
+        request_block(&bars->answer, &bars->next);
+        // keys that any of the unit's rows sees, and this split's run of tiles
+        x = unit_of(static_cast<int>(g));
+        const int ulo = row_span(a.mask, x.b, x.q0).lo;
+        uhi = row_span(a.mask, x.b, min(x.q0 + T * a.qn, a.Nq) - 1).hi;
+        const int ntiles = uhi > ulo ? (uhi - ulo + BN - 1) / BN : 0;
+        const int j0 = static_cast<int>(int64_t(ntiles) * x.split / x.splits);
+        n = static_cast<int>(int64_t(ntiles) * (x.split + 1) / x.splits) - j0;
+        key0 = ulo + j0 * BN;
       }
+      if (i >= 2 && !mbar_wait(&bars->ring_empty[i & 1], ((i >> 1) - 1) & 1, abort)) break;
+      bars->ring[i & 1] = make_int4(static_cast<int>(g), key0, n, uhi);
+      mbar_arrive(&bars->ring_full[i & 1]);
+      if (g < 0) break;
+      if (n > 0) {
+        if (uc > 0 && !mbar_wait(&bars->qempty, (uc - 1) & 1, abort)) break;
+        ++uc;
+        mbar_expect_tx(&bars->qfull, T * a.qn * a.R * D * 2);
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+          for (int cb = 0; cb < D / 64; ++cb)
+            tma_load_4d(q_addr + t * 128 * D * 2 + cb * 128 * 128, &tm_q, 64 * cb, x.hk * a.R, x.q0 + t * a.qn, x.b,
+                        &bars->qfull);
+        for (int f = 0; f < 2 * n; ++f, ++it) {
+          const uint32_t s = it % S;
+          if (!(ok = mbar_wait(&bars->empty[s], ((it / S) & 1) ^ 1, abort))) break;
+          mbar_expect_tx(&bars->full[s], C::kTile);
+          const int key = key0 + (n - 1 - (f >> 1)) * BN;
+#pragma unroll
+          for (int cb = 0; cb < D / 64; ++cb)
+            tma_load_4d(kv_addr + s * C::kTile + cb * BN * 128, (f & 1) ? &tm_v : &tm_k, 64 * cb, key, x.hk, x.b,
+                        &bars->full[s]);
+        }
+        if (!ok) break;
+      }
+      if (!(ok = mbar_wait(&bars->next, i & 1, abort))) break;
+      g = answered_block(&bars->answer);
+      fence_proxy_async_smem();  // read before the next answer is written
+    }
+    if (*abort) {
+      // After an abort: what is in flight lands before the block ends.
+      auto settle = [&](uint64_t* bar, uint32_t parity) {
+        const long long t0 = clock64();
+        while (!mbar_test(bar, parity) && clock64() - t0 < kWaitLimitCycles) {
+        }
+      };
+      for (uint32_t f = it > S ? it - S : 0; f < it; ++f) settle(&bars->full[f % S], (f / S) & 1);
+      if (uc > 0) settle(&bars->qfull, (uc - 1) & 1);
+      if (g >= 0) settle(&bars->next, i & 1);
+    }
   }
 done:
+  if (warp < C::kSoftWarps && *abort) named_barrier_arrive(1 + (warp >> 3) * 4 + (warp & 3), 64);
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && bars->abort) report(a.status, SA_DEVERR_TIMEOUT);
@@ -519,16 +650,18 @@ done:
 // One warp per row of a split unit: lse = ln sum_s e^(lse_s),
 // o = sum_s e^(lse_s - lse) o_s.
 template <int D>
-__global__ void __launch_bounds__(256) sa_masked_join_kernel(const MaskedArgs a, int unit_rows) {
+__global__ void __launch_bounds__(256) sa_masked_join_kernel(const __grid_constant__ MaskedArgs a) {
   const int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  const int unit_rows = a.unit_rows;
   const int64_t su = i / unit_rows;  // split unit
   const int r = static_cast<int>(i % unit_rows);
   const int64_t u = a.full_units + su;
   const int64_t bh = u / a.row_blocks;
   if (bh >= int64_t(a.B) * a.Hkv) return;
-  const int64_t row = (a.row_blocks - 1 - u % a.row_blocks) * unit_rows + r;
-  if (row >= a.rows) return;
+  const int tr = r % 128;  // row of its Q tile
+  const int64_t q = (a.row_blocks - 1 - u % a.row_blocks) * (unit_rows / 128 * a.qn) + r / 128 * a.qn + tr / a.R;
+  if (tr >= a.qn * a.R || q >= a.Nq) return;
   const float* pl = a.part_lse + su * a.splits * unit_rows + r;
   float mx = -INFINITY;
   for (int s = lane; s < a.splits; s += 32) mx = fmaxf(mx, __ldg(pl + s * unit_rows));
@@ -545,7 +678,7 @@ __global__ void __launch_bounds__(256) sa_masked_join_kernel(const MaskedArgs a,
       for (int e = 0; e < V; ++e) acc[e] += w * src[e];
     }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t q = row / a.R, h = (bh % a.Hkv) * a.R + row % a.R, b = bh / a.Hkv;
+  const int64_t h = (bh % a.Hkv) * a.R + tr % a.R, b = bh / a.Hkv;
   const int64_t oo = b * a.os.b + h * a.os.h + q * a.os.n + lane * V;
 #pragma unroll
   for (int e = 0; e < V; e += 2) {
@@ -562,9 +695,11 @@ __global__ void __launch_bounds__(256) sa_masked_join_kernel(const MaskedArgs a,
 // this count of tile times: a wave costs its tiles plus a block's start, a
 // split the join.
 void masked_plan(MaskedArgs* a) {
-  const int T = a->rows > 128 ? 2 : 1;
+  a->qn = 128 / a->R;
+  const int T = a->Nq > a->qn ? 2 : 1;
   a->unit_rows = 128 * T;
-  a->row_blocks = static_cast<int32_t>((a->rows + a->unit_rows - 1) / a->unit_rows);
+  a->row_blocks = (a->Nq + T * a->qn - 1) / (T * a->qn);
+  if (a->qn > a->Nq) a->qn = a->Nq;
   const int64_t units = int64_t(a->B) * a->Hkv * a->row_blocks, rest = units % kSms;
   const int64_t tiles = (int64_t(a->Nk) + BN - 1) / BN;
   constexpr int64_t kStart = 5, kJoin = 8;
@@ -582,7 +717,8 @@ void masked_plan(MaskedArgs* a) {
 }
 
 template <int D, int T, bool CAP, bool BIAS>
-static cudaError_t launch_m(const MaskedArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
+static cudaError_t launch_m(const MaskedArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                            cudaStream_t st) {
   using C = MCfg<D, T>;
   auto kern = sa_masked_kernel<D, T, CAP, BIAS>;
   // at least half the SM's shared memory: one block per SM owns its TMEM
@@ -600,31 +736,33 @@ static cudaError_t launch_m(const MaskedArgs& a, const CUtensorMap& tk, const CU
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t grid = a.full_units + a.split_units * a.splits;
-  kern<<<static_cast<unsigned>(grid), C::kThreads, smem, st>>>(a, tk, tv);
+  kern<<<static_cast<unsigned>(grid), C::kThreads, smem, st>>>(a, tq, tk, tv);
   return cudaGetLastError();
 }
 
 template <int D, int T>
-static cudaError_t launch_t(const MaskedArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
+static cudaError_t launch_t(const MaskedArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                            cudaStream_t st) {
   const bool cap = a.cap_log2 > 0.f, bias = a.slopes != nullptr;
-  if (cap) return bias ? launch_m<D, T, true, true>(a, tk, tv, st) : launch_m<D, T, true, false>(a, tk, tv, st);
-  return bias ? launch_m<D, T, false, true>(a, tk, tv, st) : launch_m<D, T, false, false>(a, tk, tv, st);
+  if (cap) return bias ? launch_m<D, T, true, true>(a, tq, tk, tv, st) : launch_m<D, T, true, false>(a, tq, tk, tv, st);
+  return bias ? launch_m<D, T, false, true>(a, tq, tk, tv, st) : launch_m<D, T, false, false>(a, tq, tk, tv, st);
 }
 
 cudaError_t launch_masked(const MaskedArgs& a, cudaStream_t st) {
-  CUtensorMap tk, tv;
-  if (!make_view_map(&tk, a.k, a.d, a.Nk, a.Hkv, a.B, a.ks.n, a.ks.h, a.ks.b, BN, 1, false) ||
+  CUtensorMap tq, tk, tv;
+  if (!make_view_map(&tq, a.q, a.d, a.Nq, a.Hq, a.B, a.qs.n, a.qs.h, a.qs.b, a.qn, a.R, true) ||
+      !make_view_map(&tk, a.k, a.d, a.Nk, a.Hkv, a.B, a.ks.n, a.ks.h, a.ks.b, BN, 1, false) ||
       !make_view_map(&tv, a.v, a.d, a.Nk, a.Hkv, a.B, a.vs.n, a.vs.h, a.vs.b, BN, 1, false))
     return cudaErrorInvalidValue;
   const bool two = a.unit_rows == 256;
-  cudaError_t e = a.d == 128 ? (two ? launch_t<128, 2>(a, tk, tv, st) : launch_t<128, 1>(a, tk, tv, st))
-                             : (two ? launch_t<64, 2>(a, tk, tv, st) : launch_t<64, 1>(a, tk, tv, st));
+  cudaError_t e = a.d == 128 ? (two ? launch_t<128, 2>(a, tq, tk, tv, st) : launch_t<128, 1>(a, tq, tk, tv, st))
+                             : (two ? launch_t<64, 2>(a, tq, tk, tv, st) : launch_t<64, 1>(a, tq, tk, tv, st));
   if (e != cudaSuccess || a.split_units == 0) return e;
   const unsigned blocks = static_cast<unsigned>((a.split_units * a.unit_rows + 7) / 8);
   if (a.d == 128)
-    sa_masked_join_kernel<128><<<blocks, 256, 0, st>>>(a, a.unit_rows);
+    sa_masked_join_kernel<128><<<blocks, 256, 0, st>>>(a);
   else
-    sa_masked_join_kernel<64><<<blocks, 256, 0, st>>>(a, a.unit_rows);
+    sa_masked_join_kernel<64><<<blocks, 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -15,6 +15,10 @@ using sa::aligned;
 using sa::device_info;
 using sa::in_device_allocation;
 
+// (tanh(z)/z - 1)/z^2 as a quadratic in z^2 through its Chebyshev nodes on
+// [0, 0.16]: |z| times the error stays below 1.6e-7.
+constexpr double kTanh1 = -0.3333307876878961, kTanh2 = 0.13304591654903536, kTanh3 = -0.04907868548467837;
+
 sa_status map_cuda(cudaError_t e) { return e == cudaSuccess ? SA_OK : SA_ERR_CUDA; }
 
 // A [B, H, N, d] view: 16-byte aligned rows, no negative strides.  Strides of
@@ -73,6 +77,7 @@ sa_status check_masked(const sa_masked* p, sa::MaskedArgs* a) {
   if (p->d != 64 && p->d != 128) return SA_ERR_UNSUPPORTED;
   const int64_t R = p->Hq / p->Hkv;
   // packed rows and key coordinates are 32-bit with room for a tile behind them
+  if (R > 128) return SA_ERR_UNSUPPORTED;  // a Q tile holds all of a query's heads
   if (p->Nq > (1 << 30) || p->Nk > (1 << 30) || R * p->Nq > (int64_t(1) << 40) ||
       int64_t(p->B) * p->Hq > (1 << 24))
     return SA_ERR_UNSUPPORTED;
@@ -95,9 +100,14 @@ sa_status check_masked(const sa_masked* p, sa::MaskedArgs* a) {
   a->scale_log2 = static_cast<float>(s * log2e);
   a->cap_log2 = static_cast<float>(p->cap * log2e);
   a->cap_k1 = p->cap > 0.f ? static_cast<float>(2.0 * s * log2e / p->cap) : 0.f;
-  a->rows = R * p->Nq;
+  // tanh(z) = z (1 + z^2 (c1 + z^2 (c2 + z^2 c3))) for |z| <= 0.4, z = x |scale| / cap
+  const double r2 = p->cap > 0.f ? s / p->cap * (s / p->cap) : 0.0;
+  a->cap_p1 = static_cast<float>(kTanh1 * s * log2e * r2);
+  a->cap_p2 = static_cast<float>(kTanh2 * s * log2e * r2 * r2);
+  a->cap_p3 = static_cast<float>(kTanh3 * s * log2e * r2 * r2 * r2);
+  a->cap_limit = r2 > 0.0 && r2 < 1e6 ? static_cast<float>(0.16 / r2) : -1.f;
   a->total_rows = int64_t(p->B) * p->Hq * p->Nq;
-  a->unit_rows = a->row_blocks = a->splits = 1;
+  a->qn = a->unit_rows = a->row_blocks = a->splits = 1;
   a->full_units = a->split_units = 0;
   a->part_o = nullptr;
   a->part_lse = nullptr;
@@ -141,7 +151,7 @@ sa_status sparse_attn_forward_masked(const sa_masked* p, const void* q, const vo
   sa_status st = check_masked(p, &a);
   if (st != SA_OK) return st;
   uint64_t nq, nk, nv, no;
-  if (!check_view(q, &a.qs, p->B, p->Hq, p->Nq, p->d, 2, false, true, &nq) ||
+  if (!check_view(q, &a.qs, p->B, p->Hq, p->Nq, p->d, 2, false, false, &nq) ||
       !check_view(k, &a.ks, p->B, p->Hkv, p->Nk, p->d, 2, false, false, &nk) ||
       !check_view(v, &a.vs, p->B, p->Hkv, p->Nk, p->d, 2, false, false, &nv) ||
       !check_view(o, &a.os, p->B, p->Hq, p->Nq, p->d, a.out_fp32 ? 4 : 2, true, false, &no))
@@ -186,7 +196,6 @@ sa_status sparse_attn_cache_weights(const sa_masked* p, const void* q, const voi
   if (!lse || !w_out || !std::isfinite(decay) || (decay != 0.f && !w_in)) return SA_ERR_INVALID_ARG;
   if (!aligned(lse, 4) || !aligned(w_in, 4) || !aligned(w_out, 4) || !aligned(dev_status, 4))
     return SA_ERR_INVALID_ARG;
-  if (a.R > 256) return SA_ERR_UNSUPPORTED;  // a Q tile holds a query's heads
   const uint64_t wbytes = uint64_t(p->B) * p->Hkv * p->Nk * 4, lbytes = uint64_t(a.total_rows) * 4;
   if (w_in && w_in != w_out && overlap(w_in, wbytes, w_out, wbytes)) return SA_ERR_INVALID_ARG;
   if (overlap(lse, lbytes, w_out, wbytes) || overlap(q, nq, w_out, wbytes) || overlap(k, nk, w_out, wbytes))
