@@ -10,14 +10,16 @@
 //
 // Weights.  S^T = K Q^T puts keys on the 128 TMEM lanes and query rows on the
 // columns, so an epilogue thread owns one key and sums over queries in its own
-// registers: no cross-lane reduction, no atomics, a fixed order.  A unit is one
-// 128-key tile; its K stays in shared memory while Q tiles of up to 256 packed
-// rows (query * R + head-in-group) stream by.  Q tiles alternate between two
-// TMEM buffers; each buffer has its own MMA warp (its waits and commits overlap
-// the other's MMAs; they take turns, so that one buffer's sums run beside the
-// other's MMA) and two sets of four epilogue warps, one per half of the columns.
-// With many rows the bound is the tensor core (one exponential a pair is 0.8 of
-// its time on the MUFU); with one token per sequence it is the read of K.
+// registers: no cross-lane reduction, no atomics, a fixed order.  A unit is 256
+// keys, two tiles that stay in shared memory while Q tiles of up to 256 packed
+// rows (query * R + head-in-group) stream by, each read once for both (with one
+// 128-key tile a unit, Q came from L2 at 51 bytes a cycle and SM, its limit).
+// Each key tile has its own TMEM buffer, its own MMA warp (its waits and commits
+// overlap the other's MMAs; they take turns, so that one buffer's sums run
+// beside the other's MMA) and two sets of four epilogue warps, one per half of
+// the columns.  With many rows the bound is the tensor core (one exponential a
+// pair is 0.8 of its time on the MUFU); with one token per sequence it is the
+// read of K.
 #include <atomic>
 #include <climits>
 
@@ -42,29 +44,39 @@ struct WCfg {
 
 struct WBars {
   uint64_t kfull[kMaxStages], kempty[kMaxStages], qfull[kMaxStages], qempty[kMaxStages];
-  uint64_t dfull[2], dempty[2], xfull[2], xempty[2], turn[2], drain[2];
+  uint64_t dfull[2], dempty[2], hfull[2], hempty[2], turn[2], drain[2];
   uint32_t tmem_base;
   int abort;
 };
 
 // What a launch fixes: the Q tile (qn queries x R heads = rows, NR columns),
-// the rings and the shared-memory offsets.
+// the rings and the units.
 struct WPlan {
   int32_t qn, rows, NR, qtiles, qst, kst, kqbytes, ktile;
-  int64_t units;
-  int32_t ktiles;
+  int32_t units, kunits;  // in all, and per head
 };
+constexpr int kUnitKeys = 256;
 
-// Q tiles [t0, t1) with a row that sees one of the keys [k0, k0 + 128).
-__device__ __forceinline__ void tile_range(const MaskDev& m, const WPlan& p, int b, int k0, int* t0, int* t1) {
-  int a = 0, z = p.qtiles;
-  if (m.causal || m.nd || m.len) {
-    while (a < z && row_span(m, b, min((a + 1) * p.qn, m.Nq) - 1).hi <= k0) ++a;
+struct WUnit {
+  int b, hk, k0, len;  // len: keys of the batch entry
+  int t0, t1;          // Q tiles with a row that sees one of the unit's keys
+};
+__device__ __forceinline__ WUnit unit_at(const MaskedArgs& a, const WPlan& p, int u) {
+  WUnit x;
+  const int bh = u / p.kunits;
+  x.k0 = (u - bh * p.kunits) * kUnitKeys;
+  x.b = bh / a.Hkv;
+  x.hk = bh - x.b * a.Hkv;
+  const MaskDev& m = a.mask;
+  x.len = m.len ? clamp_int(__ldg(m.len + x.b), 0, m.Nk) : m.Nk;
+  x.t0 = 0;
+  x.t1 = x.k0 < x.len ? p.qtiles : 0;
+  if (m.causal || m.nd) {
+    while (x.t0 < x.t1 && row_span(m, x.b, min((x.t0 + 1) * p.qn, m.Nq) - 1).hi <= x.k0) ++x.t0;
     if (m.nd)
-      while (z > a && row_span(m, b, (z - 1) * p.qn).lo >= k0 + 128) --z;
+      while (x.t1 > x.t0 && row_span(m, x.b, (x.t1 - 1) * p.qn).lo >= x.k0 + kUnitKeys) --x.t1;
   }
-  *t0 = a;
-  *t1 = z;
+  return x;
 }
 
 }  // namespace
@@ -78,23 +90,24 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sK = smem;
   uint8_t* sQ = sK + p.kst * p.ktile;
-  float* sL = reinterpret_cast<float*>(sQ + p.qst * p.kqbytes);  // [16 warps][128] -lse in exp2 units
-  float* sX = sL + WCfg::kEpiWarps * WCfg::kCols / 2;            // [2][3][128] sums of sets 1 to 3
-  WBars* bars = reinterpret_cast<WBars*>(sX + 2 * 3 * 128);
+  float* sL = reinterpret_cast<float*>(sQ + p.qst * p.kqbytes);  // [2][4 sets][128] -lse in exp2 units
+  int* sD = reinterpret_cast<int*>(sL + 2 * 4 * 128);            // [2][4 sets][4 warps] a row without lse
+  float* sX = reinterpret_cast<float*>(sD + 2 * 4 * 4);          // [2][128] half 1's sums of each key tile
+  WBars* bars = reinterpret_cast<WBars*>(sX + 2 * 128);
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&bars->kfull[s], 1);
-      mbar_init(&bars->kempty[s], 2);
+      mbar_init(&bars->kempty[s], 1);
       mbar_init(&bars->qfull[s], 1);
-      mbar_init(&bars->qempty[s], 1);
+      mbar_init(&bars->qempty[s], 2);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->dfull[b], 1);
       mbar_init(&bars->dempty[b], 256);
-      mbar_init(&bars->xfull[b], 3 * 128);
-      mbar_init(&bars->xempty[b], 128);
+      mbar_init(&bars->hfull[b], 128);
+      mbar_init(&bars->hempty[b], 128);
       mbar_init(&bars->turn[b], 1);
       mbar_init(&bars->drain[b], 1);
     }
@@ -122,96 +135,105 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
 
   if (warp < WCfg::kEpiWarps) {
     // ------------------------------------------------------------ epilogue
-    // Set = warp / 4: TMEM buffer set / 2, columns' half set % 2.
+    // Set = warp / 4: key tile set / 2, columns' half set % 2.
     const int set = warp >> 2, d = set >> 1, half = set & 1, tid = threadIdx.x & 127;
     const int H = p.NR / 2, col0 = half * H;
     const uint32_t sbase = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + d * WCfg::kCols + col0;
-    float* wL = sL + warp * (WCfg::kCols / 2);
-    // Column col0 + c * 32 + lane is query tile * qn + qo[c]: fixed per lane.
-    int off[4], qo[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int r = col0 + c * 32 + lane;
-      const bool row = c * 32 + lane < H && r < p.rows;
-      qo[c] = row ? r / a.R : INT_MAX / 2;
-      off[c] = row ? (r % a.R) * a.Nq + r / a.R : 0;
-    }
+    // The set's thread tid holds column col0 + tid: query tile * qn + qo of a head.
+    const int cr = col0 + tid;
+    const bool has = tid < H && cr < p.rows;
+    const int qo = has ? cr / a.R : INT_MAX / 2, off = has ? (cr % a.R) * a.Nq + qo : 0;
     const float sl = a.scale_log2;
-    uint32_t it = 0, xn = 0;
-    for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x, ++xn) {
-      const int bh = static_cast<int>(u / p.ktiles), k0 = static_cast<int>(u % p.ktiles) * 128;
-      const int b = bh / a.Hkv, hk = bh % a.Hkv;
-      int t0, t1;
-      tile_range(a.mask, p, b, k0, &t0, &t1);
-      const int key = k0 + tid;
-      const float* lse = wa.lse + (int64_t(b) * a.Hq + int64_t(hk) * a.R) * a.Nq;
-      const float* slopes = BIAS ? a.slopes + hk * a.R : nullptr;
+    const bool masks = a.mask.causal || a.mask.nd;  // (a length alone only decides which keys are written)
+    uint32_t it = 0, hn = 0;  // Q tiles, and sums handed on so far
+    // What a unit needs first is loaded while the unit before it is worked on.
+    WUnit nu = {};
+    float nwas = 0.f, next = 0.f;  // its entry as it was; lse of the coming tile's column
+    auto fetch = [&](const WUnit& x, int t) {
+      next = qo < a.Nq - t * p.qn
+                 ? __ldg(wa.lse + (int64_t(x.b) * a.Hq + int64_t(x.hk) * a.R) * a.Nq + int64_t(t) * p.qn + off)
+                 : 0.f;
+    };
+    auto look = [&](int u) {
+      nu = unit_at(a, p, u);
+      nwas = 0.f;
+      const int key = nu.k0 + d * 128 + tid;
+      if (!half && key < a.Nk && wa.w_in && (key >= nu.len || wa.decay != 0.f))
+        nwas = wa.w_in[(int64_t(nu.b) * a.Hkv + nu.hk) * a.Nk + key];
+      if (nu.t0 < nu.t1) fetch(nu, nu.t0);
+    };
+    if (static_cast<int>(blockIdx.x) < p.units) look(blockIdx.x);
+    for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+      const WUnit x = nu;
+      const float was = nwas;
+      const int b = x.b, key = x.k0 + d * 128 + tid;
+      const float* slopes = BIAS ? a.slopes + x.hk * a.R : nullptr;
       float total = 0.f;
-      float next[4];
-      const int first = t0 + ((it ^ d) & 1);
-      auto fetch = [&](int t) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) next[c] = qo[c] < a.Nq - t * p.qn ? __ldg(lse + int64_t(t) * p.qn + off[c]) : 0.f;
-      };
-      if (first < t1) fetch(first);
-      // set 0 writes: the entry as it was, and whether it takes part
-      const int len = a.mask.len ? clamp_int(__ldg(a.mask.len + b), 0, a.Nk) : a.Nk;
-      const int64_t wi = int64_t(bh) * a.Nk + key;
-      const bool mine = key < a.Nk && set == 0;
-      float was = 0.f;
-      if (mine && wa.w_in && (key >= len || wa.decay != 0.f)) was = wa.w_in[wi];
-      for (int t = first; t < t1; t += 2) {
-        const uint32_t n = it + (t - t0);
-        // lse of this tile's columns; a row without a finite one adds nothing
-        uint32_t dead = 0;
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const bool row = qo[c] < a.Nq - t * p.qn;
-          const bool fin = isfinite(next[c]);
-          wL[c * 32 + lane] = row && fin ? -next[c] * kLog2e : -INFINITY;
-          if (__any_sync(0xffffffffu, row && !fin)) dead |= 3u << (2 * c);
-        }
-        __syncwarp();
-        const int qa = t * p.qn, qz = min(qa + p.qn, a.Nq) - 1;
+      const bool more = static_cast<int>(u + gridDim.x) < p.units;
+      if (x.t0 >= x.t1 && more) look(u + gridDim.x);
+      for (int t = x.t0; t < x.t1; ++t, ++it) {
+        // lse of this tile's columns, by all of the set; a row without a finite one
+        // adds nothing.  (A warp that gives up arrives once, below `done`.)
+        float* wL = sL + ((it & 1) * 4 + set) * 128;
+        int* wD = sD + ((it & 1) * 4 + set) * 4;
+        const bool row = qo < a.Nq - t * p.qn, fin = isfinite(next);
+        wL[tid] = row && fin ? -next * kLog2e : -INFINITY;
+        const bool none = __any_sync(0xffffffffu, row && !fin);
+        if (lane == 0) wD[warp & 3] = none;
+        named_barrier(1 + set, 128);
+        if (*abort) goto done;
+        const int4 dead4 = *reinterpret_cast<const int4*>(wD);
+        const bool dead = (dead4.x | dead4.y | dead4.z | dead4.w) != 0;
+        const int qa = t * p.qn, qz = min(qa + p.qn, a.Nq) - 1, kt = x.k0 + d * 128;
         bool edge = false;
-        if (a.mask.causal || a.mask.nd || a.mask.len)
-          edge = row_span(a.mask, b, qz).lo > k0 || row_span(a.mask, b, qa).hi < min(k0 + 128, a.Nk);
-        if (t + 2 < t1) fetch(t + 2);
-        if (!mbar_wait(&bars->dfull[d], (n >> 1) & 1, abort)) goto done;
+        if (masks)
+          edge = row_span(a.mask, b, qz).lo > kt || row_span(a.mask, b, qa).hi < min(kt + 128, a.Nk);
+        if (t + 1 < x.t1)
+          fetch(x, t + 1);
+        else if (more)
+          look(u + gridDim.x);
+        if (!mbar_wait(&bars->dfull[d], it & 1, abort)) goto done;
         __syncwarp();
         tc_fence_after();
         uint64_t acc[2] = {0, 0};
-        // One pair's exponents from its raw products and -lse.
-        auto exponents = [&](uint64_t x, uint64_t L, int c) -> uint64_t {
-          uint64_t v = x;
-          if (CAP) {
-            const uint64_t ex = mul2(x, f2(a.cap_k1, a.cap_k1));
-            const uint64_t d1 = add2(f2(fast_exp2(f2lo(ex)), fast_exp2(f2hi(ex))), f2(1.f, 1.f));
-            v = fma2(f2(fast_rcp(f2lo(d1)), fast_rcp(f2hi(d1))), f2(-2.f * a.cap_log2, -2.f * a.cap_log2),
-                     f2(a.cap_log2, a.cap_log2));
-          }
-          return CAP ? add2(v, L) : fma2(v, f2(sl, sl), L);
+        // An exponent from its raw product and -lse.
+        auto exponent = [&](float x, float L) -> float {
+          if (CAP) return fmaf(-2.f * a.cap_log2, fast_rcp(1.f + fast_exp2(x * a.cap_k1)), a.cap_log2) + L;
+          return fmaf(x, sl, L);
         };
-        // The plain columns of the tile: the next 16 load while 16 are summed.
-        auto plain = [&]() {
-          float buf[2][16];
-          tmem_ld16(sbase, reinterpret_cast<uint32_t*>(buf[0]));
-          auto chunk = [&](int c, float* x, float* y) {
-            tmem_ld_wait();
-            if (c + 16 < H) tmem_ld16(sbase + c + 16, reinterpret_cast<uint32_t*>(y));
+        // The plain columns of the tile: the next 32 load while 32 are summed.
+        auto sum = [&](const float* x, int c, int count) {
+          const uint64_t sl2 = f2(sl, sl);
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const ulonglong2 L = *reinterpret_cast<const ulonglong2*>(wL + c + e);
-              const uint64_t v0 = exponents(f2(x[e], x[e + 1]), L.x, c + e);
-              const uint64_t v1 = exponents(f2(x[e + 2], x[e + 3]), L.y, c + e + 2);
-              acc[0] = add2(acc[0], f2(fast_exp2(f2lo(v0)), fast_exp2(f2hi(v0))));
-              acc[1] = add2(acc[1], f2(fast_exp2(f2lo(v1)), fast_exp2(f2hi(v1))));
+          for (int e = 0; e < count; e += 4) {
+            const ulonglong2 L = *reinterpret_cast<const ulonglong2*>(wL + c + e);
+            if (CAP) {
+              acc[0] = add2(acc[0], f2(fast_exp2(exponent(x[e], f2lo(L.x))), fast_exp2(exponent(x[e + 1], f2hi(L.x)))));
+              acc[1] = add2(acc[1], f2(fast_exp2(exponent(x[e + 2], f2lo(L.y))), fast_exp2(exponent(x[e + 3], f2hi(L.y)))));
+            } else {
+              const uint64_t y0 = fma2(f2(x[e], x[e + 1]), sl2, L.x), y1 = fma2(f2(x[e + 2], x[e + 3]), sl2, L.y);
+              acc[0] = add2(acc[0], f2(fast_exp2(f2lo(y0)), fast_exp2(f2hi(y0))));
+              acc[1] = add2(acc[1], f2(fast_exp2(f2lo(y1)), fast_exp2(f2hi(y1))));
             }
-          };
-          for (int c = 0; c < H; c += 32) {
-            chunk(c, buf[0], buf[1]);
-            if (c + 16 < H) chunk(c + 16, buf[1], buf[0]);
+          }
+        };
+        auto plain = [&]() {
+          if (H == 128) {
+            float buf[2][32];
+            tmem_ld32(sbase, reinterpret_cast<uint32_t*>(buf[0]));
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) {
+              tmem_ld_wait();
+              if (c + 32 < 128) tmem_ld32(sbase + c + 32, reinterpret_cast<uint32_t*>(buf[(c / 32 + 1) & 1]));
+              sum(buf[(c / 32) & 1], c, 32);
+            }
+          } else {
+            for (int c = 0; c < H; c += 16) {
+              float x[16];
+              tmem_ld16(sbase + c, reinterpret_cast<uint32_t*>(x));
+              tmem_ld_wait();
+              sum(x, c, 16);
+            }
           }
         };
         // With masked or dead columns, or a bias: each column's span, position
@@ -234,18 +256,18 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              const float2 L = *reinterpret_cast<const float2*>(wL + c + e);
-              const uint64_t v = exponents(f2(x[e], x[e + 1]), f2(L.x, L.y), c + e);
-              float y[2] = {f2lo(v), f2hi(v)};
+              float y[2];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
+                const float L = wL[c + e + i];
+                y[i] = exponent(x[e + i], L);
                 const int clo = __shfl_sync(0xffffffffu, lo, e + i), chi = __shfl_sync(0xffffffffu, hi, e + i);
                 if (BIAS) {
                   const float s = __shfl_sync(0xffffffffu, slope, e + i);
                   const int cp = __shfl_sync(0xffffffffu, pos, e + i);
                   y[i] = fmaf(s, fabsf(static_cast<float>(cp - key)), y[i]);
                 }
-                if (key < clo || key >= chi || (i ? L.y : L.x) == -INFINITY) y[i] = -INFINITY;
+                if (key < clo || key >= chi || L == -INFINITY) y[i] = -INFINITY;
               }
               acc[0] = add2(acc[0], f2(fast_exp2(y[0]), fast_exp2(y[1])));
             }
@@ -260,21 +282,21 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
         const uint64_t s2 = add2(acc[0], acc[1]);
         total += f2lo(s2) + f2hi(s2);
       }
-      it += t1 > t0 ? t1 - t0 : 0;
-      // sets 1 to 3 hand their sums to set 0
-      const uint32_t xb = xn & 1, xp = (xn >> 1) & 1;
-      float* x = sX + xb * 3 * 128 + tid;
-      if (set != 0) {
-        if (!mbar_wait(&bars->xempty[xb], xp ^ 1, abort)) goto done;
-        x[(set - 1) * 128] = total;
-        mbar_arrive(&bars->xfull[xb]);
-      } else {
-        if (!mbar_wait(&bars->xfull[xb], xp, abort)) goto done;
-        total = (total + x[0]) + (x[128] + x[256]);
-        mbar_arrive(&bars->xempty[xb]);
+      if (x.t0 < x.t1) {  // half 1 hands its sums to half 0
+        if (half) {
+          if (!mbar_wait(&bars->hempty[d], (hn & 1) ^ 1, abort)) goto done;
+          sX[d * 128 + tid] = total;
+          mbar_arrive(&bars->hfull[d]);
+        } else {
+          if (!mbar_wait(&bars->hfull[d], hn & 1, abort)) goto done;
+          total += sX[d * 128 + tid];
+          mbar_arrive(&bars->hempty[d]);
+        }
+        ++hn;
       }
-      if (mine) {
-        if (key < len)
+      if (!half && key < a.Nk) {
+        const int64_t wi = (int64_t(b) * a.Hkv + x.hk) * a.Nk + key;
+        if (key < x.len)
           wa.w_out[wi] = wa.decay != 0.f ? fmaf(wa.decay, was, total) : total;
         else if (wa.w_in && wa.w_in != wa.w_out)
           wa.w_out[wi] = was;  // an entry past the sequence stays as it was
@@ -282,36 +304,32 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
     }
   } else if (warp < WCfg::kTmaWarp) {
     // ------------------------------------------------------------ MMA issue
-    const int d = warp - WCfg::kMmaWarp;  // the TMEM buffer
+    const int d = warp - WCfg::kMmaWarp;  // the key tile
     if (lane == 0) {
       const uint32_t base = idesc_bf16(128, p.NR, false, false);
       const uint32_t kIdesc = a.neg_scale ? idesc_negate_b(base) : base;
       const uint64_t dq = sw128_desc(smem_u32(sQ), 16, 1024), dk = sw128_desc(smem_u32(sK), 16, 1024);
       const uint32_t q_lo = static_cast<uint32_t>(dq), q_hi = static_cast<uint32_t>(dq >> 32);
       const uint32_t k_lo = static_cast<uint32_t>(dk), k_hi = static_cast<uint32_t>(dk >> 32);
-      uint32_t it = 0, un = 0;
+      const uint32_t qstep = (p.NR * 128) >> 4;
+      uint32_t it = 0, kn = d;  // Q tiles so far; this warp's key tile in the ring
       bool ok = true;
-      for (int64_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
-        const int bh = static_cast<int>(u / p.ktiles), k0 = static_cast<int>(u % p.ktiles) * 128;
-        int t0, t1;
-        tile_range(a.mask, p, bh / a.Hkv, k0, &t0, &t1);
-        if (t1 <= t0) continue;
-        const uint32_t ks = un % p.kst;
-        if (!mbar_wait(&bars->kfull[ks], (un / p.kst) & 1, abort)) break;
-        bool any = false;
-        for (int t = t0; t < t1; ++t, ++it) {
-          if ((it & 1) != static_cast<uint32_t>(d)) continue;
-          any = true;
+      for (int u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
+        const WUnit x = unit_at(a, p, u);
+        if (x.t1 <= x.t0) continue;
+        const uint32_t ks = kn % p.kst;
+        if (!mbar_wait(&bars->kfull[ks], (kn / p.kst) & 1, abort)) break;
+        const uint32_t kl = k_lo + ((ks * p.ktile) >> 4);
+        for (int t = x.t0; t < x.t1; ++t, ++it) {
           const uint32_t qs = it % p.qst;
           if (!mbar_wait(&bars->qfull[qs], (it / p.qst) & 1, abort) ||
-              !mbar_wait(&bars->dempty[d], ((it >> 1) & 1) ^ 1, abort) ||
-              (it > 0 && !mbar_wait(&bars->turn[d], ((it - 1) >> 1) & 1, abort))) {
+              !mbar_wait(&bars->dempty[d], (it & 1) ^ 1, abort) ||
+              (it + d > 0 && !mbar_wait(&bars->turn[d], (it + d - 1) & 1, abort))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t kl = k_lo + ((ks * p.ktile) >> 4), ql = q_lo + ((qs * p.kqbytes) >> 4);
-          const uint32_t qstep = (p.NR * 128) >> 4;
+          const uint32_t ql = q_lo + ((qs * p.kqbytes) >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t in = ((kk & 3) * 32) >> 4;
@@ -321,10 +339,9 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
           }
           mma_commit(&bars->dfull[d]);
           mma_commit(&bars->qempty[qs]);
-          if (t + 2 >= t1) mma_commit(&bars->kempty[ks]);
         }
-        if (ok && !any) mbar_arrive(&bars->kempty[ks]);
-        ++un;
+        if (ok) mma_commit(&bars->kempty[ks]);
+        kn += 2;
       }
       mma_commit(&bars->drain[d]);
       const long long c0 = clock64();
@@ -334,33 +351,35 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
   } else if (warp == WCfg::kTmaWarp && lane == 0) {
     // ------------------------------------------------------------ loads (TMA)
     const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sK);
-    uint32_t it = 0, un = 0;
+    uint32_t it = 0, un = 0;  // Q tiles and key tiles loaded
     bool ok = true;
-    for (int64_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
-      const int bh = static_cast<int>(u / p.ktiles), k0 = static_cast<int>(u % p.ktiles) * 128;
-      const int b = bh / a.Hkv, hk = bh % a.Hkv;
-      int t0, t1;
-      tile_range(a.mask, p, b, k0, &t0, &t1);
-      if (t1 <= t0) continue;
-      const uint32_t ks = un % p.kst;
-      if (!mbar_wait(&bars->kempty[ks], ((un / p.kst) & 1) ^ 1, abort)) break;
-      mbar_expect_tx(&bars->kfull[ks], p.ktile);
+    auto load_q = [&](const WUnit& x, int t) -> bool {
+      const uint32_t qs = it % p.qst;
+      if (!mbar_wait(&bars->qempty[qs], ((it / p.qst) & 1) ^ 1, abort)) return false;
+      mbar_expect_tx(&bars->qfull[qs], p.rows * D * 2);
 #pragma unroll
       for (int cb = 0; cb < D / 64; ++cb)
-        tma_load_4d(k_addr + ks * p.ktile + cb * 128 * 128, &tm_k, 64 * cb, k0, hk, b, &bars->kfull[ks]);
-      ++un;
-      for (int t = t0; t < t1; ++t, ++it) {
-        const uint32_t qs = it % p.qst;
-        if (!mbar_wait(&bars->qempty[qs], ((it / p.qst) & 1) ^ 1, abort)) {
-          ok = false;
-          break;
-        }
-        mbar_expect_tx(&bars->qfull[qs], p.rows * D * 2);
+        tma_load_4d(q_addr + qs * p.kqbytes + cb * p.NR * 128, &tm_q, 64 * cb, x.hk * a.R, t * p.qn, x.b,
+                    &bars->qfull[qs]);
+      ++it;
+      return true;
+    };
+    for (int u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
+      const WUnit x = unit_at(a, p, u);
+      if (x.t1 <= x.t0) continue;
+      // the first Q tile ahead of K, whose place may still be in use
+      if (!(ok = load_q(x, x.t0))) break;
+      for (int d = 0; d < 2 && ok; ++d) {
+        const uint32_t ks = un % p.kst;
+        if (!(ok = mbar_wait(&bars->kempty[ks], ((un / p.kst) & 1) ^ 1, abort))) break;
+        mbar_expect_tx(&bars->kfull[ks], p.ktile);
 #pragma unroll
         for (int cb = 0; cb < D / 64; ++cb)
-          tma_load_4d(q_addr + qs * p.kqbytes + cb * p.NR * 128, &tm_q, 64 * cb, hk * a.R, t * p.qn, b,
-                      &bars->qfull[qs]);
+          tma_load_4d(k_addr + ks * p.ktile + cb * 128 * 128, &tm_k, 64 * cb, x.k0 + d * 128, x.hk, x.b,
+                      &bars->kfull[ks]);
+        ++un;
       }
+      for (int t = x.t0 + 1; t < x.t1 && ok; ++t) ok = load_q(x, t);
     }
     // After an abort: the copies in flight land before the block ends.
     if (*abort) {
@@ -377,6 +396,7 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
     }
   }
 done:
+  if (warp < WCfg::kEpiWarps && *abort) named_barrier_arrive(1 + (warp >> 2), 128);
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && bars->abort) report(a.status, SA_DEVERR_TIMEOUT);
@@ -391,7 +411,7 @@ template <int D, bool CAP, bool BIAS>
 static cudaError_t launch_w(const WeightArgs& a, const WPlan& p, const CUtensorMap& tq, const CUtensorMap& tk,
                             int num_sms, cudaStream_t st) {
   auto kern = sa_cache_weights_kernel<D, CAP, BIAS>;
-  int smem = 1024 + p.kst * p.ktile + p.qst * p.kqbytes + WCfg::kEpiWarps * WCfg::kCols * 2 + 2 * 3 * 128 * 4 +
+  int smem = 1024 + p.kst * p.ktile + p.qst * p.kqbytes + 2 * 4 * 128 * 4 + 2 * 4 * 4 * 4 + 2 * 128 * 4 +
              static_cast<int>(sizeof(WBars)) + 64;
   if (smem < 120 * 1024) smem = 120 * 1024;  // one block per SM owns its TMEM
   static std::atomic<int> regs_ok{0};  // 0 unknown, 1 enough, 2 too few
@@ -405,8 +425,8 @@ static cudaError_t launch_w(const WeightArgs& a, const WPlan& p, const CUtensorM
   if (regs_ok.load() != 1) return cudaErrorLaunchOutOfResources;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t grid = p.units < num_sms ? p.units : num_sms;
-  kern<<<static_cast<unsigned>(grid), WCfg::kThreads, smem, st>>>(a, p, tq, tk);
+  const int grid = p.units < num_sms ? p.units : num_sms;
+  kern<<<grid, WCfg::kThreads, smem, st>>>(a, p, tq, tk);
   return cudaGetLastError();
 }
 
@@ -419,11 +439,12 @@ cudaError_t launch_cache_weights(const WeightArgs& a, int num_sms, cudaStream_t 
   p.qtiles = (m.Nq + p.qn - 1) / p.qn;
   p.ktile = 128 * m.d * 2;
   p.kqbytes = p.NR * m.d * 2;
-  p.qst = p.NR <= 64 ? kMaxStages : 2;
+  p.qst = p.NR <= 64 ? 4 : 2;
   const int room = 212 * 1024 - p.qst * p.kqbytes;  // the rest is under 15 KB
   p.kst = room / p.ktile < kMaxStages ? room / p.ktile : kMaxStages;
-  p.ktiles = (m.Nk + 127) / 128;
-  p.units = int64_t(m.B) * m.Hkv * p.ktiles;
+  p.kst &= ~1;  // whole units
+  p.kunits = (m.Nk + kUnitKeys - 1) / kUnitKeys;
+  p.units = m.B * m.Hkv * p.kunits;  // (the entry point checks that it fits)
   CUtensorMap tq, tk;
   if (!make_view_map(&tq, m.q, m.d, m.Nq, m.Hq, m.B, m.qs.n, m.qs.h, m.qs.b, p.qn, m.R, true) ||
       !make_view_map(&tk, m.k, m.d, m.Nk, m.Hkv, m.B, m.ks.n, m.ks.h, m.ks.b, 128, 1, false))

@@ -196,6 +196,7 @@ sa_status sparse_attn_cache_weights(const sa_masked* p, const void* q, const voi
   if (!lse || !w_out || !std::isfinite(decay) || (decay != 0.f && !w_in)) return SA_ERR_INVALID_ARG;
   if (!aligned(lse, 4) || !aligned(w_in, 4) || !aligned(w_out, 4) || !aligned(dev_status, 4))
     return SA_ERR_INVALID_ARG;
+  if (int64_t(p->B) * p->Hkv * ((int64_t(p->Nk) + 255) / 256) >= (int64_t(1) << 30)) return SA_ERR_UNSUPPORTED;
   const uint64_t wbytes = uint64_t(p->B) * p->Hkv * p->Nk * 4, lbytes = uint64_t(a.total_rows) * 4;
   if (w_in && w_in != w_out && overlap(w_in, wbytes, w_out, wbytes)) return SA_ERR_INVALID_ARG;
   if (overlap(lse, lbytes, w_out, wbytes) || overlap(q, nq, w_out, wbytes) || overlap(k, nk, w_out, wbytes))
