@@ -69,7 +69,8 @@ struct MCfg {
   static constexpr int kTile = BN * D * 2;
   static constexpr int kQBytes = T * 128 * D * 2;
   static constexpr int kStages = D == 128 ? (T == 2 ? 4 : 5) : 8;
-  static constexpr int kXch = T * 2 * 2 * 128 * 8;  // [slot][tile][half][row] float2
+  static constexpr int kWarpBytes = 2048;  // a softmax warp's own: exchange slots, output staging
+  static constexpr int kXch = kSoftWarps * kWarpBytes;
   static constexpr int kSmemBytes = 1024 + kQBytes + kStages * kTile + kXch + 1024;
   static constexpr int kOCol = T * 128;
   static constexpr int kTmemCols = T == 2 ? 512 : 256;
@@ -82,7 +83,11 @@ struct MBars {
   uint64_t sfull[T], pfull[T], ofull[T], ofree[T];
   uint64_t qfull, qempty, next, tail, tail_here, turn[T], ring_full[2], ring_empty[2], drain[T];
   uint4 answer;   // of the request for the next unit
-  int4 ring[2];   // unit (-1: no more), first key, key tiles, end of the span
+  struct Unit {
+    int go;                // 0: no more units
+    int key0, n, uhi;      // first key, key tiles, end of the rows' span
+    int part, q0, b, hk;   // partial result (-1: whole), first query, batch entry, key head
+  } ring[2];
   int flag[T * 4][2];
   uint32_t tmem_base;
   int abort;
@@ -91,6 +96,10 @@ struct MBars {
 template <bool M>
 struct Masked {
   static constexpr bool value = M;
+};
+template <int N>
+struct Words {
+  static constexpr int value = N;
 };
 
 }  // namespace
@@ -106,8 +115,8 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem;
   uint8_t* sKV = sQ + C::kQBytes;
-  float2* sX = reinterpret_cast<float2*>(sKV + S * C::kTile);
-  MBars<T, S>* bars = reinterpret_cast<MBars<T, S>*>(reinterpret_cast<uint8_t*>(sX) + C::kXch);
+  uint8_t* sX = sKV + S * C::kTile;
+  MBars<T, S>* bars = reinterpret_cast<MBars<T, S>*>(sX + C::kXch);
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -160,27 +169,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
       reg_dealloc<C::kRegOther>();
   }
 
-  // Unit number -> heads outermost (their K and V stay in L2), row blocks from
-  // the last (with a causal mask the longest) to the first; units from
-  // full_units on are split over their keys.
-  struct Unit {
-    int part, splits, split, q0, b, hk;
-  };
-  auto unit_of = [&](int g) -> Unit {
-    Unit x = {-1, 1, 0, 0, 0, 0};
-    int u = g;
-    if (g >= a.full_units) {
-      x.part = g - static_cast<int>(a.full_units);
-      x.splits = a.splits;
-      x.split = x.part % a.splits;
-      u = static_cast<int>(a.full_units) + x.part / a.splits;
-    }
-    x.q0 = (a.row_blocks - 1 - u % a.row_blocks) * (T * a.qn);
-    const int bh = u / a.row_blocks;
-    x.b = bh / a.Hkv;
-    x.hk = bh % a.Hkv;
-    return x;
-  };
+  using Unit = typename MBars<T, S>::Unit;
 
   if (warp < C::kSoftWarps) {
     // ------------------------------------------------------------ softmax
@@ -199,8 +188,11 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
     uint32_t xn = 0;           // pair exchanges so far
     uint32_t tc = 0, uc = 0;   // key tiles and units with keys so far
     // Slot of exchange xn: this half's value, and the other half's.
-    auto mine = [&]() -> float2* { return sX + (((xn & 1) * T + t) * 2 + half) * 128 + trow; };
-    auto other = [&]() -> float2* { return sX + (((xn & 1) * T + t) * 2 + (half ^ 1)) * 128 + trow; };
+    uint8_t* own = sX + warp * C::kWarpBytes;
+    auto mine = [&]() -> float2* { return reinterpret_cast<float2*>(own) + (xn & 1) * 32 + lane; };
+    auto other = [&]() -> float2* {
+      return reinterpret_cast<float2*>(sX + (warp ^ 4) * C::kWarpBytes) + (xn & 1) * 32 + lane;
+    };
     // Meets the other half's warp.  A warp that gives up sets *abort and arrives
     // once (below `done`), and whoever it releases gives up too.
     auto pair_sync = [&]() -> bool {
@@ -209,12 +201,11 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
     };
     for (uint32_t i = 0;; ++i) {
       if (!mbar_wait(&bars->ring_full[i & 1], (i >> 1) & 1, abort)) goto done;
-      const int4 e = *const_cast<const int4*>(&bars->ring[i & 1]);
+      const Unit x = bars->ring[i & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->ring_empty[i & 1]);
-      if (e.x < 0) break;
-      const Unit x = unit_of(e.x);
-      const int key0 = e.y, n = e.z;
+      if (!x.go) break;
+      const int key0 = x.key0, n = x.n;
       const int qi = x.q0 + t * a.qn + rq, hq = x.hk * a.R + rh;
       const bool valid = in_tile && qi < a.Nq;
       const bool idle = !__any_sync(0xffffffffu, valid);
@@ -424,36 +415,58 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
           else if (a.lse)
             a.lse[(int64_t(x.b) * a.Hq + hq) * a.Nq + qi] = lse;
         }
-        const int64_t oo = int64_t(x.b) * a.os.b + int64_t(hq) * a.os.h + int64_t(qi) * a.os.n + half * (D / 2);
-        float* dst32 = x.part >= 0 ? a.part_o + prow * D + half * (D / 2) : static_cast<float*>(a.o) + oo;
+        // The warp's 32 half rows go out through its own shared memory, so that
+        // consecutive lanes write consecutive bytes of a row (a store of 16 bytes
+        // from each of 32 rows touches 32 lines; the output of a unit took 3.5 us).
+        const bool wide = x.part >= 0 || a.out_fp32;
+        char* base = x.part >= 0 ? reinterpret_cast<char*>(a.part_o) : static_cast<char*>(a.o);
+        int64_t at = x.part >= 0 ? prow * D : int64_t(x.b) * a.os.b + int64_t(hq) * a.os.h + int64_t(qi) * a.os.n;
+        at = valid ? (at + half * (D / 2)) * (wide ? 4 : 2) : -1;
+        uint32_t v[D / 2];
+        if (n > 0) {
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          float v[32];
-          if (n > 0) {
-            tmem_ld32(obase + c * 32, reinterpret_cast<uint32_t*>(v));
-            tmem_ld_wait();
-            if (c == D / 64 - 1) {
-              tc_fence_before();
-              mbar_arrive(&bars->ofree[t]);
+          for (int c = 0; c < D / 64; ++c) tmem_ld32(obase + c * 32, v + c * 32);
+          tmem_ld_wait();
+          tc_fence_before();
+          mbar_arrive(&bars->ofree[t]);
+#pragma unroll
+          for (int y = 0; y < D / 2; ++y) v[y] = __float_as_uint(inv == 0.f ? 0.f : __uint_as_float(v[y]) * inv);
+        } else {
+#pragma unroll
+          for (int y = 0; y < D / 2; ++y) v[y] = 0;
+        }
+        if (!pair_sync()) goto done;  // the other half has read this warp's slot
+        auto put = [&](auto words) {  // words per half row
+          constexpr int P = decltype(words)::value / 4;                // 16-byte pieces of it
+          constexpr int kRows = C::kWarpBytes / 16 / P;                // rows at a time
+          uint4* st = reinterpret_cast<uint4*>(own);
+          auto cell = [&](int r, int c) -> uint4* {  // (no bank conflicts either way)
+            return st + r * P + (P >= 8 ? (c & ~7) | ((c ^ r) & 7) : c ^ ((r >> 1) & 3));
+          };
+#pragma unroll
+          for (int r0 = 0; r0 < 32; r0 += kRows) {
+            if (lane >= r0 && lane < r0 + kRows) {
+#pragma unroll
+              for (int c = 0; c < P; ++c) *cell(lane - r0, c) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
             }
+            __syncwarp();
 #pragma unroll
-            for (int y = 0; y < 32; ++y) v[y] = inv == 0.f ? 0.f : v[y] * inv;
-          } else {
-#pragma unroll
-            for (int y = 0; y < 32; ++y) v[y] = 0.f;
+            for (int f = 0; f < kRows * P; f += 32) {
+              const int r = (f + lane) / P, c = (f + lane) % P;
+              const int64_t to = __shfl_sync(0xffffffffu, at, r0 + r);
+              const uint4 w = *cell(r, c);
+              if (to >= 0) *reinterpret_cast<uint4*>(base + to + c * 16) = w;
+            }
+            __syncwarp();
           }
-          if (valid && (x.part >= 0 || a.out_fp32)) {
-            float4* dst = reinterpret_cast<float4*>(dst32 + c * 32);
+        };
+        if (wide) {
+          put(Words<D / 2>());
+        } else {
 #pragma unroll
-            for (int y = 0; y < 8; ++y) dst[y] = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
-          } else if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + oo + c * 32);
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-              dst[y] = make_uint4(pack_bf16(v[8 * y], v[8 * y + 1]), pack_bf16(v[8 * y + 2], v[8 * y + 3]),
-                                  pack_bf16(v[8 * y + 4], v[8 * y + 5]), pack_bf16(v[8 * y + 6], v[8 * y + 7]));
-          }
-          __syncwarp();
+          for (int y = 0; y < D / 4; ++y)
+            v[y] = pack_bf16(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1]));
+          put(Words<D / 4>());
         }
       } else if (n > 0) {
         mbar_arrive(&bars->ofree[t]);
@@ -502,10 +515,10 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
       uint32_t tc = 0, uc = 0, zc = 0;  // key tiles, units with keys and cleared tails so far
       for (uint32_t i = 0; ok; ++i) {
         if (!mbar_wait(&bars->ring_full[i & 1], (i >> 1) & 1, abort)) break;
-        const int4 e = *const_cast<const int4*>(&bars->ring[i & 1]);
+        const Unit x = bars->ring[i & 1];
         mbar_arrive(&bars->ring_empty[i & 1]);
-        if (e.x < 0) break;
-        const int key0 = e.y, n = e.z, uhi = e.w;
+        if (!x.go) break;
+        const int key0 = x.key0, n = x.n, uhi = x.uhi;
         if (n == 0) continue;
         // Ring entries: K(j) is number 2 (tc + j), V(j) the one behind it.
         if (!(ok = mbar_wait(&bars->qfull, uc & 1, abort)) || !(ok = ready(2 * tc))) break;
@@ -553,14 +566,14 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
     uint32_t tc = 0, zc = 0;
     for (uint32_t i = 0;; ++i) {
       if (!mbar_wait(&bars->ring_full[i & 1], (i >> 1) & 1, abort)) break;
-      const int4 e = *const_cast<const int4*>(&bars->ring[i & 1]);
+      const Unit x = bars->ring[i & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->ring_empty[i & 1]);
-      if (e.x < 0) break;
+      if (!x.go) break;
       const uint32_t iv = 2 * tc + 1;  // the unit's first V: tiles come last first
-      tc += e.z;
-      const int live = e.w - (e.y + (e.z - 1) * BN);
-      if (e.z == 0 || live >= BN) continue;
+      tc += x.n;
+      const int live = x.uhi - (x.key0 + (x.n - 1) * BN);
+      if (x.n == 0 || live >= BN) continue;
       if (!mbar_wait(&bars->tail_here, zc++ & 1, abort)) break;
       uint8_t* vt = sKV + (iv % S) * C::kTile;
       for (int f = lane; f < (BN - live) * (D / 8); f += 32) {
@@ -579,22 +592,37 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
     bool ok = true;
     uint32_t i = 0;
     for (; ok; ++i) {
-      int key0 = 0, n = 0, uhi = 0;
       Unit x = {};
       if (g >= 0) {
         mbar_expect_tx(&bars->next, 16);
         request_block(&bars->answer, &bars->next);
+        // Heads outermost (their K and V stay in L2), row blocks from the last
+        // (with a causal mask the longest) to the first; units from full_units on
+        // are split over their keys.
+        int u = static_cast<int>(g), split = 0, splits = 1;
+        x.go = 1;
+        x.part = -1;
+        if (g >= a.full_units) {
+          splits = a.splits;
+          x.part = static_cast<int>(g - a.full_units);
+          split = x.part % splits;
+          u = static_cast<int>(a.full_units) + x.part / splits;
+        }
+        const int bh = u / a.row_blocks;
+        x.q0 = (a.row_blocks - 1 - (u - bh * a.row_blocks)) * (T * a.qn);
+        x.b = bh / a.Hkv;
+        x.hk = bh - x.b * a.Hkv;
         // keys that any of the unit's rows sees, and this split's run of tiles
-        x = unit_of(static_cast<int>(g));
         const int ulo = row_span(a.mask, x.b, x.q0).lo;
-        uhi = row_span(a.mask, x.b, min(x.q0 + T * a.qn, a.Nq) - 1).hi;
-        const int ntiles = uhi > ulo ? (uhi - ulo + BN - 1) / BN : 0;
-        const int j0 = static_cast<int>(int64_t(ntiles) * x.split / x.splits);
-        n = static_cast<int>(int64_t(ntiles) * (x.split + 1) / x.splits) - j0;
-        key0 = ulo + j0 * BN;
+        x.uhi = row_span(a.mask, x.b, min(x.q0 + T * a.qn, a.Nq) - 1).hi;
+        const int ntiles = x.uhi > ulo ? (x.uhi - ulo + BN - 1) / BN : 0;
+        const int j0 = static_cast<int>(int64_t(ntiles) * split / splits);
+        x.n = static_cast<int>(int64_t(ntiles) * (split + 1) / splits) - j0;
+        x.key0 = ulo + j0 * BN;
       }
+      const int key0 = x.key0, n = x.n;
       if (i >= 2 && !mbar_wait(&bars->ring_empty[i & 1], ((i >> 1) - 1) & 1, abort)) break;
-      bars->ring[i & 1] = make_int4(static_cast<int>(g), key0, n, uhi);
+      bars->ring[i & 1] = x;
       mbar_arrive(&bars->ring_full[i & 1]);
       if (g < 0) break;
       if (n > 0) {
