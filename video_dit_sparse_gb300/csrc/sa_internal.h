@@ -143,9 +143,9 @@ struct MaskedArgs {
   float cap_p1, cap_p2, cap_p3, cap_limit;
   int64_t total_rows;  // B * Hq * Nq
   // masked_plan: a Q tile holds qn queries of R heads each, a unit unit_rows / 128
-  // tiles, a key head row_blocks units; the first
+  // tiles, a key head row_blocks units, `group` heads are worked on at a time; the first
   // full_units run whole, the other split_units in `splits` runs of keys
-  int32_t qn, unit_rows, row_blocks, splits;
+  int32_t qn, unit_rows, row_blocks, group, splits;
   int64_t full_units, split_units;
   float* part_o;       // [split_units * splits, unit_rows, d] partials
   float* part_lse;     // [split_units * splits, unit_rows]

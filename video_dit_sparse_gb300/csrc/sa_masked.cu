@@ -93,6 +93,17 @@ struct MBars {
   int abort;
 };
 
+// Unit number -> key head of the batch and row block.
+struct Place {
+  int bh, rb;
+};
+__host__ __device__ __forceinline__ Place place_of(const MaskedArgs& a, int u) {
+  const int per = a.group * a.row_blocks, grp = u / per, r = u - grp * per;
+  const int heads = a.B * a.Hkv - grp * a.group < a.group ? a.B * a.Hkv - grp * a.group : a.group;
+  const int k = r / heads;
+  return {grp * a.group + (r - k * heads), a.row_blocks - 1 - k};
+}
+
 template <bool M>
 struct Masked {
   static constexpr bool value = M;
@@ -308,22 +319,36 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
             tmem_ld_wait();
             if (base + W < H) load(buf[(base / W + 1) & 1], base + W);
             if (BIAS && base) g = f2(g0 - static_cast<float>(base) * ns, g0 - static_cast<float>(base + 1) * ns);
+            auto columns = [&](auto some) {
 #pragma unroll
-            for (int c = 0; c < W / 2; ++c) {
-              const uint64_t xx = f2(s[2 * c], s[2 * c + 1]);
-              uint64_t f = sl2;
-              if (CAP) {
-                const uint64_t w = mul2(xx, xx);
-                wm = fmax3(wm, f2lo(w), f2hi(w));
-                f = fma2(w, fma2(w, fma2(w, k3, k2), k1), sl2);
+              for (int c = 0; c < W / 2; ++c) {
+                const uint64_t xx = f2(s[2 * c], s[2 * c + 1]);
+                uint64_t f = sl2;
+                if (CAP) {
+                  const uint64_t w = mul2(xx, xx);
+                  wm = fmax3(wm, f2lo(w), f2hi(w));
+                  f = fma2(w, fma2(w, fma2(w, k3, k2), k1), sl2);
+                }
+                const uint64_t y = fma2(xx, f, g);
+                if (decltype(some)::value)
+                  take(hidden(base + 2 * c) ? -INFINITY : f2lo(y), hidden(base + 2 * c + 1) ? -INFINITY : f2hi(y),
+                       base / 2 + c);
+                else
+                  take(f2lo(y), f2hi(y), base / 2 + c);
+                if (BIAS) g = add2(g, step);
               }
-              const uint64_t y = fma2(xx, f, g);
-              if (decltype(masked)::value)
-                take(hidden(base + 2 * c) ? -INFINITY : f2lo(y), hidden(base + 2 * c + 1) ? -INFINITY : f2hi(y),
-                     base / 2 + c);
-              else
-                take(f2lo(y), f2hi(y), base / 2 + c);
-              if (BIAS) g = add2(g, step);
+            };
+            // Of a tile at the mask's edge, columns that no row sees cost nothing
+            // and those that every row sees what they always do.
+            if (!decltype(masked)::value) {
+              columns(Masked<false>());
+            } else if (!__any_sync(0xffffffffu, valid && va < base + W && vb > base)) {
+#pragma unroll
+              for (int c = 0; c < W / 2; ++c) p[base / 2 + c] = 0;
+            } else if (__any_sync(0xffffffffu, valid && (va > base || vb < base + W))) {
+              columns(Masked<true>());
+            } else {
+              columns(Masked<false>());
             }
           }
           return !CAP || !__any_sync(0xffffffffu, valid && !(wm <= a.cap_limit));
@@ -596,9 +621,11 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
       if (g >= 0) {
         mbar_expect_tx(&bars->next, 16);
         request_block(&bars->answer, &bars->next);
-        // Heads outermost (their K and V stay in L2), row blocks from the last
-        // (with a causal mask the longest) to the first; units from full_units on
-        // are split over their keys.
+        // Heads in groups whose K and V stay in L2; in a group the row blocks from
+        // the last (with a causal mask the longest) to the first, each of all its
+        // heads: long units start first and short ones fill the end (one head
+        // after the other left a fifth of the time to the last head's long units).
+        // Units from full_units on are split over their keys.
         int u = static_cast<int>(g), split = 0, splits = 1;
         x.go = 1;
         x.part = -1;
@@ -608,8 +635,9 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
           split = x.part % splits;
           u = static_cast<int>(a.full_units) + x.part / splits;
         }
-        const int bh = u / a.row_blocks;
-        x.q0 = (a.row_blocks - 1 - (u - bh * a.row_blocks)) * (T * a.qn);
+        const Place at = place_of(a, u);
+        const int bh = at.bh;
+        x.q0 = at.rb * (T * a.qn);
         x.b = bh / a.Hkv;
         x.hk = bh - x.b * a.Hkv;
         // keys that any of the unit's rows sees, and this split's run of tiles
@@ -684,11 +712,11 @@ __global__ void __launch_bounds__(256) sa_masked_join_kernel(const __grid_consta
   const int unit_rows = a.unit_rows;
   const int64_t su = i / unit_rows;  // split unit
   const int r = static_cast<int>(i % unit_rows);
-  const int64_t u = a.full_units + su;
-  const int64_t bh = u / a.row_blocks;
-  if (bh >= int64_t(a.B) * a.Hkv) return;
+  if (su >= a.split_units) return;
+  const Place at = place_of(a, static_cast<int>(a.full_units + su));
+  const int64_t bh = at.bh;
   const int tr = r % 128;  // row of its Q tile
-  const int64_t q = (a.row_blocks - 1 - u % a.row_blocks) * (unit_rows / 128 * a.qn) + r / 128 * a.qn + tr / a.R;
+  const int64_t q = int64_t(at.rb) * (unit_rows / 128 * a.qn) + r / 128 * a.qn + tr / a.R;
   if (tr >= a.qn * a.R || q >= a.Nq) return;
   const float* pl = a.part_lse + su * a.splits * unit_rows + r;
   float mx = -INFINITY;
@@ -721,18 +749,34 @@ __global__ void __launch_bounds__(256) sa_masked_join_kernel(const __grid_consta
 // Units that fill whole waves of SMs run whole; the rest (all, if they are
 // fewer than the SMs) are split into the number of key runs that ends first by
 // this count of tile times: a wave costs its tiles plus a block's start, a
-// split the join.
+// split the join.  What the host knows of their tiles: the mask without
+// documents and lengths (a causal mask leaves little to the last units).
 void masked_plan(MaskedArgs* a) {
   a->qn = 128 / a->R;
   const int T = a->Nq > a->qn ? 2 : 1;
   a->unit_rows = 128 * T;
-  a->row_blocks = (a->Nq + T * a->qn - 1) / (T * a->qn);
+  const int64_t unit_q = int64_t(T) * a->qn;
+  a->row_blocks = static_cast<int32_t>((a->Nq + unit_q - 1) / unit_q);
   if (a->qn > a->Nq) a->qn = a->Nq;
-  const int64_t units = int64_t(a->B) * a->Hkv * a->row_blocks, rest = units % kSms;
-  const int64_t tiles = (int64_t(a->Nk) + BN - 1) / BN;
+  // heads whose K and V (together half the L2) are worked on at a time
+  const int64_t heads = int64_t(a->B) * a->Hkv, fit = (int64_t(64) << 20) / (int64_t(a->Nk) * a->d * 4);
+  const int64_t groups = fit < 1 ? heads : (heads + fit - 1) / fit;
+  a->group = static_cast<int32_t>((heads + groups - 1) / groups);
+  const int64_t units = heads * a->row_blocks, rest = units % kSms;
+  int64_t seen = 0;  // keys that the last units see
+  for (int64_t u = units - rest; u < units; ++u) {
+    const int64_t q1 = min64(a->Nq, (place_of(*a, static_cast<int>(u)).rb + 1) * unit_q);
+    int64_t hi = a->Nk;
+    if (a->mask.causal) {
+      const int64_t pos = q1 - 1 + a->Nk - a->Nq;
+      hi = pos < 0 ? 0 : min64(hi, (pos / a->mask.causal + 1) * a->mask.causal);
+    }
+    seen += hi;
+  }
+  const int64_t tiles = rest ? (seen / rest + BN - 1) / BN : 0;
   constexpr int64_t kStart = 5, kJoin = 8;
   int64_t best = 1, cost = tiles + kStart;
-  for (int64_t s = 2; s <= tiles && s <= 64 && rest; ++s) {
+  for (int64_t s = 2; s <= tiles && s <= 64; ++s) {
     const int64_t c = (rest * s + kSms - 1) / kSms * ((tiles + s - 1) / s + kStart) + kJoin;
     if (c < cost) {
       cost = c;

@@ -107,7 +107,7 @@ sa_status check_masked(const sa_masked* p, sa::MaskedArgs* a) {
   a->cap_p3 = static_cast<float>(kTanh3 * s * log2e * r2 * r2 * r2);
   a->cap_limit = r2 > 0.0 && r2 < 1e6 ? static_cast<float>(0.16 / r2) : -1.f;
   a->total_rows = int64_t(p->B) * p->Hq * p->Nq;
-  a->qn = a->unit_rows = a->row_blocks = a->splits = 1;
+  a->qn = a->unit_rows = a->row_blocks = a->group = a->splits = 1;
   a->full_units = a->split_units = 0;
   a->part_o = nullptr;
   a->part_lse = nullptr;
@@ -160,7 +160,6 @@ sa_status sparse_attn_forward_masked(const sa_masked* p, const void* q, const vo
   sa::masked_plan(&a);
   const size_t need = masked_workspace(a);
   if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return SA_ERR_INVALID_ARG;
-  if (a.full_units + a.split_units * a.splits >= (int64_t(1) << 31)) return SA_ERR_UNSUPPORTED;  // grid.x
   int sms = 0;
   if ((st = device_info(&sms)) != SA_OK) return st;
   if (!in_device_allocation(q, nq) || !in_device_allocation(k, nk) || !in_device_allocation(v, nv) ||
