@@ -226,6 +226,11 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
       if (BIAS && valid) nslope = -__ldg(a.slopes + hq) * kLog2e;
       float m = -INFINITY, l = 0.f, lr = 0.f;
       for (int j = 0; j < n; ++j) {
+        const int k0 = key0 + (n - 1 - j) * BN, c0 = k0 + half * H;  // first keys of the tile and of the half
+        const int va = sp.lo - c0, vb = sp.hi - c0;
+        const bool edge = __any_sync(0xffffffffu, valid && (va > 0 || vb < H));
+        // The first tile that shows a row a key sets its reference.
+        const bool first = j == 0 || __any_sync(0xffffffffu, m == -INFINITY && sp.lo < k0 + BN && sp.hi > k0);
         if (!mbar_wait(&bars->sfull[t], (tc + j) & 1, abort)) goto done;
         if (idle) {
           mbar_arrive(&bars->pfull[t]);
@@ -233,9 +238,6 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         }
         __syncwarp();
         tc_fence_after();
-        const int k0 = key0 + (n - 1 - j) * BN, c0 = k0 + half * H;  // first keys of the tile and of the half
-        const int va = sp.lo - c0, vb = sp.hi - c0;
-        const bool edge = __any_sync(0xffffffffu, valid && (va > 0 || vb < H));
         auto load = [&](float* s, int base) { tmem_ld16(sbase + base, reinterpret_cast<uint32_t*>(s)); };
         auto hidden = [&](int c) -> bool { return c < va || c >= vb; };
         // cap tanh(x scale / cap) = cap (1 - 2 / (1 + e^2y)) in exp2 units; exact at
@@ -375,10 +377,10 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
           ts = f2lo(s2) + f2hi(s2);
           tr = pr[0] + pr[1];
         };
-        // The first tile that shows a row a key sets its reference; later tiles
-        // raise it only when needed.  (A row without one has P = 0, l = 0, O = 0.)
-        // Both warps of a pair hold the same references and spans, so they agree.
-        if (j == 0 || __any_sync(0xffffffffu, m == -INFINITY && sp.lo < k0 + BN && sp.hi > k0)) {
+        // Later tiles raise the reference only when needed.  (A row without one has
+        // P = 0, l = 0, O = 0.)  Both warps of a pair hold the same references and
+        // spans, so they agree.
+        if (first) {
           float mx;
           if (!row_max(&mx)) goto done;
           if (m == -INFINITY) m = mx;
@@ -557,12 +559,13 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
           if (!(ok = ready(iv)) || (more && !(ok = ready(ik)))) break;
           const bool tail = j == 0 && uhi - (key0 + (n - 1) * BN) < BN;  // to be cleared behind the span
           if (tail) mbar_arrive(&bars->tail_here);
-          if (!(ok = mbar_wait(&bars->pfull[t], (tc + j) & 1, abort))) break;
           if (tail && !(ok = mbar_wait(&bars->tail, zc++ & 1, abort))) break;
           if (j == 0 && uc > 0 && !(ok = mbar_wait(&bars->ofree[t], (uc - 1) & 1, abort))) break;
           // Turns: the tiles' steps alternate (side by side they would fall into
           // step and leave the tensor core idle during both softmaxes).
           if (T == 2 && tc + j + t > 0 && !(ok = mbar_wait(&bars->turn[t], (tc + j + t - 1) & 1, abort))) break;
+          // (P last: even a wait for what is long done takes about 100 cycles)
+          if (!(ok = mbar_wait(&bars->pfull[t], (tc + j) & 1, abort))) break;
           tc_fence_after();
           pv(iv, j == 0);
           if (more)
