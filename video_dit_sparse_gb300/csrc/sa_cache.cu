@@ -42,13 +42,6 @@ struct WCfg {
   static constexpr int kCols = 256;  // columns of a TMEM buffer
 };
 
-struct WBars {
-  uint64_t kfull[kMaxStages], kempty[kMaxStages], qfull[kMaxStages], qempty[kMaxStages];
-  uint64_t dfull[2], dempty[2], hfull[2], hempty[2], turn[2], drain[2];
-  uint32_t tmem_base;
-  int abort;
-};
-
 // What a launch fixes: the Q tile (qn queries x R heads = rows, NR columns),
 // the rings and the units.
 struct WPlan {
@@ -58,11 +51,23 @@ struct WPlan {
 constexpr int kUnitKeys = 256;
 
 struct WUnit {
+  int go;              // 0: no more units
   int b, hk, k0, len;  // len: keys of the batch entry
   int t0, t1;          // Q tiles with a row that sees one of the unit's keys
 };
+struct WBars {
+  uint64_t kfull[kMaxStages], kempty[kMaxStages], qfull[kMaxStages], qempty[kMaxStages];
+  uint64_t dfull[2], dempty[2], hfull[2], hempty[2], turn[2], drain[2];
+  uint64_t next, ring_full[2], ring_empty[2];
+  uint4 answer;  // of the request for the next unit
+  WUnit ring[2];
+  uint32_t tmem_base;
+  int abort;
+};
+
 __device__ __forceinline__ WUnit unit_at(const MaskedArgs& a, const WPlan& p, int u) {
   WUnit x;
+  x.go = 1;
   const int bh = u / p.kunits;
   x.k0 = (u - bh * p.kunits) * kUnitKeys;
   x.b = bh / a.Hkv;
@@ -109,8 +114,11 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
       mbar_init(&bars->hfull[b], 128);
       mbar_init(&bars->hempty[b], 128);
       mbar_init(&bars->turn[b], 1);
+      mbar_init(&bars->ring_full[b], 1);
+      mbar_init(&bars->ring_empty[b], WCfg::kEpiWarps + 2);
       mbar_init(&bars->drain[b], 1);
     }
+    mbar_init(&bars->next, 1);
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -148,29 +156,35 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
     uint32_t it = 0, hn = 0;  // Q tiles, and sums handed on so far
     // What a unit needs first is loaded while the unit before it is worked on.
     WUnit nu = {};
+    uint32_t un = 0;  // units read from the ring
     float nwas = 0.f, next = 0.f;  // its entry as it was; lse of the coming tile's column
     auto fetch = [&](const WUnit& x, int t) {
       next = qo < a.Nq - t * p.qn
                  ? __ldg(wa.lse + (int64_t(x.b) * a.Hq + int64_t(x.hk) * a.R) * a.Nq + int64_t(t) * p.qn + off)
                  : 0.f;
     };
-    auto look = [&](int u) {
-      nu = unit_at(a, p, u);
+    auto look = [&]() -> bool {
+      if (!mbar_wait(&bars->ring_full[un & 1], (un >> 1) & 1, abort)) return false;
+      nu = bars->ring[un & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->ring_empty[un & 1]);
+      ++un;
       nwas = 0.f;
+      if (!nu.go) return true;
       const int key = nu.k0 + d * 128 + tid;
       if (!half && key < a.Nk && wa.w_in && (key >= nu.len || wa.decay != 0.f))
         nwas = wa.w_in[(int64_t(nu.b) * a.Hkv + nu.hk) * a.Nk + key];
       if (nu.t0 < nu.t1) fetch(nu, nu.t0);
+      return true;
     };
-    if (static_cast<int>(blockIdx.x) < p.units) look(blockIdx.x);
-    for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+    if (!look()) goto done;
+    while (nu.go) {
       const WUnit x = nu;
       const float was = nwas;
       const int b = x.b, key = x.k0 + d * 128 + tid;
       const float* slopes = BIAS ? a.slopes + x.hk * a.R : nullptr;
       float total = 0.f;
-      const bool more = static_cast<int>(u + gridDim.x) < p.units;
-      if (x.t0 >= x.t1 && more) look(u + gridDim.x);
+      if (x.t0 >= x.t1 && !look()) goto done;
       for (int t = x.t0; t < x.t1; ++t, ++it) {
         // lse of this tile's columns, by all of the set; a row without a finite one
         // adds nothing.  (A warp that gives up arrives once, below `done`.)
@@ -190,8 +204,8 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
           edge = row_span(a.mask, b, qz).lo > kt || row_span(a.mask, b, qa).hi < min(kt + 128, a.Nk);
         if (t + 1 < x.t1)
           fetch(x, t + 1);
-        else if (more)
-          look(u + gridDim.x);
+        else if (!look())
+          goto done;
         if (!mbar_wait(&bars->dfull[d], it & 1, abort)) goto done;
         __syncwarp();
         tc_fence_after();
@@ -314,17 +328,21 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
       const uint32_t qstep = (p.NR * 128) >> 4;
       uint32_t it = 0, kn = d;  // Q tiles so far; this warp's key tile in the ring
       bool ok = true;
-      for (int u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
-        const WUnit x = unit_at(a, p, u);
+      for (uint32_t i = 0; ok; ++i) {
+        if (!mbar_wait(&bars->ring_full[i & 1], (i >> 1) & 1, abort)) break;
+        const WUnit x = bars->ring[i & 1];
+        mbar_arrive(&bars->ring_empty[i & 1]);
+        if (!x.go) break;
         if (x.t1 <= x.t0) continue;
         const uint32_t ks = kn % p.kst;
         if (!mbar_wait(&bars->kfull[ks], (kn / p.kst) & 1, abort)) break;
         const uint32_t kl = k_lo + ((ks * p.ktile) >> 4);
         for (int t = x.t0; t < x.t1; ++t, ++it) {
           const uint32_t qs = it % p.qst;
+          // (the buffer last: even a wait for what is long done takes 100 cycles)
           if (!mbar_wait(&bars->qfull[qs], (it / p.qst) & 1, abort) ||
-              !mbar_wait(&bars->dempty[d], (it & 1) ^ 1, abort) ||
-              (it + d > 0 && !mbar_wait(&bars->turn[d], (it + d - 1) & 1, abort))) {
+              (it + d > 0 && !mbar_wait(&bars->turn[d], (it + d - 1) & 1, abort)) ||
+              !mbar_wait(&bars->dempty[d], (it & 1) ^ 1, abort)) {
             ok = false;
             break;
           }
@@ -349,7 +367,7 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
       }
     }
   } else if (warp == WCfg::kTmaWarp && lane == 0) {
-    // ------------------------------------------------------------ loads (TMA)
+    // ------------------------------------------------------------ units and loads
     const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sK);
     uint32_t it = 0, un = 0;  // Q tiles and key tiles loaded
     bool ok = true;
@@ -364,9 +382,30 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
       ++it;
       return true;
     };
-    for (int u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
-      const WUnit x = unit_at(a, p, u);
-      if (x.t1 <= x.t0) continue;
+    // The block's own unit, then units of blocks that have not started.
+    int64_t u = blockIdx.x;
+    uint32_t i = 0;
+    for (; ok; ++i) {
+      WUnit x = {};
+      if (u >= 0) {
+        mbar_expect_tx(&bars->next, 16);
+        request_block(&bars->answer, &bars->next);
+        x = unit_at(a, p, static_cast<int>(u));
+      }
+      if (i >= 2 && !mbar_wait(&bars->ring_empty[i & 1], ((i >> 1) - 1) & 1, abort)) break;
+      bars->ring[i & 1] = x;
+      mbar_arrive(&bars->ring_full[i & 1]);
+      if (u < 0) break;
+      auto following = [&]() -> bool {
+        if (!mbar_wait(&bars->next, i & 1, abort)) return false;
+        u = answered_block(&bars->answer);
+        fence_proxy_async_smem();  // read before the next answer is written
+        return true;
+      };
+      if (x.t1 <= x.t0) {
+        ok = following();
+        continue;
+      }
       // the first Q tile ahead of K, whose place may still be in use
       if (!(ok = load_q(x, x.t0))) break;
       for (int d = 0; d < 2 && ok; ++d) {
@@ -380,17 +419,23 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
         ++un;
       }
       for (int t = x.t0 + 1; t < x.t1 && ok; ++t) ok = load_q(x, t);
+      if (ok) ok = following();
     }
     // After an abort: the copies in flight land before the block ends.
     if (*abort) {
-      for (uint32_t i = it > uint32_t(p.qst) ? it - p.qst : 0; i < it; ++i) {
+      for (uint32_t f = it > uint32_t(p.qst) ? it - p.qst : 0; f < it; ++f) {
         const long long c0 = clock64();
-        while (!mbar_test(&bars->qfull[i % p.qst], (i / p.qst) & 1) && clock64() - c0 < kWaitLimitCycles) {
+        while (!mbar_test(&bars->qfull[f % p.qst], (f / p.qst) & 1) && clock64() - c0 < kWaitLimitCycles) {
         }
       }
-      for (uint32_t i = un > uint32_t(p.kst) ? un - p.kst : 0; i < un; ++i) {
+      for (uint32_t f = un > uint32_t(p.kst) ? un - p.kst : 0; f < un; ++f) {
         const long long c0 = clock64();
-        while (!mbar_test(&bars->kfull[i % p.kst], (i / p.kst) & 1) && clock64() - c0 < kWaitLimitCycles) {
+        while (!mbar_test(&bars->kfull[f % p.kst], (f / p.kst) & 1) && clock64() - c0 < kWaitLimitCycles) {
+        }
+      }
+      if (u >= 0) {
+        const long long c0 = clock64();
+        while (!mbar_test(&bars->next, i & 1) && clock64() - c0 < kWaitLimitCycles) {
         }
       }
     }
@@ -425,8 +470,7 @@ static cudaError_t launch_w(const WeightArgs& a, const WPlan& p, const CUtensorM
   if (regs_ok.load() != 1) return cudaErrorLaunchOutOfResources;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int grid = p.units < num_sms ? p.units : num_sms;
-  kern<<<grid, WCfg::kThreads, smem, st>>>(a, p, tq, tk);
+  kern<<<p.units, WCfg::kThreads, smem, st>>>(a, p, tq, tk);
   return cudaGetLastError();
 }
 
