@@ -179,6 +179,13 @@ __device__ __forceinline__ void bulk_wait_read() {
 // Waits until this thread's bulk stores are complete in global memory.
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// ------------------------------------------------- programmatic launch order
+// In a kernel launched by launch_early: waits until the kernel ahead of it on
+// the stream has finished and its writes are visible.
+__device__ __forceinline__ void wait_for_earlier_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---------------------------------------------------- cluster launch control
 // Asks for a block of the grid that has not started yet, to be run by this one
 // instead.  The 16-byte answer lands at `dst` and completes 16 bytes of `bar`'s

@@ -239,6 +239,24 @@ struct NvtxRange {
   NvtxRange& operator=(const NvtxRange&) = delete;
 };
 
+// Launches a kernel that may start while the one ahead of it on the stream still
+// runs; the kernel calls wait_for_earlier_kernel() before it touches memory.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+                         const A&... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 cudaError_t launch_validate(const int64_t* row_ptr, const int32_t* col_idx, int64_t rows,
                             int64_t nnz, int32_t Nk, int32_t* status, cudaStream_t stream);
 

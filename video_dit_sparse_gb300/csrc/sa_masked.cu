@@ -72,15 +72,16 @@ struct MCfg {
   static constexpr int kWarpBytes = 2048;  // a softmax warp's own: exchange slots, output staging
   static constexpr int kXch = kSoftWarps * kWarpBytes;
   static constexpr int kSmemBytes = 1024 + kQBytes + kStages * kTile + kXch + 1024;
-  static constexpr int kOCol = T * 128;
-  static constexpr int kTmemCols = T == 2 ? 512 : 256;
+  // one tile: two S buffers, so that S(j+1) is computed beside softmax(j)
+  static constexpr int kOCol = 256;
+  static constexpr int kTmemCols = 512;
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
 template <int T, int STAGES>
 struct MBars {
   uint64_t full[STAGES], empty[STAGES];
-  uint64_t sfull[T], pfull[T], ofull[T], ofree[T];
+  uint64_t sfull[2], pfull[2], pvdone, ofull[T], ofree[T];
   uint64_t qfull, qempty, next, tail, tail_here, turn[T], ring_full[2], ring_empty[2], drain[T];
   uint4 answer;   // of the request for the next unit
   struct Unit {
@@ -137,15 +138,16 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
       mbar_init(&bars->empty[s], T);
     }
     for (int i = 0; i < T; ++i) {
-      mbar_init(&bars->sfull[i], 1);
-      mbar_init(&bars->pfull[i], 256);
       mbar_init(&bars->ofull[i], 1);
       mbar_init(&bars->ofree[i], 256);
     }
     for (int i = 0; i < T * 4; ++i) {
       bars->flag[i][0] = bars->flag[i][1] = 0;
     }
+    mbar_init(&bars->pvdone, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->sfull[i], 1);  // S and P of each S buffer
+      mbar_init(&bars->pfull[i], 256);
       mbar_init(&bars->ring_full[i], 1);
       mbar_init(&bars->ring_empty[i], C::kSoftWarps + T + 1);
     }
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
     const int rq = trow / a.R, rh = trow - rq * a.R;  // its query and head in the tile
     const bool in_tile = trow < a.qn * a.R;
     const float sl = a.scale_log2;
-    const uint32_t sbase = tmem + lane_base + t * 128 + half * H;
+    uint32_t sbase = tmem + lane_base + t * 128 + half * H;
     const uint32_t obase = tmem + lane_base + C::kOCol + t * D + half * (D / 2);
     volatile int* flag = bars->flag[t * 4 + quarter];
     uint32_t xn = 0;           // pair exchanges so far
@@ -231,9 +233,12 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         const bool edge = __any_sync(0xffffffffu, valid && (va > 0 || vb < H));
         // The first tile that shows a row a key sets its reference.
         const bool first = j == 0 || __any_sync(0xffffffffu, m == -INFINITY && sp.lo < k0 + BN && sp.hi > k0);
-        if (!mbar_wait(&bars->sfull[t], (tc + j) & 1, abort)) goto done;
+        // S buffer and its phase: one buffer a tile, or one tile's two in turn
+        const uint32_t sb = T == 2 ? t : (tc + j) & 1;
+        if (T == 1) sbase = tmem + lane_base + sb * 128 + half * H;
+        if (!mbar_wait(&bars->sfull[sb], (T == 2 ? tc + j : (tc + j) >> 1) & 1, abort)) goto done;
         if (idle) {
-          mbar_arrive(&bars->pfull[t]);
+          mbar_arrive(&bars->pfull[sb]);
           continue;
         }
         __syncwarp();
@@ -400,7 +405,11 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
           m = mn;
           l *= alpha;
           lr *= alpha;
-          // O holds PV of every earlier tile: its commit came with this S.
+          // O holds PV of every earlier tile: with two Q tiles its commit came with
+          // this S.  (j > 0, and no later PV has been issued.)
+          if (T == 1 && !mbar_wait(&bars->pvdone, (tc + j - 1) & 1, abort)) goto done;
+          __syncwarp();
+          tc_fence_after();
 #pragma unroll
           for (int c = 0; c < D / 64; ++c) {
             uint32_t r[32];
@@ -417,7 +426,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         tmem_st32(sbase, p);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&bars->pfull[t]);
+        mbar_arrive(&bars->pfull[sb]);
       }
       tc += n;
       if (n > 0) {
@@ -514,12 +523,14 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
     const uint32_t q_lo = static_cast<uint32_t>(dq), q_hi = static_cast<uint32_t>(dq >> 32);
     const uint32_t k_lo = static_cast<uint32_t>(dk), k_hi = static_cast<uint32_t>(dk >> 32);
     const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
-    const uint32_t s_tmem = tmem + t * 128, o_tmem = tmem + C::kOCol + t * D;
+    const uint32_t o_tmem = tmem + C::kOCol + t * D;
     auto ready = [&](uint32_t i) -> bool { return mbar_wait(&bars->full[i % S], (i / S) & 1, abort); };
     auto pass = [&]() {  // the other tile's turn
       if (T == 2) mbar_arrive(&bars->turn[t ^ 1]);
     };
-    auto qk = [&](uint32_t i, bool turn) {
+    auto sbuf = [&](uint32_t step) -> uint32_t { return T == 2 ? t : step & 1; };
+    auto qk = [&](uint32_t i, uint32_t step, bool turn) {
+      const uint32_t s_tmem = tmem + sbuf(step) * 128;
       const uint32_t kl = k_lo + (((i % S) * C::kTile) >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
@@ -527,9 +538,10 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         mma_ss_w(s_tmem, q_lo + off, q_hi, kl + off, k_hi, kIdescS, kk > 0 ? 1u : 0u);
         if (kk == D / 16 - 3 && turn) pass();  // (two MMAs cover the hand-over)
       }
-      mma_commit(&bars->sfull[t]);
+      mma_commit(&bars->sfull[sbuf(step)]);
     };
-    auto pv = [&](uint32_t i, bool first) {
+    auto pv = [&](uint32_t i, uint32_t step, bool first) {
+      const uint32_t s_tmem = tmem + sbuf(step) * 128;
       const uint32_t vl = v_lo + (((i % S) * C::kTile) >> 4);
 #pragma unroll
       for (int kk = 0; kk < BN / 16; ++kk)
@@ -550,7 +562,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         // Ring entries: K(j) is number 2 (tc + j), V(j) the one behind it.
         if (!(ok = mbar_wait(&bars->qfull, uc & 1, abort)) || !(ok = ready(2 * tc))) break;
         tc_fence_after();
-        qk(2 * tc, false);
+        qk(2 * tc, tc, false);
         mma_commit(&bars->empty[(2 * tc) % S]);
         if (n == 1) mma_commit(&bars->qempty);
         for (int j = 0; j < n; ++j) {
@@ -564,18 +576,26 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
           // Turns: the tiles' steps alternate (side by side they would fall into
           // step and leave the tensor core idle during both softmaxes).
           if (T == 2 && tc + j + t > 0 && !(ok = mbar_wait(&bars->turn[t], (tc + j + t - 1) & 1, abort))) break;
+          // One tile: the other S buffer is free once PV(j-1) has been issued.
+          if (T == 1 && more) {
+            tc_fence_after();
+            qk(ik, tc + j + 1, false);
+            mma_commit(&bars->empty[ik % S]);
+            if (j + 2 == n) mma_commit(&bars->qempty);
+          }
           // (P last: even a wait for what is long done takes about 100 cycles)
-          if (!(ok = mbar_wait(&bars->pfull[t], (tc + j) & 1, abort))) break;
+          if (!(ok = mbar_wait(&bars->pfull[sbuf(tc + j)], (T == 2 ? tc + j : (tc + j) >> 1) & 1, abort))) break;
           tc_fence_after();
-          pv(iv, j == 0);
-          if (more)
-            qk(ik, true);
+          pv(iv, tc + j, j == 0);
+          if (T == 1) mma_commit(&bars->pvdone);
+          if (T == 2 && more)
+            qk(ik, tc + j + 1, true);
           else
             pass();
           if (!more) mma_commit(&bars->ofull[t]);
           mma_commit(&bars->empty[iv % S]);
-          if (more) mma_commit(&bars->empty[ik % S]);
-          if (j + 2 == n) mma_commit(&bars->qempty);
+          if (T == 2 && more) mma_commit(&bars->empty[ik % S]);
+          if (T == 2 && j + 2 == n) mma_commit(&bars->qempty);
         }
         tc += n;
         ++uc;
@@ -710,6 +730,7 @@ done:
 // o = sum_s e^(lse_s - lse) o_s.
 template <int D>
 __global__ void __launch_bounds__(256) sa_masked_join_kernel(const __grid_constant__ MaskedArgs a) {
+  wait_for_earlier_kernel();  // (launched while the partial results are still being made)
   const int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const int unit_rows = a.unit_rows;
@@ -834,11 +855,7 @@ cudaError_t launch_masked(const MaskedArgs& a, cudaStream_t st) {
                              : (two ? launch_t<64, 2>(a, tq, tk, tv, st) : launch_t<64, 1>(a, tq, tk, tv, st));
   if (e != cudaSuccess || a.split_units == 0) return e;
   const unsigned blocks = static_cast<unsigned>((a.split_units * a.unit_rows + 7) / 8);
-  if (a.d == 128)
-    sa_masked_join_kernel<128><<<blocks, 256, 0, st>>>(a);
-  else
-    sa_masked_join_kernel<64><<<blocks, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(a.d == 128 ? sa_masked_join_kernel<128> : sa_masked_join_kernel<64>, dim3(blocks), 256, 0, st, a);
 }
 
 }  // namespace sa
