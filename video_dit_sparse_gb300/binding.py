@@ -8,7 +8,6 @@ a missing library raises at import.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 import struct
@@ -479,16 +478,9 @@ def _flat(t, dtype, name, dev, shape=None) -> int:
     return t.data_ptr()
 
 
-def _on_device(f):
-    """Runs f with the device of its first tensor current."""
-    @functools.wraps(f)
-    def g(first, *args, **kw):
-        dev = first.get_device()
-        if dev >= 0 and dev != torch.cuda.current_device():
-            with torch.cuda.device(dev):
-                return f(first, *args, **kw)
-        return f(first, *args, **kw)
-    return g
+def _elsewhere(dev: int) -> bool:
+    """Whether `dev` is another CUDA device than the current one."""
+    return dev >= 0 and dev != torch._C._cuda_getDevice()
 
 
 def _raw_stream(stream, dev: int, *made) -> int:
@@ -502,7 +494,6 @@ def _raw_stream(stream, dev: int, *made) -> int:
     return stream.cuda_stream
 
 
-@_on_device
 def sparse_attn_rope(q: torch.Tensor, k: torch.Tensor | None = None, *, axes=(44, 42, 42),
                      theta: float = 10000.0, inv_freq=None, pairing: str = "interleaved",
                      grid=None, voxel=None, offset=(0, 0, 0), positions: torch.Tensor | None = None,
@@ -515,6 +506,11 @@ def sparse_attn_rope(q: torch.Tensor, k: torch.Tensor | None = None, *, axes=(44
     `offset`.  inv_freq: r/2 frequencies (radians per position) instead of theta's.  inverse rotates
     back, which is also the gradient.  out: the output (or a pair of them); it may be the input."""
     dtype, dev = q.dtype, q.get_device()
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return sparse_attn_rope(q, k, axes=axes, theta=theta, inv_freq=inv_freq, pairing=pairing,
+                                    grid=grid, voxel=voxel, offset=offset, positions=positions,
+                                    inverse=inverse, out=out, stream=stream)
     if dtype not in _OUT:
         raise ValueError("q must be bfloat16 or float32")
     qs = _view(q, dtype, "q", dev)
@@ -601,7 +597,6 @@ def _mask_fields(q, k, dev, slopes, docs_q, docs_k, prefix, lengths):
     return n, slopes, dq, dk, px, _flat(lengths, torch.int32, "lengths", dev, (B,)), made
 
 
-@_on_device
 def sparse_attn_forward_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
                                scale: float | None = None, cap: float = 0.0,
                                slopes: torch.Tensor | None = None, causal: int = 0,
@@ -622,6 +617,12 @@ def sparse_attn_forward_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     frame when `causal` (tokens per frame, 1: per token), and the document's first `prefix` keys.  A
     document's rows are its last positions, so one new token over a cache is Nq = 1 with lengths."""
     dev = q.get_device()
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return sparse_attn_forward_masked(q, k, v, scale=scale, cap=cap, slopes=slopes, causal=causal,
+                                              docs_q=docs_q, docs_k=docs_k, prefix=prefix, lengths=lengths,
+                                              out=out, out_dtype=out_dtype, lse=lse, workspace=workspace,
+                                              status=status, stream=stream)
     qs, ks = _view(q, torch.bfloat16, "q", dev), _view(k, torch.bfloat16, "k", dev)
     vs = _view(v, torch.bfloat16, "v", dev)
     if v.shape != k.shape:
@@ -629,13 +630,13 @@ def sparse_attn_forward_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     n, sl, dq, dk, px, lens, made = _mask_fields(q, k, dev, slopes, docs_q, docs_k, prefix, lengths)
     B, H, Nq, d = shape = q.shape
     if out is None:
-        out = q.new_empty(shape, dtype=out_dtype)
+        out = torch.empty_like(q) if out_dtype is q.dtype else torch.empty_like(q, dtype=out_dtype)
     elif out.shape != shape:
         raise ValueError("out must have q's shape")
     if out.dtype not in _OUT:
         raise ValueError("out must be bfloat16 or float32")
     if lse is True:
-        lse = q.new_empty(shape[:3], dtype=torch.float32)
+        lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
     elif lse is False:
         lse = None
     p = _MASKED.pack(B, H, k.shape[1], Nq, k.shape[2], d, 1.0 / math.sqrt(d) if scale is None else scale,
@@ -643,7 +644,7 @@ def sparse_attn_forward_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
                      dq, dk, px, lens)
     need = _c_masked_ws(p)
     if need and workspace is None:
-        workspace = q.new_empty(need, dtype=torch.uint8)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     st = _c_masked(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                    _flat(lse, torch.float32, "lse", dev, shape[:3]), _flat(status, torch.int32, "status", dev),
                    _flat(workspace, torch.uint8, "workspace", dev),
@@ -654,7 +655,6 @@ def sparse_attn_forward_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     return out, lse
 
 
-@_on_device
 def sparse_attn_cache_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor,
                               weights: torch.Tensor | None = None, *, decay: float = 1.0,
                               scale: float | None = None, cap: float = 0.0,
@@ -670,6 +670,12 @@ def sparse_attn_cache_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tenso
     that wrote lse.  weights None starts from zero; out=weights accumulates in place; entries past
     lengths[b] stay as they were (zero when there were none)."""
     dev = q.get_device()
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return sparse_attn_cache_weights(q, k, lse, weights, decay=decay, scale=scale, cap=cap,
+                                             slopes=slopes, causal=causal, docs_q=docs_q, docs_k=docs_k,
+                                             prefix=prefix, lengths=lengths, out=out, status=status,
+                                             stream=stream)
     qs, ks = _view(q, torch.bfloat16, "q", dev), _view(k, torch.bfloat16, "k", dev)
     n, sl, dq, dk, px, lens, made = _mask_fields(q, k, dev, slopes, docs_q, docs_k, prefix, lengths)
     B, H, Nq, d = q.shape
@@ -688,7 +694,6 @@ def sparse_attn_cache_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tenso
     return out
 
 
-@_on_device
 def sparse_attn_cache_evict(weights: torch.Tensor, k: torch.Tensor | None, v: torch.Tensor | None,
                             budget: int, *, sink: int = 0, recent: int = 0,
                             lengths: torch.Tensor | None = None, out=None,
@@ -701,6 +706,10 @@ def sparse_attn_cache_evict(weights: torch.Tensor, k: torch.Tensor | None, v: to
     order; behind a shorter one kept is -1 and the rows of `out` = (k, v, weights) are left as they
     were (zero when out is not given)."""
     dev = weights.get_device()
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return sparse_attn_cache_evict(weights, k, v, budget, sink=sink, recent=recent, lengths=lengths,
+                                           out=out, kept=kept, stream=stream)
     if weights.dim() != 3 or dev < 0:
         raise ValueError("weights must be a CUDA tensor [B, Hk, Nk]")
     B, H, N = weights.shape
@@ -726,7 +735,7 @@ def sparse_attn_cache_evict(weights: torch.Tensor, k: torch.Tensor | None, v: to
     else:
         ko, vo, wo = out
     if kept is None:
-        kept = weights.new_empty((B, H, budget), dtype=torch.int32)
+        kept = torch.empty((B, H, budget), dtype=torch.int32, device=weights.device)
     kp = vp = kop = vop = 0
     if k is not None:
         if ko.shape != (B, H, budget, d) or vo.shape != ko.shape:

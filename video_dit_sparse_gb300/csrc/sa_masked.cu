@@ -727,39 +727,46 @@ done:
 }
 
 // One warp per row of a split unit: lse = ln sum_s e^(lse_s),
-// o = sum_s e^(lse_s - lse) o_s.
+// o = sum_s e^(lse_s - lse) o_s.  Bound by its launch and two rounds of loads.
 template <int D>
-__global__ void __launch_bounds__(256) sa_masked_join_kernel(const __grid_constant__ MaskedArgs a) {
+__global__ void __launch_bounds__(128) sa_masked_join_kernel(const __grid_constant__ MaskedArgs a) {
   wait_for_earlier_kernel();  // (launched while the partial results are still being made)
-  const int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const uint32_t i = blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const int unit_rows = a.unit_rows;
-  const int64_t su = i / unit_rows;  // split unit
-  const int r = static_cast<int>(i % unit_rows);
+  const uint32_t tile_rows = a.qn * a.R, unit_rows = a.unit_rows / 128 * tile_rows;  // that exist
+  const uint32_t su = i / unit_rows, r = i - su * unit_rows, t = r / tile_rows, tr = r - t * tile_rows;
   if (su >= a.split_units) return;
   const Place at = place_of(a, static_cast<int>(a.full_units + su));
-  const int64_t bh = at.bh;
-  const int tr = r % 128;  // row of its Q tile
-  const int64_t q = int64_t(at.rb) * (unit_rows / 128 * a.qn) + r / 128 * a.qn + tr / a.R;
-  if (tr >= a.qn * a.R || q >= a.Nq) return;
-  const float* pl = a.part_lse + su * a.splits * unit_rows + r;
+  const int q = at.rb * (a.unit_rows / 128 * a.qn) + t * a.qn + tr / a.R;
+  if (q >= a.Nq) return;
+  const int64_t row0 = int64_t(su) * a.splits * a.unit_rows + t * 128 + tr;
   float mx = -INFINITY;
-  for (int s = lane; s < a.splits; s += 32) mx = fmaxf(mx, __ldg(pl + s * unit_rows));
+  for (int s = lane; s < a.splits; s += 32) mx = fmaxf(mx, __ldg(a.part_lse + row0 + s * a.unit_rows));
 #pragma unroll
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   constexpr int V = D / 32;
   float acc[V] = {}, sum = 0.f;
-  if (mx != -INFINITY)
+  if (mx != -INFINITY) {
+#pragma unroll 8
     for (int s = 0; s < a.splits; ++s) {
-      const float w = __expf(__ldg(pl + s * unit_rows) - mx);
+      const int64_t row = row0 + s * a.unit_rows;
+      const float w = __expf(__ldg(a.part_lse + row) - mx);
+      float f[V];
+      if (V == 4) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(a.part_o + row * D) + lane);
+        f[0] = x.x, f[1] = x.y, f[V - 2] = x.z, f[V - 1] = x.w;
+      } else {
+        const float2 x = __ldg(reinterpret_cast<const float2*>(a.part_o + row * D) + lane);
+        f[0] = x.x, f[1] = x.y;
+      }
       sum += w;
-      const float* src = a.part_o + ((su * a.splits + s) * unit_rows + r) * D + lane * V;
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] += w * src[e];
+      for (int e = 0; e < V; ++e) acc[e] += w * f[e];
     }
+  }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t h = (bh % a.Hkv) * a.R + tr % a.R, b = bh / a.Hkv;
-  const int64_t oo = b * a.os.b + h * a.os.h + q * a.os.n + lane * V;
+  const int h = (at.bh % a.Hkv) * a.R + tr % a.R, b = at.bh / a.Hkv;
+  const int64_t oo = int64_t(b) * a.os.b + int64_t(h) * a.os.h + int64_t(q) * a.os.n + lane * V;
 #pragma unroll
   for (int e = 0; e < V; e += 2) {
     if (a.out_fp32)
@@ -767,7 +774,7 @@ __global__ void __launch_bounds__(256) sa_masked_join_kernel(const __grid_consta
     else
       *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + oo + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
   }
-  if (lane == 0 && a.lse) a.lse[(b * a.Hq + h) * a.Nq + q] = sum == 0.f ? -INFINITY : mx + logf(sum);
+  if (lane == 0 && a.lse) a.lse[(int64_t(b) * a.Hq + h) * a.Nq + q] = sum == 0.f ? -INFINITY : mx + logf(sum);
 }
 
 // Units that fill whole waves of SMs run whole; the rest (all, if they are
@@ -854,8 +861,9 @@ cudaError_t launch_masked(const MaskedArgs& a, cudaStream_t st) {
   cudaError_t e = a.d == 128 ? (two ? launch_t<128, 2>(a, tq, tk, tv, st) : launch_t<128, 1>(a, tq, tk, tv, st))
                              : (two ? launch_t<64, 2>(a, tq, tk, tv, st) : launch_t<64, 1>(a, tq, tk, tv, st));
   if (e != cudaSuccess || a.split_units == 0) return e;
-  const unsigned blocks = static_cast<unsigned>((a.split_units * a.unit_rows + 7) / 8);
-  return launch_early(a.d == 128 ? sa_masked_join_kernel<128> : sa_masked_join_kernel<64>, dim3(blocks), 256, 0, st, a);
+  const int64_t rows = a.split_units * (a.unit_rows / 128) * a.qn * a.R;
+  return launch_early(a.d == 128 ? sa_masked_join_kernel<128> : sa_masked_join_kernel<64>,
+                      dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, st, a);
 }
 
 }  // namespace sa
