@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         // the largest product has the largest score).
         auto row_max = [&](float* res) -> bool {
           float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
           for (int base = 0; base < H; base += W) {
             float s[W];
             load(s, base);
