@@ -54,6 +54,8 @@ struct WUnit {
   int go;              // 0: no more units
   int b, hk, k0, len;  // len: keys of the batch entry
   int t0, t1;          // Q tiles with a row that sees one of the unit's keys
+  int rot;             // taken from t0 + rot on, round
+  __device__ __forceinline__ int tile(int s) const { return t0 + rot + s < t1 ? t0 + rot + s : rot + s + t0 - (t1 - t0); }
 };
 struct WBars {
   uint64_t kfull[kMaxStages], kempty[kMaxStages], qfull[kMaxStages], qempty[kMaxStages];
@@ -81,6 +83,9 @@ __device__ __forceinline__ WUnit unit_at(const MaskedArgs& a, const WPlan& p, in
     if (m.nd)
       while (x.t1 > x.t0 && row_span(m, x.b, (x.t1 - 1) * p.qn).lo >= x.k0 + kUnitKeys) --x.t1;
   }
+  // Blocks that work on the same head's keys start at different Q tiles (in step
+  // they would all ask L2 for the same lines).
+  x.rot = (u & 15) * (x.t1 - x.t0) / 16;
   return x;
 }
 
@@ -174,7 +179,7 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
       const int key = nu.k0 + d * 128 + tid;
       if (!half && key < a.Nk && wa.w_in && (key >= nu.len || wa.decay != 0.f))
         nwas = wa.w_in[(int64_t(nu.b) * a.Hkv + nu.hk) * a.Nk + key];
-      if (nu.t0 < nu.t1) fetch(nu, nu.t0);
+      if (nu.t0 < nu.t1) fetch(nu, nu.tile(0));
       return true;
     };
     if (!look()) goto done;
@@ -185,7 +190,8 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
       const float* slopes = BIAS ? a.slopes + x.hk * a.R : nullptr;
       float total = 0.f;
       if (x.t0 >= x.t1 && !look()) goto done;
-      for (int t = x.t0; t < x.t1; ++t, ++it) {
+      for (int s = 0; s < x.t1 - x.t0; ++s, ++it) {
+        const int t = x.tile(s);
         // lse of this tile's columns, by all of the set; a row without a finite one
         // adds nothing.  (A warp that gives up arrives once, below `done`.)
         float* wL = sL + ((it & 1) * 4 + set) * 128;
@@ -202,8 +208,8 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
         bool edge = false;
         if (masks)
           edge = row_span(a.mask, b, qz).lo > kt || row_span(a.mask, b, qa).hi < min(kt + 128, a.Nk);
-        if (t + 1 < x.t1)
-          fetch(x, t + 1);
+        if (s + 1 < x.t1 - x.t0)
+          fetch(x, x.tile(s + 1));
         else if (!look())
           goto done;
         if (!mbar_wait(&bars->dfull[d], it & 1, abort)) goto done;
@@ -407,7 +413,7 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
         continue;
       }
       // the first Q tile ahead of K, whose place may still be in use
-      if (!(ok = load_q(x, x.t0))) break;
+      if (!(ok = load_q(x, x.tile(0)))) break;
       for (int d = 0; d < 2 && ok; ++d) {
         const uint32_t ks = un % p.kst;
         if (!(ok = mbar_wait(&bars->kempty[ks], ((un / p.kst) & 1) ^ 1, abort))) break;
@@ -418,7 +424,7 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
                       &bars->kfull[ks]);
         ++un;
       }
-      for (int t = x.t0 + 1; t < x.t1 && ok; ++t) ok = load_q(x, t);
+      for (int s = 1; s < x.t1 - x.t0 && ok; ++s) ok = load_q(x, x.tile(s));
       if (ok) ok = following();
     }
     // After an abort: the copies in flight land before the block ends.
