@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
     const bool has = tid < H && cr < p.rows;
     const int qo = has ? cr / a.R : INT_MAX / 2, off = has ? (cr % a.R) * a.Nq + qo : 0;
     const float sl = a.scale_log2;
-    const bool masks = a.mask.causal || a.mask.nd;  // (a length alone only decides which keys are written)
+    const bool docs = a.mask.nd > 0;  // (a length alone only decides which keys are written)
     uint32_t it = 0, hn = 0;  // Q tiles, and sums handed on so far
     // What a unit needs first is loaded while the unit before it is worked on.
     WUnit nu = {};
@@ -189,6 +189,9 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
       const int b = x.b, key = x.k0 + d * 128 + tid;
       const float* slopes = BIAS ? a.slopes + x.hk * a.R : nullptr;
       float total = 0.f;
+      // Without documents a key is seen from one query on.
+      int from = INT_MIN / 2;
+      if (a.mask.causal && !docs) from = key / a.mask.causal * a.mask.causal - (x.len - a.Nq);
       if (x.t0 >= x.t1 && !look()) goto done;
       for (int s = 0; s < x.t1 - x.t0; ++s, ++it) {
         const int t = x.tile(s);
@@ -206,8 +209,10 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
         const bool dead = (dead4.x | dead4.y | dead4.z | dead4.w) != 0;
         const int qa = t * p.qn, qz = min(qa + p.qn, a.Nq) - 1, kt = x.k0 + d * 128;
         bool edge = false;
-        if (masks)
+        if (docs)
           edge = row_span(a.mask, b, qz).lo > kt || row_span(a.mask, b, qa).hi < min(kt + 128, a.Nk);
+        const int first = from > qa ? (min(from - qa, p.qn) * a.R) - col0 : 0;  // the half's first column to count
+        const bool cut = __any_sync(0xffffffffu, first > 0);
         if (s + 1 < x.t1 - x.t0)
           fetch(x, x.tile(s + 1));
         else if (!look())
@@ -227,13 +232,31 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < count; e += 4) {
             const ulonglong2 L = *reinterpret_cast<const ulonglong2*>(wL + c + e);
+            uint64_t y0, y1;
             if (CAP) {
-              acc[0] = add2(acc[0], f2(fast_exp2(exponent(x[e], f2lo(L.x))), fast_exp2(exponent(x[e + 1], f2hi(L.x)))));
-              acc[1] = add2(acc[1], f2(fast_exp2(exponent(x[e + 2], f2lo(L.y))), fast_exp2(exponent(x[e + 3], f2hi(L.y)))));
+              y0 = f2(exponent(x[e], f2lo(L.x)), exponent(x[e + 1], f2hi(L.x)));
+              y1 = f2(exponent(x[e + 2], f2lo(L.y)), exponent(x[e + 3], f2hi(L.y)));
             } else {
-              const uint64_t y0 = fma2(f2(x[e], x[e + 1]), sl2, L.x), y1 = fma2(f2(x[e + 2], x[e + 3]), sl2, L.y);
-              acc[0] = add2(acc[0], f2(fast_exp2(f2lo(y0)), fast_exp2(f2hi(y0))));
-              acc[1] = add2(acc[1], f2(fast_exp2(f2lo(y1)), fast_exp2(f2hi(y1))));
+              y0 = fma2(f2(x[e], x[e + 1]), sl2, L.x);
+              y1 = fma2(f2(x[e + 2], x[e + 3]), sl2, L.y);
+            }
+            acc[0] = add2(acc[0], f2(fast_exp2(f2lo(y0)), fast_exp2(f2hi(y0))));
+            acc[1] = add2(acc[1], f2(fast_exp2(f2lo(y1)), fast_exp2(f2hi(y1))));
+          }
+        };
+        // Columns before each key's first one are left out.
+        auto after_first = [&]() {
+          for (int c = 0; c < H; c += 16) {
+            if (!__any_sync(0xffffffffu, first < c + 16)) continue;
+            float x[16];
+            tmem_ld16(sbase + c, reinterpret_cast<uint32_t*>(x));
+            tmem_ld_wait();
+            const int f = first - c;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float2 L = *reinterpret_cast<const float2*>(wL + c + e);
+              const float y0 = exponent(x[e], L.x), y1 = exponent(x[e + 1], L.y);
+              acc[0] = add2(acc[0], f2(fast_exp2(e < f ? -INFINITY : y0), fast_exp2(e + 1 < f ? -INFINITY : y1)));
             }
           }
         };
@@ -295,6 +318,8 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
         };
         if (BIAS || edge || dead)
           careful();
+        else if (cut)
+          after_first();
         else
           plain();
         tc_fence_before();
