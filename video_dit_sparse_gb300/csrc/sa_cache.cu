@@ -20,6 +20,8 @@
 // the columns.  With many rows the bound is the tensor core (one exponential a
 // pair is 0.8 of its time on the MUFU); with one token per sequence it is the
 // read of K.
+#include <cooperative_groups.h>
+
 #include <atomic>
 #include <climits>
 
@@ -546,24 +548,43 @@ __device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0u : o
 
 }  // namespace
 
-__global__ void __launch_bounds__(kSelThreads) sa_evict_select_kernel(const EvictArgs a) {
+// C blocks (a cluster) per row, each with a run of the row's entries in its
+// shared memory: 24 us for 12 rows of 35200 entries with one block a row.  The
+// blocks add up their histograms through distributed shared memory, so that all
+// of them find the same digit.
+template <int C>
+__global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kSelThreads) sa_evict_select_kernel(const EvictArgs a) {
   extern __shared__ uint32_t s_keys[];
-  __shared__ uint32_t hist[kBins];
-  __shared__ uint32_t wsum[32], weq[32];
+  __shared__ __align__(8) uint32_t hist[kBins];
+  __shared__ uint32_t wsum[32], weq[32], s_total[2];
   __shared__ uint32_t s_digit, s_left;
-  const int64_t row = blockIdx.x;
+  namespace cg = cooperative_groups;
+  const cg::cluster_group cluster = cg::this_cluster();
+  auto sync_all = [&]() {
+    if (C == 1)
+      __syncthreads();
+    else
+      cluster.sync();
+  };
+  const int rank = C == 1 ? 0 : static_cast<int>(cluster.block_rank());
+  const int64_t row = blockIdx.x / C;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int first = rank * kSelThreads + tid;  // among the row's threads
   int32_t* kept = a.kept + row * a.budget;
   const int n = a.len ? min(max(__ldg(a.len + row / a.Hkv), 0), a.Nk) : a.Nk;
+  // (n and what depends on it is the same in every block of the cluster)
   if (n <= a.budget) {
-    for (int i = tid; i < a.budget; i += kSelThreads) kept[i] = i < n ? i : -1;
+    for (int i = first; i < a.budget; i += C * kSelThreads) kept[i] = i < n ? i : -1;
     return;
   }
-  const int lo = a.sink, M = n - a.recent - a.sink;
-  const uint32_t want = a.budget - a.sink - a.recent;  // of the M in between: 0 <= want < M
-  for (int i = tid; i < a.sink; i += kSelThreads) kept[i] = i;
-  for (int i = tid; i < a.recent; i += kSelThreads) kept[a.budget - a.recent + i] = n - a.recent + i;
+  const int middle = n - a.recent - a.sink;
+  const uint32_t want = a.budget - a.sink - a.recent;  // of the ones in between: 0 <= want < middle
+  for (int i = first; i < a.sink; i += C * kSelThreads) kept[i] = i;
+  for (int i = first; i < a.recent; i += C * kSelThreads) kept[a.budget - a.recent + i] = n - a.recent + i;
   if (want == 0) return;
+  // This block's run of them.
+  const int per = ((middle + C - 1) / C + 31) / 32 * 32;
+  const int lo = a.sink + min(rank * per, middle), M = min((rank + 1) * per, middle) - min(rank * per, middle);
   const float* w = a.w + row * a.Nk + lo;
   const bool cached = M <= kCached;
   auto key_at = [&](int i) -> uint32_t { return cached ? s_keys[i] : weight_key(__ldg(w + i)); };
@@ -577,13 +598,21 @@ __global__ void __launch_bounds__(kSelThreads) sa_evict_select_kernel(const Evic
     const uint32_t dmask = pass == 2 ? 1023u : 2047u;
     for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
     __syncthreads();
+    // (adding a warp's equal digits at once, by a match, took twice as long)
     for (int i = tid; i < M; i += kSelThreads) {
       const uint32_t k = key_at(i);
       if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & dmask], 1u);
     }
-    __syncthreads();
-    // suffix sums: thread t holds bins 2047 - 2t and 2046 - 2t
-    const uint32_t h0 = hist[kBins - 1 - 2 * tid], h1 = hist[kBins - 2 - 2 * tid];
+    sync_all();
+    // suffix sums over the row: thread t holds bins 2047 - 2t and 2046 - 2t
+    uint32_t h0 = 0, h1 = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint32_t* h = C == 1 ? hist : cluster.map_shared_rank(hist, c);
+      const uint2 x = *reinterpret_cast<const uint2*>(h + kBins - 2 - 2 * tid);
+      h0 += x.y;
+      h1 += x.x;
+    }
     uint32_t inc = h0 + h1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -610,14 +639,14 @@ __global__ void __launch_bounds__(kSelThreads) sa_evict_select_kernel(const Evic
       s_digit = kBins - 2 - 2 * tid;
       s_left = left - above - h0;
     }
-    __syncthreads();
+    sync_all();  // (and every block has read this one's histogram)
     prefix |= s_digit << shift;
     mask |= dmask << shift;
     left = s_left;
-    __syncthreads();
   }
   // Keep every key above the cut, and the first `left` of those at it.  Each
-  // warp owns a run of the row; the counts of the runs before it place its own.
+  // warp owns a run of the block's entries; the counts of the runs before it, in
+  // this block and in the blocks before it, place its own.
   const uint32_t cut = prefix;
   const int run = ((M + 31) / 32 + 31) / 32 * 32;
   const int i0 = warp * run, i1 = min(i0 + run, M);
@@ -635,6 +664,21 @@ __global__ void __launch_bounds__(kSelThreads) sa_evict_select_kernel(const Evic
   }
   __syncthreads();
   uint32_t gb = 0, eb = 0;
+  if (C > 1) {
+    if (warp == 0) {
+      const uint32_t g = __reduce_add_sync(0xffffffffu, wsum[lane]), e = __reduce_add_sync(0xffffffffu, weq[lane]);
+      if (lane == 0) {
+        s_total[0] = g;
+        s_total[1] = e;
+      }
+    }
+    cluster.sync();
+    for (int c = 0; c < rank; ++c) {
+      const uint32_t* t = cluster.map_shared_rank(s_total, c);
+      gb += t[0];
+      eb += t[1];
+    }
+  }
   for (int x = 0; x < warp; ++x) {
     gb += wsum[x];
     eb += weq[x];
@@ -650,11 +694,13 @@ __global__ void __launch_bounds__(kSelThreads) sa_evict_select_kernel(const Evic
     gb += __popc(bg);
     eb += __popc(be);
   }
+  if (C > 1) cluster.sync();  // no block leaves while another may read its totals
 }
 
 // PIECES 16-byte pieces per row (d / 8); U slots per thread in flight.
 template <int PIECES>
 __global__ void __launch_bounds__(256) sa_evict_gather_kernel(const EvictArgs a) {
+  wait_for_earlier_kernel();  // (launched while the entries are still being chosen)
   constexpr int U = 4, kSlots = 256 / PIECES;
   const int piece = threadIdx.x % PIECES;
   const int64_t row = blockIdx.y, b = row / a.Hkv, h = row % a.Hkv;
@@ -694,22 +740,19 @@ __global__ void __launch_bounds__(256) sa_evict_gather_kernel(const EvictArgs a)
 }
 
 cudaError_t launch_cache_evict(const EvictArgs& a, int num_sms, cudaStream_t st) {
-  (void)num_sms;
   const int64_t rows = int64_t(a.B) * a.Hkv;
-  const int smem = kCached * 4;
-  cudaError_t e = cudaFuncSetAttribute(sa_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int blocks = a.Nk > 8192 && rows * 8 <= 4 * num_sms ? 8 : 1;  // a row's
+  const int run = blocks == 1 ? a.Nk : (a.Nk + blocks - 1) / blocks + 32;
+  const int smem = (run < kCached ? run : kCached) * 4;
+  auto kern = blocks == 8 ? sa_evict_select_kernel<8> : sa_evict_select_kernel<1>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4);
   if (e != cudaSuccess) return e;
-  const int64_t need = int64_t(a.Nk) < kCached ? int64_t(a.Nk) * 4 : smem;
-  sa_evict_select_kernel<<<static_cast<unsigned>(rows), kSelThreads, need, st>>>(a);
+  kern<<<static_cast<unsigned>(rows * blocks), kSelThreads, smem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (!a.k && !a.w_out) return cudaSuccess;
   const int slots = 4 * (256 / (a.d / 8));
   const dim3 grid((a.budget + slots - 1) / slots, static_cast<unsigned>(rows));
-  if (a.d == 128)
-    sa_evict_gather_kernel<16><<<grid, 256, 0, st>>>(a);
-  else
-    sa_evict_gather_kernel<8><<<grid, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(a.d == 128 ? sa_evict_gather_kernel<16> : sa_evict_gather_kernel<8>, grid, 256, 0, st, a);
 }
 
 }  // namespace sa
