@@ -466,7 +466,11 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
           tc_fence_before();
           mbar_arrive(&bars->ofree[t]);
 #pragma unroll
-          for (int y = 0; y < D / 2; ++y) v[y] = __float_as_uint(inv == 0.f ? 0.f : __uint_as_float(v[y]) * inv);
+          for (int y = 0; y < D / 2; ++y) v[y] = __float_as_uint(__uint_as_float(v[y]) * inv);
+          if (__any_sync(0xffffffffu, inv == 0.f)) {  // (a row that saw nothing: 0 whatever O holds)
+#pragma unroll
+            for (int y = 0; y < D / 2; ++y) v[y] = inv == 0.f ? 0 : v[y];
+          }
         } else {
 #pragma unroll
           for (int y = 0; y < D / 2; ++y) v[y] = 0;
@@ -486,7 +490,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
               for (int c = 0; c < P; ++c) *cell(lane - r0, c) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
             }
             __syncwarp();
-#pragma unroll
+#pragma unroll 1
             for (int f = 0; f < kRows * P; f += 32) {
               const int r = (f + lane) / P, c = (f + lane) % P;
               const int64_t to = __shfl_sync(0xffffffffu, at, r0 + r);
