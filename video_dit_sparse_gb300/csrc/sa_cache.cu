@@ -49,6 +49,7 @@ struct WCfg {
 struct WPlan {
   int32_t qn, rows, NR, qtiles, qst, kst, kqbytes, ktile;
   int32_t units, kunits;  // in all, and per head
+  int32_t parts;          // blocks (a cluster) that share a unit's Q tiles
 };
 constexpr int kUnitKeys = 256;
 
@@ -69,7 +70,8 @@ struct WBars {
   int abort;
 };
 
-__device__ __forceinline__ WUnit unit_at(const MaskedArgs& a, const WPlan& p, int u) {
+// Unit u, and of its Q tiles the run that block `rank` of its cluster takes.
+__device__ __forceinline__ WUnit unit_at(const MaskedArgs& a, const WPlan& p, int u, int rank) {
   WUnit x;
   x.go = 1;
   const int bh = u / p.kunits;
@@ -85,6 +87,9 @@ __device__ __forceinline__ WUnit unit_at(const MaskedArgs& a, const WPlan& p, in
     if (m.nd)
       while (x.t1 > x.t0 && row_span(m, x.b, (x.t1 - 1) * p.qn).lo >= x.k0 + kUnitKeys) --x.t1;
   }
+  const int n = x.t1 - x.t0;
+  x.t1 = x.t0 + n * (rank + 1) / p.parts;
+  x.t0 += n * rank / p.parts;
   // Blocks that work on the same head's keys start at different Q tiles (in step
   // they would all ask L2 for the same lines).
   x.rot = (u & 15) * (x.t1 - x.t0) / 16;
@@ -104,10 +109,12 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
   uint8_t* sQ = sK + p.kst * p.ktile;
   float* sL = reinterpret_cast<float*>(sQ + p.qst * p.kqbytes);  // [2][4 sets][128] -lse in exp2 units
   int* sD = reinterpret_cast<int*>(sL + 2 * 4 * 128);            // [2][4 sets][4 warps] a row without lse
-  float* sX = reinterpret_cast<float*>(sD + 2 * 4 * 4);          // [2][128] half 1's sums of each key tile
-  WBars* bars = reinterpret_cast<WBars*>(sX + 2 * 128);
+  float* sX = reinterpret_cast<float*>(sD + 2 * 4 * 4);          // [2][128] half 1's sums of each key tile; [2][128] the block's
+  WBars* bars = reinterpret_cast<WBars*>(sX + 4 * 128);
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % p.parts;
+  if (threadIdx.x < 256) sX[2 * 128 + threadIdx.x] = 0.f;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&bars->kfull[s], 1);
@@ -179,7 +186,7 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
       nwas = 0.f;
       if (!nu.go) return true;
       const int key = nu.k0 + d * 128 + tid;
-      if (!half && key < a.Nk && wa.w_in && (key >= nu.len || wa.decay != 0.f))
+      if (p.parts == 1 && !half && key < a.Nk && wa.w_in && (key >= nu.len || wa.decay != 0.f))
         nwas = wa.w_in[(int64_t(nu.b) * a.Hkv + nu.hk) * a.Nk + key];
       if (nu.t0 < nu.t1) fetch(nu, nu.tile(0));
       return true;
@@ -341,7 +348,9 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
         }
         ++hn;
       }
-      if (!half && key < a.Nk) {
+      if (p.parts > 1) {
+        if (!half) sX[(2 + d) * 128 + tid] = total;  // joined below
+      } else if (!half && key < a.Nk) {
         const int64_t wi = (int64_t(b) * a.Hkv + x.hk) * a.Nk + key;
         if (key < x.len)
           wa.w_out[wi] = wa.decay != 0.f ? fmaf(wa.decay, was, total) : total;
@@ -415,21 +424,28 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
       ++it;
       return true;
     };
-    // The block's own unit, then units of blocks that have not started.
-    int64_t u = blockIdx.x;
+    // The block's own unit, then (unless units are shared) units of blocks that
+    // have not started.
+    int64_t u = blockIdx.x / p.parts;
     uint32_t i = 0;
     for (; ok; ++i) {
       WUnit x = {};
       if (u >= 0) {
-        mbar_expect_tx(&bars->next, 16);
-        request_block(&bars->answer, &bars->next);
-        x = unit_at(a, p, static_cast<int>(u));
+        if (p.parts == 1) {
+          mbar_expect_tx(&bars->next, 16);
+          request_block(&bars->answer, &bars->next);
+        }
+        x = unit_at(a, p, static_cast<int>(u), rank);
       }
       if (i >= 2 && !mbar_wait(&bars->ring_empty[i & 1], ((i >> 1) - 1) & 1, abort)) break;
       bars->ring[i & 1] = x;
       mbar_arrive(&bars->ring_full[i & 1]);
       if (u < 0) break;
       auto following = [&]() -> bool {
+        if (p.parts > 1) {
+          u = -1;
+          return true;
+        }
         if (!mbar_wait(&bars->next, i & 1, abort)) return false;
         u = answered_block(&bars->answer);
         fence_proxy_async_smem();  // read before the next answer is written
@@ -466,7 +482,7 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
         while (!mbar_test(&bars->kfull[f % p.kst], (f / p.kst) & 1) && clock64() - c0 < kWaitLimitCycles) {
         }
       }
-      if (u >= 0) {
+      if (u >= 0 && p.parts == 1) {
         const long long c0 = clock64();
         while (!mbar_test(&bars->next, i & 1) && clock64() - c0 < kWaitLimitCycles) {
         }
@@ -478,6 +494,23 @@ done:
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && bars->abort) report(a.status, SA_DEVERR_TIMEOUT);
+  if (p.parts > 1) {
+    // The blocks' sums, in the order of their ranks.
+    const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    cluster.sync();
+    const WUnit x = unit_at(a, p, blockIdx.x / p.parts, rank);
+    const int key = x.k0 + threadIdx.x;
+    if (rank == 0 && threadIdx.x < kUnitKeys && key < a.Nk) {
+      float total = 0.f;
+      for (int r = 0; r < p.parts; ++r) total += cluster.map_shared_rank(sX, r)[2 * 128 + threadIdx.x];
+      const int64_t wi = (int64_t(x.b) * a.Hkv + x.hk) * a.Nk + key;
+      if (key < x.len)
+        wa.w_out[wi] = wa.decay != 0.f ? fmaf(wa.decay, wa.w_in[wi], total) : total;
+      else if (wa.w_in && wa.w_in != wa.w_out)
+        wa.w_out[wi] = wa.w_in[wi];
+    }
+    cluster.sync();  // no block leaves while its sums are read
+  }
   if (warp == WCfg::kMmaWarp) {
     __syncwarp();
     tc_fence_after();
@@ -489,7 +522,7 @@ template <int D, bool CAP, bool BIAS>
 static cudaError_t launch_w(const WeightArgs& a, const WPlan& p, const CUtensorMap& tq, const CUtensorMap& tk,
                             int num_sms, cudaStream_t st) {
   auto kern = sa_cache_weights_kernel<D, CAP, BIAS>;
-  int smem = 1024 + p.kst * p.ktile + p.qst * p.kqbytes + 2 * 4 * 128 * 4 + 2 * 4 * 4 * 4 + 2 * 128 * 4 +
+  int smem = 1024 + p.kst * p.ktile + p.qst * p.kqbytes + 2 * 4 * 128 * 4 + 2 * 4 * 4 * 4 + 4 * 128 * 4 +
              static_cast<int>(sizeof(WBars)) + 64;
   if (smem < 120 * 1024) smem = 120 * 1024;  // one block per SM owns its TMEM
   static std::atomic<int> regs_ok{0};  // 0 unknown, 1 enough, 2 too few
@@ -503,8 +536,18 @@ static cudaError_t launch_w(const WeightArgs& a, const WPlan& p, const CUtensorM
   if (regs_ok.load() != 1) return cudaErrorLaunchOutOfResources;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<p.units, WCfg::kThreads, smem, st>>>(a, p, tq, tk);
-  return cudaGetLastError();
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(p.units * p.parts);
+  c.blockDim = dim3(WCfg::kThreads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = p.parts;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  c.attrs = &attr;
+  c.numAttrs = p.parts > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kern, a, p, tq, tk);
 }
 
 cudaError_t launch_cache_weights(const WeightArgs& a, int num_sms, cudaStream_t st) {
@@ -522,6 +565,10 @@ cudaError_t launch_cache_weights(const WeightArgs& a, int num_sms, cudaStream_t 
   p.kst &= ~1;  // whole units
   p.kunits = (m.Nk + kUnitKeys - 1) / kUnitKeys;
   p.units = m.B * m.Hkv * p.kunits;  // (the entry point checks that it fits)
+  // Few keys and many rows: up to eight blocks share a unit's Q tiles (four SMs in
+  // five can hold such a cluster, so the SMs are not filled to the last).
+  p.parts = 1;
+  while (p.parts < 8 && p.units * p.parts * 2 <= num_sms * 4 / 5 && p.parts * 2 <= p.qtiles) p.parts *= 2;
   CUtensorMap tq, tk;
   if (!make_view_map(&tq, m.q, m.d, m.Nq, m.Hq, m.B, m.qs.n, m.qs.h, m.qs.b, p.qn, m.R, true) ||
       !make_view_map(&tk, m.k, m.d, m.Nk, m.Hkv, m.B, m.ks.n, m.ks.h, m.ks.b, 128, 1, false))
