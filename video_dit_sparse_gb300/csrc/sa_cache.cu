@@ -230,19 +230,32 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
         __syncwarp();
         tc_fence_after();
         uint64_t acc[2] = {0, 0};
-        // An exponent from its raw product and -lse.
+        // An exponent from its raw product and -lse.  With a cap: exactly (three MUFU
+        // results), or (`quick`) tanh(z)/z by the masked forward's polynomial for
+        // |z| <= 0.4; a tile with a larger score is summed again exactly.
         auto exponent = [&](float x, float L) -> float {
           if (CAP) return fmaf(-2.f * a.cap_log2, fast_rcp(1.f + fast_exp2(x * a.cap_k1)), a.cap_log2) + L;
           return fmaf(x, sl, L);
         };
         // The plain columns of the tile: the next 32 load while 32 are summed.
+        bool quick = CAP;
+        float wm = 0.f;
         auto sum = [&](const float* x, int c, int count) {
           const uint64_t sl2 = f2(sl, sl);
+          const uint64_t k1 = f2(a.cap_p1, a.cap_p1), k2 = f2(a.cap_p2, a.cap_p2), k3 = f2(a.cap_p3, a.cap_p3);
+          auto bent = [&](float x0, float x1, uint64_t L) -> uint64_t {
+            const uint64_t xx = f2(x0, x1), w = mul2(xx, xx);
+            wm = fmax3(wm, f2lo(w), f2hi(w));
+            return fma2(xx, fma2(w, fma2(w, fma2(w, k3, k2), k1), sl2), L);
+          };
 #pragma unroll
           for (int e = 0; e < count; e += 4) {
             const ulonglong2 L = *reinterpret_cast<const ulonglong2*>(wL + c + e);
             uint64_t y0, y1;
-            if (CAP) {
+            if (CAP && quick) {
+              y0 = bent(x[e], x[e + 1], L.x);
+              y1 = bent(x[e + 2], x[e + 3], L.y);
+            } else if (CAP) {
               y0 = f2(exponent(x[e], f2lo(L.x)), exponent(x[e + 1], f2hi(L.x)));
               y1 = f2(exponent(x[e + 2], f2lo(L.y)), exponent(x[e + 3], f2hi(L.y)));
             } else {
@@ -331,6 +344,13 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
           after_first();
         else
           plain();
+        // (keys behind the tensor are zeros; what lies behind a sequence may hold anything)
+        if (CAP && !(BIAS || edge || dead || cut) &&
+            __any_sync(0xffffffffu, key < x.len && !(wm <= a.cap_limit))) {
+          quick = false;
+          acc[0] = acc[1] = 0;
+          plain();
+        }
         tc_fence_before();
         mbar_arrive(&bars->dempty[d]);
         const uint64_t s2 = add2(acc[0], acc[1]);
