@@ -230,3 +230,65 @@ def test_one_step_of_a_rolling_cache():
             kc[:, :, :budget], vc[:, :, :budget], w[:, :, :budget] = k2, v2, w2
             n = budget
     assert n == budget
+
+
+@pytest.mark.parametrize("causal,cap", [(0, 0.0), (33, 0.0), (1, 9.0), (0, 9.0)])
+@pytest.mark.parametrize("H,Hk,Nq,Nk", [(1, 1, 3000, 70), (4, 2, 1500, 300), (84, 84, 40, 600), (128, 1, 9, 200)])
+def test_weights_shared_and_many_units(H, Hk, Nq, Nk, causal, cap):
+    """Few keys: a cluster shares a unit's rows.  Many units: a block takes several."""
+    q, k, v, lse, w, got, dev = case(H, Hk, Nq, Nk, 64, seed=31, causal=causal, cap=cap)
+    from video_dit_sparse_gb300 import binding as sa
+    acc = w.clone()
+    sa.sparse_attn_cache_weights(q, k, lse, acc, decay=0.9, out=acc, **dev)
+    assert torch.equal(acc, got)
+
+
+def test_weights_large_scores_under_a_cap():
+    """Scores past the polynomial's range: the tile is summed again exactly."""
+    from video_dit_sparse_gb300 import binding as sa
+    q, k, v = tensors(1, 2, 2, 300, 400, 64, seed=32, sigma=6.0)
+    k[:, :, 200:] = float("inf")  # behind the sequence
+    lens = torch.tensor([200], dtype=torch.int32, device="cuda")
+    _, lse = sa.sparse_attn_forward_masked(q, k, torch.nan_to_num(v), cap=7.0, lengths=lens)
+    got = sa.sparse_attn_cache_weights(q, k, lse, cap=7.0, lengths=lens)
+    want, tol = weights_want(q, torch.nan_to_num(k, posinf=0.0), lse, None, decay=0.0, cap=7.0, lengths=[200])
+    assert (np.abs(got.double().cpu().numpy() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("B,H,N,budget", [(1, 1, 500000, 1000), (77, 1, 50000, 49000), (1, 2, 8193, 8192), (2, 3, 40000, 20)])
+def test_evict_long_rows(B, H, N, budget):
+    from video_dit_sparse_gb300 import binding as sa
+    g = torch.Generator(device="cuda").manual_seed(N)
+    w = torch.rand(B, H, N, generator=g, device="cuda").mul(1 << 12).round() / (1 << 12)  # many ties
+    kept, _, _, wo = sa.sparse_attn_cache_evict(w, None, None, budget, sink=3, recent=5)
+    assert torch.equal(wo, w.gather(2, kept.long()))
+    for b, h in ((0, 0), (B - 1, H - 1)):
+        want = O.evict(w[b, h].cpu().numpy(), N, budget, 3, 5)
+        assert np.array_equal(kept[b, h].cpu().numpy(), want)
+
+
+def test_a_step_in_a_graph():
+    from video_dit_sparse_gb300 import binding as sa
+    q, k, v = tensors(1, 4, 2, 1, 2000, 64, seed=33)
+    lens = torch.tensor([1500], dtype=torch.int32, device="cuda")
+    w = torch.rand(1, 2, 2000, device="cuda")
+    kept = torch.empty(1, 2, 700, dtype=torch.int32, device="cuda")
+    out = (torch.zeros(1, 2, 700, 64, dtype=torch.bfloat16, device="cuda"),
+           torch.zeros(1, 2, 700, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 2, 700, device="cuda"))
+
+    def step():
+        o, lse = sa.sparse_attn_forward_masked(q, k, v, lengths=lens)
+        acc = sa.sparse_attn_cache_weights(q, k, lse, w, lengths=lens)
+        sa.sparse_attn_cache_evict(acc, k, v, 700, recent=10, lengths=lens, out=out, kept=kept)
+        return o, acc
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, acc = step()
+    for n in (1999, 3, 800):
+        lens.fill_(n)
+        g.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (o, acc, kept)]
+        want = step()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2], kept)

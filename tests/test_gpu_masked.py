@@ -206,3 +206,57 @@ def test_tables_that_point_outside_read_nothing_outside():
     check(o, lse, q, k, v)
     o, lse = run(q, k, v, lengths=[-4])
     assert bool((o == 0).all()) and bool((lse == -float("inf")).all())
+
+
+@pytest.mark.parametrize("d,R,causal,bias", [(64, 1, 1, True), (128, 3, 0, False), (128, 1, 50, False)])
+def test_more_units_than_blocks(d, R, causal, bias):
+    """Every block takes several units, of different lengths, and the last ones are split."""
+    H = 42 * R
+    q, k, v = tensors(2, H, 42, 515 // R, 500, d, seed=21)
+    kw = dict(causal=causal, slopes=[0.02 * (h % 5) for h in range(H)] if bias else None,
+              docs_q=[[0, 60, 61, 515 // R], [0, 0, 100, 515 // R]], docs_k=[[0, 100, 130, 500], [0, 250, 257, 499]])
+    check(*run(q, k, v, **kw), q, k, v, **kw)
+
+
+def test_most_heads_that_share_a_key_head():
+    q, k, v = tensors(1, 128, 1, 3, 300, 64, seed=22)
+    check(*run(q, k, v, causal=1), q, k, v, causal=1)
+
+
+def test_offsets_past_32_bits():
+    from video_dit_sparse_gb300 import binding as sa
+    n, d, far = 300, 64, 1 << 31  # heads 2^31 elements apart
+    buf = torch.empty(far + 4 * n * d, dtype=torch.bfloat16, device="cuda")
+    views = [buf.as_strided((1, 2, n, d), (0, far, d, 1), i * n * d) for i in range(4)]
+    q, k, v = tensors(1, 2, 2, n, n, d, seed=23)
+    for to, of in zip(views, (q, k, v)):
+        to.copy_(of)
+    o, lse = sa.sparse_attn_forward_masked(*views[:3], causal=1, out=views[3])
+    want, wl = sa.sparse_attn_forward_masked(q, k, v, causal=1)
+    assert torch.equal(o, want) and torch.equal(lse, wl)
+    w = sa.sparse_attn_cache_weights(views[0], views[1], lse, causal=1)
+    assert torch.equal(w, sa.sparse_attn_cache_weights(q, k, lse, causal=1))
+    kept, k2, v2, w2 = sa.sparse_attn_cache_evict(w, views[1], views[2], 100)
+    at = kept.long()[..., None].expand(1, 2, 100, d)
+    assert torch.equal(k2, k.gather(2, at)) and torch.equal(v2, v.gather(2, at))
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")[:, None]
+    got = sa.sparse_attn_rope(views[0], views[1], axes=(d,), positions=pos, out=(views[3], views[1]))
+    assert torch.equal(got[0], sa.sparse_attn_rope(q, axes=(d,), positions=pos))
+    assert torch.equal(got[1], sa.sparse_attn_rope(k, axes=(d,), positions=pos))
+
+
+def test_two_streams_at_once():
+    from video_dit_sparse_gb300 import binding as sa
+    q, k, v = tensors(1, 4, 4, 700, 900, 128, seed=24)
+    t, kc, vc = tensors(2, 8, 2, 1, 5000, 128, seed=25)
+    a = sa.sparse_attn_forward_masked(q, k, v, causal=1)
+    b = sa.sparse_attn_forward_masked(t, kc, vc)
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        x = sa.sparse_attn_forward_masked(q, k, v, causal=1, stream=s[0])
+        y = sa.sparse_attn_forward_masked(t, kc, vc, stream=s[1])
+        z = sa.sparse_attn_forward_masked(t, kc, vc, stream=s[0])
+        torch.cuda.synchronize()
+        for got, want in ((x, a), (y, b), (z, b)):
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -140,6 +140,11 @@ def test_rope_refusals(sa):
     assert call(far) == INVALID
     for bad in (dict(d=96), dict(pairing=1, dims=(10, 10, 10)), dict(B=70000)):
         assert call(prob(**bad)) == UNSUPPORTED, bad
+    # two slots of one buffer interleave; a row less apart they would meet
+    two = prob(N=2, grid=sa.sa_voxel_grid(1, 1, 2, 0, 0, 0))
+    wide = S(0, 64, 3 * 2 * 64)
+    assert call(two, xs=wide, ys=wide, y=X + 2 * 2 * 64) != INVALID
+    assert call(two, xs=wide, ys=wide, y=X + 2 * 64) == INVALID
     ok = prob()
     for bad in (dict(H=0), dict(H1=-1), dict(x=None), dict(y=None), dict(xs=None), dict(ys=None), dict(x=X + 8),
                 dict(H1=2), dict(H1=2, x1=X, x1s=st, y1=None, y1s=st), dict(y=X + 3840), dict(ys=S(1920, 960, 64)),

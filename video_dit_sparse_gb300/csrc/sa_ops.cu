@@ -5,6 +5,8 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
+#include <numeric>
 
 #include "sa_internal.h"
 #include "sparse_attn.h"
@@ -58,6 +60,33 @@ bool check_view(const void* p, sa_strides* s, int64_t B, int64_t H, int64_t N, i
 bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
+}
+
+// Whether two views of the same shape (checked by check_view) may share an
+// element.  With the same strides they may interleave in one buffer: rows that
+// follow one another make blocks, and blocks start at multiples of the other
+// strides' common divisor g from the view's start, so views whose starts differ by
+// at least a block modulo g, either way round, never meet.
+bool views_overlap(const void* a, const sa_strides& as, uint64_t na, const void* b, const sa_strides& bs,
+                   uint64_t nb, int64_t B, int64_t H, int64_t N, int64_t d, int esz) {
+  if (!overlap(a, na, b, nb)) return false;
+  if (as.b != bs.b || as.h != bs.h || as.n != bs.n) return true;
+  struct Dim {
+    int64_t n, stride;
+  } dims[3] = {{B, as.b}, {H, as.h}, {N, as.n}};
+  std::sort(dims, dims + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+  int64_t block = d, g = 0;
+  for (const Dim& x : dims) {
+    if (x.n == 1) continue;
+    if (g == 0 && x.stride == block)
+      block *= x.n;
+    else
+      g = std::gcd(g, x.stride);
+  }
+  const int64_t apart = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a)) / esz;
+  if (g == 0) return std::llabs(apart) < block;
+  const int64_t m = ((apart % g) + g) % g;
+  return m < block || g - m < block;
 }
 
 // Shapes and options of sa_masked; fills everything but the tensor pointers.
@@ -256,12 +285,12 @@ sa_status sparse_attn_cache_evict(const sa_evict* p, const float* weights, const
     if (!out[i].n) continue;
     for (const Span& x : in)
       if (x.n && overlap(x.p, x.n, out[i].p, out[i].n)) return SA_ERR_INVALID_ARG;
-    // (k_out and v_out may be interleaved views of one buffer)
-    for (int j = 0; j < i; ++j)
+    for (int j = 0; j < i; ++j)  // (k_out and v_out: below)
       if (out[j].n && !(j == 1 && i == 2) && overlap(out[j].p, out[j].n, out[i].p, out[i].n))
         return SA_ERR_INVALID_ARG;
   }
-  if (kv && k_out == v_out) return SA_ERR_INVALID_ARG;
+  if (kv && views_overlap(k_out, a.kos, nko, v_out, a.vos, nvo, p->B, p->Hkv, p->budget, p->d, 2))
+    return SA_ERR_INVALID_ARG;
   int sms = 0;
   sa_status st = device_info(&sms);
   if (st != SA_OK) return st;
@@ -372,7 +401,8 @@ sa_status sparse_attn_rope(const sa_rope* p, int32_t H0, const void* x0, const s
       return SA_ERR_INVALID_ARG;
     // in place (the same view) or apart: a row is read only by the threads that write it
     const bool same = x[i] == y[i] && a.xs[i].b == a.ys[i].b && a.xs[i].h == a.ys[i].h && a.xs[i].n == a.ys[i].n;
-    if (!same && overlap(x[i], nx[i], y[i], ny[i])) return SA_ERR_INVALID_ARG;
+    if (!same && views_overlap(x[i], a.xs[i], nx[i], y[i], a.ys[i], ny[i], p->B, H[i], p->N, p->d, esz))
+      return SA_ERR_INVALID_ARG;
   }
   int sms = 0;
   sa_status st = device_info(&sms);
