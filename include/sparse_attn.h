@@ -511,7 +511,8 @@ typedef struct {
 
 size_t sparse_attn_forward_masked_workspace_size(const sa_masked* problem);
 
-/* lse (fp32 [B, Hq, Nq]) and dev_status are nullable. */
+/* lse (fp32 [B, Hq, Nq]) and dev_status are nullable.  o may be q's own view
+ * (bf16); otherwise no output or workspace may share memory with another argument. */
 sa_status sparse_attn_forward_masked(const sa_masked* problem, const void* q, const void* k, const void* v,
                                      void* o, float* lse, int32_t* dev_status, void* workspace,
                                      size_t workspace_bytes, sa_stream_t stream);

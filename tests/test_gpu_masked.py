@@ -260,3 +260,14 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for got, want in ((x, a), (y, b), (z, b)):
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_output_over_the_queries():
+    from video_dit_sparse_gb300 import binding as sa
+    for H, Nq, Nk in ((4, 700, 900), (42, 515, 300), (8, 1, 4000)):
+        q, k, v = tensors(2, H, 2, Nq, Nk, 128, seed=26)
+        want, wl = sa.sparse_attn_forward_masked(q, k, v, causal=1)
+        o, lse = sa.sparse_attn_forward_masked(q, k, v, causal=1, out=q)
+        assert o is q and torch.equal(o, want) and torch.equal(lse, wl)
+    with pytest.raises(sa.SparseAttnError):
+        sa.sparse_attn_forward_masked(k, k, v, out=k)

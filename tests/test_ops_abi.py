@@ -30,7 +30,10 @@ def masked(sa, **kw):
     return p
 
 
-def forward(sa, p, q=A16, k=A16, v=A16, o=A16, lse=None, ws=A16, nws=1 << 30):
+Q, K, V, OUT, WS, LSE = (i << 24 for i in range(1, 7))
+
+
+def forward(sa, p, q=Q, k=K, v=V, o=OUT, lse=None, ws=WS, nws=1 << 30):
     return sa.lib.sparse_attn_forward_masked(p, q, k, v, o, lse, None, ws, nws, None)
 
 
@@ -38,7 +41,7 @@ def test_forward_masked_refusals(sa):
     assert forward(sa, None) == INVALID
     for bad in (dict(B=0), dict(Hq=0), dict(Hkv=0), dict(Nq=0), dict(Nk=0), dict(d=0), dict(Hq=3), dict(scale=0.0),
                 dict(scale=float("nan")), dict(cap=-1.0), dict(cap=float("inf")), dict(causal=-1), dict(ndocs=-1),
-                dict(out_dtype=5), dict(ndocs=2), dict(ndocs=2, docs_q=A16), dict(docs_q=A16), dict(prefix=A16),
+                dict(out_dtype=5), dict(scale=3e38), dict(cap=1e-38, scale=1e5), dict(ndocs=2), dict(ndocs=2, docs_q=A16), dict(docs_q=A16), dict(prefix=A16),
                 dict(ndocs=1, docs_q=A16, docs_k=A16, lengths=A16), dict(slopes=A16 + 2), dict(lengths=A16 + 1)):
         assert forward(sa, masked(sa, **bad)) == INVALID, bad
     for bad in (dict(d=96), dict(Nk=2 ** 30 + 1), dict(Nq=2 ** 30 + 1), dict(B=2 ** 23)):
@@ -48,7 +51,12 @@ def test_forward_masked_refusals(sa):
         assert forward(sa, ok, **{name: None}) == INVALID
         assert forward(sa, ok, **{name: MIS}) == INVALID
     assert forward(sa, masked(sa, Hq=258, q=sa.sa_strides(258 * 1024, 1024, 128), o=sa.sa_strides(258 * 1024, 1024, 128))) == UNSUPPORTED
-    assert forward(sa, ok, lse=A16 + 2) == INVALID
+    assert forward(sa, ok, lse=LSE + 2) == INVALID
+    if not torch.cuda.is_available():  # what passes the checks on arguments ends at the device's
+        assert forward(sa, ok) not in (0, INVALID) and forward(sa, ok, o=Q) not in (0, INVALID)
+    for bad in (dict(o=K), dict(o=V + 256), dict(o=Q + 256), dict(lse=K), dict(lse=OUT), dict(lse=Q + 64)):
+        assert forward(sa, ok, **bad) == INVALID, bad
+    assert forward(sa, masked(sa, out_dtype=1), o=Q) == INVALID  # fp32 rows are not q's
     S = sa.sa_strides
     for bad in (dict(q=S(4096, 1024, -128)), dict(q=S(4096, 1024, 100)), dict(k=S(16384, 8192, 0)),
                 dict(o=S(4096, 1024, 0)), dict(o=S(4096, 128, 128)), dict(o=S(4096, 1024, 64)),
@@ -62,7 +70,7 @@ def test_forward_masked_refusals(sa):
     assert need > 0 and need % 256 == 0
     assert forward(sa, few, ws=None, nws=0) == INVALID
     assert forward(sa, few, nws=need - 1) == INVALID
-    assert forward(sa, few, ws=A16 + 16) == INVALID
+    assert forward(sa, few, ws=WS + 16) == INVALID and forward(sa, few, ws=K) == INVALID
     assert sa.lib.sparse_attn_forward_masked_workspace_size(None) == 0
     assert sa.lib.sparse_attn_forward_masked_workspace_size(masked(sa, d=96)) == 0
 
@@ -143,7 +151,8 @@ def test_rope_refusals(sa):
     # two slots of one buffer interleave; a row less apart they would meet
     two = prob(N=2, grid=sa.sa_voxel_grid(1, 1, 2, 0, 0, 0))
     wide = S(0, 64, 3 * 2 * 64)
-    assert call(two, xs=wide, ys=wide, y=X + 2 * 2 * 64) != INVALID
+    if not torch.cuda.is_available():
+        assert call(two, xs=wide, ys=wide, y=X + 2 * 2 * 64) != INVALID
     assert call(two, xs=wide, ys=wide, y=X + 2 * 64) == INVALID
     ok = prob()
     for bad in (dict(H=0), dict(H1=-1), dict(x=None), dict(y=None), dict(xs=None), dict(ys=None), dict(x=X + 8),

@@ -441,6 +441,9 @@ _ROPE = struct.Struct("@10id2Pq6ii3q")
 assert _MASKED.size == ctypes.sizeof(sa_masked) and _EVICT.size == ctypes.sizeof(sa_evict)
 assert _ROPE.size == ctypes.sizeof(sa_rope)
 _STRIDES = struct.Struct("@3q")
+_bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
+_empty, _empty_like = torch.empty, torch.empty_like
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _by_bytes(name, argtypes, restype=ctypes.c_int):
@@ -478,16 +481,9 @@ def _flat(t, dtype, name, dev, shape=None) -> int:
     return t.data_ptr()
 
 
-def _elsewhere(dev: int) -> bool:
-    """Whether `dev` is another CUDA device than the current one."""
-    return dev >= 0 and dev != torch._C._cuda_getDevice()
-
-
 def _raw_stream(stream, dev: int, *made) -> int:
-    """The stream's handle.  Tensors made for a call on another stream than the current one are
-    recorded there."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+    """The handle of a stream other than the current one; tensors made for the call are recorded
+    there."""
     for t in made:
         if t is not None:
             t.record_stream(stream)
@@ -506,7 +502,7 @@ def sparse_attn_rope(q: torch.Tensor, k: torch.Tensor | None = None, *, axes=(44
     `offset`.  inv_freq: r/2 frequencies (radians per position) instead of theta's.  inverse rotates
     back, which is also the gradient.  out: the output (or a pair of them); it may be the input."""
     dtype, dev = q.dtype, q.get_device()
-    if _elsewhere(dev):
+    if dev >= 0 and dev != _current_device():  # the tensor's device made current
         with torch.cuda.device(dev):
             return sparse_attn_rope(q, k, axes=axes, theta=theta, inv_freq=inv_freq, pairing=pairing,
                                     grid=grid, voxel=voxel, offset=offset, positions=positions,
@@ -542,28 +538,28 @@ def sparse_attn_rope(q: torch.Tensor, k: torch.Tensor | None = None, *, axes=(44
         if voxel is not None or any(offset):
             raise ValueError("voxel and offset go with grid")
         shared = positions.dim() == 2
-        pos = _flat(positions, torch.int32, "positions", dev, (N, na) if shared else (B, N, na))
+        pos = _flat(positions, _i32, "positions", dev, (N, na) if shared else (B, N, na))
         pos_b = 0 if shared else N * na
     else:
         order = 0 if voxel is None else 1
         cells = (*grid, *(voxel or (0, 0, 0)))
     p = _ROPE.pack(B, N, d, na, *axes, *(0,) * (3 - na), _PAIRINGS[pairing], _OUT[dtype],
                    1 if inverse else 0, theta, freq, pos, pos_b, *cells, order, *offset)
-    y = torch.empty_like(q) if oq is None else oq
+    y = _empty_like(q) if oq is None else oq
     if y.shape != q.shape:
         raise ValueError("out must have q's shape")
     ys = _STRIDES.pack(*_view(y, dtype, "out", dev))
     z = None
     if k is None:
         st = _c_rope(p, H, q.data_ptr(), _STRIDES.pack(*qs), y.data_ptr(), ys, 0, None, None, None, None,
-                     _raw_stream(stream, dev, y))
+                     _current_stream(dev) if stream is None else _raw_stream(stream, dev, y))
     else:
-        z = torch.empty_like(k) if ok is None else ok
+        z = _empty_like(k) if ok is None else ok
         if z.shape != k.shape:
             raise ValueError("out of k must have k's shape")
         st = _c_rope(p, H, q.data_ptr(), _STRIDES.pack(*qs), y.data_ptr(), ys, k.shape[1], k.data_ptr(), ks,
                      z.data_ptr(), _STRIDES.pack(*_view(z, dtype, "out of k", dev)),
-                     _raw_stream(stream, dev, y, z))
+                     _current_stream(dev) if stream is None else _raw_stream(stream, dev, y, z))
     if st != SA_OK:
         raise SparseAttnError(st, "sparse_attn_rope")
     return y if k is None else (y, z)
@@ -571,10 +567,11 @@ def sparse_attn_rope(q: torch.Tensor, k: torch.Tensor | None = None, *, axes=(44
 
 def _mask_fields(q, k, dev, slopes, docs_q, docs_k, prefix, lengths):
     """The mask's tables: (number of documents, their addresses, tensors to keep)."""
-    B, H = q.shape[:2]
-    if k.shape[0] != B or k.shape[3] != q.shape[3] or not k.shape[1] or H % k.shape[1]:
+    B, H, _, d = q.shape
+    kb, kh, _, kd = k.shape
+    if kb != B or kd != d or not kh or H % kh:
         raise ValueError("k must be [B, Hk, Nk, d] with q's B and d, and H a multiple of Hk")
-    slopes = _flat(slopes, torch.float32, "slopes", dev, (H,))
+    slopes = 0 if slopes is None else _flat(slopes, _f32, "slopes", dev, (H,))
     n, made = 0, ()
     if docs_q is None:
         if docs_k is not None or prefix is not None:
@@ -591,10 +588,11 @@ def _mask_fields(q, k, dev, slopes, docs_q, docs_k, prefix, lengths):
             prefix = None if prefix is None else prefix.expand(B, n).contiguous()
             made = (docs_q, docs_k, prefix)
         one = docs_q.dim() == 1
-        dq = _flat(docs_q, torch.int32, "docs_q", dev, (n + 1,) if one else (B, n + 1))
-        dk = _flat(docs_k, torch.int32, "docs_k", dev, (n + 1,) if one else (B, n + 1))
-        px = _flat(prefix, torch.int32, "prefix", dev, (n,) if one else (B, n))
-    return n, slopes, dq, dk, px, _flat(lengths, torch.int32, "lengths", dev, (B,)), made
+        dq = _flat(docs_q, _i32, "docs_q", dev, (n + 1,) if one else (B, n + 1))
+        dk = _flat(docs_k, _i32, "docs_k", dev, (n + 1,) if one else (B, n + 1))
+        px = _flat(prefix, _i32, "prefix", dev, (n,) if one else (B, n))
+    lengths = 0 if lengths is None else _flat(lengths, _i32, "lengths", dev, (B,))
+    return n, slopes, dq, dk, px, lengths, made
 
 
 def sparse_attn_forward_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
@@ -617,26 +615,26 @@ def sparse_attn_forward_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     frame when `causal` (tokens per frame, 1: per token), and the document's first `prefix` keys.  A
     document's rows are its last positions, so one new token over a cache is Nq = 1 with lengths."""
     dev = q.get_device()
-    if _elsewhere(dev):
+    if dev >= 0 and dev != _current_device():  # the tensor's device made current
         with torch.cuda.device(dev):
             return sparse_attn_forward_masked(q, k, v, scale=scale, cap=cap, slopes=slopes, causal=causal,
                                               docs_q=docs_q, docs_k=docs_k, prefix=prefix, lengths=lengths,
                                               out=out, out_dtype=out_dtype, lse=lse, workspace=workspace,
                                               status=status, stream=stream)
-    qs, ks = _view(q, torch.bfloat16, "q", dev), _view(k, torch.bfloat16, "k", dev)
-    vs = _view(v, torch.bfloat16, "v", dev)
+    qs, ks = _view(q, _bf16, "q", dev), _view(k, _bf16, "k", dev)
+    vs = _view(v, _bf16, "v", dev)
     if v.shape != k.shape:
         raise ValueError("v must have k's shape")
     n, sl, dq, dk, px, lens, made = _mask_fields(q, k, dev, slopes, docs_q, docs_k, prefix, lengths)
     B, H, Nq, d = shape = q.shape
     if out is None:
-        out = torch.empty_like(q) if out_dtype is q.dtype else torch.empty_like(q, dtype=out_dtype)
+        out = _empty_like(q) if out_dtype is q.dtype else _empty_like(q, dtype=out_dtype)
     elif out.shape != shape:
         raise ValueError("out must have q's shape")
     if out.dtype not in _OUT:
         raise ValueError("out must be bfloat16 or float32")
     if lse is True:
-        lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
+        lse = _empty(shape[:3], dtype=_f32, device=q.device)
     elif lse is False:
         lse = None
     p = _MASKED.pack(B, H, k.shape[1], Nq, k.shape[2], d, 1.0 / math.sqrt(d) if scale is None else scale,
@@ -646,10 +644,10 @@ def sparse_attn_forward_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     st = _c_masked(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                   _flat(lse, torch.float32, "lse", dev, shape[:3]), _flat(status, torch.int32, "status", dev),
+                   _flat(lse, _f32, "lse", dev, shape[:3]), 0 if status is None else _flat(status, _i32, "status", dev),
                    _flat(workspace, torch.uint8, "workspace", dev),
                    0 if workspace is None else workspace.numel(),
-                   _raw_stream(stream, dev, out, lse, workspace, *made))
+                   _current_stream(dev) if stream is None else _raw_stream(stream, dev, out, lse, workspace, *made))
     if st != SA_OK:
         raise SparseAttnError(st, "sparse_attn_forward_masked")
     return out, lse
@@ -670,25 +668,26 @@ def sparse_attn_cache_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tenso
     that wrote lse.  weights None starts from zero; out=weights accumulates in place; entries past
     lengths[b] stay as they were (zero when there were none)."""
     dev = q.get_device()
-    if _elsewhere(dev):
+    if dev >= 0 and dev != _current_device():  # the tensor's device made current
         with torch.cuda.device(dev):
             return sparse_attn_cache_weights(q, k, lse, weights, decay=decay, scale=scale, cap=cap,
                                              slopes=slopes, causal=causal, docs_q=docs_q, docs_k=docs_k,
                                              prefix=prefix, lengths=lengths, out=out, status=status,
                                              stream=stream)
-    qs, ks = _view(q, torch.bfloat16, "q", dev), _view(k, torch.bfloat16, "k", dev)
+    qs, ks = _view(q, _bf16, "q", dev), _view(k, _bf16, "k", dev)
     n, sl, dq, dk, px, lens, made = _mask_fields(q, k, dev, slopes, docs_q, docs_k, prefix, lengths)
     B, H, Nq, d = q.shape
     shape = k.shape[:3]
     if out is None:
         make = torch.zeros if weights is None and lengths is not None else torch.empty
-        out = make(shape, dtype=torch.float32, device=q.device)
+        out = make(shape, dtype=_f32, device=q.device)
     p = _MASKED.pack(B, H, shape[1], Nq, shape[2], d, 1.0 / math.sqrt(d) if scale is None else scale, 0,
                      *qs, *ks, 0, 0, 0, 0, 0, 0, cap, sl, causal, n, dq, dk, px, lens)
-    st = _c_weights(p, q.data_ptr(), k.data_ptr(), _flat(lse, torch.float32, "lse", dev, (B, H, Nq)),
-                    _flat(weights, torch.float32, "weights", dev, shape),
-                    _flat(out, torch.float32, "out", dev, shape), 0.0 if weights is None else decay,
-                    _flat(status, torch.int32, "status", dev), _raw_stream(stream, dev, out, *made))
+    st = _c_weights(p, q.data_ptr(), k.data_ptr(), _flat(lse, _f32, "lse", dev, (B, H, Nq)),
+                    _flat(weights, _f32, "weights", dev, shape),
+                    _flat(out, _f32, "out", dev, shape), 0.0 if weights is None else decay,
+                    0 if status is None else _flat(status, _i32, "status", dev),
+                    _current_stream(dev) if stream is None else _raw_stream(stream, dev, out, *made))
     if st != SA_OK:
         raise SparseAttnError(st, "sparse_attn_cache_weights")
     return out
@@ -706,7 +705,7 @@ def sparse_attn_cache_evict(weights: torch.Tensor, k: torch.Tensor | None, v: to
     order; behind a shorter one kept is -1 and the rows of `out` = (k, v, weights) are left as they
     were (zero when out is not given)."""
     dev = weights.get_device()
-    if _elsewhere(dev):
+    if dev >= 0 and dev != _current_device():  # the tensor's device made current
         with torch.cuda.device(dev):
             return sparse_attn_cache_evict(weights, k, v, budget, sink=sink, recent=recent, lengths=lengths,
                                            out=out, kept=kept, stream=stream)
@@ -717,12 +716,12 @@ def sparse_attn_cache_evict(weights: torch.Tensor, k: torch.Tensor | None, v: to
         raise ValueError("k and v come together")
     if budget < 1:
         raise ValueError("budget must be at least 1")
-    w = _flat(weights, torch.float32, "weights", dev)
-    lens = _flat(lengths, torch.int32, "lengths", dev, (B,))
+    w = _flat(weights, _f32, "weights", dev)
+    lens = _flat(lengths, _i32, "lengths", dev, (B,))
     d = 128
     strides = (0,) * 12
     if k is not None:
-        ks, vs = _view(k, torch.bfloat16, "k", dev), _view(v, torch.bfloat16, "v", dev)
+        ks, vs = _view(k, _bf16, "k", dev), _view(v, _bf16, "v", dev)
         d = k.shape[3]
         if k.shape != v.shape or k.shape[:3] != weights.shape:
             raise ValueError("k and v must be [B, Hk, Nk, d] with weights' B, Hk and Nk")
@@ -730,22 +729,22 @@ def sparse_attn_cache_evict(weights: torch.Tensor, k: torch.Tensor | None, v: to
         make = torch.empty if lengths is None and budget <= N else torch.zeros
         ko = vo = None
         if k is not None:
-            ko, vo = (make((B, H, budget, d), dtype=torch.bfloat16, device=weights.device) for _ in range(2))
-        wo = make((B, H, budget), dtype=torch.float32, device=weights.device)
+            ko, vo = (make((B, H, budget, d), dtype=_bf16, device=weights.device) for _ in range(2))
+        wo = make((B, H, budget), dtype=_f32, device=weights.device)
     else:
         ko, vo, wo = out
     if kept is None:
-        kept = torch.empty((B, H, budget), dtype=torch.int32, device=weights.device)
+        kept = torch.empty((B, H, budget), dtype=_i32, device=weights.device)
     kp = vp = kop = vop = 0
     if k is not None:
         if ko.shape != (B, H, budget, d) or vo.shape != ko.shape:
             raise ValueError("out must hold k and v as [B, Hk, budget, d]")
-        strides = (*ks, *vs, *_view(ko, torch.bfloat16, "out", dev), *_view(vo, torch.bfloat16, "out", dev))
+        strides = (*ks, *vs, *_view(ko, _bf16, "out", dev), *_view(vo, _bf16, "out", dev))
         kp, vp, kop, vop = k.data_ptr(), v.data_ptr(), ko.data_ptr(), vo.data_ptr()
     st = _c_evict(_EVICT.pack(B, H, N, d, budget, sink, recent, lens, *strides), w, kp, vp,
-                  _flat(kept, torch.int32, "kept", dev, (B, H, budget)), kop, vop,
-                  _flat(wo, torch.float32, "out", dev, (B, H, budget)),
-                  _raw_stream(stream, dev, ko, vo, wo, kept))
+                  _flat(kept, _i32, "kept", dev, (B, H, budget)), kop, vop,
+                  _flat(wo, _f32, "out", dev, (B, H, budget)),
+                  _current_stream(dev) if stream is None else _raw_stream(stream, dev, ko, vo, wo, kept))
     if st != SA_OK:
         raise SparseAttnError(st, "sparse_attn_cache_evict")
     return kept, ko, vo, wo

@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdlib>
 #include <numeric>
+#include <utility>
 
 #include "sa_internal.h"
 #include "sparse_attn.h"
@@ -134,6 +135,9 @@ sa_status check_masked(const sa_masked* p, sa::MaskedArgs* a) {
   a->cap_p1 = static_cast<float>(kTanh1 * s * log2e * r2);
   a->cap_p2 = static_cast<float>(kTanh2 * s * log2e * r2 * r2);
   a->cap_p3 = static_cast<float>(kTanh3 * s * log2e * r2 * r2 * r2);
+  // a scale or a ratio to the cap that fp32 cannot hold would turn scores into NaN
+  if (!std::isfinite(a->scale_log2) || !std::isfinite(a->cap_log2) || !std::isfinite(a->cap_k1))
+    return SA_ERR_INVALID_ARG;
   a->cap_limit = r2 > 0.0 && r2 < 1e6 ? static_cast<float>(0.16 / r2) : -1.f;
   a->total_rows = int64_t(p->B) * p->Hq * p->Nq;
   a->qn = a->unit_rows = a->row_blocks = a->group = a->splits = 1;
@@ -186,9 +190,24 @@ sa_status sparse_attn_forward_masked(const sa_masked* p, const void* q, const vo
       !check_view(o, &a.os, p->B, p->Hq, p->Nq, p->d, a.out_fp32 ? 4 : 2, true, false, &no))
     return SA_ERR_INVALID_ARG;
   if (!aligned(lse, 4) || !aligned(dev_status, 4)) return SA_ERR_INVALID_ARG;
+  // Outputs may not share elements with inputs or each other; o may be q's view
+  // (a row of q is read only ahead of the row of o that takes its place).
+  const int esz = a.out_fp32 ? 4 : 2;
+  const int64_t H = p->Hq, N = std::max(p->Nq, p->Nk);
+  auto apart = [&](const void* x, const sa_strides& xs, uint64_t nx) {
+    return esz == 2 ? !views_overlap(o, a.os, no, x, xs, nx, p->B, H, N, p->d, 2) : !overlap(o, no, x, nx);
+  };
+  const bool same = o == q && esz == 2 && a.os.b == a.qs.b && a.os.h == a.qs.h && a.os.n == a.qs.n;
+  if ((!same && !apart(q, a.qs, nq)) || !apart(k, a.ks, nk) || !apart(v, a.vs, nv)) return SA_ERR_INVALID_ARG;
+  const uint64_t nl = lse ? uint64_t(a.total_rows) * 4 : 0;
+  if (nl && (overlap(lse, nl, q, nq) || overlap(lse, nl, k, nk) || overlap(lse, nl, v, nv) || overlap(lse, nl, o, no)))
+    return SA_ERR_INVALID_ARG;
   sa::masked_plan(&a);
   const size_t need = masked_workspace(a);
   if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return SA_ERR_INVALID_ARG;
+  if (need)
+    for (const auto& x : {std::pair<const void*, uint64_t>{q, nq}, {k, nk}, {v, nv}, {o, no}, {lse, nl}})
+      if (x.second && overlap(workspace, need, x.first, x.second)) return SA_ERR_INVALID_ARG;
   int sms = 0;
   if ((st = device_info(&sms)) != SA_OK) return st;
   if (!in_device_allocation(q, nq) || !in_device_allocation(k, nk) || !in_device_allocation(v, nv) ||
