@@ -451,9 +451,9 @@ typedef struct {
 /*
  * Rotates x0 (H0 heads) into y0 and, when H1 > 0, x1 (H1 heads) into y1 with
  * the same positions (queries and keys of a layer in one launch).  y may be
- * the same view as its x (in place); otherwise they must not overlap.  Views
- * of the two pairs may interleave in one buffer but must not share elements.
- * Inputs may repeat a dimension.
+ * the same view as its x (in place); otherwise no y shares elements with another
+ * tensor of the call.  Views of the same strides may interleave in one buffer
+ * (the heads of a fused projection).  Inputs may repeat a dimension.
  */
 sa_status sparse_attn_rope(const sa_rope* rope, int32_t H0, const void* x0, const sa_strides* x0_strides,
                            void* y0, const sa_strides* y0_strides, int32_t H1, const void* x1,
@@ -487,7 +487,8 @@ sa_status sparse_attn_rope(const sa_rope* rope, int32_t H0, const void* x0, cons
  *
  * q, k, v bf16; o bf16 or fp32 by out_dtype; P is rounded to bf16 for the
  * second product (o is normalised by the sum of the rounded values), all sums
- * are fp32.  Hq / Hkv <= 128.  Keys and values past a row's document
+ * are fp32.  Hq / Hkv <= 128; B Hq <= 2^24, Hq / Hkv Nq < 2^32 and B Hkv times
+ * the tiles of 128 / (Hq / Hkv) queries <= 2^30.  Keys and values past a row's document
  * never reach it, whatever they hold; a NaN or an infinite V row inside the
  * document may reach other rows of the same document that do not see it.
  * Few rows split the keys over the GPU: the workspace (256-byte aligned, may
@@ -512,7 +513,8 @@ typedef struct {
 size_t sparse_attn_forward_masked_workspace_size(const sa_masked* problem);
 
 /* lse (fp32 [B, Hq, Nq]) and dev_status are nullable.  o may be q's own view
- * (bf16); otherwise no output or workspace may share memory with another argument. */
+ * (bf16), also in one buffer with k and v when all have the same strides; otherwise
+ * no output or workspace may share memory with another argument. */
 sa_status sparse_attn_forward_masked(const sa_masked* problem, const void* q, const void* k, const void* v,
                                      void* o, float* lse, int32_t* dev_status, void* workspace,
                                      size_t workspace_bytes, sa_stream_t stream);
@@ -543,7 +545,8 @@ sa_status sparse_attn_cache_weights(const sa_masked* problem, const void* q, con
  *                the last are left as they were); k, v, k_out, v_out are all
  *                NULL to select only
  *   weights_out  fp32 [B, Hkv, budget] (likewise), nullable
- * No output may overlap an input.  sink + recent <= budget; B*Hkv <= 65535.
+ * No output may overlap an input.  sink + recent <= budget; B*Hkv <= 65535; Nk,
+ * budget <= 2^30.
  * k and v may repeat a dimension.
  */
 typedef struct {

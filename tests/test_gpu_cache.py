@@ -123,6 +123,35 @@ def test_weights_repeat_and_stream():
     assert torch.equal(other, got)
 
 
+def test_weights_of_many_documents():
+    """Units find their run of Q tiles among many; empty documents, rows of none, prefixes."""
+    g = np.random.default_rng(3)
+    nq, nk = g.integers(0, 120, 60), g.integers(0, 90, 60)
+    docs_q, docs_k = ([int(x) for x in np.concatenate([[5], 5 + np.cumsum(n)])] for n in (nq, nk))
+    case(2, 1, docs_q[-1] + 7, docs_k[-1] + 300, 64, seed=10, causal=9, docs_q=docs_q, docs_k=docs_k,
+         prefix=[int(x) for x in g.integers(0, 40, 60)])
+
+
+def test_results_made_on_another_stream():
+    """What a call on a stream makes and fills is ordered with that stream, not with a busy current one."""
+    from video_dit_sparse_gb300 import binding as sa
+    q, k, v, lse, w, got, dev = case(2, 2, 40, 400, 64, seed=11, lengths=[400, 130, 0])
+    docs = dict(docs_q=torch.tensor([0, 40], dtype=torch.int32, device="cuda"),
+                docs_k=torch.tensor([0, 300], dtype=torch.int32, device="cuda"))
+    want = sa.sparse_attn_cache_weights(q, k, lse, **dev)
+    want_o, want_l = sa.sparse_attn_forward_masked(q, k, v, **docs)
+    want_e = sa.sparse_attn_cache_evict(w, k, v, 200, sink=4, recent=8, lengths=dev["lengths"])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    mine = sa.sparse_attn_cache_weights(q, k, lse, stream=s, **dev)
+    o, l = sa.sparse_attn_forward_masked(q, k, v, stream=s, **docs)
+    e = sa.sparse_attn_cache_evict(w, k, v, 200, sink=4, recent=8, lengths=dev["lengths"], stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(mine, want) and torch.equal(o, want_o) and torch.equal(l, want_l)
+    assert all(torch.equal(a, b) for a, b in zip(e, want_e))
+
+
 # ---------------------------------------------------------------- eviction
 
 def evict_case(w, n_of, budget, sink, recent, d=64, layout="bhnd"):

@@ -269,5 +269,11 @@ def test_output_over_the_queries():
         want, wl = sa.sparse_attn_forward_masked(q, k, v, causal=1)
         o, lse = sa.sparse_attn_forward_masked(q, k, v, causal=1, out=q)
         assert o is q and torch.equal(o, want) and torch.equal(lse, wl)
+    qkv = tensors(2, 16, 1, 515, 1, 64, seed=27)[0].transpose(1, 2).contiguous().transpose(1, 2)
+    q, k, v = qkv[:, :12], qkv[:, 12:14], qkv[:, 14:]
+    want, _ = sa.sparse_attn_forward_masked(q, k, v, causal=1)
+    rest = qkv[:, 12:].clone()
+    sa.sparse_attn_forward_masked(q, k, v, causal=1, out=q)
+    assert torch.equal(q, want) and torch.equal(qkv[:, 12:], rest)
     with pytest.raises(sa.SparseAttnError):
         sa.sparse_attn_forward_masked(k, k, v, out=k)

@@ -105,6 +105,16 @@ def test_in_place_into_a_cache_and_interleaved_views():
     assert bool((cache[:, :, :80] == 7).all()) and bool((cache[:, :, 120:] == 7).all())
 
 
+def test_in_place_on_a_fused_projection():
+    from video_dit_sparse_gb300 import binding as sa
+    qkv = torch.randn(2, 40, 12 + 2 + 2, 64, device="cuda").to(torch.bfloat16)
+    src = qkv.clone()
+    q, k = (qkv.transpose(1, 2)[:, a:b] for a, b in ((0, 12), (12, 14)))
+    want = sa.sparse_attn_rope(src.transpose(1, 2)[:, :14], axes=(24, 20, 20), grid=(2, 4, 5))
+    sa.sparse_attn_rope(q, k, axes=(24, 20, 20), grid=(2, 4, 5), out=(q, k))
+    assert torch.equal(qkv.transpose(1, 2)[:, :14], want) and torch.equal(qkv[:, :, 14:], src[:, :, 14:])
+
+
 def test_elements_outside_the_rotation_and_non_finite_rows():
     from video_dit_sparse_gb300 import binding as sa
     for pairing in ("interleaved", "half"):

@@ -41,7 +41,8 @@ def test_forward_masked_refusals(sa):
     assert forward(sa, None) == INVALID
     for bad in (dict(B=0), dict(Hq=0), dict(Hkv=0), dict(Nq=0), dict(Nk=0), dict(d=0), dict(Hq=3), dict(scale=0.0),
                 dict(scale=float("nan")), dict(cap=-1.0), dict(cap=float("inf")), dict(causal=-1), dict(ndocs=-1),
-                dict(out_dtype=5), dict(scale=3e38), dict(cap=1e-38, scale=1e5), dict(ndocs=2), dict(ndocs=2, docs_q=A16), dict(docs_q=A16), dict(prefix=A16),
+                dict(out_dtype=5), dict(scale=3e38), dict(cap=1e-38, scale=1e5), dict(ndocs=2),
+                dict(ndocs=2, docs_q=A16), dict(docs_q=A16), dict(prefix=A16),
                 dict(ndocs=1, docs_q=A16, docs_k=A16, lengths=A16), dict(slopes=A16 + 2), dict(lengths=A16 + 1)):
         assert forward(sa, masked(sa, **bad)) == INVALID, bad
     for bad in (dict(d=96), dict(Nk=2 ** 30 + 1), dict(Nq=2 ** 30 + 1), dict(B=2 ** 23)):
@@ -50,7 +51,8 @@ def test_forward_masked_refusals(sa):
     for name in ("q", "k", "v", "o"):
         assert forward(sa, ok, **{name: None}) == INVALID
         assert forward(sa, ok, **{name: MIS}) == INVALID
-    assert forward(sa, masked(sa, Hq=258, q=sa.sa_strides(258 * 1024, 1024, 128), o=sa.sa_strides(258 * 1024, 1024, 128))) == UNSUPPORTED
+    wide = sa.sa_strides(258 * 1024, 1024, 128)
+    assert forward(sa, masked(sa, Hq=258, q=wide, o=wide)) == UNSUPPORTED
     assert forward(sa, ok, lse=LSE + 2) == INVALID
     if not torch.cuda.is_available():  # what passes the checks on arguments ends at the device's
         assert forward(sa, ok) not in (0, INVALID) and forward(sa, ok, o=Q) not in (0, INVALID)
@@ -72,6 +74,9 @@ def test_forward_masked_refusals(sa):
     assert forward(sa, few, nws=need - 1) == INVALID
     assert forward(sa, few, ws=WS + 16) == INVALID and forward(sa, few, ws=K) == INVALID
     assert sa.lib.sparse_attn_forward_masked_workspace_size(None) == 0
+    for big in (dict(Hq=2 ** 24, Hkv=2 ** 24, Nq=2 ** 30), dict(Hq=2 ** 22, Hkv=2 ** 22, Nq=2 ** 18 + 1),
+                dict(Hq=128, Hkv=1, Nq=2 ** 30, B=2)):  # products of these do not fit 32 bits
+        assert sa.lib.sparse_attn_forward_masked_workspace_size(masked(sa, Nk=1, **big)) == 0, big
     assert sa.lib.sparse_attn_forward_masked_workspace_size(masked(sa, d=96)) == 0
 
 
@@ -110,7 +115,7 @@ def test_cache_evict_refusals(sa):
                 dict(sink=2 ** 31 - 1, recent=2 ** 31 - 1), dict(lengths=A16 + 2), dict(k=S(1, 1, 1)),
                 dict(k_out=S(16 * 256, 16 * 128, 64)), dict(v_out=S(0, 0, 128))):
         assert call(prob(**bad)) == INVALID, bad
-    for bad in (dict(d=96), dict(B=65536, Hkv=1)):
+    for bad in (dict(d=96), dict(B=65536, Hkv=1), dict(Nk=2 ** 30 + 1), dict(budget=2 ** 30 + 1)):
         assert call(prob(**bad)) == UNSUPPORTED, bad
     ok = prob()
     for bad in (dict(w=None), dict(kept=None), dict(k=None), dict(vo=None), dict(ko=at["k"]), dict(vo=at["v"] + 4096),
@@ -137,8 +142,8 @@ def test_rope_refusals(sa):
         return sa.lib.sparse_attn_rope(p, H, x, xs, y, ys, H1, x1, x1s, y1, y1s, None)
     assert call(None) == INVALID
     nan = (ctypes.c_double * 32)(*([float("nan")] * 32))
-    for bad in (dict(B=0), dict(N=0), dict(d=0), dict(axes=0), dict(axes=4), dict(pairing=2), dict(dtype=9), dict(theta=0.0),
-                dict(theta=float("inf")), dict(dims=(3, 20, 20)), dict(dims=(-2, 20, 20)), dict(dims=(24, 24, 24)),
+    for bad in (dict(B=0), dict(N=0), dict(d=0), dict(axes=0), dict(axes=4), dict(pairing=2), dict(dtype=9),
+                dict(theta=0.0), dict(theta=float("inf")), dict(dims=(3, 20, 20)), dict(dims=(-2, 20, 20)), dict(dims=(24, 24, 24)),
                 dict(dims=(0, 0, 0)), dict(N=31), dict(axes=2), dict(voxel_order=1), dict(positions=A16 + 2),
                 dict(positions=A16, positions_b=-1), dict(positions=A16, positions_b=89), dict(inv_freq=nan),
                 dict(grid=sa.sa_voxel_grid(30, 2 ** 31 - 1, 1, 0, 0, 0))):
@@ -159,6 +164,29 @@ def test_rope_refusals(sa):
                 dict(H1=2), dict(H1=2, x1=X, x1s=st, y1=None, y1s=st), dict(y=X + 3840), dict(ys=S(1920, 960, 64)),
                 dict(y=X, ys=S(3840, 64, 128))):
         assert call(ok, **bad) == INVALID, bad
+
+
+def test_views_of_one_buffer(sa):
+    """Heads of a fused projection [B, N, Hq + 2 Hkv, d]: views that interleave pass the checks, views that meet do not."""
+    Hq, Hk, N, d = 12, 2, 40, 128
+    st = sa.sa_strides(N * (Hq + 2 * Hk) * d, d, (Hq + 2 * Hk) * d)
+    q, k, v = Q, Q + Hq * d * 2, Q + (Hq + Hk) * d * 2
+    p = masked(sa, B=2, Hq=Hq, Hkv=Hk, Nq=N, Nk=N, q=st, k=st, v=st, o=st)
+    rope = sa.sa_rope(2, N, d, 3)
+    rope.axis_dim[0], rope.theta, rope.grid = 64, 1e4, sa.sa_voxel_grid(1, 5, 8, 0, 0, 0)
+
+    def turn(x1, y1, H1=Hk, x0=q, y0=q):
+        return sa.lib.sparse_attn_rope(rope, Hq, x0, st, y0, st, H1, x1, st, y1, st, None)
+    if not torch.cuda.is_available():
+        assert forward(sa, p, q, k, v, o=q) not in (0, INVALID)
+        assert turn(k, k) not in (0, INVALID) and turn(v, k) not in (0, INVALID)
+        assert turn(k, k, H1=1) not in (0, INVALID)
+    row = d * 2
+    for o in (k, v, q + row, q - row, k - row, v + row):
+        assert forward(sa, p, q, k, v, o=o) == INVALID
+    for x1, y1 in ((k, q), (q, k), (k - row, k - row), (v + row, v + row), (q, q)):
+        assert turn(x1, y1) == INVALID
+    assert turn(v, v, H1=3) == INVALID  # three heads from v's reach the next token's q
 
 
 def test_binding_refusals(sa):

@@ -481,13 +481,22 @@ def _flat(t, dtype, name, dev, shape=None) -> int:
     return t.data_ptr()
 
 
-def _raw_stream(stream, dev: int, *made) -> int:
-    """The handle of a stream other than the current one; tensors made for the call are recorded
-    there."""
-    for t in made:
-        if t is not None:
-            t.record_stream(stream)
-    return stream.cuda_stream
+def _elsewhere(dev: int, stream, call, *args, **options):
+    """The call with the tensors' device current and, when one is given, on `stream`: what the call
+    makes and fills is made there, and its results are not reused while the caller's stream may
+    still read them."""
+    if stream is None:
+        with torch.cuda.device(dev):
+            return call(*args, **options)
+    if stream.device.index != dev:
+        raise ValueError("stream must be on the first tensor's device")
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        made = call(*args, **options)
+        for t in made if isinstance(made, tuple) else (made,):
+            if t is not None:
+                t.record_stream(here)
+    return made
 
 
 def sparse_attn_rope(q: torch.Tensor, k: torch.Tensor | None = None, *, axes=(44, 42, 42),
@@ -502,11 +511,10 @@ def sparse_attn_rope(q: torch.Tensor, k: torch.Tensor | None = None, *, axes=(44
     `offset`.  inv_freq: r/2 frequencies (radians per position) instead of theta's.  inverse rotates
     back, which is also the gradient.  out: the output (or a pair of them); it may be the input."""
     dtype, dev = q.dtype, q.get_device()
-    if dev >= 0 and dev != _current_device():  # the tensor's device made current
-        with torch.cuda.device(dev):
-            return sparse_attn_rope(q, k, axes=axes, theta=theta, inv_freq=inv_freq, pairing=pairing,
-                                    grid=grid, voxel=voxel, offset=offset, positions=positions,
-                                    inverse=inverse, out=out, stream=stream)
+    if dev >= 0 and (stream is not None or dev != _current_device()):
+        return _elsewhere(dev, stream, sparse_attn_rope, q, k, axes=axes, theta=theta, inv_freq=inv_freq,
+                          pairing=pairing, grid=grid, voxel=voxel, offset=offset, positions=positions,
+                          inverse=inverse, out=out)
     if dtype not in _OUT:
         raise ValueError("q must be bfloat16 or float32")
     qs = _view(q, dtype, "q", dev)
@@ -552,21 +560,21 @@ def sparse_attn_rope(q: torch.Tensor, k: torch.Tensor | None = None, *, axes=(44
     z = None
     if k is None:
         st = _c_rope(p, H, q.data_ptr(), _STRIDES.pack(*qs), y.data_ptr(), ys, 0, None, None, None, None,
-                     _current_stream(dev) if stream is None else _raw_stream(stream, dev, y))
+                     _current_stream(dev))
     else:
         z = _empty_like(k) if ok is None else ok
         if z.shape != k.shape:
             raise ValueError("out of k must have k's shape")
         st = _c_rope(p, H, q.data_ptr(), _STRIDES.pack(*qs), y.data_ptr(), ys, k.shape[1], k.data_ptr(), ks,
                      z.data_ptr(), _STRIDES.pack(*_view(z, dtype, "out of k", dev)),
-                     _current_stream(dev) if stream is None else _raw_stream(stream, dev, y, z))
+                     _current_stream(dev))
     if st != SA_OK:
         raise SparseAttnError(st, "sparse_attn_rope")
     return y if k is None else (y, z)
 
 
 def _mask_fields(q, k, dev, slopes, docs_q, docs_k, prefix, lengths):
-    """The mask's tables: (number of documents, their addresses, tensors to keep)."""
+    """The mask's tables: (number of documents, their addresses, tensors to keep until the launch)."""
     B, H, _, d = q.shape
     kb, kh, _, kd = k.shape
     if kb != B or kd != d or not kh or H % kh:
@@ -615,12 +623,11 @@ def sparse_attn_forward_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     frame when `causal` (tokens per frame, 1: per token), and the document's first `prefix` keys.  A
     document's rows are its last positions, so one new token over a cache is Nq = 1 with lengths."""
     dev = q.get_device()
-    if dev >= 0 and dev != _current_device():  # the tensor's device made current
-        with torch.cuda.device(dev):
-            return sparse_attn_forward_masked(q, k, v, scale=scale, cap=cap, slopes=slopes, causal=causal,
-                                              docs_q=docs_q, docs_k=docs_k, prefix=prefix, lengths=lengths,
-                                              out=out, out_dtype=out_dtype, lse=lse, workspace=workspace,
-                                              status=status, stream=stream)
+    if dev >= 0 and (stream is not None or dev != _current_device()):
+        return _elsewhere(dev, stream, sparse_attn_forward_masked, q, k, v, scale=scale, cap=cap,
+                          slopes=slopes, causal=causal, docs_q=docs_q, docs_k=docs_k, prefix=prefix,
+                          lengths=lengths, out=out, out_dtype=out_dtype, lse=lse, workspace=workspace,
+                          status=status)
     qs, ks = _view(q, _bf16, "q", dev), _view(k, _bf16, "k", dev)
     vs = _view(v, _bf16, "v", dev)
     if v.shape != k.shape:
@@ -647,7 +654,7 @@ def sparse_attn_forward_masked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
                    _flat(lse, _f32, "lse", dev, shape[:3]), 0 if status is None else _flat(status, _i32, "status", dev),
                    _flat(workspace, torch.uint8, "workspace", dev),
                    0 if workspace is None else workspace.numel(),
-                   _current_stream(dev) if stream is None else _raw_stream(stream, dev, out, lse, workspace, *made))
+                   _current_stream(dev))
     if st != SA_OK:
         raise SparseAttnError(st, "sparse_attn_forward_masked")
     return out, lse
@@ -668,12 +675,10 @@ def sparse_attn_cache_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tenso
     that wrote lse.  weights None starts from zero; out=weights accumulates in place; entries past
     lengths[b] stay as they were (zero when there were none)."""
     dev = q.get_device()
-    if dev >= 0 and dev != _current_device():  # the tensor's device made current
-        with torch.cuda.device(dev):
-            return sparse_attn_cache_weights(q, k, lse, weights, decay=decay, scale=scale, cap=cap,
-                                             slopes=slopes, causal=causal, docs_q=docs_q, docs_k=docs_k,
-                                             prefix=prefix, lengths=lengths, out=out, status=status,
-                                             stream=stream)
+    if dev >= 0 and (stream is not None or dev != _current_device()):
+        return _elsewhere(dev, stream, sparse_attn_cache_weights, q, k, lse, weights, decay=decay,
+                          scale=scale, cap=cap, slopes=slopes, causal=causal, docs_q=docs_q,
+                          docs_k=docs_k, prefix=prefix, lengths=lengths, out=out, status=status)
     qs, ks = _view(q, _bf16, "q", dev), _view(k, _bf16, "k", dev)
     n, sl, dq, dk, px, lens, made = _mask_fields(q, k, dev, slopes, docs_q, docs_k, prefix, lengths)
     B, H, Nq, d = q.shape
@@ -687,7 +692,7 @@ def sparse_attn_cache_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tenso
                     _flat(weights, _f32, "weights", dev, shape),
                     _flat(out, _f32, "out", dev, shape), 0.0 if weights is None else decay,
                     0 if status is None else _flat(status, _i32, "status", dev),
-                    _current_stream(dev) if stream is None else _raw_stream(stream, dev, out, *made))
+                    _current_stream(dev))
     if st != SA_OK:
         raise SparseAttnError(st, "sparse_attn_cache_weights")
     return out
@@ -705,10 +710,9 @@ def sparse_attn_cache_evict(weights: torch.Tensor, k: torch.Tensor | None, v: to
     order; behind a shorter one kept is -1 and the rows of `out` = (k, v, weights) are left as they
     were (zero when out is not given)."""
     dev = weights.get_device()
-    if dev >= 0 and dev != _current_device():  # the tensor's device made current
-        with torch.cuda.device(dev):
-            return sparse_attn_cache_evict(weights, k, v, budget, sink=sink, recent=recent, lengths=lengths,
-                                           out=out, kept=kept, stream=stream)
+    if dev >= 0 and (stream is not None or dev != _current_device()):
+        return _elsewhere(dev, stream, sparse_attn_cache_evict, weights, k, v, budget, sink=sink,
+                          recent=recent, lengths=lengths, out=out, kept=kept)
     if weights.dim() != 3 or dev < 0:
         raise ValueError("weights must be a CUDA tensor [B, Hk, Nk]")
     B, H, N = weights.shape
@@ -744,7 +748,7 @@ def sparse_attn_cache_evict(weights: torch.Tensor, k: torch.Tensor | None, v: to
     st = _c_evict(_EVICT.pack(B, H, N, d, budget, sink, recent, lens, *strides), w, kp, vp,
                   _flat(kept, _i32, "kept", dev, (B, H, budget)), kop, vop,
                   _flat(wo, _f32, "out", dev, (B, H, budget)),
-                  _current_stream(dev) if stream is None else _raw_stream(stream, dev, ko, vo, wo, kept))
+                  _current_stream(dev))
     if st != SA_OK:
         raise SparseAttnError(st, "sparse_attn_cache_evict")
     return kept, ko, vo, wo

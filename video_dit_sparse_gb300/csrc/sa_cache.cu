@@ -82,11 +82,23 @@ __device__ __forceinline__ WUnit unit_at(const MaskedArgs& a, const WPlan& p, in
   x.len = m.len ? clamp_int(__ldg(m.len + x.b), 0, m.Nk) : m.Nk;
   x.t0 = 0;
   x.t1 = x.k0 < x.len ? p.qtiles : 0;
-  if (m.causal || m.nd) {
-    while (x.t0 < x.t1 && row_span(m, x.b, min((x.t0 + 1) * p.qn, m.Nq) - 1).hi <= x.k0) ++x.t0;
-    if (m.nd)
-      while (x.t1 > x.t0 && row_span(m, x.b, (x.t1 - 1) * p.qn).lo >= x.k0 + kUnitKeys) --x.t1;
-  }
+  // Both ends of the rows' spans never decrease, so the tiles form a run.
+  if (m.causal || m.nd)
+    for (int top = x.t1; x.t0 < top;) {  // the first tile that sees a key of the unit or behind it
+      const int mid = (x.t0 + top) >> 1;
+      if (row_span(m, x.b, min((mid + 1) * p.qn, m.Nq) - 1).hi <= x.k0)
+        x.t0 = mid + 1;
+      else
+        top = mid;
+    }
+  if (m.nd)
+    for (int low = x.t0; low < x.t1;) {  // the first one that sees only keys behind the unit
+      const int mid = (low + x.t1) >> 1;
+      if (row_span(m, x.b, mid * p.qn).lo >= x.k0 + kUnitKeys)
+        x.t1 = mid;
+      else
+        low = mid + 1;
+    }
   const int n = x.t1 - x.t0;
   x.t1 = x.t0 + n * (rank + 1) / p.parts;
   x.t0 += n * rank / p.parts;
@@ -100,8 +112,8 @@ __device__ __forceinline__ WUnit unit_at(const MaskedArgs& a, const WPlan& p, in
 
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(WCfg::kThreads, 1)
-    sa_cache_weights_kernel(const __grid_constant__ WeightArgs wa, const __grid_constant__ WPlan p, const __grid_constant__ CUtensorMap tm_q,
-                            const __grid_constant__ CUtensorMap tm_k) {
+    sa_cache_weights_kernel(const __grid_constant__ WeightArgs wa, const __grid_constant__ WPlan p,
+                            const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k) {
   const MaskedArgs& a = wa.m;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -164,7 +176,8 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
     // The set's thread tid holds column col0 + tid: query tile * qn + qo of a head.
     const int cr = col0 + tid;
     const bool has = tid < H && cr < p.rows;
-    const int qo = has ? cr / a.R : INT_MAX / 2, off = has ? (cr % a.R) * a.Nq + qo : 0;
+    const int qo = has ? cr / a.R : INT_MAX / 2;
+    const uint32_t off = has ? uint32_t(cr % a.R) * uint32_t(a.Nq) + uint32_t(qo) : 0;
     const float sl = a.scale_log2;
     const bool docs = a.mask.nd > 0;  // (a length alone only decides which keys are written)
     uint32_t it = 0, hn = 0;  // Q tiles, and sums handed on so far
@@ -540,7 +553,7 @@ done:
 
 template <int D, bool CAP, bool BIAS>
 static cudaError_t launch_w(const WeightArgs& a, const WPlan& p, const CUtensorMap& tq, const CUtensorMap& tk,
-                            int num_sms, cudaStream_t st) {
+                            cudaStream_t st) {
   auto kern = sa_cache_weights_kernel<D, CAP, BIAS>;
   int smem = 1024 + p.kst * p.ktile + p.qst * p.kqbytes + 2 * 4 * 128 * 4 + 2 * 4 * 4 * 4 + 4 * 128 * 4 +
              static_cast<int>(sizeof(WBars)) + 64;
@@ -595,11 +608,11 @@ cudaError_t launch_cache_weights(const WeightArgs& a, int num_sms, cudaStream_t 
     return cudaErrorInvalidValue;
   const bool cap = m.cap_log2 > 0.f, bias = m.slopes != nullptr;
   if (m.d == 128) {
-    if (cap) return bias ? launch_w<128, true, true>(a, p, tq, tk, num_sms, st) : launch_w<128, true, false>(a, p, tq, tk, num_sms, st);
-    return bias ? launch_w<128, false, true>(a, p, tq, tk, num_sms, st) : launch_w<128, false, false>(a, p, tq, tk, num_sms, st);
+    if (cap) return bias ? launch_w<128, true, true>(a, p, tq, tk, st) : launch_w<128, true, false>(a, p, tq, tk, st);
+    return bias ? launch_w<128, false, true>(a, p, tq, tk, st) : launch_w<128, false, false>(a, p, tq, tk, st);
   }
-  if (cap) return bias ? launch_w<64, true, true>(a, p, tq, tk, num_sms, st) : launch_w<64, true, false>(a, p, tq, tk, num_sms, st);
-  return bias ? launch_w<64, false, true>(a, p, tq, tk, num_sms, st) : launch_w<64, false, false>(a, p, tq, tk, num_sms, st);
+  if (cap) return bias ? launch_w<64, true, true>(a, p, tq, tk, st) : launch_w<64, true, false>(a, p, tq, tk, st);
+  return bias ? launch_w<64, false, true>(a, p, tq, tk, st) : launch_w<64, false, false>(a, p, tq, tk, st);
 }
 
 // ---------------------------------------------------------------- eviction

@@ -63,31 +63,46 @@ bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
   return x < y + nb && y < x + na;
 }
 
-// Whether two views of the same shape (checked by check_view) may share an
-// element.  With the same strides they may interleave in one buffer: rows that
-// follow one another make blocks, and blocks start at multiples of the other
-// strides' common divisor g from the view's start, so views whose starts differ by
-// at least a block modulo g, either way round, never meet.
-bool views_overlap(const void* a, const sa_strides& as, uint64_t na, const void* b, const sa_strides& bs,
-                   uint64_t nb, int64_t B, int64_t H, int64_t N, int64_t d, int esz) {
-  if (!overlap(a, na, b, nb)) return false;
-  if (as.b != bs.b || as.h != bs.h || as.n != bs.n) return true;
+// A checked view: its first element, strides, sizes and extent in bytes.
+struct View {
+  const void* p;
+  sa_strides s;
+  int64_t B, H, N;
+  uint64_t n;
+};
+
+// Whether two views of rows of d elements (checked by check_view) may share an
+// element.  With the same strides they may interleave in one buffer (heads of a
+// fused projection): rows that follow one another make blocks, and blocks start at
+// multiples of the other strides' common divisor g from the view's start, so views
+// whose starts differ modulo g by at least the first one's block one way round and
+// the second one's the other never meet.  A dimension of size one has no stride of
+// its own and takes the other view's.
+bool views_overlap(const View& a, const View& b, int64_t d, int esz) {
+  if (!overlap(a.p, a.n, b.p, b.n)) return false;
   struct Dim {
-    int64_t n, stride;
-  } dims[3] = {{B, as.b}, {H, as.h}, {N, as.n}};
-  std::sort(dims, dims + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
-  int64_t block = d, g = 0;
-  for (const Dim& x : dims) {
-    if (x.n == 1) continue;
-    if (g == 0 && x.stride == block)
-      block *= x.n;
-    else
-      g = std::gcd(g, x.stride);
+    int64_t na, nb, sa, sb;
+  } dims[3] = {{a.B, b.B, a.s.b, b.s.b}, {a.H, b.H, a.s.h, b.s.h}, {a.N, b.N, a.s.n, b.s.n}};
+  for (Dim& x : dims) {
+    if (x.na == 1) x.sa = x.sb;
+    if (x.nb == 1) x.sb = x.sa;
+    if (x.sa != x.sb) return true;
   }
-  const int64_t apart = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a)) / esz;
-  if (g == 0) return std::llabs(apart) < block;
+  std::sort(dims, dims + 3, [](const Dim& x, const Dim& y) { return x.sa < y.sa; });
+  int64_t block_a = d, block_b = d, g = 0;
+  for (const Dim& x : dims) {
+    if (x.na == 1 && x.nb == 1) continue;
+    if (g == 0 && x.sa == block_a && x.sa == block_b) {
+      block_a *= x.na;
+      block_b *= x.nb;
+    } else {
+      g = std::gcd(g, x.sa);
+    }
+  }
+  const int64_t apart = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) / esz;
+  if (g == 0) return apart < block_a && -apart < block_b;
   const int64_t m = ((apart % g) + g) % g;
-  return m < block || g - m < block;
+  return m < block_a || g - m < block_b;
 }
 
 // Shapes and options of sa_masked; fills everything but the tensor pointers.
@@ -106,10 +121,11 @@ sa_status check_masked(const sa_masked* p, sa::MaskedArgs* a) {
     if (!aligned(t, 4)) return SA_ERR_INVALID_ARG;
   if (p->d != 64 && p->d != 128) return SA_ERR_UNSUPPORTED;
   const int64_t R = p->Hq / p->Hkv;
-  // packed rows and key coordinates are 32-bit with room for a tile behind them
   if (R > 128) return SA_ERR_UNSUPPORTED;  // a Q tile holds all of a query's heads
-  if (p->Nq > (1 << 30) || p->Nk > (1 << 30) || R * p->Nq > (int64_t(1) << 40) ||
-      int64_t(p->B) * p->Hq > (1 << 24))
+  // key coordinates and numbers of Q tiles are 32-bit with room for a tile behind them
+  const int64_t heads = int64_t(p->B) * p->Hkv, qn = 128 / R;
+  if (p->Nq > (1 << 30) || p->Nk > (1 << 30) || heads * R > (1 << 24) ||
+      heads * ((p->Nq + qn - 1) / qn) > (1 << 30) || R * p->Nq > UINT32_MAX)
     return SA_ERR_UNSUPPORTED;
   a->qs = p->q;
   a->ks = p->k;
@@ -193,12 +209,14 @@ sa_status sparse_attn_forward_masked(const sa_masked* p, const void* q, const vo
   // Outputs may not share elements with inputs or each other; o may be q's view
   // (a row of q is read only ahead of the row of o that takes its place).
   const int esz = a.out_fp32 ? 4 : 2;
-  const int64_t H = p->Hq, N = std::max(p->Nq, p->Nk);
-  auto apart = [&](const void* x, const sa_strides& xs, uint64_t nx) {
-    return esz == 2 ? !views_overlap(o, a.os, no, x, xs, nx, p->B, H, N, p->d, 2) : !overlap(o, no, x, nx);
+  const View out{o, a.os, p->B, p->Hq, p->Nq, no};
+  auto apart = [&](const View& x) {
+    return esz == 2 ? !views_overlap(out, x, p->d, 2) : !overlap(o, no, x.p, x.n);
   };
   const bool same = o == q && esz == 2 && a.os.b == a.qs.b && a.os.h == a.qs.h && a.os.n == a.qs.n;
-  if ((!same && !apart(q, a.qs, nq)) || !apart(k, a.ks, nk) || !apart(v, a.vs, nv)) return SA_ERR_INVALID_ARG;
+  if ((!same && !apart({q, a.qs, p->B, p->Hq, p->Nq, nq})) || !apart({k, a.ks, p->B, p->Hkv, p->Nk, nk}) ||
+      !apart({v, a.vs, p->B, p->Hkv, p->Nk, nv}))
+    return SA_ERR_INVALID_ARG;
   const uint64_t nl = lse ? uint64_t(a.total_rows) * 4 : 0;
   if (nl && (overlap(lse, nl, q, nq) || overlap(lse, nl, k, nk) || overlap(lse, nl, v, nv) || overlap(lse, nl, o, no)))
     return SA_ERR_INVALID_ARG;
@@ -276,7 +294,7 @@ sa_status sparse_attn_cache_evict(const sa_evict* p, const float* weights, const
     return SA_ERR_INVALID_ARG;
   if (p->d != 64 && p->d != 128) return SA_ERR_UNSUPPORTED;
   const int64_t rows = int64_t(p->B) * p->Hkv;
-  if (rows > 65535) return SA_ERR_UNSUPPORTED;  // grid.y
+  if (rows > 65535 || p->Nk > (1 << 30) || p->budget > (1 << 30)) return SA_ERR_UNSUPPORTED;  // grid.y, int indexes
   if (!weights || !kept || !aligned(weights, 4) || !aligned(kept, 4) || !aligned(weights_out, 4) ||
       !aligned(p->lengths, 4))
     return SA_ERR_INVALID_ARG;
@@ -308,7 +326,8 @@ sa_status sparse_attn_cache_evict(const sa_evict* p, const float* weights, const
       if (out[j].n && !(j == 1 && i == 2) && overlap(out[j].p, out[j].n, out[i].p, out[i].n))
         return SA_ERR_INVALID_ARG;
   }
-  if (kv && views_overlap(k_out, a.kos, nko, v_out, a.vos, nvo, p->B, p->Hkv, p->budget, p->d, 2))
+  if (kv && views_overlap({k_out, a.kos, p->B, p->Hkv, p->budget, nko}, {v_out, a.vos, p->B, p->Hkv, p->budget, nvo},
+                          p->d, 2))
     return SA_ERR_INVALID_ARG;
   int sms = 0;
   sa_status st = device_info(&sms);
@@ -420,7 +439,15 @@ sa_status sparse_attn_rope(const sa_rope* p, int32_t H0, const void* x0, const s
       return SA_ERR_INVALID_ARG;
     // in place (the same view) or apart: a row is read only by the threads that write it
     const bool same = x[i] == y[i] && a.xs[i].b == a.ys[i].b && a.xs[i].h == a.ys[i].h && a.xs[i].n == a.ys[i].n;
-    if (!same && views_overlap(x[i], a.xs[i], nx[i], y[i], a.ys[i], ny[i], p->B, H[i], p->N, p->d, esz))
+    if (!same && views_overlap({x[i], a.xs[i], p->B, H[i], p->N, nx[i]}, {y[i], a.ys[i], p->B, H[i], p->N, ny[i]},
+                               p->d, esz))
+      return SA_ERR_INVALID_ARG;
+  }
+  if (H1) {  // one pair's rows are not to be written while the other's are read or written
+    const View vx[2] = {{x0, a.xs[0], p->B, H0, p->N, nx[0]}, {x1, a.xs[1], p->B, H1, p->N, nx[1]}};
+    const View vy[2] = {{y0, a.ys[0], p->B, H0, p->N, ny[0]}, {y1, a.ys[1], p->B, H1, p->N, ny[1]}};
+    if (views_overlap(vy[0], vy[1], p->d, esz) || views_overlap(vy[0], vx[1], p->d, esz) ||
+        views_overlap(vx[0], vy[1], p->d, esz))
       return SA_ERR_INVALID_ARG;
   }
   int sms = 0;
