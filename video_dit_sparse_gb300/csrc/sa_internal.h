@@ -142,10 +142,11 @@ struct MaskedArgs {
   // tanh's polynomial on raw products: x (scale_log2 + w (p1 + w (p2 + w p3))), w = x^2 <= cap_limit
   float cap_p1, cap_p2, cap_p3, cap_limit;
   int64_t total_rows;  // B * Hq * Nq
-  // masked_plan: a Q tile holds qn queries of R heads each, a unit unit_rows / 128
-  // tiles, a key head row_blocks units, `group` heads are worked on at a time; the first
-  // full_units run whole, the other split_units in `splits` runs of keys
-  int32_t qn, unit_rows, row_blocks, group, splits;
+  // masked_plan: a Q tile holds qn queries of R heads each, a unit one or two tiles, a key
+  // head row_blocks units, `group` heads are worked on at a time; the first full_units run
+  // whole, the other split_units in `splits` runs of keys.  A run's partial result has
+  // unit_rows rows (128 a tile; quads: four times the rows of the tile)
+  int32_t qn, tiles, quads, unit_rows, row_blocks, group, splits;
   int64_t full_units, split_units;
   float* part_o;       // [split_units * splits, unit_rows, d] partials
   float* part_lse;     // [split_units * splits, unit_rows]

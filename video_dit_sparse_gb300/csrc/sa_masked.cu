@@ -74,6 +74,7 @@ struct MCfg {
   static constexpr int kSmemBytes = 1024 + kQBytes + kStages * kTile + kXch + 1024;
   // one tile: two S buffers, so that S(j+1) is computed beside softmax(j)
   static constexpr int kOCol = 256;
+  static constexpr int kPCol = 384;  // quads: P has columns of its own, 64 for each S buffer
   static constexpr int kTmemCols = 512;
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
@@ -116,13 +117,14 @@ struct Words {
 
 }  // namespace
 
-template <int D, int T, bool CAP, bool BIAS>
+template <int D, int T, bool QUADS, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
     sa_masked_kernel(const __grid_constant__ MaskedArgs a, const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
   using C = MCfg<D, T>;
   constexpr int S = C::kStages;
   constexpr int W = 16;  // S columns a register buffer holds
+  static_assert(!QUADS || T == 1, "quads have one tile");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem;
@@ -189,17 +191,26 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
     // Warps 8t .. 8t+3 take columns 0-63 of tile t's S (half 0), 8t+4 .. 8t+7
     // columns 64-127; warps of both halves with the same lane quarter share rows.
     const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
-    constexpr int H = BN / 2;
-    const int trow = quarter * 32 + lane;  // row of the tile
+    // Quads: the tile's up to 32 rows stand in each lane quarter, whose two warps take
+    // 32 of the columns, 16 each; the quarters' results are joined like splits.
+    constexpr int H = QUADS ? 16 : BN / 2;
+    const int col0 = (QUADS ? quarter * 2 + half : half) * H;
+    const int trow = QUADS ? lane : quarter * 32 + lane;  // row of the tile
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const int rq = trow / a.R, rh = trow - rq * a.R;  // its query and head in the tile
     const bool in_tile = trow < a.qn * a.R;
     const float sl = a.scale_log2;
-    uint32_t sbase = tmem + lane_base + t * 128 + half * H;
+    uint32_t sbase = tmem + lane_base + t * 128 + col0;
     const uint32_t obase = tmem + lane_base + C::kOCol + t * D + half * (D / 2);
     volatile int* flag = bars->flag[t * 4 + quarter];
     uint32_t xn = 0;           // pair exchanges so far
     uint32_t tc = 0, uc = 0;   // key tiles and units with keys so far
+    if (QUADS) {  // the other quarters' columns of P stay 0
+      uint32_t zero[32] = {};
+      tmem_st32(tmem + lane_base + C::kPCol + half * 64, zero);
+      tmem_st32(tmem + lane_base + C::kPCol + half * 64 + 32, zero);
+      tmem_st_wait();
+    }
     // Slot of exchange xn: this half's value, and the other half's.
     uint8_t* own = sX + warp * C::kWarpBytes;
     auto mine = [&]() -> float2* { return reinterpret_cast<float2*>(own) + (xn & 1) * 32 + lane; };
@@ -228,14 +239,14 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
       if (BIAS && valid) nslope = -__ldg(a.slopes + hq) * kLog2e;
       float m = -INFINITY, l = 0.f, lr = 0.f;
       for (int j = 0; j < n; ++j) {
-        const int k0 = key0 + (n - 1 - j) * BN, c0 = k0 + half * H;  // first keys of the tile and of the half
+        const int k0 = key0 + (n - 1 - j) * BN, c0 = k0 + col0;  // first keys of the tile and of the warp's columns
         const int va = sp.lo - c0, vb = sp.hi - c0;
         const bool edge = __any_sync(0xffffffffu, valid && (va > 0 || vb < H));
         // The first tile that shows a row a key sets its reference.
         const bool first = j == 0 || __any_sync(0xffffffffu, m == -INFINITY && sp.lo < k0 + BN && sp.hi > k0);
         // S buffer and its phase: one buffer a tile, or one tile's two in turn
         const uint32_t sb = T == 2 ? t : (tc + j) & 1;
-        if (T == 1) sbase = tmem + lane_base + sb * 128 + half * H;
+        if (T == 1) sbase = tmem + lane_base + sb * 128 + col0;
         if (!mbar_wait(&bars->sfull[sb], (T == 2 ? tc + j : (tc + j) >> 1) & 1, abort)) goto done;
         if (idle) {
           mbar_arrive(&bars->pfull[sb]);
@@ -318,13 +329,13 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
           const uint64_t sl2 = f2(sl, sl), k1 = f2(a.cap_p1, a.cap_p1), k2 = f2(a.cap_p2, a.cap_p2),
                          k3 = f2(a.cap_p3, a.cap_p3);
           float wm = 0.f;
-          float buf[2][W];  // the next columns load while these are worked on
+          float buf[QUADS ? 1 : 2][W];  // the next columns load while these are worked on
           load(buf[0], 0);
 #pragma unroll
           for (int base = 0; base < H; base += W) {
-            float* s = buf[(base / W) & 1];
+            float* s = buf[QUADS ? 0 : (base / W) & 1];
             tmem_ld_wait();
-            if (base + W < H) load(buf[(base / W + 1) & 1], base + W);
+            if (base + W < H) load(buf[QUADS ? 0 : (base / W + 1) & 1], base + W);
             if (BIAS && base) g = f2(g0 - static_cast<float>(base) * ns, g0 - static_cast<float>(base + 1) * ns);
             auto columns = [&](auto some) {
 #pragma unroll
@@ -423,7 +434,10 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         }
         l += ts;
         lr += tr;
-        tmem_st32(sbase, p);
+        if (QUADS)
+          tmem_st8(tmem + lane_base + C::kPCol + sb * 64 + col0 / 2, p);
+        else
+          tmem_st32(sbase, p);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&bars->pfull[sb]);
@@ -443,7 +457,8 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         lr += other()->y;
         ++xn;
         const float inv = l == 0.f ? 0.f : 1.f / lr;
-        const int64_t prow = int64_t(x.part) * (128 * T) + t * 128 + trow;
+        const int64_t prow = QUADS ? int64_t(x.part) * a.unit_rows + quarter * (a.qn * a.R) + trow
+                                   : int64_t(x.part) * (128 * T) + t * 128 + trow;
         if (valid && half == 0) {
           const float lse = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
           if (x.part >= 0)
@@ -545,12 +560,12 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
       mma_commit(&bars->sfull[sbuf(step)]);
     };
     auto pv = [&](uint32_t i, uint32_t step, bool first) {
-      const uint32_t s_tmem = tmem + sbuf(step) * 128;
+      const uint32_t s_tmem = tmem + sbuf(step) * 128, p_tmem = tmem + C::kPCol + sbuf(step) * 64;
       const uint32_t vl = v_lo + (((i % S) * C::kTile) >> 4);
 #pragma unroll
       for (int kk = 0; kk < BN / 16; ++kk)
         // P of keys 0-63 lies in S columns 0-31, of keys 64-127 in 64-95
-        mma_ts_w(o_tmem, s_tmem + (kk >> 2) * 64 + (kk & 3) * 8, vl + ((kk * 2048) >> 4), v_hi, kIdescPV,
+        mma_ts_w(o_tmem, QUADS ? p_tmem + kk * 8 : s_tmem + (kk >> 2) * 64 + (kk & 3) * 8, vl + ((kk * 2048) >> 4), v_hi, kIdescPV,
                  (!first || kk > 0) ? 1u : 0u);
     };
     if (lane == 0) {
@@ -683,13 +698,14 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
       if (n > 0) {
         if (uc > 0 && !mbar_wait(&bars->qempty, (uc - 1) & 1, abort)) break;
         ++uc;
-        mbar_expect_tx(&bars->qfull, T * a.qn * a.R * D * 2);
+        constexpr int kCopies = QUADS ? 4 : T;  // of one tile, or of each
+        mbar_expect_tx(&bars->qfull, kCopies * a.qn * a.R * D * 2);
 #pragma unroll
-        for (int t = 0; t < T; ++t)
+        for (int t = 0; t < kCopies; ++t)
 #pragma unroll
           for (int cb = 0; cb < D / 64; ++cb)
-            tma_load_4d(q_addr + t * 128 * D * 2 + cb * 128 * 128, &tm_q, 64 * cb, x.hk * a.R, x.q0 + t * a.qn, x.b,
-                        &bars->qfull);
+            tma_load_4d(q_addr + (QUADS ? t * 32 * 128 : t * 128 * D * 2) + cb * 128 * 128, &tm_q, 64 * cb, x.hk * a.R,
+                        x.q0 + (QUADS ? 0 : t * a.qn), x.b, &bars->qfull);
         for (int f = 0; f < 2 * n; ++f, ++it) {
           const uint32_t s = it % S;
           if (!(ok = mbar_wait(&bars->empty[s], ((it / S) & 1) ^ 1, abort))) break;
@@ -730,30 +746,33 @@ done:
   }
 }
 
-// One warp per row of a split unit: lse = ln sum_s e^(lse_s),
-// o = sum_s e^(lse_s - lse) o_s.  Bound by its launch and two rounds of loads.
-template <int D>
+// A row of a split unit: lse = ln sum_p e^(lse_p), o = sum_p e^(lse_p - lse) o_p over
+// its partial results (quads: four a split), by one warp, or for quads by the four warps
+// of a block.  Bound by its launch and two rounds of loads.
+template <int D, bool QUADS>
 __global__ void __launch_bounds__(128) sa_masked_join_kernel(const __grid_constant__ MaskedArgs a) {
+  constexpr int V = D / 32, WARPS = QUADS ? 4 : 1;
+  __shared__ float s_sum[4], s_acc[QUADS ? 4 : 1][QUADS ? D : 1];
   wait_for_earlier_kernel();  // (launched while the partial results are still being made)
-  const uint32_t i = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const uint32_t tile_rows = a.qn * a.R, unit_rows = a.unit_rows / 128 * tile_rows;  // that exist
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t i = QUADS ? blockIdx.x : blockIdx.x * 4 + warp;
+  const uint32_t tile_rows = a.qn * a.R, unit_rows = a.tiles * tile_rows;  // that exist
   const uint32_t su = i / unit_rows, r = i - su * unit_rows, t = r / tile_rows, tr = r - t * tile_rows;
   if (su >= a.split_units) return;
   const Place at = place_of(a, static_cast<int>(a.full_units + su));
-  const int q = at.rb * (a.unit_rows / 128 * a.qn) + t * a.qn + tr / a.R;
+  const int q = at.rb * (a.tiles * a.qn) + t * a.qn + tr / a.R;
   if (q >= a.Nq) return;
+  const int parts = QUADS ? a.splits * 4 : a.splits, step = QUADS ? tile_rows : a.unit_rows;
   const int64_t row0 = int64_t(su) * a.splits * a.unit_rows + t * 128 + tr;
   float mx = -INFINITY;
-  for (int s = lane; s < a.splits; s += 32) mx = fmaxf(mx, __ldg(a.part_lse + row0 + s * a.unit_rows));
+  for (int p = lane; p < parts; p += 32) mx = fmaxf(mx, __ldg(a.part_lse + row0 + p * step));
 #pragma unroll
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  constexpr int V = D / 32;
   float acc[V] = {}, sum = 0.f;
   if (mx != -INFINITY) {
 #pragma unroll 8
-    for (int s = 0; s < a.splits; ++s) {
-      const int64_t row = row0 + s * a.unit_rows;
+    for (int p = QUADS ? warp : 0; p < parts; p += WARPS) {
+      const int64_t row = row0 + p * step;
       const float w = __expf(__ldg(a.part_lse + row) - mx);
       float f[V];
       if (V == 4) {
@@ -766,6 +785,19 @@ __global__ void __launch_bounds__(128) sa_masked_join_kernel(const __grid_consta
       sum += w;
 #pragma unroll
       for (int e = 0; e < V; ++e) acc[e] += w * f[e];
+    }
+  }
+  if (QUADS) {
+    if (lane == 0) s_sum[warp] = sum;
+#pragma unroll
+    for (int e = 0; e < V; ++e) s_acc[QUADS ? warp : 0][QUADS ? lane * V + e : 0] = acc[e];
+    __syncthreads();
+    if (warp) return;
+    sum = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const int c = QUADS ? lane * V + e : 0;
+      acc[e] = (s_acc[0][c] + s_acc[QUADS ? 1 : 0][c]) + (s_acc[QUADS ? 2 : 0][c] + s_acc[QUADS ? 3 : 0][c]);
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -788,11 +820,13 @@ __global__ void __launch_bounds__(128) sa_masked_join_kernel(const __grid_consta
 // documents and lengths (a causal mask leaves little to the last units).
 void masked_plan(MaskedArgs* a) {
   a->qn = 128 / a->R;
-  const int T = a->Nq > a->qn ? 2 : 1;
+  const int T = a->tiles = a->Nq > a->qn ? 2 : 1;
   a->unit_rows = 128 * T;
   const int64_t unit_q = int64_t(T) * a->qn;
   a->row_blocks = static_cast<int32_t>((a->Nq + unit_q - 1) / unit_q);
   if (a->qn > a->Nq) a->qn = a->Nq;
+  a->quads = T == 1 && a->qn * a->R <= 32;
+  if (a->quads) a->unit_rows = 4 * a->qn * a->R;
   // Heads that are worked on at a time.  Units of one length: as many as keep K
   // and V in half the L2 (24 heads of 16384 x 16384: 2.17 ms, 2.23 with all at
   // once).  Units of different lengths (causal, documents) want more of them to
@@ -803,9 +837,10 @@ void masked_plan(MaskedArgs* a) {
                 fit = (int64_t(even ? 64 : 256) << 20) / (int64_t(a->Nk) * a->d * 4);
   const int64_t groups = fit < 1 ? heads : (heads + fit - 1) / fit;
   a->group = static_cast<int32_t>((heads + groups - 1) / groups);
-  const int64_t units = heads * a->row_blocks, rest = units % kSms;
+  const int64_t units = heads * a->row_blocks, rest = a->quads ? units : units % kSms;
+  const int64_t some = min64(rest, kSms);
   int64_t seen = 0;  // keys that the last units see
-  for (int64_t u = units - rest; u < units; ++u) {
+  for (int64_t u = units - some; u < units; ++u) {
     const int64_t q1 = min64(a->Nq, (place_of(*a, static_cast<int>(u)).rb + 1) * unit_q);
     int64_t hi = a->Nk;
     if (a->mask.causal) {
@@ -814,7 +849,7 @@ void masked_plan(MaskedArgs* a) {
     }
     seen += hi;
   }
-  const int64_t tiles = rest ? (seen / rest + BN - 1) / BN : 0;
+  const int64_t tiles = rest ? (seen / some + BN - 1) / BN : 0;
   constexpr int64_t kStart = 5, kJoin = 8;
   int64_t best = 1, cost = tiles + kStart;
   for (int64_t s = 2; s <= tiles && s <= 64; ++s) {
@@ -825,15 +860,15 @@ void masked_plan(MaskedArgs* a) {
     }
   }
   a->splits = static_cast<int32_t>(best);
-  a->full_units = best == 1 ? units : units - rest;
+  a->full_units = best == 1 && !a->quads ? units : units - rest;
   a->split_units = units - a->full_units;
 }
 
-template <int D, int T, bool CAP, bool BIAS>
+template <int D, int T, bool QUADS, bool CAP, bool BIAS>
 static cudaError_t launch_m(const MaskedArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             cudaStream_t st) {
   using C = MCfg<D, T>;
-  auto kern = sa_masked_kernel<D, T, CAP, BIAS>;
+  auto kern = sa_masked_kernel<D, T, QUADS, CAP, BIAS>;
   // at least half the SM's shared memory: one block per SM owns its TMEM
   const int smem = C::kSmemBytes > 120 * 1024 ? C::kSmemBytes : 120 * 1024;
   static std::atomic<int> regs_ok{0};  // 0 unknown, 1 enough, 2 too few
@@ -853,12 +888,25 @@ static cudaError_t launch_m(const MaskedArgs& a, const CUtensorMap& tq, const CU
   return cudaGetLastError();
 }
 
-template <int D, int T>
-static cudaError_t launch_t(const MaskedArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+template <int D, int T, bool QUADS>
+static cudaError_t launch_t(const MaskedArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                             cudaStream_t st) {
   const bool cap = a.cap_log2 > 0.f, bias = a.slopes != nullptr;
-  if (cap) return bias ? launch_m<D, T, true, true>(a, tq, tk, tv, st) : launch_m<D, T, true, false>(a, tq, tk, tv, st);
-  return bias ? launch_m<D, T, false, true>(a, tq, tk, tv, st) : launch_m<D, T, false, false>(a, tq, tk, tv, st);
+  if (cap)
+    return bias ? launch_m<D, T, QUADS, true, true>(a, q, k, v, st) : launch_m<D, T, QUADS, true, false>(a, q, k, v, st);
+  return bias ? launch_m<D, T, QUADS, false, true>(a, q, k, v, st) : launch_m<D, T, QUADS, false, false>(a, q, k, v, st);
+}
+
+template <int D>
+static cudaError_t launch_d(const MaskedArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                            cudaStream_t st) {
+  const cudaError_t e = a.tiles == 2 ? launch_t<D, 2, false>(a, q, k, v, st)
+                        : a.quads    ? launch_t<D, 1, true>(a, q, k, v, st)
+                                     : launch_t<D, 1, false>(a, q, k, v, st);
+  if (e != cudaSuccess || a.split_units == 0) return e;
+  const int64_t rows = a.split_units * a.tiles * a.qn * a.R;
+  if (a.quads) return launch_early(sa_masked_join_kernel<D, true>, dim3(static_cast<unsigned>(rows)), 128, 0, st, a);
+  return launch_early(sa_masked_join_kernel<D, false>, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, st, a);
 }
 
 cudaError_t launch_masked(const MaskedArgs& a, cudaStream_t st) {
@@ -867,13 +915,7 @@ cudaError_t launch_masked(const MaskedArgs& a, cudaStream_t st) {
       !make_view_map(&tk, a.k, a.d, a.Nk, a.Hkv, a.B, a.ks.n, a.ks.h, a.ks.b, BN, 1, false) ||
       !make_view_map(&tv, a.v, a.d, a.Nk, a.Hkv, a.B, a.vs.n, a.vs.h, a.vs.b, BN, 1, false))
     return cudaErrorInvalidValue;
-  const bool two = a.unit_rows == 256;
-  cudaError_t e = a.d == 128 ? (two ? launch_t<128, 2>(a, tq, tk, tv, st) : launch_t<128, 1>(a, tq, tk, tv, st))
-                             : (two ? launch_t<64, 2>(a, tq, tk, tv, st) : launch_t<64, 1>(a, tq, tk, tv, st));
-  if (e != cudaSuccess || a.split_units == 0) return e;
-  const int64_t rows = a.split_units * (a.unit_rows / 128) * a.qn * a.R;
-  return launch_early(a.d == 128 ? sa_masked_join_kernel<128> : sa_masked_join_kernel<64>,
-                      dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, st, a);
+  return a.d == 128 ? launch_d<128>(a, tq, tk, tv, st) : launch_d<64>(a, tq, tk, tv, st);
 }
 
 }  // namespace sa

@@ -156,7 +156,8 @@ sa_status check_masked(const sa_masked* p, sa::MaskedArgs* a) {
     return SA_ERR_INVALID_ARG;
   a->cap_limit = r2 > 0.0 && r2 < 1e6 ? static_cast<float>(0.16 / r2) : -1.f;
   a->total_rows = int64_t(p->B) * p->Hq * p->Nq;
-  a->qn = a->unit_rows = a->row_blocks = a->group = a->splits = 1;
+  a->qn = a->tiles = a->unit_rows = a->row_blocks = a->group = a->splits = 1;
+  a->quads = 0;
   a->full_units = a->split_units = 0;
   a->part_o = nullptr;
   a->part_lse = nullptr;
