@@ -262,6 +262,73 @@ def test_two_streams_at_once():
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+# few rows over many keys: each lane quarter takes a quarter of them, and the runs are joined
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hk,Nq", [(1, 1, 1), (4, 2, 1), (32, 1, 1), (3, 1, 10), (5, 1, 6), (6, 2, 11)])
+@pytest.mark.parametrize("kw", [{}, dict(causal=1), dict(cap=20.0), dict(bias=True, causal=1), dict(bias=True, cap=5.0)])
+def test_few_rows(d, H, Hk, Nq, kw):
+    q, k, v = tensors(2, H, Hk, Nq, 3001, d, seed=30 + H, sigma=3.0)
+    kw = dict(kw)
+    if kw.pop("bias", False):
+        kw["slopes"] = [2.0 ** -(2 + i % 8) for i in range(H)]
+    check(*run(q, k, v, out_dtype=torch.float32, **kw), q, k, v, **kw)
+
+
+@pytest.mark.parametrize("Nq", [1, 3])
+@pytest.mark.parametrize("lengths", [[20000, 0, 1, 129, 15001], [0, 0, 0, 0, 0], [5, 20000, 20000, 3, 2], [-7, 2, 99999, 128, 0]])
+def test_few_rows_over_ragged_lengths(Nq, lengths):
+    q, k, v = tensors(5, 8, 2, Nq, 20000, 64, seed=31)
+    for b, n in enumerate(lengths):
+        k[b, :, max(n, 0):] = float("nan")
+        v[b, :, max(n, 0):] = float("nan")
+    live = [min(max(n, 0), 20000) for n in lengths]
+    check(*run(q, k, v, lengths=lengths, causal=1), q, k, v, lengths=live, causal=1)
+    check(*run(q, k, v, lengths=lengths, cap=30.0), q, k, v, lengths=live, cap=30.0)
+
+
+def test_few_rows_of_many_sequences_and_documents():
+    g = np.random.default_rng(4)
+    lengths = [int(x) for x in g.integers(0, 4001, 40)]
+    q, k, v = tensors(40, 1, 1, 1, 4000, 64, seed=32)
+    check(*run(q, k, v, lengths=lengths), q, k, v, lengths=lengths)
+    docs = dict(docs_q=[[0, 2, 2, 9], [1, 1, 1, 8], [0, 3, 6, 9]], docs_k=[[0, 7000, 7001, 9000], [10, 20, 30, 9001],
+                                                                          [0, 0, 4000, 4100]])
+    q, k, v = tensors(3, 3, 1, 9, 9001, 128, seed=33)
+    check(*run(q, k, v, causal=1, **docs), q, k, v, causal=1, **docs)
+    check(*run(q, k, v, cap=9.0, **docs), q, k, v, cap=9.0, **docs)
+
+
+@pytest.mark.parametrize("slopes", [None, [0.01, 0.02]])
+def test_few_rows_late_maximum(slopes):
+    q, k, v = tensors(1, 2, 1, 4, 5000, 128, seed=34)
+    k[:, :, :100] *= 12  # tiles are taken from the last to the first
+    k[:, :, 2500:2520] *= 6
+    check(*run(q, k, v, slopes=slopes), q, k, v, slopes=slopes)
+    check(*run(q, k, v, scale=-0.2), q, k, v, scale=-0.2)
+
+
+def test_few_rows_streams_graphs_and_repeatability():
+    from video_dit_sparse_gb300 import binding as sa
+    q, k, v = tensors(3, 8, 2, 1, 20000, 128, seed=35)
+    n = torch.tensor([20000, 1, 9000], dtype=torch.int32, device="cuda")
+    want = sa.sparse_attn_forward_masked(q, k, v, lengths=n)
+    other = sa.sparse_attn_forward_masked(q, k, v, lengths=n)
+    assert torch.equal(want[0], other[0]) and torch.equal(want[1], other[1])
+    out, lse = torch.empty_like(q), torch.empty(3, 8, 1, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sa.sparse_attn_forward_masked(q, k, v, lengths=n, out=out, lse=lse)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    n.copy_(torch.tensor([300, 20000, 0]))  # the captured call reads the lengths when it runs
+    want = sa.sparse_attn_forward_masked(q, k, v, lengths=n)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert bool((out[2] == 0).all()) and bool((lse[2] == -float("inf")).all())
+
+
 def test_output_over_the_queries():
     from video_dit_sparse_gb300 import binding as sa
     for H, Nq, Nk in ((4, 700, 900), (42, 515, 300), (8, 1, 4000)):

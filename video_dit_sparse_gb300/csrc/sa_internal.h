@@ -145,11 +145,15 @@ struct MaskedArgs {
   // masked_plan: a Q tile holds qn queries of R heads each, a unit one or two tiles, a key
   // head row_blocks units, `group` heads are worked on at a time; the first full_units run
   // whole, the other split_units in `splits` runs of keys.  A run's partial result has
-  // unit_rows rows (128 a tile; quads: four times the rows of the tile)
-  int32_t qn, tiles, quads, unit_rows, row_blocks, group, splits;
+  // unit_rows rows (128 a tile; quads: four times the
+  // rows of the tile).  slots > 0: the runs are shared out on the device instead, so that
+  // all are about as long (quads with at most a unit an SM; slots: partial results)
+  int32_t qn, tiles, quads, unit_rows, row_blocks, group, splits, slots;
   int64_t full_units, split_units;
-  float* part_o;       // [split_units * splits, unit_rows, d] partials
-  float* part_lse;     // [split_units * splits, unit_rows]
+  float* part_o;       // [partial results, unit_rows, d]
+  float* part_lse;     // [partial results, unit_rows]
+  int32_t* part_first; // slots: first partial result of each batch entry's first head [B],
+                       // then how many each head has [B]
 };
 void masked_plan(MaskedArgs* a);
 cudaError_t launch_masked(const MaskedArgs& a, cudaStream_t stream);

@@ -35,6 +35,12 @@
 // a long cache) are cut into `splits` runs of key tiles; each writes a
 // normalised fp32 partial and its lse, and a second kernel joins them:
 // o = sum_s e^(lse_s - lse) o_s.
+// A new token's few rows would leave all but two softmax warps idle, and those two
+// 64 columns a tile each (1.26 us a tile of 128 keys with a cap).  With up to 32 rows
+// the tile holds them four times, once per TMEM lane quarter, and each quarter's two
+// warps take 32 of the 128 keys; the other keys' P is 0 there, so the quarters' O and
+// sums are those of four splits, and are joined like them (1.01 us a tile; a key head's
+// run of K and V then arrives at 65 GB/s a SM, beyond an even share of the HBM).
 #include <atomic>
 #include <cmath>
 
@@ -48,7 +54,7 @@ namespace sa {
 namespace {
 
 constexpr int BN = 128;
-constexpr int64_t kSms = 152;
+constexpr int kSms = 152;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 // P is computed against a row reference m that only moves when a tile's sum
@@ -71,7 +77,7 @@ struct MCfg {
   static constexpr int kStages = D == 128 ? (T == 2 ? 4 : 5) : 8;
   static constexpr int kWarpBytes = 2048;  // a softmax warp's own: exchange slots, output staging
   static constexpr int kXch = kSoftWarps * kWarpBytes;
-  static constexpr int kSmemBytes = 1024 + kQBytes + kStages * kTile + kXch + 1024;
+  static constexpr int kSmemBytes = 1024 + kQBytes + kStages * kTile + kXch + 1024 + (T == 1 ? 2048 : 0);
   // one tile: two S buffers, so that S(j+1) is computed beside softmax(j)
   static constexpr int kOCol = 256;
   static constexpr int kPCol = 384;  // quads: P has columns of its own, 64 for each S buffer
@@ -91,6 +97,8 @@ struct MBars {
     int part, q0, b, hk;   // partial result (-1: whole), first query, batch entry, key head
   } ring[2];
   int flag[T * 4][2];
+  int first[T == 1 ? kSms : 1], runs[T == 1 ? kSms : 1];  // slots of each batch entry (share_out)
+  int used;
   uint32_t tmem_base;
   int abort;
 };
@@ -104,6 +112,71 @@ __host__ __device__ __forceinline__ Place place_of(const MaskedArgs& a, int u) {
   const int heads = a.B * a.Hkv - grp * a.group < a.group ? a.B * a.Hkv - grp * a.group : a.group;
   const int k = r / heads;
   return {grp * a.group + (r - k * heads), a.row_blocks - 1 - k};
+}
+
+// Key tiles that the rows of a unit with the queries q0 .. q1 see.
+__device__ __forceinline__ int tiles_of(const MaskedArgs& a, int b, int q0, int q1, int* lo, int* hi) {
+  *lo = row_span(a.mask, b, q0).lo;
+  *hi = row_span(a.mask, b, q1).hi;
+  return *hi > *lo ? (*hi - *lo + BN - 1) / BN : 0;
+}
+
+// Shares the slots out among the units of a batch of at most kSms, by one warp: the
+// shortest run L for which sum_b Hkv ceil(tiles_b / L) slots are enough, ceil(tiles_b / L)
+// runs for each head of entry b.  (With as many for each, whatever its length, 4 sequences
+// of 28160, 7041, 20000 and 27999 keys took as long as 4 of 28160: 60.5 us, now 54.8.)
+template <typename Bars>
+__device__ __forceinline__ void share_out(const MaskedArgs& a, Bars* bars, int lane) {
+  constexpr int N = (kSms + 31) / 32;
+  int t[N], sum = 0, most = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int b = i * 32 + lane;
+    int lo, hi;
+    t[i] = b < a.B ? tiles_of(a, b, 0, a.Nq - 1, &lo, &hi) : 0;
+    sum += t[i];
+    most = max(most, t[i]);
+  }
+  sum = __reduce_add_sync(0xffffffffu, sum) * a.Hkv;
+  most = __reduce_max_sync(0xffffffffu, most);
+  int L = max(1, (sum + a.slots - 1) / a.slots), top = max(most, 1);  // (at `top` a run a head)
+  // sum_b Hkv ceil(t_b / L) < sum / L + units
+  const int spare = a.slots - a.B * a.Hkv;
+  if (spare > 0) top = min(top, max(1, (sum + spare - 1) / spare));
+  while (L < top) {
+    const int mid = (L + top) >> 1;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i * 32 < a.B) n += (t[i] + mid - 1) / mid;
+    if (static_cast<int>(__reduce_add_sync(0xffffffffu, n)) * a.Hkv <= a.slots)
+      top = mid;
+    else
+      L = mid + 1;
+  }
+  int at = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i * 32 >= a.B) break;
+    const int b = i * 32 + lane, runs = (t[i] + L - 1) / L;
+    int inc = runs * a.Hkv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (b < a.B) {
+      bars->first[b] = at + inc - runs * a.Hkv;
+      bars->runs[b] = runs;
+      if (blockIdx.x == 0) {
+        a.part_first[b] = at + inc - runs * a.Hkv;
+        a.part_first[a.B + b] = runs;
+      }
+    }
+    at += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (lane == 0) bars->used = at;
+  __syncwarp();
 }
 
 template <bool M>
@@ -168,6 +241,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
       reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
+  if (QUADS && a.slots && warp == C::kTmaWarp) share_out(a, bars, lane);
   if (warp == C::kMmaWarp) {
     tmem_alloc(&bars->tmem_base, C::kTmemCols);
     tmem_relinquish();
@@ -651,8 +725,9 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->tail);
     }
-  } else if (warp == C::kTmaWarp && lane == 0) {
+  } else if (warp == C::kTmaWarp) {
     // ------------------------------------------------------------ units and loads
+      if (lane) goto done;
     const uint32_t q_addr = smem_u32(sQ), kv_addr = smem_u32(sKV);
     int64_t g = blockIdx.x;
     uint32_t it = 0, uc = 0;
@@ -671,7 +746,23 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         int u = static_cast<int>(g), split = 0, splits = 1;
         x.go = 1;
         x.part = -1;
-        if (g >= a.full_units) {
+        bool none = false;  // a slot that no unit has
+        if (QUADS && a.slots) {
+          x.part = u;
+          none = u >= bars->used;
+          int e = 0, top = none ? 0 : a.B - 1;  // the last batch entry that starts here or before
+          while (e < top) {
+            const int mid = (e + top + 1) >> 1;
+            if (bars->first[mid] <= u)
+              e = mid;
+            else
+              top = mid - 1;
+          }
+          splits = max(bars->runs[e], 1);
+          const int in = u - bars->first[e], h = in / splits;
+          split = in - h * splits;
+          u = none ? 0 : e * a.Hkv + h;
+        } else if (g >= a.full_units) {
           splits = a.splits;
           x.part = static_cast<int>(g - a.full_units);
           split = x.part % splits;
@@ -683,12 +774,11 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         x.b = bh / a.Hkv;
         x.hk = bh - x.b * a.Hkv;
         // keys that any of the unit's rows sees, and this split's run of tiles
-        const int ulo = row_span(a.mask, x.b, x.q0).lo;
-        x.uhi = row_span(a.mask, x.b, min(x.q0 + T * a.qn, a.Nq) - 1).hi;
-        const int ntiles = x.uhi > ulo ? (x.uhi - ulo + BN - 1) / BN : 0;
+        int ulo;
+        const int ntiles = none ? 0 : tiles_of(a, x.b, x.q0, min(x.q0 + T * a.qn, a.Nq) - 1, &ulo, &x.uhi);
         const int j0 = static_cast<int>(int64_t(ntiles) * split / splits);
         x.n = static_cast<int>(int64_t(ntiles) * (split + 1) / splits) - j0;
-        x.key0 = ulo + j0 * BN;
+        x.key0 = none ? 0 : ulo + j0 * BN;
       }
       const int key0 = x.key0, n = x.n;
       if (i >= 2 && !mbar_wait(&bars->ring_empty[i & 1], ((i >> 1) - 1) & 1, abort)) break;
@@ -746,33 +836,30 @@ done:
   }
 }
 
-// A row of a split unit: lse = ln sum_p e^(lse_p), o = sum_p e^(lse_p - lse) o_p over
-// its partial results (quads: four a split), by one warp, or for quads by the four warps
-// of a block.  Bound by its launch and two rounds of loads.
-template <int D, bool QUADS>
+// One warp per row of a split unit: lse = ln sum_s e^(lse_s),
+// o = sum_s e^(lse_s - lse) o_s.  Bound by its launch and two rounds of loads.
+template <int D>
 __global__ void __launch_bounds__(128) sa_masked_join_kernel(const __grid_constant__ MaskedArgs a) {
-  constexpr int V = D / 32, WARPS = QUADS ? 4 : 1;
-  __shared__ float s_sum[4], s_acc[QUADS ? 4 : 1][QUADS ? D : 1];
   wait_for_earlier_kernel();  // (launched while the partial results are still being made)
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t i = QUADS ? blockIdx.x : blockIdx.x * 4 + warp;
+  const uint32_t i = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
   const uint32_t tile_rows = a.qn * a.R, unit_rows = a.tiles * tile_rows;  // that exist
   const uint32_t su = i / unit_rows, r = i - su * unit_rows, t = r / tile_rows, tr = r - t * tile_rows;
   if (su >= a.split_units) return;
   const Place at = place_of(a, static_cast<int>(a.full_units + su));
   const int q = at.rb * (a.tiles * a.qn) + t * a.qn + tr / a.R;
   if (q >= a.Nq) return;
-  const int parts = QUADS ? a.splits * 4 : a.splits, step = QUADS ? tile_rows : a.unit_rows;
   const int64_t row0 = int64_t(su) * a.splits * a.unit_rows + t * 128 + tr;
   float mx = -INFINITY;
-  for (int p = lane; p < parts; p += 32) mx = fmaxf(mx, __ldg(a.part_lse + row0 + p * step));
+  for (int s = lane; s < a.splits; s += 32) mx = fmaxf(mx, __ldg(a.part_lse + row0 + s * a.unit_rows));
 #pragma unroll
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  constexpr int V = D / 32;
   float acc[V] = {}, sum = 0.f;
   if (mx != -INFINITY) {
 #pragma unroll 8
-    for (int p = QUADS ? warp : 0; p < parts; p += WARPS) {
-      const int64_t row = row0 + p * step;
+    for (int s = 0; s < a.splits; ++s) {
+      const int64_t row = row0 + s * a.unit_rows;
       const float w = __expf(__ldg(a.part_lse + row) - mx);
       float f[V];
       if (V == 4) {
@@ -785,19 +872,6 @@ __global__ void __launch_bounds__(128) sa_masked_join_kernel(const __grid_consta
       sum += w;
 #pragma unroll
       for (int e = 0; e < V; ++e) acc[e] += w * f[e];
-    }
-  }
-  if (QUADS) {
-    if (lane == 0) s_sum[warp] = sum;
-#pragma unroll
-    for (int e = 0; e < V; ++e) s_acc[QUADS ? warp : 0][QUADS ? lane * V + e : 0] = acc[e];
-    __syncthreads();
-    if (warp) return;
-    sum = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const int c = QUADS ? lane * V + e : 0;
-      acc[e] = (s_acc[0][c] + s_acc[QUADS ? 1 : 0][c]) + (s_acc[QUADS ? 2 : 0][c] + s_acc[QUADS ? 3 : 0][c]);
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -813,6 +887,84 @@ __global__ void __launch_bounds__(128) sa_masked_join_kernel(const __grid_consta
   if (lane == 0 && a.lse) a.lse[(int64_t(b) * a.Hq + h) * a.Nq + q] = sum == 0.f ? -INFINITY : mx + logf(sum);
 }
 
+// The same for quads, whose rows have four partial results a split (up to 608 in all):
+// a block per row, each warp every sixteenth of them.
+template <int D>
+__global__ void __launch_bounds__(512) sa_masked_join_quads_kernel(const __grid_constant__ MaskedArgs a) {
+  constexpr int V = D / 32, WARPS = 16;
+  __shared__ float s_mx[WARPS], s_sum[WARPS], s_acc[WARPS][D];
+  wait_for_earlier_kernel();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows = a.qn * a.R, su = blockIdx.x / rows, tr = blockIdx.x - su * rows;
+  const int bh = place_of(a, su).bh, b = bh / a.Hkv, hk = bh - b * a.Hkv;
+  int parts = a.splits;
+  int64_t first = int64_t(su) * parts;
+  if (a.slots) {
+    parts = __ldg(a.part_first + a.B + b);
+    first = __ldg(a.part_first + b) + hk * parts;
+  }
+  parts *= 4;
+  const int64_t row0 = first * a.unit_rows + tr;
+  float mx = -INFINITY, sum = 0.f, acc[V] = {};
+  for (int p = warp; p < parts; p += WARPS * 8) {  // eight at a time
+    float l[8], top = mx, f[8][V];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = p + i * WARPS;
+      l[i] = at < parts ? __ldg(a.part_lse + row0 + at * rows) : -INFINITY;
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[i][e] = 0.f;
+      if (at < parts) {
+        const float* o = a.part_o + (row0 + at * rows) * D + lane * V;
+        const float2 x = __ldg(reinterpret_cast<const float2*>(o)), y = __ldg(reinterpret_cast<const float2*>(o + V - 2));
+        f[i][0] = x.x, f[i][1] = x.y, f[i][V - 2] = y.x, f[i][V - 1] = y.y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, l[i]);
+    if (top == -INFINITY) continue;
+    const float keep = __expf(mx - top);
+    mx = top;
+    sum *= keep;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] *= keep;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float w = __expf(l[i] - mx);
+      sum += w;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] += w * f[i][e];
+    }
+  }
+  if (lane == 0) {
+    s_mx[warp] = mx;
+    s_sum[warp] = sum;
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) s_acc[warp][lane * V + e] = acc[e];
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (c >= D) return;
+  float all = -INFINITY, total = 0.f, x = 0.f;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) all = fmaxf(all, s_mx[w]);
+  if (all != -INFINITY)
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float e = __expf(s_mx[w] - all);
+      total += e * s_sum[w];
+      x += e * s_acc[w][c];
+    }
+  x = total == 0.f ? 0.f : x / total;
+  const int h = hk * a.R + tr % a.R, q = tr / a.R;
+  const int64_t at = int64_t(b) * a.os.b + int64_t(h) * a.os.h + int64_t(q) * a.os.n + c;
+  if (a.out_fp32)
+    static_cast<float*>(a.o)[at] = x;
+  else
+    static_cast<uint16_t*>(a.o)[at] = static_cast<uint16_t>(pack_bf16(x, 0.f));
+  if (c == 0 && a.lse) a.lse[(int64_t(b) * a.Hq + h) * a.Nq + q] = total == 0.f ? -INFINITY : all + logf(total);
+}
+
 // Units that fill whole waves of SMs run whole; the rest (all, if they are
 // fewer than the SMs) are split into the number of key runs that ends first by
 // this count of tile times: a wave costs its tiles plus a block's start, a
@@ -825,8 +977,6 @@ void masked_plan(MaskedArgs* a) {
   const int64_t unit_q = int64_t(T) * a->qn;
   a->row_blocks = static_cast<int32_t>((a->Nq + unit_q - 1) / unit_q);
   if (a->qn > a->Nq) a->qn = a->Nq;
-  a->quads = T == 1 && a->qn * a->R <= 32;
-  if (a->quads) a->unit_rows = 4 * a->qn * a->R;
   // Heads that are worked on at a time.  Units of one length: as many as keep K
   // and V in half the L2 (24 heads of 16384 x 16384: 2.17 ms, 2.23 with all at
   // once).  Units of different lengths (causal, documents) want more of them to
@@ -837,10 +987,9 @@ void masked_plan(MaskedArgs* a) {
                 fit = (int64_t(even ? 64 : 256) << 20) / (int64_t(a->Nk) * a->d * 4);
   const int64_t groups = fit < 1 ? heads : (heads + fit - 1) / fit;
   a->group = static_cast<int32_t>((heads + groups - 1) / groups);
-  const int64_t units = heads * a->row_blocks, rest = a->quads ? units : units % kSms;
-  const int64_t some = min64(rest, kSms);
+  const int64_t units = heads * a->row_blocks, rest = units % kSms;
   int64_t seen = 0;  // keys that the last units see
-  for (int64_t u = units - some; u < units; ++u) {
+  for (int64_t u = units - rest; u < units; ++u) {
     const int64_t q1 = min64(a->Nq, (place_of(*a, static_cast<int>(u)).rb + 1) * unit_q);
     int64_t hi = a->Nk;
     if (a->mask.causal) {
@@ -849,7 +998,7 @@ void masked_plan(MaskedArgs* a) {
     }
     seen += hi;
   }
-  const int64_t tiles = rest ? (seen / some + BN - 1) / BN : 0;
+  const int64_t tiles = rest ? (seen / rest + BN - 1) / BN : 0;
   constexpr int64_t kStart = 5, kJoin = 8;
   int64_t best = 1, cost = tiles + kStart;
   for (int64_t s = 2; s <= tiles && s <= 64; ++s) {
@@ -860,8 +1009,18 @@ void masked_plan(MaskedArgs* a) {
     }
   }
   a->splits = static_cast<int32_t>(best);
-  a->full_units = best == 1 && !a->quads ? units : units - rest;
+  a->full_units = best == 1 ? units : units - rest;
   a->split_units = units - a->full_units;
+  // Few rows, all units split: quads (6 key heads of 28160 keys, 4 rows each: 19.0 us, 22.2
+  // with the rows in one lane quarter).  Where lengths may differ the device shares the
+  // runs out, which costs a start of 1.7 us: not for short runs (16 key heads of 4000 keys
+  // in runs of 4 tiles: 15.8 us shared out, 14.2 not).
+  a->quads = T == 1 && a->full_units == 0 && a->qn * a->R <= 32;
+  if (a->quads) {
+    a->unit_rows = 4 * a->qn * a->R;
+    if ((a->mask.nd || a->mask.len) && tiles >= 8 * best)
+      a->slots = static_cast<int32_t>(min64(units * ((int64_t(a->Nk) + BN - 1) / BN), kSms));
+  }
 }
 
 template <int D, int T, bool QUADS, bool CAP, bool BIAS>
@@ -883,7 +1042,7 @@ static cudaError_t launch_m(const MaskedArgs& a, const CUtensorMap& tq, const CU
   if (regs_ok.load() != 1) return cudaErrorLaunchOutOfResources;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t grid = a.full_units + a.split_units * a.splits;
+  const int64_t grid = a.slots ? a.slots : a.full_units + a.split_units * a.splits;
   kern<<<static_cast<unsigned>(grid), C::kThreads, smem, st>>>(a, tq, tk, tv);
   return cudaGetLastError();
 }
@@ -905,8 +1064,9 @@ static cudaError_t launch_d(const MaskedArgs& a, const CUtensorMap& q, const CUt
                                      : launch_t<D, 1, false>(a, q, k, v, st);
   if (e != cudaSuccess || a.split_units == 0) return e;
   const int64_t rows = a.split_units * a.tiles * a.qn * a.R;
-  if (a.quads) return launch_early(sa_masked_join_kernel<D, true>, dim3(static_cast<unsigned>(rows)), 128, 0, st, a);
-  return launch_early(sa_masked_join_kernel<D, false>, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, st, a);
+  if (a.quads)
+    return launch_early(sa_masked_join_quads_kernel<D>, dim3(static_cast<unsigned>(rows)), 512, 0, st, a);
+  return launch_early(sa_masked_join_kernel<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, st, a);
 }
 
 cudaError_t launch_masked(const MaskedArgs& a, cudaStream_t st) {

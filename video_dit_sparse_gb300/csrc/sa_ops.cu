@@ -157,10 +157,11 @@ sa_status check_masked(const sa_masked* p, sa::MaskedArgs* a) {
   a->cap_limit = r2 > 0.0 && r2 < 1e6 ? static_cast<float>(0.16 / r2) : -1.f;
   a->total_rows = int64_t(p->B) * p->Hq * p->Nq;
   a->qn = a->tiles = a->unit_rows = a->row_blocks = a->group = a->splits = 1;
-  a->quads = 0;
+  a->quads = a->slots = 0;
   a->full_units = a->split_units = 0;
   a->part_o = nullptr;
   a->part_lse = nullptr;
+  a->part_first = nullptr;
   return SA_OK;
 }
 
@@ -174,13 +175,13 @@ bool masked_tables(const sa_masked* p) {
          (!p->slopes || in_device_allocation(p->slopes, uint64_t(p->Hq) * 4));
 }
 
-// The partial outputs, then their lse (each 256-byte aligned).
-size_t part_bytes(const sa::MaskedArgs& a) {
-  return size_t(a.split_units) * a.splits * a.unit_rows * a.d * 4;
-}
+// The partial outputs, then their lse, then the table of slots (each 256-byte aligned).
+size_t part_count(const sa::MaskedArgs& a) { return a.slots ? a.slots : size_t(a.split_units) * a.splits; }
+size_t part_bytes(const sa::MaskedArgs& a) { return (part_count(a) * a.unit_rows * a.d * 4 + 255) / 256 * 256; }
+size_t part_lse_bytes(const sa::MaskedArgs& a) { return (part_count(a) * a.unit_rows * 4 + 255) / 256 * 256; }
 
 size_t masked_workspace(const sa::MaskedArgs& a) {
-  return part_bytes(a) + (size_t(a.split_units) * a.splits * a.unit_rows * 4 + 255) / 256 * 256;
+  return part_bytes(a) + part_lse_bytes(a) + (a.slots ? (size_t(a.B) * 8 + 255) / 256 * 256 : 0);
 }
 
 }  // namespace
@@ -243,6 +244,7 @@ sa_status sparse_attn_forward_masked(const sa_masked* p, const void* q, const vo
   if (need) {
     a.part_o = static_cast<float*>(workspace);
     a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + part_bytes(a));
+    a.part_first = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + part_bytes(a) + part_lse_bytes(a));
   }
   sa::NvtxRange range("sparse_attn_forward_masked");
   return map_cuda(sa::launch_masked(a, reinterpret_cast<cudaStream_t>(stream)));
