@@ -17,9 +17,12 @@
 // Each key tile has its own TMEM buffer, its own MMA warp (its waits and commits
 // overlap the other's MMAs; they take turns, so that one buffer's sums run
 // beside the other's MMA) and two sets of four epilogue warps, one per half of
-// the columns.  With many rows the bound is the tensor core (one exponential a
-// pair is 0.8 of its time on the MUFU); with one token per sequence it is the
-// read of K.
+// the columns.  With many rows the tensor core is the floor, and two things come
+// near it: an exponential a pair (0.8 of its time on the MUFU) and shared memory
+// (both MMA operands, 3/4 of the time, and the reads of lse): 12 heads of 7040 rows x
+// 35200 keys take 591 us, 61 % of the measured bf16 rate.  With one token per
+// sequence the bound is the read of K (256-key units of one Q tile: 83 200 keys of 6
+// heads, 128 MB, in 27 us).
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -777,7 +780,8 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kSelThreads) sa_evic
   if (C > 1) cluster.sync();  // no block leaves while another may read its totals
 }
 
-// PIECES 16-byte pieces per row (d / 8); U slots per thread in flight.
+// PIECES 16-byte pieces per row (d / 8); U slots per thread in flight.  Bound by
+// HBM: 12 heads x 28160 rows of K and V, 173 MB each way, at 6.5 TB/s.
 template <int PIECES>
 __global__ void __launch_bounds__(256) sa_evict_gather_kernel(const EvictArgs a) {
   wait_for_earlier_kernel();  // (launched while the entries are still being chosen)

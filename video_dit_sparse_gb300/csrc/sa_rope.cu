@@ -10,7 +10,8 @@
 // exact fraction of a turn (positions are whole numbers), whose top 32 bits go
 // to sincospi.  Error: below 2^-24 of a half turn, at any 32-bit position.
 //
-// The kernel is bound by HBM (each row is read and written once).  A thread
+// The kernel is bound by HBM (each row is read and written once; 24 + 24 heads of
+// 69120 rows of 128: 259 us, 97 % of the measured copy rate).  A thread
 // owns the same two 16-byte pieces of a token's row in every head of its run,
 // so one set of cosines and sines in registers serves them all; four heads'
 // loads are in flight at a time.  Pieces c and c + half a row are a thread's
