@@ -284,7 +284,8 @@ def test_weights_large_scores_under_a_cap():
     assert (np.abs(got.double().cpu().numpy() - want) <= tol).all()
 
 
-@pytest.mark.parametrize("B,H,N,budget", [(1, 1, 500000, 1000), (77, 1, 50000, 49000), (1, 2, 8193, 8192), (2, 3, 40000, 20)])
+@pytest.mark.parametrize("B,H,N,budget", [(1, 1, 500000, 1000), (77, 1, 50000, 49000), (1, 2, 8193, 8192), (2, 3, 40000, 20),
+                                          (5, 9, 9000, 4000), (1, 2, 200001, 100000), (32, 5, 8500, 77)])
 def test_evict_long_rows(B, H, N, budget):
     from video_dit_sparse_gb300 import binding as sa
     g = torch.Generator(device="cuda").manual_seed(N)
@@ -294,6 +295,15 @@ def test_evict_long_rows(B, H, N, budget):
     for b, h in ((0, 0), (B - 1, H - 1)):
         want = O.evict(w[b, h].cpu().numpy(), N, budget, 3, 5)
         assert np.array_equal(kept[b, h].cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sink,recent", [(0, 0), (130, 200), (128, 0), (0, 128), (389, 388), (777, 0), (0, 777), (65, 711)])
+def test_evict_rows_that_need_no_choice(d, sink, recent):
+    """Tiles of only first or newest entries move before the others are chosen; tiles that hold both do not."""
+    w = torch.rand(6, 2, 1500, generator=torch.Generator().manual_seed(sink + recent))
+    evict_case(w, [1500, 777, 778, 900, 10, 0], 777, sink, recent, d=d, layout="bnhd")
+    evict_case(w, None, 777, sink, recent, d=d)
 
 
 def test_a_step_in_a_graph():

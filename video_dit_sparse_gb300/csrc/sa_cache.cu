@@ -631,12 +631,13 @@ __device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0u : o
 
 }  // namespace
 
-// C blocks (a cluster) per row, each with a run of the row's entries in its
-// shared memory: 24 us for 12 rows of 35200 entries with one block a row.  The
-// blocks add up their histograms through distributed shared memory, so that all
-// of them find the same digit.
+// C blocks (a cluster) per row, each with a run of the row's entries in its shared
+// memory.  They add up their histograms through distributed shared memory, so that all
+// of them find the same digit.  Bound by latency: three passes, each a histogram, a scan
+// and two cluster barriers (12 rows of 35200 entries: 14 us).
 template <int C>
 __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kSelThreads) sa_evict_select_kernel(const EvictArgs a) {
+  let_next_kernel_start();  // (the gather's rows that need no choice move meanwhile)
   extern __shared__ uint32_t s_keys[];
   __shared__ __align__(8) uint32_t hist[kBins];
   __shared__ uint32_t wsum[32], weq[32], s_total[2];
@@ -783,18 +784,35 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kSelThreads) sa_evic
 // PIECES 16-byte pieces per row (d / 8); U slots per thread in flight.  Bound by
 // HBM: 12 heads x 28160 rows of K and V, 173 MB each way, at 6.5 TB/s.
 template <int PIECES>
-__global__ void __launch_bounds__(256) sa_evict_gather_kernel(const EvictArgs a) {
-  wait_for_earlier_kernel();  // (launched while the entries are still being chosen)
-  constexpr int U = 4, kSlots = 256 / PIECES;
+__global__ void __launch_bounds__(256) sa_evict_gather_kernel(const EvictArgs a, int rows, int tiles) {
+  constexpr int U = 4, kSlots = 256 / PIECES, kTile = kSlots * U;
   const int piece = threadIdx.x % PIECES;
-  const int64_t row = blockIdx.y, b = row / a.Hkv, h = row % a.Hkv;
+  const uint32_t turn = blockIdx.x / uint32_t(rows);
+  const int64_t row = blockIdx.x - turn * uint32_t(rows), b = row / a.Hkv, h = row % a.Hkv;
   const int32_t* kept = a.kept + row * a.budget;
-  const int j0 = blockIdx.x * (kSlots * U) + threadIdx.x / PIECES;
+  // Tiles of slots: first those that only hold the first entries or the newest, which
+  // need not wait for the choice of the others.
+  const int sinks = a.sink / kTile, last = (a.budget - a.recent + kTile - 1) / kTile, fixed = sinks + tiles - last;
+  const int t = static_cast<int>(turn);
+  const bool early = t < fixed;
+  const int tile = t < sinks ? t : early ? last + t - sinks : sinks + t - fixed;
+  const int j0 = tile * kTile + threadIdx.x / PIECES;
   int idx[U];
+  if (early) {
+    const int n = a.len ? min(max(__ldg(a.len + b), 0), a.Nk) : a.Nk;
+    const int shift = tile < sinks || n <= a.budget ? 0 : n - a.budget;
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const int j = j0 + i * kSlots;
-    idx[i] = j < a.budget ? __ldg(kept + j) : -1;
+    for (int i = 0; i < U; ++i) {
+      const int j = j0 + i * kSlots;
+      idx[i] = j < min(a.budget, n) ? j + shift : -1;
+    }
+  } else {
+    wait_for_earlier_kernel();
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int j = j0 + i * kSlots;
+      idx[i] = j < a.budget ? __ldg(kept + j) : -1;
+    }
   }
   if (a.k) {
     const uint16_t* k = a.k + b * a.ks.b + h * a.ks.h + piece * 8;
@@ -821,22 +839,35 @@ __global__ void __launch_bounds__(256) sa_evict_gather_kernel(const EvictArgs a)
     for (int i = 0; i < U; ++i)
       if (idx[i] >= 0) a.w_out[row * a.budget + j0 + i * kSlots] = __ldg(a.w + row * a.Nk + idx[i]);
   }
+  if (early) wait_for_earlier_kernel();  // (this kernel's end is to mean the other's, too)
 }
 
 cudaError_t launch_cache_evict(const EvictArgs& a, int num_sms, cudaStream_t st) {
   const int64_t rows = int64_t(a.B) * a.Hkv;
-  const int blocks = a.Nk > 8192 && rows * 8 <= 4 * num_sms ? 8 : 1;  // a row's
+  // Blocks a row: one is enough for a short row; four, of which every SM holds one, as
+  // long as they all run at once (clusters fill about four SMs in five); eight when a
+  // fourth of a row is more than half of what a block keeps.  Selection alone, one /
+  // two / four / eight: 12 rows of 35200 entries 22.5 / 17.6 / 14.3 / 17.9 us, 48 rows
+  // (21120 to choose from) 16.3 / 14.8 / 26.1 / 63, 4 rows of 100000 116 / 33 / 21.9 / 20.7.
+  const int64_t room = num_sms * 4 / 5;
+  const int blocks = a.Nk <= 8192 || rows * 2 > room           ? 1
+                     : rows * 4 > room                         ? 2
+                     : rows * 8 > room || a.Nk <= 2 * kCached ? 4
+                                                               : 8;
   const int run = blocks == 1 ? a.Nk : (a.Nk + blocks - 1) / blocks + 32;
   const int smem = (run < kCached ? run : kCached) * 4;
-  auto kern = blocks == 8 ? sa_evict_select_kernel<8> : sa_evict_select_kernel<1>;
+  auto kern = blocks == 8   ? sa_evict_select_kernel<8>
+              : blocks == 4 ? sa_evict_select_kernel<4>
+              : blocks == 2 ? sa_evict_select_kernel<2>
+                            : sa_evict_select_kernel<1>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4);
   if (e != cudaSuccess) return e;
   kern<<<static_cast<unsigned>(rows * blocks), kSelThreads, smem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (!a.k && !a.w_out) return cudaSuccess;
-  const int slots = 4 * (256 / (a.d / 8));
-  const dim3 grid((a.budget + slots - 1) / slots, static_cast<unsigned>(rows));
-  return launch_early(a.d == 128 ? sa_evict_gather_kernel<16> : sa_evict_gather_kernel<8>, grid, 256, 0, st, a);
+  const int slots = 4 * (256 / (a.d / 8)), tiles = (a.budget + slots - 1) / slots;
+  return launch_early(a.d == 128 ? sa_evict_gather_kernel<16> : sa_evict_gather_kernel<8>,
+                      dim3(static_cast<unsigned>(rows * tiles)), 256, 0, st, a, static_cast<int>(rows), tiles);
 }
 
 }  // namespace sa

@@ -185,6 +185,9 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 __device__ __forceinline__ void wait_for_earlier_kernel() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
+// Lets the next kernel's blocks start beside this one (launch_early; they wait for its end
+// where they need it).
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---------------------------------------------------- cluster launch control
 // Asks for a block of the grid that has not started yet, to be run by this one
