@@ -839,7 +839,8 @@ __global__ void __launch_bounds__(256) sa_evict_gather_kernel(const EvictArgs a,
     for (int i = 0; i < U; ++i)
       if (idx[i] >= 0) a.w_out[row * a.budget + j0 + i * kSlots] = __ldg(a.w + row * a.Nk + idx[i]);
   }
-  if (early) wait_for_earlier_kernel();  // (this kernel's end is to mean the other's, too)
+  // (this kernel's end is to mean the other's, too; a block that waits holds its place)
+  if (early && t == tiles - 1) wait_for_earlier_kernel();
 }
 
 cudaError_t launch_cache_evict(const EvictArgs& a, int num_sms, cudaStream_t st) {

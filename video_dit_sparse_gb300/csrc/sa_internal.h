@@ -245,7 +245,9 @@ struct NvtxRange {
 };
 
 // Launches a kernel that may start while the one ahead of it on the stream still
-// runs; the kernel calls wait_for_earlier_kernel() before it touches memory.
+// runs, from that one's end on or from its let_next_kernel_start(); it calls
+// wait_for_earlier_kernel() before it touches what that one writes, and at least one
+// block calls it in any case, so that its end means the other's end.
 template <class... P, class... A>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
                          const A&... args) {
