@@ -288,9 +288,10 @@ def test_few_rows_over_ragged_lengths(Nq, lengths):
 
 def test_few_rows_of_many_sequences_and_documents():
     g = np.random.default_rng(4)
-    lengths = [int(x) for x in g.integers(0, 4001, 40)]
-    q, k, v = tensors(40, 1, 1, 1, 4000, 64, seed=32)
-    check(*run(q, k, v, lengths=lengths), q, k, v, lengths=lengths)
+    for B in (40, 76):
+        lengths = [int(x) for x in g.integers(0, 4001, B)]
+        q, k, v = tensors(B, 1, 1, 1, 4000, 64, seed=32)
+        check(*run(q, k, v, lengths=lengths), q, k, v, lengths=lengths)
     docs = dict(docs_q=[[0, 2, 2, 9], [1, 1, 1, 8], [0, 3, 6, 9]], docs_k=[[0, 7000, 7001, 9000], [10, 20, 30, 9001],
                                                                           [0, 0, 4000, 4100]])
     q, k, v = tensors(3, 3, 1, 9, 9001, 128, seed=33)
