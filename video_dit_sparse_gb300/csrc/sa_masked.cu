@@ -41,8 +41,9 @@
 // 64 columns a tile each (1.26 us a tile of 128 keys with a cap).  With up to 32 rows
 // the tile holds them four times, once per TMEM lane quarter, and each quarter's two
 // warps take 32 of the 128 keys; the other keys' P is 0 there, so the quarters' O and
-// sums are those of four splits, and are joined like them (1.01 us a tile; a key head's
-// run of K and V then arrives at 65 GB/s a SM, beyond an even share of the HBM).
+// sums are those of four splits, and are joined like them (1.01 us a tile; with a
+// warp for each of the two products 0.73, K and V at 90 GB/s a SM, twice an even share
+// of the HBM).
 #include <atomic>
 #include <cmath>
 
@@ -67,7 +68,7 @@ template <int D, int T>
 struct MCfg {
   static constexpr int kSoftWarps = 8 * T;  // per Q tile two sets of four: column halves
   static constexpr int kMmaWarp = kSoftWarps, kTmaWarp = kSoftWarps + T,  // one MMA warp a tile
-                       kTailWarp = kTmaWarp + 1;
+                       kTailWarp = kTmaWarp + 1, kPvWarp = kTailWarp + 1;  // (one tile: PV has its own)
   // whole warpgroups: setmaxnreg acts on aligned groups of four warps
   static constexpr int kThreads = 32 * (kSoftWarps + 4);
   static constexpr bool kRegSplit = T == 2;
@@ -80,7 +81,7 @@ struct MCfg {
   static constexpr int kWarpBytes = 2048;  // a softmax warp's own: exchange slots, output staging
   static constexpr int kXch = kSoftWarps * kWarpBytes;
   static constexpr int kSmemBytes = 1024 + kQBytes + kStages * kTile + kXch + 1024 + (T == 1 ? 2048 : 0);
-  // one tile: two S buffers, so that S(j+1) is computed beside softmax(j)
+  // one tile: two S buffers, so that S(j+1) is computed beside softmax(j) and PV(j)
   static constexpr int kOCol = 256;
   static constexpr int kPCol = 384;  // quads: P has columns of its own, 64 for each S buffer
   static constexpr int kTmemCols = 512;
@@ -90,8 +91,8 @@ struct MCfg {
 template <int T, int STAGES>
 struct MBars {
   uint64_t full[STAGES], empty[STAGES];
-  uint64_t sfull[2], pfull[2], pvdone, ofull[T], ofree[T];
-  uint64_t qfull, qempty, next, tail, tail_here, turn[T], ring_full[2], ring_empty[2], drain[T];
+  uint64_t sfull[2], pfull[2], pvdone[2], ofull[T], ofree[T];
+  uint64_t qfull, qempty, next, tail, tail_here, turn[T], ring_full[2], ring_empty[2], drain[2];
   uint4 answer;   // of the request for the next unit
   struct Unit {
     int go;                // 0: no more units
@@ -221,12 +222,13 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
     for (int i = 0; i < T * 4; ++i) {
       bars->flag[i][0] = bars->flag[i][1] = 0;
     }
-    mbar_init(&bars->pvdone, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->sfull[i], 1);  // S and P of each S buffer
       mbar_init(&bars->pfull[i], 256);
       mbar_init(&bars->ring_full[i], 1);
-      mbar_init(&bars->ring_empty[i], C::kSoftWarps + T + 1);
+      mbar_init(&bars->ring_empty[i], C::kSoftWarps + T + 1 + (T == 1 ? 1 : 0));
+      mbar_init(&bars->pvdone[i], 1);
+      mbar_init(&bars->drain[i], 1);
     }
     mbar_init(&bars->qfull, 1);
     mbar_init(&bars->qempty, T);
@@ -234,7 +236,6 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
     mbar_init(&bars->tail, 1);
     mbar_init(&bars->tail_here, T);
     for (int i = 0; i < T; ++i) mbar_init(&bars->turn[i], 1);
-    for (int i = 0; i < T; ++i) mbar_init(&bars->drain[i], 1);
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
           lr *= alpha;
           // O holds PV of every earlier tile: with two Q tiles its commit came with
           // this S.  (j > 0, and no later PV has been issued.)
-          if (T == 1 && !mbar_wait(&bars->pvdone, (tc + j - 1) & 1, abort)) goto done;
+          if (T == 1 && !mbar_wait(&bars->pvdone[(tc + j - 1) & 1], ((tc + j - 1) >> 1) & 1, abort)) goto done;
           __syncwarp();
           tc_fence_after();
 #pragma unroll
@@ -603,12 +604,15 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         mbar_arrive(&bars->ofree[t]);
       }
     }
-  } else if (warp < C::kTmaWarp) {
+  } else if (warp < C::kTmaWarp || (T == 1 && warp == C::kPvWarp)) {
     // ------------------------------------------------------------ MMA issue
     // One warp per Q tile: issuing an MMA blocks while the tensor core is busy,
     // so one thread for both tiles left it idle (1000 of 3600 cycles a step)
-    // whenever that thread waited for a barrier or committed.
-    const int t = warp - C::kMmaWarp;
+    // whenever that thread waited for a barrier or committed.  One tile: a warp for
+    // the first product and one for the second (12 heads of 880 keys: 13.2 -> 11.9 us, 128
+    // of 8000 83.5 -> 79.4; a step of quads 0.98 -> 0.73).
+    const bool second = T == 1 && warp == C::kPvWarp;
+    const int t = T == 1 ? 0 : warp - C::kMmaWarp;
     const uint32_t kIdescS = a.neg_scale ? idesc_negate_b(idesc_bf16(128, BN, false, false))
                                          : idesc_bf16(128, BN, false, false);
     constexpr uint32_t kIdescPV = idesc_bf16(128, D, false, true);
@@ -620,9 +624,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
     const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
     const uint32_t o_tmem = tmem + C::kOCol + t * D;
     auto ready = [&](uint32_t i) -> bool { return mbar_wait(&bars->full[i % S], (i / S) & 1, abort); };
-    auto pass = [&]() {  // the other tile's turn
-      if (T == 2) mbar_arrive(&bars->turn[t ^ 1]);
-    };
+    auto pass = [&]() { mbar_arrive(&bars->turn[t ^ 1]); };  // the other tile's turn
     auto sbuf = [&](uint32_t step) -> uint32_t { return T == 2 ? t : step & 1; };
     auto qk = [&](uint32_t i, uint32_t step, bool turn) {
       const uint32_t s_tmem = tmem + sbuf(step) * 128;
@@ -641,8 +643,8 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
 #pragma unroll
       for (int kk = 0; kk < BN / 16; ++kk)
         // P of keys 0-63 lies in S columns 0-31, of keys 64-127 in 64-95
-        mma_ts_w(o_tmem, QUADS ? p_tmem + kk * 8 : s_tmem + (kk >> 2) * 64 + (kk & 3) * 8, vl + ((kk * 2048) >> 4), v_hi, kIdescPV,
-                 (!first || kk > 0) ? 1u : 0u);
+        mma_ts_w(o_tmem, QUADS ? p_tmem + kk * 8 : s_tmem + (kk >> 2) * 64 + (kk & 3) * 8, vl + ((kk * 2048) >> 4),
+                 v_hi, kIdescPV, (!first || kk > 0) ? 1u : 0u);
     };
     if (lane == 0) {
       bool ok = true;
@@ -655,6 +657,41 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         const int key0 = x.key0, n = x.n, uhi = x.uhi;
         if (n == 0) continue;
         // Ring entries: K(j) is number 2 (tc + j), V(j) the one behind it.
+        if (T == 1 && !second) {
+          if (!(ok = mbar_wait(&bars->qfull, uc & 1, abort))) break;
+          for (int j = 0; j < n; ++j) {
+            const uint32_t step = tc + j, ik = 2 * step, was = step - 2;
+            // (the second product of two steps ago is done: S and P of this buffer are free)
+            if (!(ok = ready(ik)) || (step >= 2 && !(ok = mbar_wait(&bars->pvdone[was & 1], (was >> 1) & 1, abort)))) break;
+            tc_fence_after();
+            qk(ik, step, false);
+            mma_commit(&bars->empty[ik % S]);
+          }
+          if (ok) mma_commit(&bars->qempty);
+          tc += n;
+          ++uc;
+          continue;
+        }
+        if (second) {
+          for (int j = 0; j < n; ++j) {
+            const uint32_t step = tc + j, iv = 2 * step + 1;
+            if (!(ok = ready(iv))) break;
+            if (j == 0 && uhi - (key0 + (n - 1) * BN) < BN) {  // to be cleared behind the span
+              mbar_arrive(&bars->tail_here);
+              if (!(ok = mbar_wait(&bars->tail, zc++ & 1, abort))) break;
+            }
+            if (j == 0 && uc > 0 && !(ok = mbar_wait(&bars->ofree[t], (uc - 1) & 1, abort))) break;
+            if (!(ok = mbar_wait(&bars->pfull[step & 1], (step >> 1) & 1, abort))) break;
+            tc_fence_after();
+            pv(iv, step, j == 0);
+            mma_commit(&bars->pvdone[step & 1]);
+            mma_commit(&bars->empty[iv % S]);
+          }
+          if (ok) mma_commit(&bars->ofull[t]);
+          tc += n;
+          ++uc;
+          continue;
+        }
         if (!(ok = mbar_wait(&bars->qfull, uc & 1, abort)) || !(ok = ready(2 * tc))) break;
         tc_fence_after();
         qk(2 * tc, tc, false);
@@ -670,35 +707,28 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
           if (j == 0 && uc > 0 && !(ok = mbar_wait(&bars->ofree[t], (uc - 1) & 1, abort))) break;
           // Turns: the tiles' steps alternate (side by side they would fall into
           // step and leave the tensor core idle during both softmaxes).
-          if (T == 2 && tc + j + t > 0 && !(ok = mbar_wait(&bars->turn[t], (tc + j + t - 1) & 1, abort))) break;
-          // One tile: the other S buffer is free once PV(j-1) has been issued.
-          if (T == 1 && more) {
-            tc_fence_after();
-            qk(ik, tc + j + 1, false);
-            mma_commit(&bars->empty[ik % S]);
-            if (j + 2 == n) mma_commit(&bars->qempty);
-          }
+          if (tc + j + t > 0 && !(ok = mbar_wait(&bars->turn[t], (tc + j + t - 1) & 1, abort))) break;
           // (P last: even a wait for what is long done takes about 100 cycles)
-          if (!(ok = mbar_wait(&bars->pfull[sbuf(tc + j)], (T == 2 ? tc + j : (tc + j) >> 1) & 1, abort))) break;
+          if (!(ok = mbar_wait(&bars->pfull[t], (tc + j) & 1, abort))) break;
           tc_fence_after();
           pv(iv, tc + j, j == 0);
-          if (T == 1) mma_commit(&bars->pvdone);
-          if (T == 2 && more)
+          if (more)
             qk(ik, tc + j + 1, true);
           else
             pass();
           if (!more) mma_commit(&bars->ofull[t]);
           mma_commit(&bars->empty[iv % S]);
-          if (T == 2 && more) mma_commit(&bars->empty[ik % S]);
-          if (T == 2 && j + 2 == n) mma_commit(&bars->qempty);
+          if (more) mma_commit(&bars->empty[ik % S]);
+          if (j + 2 == n) mma_commit(&bars->qempty);
         }
         tc += n;
         ++uc;
       }
       // Every MMA issued above must finish before TMEM is released.
-      mma_commit(&bars->drain[t]);
+      const int at = second ? 1 : t;
+      mma_commit(&bars->drain[at]);
       const long long t0 = clock64();
-      while (!mbar_test(&bars->drain[t], 0) && clock64() - t0 < kWaitLimitCycles) {
+      while (!mbar_test(&bars->drain[at], 0) && clock64() - t0 < kWaitLimitCycles) {
       }
     }
   } else if (warp == C::kTailWarp) {
@@ -1013,7 +1043,7 @@ void masked_plan(MaskedArgs* a) {
   a->splits = static_cast<int32_t>(best);
   a->full_units = best == 1 ? units : units - rest;
   a->split_units = units - a->full_units;
-  // Few rows, all units split: quads (6 key heads of 28160 keys, 4 rows each: 19.0 us, 22.2
+  // Few rows, all units split: quads (6 key heads of 28160 keys, 4 rows each: 19.0 us then, 22.2
   // with the rows in one lane quarter).  Where lengths may differ the device shares the
   // runs out, which costs a start of 1.7 us: not for short runs (16 key heads of 4000 keys
   // in runs of 4 tiles: 15.8 us shared out, 14.2 not).
