@@ -345,3 +345,22 @@ def test_output_over_the_queries():
     assert torch.equal(q, want) and torch.equal(qkv[:, 12:], rest)
     with pytest.raises(sa.SparseAttnError):
         sa.sparse_attn_forward_masked(k, k, v, out=k)
+
+
+def test_few_rows_while_the_gpu_is_busy():
+    """Blocks that start late or not at all: others take their runs over, and the table of runs is there all the same."""
+    from video_dit_sparse_gb300 import binding as sa
+    q, k, v = tensors(4, 8, 2, 1, 20000, 64, seed=36)
+    n = torch.tensor([20000, 3, 0, 11001], dtype=torch.int32, device="cuda")
+    want = sa.sparse_attn_forward_masked(q, k, v, lengths=n)
+    big = tensors(1, 12, 12, 2000, 4000, 128, seed=37)
+    s = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for _ in range(2):
+            sa.sparse_attn_forward_masked(*big, stream=s[0])
+        ws = torch.full((32 << 20,), 255, dtype=torch.uint8, device="cuda")  # (a table of -1 unless written)
+        torch.cuda.current_stream().synchronize()
+        o, lse = sa.sparse_attn_forward_masked(q, k, v, lengths=n, workspace=ws, stream=s[1])
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])

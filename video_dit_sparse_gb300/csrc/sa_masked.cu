@@ -171,10 +171,6 @@ __device__ __forceinline__ void share_out(const MaskedArgs& a, Bars* bars, int l
     if (b < a.B) {
       bars->first[b] = at + inc - runs * a.Hkv;
       bars->runs[b] = runs;
-      if (blockIdx.x == 0) {
-        a.part_first[b] = at + inc - runs * a.Hkv;
-        a.part_first[a.B + b] = runs;
-      }
     }
     at += __shfl_sync(0xffffffffu, inc, 31);
   }
@@ -743,6 +739,13 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->ring_empty[i & 1]);
       if (!x.go) break;
+      // The join's table, by the block that runs the first slot (block 0 may never start:
+      // any block may take its slot over).
+      if (QUADS && a.slots && x.part == 0)
+        for (int b = lane; b < a.B; b += 32) {
+          a.part_first[b] = bars->first[b];
+          a.part_first[a.B + b] = bars->runs[b];
+        }
       const uint32_t iv = 2 * tc + 1;  // the unit's first V: tiles come last first
       tc += x.n;
       const int live = x.uhi - (x.key0 + (x.n - 1) * BN);
@@ -932,8 +935,9 @@ __global__ void __launch_bounds__(512) sa_masked_join_quads_kernel(const __grid_
   int parts = a.splits;
   int64_t first = int64_t(su) * parts;
   if (a.slots) {
-    parts = __ldg(a.part_first + a.B + b);
-    first = __ldg(a.part_first + b) + hk * parts;
+    // (within the workspace even if the attention gave up before it wrote the table)
+    parts = min(max(__ldg(a.part_first + a.B + b), 0), a.slots);
+    first = min(max(int64_t(__ldg(a.part_first + b)) + int64_t(hk) * parts, int64_t(0)), int64_t(a.slots - parts));
   }
   parts *= 4;
   const int64_t row0 = first * a.unit_rows + tr;
