@@ -18,3 +18,15 @@ def test_no_block_has_a_duty_by_its_number():
     kernel = text[text.index("__device__ __forceinline__ void share_out"):text.index("sa_masked_join_kernel")]
     assert "request_block" in kernel
     assert re.findall(r"[^\n]*blockIdx[^\n]*", kernel) == ["    int64_t g = blockIdx.x;"]
+
+
+def test_results_of_a_running_kernel_are_read_by_plain_loads():
+    """A kernel launched beside the one ahead of it reads that one's results after its wait.  A read-only load promises
+    that nothing writes the data while the kernel runs, so the compiler may move it ahead of the wait."""
+    text = source("sa_masked.cu") + source("sa_cache.cu")
+    assert text.count("wait_for_earlier_kernel();") == 4
+    loads = re.findall(r"__ldg\((?:[^()]|\((?:[^()]|\([^()]*\))*\))*\)", text)
+    assert len(loads) > 5  # (the pattern finds them)
+    assert [x for x in loads if re.search(r"\bkept\b|part_o|part_lse|part_first", x)] == []
+    quads = text[text.index("sa_masked_join_quads_kernel"):text.index("void masked_plan")]
+    assert "__ldg" not in quads  # (its rows are read through a pointer of their own)

@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(256) sa_evict_gather_kernel(const EvictArgs a,
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int j = j0 + i * kSlots;
-      idx[i] = j < a.budget ? __ldg(kept + j) : -1;
+      idx[i] = j < a.budget ? kept[j] : -1;  // (a plain load: the selection may still run beside this kernel)
     }
   }
   if (a.k) {

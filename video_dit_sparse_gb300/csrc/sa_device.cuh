@@ -181,7 +181,8 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 
 // ------------------------------------------------- programmatic launch order
 // In a kernel launched by launch_early: waits until the kernel ahead of it on
-// the stream has finished and its writes are visible.
+// the stream has finished and its writes are visible.  What that kernel writes is read
+// by plain loads: a read-only load (__ldg) may be moved ahead of the wait.
 __device__ __forceinline__ void wait_for_earlier_kernel() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

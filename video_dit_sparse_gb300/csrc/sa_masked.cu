@@ -875,7 +875,8 @@ done:
 // o = sum_s e^(lse_s - lse) o_s.  Bound by its launch and two rounds of loads.
 template <int D>
 __global__ void __launch_bounds__(128) sa_masked_join_kernel(const __grid_constant__ MaskedArgs a) {
-  wait_for_earlier_kernel();  // (launched while the partial results are still being made)
+  // (launched while the partial results are still being made: read by plain loads, which stay behind the wait)
+  wait_for_earlier_kernel();
   const uint32_t i = blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const uint32_t tile_rows = a.qn * a.R, unit_rows = a.tiles * tile_rows;  // that exist
@@ -886,7 +887,7 @@ __global__ void __launch_bounds__(128) sa_masked_join_kernel(const __grid_consta
   if (q >= a.Nq) return;
   const int64_t row0 = int64_t(su) * a.splits * a.unit_rows + t * 128 + tr;
   float mx = -INFINITY;
-  for (int s = lane; s < a.splits; s += 32) mx = fmaxf(mx, __ldg(a.part_lse + row0 + s * a.unit_rows));
+  for (int s = lane; s < a.splits; s += 32) mx = fmaxf(mx, a.part_lse[row0 + s * a.unit_rows]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   constexpr int V = D / 32;
@@ -895,13 +896,13 @@ __global__ void __launch_bounds__(128) sa_masked_join_kernel(const __grid_consta
 #pragma unroll 8
     for (int s = 0; s < a.splits; ++s) {
       const int64_t row = row0 + s * a.unit_rows;
-      const float w = __expf(__ldg(a.part_lse + row) - mx);
+      const float w = __expf(a.part_lse[row] - mx);
       float f[V];
       if (V == 4) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(a.part_o + row * D) + lane);
+        const float4 x = reinterpret_cast<const float4*>(a.part_o + row * D)[lane];
         f[0] = x.x, f[1] = x.y, f[V - 2] = x.z, f[V - 1] = x.w;
       } else {
-        const float2 x = __ldg(reinterpret_cast<const float2*>(a.part_o + row * D) + lane);
+        const float2 x = reinterpret_cast<const float2*>(a.part_o + row * D)[lane];
         f[0] = x.x, f[1] = x.y;
       }
       sum += w;
@@ -936,8 +937,8 @@ __global__ void __launch_bounds__(512) sa_masked_join_quads_kernel(const __grid_
   int64_t first = int64_t(su) * parts;
   if (a.slots) {
     // (within the workspace even if the attention gave up before it wrote the table)
-    parts = min(max(__ldg(a.part_first + a.B + b), 0), a.slots);
-    first = min(max(int64_t(__ldg(a.part_first + b)) + int64_t(hk) * parts, int64_t(0)), int64_t(a.slots - parts));
+    parts = min(max(a.part_first[a.B + b], 0), a.slots);
+    first = min(max(int64_t(a.part_first[b]) + int64_t(hk) * parts, int64_t(0)), int64_t(a.slots - parts));
   }
   parts *= 4;
   const int64_t row0 = first * a.unit_rows + tr;
@@ -947,12 +948,12 @@ __global__ void __launch_bounds__(512) sa_masked_join_quads_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int at = p + i * WARPS;
-      l[i] = at < parts ? __ldg(a.part_lse + row0 + at * rows) : -INFINITY;
+      l[i] = at < parts ? a.part_lse[row0 + at * rows] : -INFINITY;
 #pragma unroll
       for (int e = 0; e < V; ++e) f[i][e] = 0.f;
       if (at < parts) {
         const float* o = a.part_o + (row0 + at * rows) * D + lane * V;
-        const float2 x = __ldg(reinterpret_cast<const float2*>(o)), y = __ldg(reinterpret_cast<const float2*>(o + V - 2));
+        const float2 x = *reinterpret_cast<const float2*>(o), y = *reinterpret_cast<const float2*>(o + V - 2);
         f[i][0] = x.x, f[i][1] = x.y, f[i][V - 2] = y.x, f[i][V - 1] = y.y;
       }
     }
