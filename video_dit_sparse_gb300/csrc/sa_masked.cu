@@ -387,15 +387,17 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
           ps[c & 1] = add2(ps[c & 1], f2(p0, p1));
           pr[c & 1] = add_bf16x2(p[c], pr[c & 1]);
         };
-        // Most tiles: every visible key on one side of its row, where the bias is
-        // linear in the column.  The exponent is then one multiply-add a pair:
+        // Most tiles: every visible key on one side of its row (`behind`: none after the
+        // row's position; else none before it), where the bias is linear in the column.
+        // The exponent is then one multiply-add a pair:
         // x * f + g with g = -mm or, with a bias, a pair that steps along the
         // columns.  With a cap, f is tanh(z)/z as a polynomial in z^2 (|z| <= 0.4,
         // error below 1.6e-7 cap); false if a score is larger.
         const int far = sp.pos - c0;  // distance of the half's first column
+        const bool behind = !BIAS || far >= min(vb, H) - 1;
         auto fast = [&](float mm, auto masked) -> bool {
           zero();
-          const float ns = far > 0 ? nslope : -nslope;  // of (far - c)
+          const float ns = behind ? nslope : -nslope;  // of (far - c)
           const float g0 = BIAS ? fmaf(ns, static_cast<float>(far), -mm) : -mm;
           uint64_t g = BIAS ? f2(g0, g0 - ns) : f2(g0, g0);
           const uint64_t step = f2(-2.f * ns, -2.f * ns);
@@ -446,9 +448,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         };
         auto exps = [&](float mm) {
           bool ok = true;
-          if (BIAS)
-            ok = __all_sync(0xffffffffu, !valid || far >= min(vb, H) - 1) ||
-                 __all_sync(0xffffffffu, !valid || far <= max(va, 0));
+          if (BIAS) ok = __all_sync(0xffffffffu, !valid || behind || far <= max(va, 0));
           if (ok) ok = edge ? fast(mm, Masked<true>()) : fast(mm, Masked<false>());
           if ((CAP || BIAS) && !ok) {
             zero();
