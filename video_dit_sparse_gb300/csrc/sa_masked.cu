@@ -887,12 +887,17 @@ __global__ void __launch_bounds__(128) sa_masked_join_kernel(const __grid_consta
   if (q >= a.Nq) return;
   const int64_t row0 = int64_t(su) * a.splits * a.unit_rows + t * 128 + tr;
   float mx = -INFINITY;
-  for (int s = lane; s < a.splits; s += 32) mx = fmaxf(mx, a.part_lse[row0 + s * a.unit_rows]);
+  bool none = false;  // a partial result that is not a number makes the row none (fmaxf drops it)
+  for (int s = lane; s < a.splits; s += 32) {
+    const float l = a.part_lse[row0 + s * a.unit_rows];
+    mx = fmaxf(mx, l);
+    none |= l != l;
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   constexpr int V = D / 32;
   float acc[V] = {}, sum = 0.f;
-  if (mx != -INFINITY) {
+  if (mx != -INFINITY || __any_sync(0xffffffffu, none)) {
 #pragma unroll 8
     for (int s = 0; s < a.splits; ++s) {
       const int64_t row = row0 + s * a.unit_rows;
@@ -957,9 +962,13 @@ __global__ void __launch_bounds__(512) sa_masked_join_quads_kernel(const __grid_
         f[i][0] = x.x, f[i][1] = x.y, f[i][V - 2] = y.x, f[i][V - 1] = y.y;
       }
     }
+    bool none = false;  // (fmaxf drops what is not a number; it makes the sums none)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, l[i]);
-    if (top == -INFINITY) continue;
+    for (int i = 0; i < 8; ++i) {
+      top = fmaxf(top, l[i]);
+      none |= l[i] != l[i];
+    }
+    if (top == -INFINITY && !none) continue;
     const float keep = __expf(mx - top);
     mx = top;
     sum *= keep;
@@ -985,9 +994,9 @@ __global__ void __launch_bounds__(512) sa_masked_join_quads_kernel(const __grid_
   float all = -INFINITY, total = 0.f, x = 0.f;
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) all = fmaxf(all, s_mx[w]);
-  if (all != -INFINITY)
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
+  for (int w = 0; w < WARPS; ++w)
+    if (s_sum[w] != 0.f) {  // (a NaN is not 0)
       const float e = __expf(s_mx[w] - all);
       total += e * s_sum[w];
       x += e * s_acc[w][c];
