@@ -488,9 +488,10 @@ sa_status sparse_attn_rope(const sa_rope* rope, int32_t H0, const void* x0, cons
  * q, k, v bf16; o bf16 or fp32 by out_dtype; P is rounded to bf16 for the
  * second product (o is normalised by the sum of the rounded values), all sums
  * are fp32.  Hq / Hkv <= 128; B Hq <= 2^24, Hq / Hkv Nq < 2^32 and B Hkv times
- * the tiles of 128 / (Hq / Hkv) queries <= 2^30.  Keys and values past a row's document
- * never reach it, whatever they hold; a NaN or an infinite V row inside the
- * document may reach other rows of the same document that do not see it.
+ * the tiles of 128 / (Hq / Hkv) queries <= 2^30.  Keys and values that a row does not
+ * see never reach it, whatever they hold (documents packed side by side, later
+ * keys of the same document).  Values that are not finite cost time: rows
+ * computed beside rows that see them are computed once more, one by one.
  * Few rows split the keys over the GPU: the workspace (256-byte aligned, may
  * be NULL when its size is 0) holds the partial results, and two calls that
  * may overlap on the GPU need two workspaces.

@@ -100,10 +100,11 @@ struct MBars {
     int part, q0, b, hk;   // partial result (-1: whole), first query, batch entry, key head
   } ring[2];
   int flag[T * 4][2];
+  uint32_t again[T * 8]; // rows that each softmax warp computes once more
   int first[T == 1 ? kSms : 1], runs[T == 1 ? kSms : 1];  // slots of each batch entry (share_out)
   int used;
   uint32_t tmem_base;
-  int abort;
+  int abort, steps;  // steps: of rows_again
 };
 
 // Unit number -> key head of the batch and row block.
@@ -178,6 +179,126 @@ __device__ __forceinline__ void share_out(const MaskedArgs& a, Bars* bars, int l
   __syncwarp();
 }
 
+// Waits as mbar_wait does, but only gives up after kWaitLimitCycles in which no warp computed
+// rows again: abort[1] counts their steps.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_test(bar, parity)) return true;
+  long long t0 = clock64();
+  int steps = 0;
+  while (true) {
+    if (mbar_test(bar, parity)) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      if (abort[1] == steps) {
+        *abort = 1;
+        return false;
+      }
+      steps = abort[1];
+      t0 = clock64();
+    }
+  }
+}
+
+// Rows whose o is computed again, from the keys they see alone.  The second product meets every
+// key of a tile, and P = 0 times a NaN or an infinity is a NaN; so rows whose o is not finite,
+// though their scores are, and that do not see every key of their unit's run, are worked out
+// here, in fp32 with P rounded to bf16 as there.  Nothing calls this on finite values (looking
+// for others costs two operations an output value, in units whose rows do not all see the same
+// keys).  A warp takes the rows of `again` one by one, 32 keys at a time, for its half of the
+// columns; eight lanes share a key's products.  The partner warp, which has the other half,
+// calls it with the same rows: o may be in q's place, so a row is written when both have read
+// q.  False: to give up.
+struct AgainRow {
+  int hq, qi;
+  float m;     // the row's reference
+  int unused;
+  int64_t at;  // where its half row goes, in bytes
+};
+template <int D, bool QUADS>
+__device__ __noinline__ bool rows_again(const MaskedArgs& a, const AgainRow* rows, uint32_t again, int b, int part,
+                                        int key0, int n, int barrier, volatile int* abort) {
+  constexpr int V = D / 64;  // columns a lane, and pieces of 16 bytes of a key
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = (warp >> 2) & 1;
+  constexpr int kStep = QUADS ? BN : 32;  // (quads: the quarter's 32 of each tile's keys)
+  const int first = key0 + (QUADS ? (warp & 3) * 32 : 0);
+  for (; again; again &= again - 1) {
+    const AgainRow x = rows[__ffs(again) - 1];
+    const Span sp = row_span(a.mask, b, x.qi);
+    const float nslope = a.slopes ? -__ldg(a.slopes + x.hq) * kLog2e : 0.f;
+    const int hk = x.hq / a.R, end = min(key0 + n * BN, sp.hi);
+    const uint16_t* q = a.q + int64_t(b) * a.qs.b + int64_t(x.hq) * a.qs.h + int64_t(x.qi) * a.qs.n + (lane & 7) * 8;
+    const uint16_t* k = a.k + int64_t(b) * a.ks.b + int64_t(hk) * a.ks.h + (lane & 7) * 8;
+    const uint16_t* v = a.v + int64_t(b) * a.vs.b + int64_t(hk) * a.vs.h + half * (D / 2) + lane * V;
+    uint4 qr[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) qr[e] = *reinterpret_cast<const uint4*>(q + e * 64);
+    float acc[V] = {}, sum = 0.f;
+    for (int c0 = first + (sp.lo > first ? (sp.lo - first) / kStep * kStep : 0); c0 < end; c0 += kStep) {
+      if (lane == 0) atomicAdd(const_cast<int*>(abort) + 1, 1);
+      float s = 0.f;  // of key c0 + lane
+#pragma unroll 4
+      for (int i = 0; i < 8; ++i) {  // keys 4 i .. 4 i + 3
+        const int c = c0 + 4 * i + (lane >> 3);
+        float d = 0.f;
+        if (c < end) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const uint4 kr = __ldg(reinterpret_cast<const uint4*>(k + c * a.ks.n + e * 64));
+            const uint32_t qw[4] = {qr[e].x, qr[e].y, qr[e].z, qr[e].w}, kw[4] = {kr.x, kr.y, kr.z, kr.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              d = fmaf(__uint_as_float(qw[w] << 16), __uint_as_float(kw[w] << 16), d);
+              d = fmaf(__uint_as_float(qw[w] & 0xFFFF0000u), __uint_as_float(kw[w] & 0xFFFF0000u), d);
+            }
+          }
+        }
+#pragma unroll
+        for (int o = 4; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        d = __shfl_sync(0xffffffffu, d, (lane & 3) * 8);
+        if (lane >> 2 == i) s = d;
+      }
+      const int c = c0 + lane;
+      const bool sees = c >= sp.lo && c < end;
+      if (a.neg_scale) s = -s;
+      float y = s * a.scale_log2;
+      if (a.cap_log2 > 0.f) y = fmaf(-2.f * a.cap_log2, fast_rcp(1.f + fast_exp2(s * a.cap_k1)), a.cap_log2);
+      y = fmaf(nslope, fabsf(static_cast<float>(sp.pos - c)), y);
+      const float p = sees ? __uint_as_float(pack_bf16(fast_exp2(y - x.m), 0.f) << 16) : 0.f;
+      sum += p;
+      const uint32_t some = __ballot_sync(0xffffffffu, sees);
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) {
+        const float w = __shfl_sync(0xffffffffu, p, i);
+        if (!(some >> i & 1)) continue;
+        const uint16_t* row = v + (c0 + i) * a.vs.n;
+        if (V == 2) {
+          const uint32_t z = __ldg(reinterpret_cast<const uint32_t*>(row));
+          acc[0] = fmaf(w, __uint_as_float(z << 16), acc[0]);
+          acc[V - 1] = fmaf(w, __uint_as_float(z & 0xFFFF0000u), acc[V - 1]);
+        } else {
+          acc[0] = fmaf(w, __uint_as_float(uint32_t(__ldg(row)) << 16), acc[0]);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float2 y = make_float2(acc[0] / sum, acc[V - 1] / sum);
+    named_barrier(barrier, 64);
+    if (*abort) return false;  // (as after any meeting of the pair)
+    const bool wide = part >= 0 || a.out_fp32;
+    char* to = (part >= 0 ? reinterpret_cast<char*>(a.part_o) : static_cast<char*>(a.o)) + x.at + lane * V * (wide ? 4 : 2);
+    if (V == 2 && wide)
+      *reinterpret_cast<float2*>(to) = y;
+    else if (V == 2)
+      *reinterpret_cast<uint32_t*>(to) = pack_bf16(y.x, y.y);
+    else if (wide)
+      *reinterpret_cast<float*>(to) = y.x;
+    else
+      *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(pack_bf16(y.x, 0.f));
+  }
+  return true;
+}
+
 template <bool M>
 struct Masked {
   static constexpr bool value = M;
@@ -197,6 +318,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
   constexpr int S = C::kStages;
   constexpr int W = 16;  // S columns a register buffer holds
   static_assert(!QUADS || T == 1, "quads have one tile");
+  static_assert(sizeof(MBars<T, S>) <= 1024 + (T == 1 ? 2048 : 0), "shared memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem;
@@ -232,7 +354,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
     mbar_init(&bars->tail, 1);
     mbar_init(&bars->tail_here, T);
     for (int i = 0; i < T; ++i) mbar_init(&bars->turn[i], 1);
-    bars->abort = 0;
+    bars->abort = bars->steps = 0;
     fence_mbar_init();
   }
   if (a.qn * a.R < 128) {  // Q rows that no copy fills are zero for good
@@ -297,7 +419,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
       return *abort == 0;
     };
     for (uint32_t i = 0;; ++i) {
-      if (!mbar_wait(&bars->ring_full[i & 1], (i >> 1) & 1, abort)) goto done;
+      if (!bar_wait(&bars->ring_full[i & 1], (i >> 1) & 1, abort)) goto done;
       const Unit x = bars->ring[i & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->ring_empty[i & 1]);
@@ -320,7 +442,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         // S buffer and its phase: one buffer a tile, or one tile's two in turn
         const uint32_t sb = T == 2 ? t : (tc + j) & 1;
         if (T == 1) sbase = tmem + lane_base + sb * 128 + col0;
-        if (!mbar_wait(&bars->sfull[sb], (T == 2 ? tc + j : (tc + j) >> 1) & 1, abort)) goto done;
+        if (!bar_wait(&bars->sfull[sb], (T == 2 ? tc + j : (tc + j) >> 1) & 1, abort)) goto done;
         if (idle) {
           mbar_arrive(&bars->pfull[sb]);
           continue;
@@ -491,7 +613,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
           lr *= alpha;
           // O holds PV of every earlier tile: with two Q tiles its commit came with
           // this S.  (j > 0, and no later PV has been issued.)
-          if (T == 1 && !mbar_wait(&bars->pvdone[(tc + j - 1) & 1], ((tc + j - 1) >> 1) & 1, abort)) goto done;
+          if (T == 1 && !bar_wait(&bars->pvdone[(tc + j - 1) & 1], ((tc + j - 1) >> 1) & 1, abort)) goto done;
           __syncwarp();
           tc_fence_after();
 #pragma unroll
@@ -517,7 +639,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
       }
       tc += n;
       if (n > 0) {
-        if (!mbar_wait(&bars->ofull[t], uc & 1, abort)) goto done;
+        if (!bar_wait(&bars->ofull[t], uc & 1, abort)) goto done;
         ++uc;
         __syncwarp();
         tc_fence_after();
@@ -546,7 +668,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         char* base = x.part >= 0 ? reinterpret_cast<char*>(a.part_o) : static_cast<char*>(a.o);
         int64_t at = x.part >= 0 ? prow * D : int64_t(x.b) * a.os.b + int64_t(hq) * a.os.h + int64_t(qi) * a.os.n;
         at = valid ? (at + half * (D / 2)) * (wide ? 4 : 2) : -1;
-        uint32_t v[D / 2];
+        uint32_t v[D / 2], again = 0;  // again: rows to be computed once more (rows_again)
         if (n > 0) {
 #pragma unroll
           for (int c = 0; c < D / 64; ++c) tmem_ld32(obase + c * 32, v + c * 32);
@@ -559,11 +681,22 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
 #pragma unroll
             for (int y = 0; y < D / 2; ++y) v[y] = inv == 0.f ? 0 : v[y];
           }
+          // Values that are not finite may be those of keys that the row does not see.
+          const bool blind = valid && (sp.lo > key0 || sp.hi < min(key0 + n * BN, x.uhi));
+          if (__any_sync(0xffffffffu, blind)) {
+            uint32_t top[2] = {0, 0};  // the largest magnitude's bits
+#pragma unroll
+            for (int y = 0; y < D / 2; ++y) top[y & 1] = max(top[y & 1], v[y] & 0x7FFFFFFFu);
+            again = __ballot_sync(0xffffffffu, blind && max(top[0], top[1]) >= 0x7F800000u && inv != 0.f && isfinite(l));
+          }
         } else {
 #pragma unroll
           for (int y = 0; y < D / 2; ++y) v[y] = 0;
         }
-        if (!pair_sync()) goto done;  // the other half has read this warp's slot
+        if (lane == 0) bars->again[warp] = again;
+        if (!pair_sync()) goto done;  // (also: the other half has read this warp's slot)
+        again |= bars->again[warp ^ 4];
+        if (again >> lane & 1) at = -1;
         auto put = [&](auto words) {  // words per half row
           constexpr int P = decltype(words)::value / 4;                // 16-byte pieces of it
           constexpr int kRows = C::kWarpBytes / 16 / P;                // rows at a time
@@ -596,6 +729,14 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
             v[y] = pack_bf16(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1]));
           put(Words<D / 4>());
         }
+        if (again) {
+          AgainRow* rows = reinterpret_cast<AgainRow*>(own);
+          const int64_t row = x.part >= 0 ? prow * D : int64_t(x.b) * a.os.b + int64_t(hq) * a.os.h + int64_t(qi) * a.os.n;
+          rows[lane] = {hq, qi, m, 0, (row + half * (D / 2)) * (wide ? 4 : 2)};
+          __syncwarp();
+          if (!rows_again<D, QUADS>(a, rows, again, x.b, x.part, key0, n, 1 + t * 4 + quarter, abort)) goto done;
+          __syncwarp();
+        }
       } else if (n > 0) {
         mbar_arrive(&bars->ofree[t]);
       }
@@ -619,7 +760,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
     const uint32_t k_lo = static_cast<uint32_t>(dk), k_hi = static_cast<uint32_t>(dk >> 32);
     const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
     const uint32_t o_tmem = tmem + C::kOCol + t * D;
-    auto ready = [&](uint32_t i) -> bool { return mbar_wait(&bars->full[i % S], (i / S) & 1, abort); };
+    auto ready = [&](uint32_t i) -> bool { return bar_wait(&bars->full[i % S], (i / S) & 1, abort); };
     auto pass = [&]() { mbar_arrive(&bars->turn[t ^ 1]); };  // the other tile's turn
     auto sbuf = [&](uint32_t step) -> uint32_t { return T == 2 ? t : step & 1; };
     auto qk = [&](uint32_t i, uint32_t step, bool turn) {
@@ -646,7 +787,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
       bool ok = true;
       uint32_t tc = 0, uc = 0, zc = 0;  // key tiles, units with keys and cleared tails so far
       for (uint32_t i = 0; ok; ++i) {
-        if (!mbar_wait(&bars->ring_full[i & 1], (i >> 1) & 1, abort)) break;
+        if (!bar_wait(&bars->ring_full[i & 1], (i >> 1) & 1, abort)) break;
         const Unit x = bars->ring[i & 1];
         mbar_arrive(&bars->ring_empty[i & 1]);
         if (!x.go) break;
@@ -654,11 +795,11 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         if (n == 0) continue;
         // Ring entries: K(j) is number 2 (tc + j), V(j) the one behind it.
         if (T == 1 && !second) {
-          if (!(ok = mbar_wait(&bars->qfull, uc & 1, abort))) break;
+          if (!(ok = bar_wait(&bars->qfull, uc & 1, abort))) break;
           for (int j = 0; j < n; ++j) {
             const uint32_t step = tc + j, ik = 2 * step, was = step - 2;
             // (the second product of two steps ago is done: S and P of this buffer are free)
-            if (!(ok = ready(ik)) || (step >= 2 && !(ok = mbar_wait(&bars->pvdone[was & 1], (was >> 1) & 1, abort)))) break;
+            if (!(ok = ready(ik)) || (step >= 2 && !(ok = bar_wait(&bars->pvdone[was & 1], (was >> 1) & 1, abort)))) break;
             tc_fence_after();
             qk(ik, step, false);
             mma_commit(&bars->empty[ik % S]);
@@ -674,10 +815,10 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
             if (!(ok = ready(iv))) break;
             if (j == 0 && uhi - (key0 + (n - 1) * BN) < BN) {  // to be cleared behind the span
               mbar_arrive(&bars->tail_here);
-              if (!(ok = mbar_wait(&bars->tail, zc++ & 1, abort))) break;
+              if (!(ok = bar_wait(&bars->tail, zc++ & 1, abort))) break;
             }
-            if (j == 0 && uc > 0 && !(ok = mbar_wait(&bars->ofree[t], (uc - 1) & 1, abort))) break;
-            if (!(ok = mbar_wait(&bars->pfull[step & 1], (step >> 1) & 1, abort))) break;
+            if (j == 0 && uc > 0 && !(ok = bar_wait(&bars->ofree[t], (uc - 1) & 1, abort))) break;
+            if (!(ok = bar_wait(&bars->pfull[step & 1], (step >> 1) & 1, abort))) break;
             tc_fence_after();
             pv(iv, step, j == 0);
             mma_commit(&bars->pvdone[step & 1]);
@@ -688,7 +829,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
           ++uc;
           continue;
         }
-        if (!(ok = mbar_wait(&bars->qfull, uc & 1, abort)) || !(ok = ready(2 * tc))) break;
+        if (!(ok = bar_wait(&bars->qfull, uc & 1, abort)) || !(ok = ready(2 * tc))) break;
         tc_fence_after();
         qk(2 * tc, tc, false);
         mma_commit(&bars->empty[(2 * tc) % S]);
@@ -699,13 +840,13 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
           if (!(ok = ready(iv)) || (more && !(ok = ready(ik)))) break;
           const bool tail = j == 0 && uhi - (key0 + (n - 1) * BN) < BN;  // to be cleared behind the span
           if (tail) mbar_arrive(&bars->tail_here);
-          if (tail && !(ok = mbar_wait(&bars->tail, zc++ & 1, abort))) break;
-          if (j == 0 && uc > 0 && !(ok = mbar_wait(&bars->ofree[t], (uc - 1) & 1, abort))) break;
+          if (tail && !(ok = bar_wait(&bars->tail, zc++ & 1, abort))) break;
+          if (j == 0 && uc > 0 && !(ok = bar_wait(&bars->ofree[t], (uc - 1) & 1, abort))) break;
           // Turns: the tiles' steps alternate (side by side they would fall into
           // step and leave the tensor core idle during both softmaxes).
-          if (tc + j + t > 0 && !(ok = mbar_wait(&bars->turn[t], (tc + j + t - 1) & 1, abort))) break;
+          if (tc + j + t > 0 && !(ok = bar_wait(&bars->turn[t], (tc + j + t - 1) & 1, abort))) break;
           // (P last: even a wait for what is long done takes about 100 cycles)
-          if (!(ok = mbar_wait(&bars->pfull[t], (tc + j) & 1, abort))) break;
+          if (!(ok = bar_wait(&bars->pfull[t], (tc + j) & 1, abort))) break;
           tc_fence_after();
           pv(iv, tc + j, j == 0);
           if (more)
@@ -730,11 +871,12 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
   } else if (warp == C::kTailWarp) {
     // ------------------------------------------------------------ tails
     // V rows past the span (another document's, or a cache's unused rows) meet
-    // P = 0, but 0 times a NaN or an infinity would still reach O: cleared.
-    // The MMA warps say when such a tile has landed.
+    // P = 0, but 0 times a NaN or an infinity would still reach O of every row: cleared.
+    // The MMA warps say when such a tile has landed.  (Rows inside the span that only
+    // some of the unit's rows see: rows_again.)
     uint32_t tc = 0, zc = 0;
     for (uint32_t i = 0;; ++i) {
-      if (!mbar_wait(&bars->ring_full[i & 1], (i >> 1) & 1, abort)) break;
+      if (!bar_wait(&bars->ring_full[i & 1], (i >> 1) & 1, abort)) break;
       const Unit x = bars->ring[i & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->ring_empty[i & 1]);
@@ -750,7 +892,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
       tc += x.n;
       const int live = x.uhi - (x.key0 + (x.n - 1) * BN);
       if (x.n == 0 || live >= BN) continue;
-      if (!mbar_wait(&bars->tail_here, zc++ & 1, abort)) break;
+      if (!bar_wait(&bars->tail_here, zc++ & 1, abort)) break;
       uint8_t* vt = sKV + (iv % S) * C::kTile;
       for (int f = lane; f < (BN - live) * (D / 8); f += 32) {
         const int r = live + f / (D / 8), ch = f % (D / 8);
@@ -816,12 +958,12 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         x.key0 = none ? 0 : ulo + j0 * BN;
       }
       const int key0 = x.key0, n = x.n;
-      if (i >= 2 && !mbar_wait(&bars->ring_empty[i & 1], ((i >> 1) - 1) & 1, abort)) break;
+      if (i >= 2 && !bar_wait(&bars->ring_empty[i & 1], ((i >> 1) - 1) & 1, abort)) break;
       bars->ring[i & 1] = x;
       mbar_arrive(&bars->ring_full[i & 1]);
       if (g < 0) break;
       if (n > 0) {
-        if (uc > 0 && !mbar_wait(&bars->qempty, (uc - 1) & 1, abort)) break;
+        if (uc > 0 && !bar_wait(&bars->qempty, (uc - 1) & 1, abort)) break;
         ++uc;
         constexpr int kCopies = QUADS ? 4 : T;  // of one tile, or of each
         mbar_expect_tx(&bars->qfull, kCopies * a.qn * a.R * D * 2);
@@ -833,7 +975,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
                         x.q0 + (QUADS ? 0 : t * a.qn), x.b, &bars->qfull);
         for (int f = 0; f < 2 * n; ++f, ++it) {
           const uint32_t s = it % S;
-          if (!(ok = mbar_wait(&bars->empty[s], ((it / S) & 1) ^ 1, abort))) break;
+          if (!(ok = bar_wait(&bars->empty[s], ((it / S) & 1) ^ 1, abort))) break;
           mbar_expect_tx(&bars->full[s], C::kTile);
           const int key = key0 + (n - 1 - (f >> 1)) * BN;
 #pragma unroll
@@ -843,7 +985,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
         }
         if (!ok) break;
       }
-      if (!(ok = mbar_wait(&bars->next, i & 1, abort))) break;
+      if (!(ok = bar_wait(&bars->next, i & 1, abort))) break;
       g = answered_block(&bars->answer);
       fence_proxy_async_smem();  // read before the next answer is written
     }
