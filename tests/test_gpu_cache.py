@@ -331,3 +331,30 @@ def test_a_step_in_a_graph():
         got = [t.clone() for t in (o, acc, kept)]
         want = step()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2], kept)
+
+
+@pytest.mark.parametrize("H,Hk,Nq,Nk,causal,key", [(1, 1, 1, 300, 0, 5), (3, 1, 200, 200, 1, 190), (3, 1, 200, 500, 1, 490),
+                                                  (6, 2, 100, 300, 33, 299), (2, 2, 40, 300, 0, 7)])
+@pytest.mark.parametrize("cap", [0.0, 9.0])
+def test_weights_of_a_key_that_is_not_finite(H, Hk, Nq, Nk, causal, key, cap):
+    """Rows whose score is -inf give the key nothing; rows without a finite lse add nothing to any key; rows that do not
+    see it do not meet it.  So a key with such a score keeps decay * w."""
+    from video_dit_sparse_gb300 import binding as sa
+    q, k, v = tensors(1, H, Hk, Nq, Nk, 64, seed=41)
+    w = torch.rand(1, Hk, Nk, device="cuda")
+    k0 = k.clone()
+    k0[:, :, key] = 0
+    for bad in ("nan", "low") if cap == 0 else ("nan",):  # (under a cap the score of -inf is -cap)
+        if bad == "nan":
+            k[:, :, key] = float("nan")
+        else:
+            q[..., 9] = q[..., 9].abs() + 0.25
+            k[:, :, key] = 0
+            k[:, :, key, 9] = -float("inf")
+        _, lse = sa.sparse_attn_forward_masked(q, k, v, causal=causal, cap=cap)
+        got = sa.sparse_attn_cache_weights(q, k, lse, w, decay=0.9, causal=causal, cap=cap)
+        want, tol = weights_want(q, k0, lse, None, decay=0.0, causal=causal, cap=cap)
+        want[:, :, key] = tol[:, :, key] = 0
+        w64 = w.double().cpu().numpy()
+        want, tol = want + 0.9 * w64, tol + 2.0 ** -22 * np.abs(0.9 * w64)
+        assert (np.abs(got.double().cpu().numpy() - want) <= tol).all()

@@ -111,6 +111,21 @@ __device__ __forceinline__ WUnit unit_at(const MaskedArgs& a, const WPlan& p, in
   return x;
 }
 
+// A key's sum over the rows from column `first` on that have a finite lse (L: theirs in exp2
+// units, negated; -inf: another column), without a cap: for tiles whose plain sum is no number.
+__device__ __noinline__ float sum_of_rows(float scale_log2, uint32_t sbase, int H, int first, const float* L) {
+  float sum = 0.f;
+  for (int c = 0; c < H; c += 16) {
+    float x[16];
+    tmem_ld16(sbase + c, reinterpret_cast<uint32_t*>(x));
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (c + e >= first && L[c + e] != -INFINITY) sum += fast_exp2(fmaf(x[e], scale_log2, L[c + e]));
+  }
+  return sum;
+}
+
 }  // namespace
 
 template <int D, bool CAP, bool BIAS>
@@ -246,11 +261,14 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
         __syncwarp();
         tc_fence_after();
         uint64_t acc[2] = {0, 0};
-        // An exponent from its raw product and -lse.  With a cap: exactly (three MUFU
+        // An exponent from its raw product and -lse (-inf: no row's).  With a cap: exactly (three MUFU
         // results), or (`quick`) tanh(z)/z by the masked forward's polynomial for
         // |z| <= 0.4; a tile with a larger score is summed again exactly.
         auto exponent = [&](float x, float L) -> float {
-          if (CAP) return fmaf(-2.f * a.cap_log2, fast_rcp(1.f + fast_exp2(x * a.cap_k1)), a.cap_log2) + L;
+          if (CAP) {
+            const float y = fmaf(-2.f * a.cap_log2, fast_rcp(1.f + fast_exp2(x * a.cap_k1)), a.cap_log2) + L;
+            return L == -INFINITY ? L : y;
+          }
           return fmaf(x, sl, L);
         };
         // The plain columns of the tile: the next 32 load while 32 are summed.
@@ -261,7 +279,7 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
           const uint64_t k1 = f2(a.cap_p1, a.cap_p1), k2 = f2(a.cap_p2, a.cap_p2), k3 = f2(a.cap_p3, a.cap_p3);
           auto bent = [&](float x0, float x1, uint64_t L) -> uint64_t {
             const uint64_t xx = f2(x0, x1), w = mul2(xx, xx);
-            wm = fmax3(wm, f2lo(w), f2hi(w));
+            wm = fmax3_nan(wm, f2lo(w), f2hi(w));
             return fma2(xx, fma2(w, fma2(w, fma2(w, k3, k2), k1), sl2), L);
           };
 #pragma unroll
@@ -366,6 +384,16 @@ __global__ void __launch_bounds__(WCfg::kThreads, 1)
           quick = false;
           acc[0] = acc[1] = 0;
           plain();
+        }
+        // Columns of no row are zeros, which an infinity or a NaN in K turns into NaN.  (Under a cap
+        // the exact form leaves them out: the square of such a product is past the limit.)
+        if (!CAP && !(BIAS || edge || dead)) {
+          const uint64_t s2 = add2(acc[0], acc[1]);
+          const float is = f2lo(s2) + f2hi(s2);
+          if (__any_sync(0xffffffffu, key < x.len && is != is)) {
+            acc[0] = f2(sum_of_rows(sl, sbase, H, first, wL), 0.f);
+            acc[1] = 0;
+          }
         }
         tc_fence_before();
         mbar_arrive(&bars->dempty[d]);

@@ -474,6 +474,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// The same, a NaN if any is one.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // acc + both bf16 halves of a packed pair (each widened exactly to fp32).
 __device__ __forceinline__ float add_bf16x2(uint32_t packed, float acc) {
   float r;
