@@ -429,8 +429,9 @@ typedef struct {
  * number i of axis a turns by t = p_a * f, f = theta^(-2i / axis_dim[a]) (or
  * inv_freq, over all pairs):
  *   (x, y) -> (x cos t - y sin t, x sin t + y cos t);  inverse: by -t, which is
- * also the gradient.  Angles are exact to 2^-24 of a half turn at every
- * 32-bit position.
+ * also the gradient.  p f is reduced by whole turns before it is rounded: the
+ * angle is within 2^-24 of a half turn at every 32-bit position, for f as given
+ * (below 2^40) or as theta's power rounded to a double.
  */
 typedef struct {
   int32_t B, N, d;

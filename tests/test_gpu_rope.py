@@ -146,3 +146,23 @@ def test_stream_graph_and_repeated_input():
     assert torch.equal(out, sa.sparse_attn_rope(x, **kw))
     one = x[:1, :1].expand(2, 3, 50, 128)
     assert torch.equal(sa.sparse_attn_rope(one, **kw)[1, 2], sa.sparse_attn_rope(one[:1, :1], **kw)[0, 0])
+
+
+@pytest.mark.parametrize("freq", [3.14159, 100.0, 64.7, 1e6, 1.0, 0.8, -2.7182818, 1e-9])
+def test_far_positions_of_given_frequencies(freq):
+    """The angle p f is reduced exactly, whatever the size of f: a cosine and a sine within 2^-24 half turns of it and
+    two units of sincospi."""
+    from decimal import Decimal, getcontext
+    from video_dit_sparse_gb300 import binding as sa
+    getcontext().prec = 60
+    pi = Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+    pos = [2 ** 31 - 1, -2 ** 31, 2 ** 30 + 12345, -1999999999, 7, 0, 1, -1]
+    x = torch.zeros(1, 1, len(pos), 64, device="cuda")
+    x[..., 0] = 1.0
+    y = sa.sparse_attn_rope(x, axes=(2,), inv_freq=[freq], positions=torch.tensor(pos, dtype=torch.int32, device="cuda")[:, None])
+    got = y[0, 0, :, :2].double().cpu().numpy()
+    for i, p in enumerate(pos):
+        turns = Decimal(freq) * p / (2 * pi)
+        t = 2 * np.pi * float(turns - turns.to_integral_value())
+        # 2^-24 of a half turn: 2^-24 pi; sincospi: 2^-22; the two products and their sum: 2^-24
+        assert np.abs(got[i] - [np.cos(t), np.sin(t)]).max() <= 2.0 ** -24 * np.pi + 2.0 ** -22 + 2.0 ** -24, (p, got[i])

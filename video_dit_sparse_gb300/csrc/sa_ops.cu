@@ -105,6 +105,21 @@ bool views_overlap(const View& a, const View& b, int64_t d, int esz) {
   return m < block_a || g - m < block_b;
 }
 
+// f / 2 pi modulo 1 as a 64-bit fraction of a turn, to its last bits for every double f below
+// 2^40 or so: 1 / 2 pi is taken to twice a double's digits (a double's alone would leave an error
+// that 2^31 positions multiply to f 2^-22 of a radian).
+uint64_t turn_fraction(double f) {
+  constexpr double kInv1 = 0.15915494309189535, kInv2 = -9.839338337591243e-18;  // their sum is 1 / 2 pi to 2^-108
+  volatile double rounded = f * kInv1;  // (not to be fused with what follows)
+  const double hi = rounded, lo = std::fma(f, kInv1, -hi) + f * kInv2;
+  auto fraction = [](double x) -> uint64_t {
+    x -= std::trunc(x);  // exact
+    const uint64_t m = static_cast<uint64_t>(std::ldexp(std::fabs(x), 64));
+    return x < 0.0 ? 0 - m : m;
+  };
+  return fraction(hi) + fraction(lo);
+}
+
 // Shapes and options of sa_masked; fills everything but the tensor pointers.
 sa_status check_masked(const sa_masked* p, sa::MaskedArgs* a) {
   if (!p) return SA_ERR_INVALID_ARG;
@@ -382,14 +397,12 @@ sa_status sparse_attn_rope(const sa_rope* p, int32_t H0, const void* x0, const s
   if (a.rot < 2 || a.rot > p->d) return SA_ERR_INVALID_ARG;
   if (p->pairing == SA_ROPE_HALF && a.rot % 16) return SA_ERR_UNSUPPORTED;  // 16-byte halves
   if (!p->inv_freq && !(std::isfinite(p->theta) && p->theta > 0.0)) return SA_ERR_INVALID_ARG;
-  const double two_pi = 6.283185307179586476925;
   for (int x = 0; x < p->axes; ++x)
     for (int i = a.first[x]; i < a.first[x + 1]; ++i) {
       const double f = p->inv_freq ? p->inv_freq[i]
                                    : std::pow(p->theta, -2.0 * (i - a.first[x]) / p->axis_dim[x]);
       if (!std::isfinite(f)) return SA_ERR_INVALID_ARG;
-      const double turns = f / two_pi, part = turns - std::floor(turns);  // [0, 1]
-      a.turn[i] = part >= 1.0 ? 0 : static_cast<uint64_t>(std::ldexp(part, 64));
+      a.turn[i] = turn_fraction(f);
     }
   for (int i = a.rot / 2; i < 64; ++i) a.turn[i] = 0;
   a.vox = {};

@@ -6,9 +6,11 @@
 //
 // Angles.  p f_i reaches thousands of turns for far positions, where an fp32
 // product keeps no digit of the fraction.  The host passes f_i / 2 pi as a
-// 64-bit fixed-point fraction of a turn; p times that, modulo 2^64, is the
-// exact fraction of a turn (positions are whole numbers), whose top 32 bits go
-// to sincospi.  Error: below 2^-24 of a half turn, at any 32-bit position.
+// 64-bit fixed-point fraction of a turn (below 2^-62 off, whatever f_i); p times
+// that, modulo 2^64, is the fraction of a turn that p f_i ends on (positions are
+// whole numbers), whose top 32 bits go to sincospi.  Error: 2^-30 of a half turn
+// from the product at |p| = 2^31, 2^-31 from the bits left out and 2^-25 from the
+// conversion to fp32: below 2^-24 of a half turn at any 32-bit position.
 //
 // The kernel is bound by HBM (each row is read and written once; 24 + 24 heads of
 // 69120 rows of 128: 259 us, 97 % of the measured copy rate).  A thread
