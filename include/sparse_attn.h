@@ -443,7 +443,7 @@ typedef struct {
   double theta;              /* > 0; ignored with inv_freq */
   const double* inv_freq;    /* host, r/2 values, or NULL */
   const int32_t* positions;  /* device int32 [B, N, axes], or NULL: the grid */
-  int64_t positions_b;       /* elements between batch entries (0: shared by all) */
+  int64_t positions_b;       /* elements between batch entries (0: shared by all), <= 2^40 */
   sa_voxel_grid grid;        /* positions NULL: token n's (t, h, w), axes = 3, T*Hh*W = N */
   int32_t voxel_order;       /* 0: raster order, 1: the order of sparse_attn_voxel_permute */
   int64_t offset[3];         /* added to the grid's positions (frames generated so far, ...) */

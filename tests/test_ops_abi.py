@@ -249,3 +249,13 @@ def test_evict_form():
     assert O.evict([0, np.nan, -np.inf, 0], 4, 3, 0, 0).tolist() == [0, 2, 3]
     assert O.evict([0.0, -0.0, 0.0], 3, 2, 0, 0).tolist() == [0, 1]
     assert O.evict([3, 2, 1], 2, 2, 0, 0).tolist() == [0, 1]
+
+
+def test_rope_refuses_positions_beyond_any_memory(sa):
+    """A stride whose bytes do not fit 64 bits must not pass as a short one."""
+    p = sa.sa_rope(3, 30, 64, 1)
+    p.axis_dim[0], p.theta, p.positions = 64, 1e4, A16
+    st = sa.sa_strides(2 * 30 * 64, 30 * 64, 64)
+    for far in (2 ** 61, 2 ** 62, 2 ** 63 - 1, 2 ** 41):
+        p.positions_b = far
+        assert sa.lib.sparse_attn_rope(p, 2, 1 << 24, st, 2 << 24, st, 0, None, None, None, None, None) == INVALID

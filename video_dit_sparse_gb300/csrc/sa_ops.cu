@@ -410,7 +410,7 @@ sa_status sparse_attn_rope(const sa_rope* p, int32_t H0, const void* x0, const s
   a.pos_b = p->positions_b;
   a.voxel_order = 0;
   if (p->positions) {
-    if (!aligned(p->positions, 4) || p->positions_b < 0 ||
+    if (!aligned(p->positions, 4) || p->positions_b < 0 || (p->B > 1 && p->positions_b > (int64_t(1) << 40)) ||
         (p->positions_b && p->positions_b < int64_t(p->N) * p->axes))
       return SA_ERR_INVALID_ARG;
     for (int i = 0; i < 3; ++i) a.offset[i] = 0;
@@ -473,7 +473,7 @@ sa_status sparse_attn_rope(const sa_rope* p, int32_t H0, const void* x0, const s
     if (H[i] && (!in_device_allocation(x[i], nx[i]) || !in_device_allocation(y[i], ny[i])))
       return SA_ERR_INVALID_ARG;
   if (p->positions &&
-      !in_device_allocation(p->positions, (uint64_t(p->B - 1) * p->positions_b + uint64_t(p->N) * p->axes) * 4))
+      !in_device_allocation(p->positions, (uint64_t(p->B - 1) * uint64_t(p->positions_b) + uint64_t(p->N) * p->axes) * 4))
     return SA_ERR_INVALID_ARG;
   a.B = p->B;
   a.N = p->N;
