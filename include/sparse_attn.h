@@ -505,7 +505,7 @@ typedef struct {
   float cap;                      /* >= 0 */
   const float* slopes;            /* device fp32 [Hq] or NULL */
   int32_t causal;
-  int32_t ndocs;
+  int32_t ndocs;                  /* <= 2^30 */
   const int32_t* docs_q;          /* device */
   const int32_t* docs_k;
   const int32_t* prefix;

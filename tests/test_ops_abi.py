@@ -259,3 +259,11 @@ def test_rope_refuses_positions_beyond_any_memory(sa):
     for far in (2 ** 61, 2 ** 62, 2 ** 63 - 1, 2 ** 41):
         p.positions_b = far
         assert sa.lib.sparse_attn_rope(p, 2, 1 << 24, st, 2 << 24, st, 0, None, None, None, None, None) == INVALID
+
+
+def test_more_documents_than_their_indexes_hold_are_refused(sa):
+    """Indexes of documents, and sums of two of them, are 32-bit."""
+    for n in (2 ** 30 + 1, 2 ** 31 - 1):
+        p = masked(sa, B=2, ndocs=n, docs_q=A16, docs_k=A16)
+        assert forward(sa, p) == UNSUPPORTED
+        assert sa.lib.sparse_attn_cache_weights(p, Q, K, LSE, None, OUT, 0.0, None, None) == UNSUPPORTED

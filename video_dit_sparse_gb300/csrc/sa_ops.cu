@@ -139,7 +139,7 @@ sa_status check_masked(const sa_masked* p, sa::MaskedArgs* a) {
   if (R > 128) return SA_ERR_UNSUPPORTED;  // a Q tile holds all of a query's heads
   // key coordinates and numbers of Q tiles are 32-bit with room for a tile behind them
   const int64_t heads = int64_t(p->B) * p->Hkv, qn = 128 / R;
-  if (p->Nq > (1 << 30) || p->Nk > (1 << 30) || heads * R > (1 << 24) ||
+  if (p->Nq > (1 << 30) || p->Nk > (1 << 30) || p->ndocs > (1 << 30) || heads * R > (1 << 24) ||
       heads * ((p->Nq + qn - 1) / qn) > (1 << 30) || R * p->Nq > UINT32_MAX)
     return SA_ERR_UNSUPPORTED;
   a->qs = p->q;
