@@ -20,7 +20,8 @@
 // the columns.  With many rows the tensor core is the floor, and two things come
 // near it: an exponential a pair (0.8 of its time on the MUFU) and shared memory
 // (both MMA operands, 3/4 of the time, and the reads of lse): 12 heads of 7040 rows x
-// 35200 keys take 591 us, 61 % of the measured bf16 rate.  With one token per
+// 35200 keys take 590 us, 61 % of the measured bf16 rate.  (With a cap 932; with two or
+// three documents 525 to 610; with a bias 2960, every tile by column: `careful`.)  With one token per
 // sequence the bound is the read of K (256-key units of one Q tile: 83 200 keys of 6
 // heads, 128 MB, in 27 us).
 #include <cooperative_groups.h>

@@ -24,7 +24,7 @@
 // raise it).
 // Only the key span that the unit's rows see is read; tiles that every row
 // sees whole skip the mask.  A step of both tiles takes 1.59 us, 1.1 of them MMAs
-// (12 heads, 7040 rows x 28160 keys, frame-causal: 787 us, 71 % of the measured
+// (12 heads, 7040 rows x 28160 keys, frame-causal: 791 us, 71 % of the measured
 // bf16 rate).
 //
 // A block starts with its own unit and then takes units of blocks that have not
@@ -492,8 +492,8 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
           ++xn;
           return true;
         };
-        // P = exp2(score - mm) as bf16 pairs, its fp32 sum (for lse) and the sum
-        // of the rounded values, which normalises O (so that O stays a convex
+        // P = exp2(score - mm) as bf16 pairs (the second product's two operands have one type, V's:
+        // half a step of 2^-8 of each weight), its fp32 sum (for lse) and the sum of the rounded values, which normalises O (so that O stays a convex
         // combination of V rows whatever the rounding of P to bf16).
         uint32_t p[H / 2];
         uint64_t ps[2];
@@ -904,7 +904,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
     }
   } else if (warp == C::kTmaWarp) {
     // ------------------------------------------------------------ units and loads
-      if (lane) goto done;
+    if (lane) goto done;
     const uint32_t q_addr = smem_u32(sQ), kv_addr = smem_u32(sKV);
     int64_t g = blockIdx.x;
     uint32_t it = 0, uc = 0;
