@@ -103,3 +103,21 @@ def test_each_column_on_its_own():
         assert bool(torch.isnan(seen).all()) if np.isnan(bad) else bool((seen == bad).all())
         o[0, :, key:, column] = want[0, :, key:, column]
     check(o, lse, q, k, v0, causal=1)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hk,Nq,Nk", [(4, 2, 1, 9001), (1, 1, 1, 880), (3, 1, 10, 3001), (40, 1, 2, 3001), (2, 2, 300, 700)])
+def test_an_infinite_value_that_every_row_sees(H, Hk, Nq, Nk, d):
+    """It comes out as it is, in its own column: split keys and rows in every lane quarter included."""
+    q, k, v = tensors(1, H, Hk, Nq, Nk, d, seed=63, sigma=0.5)
+    v[0, 0, Nk // 2, 7], v[0, 0, 100, 9], v[0, 0, Nk - 2, 20] = INF, -INF, NAN
+    v0 = torch.nan_to_num(v, posinf=0.0, neginf=0.0)
+    o, lse = run(q, k, v, out_dtype=torch.float32)
+    want, wl = run(q, k, v0, out_dtype=torch.float32)
+    assert torch.equal(lse, wl)
+    heads = slice(0, H // Hk)
+    assert bool((o[0, heads, :, 7] == INF).all()) and bool((o[0, heads, :, 9] == -INF).all())
+    assert bool(torch.isnan(o[0, heads, :, 20]).all())
+    for column in (7, 9, 20):
+        o[0, heads, :, column] = want[0, heads, :, column]
+    check(o, lse, q, k, v0)

@@ -201,10 +201,10 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatil
 
 // Rows whose o is computed again, from the keys they see alone.  The second product meets every
 // key of a tile, and P = 0 times a NaN or an infinity is a NaN; so rows whose o is not finite,
-// though their scores are, and that do not see every key of their unit's run, are worked out
-// here, in fp32 with P rounded to bf16 as there.  Nothing calls this on finite values (looking
-// for others costs two operations an output value, in units whose rows do not all see the same
-// keys).  A warp takes the rows of `again` one by one, 32 keys at a time, for its half of the
+// though their scores are, and that do not see every key of their unit's run (or, in quads, take
+// a quarter of it) are worked out here, in fp32 with P rounded to bf16 as there.  Nothing calls
+// this on finite values (looking for others costs two operations an output value, where rows may
+// need it).  A warp takes the rows of `again` one by one, 32 keys at a time, for its half of the
 // columns; eight lanes share a key's products.  The partner warp, which has the other half,
 // calls it with the same rows: o may be in q's place, so a row is written when both have read
 // q.  False: to give up.
@@ -681,8 +681,9 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
 #pragma unroll
             for (int y = 0; y < D / 2; ++y) v[y] = inv == 0.f ? 0 : v[y];
           }
-          // Values that are not finite may be those of keys that the row does not see.
-          const bool blind = valid && (sp.lo > key0 || sp.hi < min(key0 + n * BN, x.uhi));
+          // Values that are not finite may be those of keys that the row does not see (quads: that
+          // the quarter does not take, where an infinity would become a NaN).
+          const bool blind = valid && (QUADS || sp.lo > key0 || sp.hi < min(key0 + n * BN, x.uhi));
           if (__any_sync(0xffffffffu, blind)) {
             uint32_t top[2] = {0, 0};  // the largest magnitude's bits
 #pragma unroll
