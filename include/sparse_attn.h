@@ -461,6 +461,65 @@ sa_status sparse_attn_rope(const sa_rope* rope, int32_t H0, const void* x0, cons
                            const sa_strides* x1_strides, void* y1, const sa_strides* y1_strides,
                            sa_stream_t stream);
 
+#define SA_NORM_RMS 0   /* by the root mean square */
+#define SA_NORM_LAYER 1 /* by mean and variance */
+
+/*
+ * Every head's row normalised over its d values and rotated by its position
+ * in one pass (queries and keys of a layer right behind their projections):
+ *   y = R (n w + b),  n = (x - mu) / sqrt(mean (x - mu)^2 + eps),
+ * mu = 0 (SA_NORM_RMS) or the row's mean (SA_NORM_LAYER), R the rotation that
+ * `rope` describes as for sparse_attn_rope (inverse 0).  All of it is fp32,
+ * rounded once.
+ */
+typedef struct {
+  sa_rope rope;
+  int32_t norm;
+  int32_t weight_dtype; /* SA_OUT_BF16 or SA_OUT_FP32, of weights and biases */
+  float eps;            /* >= 0 */
+} sa_norm_rope;
+
+typedef struct {
+  int32_t H;          /* heads; 0: nothing to do (side 1) */
+  const void* x;      /* view [B, H, N, d] of rope.dtype; may repeat a dimension */
+  sa_strides xs;
+  void* y;            /* view [B, H, N, d]: x's own, or apart from every other tensor */
+  sa_strides ys;
+  const void* weight; /* device [d], shared by the heads; NULL: ones */
+  const void* bias;   /* device [d]; NULL: zeros */
+} sa_norm_side;
+
+/* side1 may be NULL.  Asynchronous. */
+sa_status sparse_attn_norm_rope(const sa_norm_rope* norm, const sa_norm_side* side0, const sa_norm_side* side1,
+                                sa_stream_t stream);
+
+/*
+ * The gradient of sparse_attn_norm_rope from x (not y) and dy:
+ *   g = R^-1 dy,  h = g w,  dx = (h - n mean(h n) - mu') / sqrt(...),
+ * mu' = mean h for SA_NORM_LAYER, else 0; dweight = sum of g n and dbias = sum of g
+ * over all rows of all heads (written, not added to).  The sums have a fixed
+ * order: the same inputs give the same bits.  dx may be x's or dy's view.  The
+ * workspace (256-byte aligned) is needed for dweight or dbias; calls that may overlap
+ * on the GPU need one each.
+ */
+typedef struct {
+  int32_t H;
+  const void* x;
+  sa_strides xs;
+  const void* dy; /* may repeat a dimension */
+  sa_strides dys;
+  void* dx;
+  sa_strides dxs;
+  const void* weight;
+  float* dweight; /* device fp32 [d] or NULL */
+  float* dbias;   /* device fp32 [d] or NULL */
+} sa_norm_grad_side;
+
+size_t sparse_attn_norm_rope_backward_workspace_size(const sa_norm_rope* norm, int32_t H0, int32_t H1);
+sa_status sparse_attn_norm_rope_backward(const sa_norm_rope* norm, const sa_norm_grad_side* side0,
+                                         const sa_norm_grad_side* side1, void* workspace, size_t workspace_bytes,
+                                         sa_stream_t stream);
+
 /*
  * Attention with masks, capped scores and a distance bias.  Hq query heads
  * share Hkv key heads (Hq a multiple of Hkv; query head h reads key head
@@ -561,6 +620,55 @@ typedef struct {
 sa_status sparse_attn_cache_evict(const sa_evict* problem, const float* weights, const void* k, const void* v,
                                   int32_t* kept, void* k_out, void* v_out, float* weights_out,
                                   sa_stream_t stream);
+
+/*
+ * A key-value cache in 8 bits: e4m3 codes (four exponent bits, three of the
+ * mantissa; 0x7F and 0xFF are NaN, there is no infinity) with an fp32 scale for
+ * each head and block of tokens; a value is code * scale.  A scale that is not a
+ * positive finite number marks an empty block, whose values are 0 whatever its codes
+ * (a new cache: scales of 0).
+ */
+typedef struct {
+  int32_t B, Hkv, N, d;       /* N: tokens that a head has room for, <= 2^30; d in {64, 128} */
+  int32_t block;              /* tokens of a block: 16, 32, 64 or 128 */
+  void* k;                    /* views [B, Hkv, N, d] of codes */
+  void* v;
+  sa_strides ks, vs;
+  float* k_scale;             /* views [B, Hkv, ceil(N / block)] */
+  float* v_scale;
+  sa_strides k_scales, v_scales; /* b and h; the blocks of a head follow one another (n is ignored) */
+} sa_cache8;
+
+/*
+ * Writes tokens start[b] .. start[b] + counts[b] - 1 of every head (start NULL:
+ * start0 for all; counts NULL: n for all, else clamped to 0 .. n) from k and v,
+ * bf16 views [B, Hkv, n, d] that may repeat a dimension.  Tokens outside the cache
+ * are left out.
+ *
+ *  - A block that the call writes whole takes the least power of two (2^-126 at
+ *    least; 0 for a block of zeros) that brings its largest finite magnitude to 448
+ *    or below.  A block that it writes in part takes that of its new tokens or the
+ *    scale that it had, the larger of the two; its other tokens keep their values
+ *    (their codes are rounded again where the scale grows; an empty block's are
+ *    zeros).
+ *  - Codes are x / scale rounded to nearest, ties to even.  Infinities and NaN are
+ *    held as NaN.
+ *
+ * No view may share memory with another tensor of the call.  Asynchronous.
+ */
+sa_status sparse_attn_cache8_append(const sa_cache8* cache, int32_t n, const void* k, const sa_strides* ks,
+                                    const void* v, const sa_strides* vs, const int32_t* start, int32_t start0,
+                                    const int32_t* counts, sa_stream_t stream);
+
+/*
+ * Tokens first[b] .. first[b] + n - 1 (first NULL: first0 for all) of every head as
+ * values: k_out, v_out views [B, Hkv, n, d] of out_dtype, either may be NULL; bf16
+ * is exact where a scale is a power of two, else rounded.  Tokens outside the cache
+ * are 0.  Asynchronous.
+ */
+sa_status sparse_attn_cache8_read(const sa_cache8* cache, const int32_t* first, int32_t first0, int32_t n,
+                                  int32_t out_dtype, void* k_out, const sa_strides* ks, void* v_out,
+                                  const sa_strides* vs, sa_stream_t stream);
 
 /*
  * Checks index lists without trapping: row_ptr[0] == 0, row_ptr[rows] == nnz,

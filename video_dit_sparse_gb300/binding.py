@@ -11,6 +11,7 @@ import ctypes
 import math
 import os
 import struct
+from typing import NamedTuple
 
 import torch
 
@@ -87,6 +88,33 @@ class sa_evict(ctypes.Structure):
                 ("v", sa_strides), ("k_out", sa_strides), ("v_out", sa_strides)]
 
 
+SA_NORM_RMS, SA_NORM_LAYER = 0, 1
+_NORMS = {"rms": SA_NORM_RMS, "layer": SA_NORM_LAYER}
+
+
+class sa_norm_rope(ctypes.Structure):
+    _fields_ = [("rope", sa_rope), ("norm", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class sa_norm_side(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int32), ("x", ctypes.c_void_p), ("xs", sa_strides), ("y", ctypes.c_void_p),
+                ("ys", sa_strides), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class sa_norm_grad_side(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int32), ("x", ctypes.c_void_p), ("xs", sa_strides), ("dy", ctypes.c_void_p),
+                ("dys", sa_strides), ("dx", ctypes.c_void_p), ("dxs", sa_strides), ("weight", ctypes.c_void_p),
+                ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p)]
+
+
+class sa_cache8(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("N", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("block", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ks", sa_strides),
+                ("vs", sa_strides), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("k_scales", sa_strides), ("v_scales", sa_strides)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -137,6 +165,17 @@ def _load():
     lib.sparse_attn_cache_weights.restype = ctypes.c_int
     lib.sparse_attn_cache_evict.argtypes = [P(sa_evict), vp, vp, vp, vp, vp, vp, vp, vp]
     lib.sparse_attn_cache_evict.restype = ctypes.c_int
+    i32, sz = ctypes.c_int32, ctypes.c_size_t
+    lib.sparse_attn_norm_rope.argtypes = [P(sa_norm_rope), P(sa_norm_side), P(sa_norm_side), vp]
+    lib.sparse_attn_norm_rope.restype = ctypes.c_int
+    lib.sparse_attn_norm_rope_backward_workspace_size.argtypes = [P(sa_norm_rope), i32, i32]
+    lib.sparse_attn_norm_rope_backward_workspace_size.restype = sz
+    lib.sparse_attn_norm_rope_backward.argtypes = [P(sa_norm_rope), P(sa_norm_grad_side), P(sa_norm_grad_side), vp, sz, vp]
+    lib.sparse_attn_norm_rope_backward.restype = ctypes.c_int
+    lib.sparse_attn_cache8_append.argtypes = [P(sa_cache8), i32, vp, ps, vp, ps, vp, i32, vp, vp]
+    lib.sparse_attn_cache8_append.restype = ctypes.c_int
+    lib.sparse_attn_cache8_read.argtypes = [P(sa_cache8), vp, i32, i32, i32, vp, ps, vp, ps, vp]
+    lib.sparse_attn_cache8_read.restype = ctypes.c_int
     lib.sparse_attn_validate_index.argtypes = [P(sa_problem), vp, vp, i64, vp, vp]
     lib.sparse_attn_validate_index.restype = ctypes.c_int
     lib.sparse_attn_status_string.argtypes = [ctypes.c_int]
@@ -441,7 +480,15 @@ _ROPE = struct.Struct("@10id2Pq6ii3q")
 assert _MASKED.size == ctypes.sizeof(sa_masked) and _EVICT.size == ctypes.sizeof(sa_evict)
 assert _ROPE.size == ctypes.sizeof(sa_rope)
 _STRIDES = struct.Struct("@3q")
+_NORM = struct.Struct("@10id2Pq6ii3q2if")
+_SIDE = struct.Struct("@iP3qP3q2P")
+_GRAD_SIDE = struct.Struct("@iP3qP3qP3q3P")
+_CACHE8 = struct.Struct("@5i2P6q2P6q")
+assert _NORM.size <= ctypes.sizeof(sa_norm_rope) and sa_norm_rope.eps.offset + 4 == _NORM.size
+assert _SIDE.size == ctypes.sizeof(sa_norm_side) and _GRAD_SIDE.size == ctypes.sizeof(sa_norm_grad_side)
+assert _CACHE8.size == ctypes.sizeof(sa_cache8)
 _bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
 _empty, _empty_like = torch.empty, torch.empty_like
 _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
@@ -458,6 +505,13 @@ _c_masked = _by_bytes("sparse_attn_forward_masked", [_cp] + [_vp] * 7 + [ctypes.
 _c_masked_ws = _by_bytes("sparse_attn_forward_masked_workspace_size", [_cp], ctypes.c_size_t)
 _c_weights = _by_bytes("sparse_attn_cache_weights", [_cp] + [_vp] * 5 + [ctypes.c_float, _vp, _vp])
 _c_evict = _by_bytes("sparse_attn_cache_evict", [_cp] + [_vp] * 8)
+_c_norm = _by_bytes("sparse_attn_norm_rope", [_cp, _cp, _cp, _vp])
+_c_norm_grad_ws = _by_bytes("sparse_attn_norm_rope_backward_workspace_size", [_cp, ctypes.c_int32, ctypes.c_int32],
+                            ctypes.c_size_t)
+_c_norm_grad = _by_bytes("sparse_attn_norm_rope_backward", [_cp, _cp, _cp, _vp, ctypes.c_size_t, _vp])
+_c_append8 = _by_bytes("sparse_attn_cache8_append", [_cp, ctypes.c_int32, _vp, _cp, _vp, _cp, _vp, ctypes.c_int32, _vp, _vp])
+_c_read8 = _by_bytes("sparse_attn_cache8_read", [_cp, _vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _vp, _cp, _vp,
+                                                 _cp, _vp])
 
 
 def _view(t: torch.Tensor, dtype, name: str, dev: int):
@@ -481,6 +535,11 @@ def _flat(t, dtype, name, dev, shape=None) -> int:
     return t.data_ptr()
 
 
+def _nothing(call, *args, **options):
+    """The call for its effect alone (on another stream: of tensors that the caller keeps)."""
+    call(*args, **options)
+
+
 def _elsewhere(dev: int, stream, call, *args, **options):
     """The call with the tensors' device current and, when one is given, on `stream`: what the call
     makes and fills is made there, and its results are not reused while the caller's stream may
@@ -497,6 +556,38 @@ def _elsewhere(dev: int, stream, call, *args, **options):
             if t is not None:
                 t.record_stream(here)
     return made
+
+
+def _rope_fields(shape, dtype, dev, axes, theta, inv_freq, pairing, grid, voxel, offset, positions):
+    """The rotation's fields for a tensor [B, H, N, d] (inverse 0), and what must live until the launch."""
+    B, _, N, d = shape
+    na = len(axes)
+    if not 1 <= na <= 3:
+        raise ValueError("one to three axes")
+    if pairing not in _PAIRINGS:
+        raise ValueError("pairing must be 'interleaved' or 'half'")
+    freq, host = 0, None
+    if inv_freq is not None:
+        f = [float(x) for x in inv_freq]
+        if len(f) != sum(axes) // 2:
+            raise ValueError("inv_freq must have one value per rotated pair")
+        host = (ctypes.c_double * len(f))(*f)
+        freq = ctypes.addressof(host)
+    if (positions is None) == (grid is None):
+        raise ValueError("positions or grid, and not both")
+    pos = pos_b = 0
+    cells, order = (0, 0, 0, 0, 0, 0), 0
+    if positions is not None:
+        if voxel is not None or any(offset):
+            raise ValueError("voxel and offset go with grid")
+        shared = positions.dim() == 2
+        pos = _flat(positions, _i32, "positions", dev, (N, na) if shared else (B, N, na))
+        pos_b = 0 if shared else N * na
+    else:
+        order = 0 if voxel is None else 1
+        cells = (*grid, *(voxel or (0, 0, 0)))
+    return (B, N, d, na, *axes, *(0,) * (3 - na), _PAIRINGS[pairing], _OUT[dtype], 0, theta, freq, pos, pos_b, *cells,
+            order, *offset), host
 
 
 def sparse_attn_rope(q: torch.Tensor, k: torch.Tensor | None = None, *, axes=(44, 42, 42),
@@ -526,33 +617,8 @@ def sparse_attn_rope(q: torch.Tensor, k: torch.Tensor | None = None, *, axes=(44
             raise ValueError("k must be [B, Hk, N, d] with q's B, N and d")
     elif ok is not None:
         raise ValueError("an output for k without k")
-    na = len(axes)
-    if not 1 <= na <= 3:
-        raise ValueError("one to three axes")
-    if pairing not in _PAIRINGS:
-        raise ValueError("pairing must be 'interleaved' or 'half'")
-    freq = 0
-    if inv_freq is not None:
-        f = [float(x) for x in inv_freq]
-        if len(f) != sum(axes) // 2:
-            raise ValueError("inv_freq must have one value per rotated pair")
-        host = (ctypes.c_double * len(f))(*f)
-        freq = ctypes.addressof(host)
-    if (positions is None) == (grid is None):
-        raise ValueError("positions or grid, and not both")
-    pos = pos_b = 0
-    cells, order = (0, 0, 0, 0, 0, 0), 0
-    if positions is not None:
-        if voxel is not None or any(offset):
-            raise ValueError("voxel and offset go with grid")
-        shared = positions.dim() == 2
-        pos = _flat(positions, _i32, "positions", dev, (N, na) if shared else (B, N, na))
-        pos_b = 0 if shared else N * na
-    else:
-        order = 0 if voxel is None else 1
-        cells = (*grid, *(voxel or (0, 0, 0)))
-    p = _ROPE.pack(B, N, d, na, *axes, *(0,) * (3 - na), _PAIRINGS[pairing], _OUT[dtype],
-                   1 if inverse else 0, theta, freq, pos, pos_b, *cells, order, *offset)
+    fields, host = _rope_fields(q.shape, dtype, dev, axes, theta, inv_freq, pairing, grid, voxel, offset, positions)
+    p = _ROPE.pack(*fields[:9], 1 if inverse else 0, *fields[10:])
     y = _empty_like(q) if oq is None else oq
     if y.shape != q.shape:
         raise ValueError("out must have q's shape")
@@ -754,6 +820,231 @@ def sparse_attn_cache_evict(weights: torch.Tensor, k: torch.Tensor | None, v: to
     return kept, ko, vo, wo
 
 
+def _norm_vectors(dtype, dev, d, named):
+    """The addresses of the given [d] vectors (0 for None) and whether they are fp32."""
+    kinds = {t.dtype for _, t in named if t is not None}
+    if len(kinds) > 1:
+        raise ValueError("weights and biases must have one dtype")
+    kind = kinds.pop() if kinds else _f32
+    if kind is not _f32 and kind is not dtype:
+        raise ValueError("weights and biases must be float32 or of q's dtype")
+    return [_flat(t, kind, name, dev, (d,)) for name, t in named], _OUT[kind]
+
+
+def sparse_attn_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, *, norm: str = "rms",
+                          q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                          q_bias: torch.Tensor | None = None, k_bias: torch.Tensor | None = None,
+                          eps: float = 1e-6, axes=(44, 42, 42), theta: float = 10000.0, inv_freq=None,
+                          pairing: str = "interleaved", grid=None, voxel=None, offset=(0, 0, 0),
+                          positions: torch.Tensor | None = None, out=None, stream=None):
+    """Every head's row of q (and k) normalised over d, scaled, shifted and rotated by its position in one
+    pass: [B, H, N, d] bf16 or fp32 views; returns the new q, or (q, k) when k is given.
+
+    norm: "rms" (by the root mean square) or "layer" (by mean and variance).  Weights and biases are [d],
+    shared by the heads, fp32 or of q's dtype (None: ones, zeros).  The positions are as in
+    sparse_attn_rope.  out: the output (or a pair of them); it may be the input."""
+    dtype, dev = q.dtype, q.get_device()
+    if dev >= 0 and (stream is not None or dev != _current_device()):
+        return _elsewhere(dev, stream, sparse_attn_norm_rope, q, k, norm=norm, q_weight=q_weight, k_weight=k_weight,
+                          q_bias=q_bias, k_bias=k_bias, eps=eps, axes=axes, theta=theta, inv_freq=inv_freq,
+                          pairing=pairing, grid=grid, voxel=voxel, offset=offset, positions=positions, out=out)
+    if dtype not in _OUT:
+        raise ValueError("q must be bfloat16 or float32")
+    if norm not in _NORMS:
+        raise ValueError("norm must be 'rms' or 'layer'")
+    qs = _view(q, dtype, "q", dev)
+    B, H, N, d = q.shape
+    oq, ok = out if isinstance(out, (tuple, list)) else (out, None)
+    if k is None:
+        if ok is not None or k_weight is not None or k_bias is not None:
+            raise ValueError("an output, weight or bias for k without k")
+    else:
+        ks = _view(k, dtype, "k", dev)
+        if k.shape[0] != B or k.shape[2] != N or k.shape[3] != d:
+            raise ValueError("k must be [B, Hk, N, d] with q's B, N and d")
+    (qw, kw, qb, kb), kind = _norm_vectors(dtype, dev, d, (("q_weight", q_weight), ("k_weight", k_weight),
+                                                           ("q_bias", q_bias), ("k_bias", k_bias)))
+    fields, host = _rope_fields(q.shape, dtype, dev, axes, theta, inv_freq, pairing, grid, voxel, offset, positions)
+    y = _empty_like(q) if oq is None else oq
+    if y.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    side0 = _SIDE.pack(H, q.data_ptr(), *qs, y.data_ptr(), *_view(y, dtype, "out", dev), qw, qb)
+    z = side1 = None
+    if k is not None:
+        z = _empty_like(k) if ok is None else ok
+        if z.shape != k.shape:
+            raise ValueError("out of k must have k's shape")
+        side1 = _SIDE.pack(k.shape[1], k.data_ptr(), *ks, z.data_ptr(), *_view(z, dtype, "out of k", dev), kw, kb)
+    st = _c_norm(_NORM.pack(*fields, _NORMS[norm], kind, eps), side0, side1, _current_stream(dev))
+    if st != SA_OK:
+        raise SparseAttnError(st, "sparse_attn_norm_rope")
+    return y if k is None else (y, z)
+
+
+def sparse_attn_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.Tensor,
+                                   k: torch.Tensor | None = None, *, norm: str = "rms",
+                                   q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                                   q_bias: torch.Tensor | None = None, k_bias: torch.Tensor | None = None,
+                                   eps: float = 1e-6, axes=(44, 42, 42), theta: float = 10000.0, inv_freq=None,
+                                   pairing: str = "interleaved", grid=None, voxel=None, offset=(0, 0, 0),
+                                   positions: torch.Tensor | None = None, out=None,
+                                   workspace: torch.Tensor | None = None, stream=None):
+    """The gradient of sparse_attn_norm_rope: from the gradients dq (and dk) of its outputs and its inputs q
+    (and k), with the same options.  Returns (dq, dq_weight, dq_bias), and for k's (dk, dk_weight, dk_bias) behind
+    them: the inputs' gradients in their dtype, the [d] vectors' in fp32 (None where the vector was None).
+    out: the input gradient's tensor (or a pair of them); it may be dq or q."""
+    dtype, dev = q.dtype, q.get_device()
+    if dev >= 0 and (stream is not None or dev != _current_device()):
+        return _elsewhere(dev, stream, sparse_attn_norm_rope_backward, dq, dk, q, k, norm=norm, q_weight=q_weight,
+                          k_weight=k_weight, q_bias=q_bias, k_bias=k_bias, eps=eps, axes=axes, theta=theta,
+                          inv_freq=inv_freq, pairing=pairing, grid=grid, voxel=voxel, offset=offset,
+                          positions=positions, out=out, workspace=workspace)
+    if dtype not in _OUT:
+        raise ValueError("q must be bfloat16 or float32")
+    if norm not in _NORMS:
+        raise ValueError("norm must be 'rms' or 'layer'")
+    if (k is None) != (dk is None):
+        raise ValueError("k and dk come together")
+    qs, gs = _view(q, dtype, "q", dev), _view(dq, dtype, "dq", dev)
+    B, H, N, d = q.shape
+    if dq.shape != q.shape:
+        raise ValueError("dq must have q's shape")
+    oq, ok = out if isinstance(out, (tuple, list)) else (out, None)
+    Hk = 0
+    if k is None:
+        if ok is not None or k_weight is not None or k_bias is not None:
+            raise ValueError("an output, weight or bias for k without k")
+    else:
+        ks, hs, Hk = _view(k, dtype, "k", dev), _view(dk, dtype, "dk", dev), k.shape[1]
+        if k.shape[0] != B or k.shape[2] != N or k.shape[3] != d or dk.shape != k.shape:
+            raise ValueError("k and dk must be [B, Hk, N, d] with q's B, N and d")
+    (qw, kw, qb, kb), kind = _norm_vectors(dtype, dev, d, (("q_weight", q_weight), ("k_weight", k_weight),
+                                                           ("q_bias", q_bias), ("k_bias", k_bias)))
+    fields, host = _rope_fields(q.shape, dtype, dev, axes, theta, inv_freq, pairing, grid, voxel, offset, positions)
+    p = _NORM.pack(*fields, _NORMS[norm], kind, eps)
+    y = _empty_like(q) if oq is None else oq
+    if y.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    # one allocation holds the vectors' gradients
+    need = sum(1 for x in (qw, qb, kw, kb) if x)
+    sums = iter(_empty((need, d), dtype=_f32, device=q.device).unbind(0)) if need else iter(())
+    dqw, dqb, dkw, dkb = (next(sums) if x else None for x in (qw, qb, kw, kb))
+    at = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    side0 = _GRAD_SIDE.pack(H, q.data_ptr(), *qs, dq.data_ptr(), *gs, y.data_ptr(), *_view(y, dtype, "out", dev), qw,
+                            at(dqw), at(dqb))
+    z = side1 = None
+    if k is not None:
+        z = _empty_like(k) if ok is None else ok
+        if z.shape != k.shape:
+            raise ValueError("out of k must have k's shape")
+        side1 = _GRAD_SIDE.pack(Hk, k.data_ptr(), *ks, dk.data_ptr(), *hs, z.data_ptr(),
+                                *_view(z, dtype, "out of k", dev), kw, at(dkw), at(dkb))
+    if need and workspace is None:
+        workspace = _empty(_c_norm_grad_ws(p, H, Hk), dtype=torch.uint8, device=q.device)
+    st = _c_norm_grad(p, side0, side1, _flat(workspace, torch.uint8, "workspace", dev),
+                      0 if workspace is None else workspace.numel(), _current_stream(dev))
+    if st != SA_OK:
+        raise SparseAttnError(st, "sparse_attn_norm_rope_backward")
+    return (y, dqw, dqb) if k is None else (y, dqw, dqb, z, dkw, dkb)
+
+
+class Cache8(NamedTuple):
+    """A key-value cache in 8 bits: k, v [B, Hk, N, d] e4m3 codes (float8_e4m3fn or uint8 views), k_scale, v_scale
+    fp32 [B, Hk, ceil(N / block)]; a value is code * scale.  A scale that is not a positive finite number marks
+    an empty block of zeros.  sparse_attn_cache8 makes an empty one."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+    block: int
+
+
+def sparse_attn_cache8(B: int, Hk: int, N: int, d: int, *, block: int = 128, device=None) -> Cache8:
+    """An empty cache with room for N tokens of every head."""
+    device = torch.device("cuda" if device is None else device)
+    k, v = (torch.zeros((B, Hk, N, d), dtype=torch.float8_e4m3fn, device=device) for _ in range(2))
+    ks, vs = (torch.zeros((B, Hk, -(-N // block)), dtype=_f32, device=device) for _ in range(2))
+    return Cache8(k, v, ks, vs, block)
+
+
+def _cache8_fields(cache, dev):
+    """The packed sa_cache8 of a cache on device `dev`, and its B, Hk, N, d."""
+    k, v, ks, vs, block = cache
+    shape = k.shape
+    if k.dtype not in _E4M3 or v.dtype is not k.dtype or dev < 0:
+        raise ValueError("the cache's k and v must be CUDA tensors [B, Hk, N, d] of float8_e4m3fn (or uint8)")
+    kst, vst = _view(k, k.dtype, "the cache's k", dev), _view(v, v.dtype, "the cache's v", dev)
+    if v.shape != shape:
+        raise ValueError("the cache's v must have its k's shape")
+    B, H, N, d = shape
+    blocks = -(-N // block)
+    for name, t in (("k_scale", ks), ("v_scale", vs)):
+        if t.dtype is not _f32 or t.get_device() != dev or t.dim() != 3 or t.shape != (B, H, blocks):
+            raise ValueError(f"the cache's {name} must be float32 [B, Hk, ceil(N / block)] on its k's device")
+        if t.stride(2) != 1 and blocks != 1:
+            raise ValueError(f"the cache's {name} must have a contiguous last dimension")
+    return _CACHE8.pack(B, H, N, d, block, k.data_ptr(), v.data_ptr(), *kst, *vst, ks.data_ptr(), vs.data_ptr(),
+                        ks.stride(0), ks.stride(1), 1, vs.stride(0), vs.stride(1), 1), shape
+
+
+def _tokens(at, name, dev, B):
+    """A first token given as an int or as int32 [B]: (address, int)."""
+    if isinstance(at, torch.Tensor):
+        return _flat(at, _i32, name, dev, (B,)), 0
+    return 0, int(at)
+
+
+def sparse_attn_cache8_append(cache: Cache8, k: torch.Tensor, v: torch.Tensor, start, *,
+                              counts: torch.Tensor | None = None, stream=None) -> Cache8:
+    """Writes tokens start[b] .. start[b] + n - 1 of every head into the cache, in place: k, v bf16 views
+    [B, Hk, n, d], start an int or int32 [B], counts int32 [B] (how many of the n; default: all).  Returns the cache.
+
+    A block written whole takes the least power-of-two scale that holds its largest value; one written in part
+    keeps its other tokens' values, and its scale unless the new tokens need a larger one.  Tokens outside the cache
+    are left out."""
+    dev = cache[0].get_device()
+    if dev >= 0 and (stream is not None or dev != _current_device()):
+        _elsewhere(dev, stream, _nothing, sparse_attn_cache8_append, cache, k, v, start, counts=counts)
+        return cache
+    p, (B, H, N, d) = _cache8_fields(cache, dev)
+    n = k.shape[2] if k.dim() == 4 else 0
+    if k.shape != (B, H, n, d) or v.shape != k.shape:
+        raise ValueError("k and v must be [B, Hk, n, d] with the cache's B, Hk and d")
+    at, at0 = _tokens(start, "start", dev, B)
+    st = _c_append8(p, n, k.data_ptr(), _STRIDES.pack(*_view(k, _bf16, "k", dev)), v.data_ptr(),
+                    _STRIDES.pack(*_view(v, _bf16, "v", dev)), at, at0, _flat(counts, _i32, "counts", dev, (B,)),
+                    _current_stream(dev))
+    if st != SA_OK:
+        raise SparseAttnError(st, "sparse_attn_cache8_append")
+    return cache
+
+
+def sparse_attn_cache8_read(cache: Cache8, first, n: int, *, out=None, out_dtype=torch.bfloat16, stream=None):
+    """Tokens first[b] .. first[b] + n - 1 of every head as values: (k, v) [B, Hk, n, d] in bf16 or fp32 (first: an
+    int or int32 [B]); 0 where the cache has no such token.  out: a pair (k, v) of views to write, either may be None."""
+    dev = cache[0].get_device()
+    if dev >= 0 and (stream is not None or dev != _current_device()):
+        return _elsewhere(dev, stream, sparse_attn_cache8_read, cache, first, n, out=out, out_dtype=out_dtype)
+    p, (B, H, N, d) = _cache8_fields(cache, dev)
+    if out is None:
+        out = tuple(_empty((B, H, n, d), dtype=out_dtype, device=cache[0].device) for _ in range(2))
+    ko, vo = out
+    kind = next((t.dtype for t in (ko, vo) if t is not None), None)
+    if kind not in _OUT:
+        raise ValueError("out must hold a bfloat16 or float32 tensor")
+    strides = []
+    for t in (ko, vo):
+        if t is not None and t.shape != (B, H, n, d):
+            raise ValueError("out must hold [B, Hk, n, d]")
+        strides.append(None if t is None else _STRIDES.pack(*_view(t, kind, "out", dev)))
+    at, at0 = _tokens(first, "first", dev, B)
+    st = _c_read8(p, at, at0, n, _OUT[kind], None if ko is None else ko.data_ptr(), strides[0],
+                  None if vo is None else vo.data_ptr(), strides[1], _current_stream(dev))
+    if st != SA_OK:
+        raise SparseAttnError(st, "sparse_attn_cache8_read")
+    return ko, vo
+
+
 class HostLayer:
     """One attention layer from pinned host tensors (sparse_attn_layer_from_host):
     device staging, one chunk's scratch and two copy streams, allocated once
@@ -819,3 +1110,8 @@ rope = sparse_attn_rope
 forward_masked = sparse_attn_forward_masked
 cache_weights = sparse_attn_cache_weights
 cache_evict = sparse_attn_cache_evict
+norm_rope = sparse_attn_norm_rope
+norm_rope_backward = sparse_attn_norm_rope_backward
+cache8 = sparse_attn_cache8
+cache8_append = sparse_attn_cache8_append
+cache8_read = sparse_attn_cache8_read

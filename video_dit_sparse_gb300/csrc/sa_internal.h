@@ -197,6 +197,29 @@ struct RopeArgs {
   uint64_t turn[64];       // turns per position of each pair, in units of 2^-64
 };
 cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream);
+// Everything of a rotation but its tensors: checks, and `args` filled but for x, y, xs, ys, H.
+sa_status check_rope(const sa_rope* p, int32_t H0, int32_t H1, RopeArgs* args);
+// The explicit positions lie in device memory (after device_info).
+bool rope_positions(const sa_rope* p);
+
+// New tokens into an e4m3 cache (x: bf16 keys and values), or its tokens out (y).
+struct Cache8Args {
+  const void* x[2];      // keys, values: [B, H, n, d]
+  void* y[2];            // the reading call's outputs (either may be null)
+  sa_strides xs[2];      // of x or y
+  uint8_t* codes[2];     // [B, H, N, d]
+  sa_strides cs[2];
+  float* scales[2];      // [B, H, ceil(N / block)]
+  sa_strides ss[2];      // (n unused: blocks follow one another)
+  const int32_t* start;  // [B] first token, or null: start0
+  const int32_t* counts; // [B] tokens of each entry (at most n), or null
+  int64_t start0;
+  int32_t B, H, N, d, block, n;
+  int32_t blocks;        // set by the launch: blocks of a head that n tokens can touch
+  int64_t items;         // set by the launch
+};
+cudaError_t launch_cache8_append(Cache8Args a, cudaStream_t stream);
+cudaError_t launch_cache8_read(Cache8Args a, bool wide, cudaStream_t stream);
 
 // sparse_attn_layer_from_host splits a layer into at most this many chunks.
 constexpr int kMaxPipelineChunks = 64;

@@ -6,104 +6,27 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
-#include <numeric>
 #include <utility>
 
 #include "sa_internal.h"
+#include "sa_views.h"
 #include "sparse_attn.h"
 
 namespace {
 
 using sa::aligned;
+using sa::check_view;
 using sa::device_info;
 using sa::in_device_allocation;
+using sa::overlap;
+using sa::View;
+using sa::views_overlap;
 
 // (tanh(z)/z - 1)/z^2 as a quadratic in z^2 through its Chebyshev nodes on
 // [0, 0.16]: |z| times the error stays below 1.6e-7.
 constexpr double kTanh1 = -0.3333307876878961, kTanh2 = 0.13304591654903536, kTanh3 = -0.04907868548467837;
 
 sa_status map_cuda(cudaError_t e) { return e == cudaSuccess ? SA_OK : SA_ERR_CUDA; }
-
-// A [B, H, N, d] view: 16-byte aligned rows, no negative strides.  Strides of
-// dimensions of size one are free and are replaced by the row size.  An input
-// may repeat a dimension (stride 0) where `repeats`; an output's elements must
-// not overlap.  *extent: bytes from the first to behind the last element.
-bool check_view(const void* p, sa_strides* s, int64_t B, int64_t H, int64_t N, int64_t d, int esz,
-                bool output, bool repeats, uint64_t* extent) {
-  if (!p || !aligned(p, 16)) return false;
-  struct Dim {
-    int64_t n, stride;
-  } dims[3] = {{B, s->b}, {H, s->h}, {N, s->n}};
-  int64_t last = d;  // elements
-  for (Dim& x : dims) {
-    if (x.n == 1) x.stride = d;
-    if (x.stride < 0 || x.stride >= (int64_t(1) << 38) / esz || (x.stride * esz) % 16) return false;
-    if (x.stride == 0 && !repeats) return false;
-    if (x.stride > 0 && x.n - 1 > (int64_t(1) << 45) / x.stride) return false;
-    last += (x.n - 1) * x.stride;
-  }
-  s->b = dims[0].stride;
-  s->h = dims[1].stride;
-  s->n = dims[2].stride;
-  if (output) {
-    std::sort(dims, dims + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
-    int64_t inner = d;
-    for (const Dim& x : dims)
-      if (x.n > 1) {
-        if (x.stride < inner) return false;
-        inner = x.stride * (x.n - 1) + inner;
-      }
-  }
-  *extent = static_cast<uint64_t>(last) * esz;
-  return true;
-}
-
-bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
-
-// A checked view: its first element, strides, sizes and extent in bytes.
-struct View {
-  const void* p;
-  sa_strides s;
-  int64_t B, H, N;
-  uint64_t n;
-};
-
-// Whether two views of rows of d elements (checked by check_view) may share an
-// element.  With the same strides they may interleave in one buffer (heads of a
-// fused projection): rows that follow one another make blocks, and blocks start at
-// multiples of the other strides' common divisor g from the view's start, so views
-// whose starts differ modulo g by at least the first one's block one way round and
-// the second one's the other never meet.  A dimension of size one has no stride of
-// its own and takes the other view's.
-bool views_overlap(const View& a, const View& b, int64_t d, int esz) {
-  if (!overlap(a.p, a.n, b.p, b.n)) return false;
-  struct Dim {
-    int64_t na, nb, sa, sb;
-  } dims[3] = {{a.B, b.B, a.s.b, b.s.b}, {a.H, b.H, a.s.h, b.s.h}, {a.N, b.N, a.s.n, b.s.n}};
-  for (Dim& x : dims) {
-    if (x.na == 1) x.sa = x.sb;
-    if (x.nb == 1) x.sb = x.sa;
-    if (x.sa != x.sb) return true;
-  }
-  std::sort(dims, dims + 3, [](const Dim& x, const Dim& y) { return x.sa < y.sa; });
-  int64_t block_a = d, block_b = d, g = 0;
-  for (const Dim& x : dims) {
-    if (x.na == 1 && x.nb == 1) continue;
-    if (g == 0 && x.sa == block_a && x.sa == block_b) {
-      block_a *= x.na;
-      block_b *= x.nb;
-    } else {
-      g = std::gcd(g, x.sa);
-    }
-  }
-  const int64_t apart = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) / esz;
-  if (g == 0) return apart < block_a && -apart < block_b;
-  const int64_t m = ((apart % g) + g) % g;
-  return m < block_a || g - m < block_b;
-}
 
 // f / 2 pi modulo 1 as a 64-bit fraction of a turn, to its last bits for every double f below
 // 2^40 or so: 1 / 2 pi is taken to twice a double's digits (a double's alone would leave an error
@@ -200,6 +123,82 @@ size_t masked_workspace(const sa::MaskedArgs& a) {
 }
 
 }  // namespace
+
+namespace sa {
+
+sa_status check_rope(const sa_rope* p, int32_t H0, int32_t H1, RopeArgs* args) {
+  if (!p || p->B < 1 || p->N < 1 || p->d < 1 || H0 < 1 || H1 < 0) return SA_ERR_INVALID_ARG;
+  if (p->axes < 1 || p->axes > 3 || (p->pairing != SA_ROPE_INTERLEAVED && p->pairing != SA_ROPE_HALF) ||
+      (p->dtype != SA_OUT_BF16 && p->dtype != SA_OUT_FP32))
+    return SA_ERR_INVALID_ARG;
+  if (p->d != 64 && p->d != 128) return SA_ERR_UNSUPPORTED;
+  if (p->B > 65535 || int64_t(H0) + H1 > 65535) return SA_ERR_UNSUPPORTED;  // grid.z, grid.y
+  RopeArgs& a = *args;
+  a.axes = p->axes;
+  a.rot = 0;
+  for (int i = 0; i < 4; ++i) a.first[i] = 0;
+  for (int i = 0; i < 3; ++i) {
+    const int32_t n = i < p->axes ? p->axis_dim[i] : 0;
+    if (n < 0 || n % 2 || n > p->d) return SA_ERR_INVALID_ARG;
+    a.rot += n;
+    a.first[i + 1] = a.rot / 2;
+  }
+  if (a.rot < 2 || a.rot > p->d) return SA_ERR_INVALID_ARG;
+  if (p->pairing == SA_ROPE_HALF && a.rot % 16) return SA_ERR_UNSUPPORTED;  // 16-byte halves
+  if (!p->inv_freq && !(std::isfinite(p->theta) && p->theta > 0.0)) return SA_ERR_INVALID_ARG;
+  for (int x = 0; x < p->axes; ++x)
+    for (int i = a.first[x]; i < a.first[x + 1]; ++i) {
+      const double f = p->inv_freq ? p->inv_freq[i]
+                                   : std::pow(p->theta, -2.0 * (i - a.first[x]) / p->axis_dim[x]);
+      if (!std::isfinite(f)) return SA_ERR_INVALID_ARG;
+      a.turn[i] = turn_fraction(f);
+    }
+  for (int i = a.rot / 2; i < 64; ++i) a.turn[i] = 0;
+  a.vox = {};
+  a.pos = p->positions;
+  a.pos_b = p->positions_b;
+  a.voxel_order = 0;
+  if (p->positions) {
+    if (!aligned(p->positions, 4) || p->positions_b < 0 || (p->B > 1 && p->positions_b > (int64_t(1) << 40)) ||
+        (p->positions_b && p->positions_b < int64_t(p->N) * p->axes))
+      return SA_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i) a.offset[i] = 0;
+  } else {
+    const sa_voxel_grid& g = p->grid;
+    if (p->axes != 3 || g.T < 1 || g.Hh < 1 || g.W < 1 || g.T > p->N || g.Hh > p->N || g.W > p->N)
+      return SA_ERR_INVALID_ARG;
+    if (int64_t(g.T) * g.Hh > p->N || int64_t(g.T) * g.Hh * g.W != p->N) return SA_ERR_INVALID_ARG;
+    if (p->voxel_order && (g.vt < 1 || g.vh < 1 || g.vw < 1)) return SA_ERR_INVALID_ARG;
+    const int64_t size[3] = {g.T, g.Hh, g.W};
+    for (int i = 0; i < 3; ++i) {
+      const int64_t o = p->offset[i];
+      if (o < INT32_MIN || o + size[i] - 1 > INT32_MAX) return SA_ERR_INVALID_ARG;
+      a.offset[i] = static_cast<int32_t>(o);
+    }
+    a.vox.T = g.T;
+    a.vox.Hh = g.Hh;
+    a.vox.W = g.W;
+    // a voxel larger than the grid is the grid
+    a.vox.vt = p->voxel_order ? std::min(g.vt, g.T) : g.T;
+    a.vox.vh = p->voxel_order ? std::min(g.vh, g.Hh) : g.Hh;
+    a.vox.vw = p->voxel_order ? std::min(g.vw, g.W) : g.W;
+    a.voxel_order = p->voxel_order ? 1 : 0;
+  }
+  a.B = p->B;
+  a.N = p->N;
+  a.d = p->d;
+  a.half = p->pairing == SA_ROPE_HALF;
+  a.fp32 = p->dtype == SA_OUT_FP32;
+  a.inverse = p->inverse ? 1 : 0;
+  return SA_OK;
+}
+
+bool rope_positions(const sa_rope* p) {
+  return !p->positions ||
+         in_device_allocation(p->positions, (uint64_t(p->B - 1) * uint64_t(p->positions_b) + uint64_t(p->N) * p->axes) * 4);
+}
+
+}  // namespace sa
 
 extern "C" {
 
@@ -378,63 +377,10 @@ sa_status sparse_attn_cache_evict(const sa_evict* p, const float* weights, const
 sa_status sparse_attn_rope(const sa_rope* p, int32_t H0, const void* x0, const sa_strides* x0s, void* y0,
                            const sa_strides* y0s, int32_t H1, const void* x1, const sa_strides* x1s, void* y1,
                            const sa_strides* y1s, sa_stream_t stream) {
-  if (!p || p->B < 1 || p->N < 1 || p->d < 1 || H0 < 1 || H1 < 0 || !x0s || !y0s) return SA_ERR_INVALID_ARG;
-  if (p->axes < 1 || p->axes > 3 || (p->pairing != SA_ROPE_INTERLEAVED && p->pairing != SA_ROPE_HALF) ||
-      (p->dtype != SA_OUT_BF16 && p->dtype != SA_OUT_FP32))
-    return SA_ERR_INVALID_ARG;
-  if (p->d != 64 && p->d != 128) return SA_ERR_UNSUPPORTED;
-  if (p->B > 65535 || int64_t(H0) + H1 > 65535) return SA_ERR_UNSUPPORTED;  // grid.z, grid.y
+  if (!x0s || !y0s) return SA_ERR_INVALID_ARG;
   sa::RopeArgs a;
-  a.axes = p->axes;
-  a.rot = 0;
-  for (int i = 0; i < 4; ++i) a.first[i] = 0;
-  for (int i = 0; i < 3; ++i) {
-    const int32_t n = i < p->axes ? p->axis_dim[i] : 0;
-    if (n < 0 || n % 2 || n > p->d) return SA_ERR_INVALID_ARG;
-    a.rot += n;
-    a.first[i + 1] = a.rot / 2;
-  }
-  if (a.rot < 2 || a.rot > p->d) return SA_ERR_INVALID_ARG;
-  if (p->pairing == SA_ROPE_HALF && a.rot % 16) return SA_ERR_UNSUPPORTED;  // 16-byte halves
-  if (!p->inv_freq && !(std::isfinite(p->theta) && p->theta > 0.0)) return SA_ERR_INVALID_ARG;
-  for (int x = 0; x < p->axes; ++x)
-    for (int i = a.first[x]; i < a.first[x + 1]; ++i) {
-      const double f = p->inv_freq ? p->inv_freq[i]
-                                   : std::pow(p->theta, -2.0 * (i - a.first[x]) / p->axis_dim[x]);
-      if (!std::isfinite(f)) return SA_ERR_INVALID_ARG;
-      a.turn[i] = turn_fraction(f);
-    }
-  for (int i = a.rot / 2; i < 64; ++i) a.turn[i] = 0;
-  a.vox = {};
-  a.pos = p->positions;
-  a.pos_b = p->positions_b;
-  a.voxel_order = 0;
-  if (p->positions) {
-    if (!aligned(p->positions, 4) || p->positions_b < 0 || (p->B > 1 && p->positions_b > (int64_t(1) << 40)) ||
-        (p->positions_b && p->positions_b < int64_t(p->N) * p->axes))
-      return SA_ERR_INVALID_ARG;
-    for (int i = 0; i < 3; ++i) a.offset[i] = 0;
-  } else {
-    const sa_voxel_grid& g = p->grid;
-    if (p->axes != 3 || g.T < 1 || g.Hh < 1 || g.W < 1 || g.T > p->N || g.Hh > p->N || g.W > p->N)
-      return SA_ERR_INVALID_ARG;
-    if (int64_t(g.T) * g.Hh > p->N || int64_t(g.T) * g.Hh * g.W != p->N) return SA_ERR_INVALID_ARG;
-    if (p->voxel_order && (g.vt < 1 || g.vh < 1 || g.vw < 1)) return SA_ERR_INVALID_ARG;
-    const int64_t size[3] = {g.T, g.Hh, g.W};
-    for (int i = 0; i < 3; ++i) {
-      const int64_t o = p->offset[i];
-      if (o < INT32_MIN || o + size[i] - 1 > INT32_MAX) return SA_ERR_INVALID_ARG;
-      a.offset[i] = static_cast<int32_t>(o);
-    }
-    a.vox.T = g.T;
-    a.vox.Hh = g.Hh;
-    a.vox.W = g.W;
-    // a voxel larger than the grid is the grid
-    a.vox.vt = p->voxel_order ? std::min(g.vt, g.T) : g.T;
-    a.vox.vh = p->voxel_order ? std::min(g.vh, g.Hh) : g.Hh;
-    a.vox.vw = p->voxel_order ? std::min(g.vw, g.W) : g.W;
-    a.voxel_order = p->voxel_order ? 1 : 0;
-  }
+  sa_status st = sa::check_rope(p, H0, H1, &a);
+  if (st != SA_OK) return st;
   const int esz = p->dtype == SA_OUT_FP32 ? 4 : 2;
   const void* x[2] = {x0, x1};
   void* y[2] = {y0, y1};
@@ -467,20 +413,11 @@ sa_status sparse_attn_rope(const sa_rope* p, int32_t H0, const void* x0, const s
       return SA_ERR_INVALID_ARG;
   }
   int sms = 0;
-  sa_status st = device_info(&sms);
-  if (st != SA_OK) return st;
+  if ((st = device_info(&sms)) != SA_OK) return st;
   for (int i = 0; i < 2; ++i)
     if (H[i] && (!in_device_allocation(x[i], nx[i]) || !in_device_allocation(y[i], ny[i])))
       return SA_ERR_INVALID_ARG;
-  if (p->positions &&
-      !in_device_allocation(p->positions, (uint64_t(p->B - 1) * uint64_t(p->positions_b) + uint64_t(p->N) * p->axes) * 4))
-    return SA_ERR_INVALID_ARG;
-  a.B = p->B;
-  a.N = p->N;
-  a.d = p->d;
-  a.half = p->pairing == SA_ROPE_HALF;
-  a.fp32 = p->dtype == SA_OUT_FP32;
-  a.inverse = p->inverse ? 1 : 0;
+  if (!sa::rope_positions(p)) return SA_ERR_INVALID_ARG;
   sa::NvtxRange range("sparse_attn_rope");
   return map_cuda(sa::launch_rope(a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
