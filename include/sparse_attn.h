@@ -671,6 +671,39 @@ sa_status sparse_attn_cache8_read(const sa_cache8* cache, const int32_t* first, 
                                   const sa_strides* vs, sa_stream_t stream);
 
 /*
+ * Attention over an 8-bit cache: o = softmax(scale q k) v over the keys a row sees,
+ * lse = ln of the sum of e^(scale q k) over them; a row that sees none gets o = 0,
+ * lse = -inf.  Hq query heads share the cache's Hkv key heads (query head h reads key
+ * head h / (Hq/Hkv)).  The mask is that of sparse_attn_forward_masked without
+ * documents: a sequence is the first lengths[b] tokens of the cache (NULL: all N;
+ * clamped to 0 .. N), the query rows are its last positions, and with causal = F > 0 a
+ * row sees up to the end of its own frame of F tokens.
+ *
+ * q bf16, o bf16 or fp32 by out_dtype.  Codes enter the products as they are, a query row in
+ * two e4m3 terms (off by 2^-17 of the row's largest value at most); sums are fp32.  What a
+ * row does not see never reaches it, whatever its codes and scales.  The value scales of a head
+ * may lie up to 2^100 apart.  The workspace (256-byte aligned, may be NULL when its
+ * size is 0) holds partial results; calls that may overlap on the GPU need one each.
+ * Hq / Hkv <= 128; B Hq <= 2^24.
+ */
+typedef struct {
+  int32_t Hq, Nq;
+  float scale;            /* finite, not 0 */
+  int32_t out_dtype;
+  sa_strides q, o;        /* views [B, Hq, Nq, d] */
+  int32_t causal;
+  const int32_t* lengths; /* device [B] or NULL */
+} sa_attend8;
+
+size_t sparse_attn_forward_cache8_workspace_size(const sa_attend8* problem, const sa_cache8* cache);
+
+/* lse (fp32 [B, Hq, Nq]) and dev_status are nullable.  o may be q's own view (bf16); otherwise no
+ * output or workspace may share memory with another argument.  Asynchronous. */
+sa_status sparse_attn_forward_cache8(const sa_attend8* problem, const sa_cache8* cache, const void* q, void* o,
+                                     float* lse, int32_t* dev_status, void* workspace, size_t workspace_bytes,
+                                     sa_stream_t stream);
+
+/*
  * Checks index lists without trapping: row_ptr[0] == 0, row_ptr[rows] == nnz,
  * row_ptr non-decreasing, every index in [0, Nk) and strictly ascending
  * within its row.  dev_status is a caller-provided device int32 used as the

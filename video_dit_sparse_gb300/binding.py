@@ -115,6 +115,12 @@ class sa_cache8(ctypes.Structure):
                 ("k_scales", sa_strides), ("v_scales", sa_strides)]
 
 
+class sa_attend8(ctypes.Structure):
+    _fields_ = [("Hq", ctypes.c_int32), ("Nq", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("out_dtype", ctypes.c_int32), ("q", sa_strides), ("o", sa_strides),
+                ("causal", ctypes.c_int32), ("lengths", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -176,6 +182,10 @@ def _load():
     lib.sparse_attn_cache8_append.restype = ctypes.c_int
     lib.sparse_attn_cache8_read.argtypes = [P(sa_cache8), vp, i32, i32, i32, vp, ps, vp, ps, vp]
     lib.sparse_attn_cache8_read.restype = ctypes.c_int
+    lib.sparse_attn_forward_cache8_workspace_size.argtypes = [P(sa_attend8), P(sa_cache8)]
+    lib.sparse_attn_forward_cache8_workspace_size.restype = sz
+    lib.sparse_attn_forward_cache8.argtypes = [P(sa_attend8), P(sa_cache8), vp, vp, vp, vp, vp, sz, vp]
+    lib.sparse_attn_forward_cache8.restype = ctypes.c_int
     lib.sparse_attn_validate_index.argtypes = [P(sa_problem), vp, vp, i64, vp, vp]
     lib.sparse_attn_validate_index.restype = ctypes.c_int
     lib.sparse_attn_status_string.argtypes = [ctypes.c_int]
@@ -486,7 +496,8 @@ _GRAD_SIDE = struct.Struct("@iP3qP3qP3q3P")
 _CACHE8 = struct.Struct("@5i2P6q2P6q")
 assert _NORM.size <= ctypes.sizeof(sa_norm_rope) and sa_norm_rope.eps.offset + 4 == _NORM.size
 assert _SIDE.size == ctypes.sizeof(sa_norm_side) and _GRAD_SIDE.size == ctypes.sizeof(sa_norm_grad_side)
-assert _CACHE8.size == ctypes.sizeof(sa_cache8)
+_ATTEND8 = struct.Struct("@2ifi6qiP")
+assert _CACHE8.size == ctypes.sizeof(sa_cache8) and _ATTEND8.size == ctypes.sizeof(sa_attend8)
 _bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 _empty, _empty_like = torch.empty, torch.empty_like
@@ -512,6 +523,8 @@ _c_norm_grad = _by_bytes("sparse_attn_norm_rope_backward", [_cp, _cp, _cp, _vp, 
 _c_append8 = _by_bytes("sparse_attn_cache8_append", [_cp, ctypes.c_int32, _vp, _cp, _vp, _cp, _vp, ctypes.c_int32, _vp, _vp])
 _c_read8 = _by_bytes("sparse_attn_cache8_read", [_cp, _vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _vp, _cp, _vp,
                                                  _cp, _vp])
+_c_attend8 = _by_bytes("sparse_attn_forward_cache8", [_cp, _cp] + [_vp] * 5 + [ctypes.c_size_t, _vp])
+_c_attend8_ws = _by_bytes("sparse_attn_forward_cache8_workspace_size", [_cp, _cp], ctypes.c_size_t)
 
 
 def _view(t: torch.Tensor, dtype, name: str, dev: int):
@@ -1045,6 +1058,47 @@ def sparse_attn_cache8_read(cache: Cache8, first, n: int, *, out=None, out_dtype
     return ko, vo
 
 
+def sparse_attn_forward_cache8(q: torch.Tensor, cache: Cache8, *, scale: float | None = None, causal: int = 0,
+                               lengths: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                               out_dtype=torch.bfloat16, lse: torch.Tensor | bool = True,
+                               workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """Attention of bf16 rows q [B, H, Nq, d] over an 8-bit cache whose Hk key heads they share (H a multiple of
+    Hk).  Returns (o [B, H, Nq, d], lse fp32 [B, H, Nq] or None).
+
+    A sequence is the first lengths[b] tokens of the cache (default: all), the rows are its last positions (one new
+    token: Nq = 1), and with `causal` tokens a frame a row sees up to the end of its own frame (1: its own token)."""
+    dev = q.get_device()
+    if dev >= 0 and (stream is not None or dev != _current_device()):
+        return _elsewhere(dev, stream, sparse_attn_forward_cache8, q, cache, scale=scale, causal=causal, lengths=lengths,
+                          out=out, out_dtype=out_dtype, lse=lse, workspace=workspace, status=status)
+    qs = _view(q, _bf16, "q", dev)
+    c, (cb, Hk, N, cd) = _cache8_fields(cache, dev)
+    B, H, Nq, d = shape = q.shape
+    if cb != B or cd != d or not Hk or H % Hk:
+        raise ValueError("the cache must have q's B and d, and H be a multiple of its Hk")
+    if out is None:
+        out = _empty_like(q) if out_dtype is q.dtype else _empty_like(q, dtype=out_dtype)
+    elif out.shape != shape:
+        raise ValueError("out must have q's shape")
+    if out.dtype not in _OUT:
+        raise ValueError("out must be bfloat16 or float32")
+    if lse is True:
+        lse = _empty(shape[:3], dtype=_f32, device=q.device)
+    elif lse is False:
+        lse = None
+    p = _ATTEND8.pack(H, Nq, 1.0 / math.sqrt(d) if scale is None else scale, _OUT[out.dtype], *qs,
+                      *_view(out, out.dtype, "out", dev), causal, _flat(lengths, _i32, "lengths", dev, (B,)))
+    need = _c_attend8_ws(p, c)
+    if need and workspace is None:
+        workspace = _empty(need, dtype=torch.uint8, device=q.device)
+    st = _c_attend8(p, c, q.data_ptr(), out.data_ptr(), _flat(lse, _f32, "lse", dev, shape[:3]),
+                    _flat(status, _i32, "status", dev), _flat(workspace, torch.uint8, "workspace", dev),
+                    0 if workspace is None else workspace.numel(), _current_stream(dev))
+    if st != SA_OK:
+        raise SparseAttnError(st, "sparse_attn_forward_cache8")
+    return out, lse
+
+
 class HostLayer:
     """One attention layer from pinned host tensors (sparse_attn_layer_from_host):
     device staging, one chunk's scratch and two copy streams, allocated once
@@ -1115,3 +1169,4 @@ norm_rope_backward = sparse_attn_norm_rope_backward
 cache8 = sparse_attn_cache8
 cache8_append = sparse_attn_cache8_append
 cache8_read = sparse_attn_cache8_read
+forward_cache8 = sparse_attn_forward_cache8

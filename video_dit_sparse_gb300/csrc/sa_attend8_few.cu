@@ -1,0 +1,625 @@
+// sa_attend8_few.cu — attention of few query rows (a new token's heads, or a few tokens) over an 8-bit cache.
+//
+// The cache is read once and decides the time, so nothing is done to it but what the tensor cores do: its codes go by
+// TMA into shared memory and from there, as they are, into both products.  Keys are the rows of the first,
+//     S^T [128 keys x rows] = K Q^T  (rows in two e4m3 terms: sa_attend8.cuh),
+// so that its cost goes with the rows there are, and a thread owns a key: the key's scale is one factor, a row's sum
+// of weights stays in the thread until the end, and the mask is a comparison.  The second is
+//     O^T [d x rows] = V^T P^T,
+// with V's codes as the MN-major operand.  Its other operand has 8 bits too: a weight u = p vs 2^c (vs: the value
+// block's scale, c: so that u <= 2^15) is cut into three e5m2 terms, whose exponent reaches from 2^-16 to 2^15: three
+// digits each, eleven bits of fp16 at most, off by 2^-10 of u or by 2^-29 of the row's largest.
+// The terms are columns of their own, added up at the end.
+//
+// Work is cut evenly whatever the lengths: the key tiles of all heads of all sequences are one row of tiles, and every
+// block takes an equal run of it.  A run that covers a head in part leaves a normalised fp32 partial result and its
+// lse; a second kernel joins them.
+//
+// The row's reference is that of its run's first tile and moves when a weight passes 2^15 (eight times the first
+// tile's largest).
+#include <algorithm>
+#include <atomic>
+
+#include "sa_attend8.cuh"
+
+namespace sa {
+
+namespace {
+
+constexpr int kKeys = 128;  // keys of a tile
+constexpr float kLn2f = 0.69314718055994531f;
+constexpr float kTop = 12.f;           // a row's largest weight of its first tile is 2^12
+constexpr float kMostWeight = 32768.f;  // 2^15
+constexpr int kNever = 0x7FFFFFFF;
+
+template <int D, int RP>
+struct FCfg {
+  static constexpr int kTile = kKeys * D;
+  static constexpr int kStages = D == 128 ? 10 : 18;
+  static constexpr int kQRows = 2 * RP;                       // hi rows, then lo rows
+  static constexpr int kPRows = RP == 8 ? 32 : 3 * RP;        // columns of O^T (a multiple of 16)
+  static constexpr int kQBytes = kQRows * D, kPBytes = kPRows * kKeys;
+  static constexpr int kRing = 0, kQ = kStages * kTile, kP = kQ + (kQBytes + 1023) / 1024 * 1024, kEnd = kP + 2 * kPBytes;
+  static constexpr int kSmemBytes = 1024 + kEnd;
+  static constexpr int kOCol = 2 * kQRows;
+  static constexpr int kTmemCols = kOCol + kPRows <= 64 ? 64 : kOCol + kPRows <= 128 ? 128 : 256;
+  static constexpr int kThreads = 192;  // four softmax warps, one for the MMAs, one for the loads
+  static_assert(kSmemBytes <= 220 * 1024, "shared memory");
+};
+
+// What the blocks of a launch share out: tiles of each batch entry's heads, in order.
+struct Run {
+  int b, hk, j0, n, tiles;  // entry, key head, first tile, tiles, tiles of the head
+};
+
+__device__ __forceinline__ int keys_of(const Attend8Args& a, int b) { return row_span(a.m.mask, b, a.m.Nq - 1).hi; }
+__device__ __forceinline__ int tiles_of_entry(const Attend8Args& a, int b) { return (keys_of(a, b) + kKeys - 1) / kKeys; }
+
+// Any of `count` threads' flags, on hardware barrier `id`.
+__device__ __forceinline__ bool any_of(int id, int count, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return r != 0;
+}
+
+// A pair of fp16 values to the nearest e5m2 codes.
+__device__ __forceinline__ uint32_t encode_e5m2(uint32_t pair) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(pair));
+  return r;
+}
+__device__ __forceinline__ uint32_t half_sub(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+}  // namespace
+
+template <int D, int RP>
+__global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
+    sa_attend8_few_kernel(const __grid_constant__ Attend8Args a, const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v) {
+  using C = FCfg<D, RP>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ uint64_t full[S], empty[S], sfull[2], pfull[2], pdone[2], qfull, drain;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  __shared__ int before[kMostEntries + 1];  // tiles of the entries ahead of each
+  __shared__ float rowf[RP], rowm[RP], red[4][RP];
+  __shared__ int rowhi[RP], nan_at[D];
+  volatile int* abort = &abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nr = a.m.R * a.m.Nq;  // rows of a key head
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], 128);
+      mbar_init(&pdone[i], 1);
+    }
+    mbar_init(&qfull, 128);
+    mbar_init(&drain, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  for (int b = threadIdx.x; b < a.m.B; b += C::kThreads) before[b + 1] = tiles_of_entry(a, b) * a.m.Hkv;
+  for (int i = threadIdx.x; i < 2 * C::kPBytes / 16; i += C::kThreads)  // (columns that no term fills stay 0)
+    reinterpret_cast<uint4*>(smem + C::kP)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  if (warp == 4) {
+    tmem_alloc(&tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  if (warp == 5) {  // running sums
+    int sum = 0;
+    for (int b0 = 0; b0 < a.m.B; b0 += 32) {
+      int x = b0 + lane < a.m.B ? before[b0 + lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (b0 + lane < a.m.B) before[b0 + lane + 1] = sum + x;
+      sum += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) before[0] = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const int total = before[a.m.B], blocks = min(static_cast<int>(gridDim.x), total);
+  const bool works = static_cast<int>(blockIdx.x) < blocks;
+  const int g0 = works ? static_cast<int>(int64_t(blockIdx.x) * total / blocks) : 0;
+  const int g1 = works ? static_cast<int>(int64_t(blockIdx.x + 1) * total / blocks) : 0;
+  auto run_at = [&](int g) -> Run {
+    int b = 0, top = a.m.B - 1;  // the last entry that starts at g or before and has tiles
+    while (b < top) {
+      const int mid = (b + top + 1) >> 1;
+      if (before[mid] <= g)
+        b = mid;
+      else
+        top = mid - 1;
+    }
+    Run x;
+    x.b = b;
+    x.tiles = (before[b + 1] - before[b]) / a.m.Hkv;
+    x.hk = (g - before[b]) / x.tiles;
+    x.j0 = g - before[b] - x.hk * x.tiles;
+    x.n = min(x.tiles - x.j0, g1 - g);
+    return x;
+  };
+
+  if (warp < 4) {
+    // ------------------------------------------------------------ softmax: thread = key of a tile
+    // (A wait that gives up lets the thread go on: all meet at the same barriers to the end.)
+    const int t = threadIdx.x;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    uint32_t c = 0;  // tiles so far
+    for (int g = g0; g < g1;) {
+      const Run x = run_at(g);
+      g += x.n;
+      // The rows, in two terms: RP rows of D / 8 pieces of eight values.  (The last run's products have read the old
+      // ones: its last S is here.)
+      constexpr int kPieces = D / 8;
+#pragma unroll
+      for (int f0 = 0; f0 < RP * kPieces; f0 += 128) {
+        const int f = f0 + t, r = f / kPieces, p = f % kPieces;
+        const int qi = r / a.m.R, h = x.hk * a.m.R + r - qi * a.m.R;
+        const bool there = RP * kPieces % 128 == 0 || r < RP;
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (r < nr)
+          u = *reinterpret_cast<const uint4*>(a.m.q + int64_t(x.b) * a.m.qs.b + int64_t(h) * a.m.qs.h + int64_t(qi) * a.m.qs.n + p * 8);
+        uint32_t top = top_of(u, 0);
+#pragma unroll
+        for (int o = kPieces / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float fac = row_factor(top);
+        uint2 hi, lo;
+        two_terms(u, fac, &hi, &lo);
+        if (there) {
+          *reinterpret_cast<uint2*>(smem + C::kQ + rows8_offset<D>(r, p * 8)) = hi;
+          *reinterpret_cast<uint2*>(smem + C::kQ + rows8_offset<D>(RP + r, p * 8)) = lo;
+        }
+        if (there && p == 0) {
+          rowf[r] = r < nr ? a.scale_log2 / fac : 0.f;
+          rowhi[r] = r < nr ? row_span(a.m.mask, x.b, qi).hi : 0;
+        }
+      }
+      if (t < D) nan_at[t] = kNever;
+      fence_proxy_async_smem();
+      named_barrier(1, 128);
+      mbar_arrive(&qfull);
+      int least = kNever;
+      for (int r = 0; r < nr; ++r) least = min(least, rowhi[r]);
+      const int most = keys_of(a, x.b);
+      const float* ksc = a.k_scale + int64_t(x.b) * a.k_scales.b + int64_t(x.hk) * a.k_scales.h;
+      const float* vsc = a.v_scale + int64_t(x.b) * a.v_scales.b + int64_t(x.hk) * a.v_scales.h;
+      // value scales count from that of the run's first block
+      const float s0 = held_scale(__ldg(vsc + (x.j0 * kKeys >> a.block_log2)));
+      const float lref = s0 > 0.f ? __log2f(s0) : 0.f;
+      auto scale_at = [&](const float* s, int key) -> float { return key < a.m.Nk ? held_scale(__ldg(s + (key >> a.block_log2))) : 0.f; };
+      float l[RP];
+#pragma unroll
+      for (int r = 0; r < RP; ++r) l[r] = 0.f;
+      float ks_next = scale_at(ksc, x.j0 * kKeys + t), vs_next = scale_at(vsc, x.j0 * kKeys + t);
+      for (int j = 0; j < x.n; ++j, ++c) {
+        const int k0 = (x.j0 + j) * kKeys, key = k0 + t;
+        const float ks = ks_next, vs = vs_next;
+        if (j + 1 < x.n) {
+          ks_next = scale_at(ksc, key + kKeys);
+          vs_next = scale_at(vsc, key + kKeys);
+        }
+        const float lv = vs > 0.f ? fminf(fmaxf(__log2f(vs) - lref, -100.f), 100.f) : 0.f, iv = fast_exp2(-lv);
+        const uint32_t sb = c & 1;
+        const bool edge = k0 + kKeys > least;  // some row does not see the whole tile
+        mbar_wait(&sfull[sb], (c >> 1) & 1, abort);
+        __syncwarp();
+        tc_fence_after();
+        float y[RP];
+        {
+          float s[2 * RP];
+          uint32_t* w = reinterpret_cast<uint32_t*>(s);
+          const uint32_t at = tmem + lanes + sb * C::kQRows;
+          if (RP == 8) {
+            tmem_ld16(at, w);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2 * RP; i += 32) tmem_ld32(at + i, w + i);
+          }
+          tmem_ld_wait();
+#pragma unroll
+          for (int r = 0; r < RP; ++r) y[r] = fmaf(s[r] + s[RP + r], rowf[r] * ks, lv);
+        }
+        if (ks == 0.f) {  // (an empty block's keys are zeros, whatever their codes)
+#pragma unroll
+          for (int r = 0; r < RP; ++r) y[r] = lv;
+        }
+        if (edge) {
+#pragma unroll
+          for (int r = 0; r < RP; ++r) y[r] = key < rowhi[r] ? y[r] : -INFINITY;
+        }
+        float u[RP];
+        auto weights = [&]() -> bool {  // false: one is too large
+          float top = 0.f;
+#pragma unroll
+          for (int r = 0; r < RP; ++r) {
+            u[r] = fast_exp2(y[r] - rowm[r]);
+            top = u[r] <= kMostWeight ? top : 1.f;
+          }
+          return top == 0.f;
+        };
+        bool fits = true;
+        if (j > 0) fits = weights();
+        if (any_of(2, 128, !fits || (vs == 0.f && key < most)) || j == 0 || edge) {
+          const bool raise = any_of(2, 128, !fits) || j == 0;
+          if (raise) {
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+              const uint32_t o = __reduce_max_sync(0xffffffffu, y[r] == y[r] ? order_key(y[r]) : 0u);
+              if (lane == 0) red[warp][r] = o ? key_value(o) : -INFINITY;
+            }
+            named_barrier(1, 128);
+            float alpha[RP];
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+              const float mx = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r])) - kTop;
+              // (a row that sees nothing of the run's first tile sees nothing of the run; rows that are not there: 0 weights)
+              const float m0 = j == 0 ? -INFINITY : rowm[r];
+              float mn = j == 0 ? mx : fmaxf(m0, mx);
+              if (r >= nr || mn == -INFINITY) mn = INFINITY;
+              alpha[r] = j == 0 || mn == m0 ? 1.f : fast_exp2(m0 - mn);
+              l[r] *= alpha[r];
+              y[r] -= mn;  // (rowm changes behind the barrier)
+            }
+            named_barrier(1, 128);
+            if (t < RP) {
+              const float mx = fmaxf(fmaxf(red[0][t], red[1][t]), fmaxf(red[2][t], red[3][t])) - kTop;
+              float mn = j == 0 ? mx : fmaxf(rowm[t], mx);
+              if (t >= nr || mn == -INFINITY) mn = INFINITY;
+              rowm[t] = mn;
+            }
+            if (j > 0) {  // O holds the tiles so far
+              mbar_wait(&pdone[(c - 1) & 1], ((c - 1) >> 1) & 1, abort);
+              __syncwarp();
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < 3; ++k) {
+#pragma unroll
+                for (int r0 = 0; r0 < RP; r0 += 8) {
+                  const uint32_t at = tmem + lanes + C::kOCol + k * RP + r0;
+                  uint32_t o[8];
+                  tmem_ld8(at, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[r0 + i]);
+                  tmem_st8(at, o);
+                }
+              }
+              tmem_st_wait();
+            }
+#pragma unroll
+            for (int r = 0; r < RP; ++r) u[r] = fast_exp2(y[r]);
+            named_barrier(1, 128);
+          }
+          // Values of tokens that some row does not see, or of empty blocks, must not reach O by 0 times NaN: what no
+          // row sees is cleared, a NaN that some do is noted by its column (rows see the first keys, so its first
+          // key says which) and cleared.
+          const bool clean = edge || any_of(2, 128, vs == 0.f && key < most);
+          const uint32_t iv_at = (2 * c + 1) % S;
+          if (clean) mbar_wait(&full[iv_at], ((2 * c + 1) / S) & 1, abort);
+          uint8_t* vt = smem + C::kRing + iv_at * C::kTile;
+#pragma unroll 1
+          for (int p = 0; clean && p < D / 16; ++p) {
+            uint4* at = reinterpret_cast<uint4*>(vt + rows8_offset<D>(t, p * 16));
+            uint4 w = *at;
+            uint32_t* e = reinterpret_cast<uint32_t*>(&w);
+            bool changed = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (key >= most || vs == 0.f) {
+                changed |= e[i] != 0;
+                e[i] = 0;
+              } else if (((e[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) {
+                for (int q = 0; q < 4; ++q)
+                  if ((e[i] >> (8 * q) & 127) == 127) {
+                    atomicMin(&nan_at[p * 16 + 4 * i + q], key);
+                    e[i] &= ~(255u << (8 * q));
+                  }
+                changed = true;
+              }
+            }
+            if (changed) *at = w;
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < RP; ++r) l[r] = fmaf(u[r], iv, l[r]);
+        // the buffer's last reader
+        if (c >= 2) mbar_wait(&pdone[sb], ((c - 2) >> 1) & 1, abort);
+        uint8_t* sp = smem + C::kP + sb * C::kPBytes;
+        auto put = [&](int n, uint32_t code) {
+          sp[n * kKeys + ((((t >> 4) ^ (n & 7)) << 4) | (t & 15))] = static_cast<uint8_t>(code);
+        };
+#pragma unroll
+        for (int r = 0; r < RP; r += 2) {
+          uint32_t h = pack_half(u[r], u[r + 1]);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            const uint32_t e = encode_e5m2(h);
+            put(k * RP + r, e);
+            put(k * RP + r + 1, e >> 8);
+            if (k < 2) h = half_sub(h, __byte_perm(e, 0, 0x1404));
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&pfull[sb]);
+      }
+      // ---------------------------------------------------------- output: thread = column of d
+      mbar_wait(&pdone[(c - 1) & 1], ((c - 1) >> 1) & 1, abort);
+#pragma unroll
+      for (int r = 0; r < RP; ++r) {
+        float v = l[r];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) red[warp][r] = v;
+      }
+      named_barrier(1, 128);
+      tc_fence_after();
+      const bool whole = x.n == x.tiles;
+      const int64_t slot = int64_t(blockIdx.x) + int64_t(x.b) * a.m.Hkv + x.hk;
+      const float unit = fast_exp2(lref);
+      const int nan = t < D ? nan_at[t] : kNever;
+#pragma unroll 1
+      for (int r0 = 0; r0 < RP; r0 += 8) {
+        if (r0 >= nr) break;
+        uint32_t o[3][8];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) tmem_ld8(tmem + lanes + C::kOCol + k * RP + r0, o[k]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + i;
+          if (r >= nr) continue;
+          const float sum = (red[0][r] + red[1][r]) + (red[2][r] + red[3][r]);
+          float v = __uint_as_float(o[0][i]) + (__uint_as_float(o[1][i]) + __uint_as_float(o[2][i]));
+          v = sum == 0.f ? 0.f : v * (unit / sum);
+          if (nan < rowhi[r]) v = __uint_as_float(0x7FC00000u);
+          const int qi = r / a.m.R, h = x.hk * a.m.R + r - qi * a.m.R;
+          if (t < D) {
+            if (!whole)
+              a.m.part_o[(slot * nr + r) * D + t] = v;
+            else {
+              const int64_t at = int64_t(x.b) * a.m.os.b + int64_t(h) * a.m.os.h + int64_t(qi) * a.m.os.n + t;
+              if (a.m.out_fp32)
+                static_cast<float*>(a.m.o)[at] = v;
+              else
+                static_cast<uint16_t*>(a.m.o)[at] = static_cast<uint16_t>(pack_bf16(v, 0.f));
+            }
+          }
+          if (t == 0) {
+            const float lse = sum == 0.f ? -INFINITY : kLn2f * (rowm[r] + log2f(sum));
+            if (!whole)
+              a.m.part_lse[slot * nr + r] = lse;
+            else if (a.m.lse)
+              a.m.lse[(int64_t(x.b) * a.m.Hq + h) * a.m.Nq + qi] = lse;
+          }
+        }
+      }
+      tc_fence_before();
+      named_barrier(1, 128);  // (the next run writes rowhi, rowm, red and nan_at)
+    }
+  } else if (warp == 4) {
+    // ------------------------------------------------------------ MMA issue
+    constexpr uint32_t kIdescS = idesc_f8(128, C::kQRows, 0, 0, false, false);
+    constexpr uint32_t kIdescO = idesc_f8(128, C::kPRows, 0, 1, true, false);
+    // (d = 64: V^T has 64 rows; the MMA's other 64 repeat them and are not read)
+    const uint64_t dk = rows8_desc<D>(smem_u32(smem + C::kRing), 16), dv = rows8_desc<D>(smem_u32(smem + C::kRing), 0);
+    const uint64_t dq = rows8_desc<D>(smem_u32(smem + C::kQ), 16), dp = sw128_desc(smem_u32(smem + C::kP), 16, 1024);
+    const uint32_t k_lo = static_cast<uint32_t>(dk), k_hi = static_cast<uint32_t>(dk >> 32);
+    const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
+    const uint32_t q_lo = static_cast<uint32_t>(dq), q_hi = static_cast<uint32_t>(dq >> 32);
+    const uint32_t p_lo = static_cast<uint32_t>(dp), p_hi = static_cast<uint32_t>(dp >> 32);
+    auto ready = [&](uint32_t i) -> bool { return mbar_wait(&full[i % S], (i / S) & 1, abort); };
+    auto first = [&](uint32_t c) {  // S^T of tile number c
+      const uint32_t at = (((2 * c) % S) * C::kTile) >> 4;
+#pragma unroll
+      for (int kk = 0; kk < D / 32; ++kk)
+        mma8_ss_w(tmem + (c & 1) * C::kQRows, k_lo + at + kk * 2, k_hi, q_lo + kk * 2, q_hi, kIdescS, kk > 0);
+      mma_commit(&sfull[c & 1]);
+      mma_commit(&empty[(2 * c) % S]);
+    };
+    if (lane == 0) {
+      bool ok = true;
+      uint32_t c = 0, runs = 0;
+      for (int g = g0; ok && g < g1; ++runs) {
+        const Run x = run_at(g);
+        g += x.n;
+        if (!(ok = mbar_wait(&qfull, runs & 1, abort)) || !(ok = ready(2 * c))) break;
+        tc_fence_after();
+        first(c);
+        for (int j = 0; j < x.n; ++j, ++c) {
+          // (S^T's other buffer: its tile's P is here already)
+          if (j + 1 < x.n) {
+            if (!(ok = ready(2 * c + 2))) break;
+            first(c + 1);
+          }
+          if (!(ok = ready(2 * c + 1)) || !(ok = mbar_wait(&pfull[c & 1], (c >> 1) & 1, abort))) break;
+          tc_fence_after();
+          const uint32_t at = (((2 * c + 1) % S) * C::kTile) >> 4, bt = ((c & 1) * C::kPBytes) >> 4;
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 32; ++kk)
+            mma8_ss_w(tmem + C::kOCol, v_lo + at + ((kk * 32 * D) >> 4), v_hi, p_lo + bt + kk * 2, p_hi, kIdescO, j > 0 || kk > 0);
+          mma_commit(&pdone[c & 1]);
+          mma_commit(&empty[(2 * c + 1) % S]);
+        }
+      }
+      // Every MMA issued above must finish before TMEM is released.
+      mma_commit(&drain);
+      const long long t0 = clock64();
+      while (!mbar_test(&drain, 0) && clock64() - t0 < kWaitLimitCycles) {
+      }
+    }
+  } else if (lane == 0) {
+    // ------------------------------------------------------------ loads
+    uint32_t it = 0;
+    bool ok = true;
+    for (int g = g0; ok && g < g1;) {
+      const Run x = run_at(g);
+      g += x.n;
+      for (int f = 0; f < 2 * x.n; ++f, ++it) {
+        const uint32_t s = it % S;
+        if (!(ok = mbar_wait(&empty[s], ((it / S) & 1) ^ 1, abort))) break;
+        mbar_expect_tx(&full[s], C::kTile);
+        tma_load_4d(smem_u32(smem + C::kRing) + s * C::kTile, (f & 1) ? &tm_v : &tm_k, 0, (x.j0 + (f >> 1)) * kKeys, x.hk, x.b,
+                    &full[s]);
+      }
+    }
+    if (*abort) {  // what is in flight lands before the block ends
+      for (uint32_t f = it > S ? it - S : 0; f < it; ++f) {
+        const long long t0 = clock64();
+        while (!mbar_test(&full[f % S], (f / S) & 1) && clock64() - t0 < kWaitLimitCycles) {
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && abort_flag) report(a.m.status, SA_DEVERR_TIMEOUT);
+  if (warp == 4) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// A block joins a row's partial results (or writes that it saw nothing): lse = ln sum_p e^(lse_p), o = sum_p
+// e^(lse_p - lse) o_p.  Every column has four threads, each takes every fourth partial result.
+template <int D>
+__global__ void __launch_bounds__(4 * D) sa_attend8_join_kernel(const __grid_constant__ Attend8Args a, int grid) {
+  __shared__ int sums[2][4 * D / 32];
+  __shared__ float acc[4][D], wsum[4];
+  wait_for_earlier_kernel();
+  const int nr = a.m.R * a.m.Nq, v = blockIdx.x / nr, r = blockIdx.x - v * nr, b = v / a.m.Hkv, hk = v - b * a.m.Hkv;
+  int ahead = 0, total = 0;  // tiles of the entries ahead of b, and of all
+  for (int i = threadIdx.x; i < a.m.B; i += 4 * D) {
+    const int n = tiles_of_entry(a, i) * a.m.Hkv;
+    total += n;
+    if (i < b) ahead += n;
+  }
+  ahead = __reduce_add_sync(0xffffffffu, ahead);
+  total = __reduce_add_sync(0xffffffffu, total);
+  if ((threadIdx.x & 31) == 0) {
+    sums[0][threadIdx.x >> 5] = ahead;
+    sums[1][threadIdx.x >> 5] = total;
+  }
+  __syncthreads();
+  ahead = total = 0;
+#pragma unroll
+  for (int i = 0; i < 4 * D / 32; ++i) {
+    ahead += sums[0][i];
+    total += sums[1][i];
+  }
+  const int tiles = tiles_of_entry(a, b), blocks = min(grid, total);
+  const int64_t t0 = ahead + int64_t(hk) * tiles;
+  int first = 0, parts = 0;
+  if (tiles > 0) {
+    first = static_cast<int>(((t0 + 1) * blocks - 1) / total);
+    parts = static_cast<int>(((t0 + tiles) * blocks - 1) / total) - first + 1;
+    if (parts == 1) return;  // one block did it all
+  }
+  const int k = threadIdx.x / D, c = threadIdx.x % D;
+  const int64_t row0 = (int64_t(first) + v) * nr + r;
+  float mx = -INFINITY;
+  bool none = false;  // a partial result that is not a number makes the row none (fmaxf drops it)
+#pragma unroll 8
+  for (int p = 0; p < parts; ++p) {
+    const float x = a.m.part_lse[row0 + int64_t(p) * nr];
+    mx = fmaxf(mx, x);
+    none |= x != x;
+  }
+  float sum = 0.f, o = 0.f;
+  if (mx != -INFINITY || none) {
+#pragma unroll 4
+    for (int p = k; p < parts; p += 4) {
+      const int64_t row = row0 + int64_t(p) * nr;
+      const float w = __expf(a.m.part_lse[row] - mx);
+      sum += w;
+      o = fmaf(w, a.m.part_o[row * D + c], o);
+    }
+  }
+  acc[k][c] = o;
+  if (c == 0) wsum[k] = sum;
+  __syncthreads();
+  if (k) return;
+  sum = (wsum[0] + wsum[1]) + (wsum[2] + wsum[3]);
+  o = (acc[0][c] + acc[1][c]) + (acc[2][c] + acc[3][c]);
+  o = sum == 0.f ? 0.f : o / sum;
+  const int qi = r / a.m.R, h = hk * a.m.R + r - qi * a.m.R;
+  const int64_t at = int64_t(b) * a.m.os.b + int64_t(h) * a.m.os.h + int64_t(qi) * a.m.os.n + c;
+  if (a.m.out_fp32)
+    static_cast<float*>(a.m.o)[at] = o;
+  else
+    static_cast<uint16_t*>(a.m.o)[at] = static_cast<uint16_t>(pack_bf16(o, 0.f));
+  if (c == 0 && a.m.lse) a.m.lse[(int64_t(b) * a.m.Hq + h) * a.m.Nq + qi] = sum == 0.f ? -INFINITY : mx + logf(sum);
+}
+
+namespace {
+
+template <int D, int RP>
+cudaError_t launch_f(const Attend8Args& a, int grid, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
+  using C = FCfg<D, RP>;
+  auto kern = sa_attend8_few_kernel<D, RP>;
+  // at least half the SM's shared memory: one block per SM owns its TMEM
+  const int smem = C::kSmemBytes > 120 * 1024 ? C::kSmemBytes : 120 * 1024;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, C::kThreads, smem, st>>>(a, tk, tv);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d8(const Attend8Args& a, int grid, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
+  const int nr = a.m.R * a.m.Nq;
+  cudaError_t e = nr <= 8    ? launch_f<D, 8>(a, grid, tk, tv, st)
+                  : nr <= 16 ? launch_f<D, 16>(a, grid, tk, tv, st)
+                             : launch_f<D, 32>(a, grid, tk, tv, st);
+  if (e != cudaSuccess) return e;
+  return launch_early(sa_attend8_join_kernel<D>, dim3(a.m.B * a.m.Hkv * nr), 4 * D, 0, st, a, grid);
+}
+
+}  // namespace
+
+// Blocks of the few-row kernel: one an SM, or a tile each.
+int attend8_few_grid(const Attend8Args& a) {
+  const int64_t tiles = int64_t(a.m.B) * a.m.Hkv * ((int64_t(a.m.Nk) + kKeys - 1) / kKeys);
+  return static_cast<int>(std::min<int64_t>(tiles, kAttend8Sms));
+}
+
+cudaError_t launch_attend8_few(const Attend8Args& a, cudaStream_t st) {
+  CUtensorMap tk, tv;
+  if (!make_codes_map(&tk, a.k8, a.m.d, a.m.Nk, a.m.Hkv, a.m.B, a.m.ks, kKeys, true) ||
+      !make_codes_map(&tv, a.v8, a.m.d, a.m.Nk, a.m.Hkv, a.m.B, a.m.vs, kKeys, true))
+    return cudaErrorInvalidValue;
+  const int grid = attend8_few_grid(a);
+  return a.m.d == 128 ? launch_d8<128>(a, grid, tk, tv, st) : launch_d8<64>(a, grid, tk, tv, st);
+}
+
+}  // namespace sa

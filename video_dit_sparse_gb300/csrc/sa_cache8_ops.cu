@@ -91,9 +91,114 @@ void fill(const sa_cache8* p, const Cache& c, int32_t n, const int32_t* start, i
   a->n = n;
 }
 
+// Shapes and options of sa_attend8; fills what the plan goes by.
+sa_status check_attend(const sa_attend8* p, const sa_cache8* c, Attend8Args* a) {
+  if (!p || !c || p->Hq < 1 || p->Nq < 1 || c->B < 1 || c->Hkv < 1 || c->N < 1 || c->d < 1) return SA_ERR_INVALID_ARG;
+  if (p->Hq % c->Hkv || p->causal < 0 || !aligned(p->lengths, 4)) return SA_ERR_INVALID_ARG;
+  if (p->out_dtype != SA_OUT_BF16 && p->out_dtype != SA_OUT_FP32) return SA_ERR_INVALID_ARG;
+  if (!std::isfinite(p->scale) || p->scale == 0.f || !std::isfinite(p->scale * 1.4426950408889634f)) return SA_ERR_INVALID_ARG;
+  if (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128) return SA_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128) return SA_ERR_UNSUPPORTED;
+  const int64_t R = p->Hq / c->Hkv, heads = int64_t(c->B) * c->Hkv, qn = R > 128 ? 1 : 128 / R;
+  // row and tile numbers are 32-bit
+  if (R > 128 || p->Nq > (1 << 30) || c->N > (1 << 30) || heads * R > (1 << 24) ||
+      heads * ((p->Nq + qn - 1) / qn) > (1 << 30) || R * p->Nq > UINT32_MAX ||
+      heads * ((int64_t(c->N) + 127) / 128) > (1 << 30))
+    return SA_ERR_UNSUPPORTED;
+  *a = Attend8Args{};
+  MaskedArgs& m = a->m;
+  m.mask = {nullptr, nullptr, nullptr, p->lengths, 0, p->causal, p->Nq, c->N};
+  m.qs = p->q;
+  m.os = p->o;
+  m.B = c->B;
+  m.Hq = p->Hq;
+  m.Hkv = c->Hkv;
+  m.R = static_cast<int32_t>(R);
+  m.Nq = p->Nq;
+  m.Nk = c->N;
+  m.d = c->d;
+  m.out_fp32 = p->out_dtype == SA_OUT_FP32;
+  m.total_rows = heads * R * p->Nq;
+  a->scale_log2 = p->scale * 1.4426950408889634f;
+  while ((1 << a->block_log2) < c->block) ++a->block_log2;
+  if (!attend8_few(*a)) return SA_ERR_UNSUPPORTED;
+  return SA_OK;
+}
+
+// Partial results (fp32 rows), then their lse: each 256-byte aligned.
+struct Parts {
+  size_t o, lse;
+};
+Parts parts_of(const Attend8Args& a) {
+  const size_t rows = (size_t(attend8_few_grid(a)) + size_t(a.m.B) * a.m.Hkv) * a.m.R * a.m.Nq;
+  return {(rows * a.m.d * 4 + 255) / 256 * 256, (rows * 4 + 255) / 256 * 256};
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t sparse_attn_forward_cache8_workspace_size(const sa_attend8* p, const sa_cache8* cache) {
+  Attend8Args a;
+  if (check_attend(p, cache, &a) != SA_OK) return 0;
+  const Parts n = parts_of(a);
+  return n.o + n.lse;
+}
+
+sa_status sparse_attn_forward_cache8(const sa_attend8* p, const sa_cache8* cache, const void* q, void* o, float* lse,
+                                     int32_t* dev_status, void* workspace, size_t workspace_bytes, sa_stream_t stream) {
+  Attend8Args a;
+  sa_status st = check_attend(p, cache, &a);
+  if (st != SA_OK) return st;
+  MaskedArgs& m = a.m;
+  Cache c;
+  if ((st = check_cache(cache, false, &c)) != SA_OK) return st;
+  const int esz = m.out_fp32 ? 4 : 2;
+  View in{q, m.qs, m.B, m.Hq, m.Nq, 0}, out{o, m.os, m.B, m.Hq, m.Nq, 0};
+  if (!check_view(q, &in.s, m.B, m.Hq, m.Nq, m.d, 2, false, false, &in.n) ||
+      !check_view(o, &out.s, m.B, m.Hq, m.Nq, m.d, esz, true, false, &out.n) || !aligned(lse, 4) || !aligned(dev_status, 4))
+    return SA_ERR_INVALID_ARG;
+  m.qs = in.s;
+  m.os = out.s;
+  // Nothing that is written may share memory with anything else of the call, but o may be q's view: a row of q is
+  // read ahead of the row of o that takes its place.
+  const uint64_t nl = lse ? uint64_t(m.total_rows) * 4 : 0;
+  const Parts n = parts_of(a);
+  const size_t need = n.o + n.lse;
+  if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return SA_ERR_INVALID_ARG;
+  if (!(esz == 2 && same_view(in, out)) && (esz == 2 ? views_overlap(in, out, m.d, 2) : overlap(q, in.n, o, out.n)))
+    return SA_ERR_INVALID_ARG;
+  if (meets_cache(c, o, out.n)) return SA_ERR_INVALID_ARG;
+  if (nl && (overlap(lse, nl, q, in.n) || overlap(lse, nl, o, out.n) || meets_cache(c, lse, nl))) return SA_ERR_INVALID_ARG;
+  if (need && (overlap(workspace, need, q, in.n) || overlap(workspace, need, o, out.n) || meets_cache(c, workspace, need) ||
+               (nl && overlap(workspace, need, lse, nl))))
+    return SA_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = device_info(&sms)) != SA_OK) return st;
+  if (!cache_in_device(c) || !in_device_allocation(q, in.n) || !in_device_allocation(o, out.n) ||
+      (nl && !in_device_allocation(lse, nl)) || (dev_status && !in_device_allocation(dev_status, 4)) ||
+      (need && !in_device_allocation(workspace, need)) ||
+      (p->lengths && !in_device_allocation(p->lengths, uint64_t(m.B) * 4)))
+    return SA_ERR_INVALID_ARG;
+  m.q = static_cast<const uint16_t*>(q);
+  m.o = o;
+  m.lse = lse;
+  m.status = dev_status;
+  m.ks = c.codes[0].s;
+  m.vs = c.codes[1].s;
+  a.k8 = static_cast<const uint8_t*>(c.codes[0].p);
+  a.v8 = static_cast<const uint8_t*>(c.codes[1].p);
+  a.k_scale = c.scales[0];
+  a.v_scale = c.scales[1];
+  a.k_scales = c.ss[0];
+  a.v_scales = c.ss[1];
+  if (need) {
+    m.part_o = static_cast<float*>(workspace);
+    m.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + n.o);
+  }
+  NvtxRange range("sparse_attn_forward_cache8");
+  return map_cuda(launch_attend8_few(a, reinterpret_cast<cudaStream_t>(stream)));
+}
 
 sa_status sparse_attn_cache8_append(const sa_cache8* p, int32_t n, const void* k, const sa_strides* ks, const void* v,
                                     const sa_strides* vs, const int32_t* start, int32_t start0, const int32_t* counts,

@@ -221,6 +221,24 @@ struct Cache8Args {
 cudaError_t launch_cache8_append(Cache8Args a, cudaStream_t stream);
 cudaError_t launch_cache8_read(Cache8Args a, bool wide, cudaStream_t stream);
 
+// Attention over an e4m3 cache.  m: q, o, lse, mask, sizes, partial results (ks, vs: the codes' strides).
+constexpr int kAttend8Sms = 152;
+constexpr int kMostEntries = 1024;  // batch entries that the few-row kernel shares out
+struct Attend8Args {
+  MaskedArgs m;
+  const uint8_t* k8;
+  const uint8_t* v8;
+  const float* k_scale;      // [B, Hkv, ceil(Nk / block)]
+  const float* v_scale;
+  sa_strides k_scales, v_scales;
+  int32_t block_log2;
+  float scale_log2;          // scale log2(e), with its sign
+};
+// Up to 32 rows a key head, and batch entries that its table holds: the few-row kernel.
+inline bool attend8_few(const Attend8Args& a) { return int64_t(a.m.R) * a.m.Nq <= 32 && a.m.B <= kMostEntries; }
+int attend8_few_grid(const Attend8Args& a);
+cudaError_t launch_attend8_few(const Attend8Args& a, cudaStream_t stream);
+
 // sparse_attn_layer_from_host splits a layer into at most this many chunks.
 constexpr int kMaxPipelineChunks = 64;
 
