@@ -19,7 +19,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsparse_attn.so")
 SOURCES = ["sa_api.cu", "sa_forward.cu", "sa_builder.cu", "sa_colstat.cu", "sa_layout.cu", "sa_format.cu", "sa_pipeline.cu", "sa_noalloc.cu",
            "sa_rope.cu", "sa_masked.cu", "sa_cache.cu", "sa_ops.cu", "sa_norm_rope.cu", "sa_cache8.cu",
-           "sa_cache8_ops.cu", "sa_attend8_few.cu"]
+           "sa_cache8_ops.cu", "sa_attend8_few.cu", "sa_attend8_many.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -29,7 +29,7 @@ namespace {
 constexpr int kKeys = 128;  // keys of a tile
 constexpr float kLn2f = 0.69314718055994531f;
 constexpr float kTop = 12.f;           // a row's largest weight of its first tile is 2^12
-constexpr float kMostWeight = 32768.f;  // 2^15
+constexpr float kMostWeight = 32768.f;  // 2^15 (an exponent of 15 and more, as `moved` says it)
 constexpr int kNever = 0x7FFFFFFF;
 
 template <int D, int RP>
@@ -266,6 +266,12 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
           }
           return top == 0.f;
         };
+        // A row's new reference: it moves if a weight passed 2^15 (each row by itself: its bits do not go by the others).
+        auto moved = [&](int r, float m0, bool start, int rows) -> float {
+          const float mx = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r]));
+          const float mn = start || mx - m0 > 15.f ? mx - kTop : m0;
+          return r >= rows || mn == -INFINITY ? INFINITY : mn;
+        };
         bool fits = true;
         if (j > 0) fits = weights();
         if (any_of(2, 128, !fits || (vs == 0.f && key < most)) || j == 0 || edge) {
@@ -280,21 +286,15 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
             float alpha[RP];
 #pragma unroll
             for (int r = 0; r < RP; ++r) {
-              const float mx = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r])) - kTop;
               // (a row that sees nothing of the run's first tile sees nothing of the run; rows that are not there: 0 weights)
-              const float m0 = j == 0 ? -INFINITY : rowm[r];
-              float mn = j == 0 ? mx : fmaxf(m0, mx);
-              if (r >= nr || mn == -INFINITY) mn = INFINITY;
+              const float m0 = j == 0 ? -INFINITY : rowm[r], mn = moved(r, m0, j == 0, nr);
               alpha[r] = j == 0 || mn == m0 ? 1.f : fast_exp2(m0 - mn);
               l[r] *= alpha[r];
               y[r] -= mn;  // (rowm changes behind the barrier)
             }
             named_barrier(1, 128);
             if (t < RP) {
-              const float mx = fmaxf(fmaxf(red[0][t], red[1][t]), fmaxf(red[2][t], red[3][t])) - kTop;
-              float mn = j == 0 ? mx : fmaxf(rowm[t], mx);
-              if (t >= nr || mn == -INFINITY) mn = INFINITY;
-              rowm[t] = mn;
+              rowm[t] = moved(t, j == 0 ? -INFINITY : rowm[t], j == 0, nr);
             }
             if (j > 0) {  // O holds the tiles so far
               mbar_wait(&pdone[(c - 1) & 1], ((c - 1) >> 1) & 1, abort);

@@ -1,0 +1,725 @@
+// sa_attend8_many.cu — attention of many query rows over an 8-bit cache.
+//
+// Rows of one key head are packed, row = query * R + head-in-group, and a unit is two tiles of up to 128 packed rows that
+// take K and V from one ring, as in sa_masked.cu.  What differs is how eight bits reach the tensor cores.
+//
+// S = Q K^T takes K's codes as they are (kind::f8f6f4) and the query rows in two e4m3 terms (sa_attend8.cuh): two
+// products at twice the rate.  K's scale belongs to a column: it is a factor of the row's multiplier, the same for
+// the 16 columns that a chunk of the softmax works on.
+//
+// O = P V cannot have P in eight bits (a term holds four digits, and cutting P in terms would cost the softmax more
+// than its exponentials).  So V's codes become fp16 on the way: one instruction for two of them, exact, by a warp of its
+// own.  V's scale goes into P's exponent, P = 2^(x + log2 vs - m), where it is free, and comes out of the row's sum as
+// one factor a chunk.  P in fp16 keeps eleven digits; its range holds because a row's largest weight starts at 2^6 and
+// the reference m moves before a half row's sum passes 2^15: what is lost lies below 2^-31 of the row's largest.
+//
+// A V tile is cleared where no row of the unit sees it and where a block is empty; a NaN among its codes is cleared
+// too and noted by its column: rows see the first keys of the cache, so a column's first NaN says which rows
+// get one.
+//
+// Warps: sixteen softmax warps (two a row, 64 columns each), an MMA warp a tile taking turns, one for units and loads,
+// one that converts V.  The softmax warps also make the next unit's query terms, between their last tile and the
+// output, so that its first S is computed beside the output.
+#include <atomic>
+
+#include "sa_attend8.cuh"
+
+namespace sa {
+
+namespace {
+
+constexpr int BN = 128;  // keys of a tile
+constexpr int kRing = 2;  // units in flight
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kTop = 6.f;            // a row's largest weight of its first tile is 2^6
+constexpr float kMostSum = 32768.f;    // of half a row's weights in a tile
+
+template <int D>
+struct ACfg {
+  static constexpr int kSoftWarps = 16, kMmaWarp = 16, kTmaWarp = 18, kValueWarp = 19;
+  static constexpr int kThreads = 640;
+  // 640 threads launch with 96 registers each = 61440 = 512 * 104 + 128 * 64
+  static constexpr int kRegSoft = 104, kRegOther = 64;
+  static constexpr int kTile = BN * D;  // bytes of a tile of codes
+  static constexpr int kKStages = D == 128 ? 2 : 4, kCStages = D == 128 ? 2 : 3, kVStages = D == 128 ? 2 : 4;
+  static constexpr int kQ = 0, kK = kQ + 4 * kTile, kC = kK + kKStages * kTile, kV = kC + kCStages * kTile,
+                       kX = kV + kVStages * 2 * kTile;
+  static constexpr int kWarpBytes = 2048;  // a softmax warp's own: exchange slots, output staging
+  static constexpr int kSmemBytes = 1024 + kX + kSoftWarps * kWarpBytes;
+  static constexpr int kOCol = 256, kTmemCols = 512;
+  static_assert(kSmemBytes <= 232448 - 2048, "shared memory (beside 2 KB of barriers)");
+};
+
+struct AUnit {
+  int go;              // 0: no more units
+  int key0, n, uhi;    // first key, key tiles, end of the rows' keys
+  int part, q0, b, hk; // partial result (-1: whole), first query, batch entry, key head
+  int two;             // the second tile has rows
+};
+
+template <int D>
+struct ABars {
+  using C = ACfg<D>;
+  uint64_t kfull[C::kKStages], kempty[C::kKStages], cfull[C::kCStages], cempty[C::kCStages], vfull[C::kVStages],
+      vempty[C::kVStages];
+  uint64_t qfull[2], sfull[2], pfull[2], ofull[2], ofree[2], turn[2], drain[2], next, ring_full[kRing], ring_empty[kRing];
+  uint4 answer;
+  AUnit ring[kRing];
+  int flag[8][2];
+  int nans[kRing];  // a unit's values hold a NaN
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <class T, T N>
+struct Constant {
+  static constexpr T value = N;
+};
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
+    sa_attend8_many_kernel(const __grid_constant__ Attend8Args a, const __grid_constant__ CUtensorMap tm_k,
+                           const __grid_constant__ CUtensorMap tm_v) {
+  using C = ACfg<D>;
+  constexpr int W = 16;      // S columns a register buffer holds; a chunk has one scale
+  constexpr int H = BN / 2;  // columns of a warp
+  static_assert(sizeof(ABars<D>) + kRing * D * 4 <= 2048, "shared memory");
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ ABars<D> bars;
+  __shared__ int nan_at[kRing][D];  // a unit's first key with a NaN in each column of V
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  volatile int* abort = &bars.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const MaskedArgs& m_ = a.m;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kKStages; ++s) {
+      mbar_init(&bars.kfull[s], 1);
+      mbar_init(&bars.kempty[s], 2);
+    }
+    for (int s = 0; s < C::kCStages; ++s) {
+      mbar_init(&bars.cfull[s], 1);
+      mbar_init(&bars.cempty[s], 1);
+    }
+    for (int s = 0; s < C::kVStages; ++s) {
+      mbar_init(&bars.vfull[s], 1);
+      mbar_init(&bars.vempty[s], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.qfull[i], 256);
+      mbar_init(&bars.sfull[i], 1);
+      mbar_init(&bars.pfull[i], 256);
+      mbar_init(&bars.ofull[i], 1);
+      mbar_init(&bars.ofree[i], 256);
+      mbar_init(&bars.turn[i], 1);
+      mbar_init(&bars.drain[i], 1);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&bars.ring_full[i], 1);
+      mbar_init(&bars.ring_empty[i], C::kSoftWarps + 3);
+    }
+    for (int i = 0; i < 8; ++i) bars.flag[i][0] = bars.flag[i][1] = 0;
+    mbar_init(&bars.next, 1);
+    bars.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::kMmaWarp) {
+    tmem_alloc(&bars.tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+  if (warp < C::kSoftWarps)
+    reg_alloc<C::kRegSoft>();
+  else
+    reg_dealloc<C::kRegOther>();
+
+  auto unit_here = [&](uint32_t i) -> bool { return mbar_wait(&bars.ring_full[i % kRing], (i / kRing) & 1, abort); };
+
+  if (warp < C::kSoftWarps) {
+    // ------------------------------------------------------------ softmax
+    const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+    const int col0 = half * H;
+    const int trow = quarter * 32 + lane;  // row of the tile
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t sbase = tmem + lane_base + t * 128 + col0;
+    const uint32_t obase = tmem + lane_base + C::kOCol + t * D + half * (D / 2);
+    const int rq = trow / m_.R, rh = trow - rq * m_.R;  // its query and head in the tile
+    const bool in_tile = trow < m_.qn * m_.R;
+    volatile int* flag = bars.flag[t * 4 + quarter];
+    uint32_t xn = 0;          // pair exchanges so far
+    uint32_t tc = 0, uc = 0;  // key tiles and units with keys of this Q tile so far
+    uint8_t* own = smem + C::kX + warp * C::kWarpBytes;
+    auto mine = [&]() -> float2* { return reinterpret_cast<float2*>(own) + (xn & 1) * 32 + lane; };
+    auto other = [&]() -> float2* {
+      return reinterpret_cast<float2*>(smem + C::kX + (warp ^ 4) * C::kWarpBytes) + (xn & 1) * 32 + lane;
+    };
+    // Meets the other half's warp.  A warp that gives up sets *abort and arrives once (below `done`), and
+    // whoever it releases gives up too.
+    auto pair_sync = [&]() -> bool {
+      named_barrier(1 + t * 4 + quarter, 64);
+      return *abort == 0;
+    };
+    // The row of the next unit: keys it sees, its multiplier, what value scales count from.
+    int hi_next = 0;
+    float rf_next = 0.f, lref_next = 0.f;
+    // Its query terms into shared memory.  (The last unit's products have read the old ones: its last S is here.)
+    auto prepare = [&](const AUnit& x) -> bool {
+      hi_next = 0;
+      if (x.n == 0 || (t && !x.two)) return true;
+      const int qi = x.q0 + t * m_.qn + rq;
+      const bool valid = in_tile && qi < m_.Nq;
+      uint4 u[D / 16];
+      uint32_t top = 0;
+      const uint16_t* q = m_.q + int64_t(x.b) * m_.qs.b + int64_t(x.hk * m_.R + rh) * m_.qs.h + int64_t(qi) * m_.qs.n + half * (D / 2);
+#pragma unroll
+      for (int p = 0; p < D / 16; ++p) u[p] = valid ? *reinterpret_cast<const uint4*>(q + p * 8) : make_uint4(0, 0, 0, 0);
+      if (valid) hi_next = row_span(m_.mask, x.b, qi).hi;
+#pragma unroll
+      for (int p = 0; p < D / 16; ++p) top = top_of(u[p], top);
+      *mine() = make_float2(__uint_as_float(top), 0.f);
+      if (!pair_sync()) return false;
+      top = max(top, __float_as_uint(other()->x));
+      ++xn;
+      const float f = row_factor(top);
+      rf_next = a.scale_log2 / f;
+      uint8_t* sq = smem + C::kQ + t * 2 * C::kTile;
+#pragma unroll
+      for (int p = 0; p < D / 16; p += 2) {
+        uint2 h0, l0, h1, l1;
+        two_terms(u[p], f, &h0, &l0);
+        two_terms(u[p + 1], f, &h1, &l1);
+        const uint32_t at = rows8_offset<D>(trow, half * (D / 2) + p * 8);
+        *reinterpret_cast<uint4*>(sq + at) = make_uint4(h0.x, h0.y, h1.x, h1.y);
+        *reinterpret_cast<uint4*>(sq + C::kTile + at) = make_uint4(l0.x, l0.y, l1.x, l1.y);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&bars.qfull[t]);
+      const float s0 = held_scale(__ldg(a.v_scale + int64_t(x.b) * a.v_scales.b + int64_t(x.hk) * a.v_scales.h +
+                                        (x.key0 >> a.block_log2)));
+      lref_next = s0 > 0.f ? __log2f(s0) : 0.f;
+      return true;
+    };
+    if (!unit_here(0)) goto done;
+    if (bars.ring[0].go && !prepare(bars.ring[0])) goto done;
+    for (uint32_t i = 0;; ++i) {
+      const AUnit& x = bars.ring[i % kRing];
+      if (!x.go) break;
+      const int hi = hi_next;
+      const float rf = rf_next, lref = lref_next;
+      const int n = t && !x.two ? 0 : x.n, key0 = x.key0;
+      const bool valid = in_tile && x.q0 + t * m_.qn + rq < m_.Nq;
+      const bool idle = !__any_sync(0xffffffffu, valid);
+      float m = -INFINITY, l = 0.f;  // reference (less kTop) and sum
+      {
+        // Lanes 0-3 hold the key scales of the warp's four chunks of columns, lanes 4-7 the value scales, a tile ahead.
+        const float* scales = lane < 4 ? a.k_scale + int64_t(x.b) * a.k_scales.b + int64_t(x.hk) * a.k_scales.h
+                                       : a.v_scale + int64_t(x.b) * a.v_scales.b + int64_t(x.hk) * a.v_scales.h;
+        auto fetch = [&](int c0) -> float {
+          const int key = c0 + (lane & 3) * W;
+          return lane < 8 && key < m_.Nk ? held_scale(__ldg(scales + (key >> a.block_log2))) : 0.f;
+        };
+        float ahead = n > 0 ? fetch(key0 + col0) : 0.f;
+        for (int j = 0; j < n; ++j) {
+          const int c0 = key0 + j * BN + col0;  // the warp's first key
+          const float sc = ahead;
+          if (j + 1 < n) ahead = fetch(c0 + BN);
+          const int vb = hi - c0;
+          const bool edge = __any_sync(0xffffffffu, valid && vb < H);
+          // lanes 4-7: the value scale's exponent and its inverse (0 for an empty block: its values are cleared)
+          const float lv_ = sc > 0.f && lane >= 4 ? fminf(fmaxf(__log2f(sc) - lref, -100.f), 100.f) : 0.f;
+          const float iv_ = fast_exp2(-lv_);
+          if (!mbar_wait(&bars.sfull[t], (tc + j) & 1, abort)) goto done;
+          if (idle) {
+            mbar_arrive(&bars.pfull[t]);
+            continue;
+          }
+          __syncwarp();
+          tc_fence_after();
+          auto load = [&](float* s, int base) { tmem_ld16(sbase + base, reinterpret_cast<uint32_t*>(s)); };
+          // The row's largest exponent in this tile, over both halves, and whether either half's `over` is set.
+          auto row_max = [&](float* res, bool* over) -> bool {
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int base = 0; base < H; base += W) {
+              float s[W];
+              load(s, base);
+              const float ks = __shfl_sync(0xffffffffu, sc, base / W), lv = __shfl_sync(0xffffffffu, lv_, 4 + base / W);
+              tmem_ld_wait();
+#pragma unroll
+              for (int c = 0; c < W; ++c) {
+                const float y = ks == 0.f ? lv : fmaf(s[c], rf * ks, lv);
+                mx = fmaxf(mx, base + c < vb ? y : -INFINITY);
+              }
+            }
+            *mine() = make_float2(mx, *over ? 1.f : 0.f);
+            if (!pair_sync()) return false;
+            *res = fmaxf(mx, other()->x) - kTop;
+            *over |= other()->y != 0.f;
+            ++xn;
+            return true;
+          };
+          // P = 2^(y - mm) as fp16 pairs, its sum `ts` and that without the value scales `tl`, in fp32.
+          uint32_t p[H / 2];
+          float ts, tl;
+          auto exps = [&](float mm, auto masked) {
+            ts = tl = 0.f;
+            float buf[2][W];  // the next columns load while these are worked on
+            load(buf[0], 0);
+#pragma unroll
+            for (int base = 0; base < H; base += W) {
+              float* s = buf[(base / W) & 1];
+              const float ks = __shfl_sync(0xffffffffu, sc, base / W), lv = __shfl_sync(0xffffffffu, lv_, 4 + base / W),
+                          iv = __shfl_sync(0xffffffffu, iv_, 4 + base / W);
+              tmem_ld_wait();
+              if (base + W < H) load(buf[(base / W + 1) & 1], base + W);
+              if (ks == 0.f) {  // (an empty block's keys are zeros, whatever their codes)
+#pragma unroll
+                for (int c = 0; c < W; ++c) s[c] = 0.f;
+              }
+              const float f = rf * ks, g = lv - mm;
+              const uint64_t f_2 = f2(f, f), g_2 = f2(g, g);
+              uint64_t ps = 0;
+#pragma unroll
+              for (int c = 0; c < W / 2; ++c) {
+                const uint64_t y = fma2(f2(s[2 * c], s[2 * c + 1]), f_2, g_2);
+                float y0 = f2lo(y), y1 = f2hi(y);
+                if (decltype(masked)::value) {
+                  y0 = base + 2 * c < vb ? y0 : -INFINITY;
+                  y1 = base + 2 * c + 1 < vb ? y1 : -INFINITY;
+                }
+                const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+                p[base / 2 + c] = pack_half2(p0, p1);
+                ps = add2(ps, f2(p0, p1));
+              }
+              const float sum = f2lo(ps) + f2hi(ps);
+              ts += sum;
+              tl = fmaf(sum, iv, tl);
+            }
+          };
+          // The run's first tile sets the reference: a row that sees nothing of it sees nothing of the run.
+          // Both warps of a pair hold the same references, so they agree.
+          if (j == 0) {
+            bool over = false;
+            if (!row_max(&m, &over)) goto done;
+          }
+          const float mm = m == -INFINITY ? 0.f : m;
+          if (edge)
+            exps(mm, Constant<int, 1>());
+          else
+            exps(mm, Constant<int, 0>());
+          // A row whose sum is too large in either half moves its reference (the others keep theirs: a row's bits
+          // do not go by its neighbours).
+          if (j > 0) {
+            bool over = !(ts <= kMostSum);
+            if (__any_sync(0xffffffffu, valid && over) && lane == 0) flag[xn & 1] = tc + j + 1;
+            __syncwarp();
+            if (!pair_sync()) goto done;
+            const bool raise = flag[xn & 1] == static_cast<int>(tc + j + 1);
+            ++xn;
+            if (raise) {
+              float mx;
+              if (!row_max(&mx, &over)) goto done;
+              const float mn = over ? fmaxf(m, mx) : m;
+              const float alpha = m == mn ? 1.f : fast_exp2(m - mn);
+              m = mn;
+              l *= alpha;
+              // O holds PV of every earlier tile: its commit came with this S.
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c) {
+                uint32_t r[32];
+                tmem_ld32(obase + c * 32, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int y = 0; y < 32; ++y) r[y] = __float_as_uint(__uint_as_float(r[y]) * alpha);
+                tmem_st32(obase + c * 32, r);
+              }
+              exps(m == -INFINITY ? 0.f : m, Constant<int, 1>());
+            }
+          }
+          l += tl;
+          tmem_st32(sbase, p);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&bars.pfull[t]);
+        }
+      }
+      tc += n;
+      // the next unit's query terms, ahead of this one's output
+      if (!unit_here(i + 1)) goto done;
+      if (bars.ring[(i + 1) % kRing].go && !prepare(bars.ring[(i + 1) % kRing])) goto done;
+      if (n > 0) {
+        if (!mbar_wait(&bars.ofull[t], uc & 1, abort)) goto done;
+        ++uc;
+        __syncwarp();
+        tc_fence_after();
+      }
+      if (!idle && (t == 0 || x.two)) {
+        const int qi = x.q0 + t * m_.qn + rq, hq = x.hk * m_.R + rh;
+        // both halves' sums; each half writes its half of the row
+        *mine() = make_float2(l, 0.f);
+        if (!pair_sync()) goto done;
+        l += other()->x;
+        ++xn;
+        const float inv = l == 0.f ? 0.f : fast_exp2(lref) / l;
+        const int64_t prow = int64_t(x.part) * m_.unit_rows + t * 128 + trow;
+        if (valid && half == 0) {
+          const float lse = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+          if (x.part >= 0)
+            m_.part_lse[prow] = lse;
+          else if (m_.lse)
+            m_.lse[(int64_t(x.b) * m_.Hq + hq) * m_.Nq + qi] = lse;
+        }
+        // The warp's 32 half rows go out through its own shared memory, so that consecutive lanes write
+        // consecutive bytes of a row.
+        const bool wide = x.part >= 0 || m_.out_fp32;
+        char* base = x.part >= 0 ? reinterpret_cast<char*>(m_.part_o) : static_cast<char*>(m_.o);
+        int64_t at = x.part >= 0 ? prow * D : int64_t(x.b) * m_.os.b + int64_t(hq) * m_.os.h + int64_t(qi) * m_.os.n;
+        at = valid ? (at + half * (D / 2)) * (wide ? 4 : 2) : -1;
+        uint32_t v[D / 2];
+        if (n > 0) {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) tmem_ld32(obase + c * 32, v + c * 32);
+          tmem_ld_wait();
+          tc_fence_before();
+          mbar_arrive(&bars.ofree[t]);
+#pragma unroll
+          for (int y = 0; y < D / 2; ++y) v[y] = inv == 0.f ? 0 : __float_as_uint(__uint_as_float(v[y]) * inv);
+          if (*static_cast<volatile int*>(&bars.nans[i % kRing])) {
+            const volatile int* na = nan_at[i % kRing] + half * (D / 2);
+#pragma unroll
+            for (int y = 0; y < D / 2; ++y) v[y] = na[y] < hi ? 0x7FC00000u : v[y];
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < D / 2; ++y) v[y] = 0;
+        }
+        if (!pair_sync()) goto done;  // (the other half has read this warp's slot)
+        auto put = [&](auto words) {  // words per half row
+          constexpr int PC = decltype(words)::value / 4;  // 16-byte pieces of it
+          constexpr int kRows = C::kWarpBytes / 16 / PC;  // rows at a time
+          uint4* st = reinterpret_cast<uint4*>(own);
+          auto cell = [&](int r, int c) -> uint4* {  // (no bank conflicts either way)
+            return st + r * PC + (PC >= 8 ? (c & ~7) | ((c ^ r) & 7) : c ^ ((r >> 1) & 3));
+          };
+#pragma unroll
+          for (int r0 = 0; r0 < 32; r0 += kRows) {
+            if (lane >= r0 && lane < r0 + kRows) {
+#pragma unroll
+              for (int c = 0; c < PC; ++c) *cell(lane - r0, c) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            }
+            __syncwarp();
+#pragma unroll 1
+            for (int f = 0; f < kRows * PC; f += 32) {
+              const int r = (f + lane) / PC, c = (f + lane) % PC;
+              const int64_t to = __shfl_sync(0xffffffffu, at, r0 + r);
+              const uint4 w = *cell(r, c);
+              if (to >= 0) *reinterpret_cast<uint4*>(base + to + c * 16) = w;
+            }
+            __syncwarp();
+          }
+        };
+        if (wide) {
+          put(Constant<int, D / 2>());
+        } else {
+#pragma unroll
+          for (int y = 0; y < D / 4; ++y)
+            v[y] = pack_bf16(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1]));
+          put(Constant<int, D / 4>());
+        }
+      } else if (n > 0) {
+        mbar_arrive(&bars.ofree[t]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.ring_empty[i % kRing]);
+    }
+  } else if (warp < C::kTmaWarp) {
+    // ------------------------------------------------------------ MMA issue, a warp for each Q tile
+    const int t = warp - C::kMmaWarp;
+    constexpr uint32_t kIdescS = idesc_f8(128, BN, 0, 0, false, false);
+    // (kind::f16 with both operands fp16; V is MN-major)
+    constexpr uint32_t kIdescPV = idesc_bf16(128, D, false, true) & ~((1u << 7) | (1u << 10));
+    const uint64_t dq = rows8_desc<D>(smem_u32(smem + C::kQ) + t * 2 * C::kTile, 16);
+    const uint64_t dk = rows8_desc<D>(smem_u32(smem + C::kK), 16), dv = sw128_desc(smem_u32(smem + C::kV), BN * 128, 1024);
+    const uint32_t q_lo = static_cast<uint32_t>(dq), q_hi = static_cast<uint32_t>(dq >> 32);
+    const uint32_t k_lo = static_cast<uint32_t>(dk), k_hi = static_cast<uint32_t>(dk >> 32);
+    const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
+    const uint32_t o_tmem = tmem + C::kOCol + t * D, s_tmem = tmem + t * 128;
+    if (lane == 0) {
+      bool ok = true, two = false;
+      uint32_t tc = 0, uc = 0;  // key tiles (of the ring) and units of this tile so far
+      uint32_t pc = 0, ts = 0;  // key tiles of this Q tile, steps taken in turns
+      auto pass = [&]() { mbar_arrive(&bars.turn[t ^ 1]); };
+      auto free_both = [&](uint64_t* bar) {  // (a tile alone counts for both)
+        mma_commit(bar);
+        if (!two) mma_commit(bar);
+      };
+      auto qk = [&](uint32_t c, bool turn) {
+        const uint32_t kl = k_lo + (((c % C::kKStages) * C::kTile) >> 4);
+        constexpr int kSteps = 2 * (D / 32);
+#pragma unroll
+        for (int kk = 0; kk < kSteps; ++kk) {
+          const uint32_t off = (kk % (D / 32)) * 2, term = kk < D / 32 ? 0 : C::kTile >> 4;
+          mma8_ss_w(s_tmem, q_lo + term + off, q_hi, kl + off, k_hi, kIdescS, kk > 0);
+          if (kk == kSteps - 3 && turn) pass();  // (two MMAs cover the hand-over)
+        }
+        mma_commit(&bars.sfull[t]);
+      };
+      for (uint32_t i = 0; ok; ++i) {
+        if (!unit_here(i)) break;
+        const AUnit& u = bars.ring[i % kRing];
+        const int go = u.go, n = u.n;
+        two = u.two;
+        mbar_arrive(&bars.ring_empty[i % kRing]);
+        if (!go) break;
+        if (n == 0 || (t && !two)) {
+          tc += n;
+          continue;
+        }
+        if (!(ok = mbar_wait(&bars.qfull[t], uc & 1, abort)) ||
+            !(ok = mbar_wait(&bars.kfull[tc % C::kKStages], (tc / C::kKStages) & 1, abort)))
+          break;
+        tc_fence_after();
+        qk(tc, false);
+        free_both(&bars.kempty[tc % C::kKStages]);
+        for (int j = 0; j < n; ++j) {
+          const uint32_t c = tc + j, s = ts + j;
+          const bool more = j + 1 < n;
+          if (!(ok = mbar_wait(&bars.vfull[c % C::kVStages], (c / C::kVStages) & 1, abort)) ||
+              (more && !(ok = mbar_wait(&bars.kfull[(c + 1) % C::kKStages], ((c + 1) / C::kKStages) & 1, abort))))
+            break;
+          if (j == 0 && uc > 0 && !(ok = mbar_wait(&bars.ofree[t], (uc - 1) & 1, abort))) break;
+          // Turns: the tiles' steps alternate (side by side they would fall into step and leave the tensor core
+          // idle during both softmaxes).
+          if (two && s + t > 0 && !(ok = mbar_wait(&bars.turn[t], (s + t - 1) & 1, abort))) break;
+          if (!(ok = mbar_wait(&bars.pfull[t], (pc + j) & 1, abort))) break;
+          tc_fence_after();
+          const uint32_t vl = v_lo + (((c % C::kVStages) * 2 * C::kTile) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            // P of keys 0-63 lies in S columns 0-31, of keys 64-127 in 64-95
+            mma_ts_w(o_tmem, s_tmem + (kk >> 2) * 64 + (kk & 3) * 8, vl + ((kk * 2048) >> 4), v_hi, kIdescPV, j > 0 || kk > 0);
+          if (more)
+            qk(c + 1, two);
+          else if (two)
+            pass();
+          if (!more) mma_commit(&bars.ofull[t]);
+          free_both(&bars.vempty[c % C::kVStages]);
+          if (more) free_both(&bars.kempty[(c + 1) % C::kKStages]);
+        }
+        tc += n;
+        pc += n;
+        if (two) ts += n;
+        ++uc;
+      }
+      // Every MMA issued above must finish before TMEM is released.
+      mma_commit(&bars.drain[t]);
+      const long long t0 = clock64();
+      while (!mbar_test(&bars.drain[t], 0) && clock64() - t0 < kWaitLimitCycles) {
+      }
+    }
+  } else if (warp == C::kValueWarp) {
+    // ------------------------------------------------------------ V: codes to fp16
+    uint32_t c = 0;  // key tiles so far
+    constexpr int kLanes = D / 16, kRows = 32 / kLanes;  // lanes a row, rows at a time
+    // d = 128: eight lanes store 16-byte pieces without bank conflicts if they are four of a row and four of the next
+    const int r_lane = D == 128 ? ((lane >> 2) & 1) + 2 * (lane >> 4) : lane / kLanes;
+    const int p_lane = D == 128 ? (lane & 3) + 4 * ((lane >> 3) & 1) : lane % kLanes;
+    for (uint32_t i = 0;; ++i) {
+      if (!unit_here(i)) break;
+      const AUnit x = bars.ring[i % kRing];
+      if (!x.go) break;
+      for (int y = lane; y < D; y += 32) nan_at[i % kRing][y] = 0x7FFFFFFF;
+      if (lane == 0) bars.nans[i % kRing] = 0;
+      __syncwarp();
+      const float* scales = a.v_scale + int64_t(x.b) * a.v_scales.b + int64_t(x.hk) * a.v_scales.h;
+      auto fetch = [&](int k0) -> float {  // lane: 16 keys of a tile
+        const int key = k0 + (lane & 7) * 16;
+        return key < m_.Nk ? held_scale(__ldg(scales + (key >> a.block_log2))) : 0.f;
+      };
+      float ahead = x.n > 0 ? fetch(x.key0) : 0.f;
+      bool ok = true;
+      for (int j = 0; j < x.n; ++j, ++c) {
+        const int k0 = x.key0 + j * BN, live = x.uhi - k0;
+        const uint32_t filled = __ballot_sync(0xffffffffu, ahead > 0.f);  // bit r / 16: row r's block is not empty
+        if (j + 1 < x.n) ahead = fetch(k0 + BN);
+        const uint32_t cs = c % C::kCStages, vs = c % C::kVStages;
+        if (!(ok = mbar_wait(&bars.cfull[cs], (c / C::kCStages) & 1, abort)) ||
+            !(ok = mbar_wait(&bars.vempty[vs], ((c / C::kVStages) & 1) ^ 1, abort)))
+          break;
+        __syncwarp();
+        const uint8_t* from = smem + C::kC + cs * C::kTile + r_lane * D + p_lane * 16;
+        uint8_t* to = smem + C::kV + vs * 2 * C::kTile + (p_lane >> 2) * BN * 128 + r_lane * 128;
+        const int ch = (p_lane & 3) * 2;
+        const bool all = live >= BN && (filled & 255u) == 255u;
+        uint32_t odd = 0;
+#pragma unroll 4
+        for (int f = 0; f < BN / kRows; ++f) {
+          const int r = f * kRows + r_lane;
+          uint4 w = *reinterpret_cast<const uint4*>(from + f * kRows * D);
+          uint32_t e[4] = {w.x, w.y, w.z, w.w};
+          if (!all && (r >= live || !(filled >> (r >> 4) & 1))) e[0] = e[1] = e[2] = e[3] = 0;
+          uint32_t bad = 0;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) bad |= (e[y] & 0x7F7F7F7Fu) + 0x01010101u;
+          if (bad & 0x80808080u) {
+            odd = 1;
+            for (int y = 0; y < 16; ++y)
+              if ((e[y >> 2] >> (8 * (y & 3)) & 127) == 127) {
+                atomicMin(&nan_at[i % kRing][p_lane * 16 + y], k0 + r);
+                e[y >> 2] &= ~(255u << (8 * (y & 3)));
+              }
+          }
+          uint32_t o[8];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            o[2 * y] = decode2(e[y] & 0xFFFFu);
+            o[2 * y + 1] = decode2(e[y] >> 16);
+          }
+          uint8_t* row = to + f * kRows * 128;
+          *reinterpret_cast<uint4*>(row + ((ch ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        if (odd) bars.nans[i % kRing] = 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars.vfull[vs]);
+          mbar_arrive(&bars.cempty[cs]);
+        }
+      }
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(&bars.ring_empty[i % kRing]);
+    }
+  } else if (lane == 0) {
+    // ------------------------------------------------------------ units and loads
+    int64_t g = blockIdx.x;
+    uint32_t c = 0, i = 0;
+    bool ok = true;
+    for (; ok; ++i) {
+      AUnit x = {};
+      if (g >= 0) {
+        mbar_expect_tx(&bars.next, 16);
+        request_block(&bars.answer, &bars.next);
+        // (the order of units and their splits: masked_plan)
+        int u = static_cast<int>(g), split = 0, splits = 1;
+        x.go = 1;
+        x.part = -1;
+        if (g >= m_.full_units) {
+          splits = m_.splits;
+          x.part = static_cast<int>(g - m_.full_units);
+          split = x.part % splits;
+          u = static_cast<int>(m_.full_units) + x.part / splits;
+        }
+        const MaskedPlace at = masked_place(m_, u);
+        x.b = at.bh / m_.Hkv;
+        x.hk = at.bh - x.b * m_.Hkv;
+        x.q0 = at.rb * (m_.tiles * m_.qn);
+        const int q1 = min(x.q0 + m_.tiles * m_.qn, m_.Nq);
+        x.two = m_.tiles == 2 && x.q0 + m_.qn < q1;
+        x.uhi = row_span(m_.mask, x.b, q1 - 1).hi;
+        const int tiles = (x.uhi + BN - 1) / BN;
+        const int j0 = static_cast<int>(int64_t(tiles) * split / splits);
+        x.n = static_cast<int>(int64_t(tiles) * (split + 1) / splits) - j0;
+        x.key0 = j0 * BN;
+      }
+      if (i >= kRing && !mbar_wait(&bars.ring_empty[i % kRing], ((i / kRing) - 1) & 1, abort)) break;
+      bars.ring[i % kRing] = x;
+      mbar_arrive(&bars.ring_full[i % kRing]);
+      if (g < 0) break;
+      for (int j = 0; j < x.n; ++j, ++c) {
+        const uint32_t ks = c % C::kKStages, cs = c % C::kCStages;
+        if (!(ok = mbar_wait(&bars.kempty[ks], ((c / C::kKStages) & 1) ^ 1, abort))) break;
+        mbar_expect_tx(&bars.kfull[ks], C::kTile);
+        tma_load_4d(smem_u32(smem + C::kK) + ks * C::kTile, &tm_k, 0, x.key0 + j * BN, x.hk, x.b, &bars.kfull[ks]);
+        if (!(ok = mbar_wait(&bars.cempty[cs], ((c / C::kCStages) & 1) ^ 1, abort))) {
+          // (the K tile lands before the block ends)
+          const long long t0 = clock64();
+          while (!mbar_test(&bars.kfull[ks], (c / C::kKStages) & 1) && clock64() - t0 < kWaitLimitCycles) {
+          }
+          break;
+        }
+        mbar_expect_tx(&bars.cfull[cs], C::kTile);
+        tma_load_4d(smem_u32(smem + C::kC) + cs * C::kTile, &tm_v, 0, x.key0 + j * BN, x.hk, x.b, &bars.cfull[cs]);
+      }
+      if (!ok) break;
+      if (!(ok = mbar_wait(&bars.next, i & 1, abort))) break;
+      g = answered_block(&bars.answer);
+      fence_proxy_async_smem();  // read before the next answer is written
+    }
+    if (*abort) {
+      // After an abort: what is in flight lands before the block ends.
+      auto settle = [&](uint64_t* bar, uint32_t parity) {
+        const long long t0 = clock64();
+        while (!mbar_test(bar, parity) && clock64() - t0 < kWaitLimitCycles) {
+        }
+      };
+      for (uint32_t f = c > C::kKStages ? c - C::kKStages : 0; f < c; ++f)
+        settle(&bars.kfull[f % C::kKStages], (f / C::kKStages) & 1);
+      for (uint32_t f = c > C::kCStages ? c - C::kCStages : 0; f < c; ++f)
+        settle(&bars.cfull[f % C::kCStages], (f / C::kCStages) & 1);
+      if (g >= 0) settle(&bars.next, i & 1);
+    }
+  }
+done:
+  if (warp < C::kSoftWarps && *abort) named_barrier_arrive(1 + (warp >> 3) * 4 + (warp & 3), 64);
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && bars.abort) report(m_.status, SA_DEVERR_TIMEOUT);
+  if (warp == C::kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Units, splits and their order are the masked forward's.
+void attend8_many_plan(Attend8Args* a) {
+  masked_plan(&a->m);
+  a->m.quads = a->m.slots = 0;
+  a->m.unit_rows = 128 * a->m.tiles;
+}
+
+template <int D>
+static cudaError_t launch_a(const Attend8Args& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
+  using C = ACfg<D>;
+  auto kern = sa_attend8_many_kernel<D>;
+  // at least half the SM's shared memory: one block per SM owns its TMEM
+  const int smem = C::kSmemBytes > 120 * 1024 ? C::kSmemBytes : 120 * 1024;
+  static std::atomic<int> regs_ok{0};  // 0 unknown, 1 enough, 2 too few
+  if (regs_ok.load() == 0) {
+    cudaFuncAttributes attr;
+    cudaError_t e = cudaFuncGetAttributes(&attr, kern);
+    if (e != cudaSuccess) return e;
+    // setmaxnreg.inc waits until the block's launch registers cover the split
+    const long need = long(C::kRegSoft) * C::kSoftWarps * 32 + long(C::kRegOther) * 128;
+    regs_ok.store(long(attr.numRegs) * C::kThreads >= need ? 1 : 2);
+  }
+  if (regs_ok.load() != 1) return cudaErrorLaunchOutOfResources;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = a.m.full_units + a.m.split_units * a.m.splits;
+  kern<<<static_cast<unsigned>(grid), C::kThreads, smem, st>>>(a, tk, tv);
+  if ((e = cudaGetLastError()) != cudaSuccess || a.m.split_units == 0) return e;
+  return launch_masked_join(a.m, st);
+}
+
+cudaError_t launch_attend8_many(const Attend8Args& a, cudaStream_t st) {
+  CUtensorMap tk, tv;
+  if (!make_codes_map(&tk, a.k8, a.m.d, a.m.Nk, a.m.Hkv, a.m.B, a.m.ks, BN, true) ||
+      !make_codes_map(&tv, a.v8, a.m.d, a.m.Nk, a.m.Hkv, a.m.B, a.m.vs, BN, false))
+    return cudaErrorInvalidValue;
+  return a.m.d == 128 ? launch_a<128>(a, tk, tv, st) : launch_a<64>(a, tk, tv, st);
+}
+
+}  // namespace sa

@@ -121,7 +121,7 @@ sa_status check_attend(const sa_attend8* p, const sa_cache8* c, Attend8Args* a) 
   m.total_rows = heads * R * p->Nq;
   a->scale_log2 = p->scale * 1.4426950408889634f;
   while ((1 << a->block_log2) < c->block) ++a->block_log2;
-  if (!attend8_few(*a)) return SA_ERR_UNSUPPORTED;
+  if (!attend8_few(*a)) attend8_many_plan(a);
   return SA_OK;
 }
 
@@ -130,7 +130,8 @@ struct Parts {
   size_t o, lse;
 };
 Parts parts_of(const Attend8Args& a) {
-  const size_t rows = (size_t(attend8_few_grid(a)) + size_t(a.m.B) * a.m.Hkv) * a.m.R * a.m.Nq;
+  const size_t rows = attend8_few(a) ? (size_t(attend8_few_grid(a)) + size_t(a.m.B) * a.m.Hkv) * a.m.R * a.m.Nq
+                                     : size_t(a.m.split_units) * a.m.splits * a.m.unit_rows;
   return {(rows * a.m.d * 4 + 255) / 256 * 256, (rows * 4 + 255) / 256 * 256};
 }
 
@@ -197,7 +198,8 @@ sa_status sparse_attn_forward_cache8(const sa_attend8* p, const sa_cache8* cache
     m.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + n.o);
   }
   NvtxRange range("sparse_attn_forward_cache8");
-  return map_cuda(launch_attend8_few(a, reinterpret_cast<cudaStream_t>(stream)));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return map_cuda(attend8_few(a) ? launch_attend8_few(a, s) : launch_attend8_many(a, s));
 }
 
 sa_status sparse_attn_cache8_append(const sa_cache8* p, int32_t n, const void* k, const sa_strides* ks, const void* v,

@@ -156,6 +156,18 @@ struct MaskedArgs {
                        // then how many each head has [B]
 };
 void masked_plan(MaskedArgs* a);
+// Unit number -> key head of the batch and row block.
+struct MaskedPlace {
+  int bh, rb;
+};
+__host__ __device__ __forceinline__ MaskedPlace masked_place(const MaskedArgs& a, int u) {
+  const int per = a.group * a.row_blocks, grp = u / per, r = u - grp * per;
+  const int heads = a.B * a.Hkv - grp * a.group < a.group ? a.B * a.Hkv - grp * a.group : a.group;
+  const int k = r / heads;
+  return {grp * a.group + (r - k * heads), a.row_blocks - 1 - k};
+}
+// Joins the partial results of the split units (not those of quads).
+cudaError_t launch_masked_join(const MaskedArgs& a, cudaStream_t stream);
 cudaError_t launch_masked(const MaskedArgs& a, cudaStream_t stream);
 
 struct WeightArgs {
@@ -238,6 +250,8 @@ struct Attend8Args {
 inline bool attend8_few(const Attend8Args& a) { return int64_t(a.m.R) * a.m.Nq <= 32 && a.m.B <= kMostEntries; }
 int attend8_few_grid(const Attend8Args& a);
 cudaError_t launch_attend8_few(const Attend8Args& a, cudaStream_t stream);
+void attend8_many_plan(Attend8Args* a);
+cudaError_t launch_attend8_many(const Attend8Args& a, cudaStream_t stream);
 
 // sparse_attn_layer_from_host splits a layer into at most this many chunks.
 constexpr int kMaxPipelineChunks = 64;

@@ -107,17 +107,6 @@ struct MBars {
   int abort, steps;  // steps: of rows_again
 };
 
-// Unit number -> key head of the batch and row block.
-struct Place {
-  int bh, rb;
-};
-__host__ __device__ __forceinline__ Place place_of(const MaskedArgs& a, int u) {
-  const int per = a.group * a.row_blocks, grp = u / per, r = u - grp * per;
-  const int heads = a.B * a.Hkv - grp * a.group < a.group ? a.B * a.Hkv - grp * a.group : a.group;
-  const int k = r / heads;
-  return {grp * a.group + (r - k * heads), a.row_blocks - 1 - k};
-}
-
 // Key tiles that the rows of a unit with the queries q0 .. q1 see.
 __device__ __forceinline__ int tiles_of(const MaskedArgs& a, int b, int q0, int q1, int* lo, int* hi) {
   *lo = row_span(a.mask, b, q0).lo;
@@ -946,7 +935,7 @@ __global__ void __launch_bounds__(MCfg<D, T>::kThreads, 1)
           split = x.part % splits;
           u = static_cast<int>(a.full_units) + x.part / splits;
         }
-        const Place at = place_of(a, u);
+        const MaskedPlace at = masked_place(a, u);
         const int bh = at.bh;
         x.q0 = at.rb * (T * a.qn);
         x.b = bh / a.Hkv;
@@ -1025,7 +1014,7 @@ __global__ void __launch_bounds__(128) sa_masked_join_kernel(const __grid_consta
   const uint32_t tile_rows = a.qn * a.R, unit_rows = a.tiles * tile_rows;  // that exist
   const uint32_t su = i / unit_rows, r = i - su * unit_rows, t = r / tile_rows, tr = r - t * tile_rows;
   if (su >= a.split_units) return;
-  const Place at = place_of(a, static_cast<int>(a.full_units + su));
+  const MaskedPlace at = masked_place(a, static_cast<int>(a.full_units + su));
   const int q = at.rb * (a.tiles * a.qn) + t * a.qn + tr / a.R;
   if (q >= a.Nq) return;
   const int64_t row0 = int64_t(su) * a.splits * a.unit_rows + t * 128 + tr;
@@ -1080,7 +1069,7 @@ __global__ void __launch_bounds__(512) sa_masked_join_quads_kernel(const __grid_
   wait_for_earlier_kernel();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = a.qn * a.R, su = blockIdx.x / rows, tr = blockIdx.x - su * rows;
-  const int bh = place_of(a, su).bh, b = bh / a.Hkv, hk = bh - b * a.Hkv;
+  const int bh = masked_place(a, su).bh, b = bh / a.Hkv, hk = bh - b * a.Hkv;
   int parts = a.splits;
   int64_t first = int64_t(su) * parts;
   if (a.slots) {
@@ -1179,7 +1168,7 @@ void masked_plan(MaskedArgs* a) {
   const int64_t units = heads * a->row_blocks, rest = units % kSms;
   int64_t seen = 0;  // keys that the last units see
   for (int64_t u = units - rest; u < units; ++u) {
-    const int64_t q1 = min64(a->Nq, (place_of(*a, static_cast<int>(u)).rb + 1) * unit_q);
+    const int64_t q1 = min64(a->Nq, (masked_place(*a, static_cast<int>(u)).rb + 1) * unit_q);
     int64_t hi = a->Nk;
     if (a->mask.causal) {
       const int64_t pos = q1 - 1 + a->Nk - a->Nq;
@@ -1255,7 +1244,13 @@ static cudaError_t launch_d(const MaskedArgs& a, const CUtensorMap& q, const CUt
   const int64_t rows = a.split_units * a.tiles * a.qn * a.R;
   if (a.quads)
     return launch_early(sa_masked_join_quads_kernel<D>, dim3(static_cast<unsigned>(rows)), 512, 0, st, a);
-  return launch_early(sa_masked_join_kernel<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, st, a);
+  return launch_masked_join(a, st);
+}
+
+cudaError_t launch_masked_join(const MaskedArgs& a, cudaStream_t st) {
+  const int64_t rows = a.split_units * a.tiles * a.qn * a.R;
+  return launch_early(a.d == 128 ? sa_masked_join_kernel<128> : sa_masked_join_kernel<64>,
+                      dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, st, a);
 }
 
 cudaError_t launch_masked(const MaskedArgs& a, cudaStream_t st) {
