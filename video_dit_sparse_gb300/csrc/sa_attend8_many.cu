@@ -8,8 +8,8 @@
 // the 16 columns that a chunk of the softmax works on.
 //
 // O = P V cannot have P in eight bits (a term holds four digits, and cutting P in terms would cost the softmax more
-// than its exponentials).  So V's codes become fp16 on the way: one instruction for two of them, exact, by a warp of its
-// own.  V's scale goes into P's exponent, P = 2^(x + log2 vs - m), where it is free, and comes out of the row's sum as
+// than its exponentials).  So V's codes become fp16 on the way: one instruction for two of them, exact.
+// V's scale goes into P's exponent, P = 2^(x + log2 vs - m), where it is free, and comes out of the row's sum as
 // one factor a chunk.  P in fp16 keeps eleven digits; its range holds because a row's largest weight starts at 2^6 and
 // the reference m moves before a half row's sum passes 2^15: what is lost lies below 2^-31 of the row's largest.
 //
@@ -17,9 +17,10 @@
 // too and noted by its column: rows see the first keys of the cache, so a column's first NaN says which rows
 // get one.
 //
-// Warps: sixteen softmax warps (two a row, 64 columns each), an MMA warp a tile taking turns, one for units and loads,
-// one that converts V.  The softmax warps also make the next unit's query terms, between their last tile and the
-// output, so that its first S is computed beside the output.
+// Warps: sixteen softmax warps (two a row, 64 columns each), an MMA warp a tile taking turns, one for units and loads.
+// The softmax warps convert V too, a sixteenth of the next tile each behind their P, while they would wait for S
+// (a warp of its own for it took 5000 cycles a tile: 12 heads, 7040 rows x 28160 keys 1124 us), and make the next
+// unit's query terms between their last tile and the output, so that its first S is computed beside the output.
 #include <atomic>
 
 #include "sa_attend8.cuh"
@@ -36,7 +37,7 @@ constexpr float kMostSum = 32768.f;    // of half a row's weights in a tile
 
 template <int D>
 struct ACfg {
-  static constexpr int kSoftWarps = 16, kMmaWarp = 16, kTmaWarp = 18, kValueWarp = 19;
+  static constexpr int kSoftWarps = 16, kMmaWarp = 16, kTmaWarp = 18;
   static constexpr int kThreads = 640;
   // 640 threads launch with 96 registers each = 61440 = 512 * 104 + 128 * 64
   static constexpr int kRegSoft = 104, kRegOther = 64;
@@ -107,10 +108,10 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
     }
     for (int s = 0; s < C::kCStages; ++s) {
       mbar_init(&bars.cfull[s], 1);
-      mbar_init(&bars.cempty[s], 1);
+      mbar_init(&bars.cempty[s], C::kSoftWarps);
     }
     for (int s = 0; s < C::kVStages; ++s) {
-      mbar_init(&bars.vfull[s], 1);
+      mbar_init(&bars.vfull[s], C::kSoftWarps);
       mbar_init(&bars.vempty[s], 2);
     }
     for (int i = 0; i < 2; ++i) {
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&bars.ring_full[i], 1);
-      mbar_init(&bars.ring_empty[i], C::kSoftWarps + 3);
+      mbar_init(&bars.ring_empty[i], C::kSoftWarps + 2);
     }
     for (int i = 0; i < 8; ++i) bars.flag[i][0] = bars.flag[i][1] = 0;
     mbar_init(&bars.next, 1);
@@ -170,79 +171,145 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
       named_barrier(1 + t * 4 + quarter, 64);
       return *abort == 0;
     };
+    // Scales that the warp needs of a tile, fetched a tile ahead: lanes 0-3 the key scales of its four chunks of columns,
+    // lanes 4-7 the value scales, lane 8 that of the eight keys whose values it converts.
+    const float* scales = nullptr;
+    float ahead = 0.f;
+    auto fetch = [&](int k0) -> float {
+      const int key = k0 + (lane < 8 ? col0 + (lane & 3) * W : warp * 8);
+      return lane < 9 && key < m_.Nk ? held_scale(__ldg(scales + (key >> a.block_log2))) : 0.f;
+    };
+    // The warp's eight keys of a tile's values from codes to fp16.
+    uint32_t vc = 0;  // tiles converted so far
+    auto convert = [&](uint32_t slot, int k0) -> bool {
+      constexpr int kLanes = D / 16, kRows = 32 / kLanes;  // lanes a row, rows at a time
+      // d = 128: eight lanes store 16-byte pieces without bank conflicts if they are four of a row and four of the next
+      const int r_lane = D == 128 ? ((lane >> 2) & 1) + 2 * (lane >> 4) : lane / kLanes;
+      const int p_lane = D == 128 ? (lane & 3) + 4 * ((lane >> 3) & 1) : lane % kLanes;
+      const uint32_t cs = vc % C::kCStages, vs = vc % C::kVStages;
+      const bool filled = __shfl_sync(0xffffffffu, ahead, 8) > 0.f;
+      const int live = filled ? bars.ring[slot].uhi - k0 : 0;
+      if (!mbar_wait(&bars.cfull[cs], (vc / C::kCStages) & 1, abort) ||
+          !mbar_wait(&bars.vempty[vs], ((vc / C::kVStages) & 1) ^ 1, abort))
+        return false;
+      __syncwarp();
+      uint4 w[8 / kRows];
+      uint32_t bad = 0;
+#pragma unroll
+      for (int y = 0; y < 8 / kRows; ++y) {
+        const int r = warp * 8 + y * kRows + r_lane;
+        w[y] = *reinterpret_cast<const uint4*>(smem + C::kC + cs * C::kTile + r * D + p_lane * 16);
+        if (r >= live) w[y] = make_uint4(0, 0, 0, 0);
+        bad |= ((w[y].x & 0x7F7F7F7Fu) + 0x01010101u) | ((w[y].y & 0x7F7F7F7Fu) + 0x01010101u) |
+               ((w[y].z & 0x7F7F7F7Fu) + 0x01010101u) | ((w[y].w & 0x7F7F7F7Fu) + 0x01010101u);
+      }
+      if (bad & 0x80808080u) {
+        bars.nans[slot] = 1;
+#pragma unroll
+        for (int y = 0; y < 8 / kRows; ++y) {
+          auto sift = [&](uint32_t e, int p) -> uint32_t {
+            for (int b = 0; b < 4; ++b)
+              if ((e >> (8 * b) & 127) == 127) {
+                atomicMin(&nan_at[slot][p_lane * 16 + p + b], k0 + warp * 8 + y * kRows + r_lane);
+                e &= ~(255u << (8 * b));
+              }
+            return e;
+          };
+          w[y] = make_uint4(sift(w[y].x, 0), sift(w[y].y, 4), sift(w[y].z, 8), sift(w[y].w, 12));
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < 8 / kRows; ++y) {
+        const int r = warp * 8 + y * kRows + r_lane, ch = (p_lane & 3) * 2;
+        uint8_t* row = smem + C::kV + vs * 2 * C::kTile + (p_lane >> 2) * BN * 128 + r * 128;
+        *reinterpret_cast<uint4*>(row + ((ch ^ (r & 7)) << 4)) =
+            make_uint4(decode2(w[y].x & 0xFFFFu), decode2(w[y].x >> 16), decode2(w[y].y & 0xFFFFu), decode2(w[y].y >> 16));
+        *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (r & 7)) << 4)) =
+            make_uint4(decode2(w[y].z & 0xFFFFu), decode2(w[y].z >> 16), decode2(w[y].w & 0xFFFFu), decode2(w[y].w >> 16));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bars.vfull[vs]);
+        mbar_arrive(&bars.cempty[cs]);
+      }
+      ++vc;
+      return true;
+    };
     // The row of the next unit: keys it sees, its multiplier, what value scales count from.
     int hi_next = 0;
     float rf_next = 0.f, lref_next = 0.f;
-    // Its query terms into shared memory.  (The last unit's products have read the old ones: its last S is here.)
-    auto prepare = [&](const AUnit& x) -> bool {
+    // The next unit's query terms into shared memory, and its first values.  (The last unit's products have read
+    // the old terms: its last S is here.)
+    auto prepare = [&](uint32_t slot) -> bool {
+      const AUnit& x = bars.ring[slot];
       hi_next = 0;
-      if (x.n == 0 || (t && !x.two)) return true;
-      const int qi = x.q0 + t * m_.qn + rq;
-      const bool valid = in_tile && qi < m_.Nq;
-      uint4 u[D / 16];
-      uint32_t top = 0;
-      const uint16_t* q = m_.q + int64_t(x.b) * m_.qs.b + int64_t(x.hk * m_.R + rh) * m_.qs.h + int64_t(qi) * m_.qs.n + half * (D / 2);
+      if (x.n == 0) return true;
+      scales = lane < 4 ? a.k_scale + int64_t(x.b) * a.k_scales.b + int64_t(x.hk) * a.k_scales.h
+                        : a.v_scale + int64_t(x.b) * a.v_scales.b + int64_t(x.hk) * a.v_scales.h;
+      ahead = fetch(x.key0);
+      if (t == 0 || x.two) {
+        const int qi = x.q0 + t * m_.qn + rq;
+        const bool valid = in_tile && qi < m_.Nq;
+        uint4 u[D / 16];
+        uint32_t top = 0;
+        const uint16_t* q = m_.q + int64_t(x.b) * m_.qs.b + int64_t(x.hk * m_.R + rh) * m_.qs.h + int64_t(qi) * m_.qs.n + half * (D / 2);
 #pragma unroll
-      for (int p = 0; p < D / 16; ++p) u[p] = valid ? *reinterpret_cast<const uint4*>(q + p * 8) : make_uint4(0, 0, 0, 0);
-      if (valid) hi_next = row_span(m_.mask, x.b, qi).hi;
+        for (int p = 0; p < D / 16; ++p) u[p] = valid ? *reinterpret_cast<const uint4*>(q + p * 8) : make_uint4(0, 0, 0, 0);
+        if (valid) hi_next = row_span(m_.mask, x.b, qi).hi;
 #pragma unroll
-      for (int p = 0; p < D / 16; ++p) top = top_of(u[p], top);
-      *mine() = make_float2(__uint_as_float(top), 0.f);
-      if (!pair_sync()) return false;
-      top = max(top, __float_as_uint(other()->x));
-      ++xn;
-      const float f = row_factor(top);
-      rf_next = a.scale_log2 / f;
-      uint8_t* sq = smem + C::kQ + t * 2 * C::kTile;
+        for (int p = 0; p < D / 16; ++p) top = top_of(u[p], top);
+        *mine() = make_float2(__uint_as_float(top), 0.f);
+        if (!pair_sync()) return false;
+        top = max(top, __float_as_uint(other()->x));
+        ++xn;
+        const float f = row_factor(top);
+        rf_next = a.scale_log2 / f;
+        uint8_t* sq = smem + C::kQ + t * 2 * C::kTile;
 #pragma unroll
-      for (int p = 0; p < D / 16; p += 2) {
-        uint2 h0, l0, h1, l1;
-        two_terms(u[p], f, &h0, &l0);
-        two_terms(u[p + 1], f, &h1, &l1);
-        const uint32_t at = rows8_offset<D>(trow, half * (D / 2) + p * 8);
-        *reinterpret_cast<uint4*>(sq + at) = make_uint4(h0.x, h0.y, h1.x, h1.y);
-        *reinterpret_cast<uint4*>(sq + C::kTile + at) = make_uint4(l0.x, l0.y, l1.x, l1.y);
+        for (int p = 0; p < D / 16; p += 2) {
+          uint2 h0, l0, h1, l1;
+          two_terms(u[p], f, &h0, &l0);
+          two_terms(u[p + 1], f, &h1, &l1);
+          const uint32_t at = rows8_offset<D>(trow, half * (D / 2) + p * 8);
+          *reinterpret_cast<uint4*>(sq + at) = make_uint4(h0.x, h0.y, h1.x, h1.y);
+          *reinterpret_cast<uint4*>(sq + C::kTile + at) = make_uint4(l0.x, l0.y, l1.x, l1.y);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bars.qfull[t]);
+        const float s0 = held_scale(__ldg(a.v_scale + int64_t(x.b) * a.v_scales.b + int64_t(x.hk) * a.v_scales.h +
+                                          (x.key0 >> a.block_log2)));
+        lref_next = s0 > 0.f ? __log2f(s0) : 0.f;
       }
-      fence_proxy_async_smem();
-      mbar_arrive(&bars.qfull[t]);
-      const float s0 = held_scale(__ldg(a.v_scale + int64_t(x.b) * a.v_scales.b + int64_t(x.hk) * a.v_scales.h +
-                                        (x.key0 >> a.block_log2)));
-      lref_next = s0 > 0.f ? __log2f(s0) : 0.f;
-      return true;
+      return convert(slot, x.key0);
     };
     if (!unit_here(0)) goto done;
-    if (bars.ring[0].go && !prepare(bars.ring[0])) goto done;
+    if (bars.ring[0].go && !prepare(0)) goto done;
     for (uint32_t i = 0;; ++i) {
       const AUnit& x = bars.ring[i % kRing];
       if (!x.go) break;
       const int hi = hi_next;
       const float rf = rf_next, lref = lref_next;
-      const int n = t && !x.two ? 0 : x.n, key0 = x.key0;
+      const bool here = t == 0 || x.two;  // the tile has rows
+      const int n = x.n, key0 = x.key0;
       const bool valid = in_tile && x.q0 + t * m_.qn + rq < m_.Nq;
       const bool idle = !__any_sync(0xffffffffu, valid);
       float m = -INFINITY, l = 0.f;  // reference (less kTop) and sum
       {
-        // Lanes 0-3 hold the key scales of the warp's four chunks of columns, lanes 4-7 the value scales, a tile ahead.
-        const float* scales = lane < 4 ? a.k_scale + int64_t(x.b) * a.k_scales.b + int64_t(x.hk) * a.k_scales.h
-                                       : a.v_scale + int64_t(x.b) * a.v_scales.b + int64_t(x.hk) * a.v_scales.h;
-        auto fetch = [&](int c0) -> float {
-          const int key = c0 + (lane & 3) * W;
-          return lane < 8 && key < m_.Nk ? held_scale(__ldg(scales + (key >> a.block_log2))) : 0.f;
-        };
-        float ahead = n > 0 ? fetch(key0 + col0) : 0.f;
         for (int j = 0; j < n; ++j) {
-          const int c0 = key0 + j * BN + col0;  // the warp's first key
+          const int k0 = key0 + j * BN, c0 = k0 + col0;  // the tile's and the warp's first key
           const float sc = ahead;
-          if (j + 1 < n) ahead = fetch(c0 + BN);
+          if (j + 1 < n) ahead = fetch(k0 + BN);
+          auto step = [&]() -> bool {
           const int vb = hi - c0;
           const bool edge = __any_sync(0xffffffffu, valid && vb < H);
           // lanes 4-7: the value scale's exponent and its inverse (0 for an empty block: its values are cleared)
           const float lv_ = sc > 0.f && lane >= 4 ? fminf(fmaxf(__log2f(sc) - lref, -100.f), 100.f) : 0.f;
           const float iv_ = fast_exp2(-lv_);
-          if (!mbar_wait(&bars.sfull[t], (tc + j) & 1, abort)) goto done;
+          if (!mbar_wait(&bars.sfull[t], (tc + j) & 1, abort)) return false;
           if (idle) {
             mbar_arrive(&bars.pfull[t]);
-            continue;
+            return true;
           }
           __syncwarp();
           tc_fence_after();
@@ -311,7 +378,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
           // Both warps of a pair hold the same references, so they agree.
           if (j == 0) {
             bool over = false;
-            if (!row_max(&m, &over)) goto done;
+            if (!row_max(&m, &over)) return false;
           }
           const float mm = m == -INFINITY ? 0.f : m;
           if (edge)
@@ -324,12 +391,12 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
             bool over = !(ts <= kMostSum);
             if (__any_sync(0xffffffffu, valid && over) && lane == 0) flag[xn & 1] = tc + j + 1;
             __syncwarp();
-            if (!pair_sync()) goto done;
+            if (!pair_sync()) return false;
             const bool raise = flag[xn & 1] == static_cast<int>(tc + j + 1);
             ++xn;
             if (raise) {
               float mx;
-              if (!row_max(&mx, &over)) goto done;
+              if (!row_max(&mx, &over)) return false;
               const float mn = over ? fmaxf(m, mx) : m;
               const float alpha = m == mn ? 1.f : fast_exp2(m - mn);
               m = mn;
@@ -352,19 +419,23 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(&bars.pfull[t]);
+          return true;
+          };
+          if (here && !step()) goto done;
+          if (j + 1 < n && !convert(i % kRing, k0 + BN)) goto done;
         }
       }
-      tc += n;
+      if (here) tc += n;
       // the next unit's query terms, ahead of this one's output
       if (!unit_here(i + 1)) goto done;
-      if (bars.ring[(i + 1) % kRing].go && !prepare(bars.ring[(i + 1) % kRing])) goto done;
-      if (n > 0) {
+      if (bars.ring[(i + 1) % kRing].go && !prepare((i + 1) % kRing)) goto done;
+      if (here && n > 0) {
         if (!mbar_wait(&bars.ofull[t], uc & 1, abort)) goto done;
         ++uc;
         __syncwarp();
         tc_fence_after();
       }
-      if (!idle && (t == 0 || x.two)) {
+      if (here && !idle) {
         const int qi = x.q0 + t * m_.qn + rq, hq = x.hk * m_.R + rh;
         // both halves' sums; each half writes its half of the row
         *mine() = make_float2(l, 0.f);
@@ -437,7 +508,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
             v[y] = pack_bf16(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1]));
           put(Constant<int, D / 4>());
         }
-      } else if (n > 0) {
+      } else if (here && n > 0) {
         mbar_arrive(&bars.ofree[t]);
       }
       __syncwarp();
@@ -528,80 +599,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
       while (!mbar_test(&bars.drain[t], 0) && clock64() - t0 < kWaitLimitCycles) {
       }
     }
-  } else if (warp == C::kValueWarp) {
-    // ------------------------------------------------------------ V: codes to fp16
-    uint32_t c = 0;  // key tiles so far
-    constexpr int kLanes = D / 16, kRows = 32 / kLanes;  // lanes a row, rows at a time
-    // d = 128: eight lanes store 16-byte pieces without bank conflicts if they are four of a row and four of the next
-    const int r_lane = D == 128 ? ((lane >> 2) & 1) + 2 * (lane >> 4) : lane / kLanes;
-    const int p_lane = D == 128 ? (lane & 3) + 4 * ((lane >> 3) & 1) : lane % kLanes;
-    for (uint32_t i = 0;; ++i) {
-      if (!unit_here(i)) break;
-      const AUnit x = bars.ring[i % kRing];
-      if (!x.go) break;
-      for (int y = lane; y < D; y += 32) nan_at[i % kRing][y] = 0x7FFFFFFF;
-      if (lane == 0) bars.nans[i % kRing] = 0;
-      __syncwarp();
-      const float* scales = a.v_scale + int64_t(x.b) * a.v_scales.b + int64_t(x.hk) * a.v_scales.h;
-      auto fetch = [&](int k0) -> float {  // lane: 16 keys of a tile
-        const int key = k0 + (lane & 7) * 16;
-        return key < m_.Nk ? held_scale(__ldg(scales + (key >> a.block_log2))) : 0.f;
-      };
-      float ahead = x.n > 0 ? fetch(x.key0) : 0.f;
-      bool ok = true;
-      for (int j = 0; j < x.n; ++j, ++c) {
-        const int k0 = x.key0 + j * BN, live = x.uhi - k0;
-        const uint32_t filled = __ballot_sync(0xffffffffu, ahead > 0.f);  // bit r / 16: row r's block is not empty
-        if (j + 1 < x.n) ahead = fetch(k0 + BN);
-        const uint32_t cs = c % C::kCStages, vs = c % C::kVStages;
-        if (!(ok = mbar_wait(&bars.cfull[cs], (c / C::kCStages) & 1, abort)) ||
-            !(ok = mbar_wait(&bars.vempty[vs], ((c / C::kVStages) & 1) ^ 1, abort)))
-          break;
-        __syncwarp();
-        const uint8_t* from = smem + C::kC + cs * C::kTile + r_lane * D + p_lane * 16;
-        uint8_t* to = smem + C::kV + vs * 2 * C::kTile + (p_lane >> 2) * BN * 128 + r_lane * 128;
-        const int ch = (p_lane & 3) * 2;
-        const bool all = live >= BN && (filled & 255u) == 255u;
-        uint32_t odd = 0;
-#pragma unroll 4
-        for (int f = 0; f < BN / kRows; ++f) {
-          const int r = f * kRows + r_lane;
-          uint4 w = *reinterpret_cast<const uint4*>(from + f * kRows * D);
-          uint32_t e[4] = {w.x, w.y, w.z, w.w};
-          if (!all && (r >= live || !(filled >> (r >> 4) & 1))) e[0] = e[1] = e[2] = e[3] = 0;
-          uint32_t bad = 0;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) bad |= (e[y] & 0x7F7F7F7Fu) + 0x01010101u;
-          if (bad & 0x80808080u) {
-            odd = 1;
-            for (int y = 0; y < 16; ++y)
-              if ((e[y >> 2] >> (8 * (y & 3)) & 127) == 127) {
-                atomicMin(&nan_at[i % kRing][p_lane * 16 + y], k0 + r);
-                e[y >> 2] &= ~(255u << (8 * (y & 3)));
-              }
-          }
-          uint32_t o[8];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            o[2 * y] = decode2(e[y] & 0xFFFFu);
-            o[2 * y + 1] = decode2(e[y] >> 16);
-          }
-          uint8_t* row = to + f * kRows * 128;
-          *reinterpret_cast<uint4*>(row + ((ch ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-        }
-        if (odd) bars.nans[i % kRing] = 1;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bars.vfull[vs]);
-          mbar_arrive(&bars.cempty[cs]);
-        }
-      }
-      if (!ok) break;
-      if (lane == 0) mbar_arrive(&bars.ring_empty[i % kRing]);
-    }
-  } else if (lane == 0) {
+  } else if (warp == C::kTmaWarp && lane == 0) {
     // ------------------------------------------------------------ units and loads
     int64_t g = blockIdx.x;
     uint32_t c = 0, i = 0;
@@ -635,6 +633,8 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
       }
       if (i >= kRing && !mbar_wait(&bars.ring_empty[i % kRing], ((i / kRing) - 1) & 1, abort)) break;
       bars.ring[i % kRing] = x;
+      for (int y = 0; y < D; ++y) nan_at[i % kRing][y] = 0x7FFFFFFF;
+      bars.nans[i % kRing] = 0;
       mbar_arrive(&bars.ring_full[i % kRing]);
       if (g < 0) break;
       for (int j = 0; j < x.n; ++j, ++c) {
