@@ -85,7 +85,8 @@ struct Constant {
 
 }  // namespace
 
-template <int D>
+// NB: scales that a warp's 64 columns have (blocks of 64 and more: 1; 32: 2; 16: 4).
+template <int D, int NB>
 __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
     sa_attend8_many_kernel(const __grid_constant__ Attend8Args a, const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v) {
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
           if (j + 1 < n) ahead = fetch(k0 + BN);
           auto step = [&]() -> bool {
           const int vb = hi - c0;
-          const bool edge = __any_sync(0xffffffffu, valid && vb < H);
+          const bool special = __any_sync(0xffffffffu, (valid && vb < H) || (lane < 4 && sc == 0.f));
           // lanes 4-7: the value scale's exponent and its inverse (0 for an empty block: its values are cleared)
           const float lv_ = sc > 0.f && lane >= 4 ? fminf(fmaxf(__log2f(sc) - lref, -100.f), 100.f) : 0.f;
           const float iv_ = fast_exp2(-lv_);
@@ -339,39 +340,46 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
           // P = 2^(y - mm) as fp16 pairs, its sum `ts` and that without the value scales `tl`, in fp32.
           uint32_t p[H / 2];
           float ts, tl;
-          auto exps = [&](float mm, auto masked) {
+          auto exps = [&](float mm, auto special) {  // special: columns are hidden, or a block of keys is empty
+            constexpr bool kSpecial = decltype(special)::value != 0;
             ts = tl = 0.f;
             float buf[2][W];  // the next columns load while these are worked on
             load(buf[0], 0);
+            float ks = 0.f, iv = 0.f;
+            uint64_t f_2 = 0, g_2 = 0, ps[2] = {0, 0};
 #pragma unroll
             for (int base = 0; base < H; base += W) {
+              if (base % (H / NB) == 0) {
+                ks = __shfl_sync(0xffffffffu, sc, base / W);
+                iv = __shfl_sync(0xffffffffu, iv_, 4 + base / W);
+                const float f = rf * ks, g = __shfl_sync(0xffffffffu, lv_, 4 + base / W) - mm;
+                f_2 = f2(f, f);
+                g_2 = f2(g, g);
+              }
               float* s = buf[(base / W) & 1];
-              const float ks = __shfl_sync(0xffffffffu, sc, base / W), lv = __shfl_sync(0xffffffffu, lv_, 4 + base / W),
-                          iv = __shfl_sync(0xffffffffu, iv_, 4 + base / W);
               tmem_ld_wait();
               if (base + W < H) load(buf[(base / W + 1) & 1], base + W);
-              if (ks == 0.f) {  // (an empty block's keys are zeros, whatever their codes)
-#pragma unroll
-                for (int c = 0; c < W; ++c) s[c] = 0.f;
-              }
-              const float f = rf * ks, g = lv - mm;
-              const uint64_t f_2 = f2(f, f), g_2 = f2(g, g);
-              uint64_t ps = 0;
 #pragma unroll
               for (int c = 0; c < W / 2; ++c) {
+                // (an empty block's keys are zeros, whatever their codes)
+                if (kSpecial) s[2 * c] = ks == 0.f ? 0.f : s[2 * c], s[2 * c + 1] = ks == 0.f ? 0.f : s[2 * c + 1];
                 const uint64_t y = fma2(f2(s[2 * c], s[2 * c + 1]), f_2, g_2);
                 float y0 = f2lo(y), y1 = f2hi(y);
-                if (decltype(masked)::value) {
+                if (kSpecial) {
                   y0 = base + 2 * c < vb ? y0 : -INFINITY;
                   y1 = base + 2 * c + 1 < vb ? y1 : -INFINITY;
                 }
                 const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
                 p[base / 2 + c] = pack_half2(p0, p1);
-                ps = add2(ps, f2(p0, p1));
+                ps[c & 1] = add2(ps[c & 1], f2(p0, p1));
               }
-              const float sum = f2lo(ps) + f2hi(ps);
-              ts += sum;
-              tl = fmaf(sum, iv, tl);
+              if ((base + W) % (H / NB) == 0) {
+                const uint64_t two = add2(ps[0], ps[1]);
+                const float sum = f2lo(two) + f2hi(two);
+                ts += sum;
+                tl = fmaf(sum, iv, tl);
+                ps[0] = ps[1] = 0;
+              }
             }
           };
           // The run's first tile sets the reference: a row that sees nothing of it sees nothing of the run.
@@ -381,7 +389,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
             if (!row_max(&m, &over)) return false;
           }
           const float mm = m == -INFINITY ? 0.f : m;
-          if (edge)
+          if (special)
             exps(mm, Constant<int, 1>());
           else
             exps(mm, Constant<int, 0>());
@@ -690,10 +698,10 @@ void attend8_many_plan(Attend8Args* a) {
   a->m.unit_rows = 128 * a->m.tiles;
 }
 
-template <int D>
+template <int D, int NB>
 static cudaError_t launch_a(const Attend8Args& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
   using C = ACfg<D>;
-  auto kern = sa_attend8_many_kernel<D>;
+  auto kern = sa_attend8_many_kernel<D, NB>;
   // at least half the SM's shared memory: one block per SM owns its TMEM
   const int smem = C::kSmemBytes > 120 * 1024 ? C::kSmemBytes : 120 * 1024;
   static std::atomic<int> regs_ok{0};  // 0 unknown, 1 enough, 2 too few
@@ -719,7 +727,13 @@ cudaError_t launch_attend8_many(const Attend8Args& a, cudaStream_t st) {
   if (!make_codes_map(&tk, a.k8, a.m.d, a.m.Nk, a.m.Hkv, a.m.B, a.m.ks, BN, true) ||
       !make_codes_map(&tv, a.v8, a.m.d, a.m.Nk, a.m.Hkv, a.m.B, a.m.vs, BN, false))
     return cudaErrorInvalidValue;
-  return a.m.d == 128 ? launch_a<128>(a, tk, tv, st) : launch_a<64>(a, tk, tv, st);
+  if (a.m.d == 128)
+    return a.block_log2 >= 6   ? launch_a<128, 1>(a, tk, tv, st)
+           : a.block_log2 == 5 ? launch_a<128, 2>(a, tk, tv, st)
+                               : launch_a<128, 4>(a, tk, tv, st);
+  return a.block_log2 >= 6   ? launch_a<64, 1>(a, tk, tv, st)
+         : a.block_log2 == 5 ? launch_a<64, 2>(a, tk, tv, st)
+                             : launch_a<64, 4>(a, tk, tv, st);
 }
 
 }  // namespace sa
