@@ -66,7 +66,6 @@ struct ABars {
   uint64_t qfull[2], sfull[2], pfull[2], ofull[2], ofree[2], turn[2], drain[2], next, ring_full[kRing], ring_empty[kRing];
   uint4 answer;
   AUnit ring[kRing];
-  int flag[8][2];
   int nans[kRing];  // a unit's values hold a NaN
   uint32_t tmem_base;
   int abort;
@@ -75,6 +74,18 @@ struct ABars {
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// How many of `count` threads say so, on hardware barrier `id`.
+__device__ __forceinline__ uint32_t count_of(int id, int count, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.popc.u32 %0, %1, %2, p;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(x))
+      : "memory");
   return r;
 }
 
@@ -116,11 +127,11 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
       mbar_init(&bars.vempty[s], 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.qfull[i], 256);
+      mbar_init(&bars.qfull[i], 8);
       mbar_init(&bars.sfull[i], 1);
-      mbar_init(&bars.pfull[i], 256);
+      mbar_init(&bars.pfull[i], 8);
       mbar_init(&bars.ofull[i], 1);
-      mbar_init(&bars.ofree[i], 256);
+      mbar_init(&bars.ofree[i], 8);
       mbar_init(&bars.turn[i], 1);
       mbar_init(&bars.drain[i], 1);
     }
@@ -128,7 +139,6 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
       mbar_init(&bars.ring_full[i], 1);
       mbar_init(&bars.ring_empty[i], C::kSoftWarps + 2);
     }
-    for (int i = 0; i < 8; ++i) bars.flag[i][0] = bars.flag[i][1] = 0;
     mbar_init(&bars.next, 1);
     bars.abort = 0;
     fence_mbar_init();
@@ -158,7 +168,6 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
     const uint32_t obase = tmem + lane_base + C::kOCol + t * D + half * (D / 2);
     const int rq = trow / m_.R, rh = trow - rq * m_.R;  // its query and head in the tile
     const bool in_tile = trow < m_.qn * m_.R;
-    volatile int* flag = bars.flag[t * 4 + quarter];
     uint32_t xn = 0;          // pair exchanges so far
     uint32_t tc = 0, uc = 0;  // key tiles and units with keys of this Q tile so far
     uint8_t* own = smem + C::kX + warp * C::kWarpBytes;
@@ -166,12 +175,20 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
     auto other = [&]() -> float2* {
       return reinterpret_cast<float2*>(smem + C::kX + (warp ^ 4) * C::kWarpBytes) + (xn & 1) * 32 + lane;
     };
-    // Meets the other half's warp.  A warp that gives up sets *abort and arrives once (below `done`), and
-    // whoever it releases gives up too.
-    auto pair_sync = [&]() -> bool {
-      named_barrier(1 + t * 4 + quarter, 64);
-      return *abort == 0;
+    // A warp's arrival (a barrier counts its warps: 256 threads' arrivals one by one took as long as the store of P).
+    auto arrive = [&](uint64_t* bar) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
     };
+    // Meets the other half's warp: how many of the two ask for something (one of their lanes counts).  At its end a
+    // warp meets it once more, and all its lanes count: whoever it meets elsewhere gives up too.
+    bool alone = false;  // the other warp has given up, and waits no more
+    auto meet = [&](bool ask) -> uint32_t {
+      const uint32_t n = count_of(1 + t * 4 + quarter, 64, ask && lane == 0);
+      alone = n >= 32;
+      return n;
+    };
+    auto pair_sync = [&]() -> bool { return meet(false) < 32; };
     // Scales that the warp needs of a tile, fetched a tile ahead: lanes 0-3 the key scales of its four chunks of columns,
     // lanes 4-7 the value scales, lane 8 that of the eight keys whose values it converts.
     const float* scales = nullptr;
@@ -184,9 +201,11 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
     uint32_t vc = 0;  // tiles converted so far
     auto convert = [&](uint32_t slot, int k0) -> bool {
       constexpr int kLanes = D / 16, kRows = 32 / kLanes;  // lanes a row, rows at a time
-      // d = 128: eight lanes store 16-byte pieces without bank conflicts if they are four of a row and four of the next
-      const int r_lane = D == 128 ? ((lane >> 2) & 1) + 2 * (lane >> 4) : lane / kLanes;
-      const int p_lane = D == 128 ? (lane & 3) + 4 * ((lane >> 3) & 1) : lane % kLanes;
+      // d = 128: eight lanes load and store 16-byte pieces without bank conflicts if they are four of row r and four of
+      // row r ^ 5, the codes as the 128-byte swizzle has them
+      const int r_lane = D == 128 ? lane >> 3 ^ ((lane & 4) ? 5 : 0) : lane / kLanes, p_lane = lane & 3;
+      auto row_of = [&](int y) -> int { return warp * 8 + r_lane + (D == 128 ? 0 : y * kRows); };
+      auto piece_of = [&](int y) -> int { return D == 128 ? p_lane + 4 * y : p_lane; };
       const uint32_t cs = vc % C::kCStages, vs = vc % C::kVStages;
       const bool filled = __shfl_sync(0xffffffffu, ahead, 8) > 0.f;
       const int live = filled ? bars.ring[slot].uhi - k0 : 0;
@@ -198,8 +217,9 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
       uint32_t bad = 0;
 #pragma unroll
       for (int y = 0; y < 8 / kRows; ++y) {
-        const int r = warp * 8 + y * kRows + r_lane;
-        w[y] = *reinterpret_cast<const uint4*>(smem + C::kC + cs * C::kTile + r * D + p_lane * 16);
+        const int r = row_of(y);
+        w[y] = *reinterpret_cast<const uint4*>(smem + C::kC + cs * C::kTile +
+                                               (D == 128 ? rows8_offset<D>(r, piece_of(y) * 16) : r * D + p_lane * 16));
         if (r >= live) w[y] = make_uint4(0, 0, 0, 0);
         bad |= ((w[y].x & 0x7F7F7F7Fu) + 0x01010101u) | ((w[y].y & 0x7F7F7F7Fu) + 0x01010101u) |
                ((w[y].z & 0x7F7F7F7Fu) + 0x01010101u) | ((w[y].w & 0x7F7F7F7Fu) + 0x01010101u);
@@ -211,7 +231,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
           auto sift = [&](uint32_t e, int p) -> uint32_t {
             for (int b = 0; b < 4; ++b)
               if ((e >> (8 * b) & 127) == 127) {
-                atomicMin(&nan_at[slot][p_lane * 16 + p + b], k0 + warp * 8 + y * kRows + r_lane);
+                atomicMin(&nan_at[slot][piece_of(y) * 16 + p + b], k0 + row_of(y));
                 e &= ~(255u << (8 * b));
               }
             return e;
@@ -221,8 +241,8 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
       }
 #pragma unroll
       for (int y = 0; y < 8 / kRows; ++y) {
-        const int r = warp * 8 + y * kRows + r_lane, ch = (p_lane & 3) * 2;
-        uint8_t* row = smem + C::kV + vs * 2 * C::kTile + (p_lane >> 2) * BN * 128 + r * 128;
+        const int r = row_of(y), ch = p_lane * 2;
+        uint8_t* row = smem + C::kV + vs * 2 * C::kTile + (piece_of(y) >> 2) * BN * 128 + r * 128;
         *reinterpret_cast<uint4*>(row + ((ch ^ (r & 7)) << 4)) =
             make_uint4(decode2(w[y].x & 0xFFFFu), decode2(w[y].x >> 16), decode2(w[y].y & 0xFFFFu), decode2(w[y].y >> 16));
         *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (r & 7)) << 4)) =
@@ -277,15 +297,15 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
           *reinterpret_cast<uint4*>(sq + C::kTile + at) = make_uint4(l0.x, l0.y, l1.x, l1.y);
         }
         fence_proxy_async_smem();
-        mbar_arrive(&bars.qfull[t]);
+        arrive(&bars.qfull[t]);
         const float s0 = held_scale(__ldg(a.v_scale + int64_t(x.b) * a.v_scales.b + int64_t(x.hk) * a.v_scales.h +
                                           (x.key0 >> a.block_log2)));
         lref_next = s0 > 0.f ? __log2f(s0) : 0.f;
       }
       return convert(slot, x.key0);
     };
-    if (!unit_here(0)) goto done;
-    if (bars.ring[0].go && !prepare(0)) goto done;
+    if (!unit_here(0)) goto end;
+    if (bars.ring[0].go && !prepare(0)) goto end;
     for (uint32_t i = 0;; ++i) {
       const AUnit& x = bars.ring[i % kRing];
       if (!x.go) break;
@@ -309,7 +329,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
           const float iv_ = fast_exp2(-lv_);
           if (!mbar_wait(&bars.sfull[t], (tc + j) & 1, abort)) return false;
           if (idle) {
-            mbar_arrive(&bars.pfull[t]);
+            arrive(&bars.pfull[t]);
             return true;
           }
           __syncwarp();
@@ -397,11 +417,9 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
           // do not go by its neighbours).
           if (j > 0) {
             bool over = !(ts <= kMostSum);
-            if (__any_sync(0xffffffffu, valid && over) && lane == 0) flag[xn & 1] = tc + j + 1;
-            __syncwarp();
-            if (!pair_sync()) return false;
-            const bool raise = flag[xn & 1] == static_cast<int>(tc + j + 1);
-            ++xn;
+            const uint32_t asked = meet(__any_sync(0xffffffffu, valid && over));
+            if (asked >= 32) return false;
+            const bool raise = asked != 0;
             if (raise) {
               float mx;
               if (!row_max(&mx, &over)) return false;
@@ -426,19 +444,19 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
           tmem_st32(sbase, p);
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(&bars.pfull[t]);
+          arrive(&bars.pfull[t]);
           return true;
           };
-          if (here && !step()) goto done;
-          if (j + 1 < n && !convert(i % kRing, k0 + BN)) goto done;
+          if (here && !step()) goto end;
+          if (j + 1 < n && !convert(i % kRing, k0 + BN)) goto end;
         }
       }
       if (here) tc += n;
       // the next unit's query terms, ahead of this one's output
-      if (!unit_here(i + 1)) goto done;
-      if (bars.ring[(i + 1) % kRing].go && !prepare((i + 1) % kRing)) goto done;
+      if (!unit_here(i + 1)) goto end;
+      if (bars.ring[(i + 1) % kRing].go && !prepare((i + 1) % kRing)) goto end;
       if (here && n > 0) {
-        if (!mbar_wait(&bars.ofull[t], uc & 1, abort)) goto done;
+        if (!mbar_wait(&bars.ofull[t], uc & 1, abort)) goto end;
         ++uc;
         __syncwarp();
         tc_fence_after();
@@ -447,7 +465,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
         const int qi = x.q0 + t * m_.qn + rq, hq = x.hk * m_.R + rh;
         // both halves' sums; each half writes its half of the row
         *mine() = make_float2(l, 0.f);
-        if (!pair_sync()) goto done;
+        if (!pair_sync()) goto end;
         l += other()->x;
         ++xn;
         const float inv = l == 0.f ? 0.f : fast_exp2(lref) / l;
@@ -471,7 +489,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
           for (int c = 0; c < D / 64; ++c) tmem_ld32(obase + c * 32, v + c * 32);
           tmem_ld_wait();
           tc_fence_before();
-          mbar_arrive(&bars.ofree[t]);
+          arrive(&bars.ofree[t]);
 #pragma unroll
           for (int y = 0; y < D / 2; ++y) v[y] = inv == 0.f ? 0 : __float_as_uint(__uint_as_float(v[y]) * inv);
           if (*static_cast<volatile int*>(&bars.nans[i % kRing])) {
@@ -483,7 +501,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
 #pragma unroll
           for (int y = 0; y < D / 2; ++y) v[y] = 0;
         }
-        if (!pair_sync()) goto done;  // (the other half has read this warp's slot)
+        if (!pair_sync()) goto end;  // (the other half has read this warp's slot)
         auto put = [&](auto words) {  // words per half row
           constexpr int PC = decltype(words)::value / 4;  // 16-byte pieces of it
           constexpr int kRows = C::kWarpBytes / 16 / PC;  // rows at a time
@@ -517,11 +535,13 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
           put(Constant<int, D / 4>());
         }
       } else if (here && n > 0) {
-        mbar_arrive(&bars.ofree[t]);
+        arrive(&bars.ofree[t]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.ring_empty[i % kRing]);
+      arrive(&bars.ring_empty[i % kRing]);
     }
+  end:
+    // (Also without a fault: one of the two may end as usual where the other gives up.)
+    if (!alone) count_of(1 + t * 4 + quarter, 64, true);
   } else if (warp < C::kTmaWarp) {
     // ------------------------------------------------------------ MMA issue, a warp for each Q tile
     const int t = warp - C::kMmaWarp;
@@ -679,8 +699,6 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
       if (g >= 0) settle(&bars.next, i & 1);
     }
   }
-done:
-  if (warp < C::kSoftWarps && *abort) named_barrier_arrive(1 + (warp >> 3) * 4 + (warp & 3), 64);
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && bars.abort) report(m_.status, SA_DEVERR_TIMEOUT);
@@ -725,7 +743,7 @@ static cudaError_t launch_a(const Attend8Args& a, const CUtensorMap& tk, const C
 cudaError_t launch_attend8_many(const Attend8Args& a, cudaStream_t st) {
   CUtensorMap tk, tv;
   if (!make_codes_map(&tk, a.k8, a.m.d, a.m.Nk, a.m.Hkv, a.m.B, a.m.ks, BN, true) ||
-      !make_codes_map(&tv, a.v8, a.m.d, a.m.Nk, a.m.Hkv, a.m.B, a.m.vs, BN, false))
+      !make_codes_map(&tv, a.v8, a.m.d, a.m.Nk, a.m.Hkv, a.m.B, a.m.vs, BN, a.m.d == 128))
     return cudaErrorInvalidValue;
   if (a.m.d == 128)
     return a.block_log2 >= 6   ? launch_a<128, 1>(a, tk, tv, st)
