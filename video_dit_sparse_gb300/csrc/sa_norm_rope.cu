@@ -15,6 +15,7 @@
 // given, a block adds its threads, and a second kernel the blocks, all in a fixed order: the same inputs give the
 // same bits.
 #include <cmath>
+#include <type_traits>
 
 #include "sa_rope.cuh"
 #include "sa_views.h"
@@ -38,21 +39,84 @@ struct NormRopeArgs {
 
 namespace {
 
+// Two fp32 values in each of `P` = V / 2 packed pairs: a lane's piece of V values.
+
 // The lane's 2 V values of a [d] vector (`none` where it is null).
 template <int V>
-__device__ __forceinline__ void load_vector(const void* p, bool wide, int e0, int e1, float none, float* f0, float* f1) {
+__device__ __forceinline__ void load_vector(const void* p, bool wide, int e0, int e1, float none, uint64_t* v0, uint64_t* v1) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    f0[i] = f1[i] = none;
-    if (p && wide) {
-      f0[i] = __ldg(static_cast<const float*>(p) + e0 + i);
-      f1[i] = __ldg(static_cast<const float*>(p) + e1 + i);
-    } else if (p) {
-      f0[i] = __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(p) + e0 + i)) << 16);
-      f1[i] = __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(p) + e1 + i)) << 16);
+  for (int i = 0; i < V; i += 2) {
+    float f[4] = {none, none, none, none};
+    const int at[4] = {e0 + i, e0 + i + 1, e1 + i, e1 + i + 1};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (p && wide) f[e] = __ldg(static_cast<const float*>(p) + at[e]);
+      if (p && !wide) f[e] = __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(p) + at[e])) << 16);
     }
+    v0[i / 2] = f2(f[0], f[1]);
+    v1[i / 2] = f2(f[2], f[3]);
   }
 }
+
+template <int V>
+__device__ __forceinline__ void unpack2(const uint4& u, uint64_t* v) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  if (V == 8) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) v[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  } else {
+    v[0] = f2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    v[1] = f2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+  }
+}
+template <int V>
+__device__ __forceinline__ uint4 pack2(const uint64_t* v) {
+  if (V == 8)
+    return make_uint4(pack_bf16(f2lo(v[0]), f2hi(v[0])), pack_bf16(f2lo(v[1]), f2hi(v[1])),
+                      pack_bf16(f2lo(v[V / 2 - 2]), f2hi(v[V / 2 - 2])), pack_bf16(f2lo(v[V / 2 - 1]), f2hi(v[V / 2 - 1])));
+  return make_uint4(f2lo_bits(v[0]), f2hi_bits(v[0]), f2lo_bits(v[1]), f2hi_bits(v[1]));
+}
+
+// Cosines and sines as `turn2` wants them: HALF: of the pairs (i, i + 1); else pair by pair, in both halves.
+template <int V, bool HALF>
+struct Angles {
+  uint64_t cs[V / 2], sn[V / 2];
+  __device__ __forceinline__ void load(const RopeArgs& a, int b, int64_t n, int e0, int e1, bool turns) {
+    int p[3] = {0, 0, 0};
+    token_position(a, b, n, p);
+    float c[V], s[V];
+    lane_angles<V, HALF>(a, p, e0, e1, turns, c, s);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      cs[i] = f2(c[2 * i], c[2 * i + 1]);
+      sn[i] = f2(s[2 * i], s[2 * i + 1]);
+    }
+  }
+  // Turns the two pieces; `part`: not all of a row turns (what does not is kept as it is).
+  __device__ __forceinline__ void turn(const RopeArgs& a, int e0, int e1, bool turns, bool part, uint64_t* x0, uint64_t* x1) const {
+    if (HALF) {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        const uint64_t y0 = sub2(mul2(x0[i], cs[i]), mul2(x1[i], sn[i])), y1 = fma2(x0[i], sn[i], mul2(x1[i], cs[i]));
+        x0[i] = turns ? y0 : x0[i];
+        x1[i] = turns ? y1 : x1[i];
+      }
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint64_t* x = k ? x1 : x0;
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {  // pair number i of the piece: angle i (k = 0) or V / 2 + i
+        const int at = k * (V / 2) + i;
+        const float c = at & 1 ? f2hi(cs[at / 2]) : f2lo(cs[at / 2]), s = at & 1 ? f2hi(sn[at / 2]) : f2lo(sn[at / 2]);
+        const float u = f2lo(x[i]), v = f2hi(x[i]);
+        const uint64_t y = f2(u * c - v * s, u * s + v * c);
+        x[i] = part && (k ? e1 : e0) + 2 * i >= a.rot ? x[i] : y;
+      }
+    }
+  }
+};
 
 // Sum over the LANES lanes of a row (every lane of the warp takes part).
 template <int LANES>
@@ -61,26 +125,28 @@ __device__ __forceinline__ float row_sum(float x) {
   for (int o = LANES / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
+__device__ __forceinline__ float both(uint64_t v) { return f2lo(v) + f2hi(v); }
 
 // Takes the mean off (LAYER) and returns r.
 template <int V, int LANES, bool LAYER>
-__device__ __forceinline__ float normalise(float* f0, float* f1, float eps) {
+__device__ __forceinline__ float normalise(uint64_t* v0, uint64_t* v1, float eps) {
   constexpr float kInv = 1.f / (2 * V * LANES);
   if (LAYER) {
-    float s = 0.f;
+    uint64_t s = add2(v0[0], v1[0]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) s += f0[i] + f1[i];
-    const float mu = row_sum<LANES>(s) * kInv;
+    for (int i = 1; i < V / 2; ++i) s = add2(s, add2(v0[i], v1[i]));
+    const float mu = row_sum<LANES>(both(s)) * kInv;
+    const uint64_t m = f2(mu, mu);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      f0[i] -= mu;
-      f1[i] -= mu;
+    for (int i = 0; i < V / 2; ++i) {
+      v0[i] = sub2(v0[i], m);
+      v1[i] = sub2(v1[i], m);
     }
   }
-  float q = 0.f;
+  uint64_t q = 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) q = fmaf(f0[i], f0[i], fmaf(f1[i], f1[i], q));
-  return rsqrtf(fmaf(row_sum<LANES>(q), kInv, eps));
+  for (int i = 0; i < V / 2; ++i) q = fma2(v0[i], v0[i], fma2(v1[i], v1[i], q));
+  return rsqrtf(fmaf(row_sum<LANES>(both(q)), kInv, eps));
 }
 
 }  // namespace
@@ -97,18 +163,16 @@ __global__ void __launch_bounds__(256, 2) sa_norm_rope_kernel(const __grid_const
   const int64_t n = valid ? tok : r.N - 1;  // (every lane takes part in the sums)
   const int b = blockIdx.z;
   const int first = blockIdx.y * heads_per_block, last = min(first + heads_per_block, r.H[0] + r.H[1]);
-  int p[3] = {0, 0, 0};
-  token_position(r, b, n, p);
   int e0, e1;
-  const bool turns = lane_pieces<V, HALF>(r, c, &e0, &e1);
-  float cs[V], sn[V];
-  lane_angles<V, HALF>(r, p, e0, e1, turns, cs, sn);
+  const bool turns = lane_pieces<V, HALF>(r, c, &e0, &e1), part = r.rot < 2 * V * LANES;
+  Angles<V, HALF> angles;
+  angles.load(r, b, n, e0, e1, turns);
   constexpr int U = 4;  // heads in flight
 #pragma unroll 1
   for (int s = 0; s < 2; ++s) {
     const int h0 = s ? max(first - r.H[0], 0) : first, h1 = s ? last - r.H[0] : min(last, r.H[0]);
     if (h0 >= h1) continue;
-    float w0[V], w1[V], b0[V], b1[V];
+    uint64_t w0[V / 2], w1[V / 2], b0[V / 2], b1[V / 2];
     load_vector<V>(a.w[s], a.wide, e0, e1, 1.f, w0, w1);
     load_vector<V>(a.b[s], a.wide, e0, e1, 0.f, b0, b1);
     const char* x = static_cast<const char*>(r.x[s]) + (b * r.xs[s].b + n * r.xs[s].n) * kBytes;
@@ -125,29 +189,30 @@ __global__ void __launch_bounds__(256, 2) sa_norm_rope_kernel(const __grid_const
 #pragma unroll
       for (int i = 0; i < U; ++i)
         if (h + i < h1) {
-          float f0[V], f1[V];
-          unpack<V>(u0[i], f0);
-          unpack<V>(u1[i], f1);
-          const float k = normalise<V, LANES, LAYER>(f0, f1, a.eps);
+          uint64_t v0[V / 2], v1[V / 2];
+          unpack2<V>(u0[i], v0);
+          unpack2<V>(u1[i], v1);
+          const float k = normalise<V, LANES, LAYER>(v0, v1, a.eps);
+          const uint64_t kk = f2(k, k);
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            f0[e] = fmaf(f0[e] * k, w0[e], b0[e]);
-            f1[e] = fmaf(f1[e] * k, w1[e], b1[e]);
+          for (int e = 0; e < V / 2; ++e) {
+            v0[e] = fma2(mul2(v0[e], kk), w0[e], b0[e]);
+            v1[e] = fma2(mul2(v1[e], kk), w1[e], b1[e]);
           }
-          turn_pieces<V, HALF>(r, e0, e1, turns, cs, sn, f0, f1);
+          angles.turn(r, e0, e1, turns, part, v0, v1);
           char* at = y + (h + i) * r.ys[s].h * kBytes;
           if (valid) {
-            *reinterpret_cast<uint4*>(at + e0 * kBytes) = pack<V>(f0);
-            *reinterpret_cast<uint4*>(at + e1 * kBytes) = pack<V>(f1);
+            *reinterpret_cast<uint4*>(at + e0 * kBytes) = pack2<V>(v0);
+            *reinterpret_cast<uint4*>(at + e1 * kBytes) = pack2<V>(v1);
           }
         }
     }
   }
 }
 
-// The gradient.  blockIdx.y: side.  A block takes every gridDim.x-th piece of work: 256 / LANES tokens of a batch
-// entry, `run` heads of them.
-template <int V, int LANES, bool HALF, bool LAYER>
+// The gradient.  blockIdx.y: side.  A block takes every blocks[side]-th piece of work: 256 / LANES tokens of a batch
+// entry, `run` heads of them.  BIAS: db is wanted.
+template <int V, int LANES, bool HALF, bool LAYER, bool BIAS>
 __global__ void __launch_bounds__(256, 2) sa_norm_rope_grad_kernel(const __grid_constant__ NormRopeArgs a) {
   constexpr int kTokens = 256 / LANES;
   constexpr int kBytes = V == 8 ? 2 : 4;
@@ -159,12 +224,11 @@ __global__ void __launch_bounds__(256, 2) sa_norm_rope_grad_kernel(const __grid_
   if (static_cast<int>(blockIdx.x) >= a.blocks[s]) return;
   const int c = threadIdx.x % LANES, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int e0, e1;
-  const bool turns = lane_pieces<V, HALF>(r, c, &e0, &e1);
-  float w0[V], w1[V], dw0[V], dw1[V], db0[V], db1[V];
+  const bool turns = lane_pieces<V, HALF>(r, c, &e0, &e1), part_turns = r.rot < kRow;
+  uint64_t w0[V / 2], w1[V / 2], dw0[V / 2], dw1[V / 2], db0[V / 2], db1[V / 2];
   load_vector<V>(a.w[s], a.wide, e0, e1, 1.f, w0, w1);
 #pragma unroll
-  for (int i = 0; i < V; ++i) dw0[i] = dw1[i] = db0[i] = db1[i] = 0.f;
-  const bool sum_w = a.dw[s] != nullptr, sum_b = a.db[s] != nullptr;
+  for (int i = 0; i < V / 2; ++i) dw0[i] = dw1[i] = db0[i] = db1[i] = 0;
   const uint32_t tiles = (static_cast<uint32_t>(r.N) + kTokens - 1) / kTokens, runs = (r.H[s] + a.run[s] - 1) / a.run[s];
   const int64_t items = int64_t(tiles) * r.B * runs;
   for (int64_t item = blockIdx.x; item < items; item += a.blocks[s]) {
@@ -174,68 +238,66 @@ __global__ void __launch_bounds__(256, 2) sa_norm_rope_grad_kernel(const __grid_
     const int64_t tok = (bt - int64_t(b) * tiles) * kTokens + threadIdx.x / LANES;
     const bool valid = tok < r.N;
     const int64_t n = valid ? tok : r.N - 1;
-    int p[3] = {0, 0, 0};
-    token_position(r, b, n, p);
-    float cs[V], sn[V];
-    lane_angles<V, HALF>(r, p, e0, e1, turns, cs, sn);  // (r.inverse is set: R^-1)
     const char* x = static_cast<const char*>(r.x[s]) + (b * r.xs[s].b + n * r.xs[s].n) * kBytes;
     const char* dy = static_cast<const char*>(a.g[s]) + (b * a.gs[s].b + n * a.gs[s].n) * kBytes;
     char* dx = static_cast<char*>(r.y[s]) + (b * r.ys[s].b + n * r.ys[s].n) * kBytes;
-    constexpr int U = 2;  // heads in flight
-    for (int h = h0; h < h1; h += U) {
-      uint4 ux0[U], ux1[U], ug0[U], ug1[U];
+    uint4 ux0, ux1, ug0, ug1;  // the next head's
+    auto load = [&](int h) {
+      const char* at = x + h * r.xs[s].h * kBytes;
+      ux0 = *reinterpret_cast<const uint4*>(at + e0 * kBytes);
+      ux1 = *reinterpret_cast<const uint4*>(at + e1 * kBytes);
+      at = dy + h * a.gs[s].h * kBytes;
+      ug0 = *reinterpret_cast<const uint4*>(at + e0 * kBytes);
+      ug1 = *reinterpret_cast<const uint4*>(at + e1 * kBytes);
+    };
+    load(h0);
+    Angles<V, HALF> angles;
+    angles.load(r, b, n, e0, e1, turns);  // (r.inverse is set: R^-1)
+    for (int h = h0; h < h1; ++h) {
+      uint64_t v0[V / 2], v1[V / 2], g0[V / 2], g1[V / 2];
+      unpack2<V>(ux0, v0);
+      unpack2<V>(ux1, v1);
+      unpack2<V>(ug0, g0);
+      unpack2<V>(ug1, g1);
+      if (h + 1 < h1) load(h + 1);
+      const float k = normalise<V, LANES, LAYER>(v0, v1, a.eps);
+      const uint64_t kk = f2(k, k);
+      angles.turn(r, e0, e1, turns, part_turns, g0, g1);
+      uint64_t hn = 0, hs = 0;
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (h + i < h1) {
-          const char* at = x + (h + i) * r.xs[s].h * kBytes;
-          ux0[i] = *reinterpret_cast<const uint4*>(at + e0 * kBytes);
-          ux1[i] = *reinterpret_cast<const uint4*>(at + e1 * kBytes);
-          at = dy + (h + i) * a.gs[s].h * kBytes;
-          ug0[i] = *reinterpret_cast<const uint4*>(at + e0 * kBytes);
-          ug1[i] = *reinterpret_cast<const uint4*>(at + e1 * kBytes);
-        }
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (h + i < h1) {
-          float f0[V], f1[V], g0[V], g1[V];
-          unpack<V>(ux0[i], f0);
-          unpack<V>(ux1[i], f1);
-          const float k = normalise<V, LANES, LAYER>(f0, f1, a.eps);
-          unpack<V>(ug0[i], g0);
-          unpack<V>(ug1[i], g1);
-          turn_pieces<V, HALF>(r, e0, e1, turns, cs, sn, g0, g1);
-          float hn = 0.f, hs = 0.f;
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            f0[e] *= k;
-            f1[e] *= k;
-            if (valid) {  // (a row that is there twice counts once)
-              dw0[e] = fmaf(g0[e], f0[e], dw0[e]);
-              dw1[e] = fmaf(g1[e], f1[e], dw1[e]);
-              db0[e] += g0[e];
-              db1[e] += g1[e];
-            }
-            g0[e] *= w0[e];
-            g1[e] *= w1[e];
-            hn = fmaf(g0[e], f0[e], fmaf(g1[e], f1[e], hn));
-            if (LAYER) hs += g0[e] + g1[e];
-          }
-          hn = row_sum<LANES>(hn) * kInv;
-          if (LAYER) hs = row_sum<LANES>(hs) * kInv;
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            f0[e] = k * (fmaf(-hn, f0[e], g0[e]) - hs);
-            f1[e] = k * (fmaf(-hn, f1[e], g1[e]) - hs);
-          }
-          char* at = dx + (h + i) * r.ys[s].h * kBytes;
-          if (valid) {
-            *reinterpret_cast<uint4*>(at + e0 * kBytes) = pack<V>(f0);
-            *reinterpret_cast<uint4*>(at + e1 * kBytes) = pack<V>(f1);
+      for (int e = 0; e < V / 2; ++e) {
+        v0[e] = mul2(v0[e], kk);
+        v1[e] = mul2(v1[e], kk);
+        if (valid) {  // (a row that is there twice counts once)
+          dw0[e] = fma2(g0[e], v0[e], dw0[e]);
+          dw1[e] = fma2(g1[e], v1[e], dw1[e]);
+          if (BIAS) {
+            db0[e] = add2(g0[e], db0[e]);
+            db1[e] = add2(g1[e], db1[e]);
           }
         }
+        g0[e] = mul2(g0[e], w0[e]);
+        g1[e] = mul2(g1[e], w1[e]);
+        hn = fma2(g0[e], v0[e], fma2(g1[e], v1[e], hn));
+        if (LAYER) hs = add2(hs, add2(g0[e], g1[e]));
+      }
+      const float mn = -row_sum<LANES>(both(hn)) * kInv, ms = LAYER ? row_sum<LANES>(both(hs)) * kInv : 0.f;
+      const uint64_t mn2 = f2(mn, mn), ms2 = f2(ms, ms);
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {
+        uint64_t y0 = fma2(mn2, v0[e], g0[e]), y1 = fma2(mn2, v1[e], g1[e]);
+        if (LAYER) y0 = sub2(y0, ms2), y1 = sub2(y1, ms2);
+        v0[e] = mul2(kk, y0);
+        v1[e] = mul2(kk, y1);
+      }
+      char* at = dx + h * r.ys[s].h * kBytes;
+      if (valid) {
+        *reinterpret_cast<uint4*>(at + e0 * kBytes) = pack2<V>(v0);
+        *reinterpret_cast<uint4*>(at + e1 * kBytes) = pack2<V>(v1);
+      }
     }
   }
-  if (!sum_w && !sum_b) return;
+  if (!a.dw[s] && !a.db[s]) return;
   let_next_kernel_start();
   // the warp's rows, then the block's warps
   auto fold = [&](float v) -> float {
@@ -245,7 +307,8 @@ __global__ void __launch_bounds__(256, 2) sa_norm_rope_grad_kernel(const __grid_
   };
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const float v[4] = {fold(dw0[i]), fold(dw1[i]), fold(db0[i]), fold(db1[i])};
+    auto value = [&](const uint64_t* v) -> float { return fold(i & 1 ? f2hi(v[i / 2]) : f2lo(v[i / 2])); };
+    const float v[4] = {value(dw0), value(dw1), BIAS ? value(db0) : 0.f, BIAS ? value(db1) : 0.f};
     if (lane < LANES) {
       sums[warp][0][e0 + i] = v[0];
       sums[warp][0][e1 + i] = v[1];
@@ -326,10 +389,16 @@ template <int V, int LANES>
 cudaError_t launch_g(const NormRopeArgs& a, bool layer, cudaStream_t st) {
   constexpr int D = 2 * V * LANES;
   const dim3 grid(std::max(a.blocks[0], a.blocks[1]), a.r.H[1] ? 2 : 1);
+  const bool bias = a.db[0] || a.db[1];
+  auto go = [&](auto half, auto lay) {
+    constexpr bool kHalf = decltype(half)::value, kLayer = decltype(lay)::value;
+    (bias ? sa_norm_rope_grad_kernel<V, LANES, kHalf, kLayer, true> : sa_norm_rope_grad_kernel<V, LANES, kHalf, kLayer, false>)
+        <<<grid, 256, 0, st>>>(a);
+  };
   if (a.r.half)
-    (layer ? sa_norm_rope_grad_kernel<V, LANES, true, true> : sa_norm_rope_grad_kernel<V, LANES, true, false>)<<<grid, 256, 0, st>>>(a);
+    layer ? go(std::true_type(), std::true_type()) : go(std::true_type(), std::false_type());
   else
-    (layer ? sa_norm_rope_grad_kernel<V, LANES, false, true> : sa_norm_rope_grad_kernel<V, LANES, false, false>)<<<grid, 256, 0, st>>>(a);
+    layer ? go(std::false_type(), std::true_type()) : go(std::false_type(), std::false_type());
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !(a.dw[0] || a.dw[1] || a.db[0] || a.db[1])) return e;
   return launch_early(sa_norm_rope_sum_kernel<D>, dim3(2, grid.y), 8 * D, 0, st, a);
