@@ -938,10 +938,9 @@ def sparse_attn_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor | None, q:
     y = _empty_like(q) if oq is None else oq
     if y.shape != q.shape:
         raise ValueError("out must have q's shape")
-    # one allocation holds the vectors' gradients
-    need = sum(1 for x in (qw, qb, kw, kb) if x)
-    sums = iter(_empty((need, d), dtype=_f32, device=q.device).unbind(0)) if need else iter(())
-    dqw, dqb, dkw, dkb = (next(sums) if x else None for x in (qw, qb, kw, kb))
+    device = q.device
+    dqw, dqb, dkw, dkb = (_empty(d, dtype=_f32, device=device) if x else None for x in (qw, qb, kw, kb))
+    need = qw or qb or kw or kb
     at = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
     side0 = _GRAD_SIDE.pack(H, q.data_ptr(), *qs, dq.data_ptr(), *gs, y.data_ptr(), *_view(y, dtype, "out", dev), qw,
                             at(dqw), at(dqb))
@@ -953,7 +952,7 @@ def sparse_attn_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor | None, q:
         side1 = _GRAD_SIDE.pack(Hk, k.data_ptr(), *ks, dk.data_ptr(), *hs, z.data_ptr(),
                                 *_view(z, dtype, "out of k", dev), kw, at(dkw), at(dkb))
     if need and workspace is None:
-        workspace = _empty(_c_norm_grad_ws(p, H, Hk), dtype=torch.uint8, device=q.device)
+        workspace = _empty(_c_norm_grad_ws(p, H, Hk), dtype=torch.uint8, device=device)
     st = _c_norm_grad(p, side0, side1, _flat(workspace, torch.uint8, "workspace", dev),
                       0 if workspace is None else workspace.numel(), _current_stream(dev))
     if st != SA_OK:
@@ -1040,8 +1039,10 @@ def sparse_attn_cache8_read(cache: Cache8, first, n: int, *, out=None, out_dtype
         return _elsewhere(dev, stream, sparse_attn_cache8_read, cache, first, n, out=out, out_dtype=out_dtype)
     p, (B, H, N, d) = _cache8_fields(cache, dev)
     if out is None:
-        out = tuple(_empty((B, H, n, d), dtype=out_dtype, device=cache[0].device) for _ in range(2))
-    ko, vo = out
+        device = cache[0].device
+        ko, vo = _empty((B, H, n, d), dtype=out_dtype, device=device), _empty((B, H, n, d), dtype=out_dtype, device=device)
+    else:
+        ko, vo = out
     kind = next((t.dtype for t in (ko, vo) if t is not None), None)
     if kind not in _OUT:
         raise ValueError("out must hold a bfloat16 or float32 tensor")

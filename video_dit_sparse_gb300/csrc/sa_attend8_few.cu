@@ -88,7 +88,7 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
 
 template <int D, int RP>
 __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
-    sa_attend8_few_kernel(const __grid_constant__ Attend8Args a, const __grid_constant__ CUtensorMap tm_k,
+    sa_attend8_few_kernel(const __grid_constant__ Attend8Args a, bool whole, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v) {
   using C = FCfg<D, RP>;
   constexpr int S = C::kStages;
@@ -98,8 +98,8 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   __shared__ int before[kMostEntries + 1];  // tiles of the entries ahead of each
-  __shared__ float rowf[RP], rowm[RP], red[4][RP];
-  __shared__ int rowhi[RP], nan_at[D];
+  __shared__ float rowf[2][RP], rowm[RP], red[4][RP];  // (two: this run's and the next one's)
+  __shared__ int rowhi[2][RP], nan_at[2][D];
   volatile int* abort = &abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nr = a.m.R * a.m.Nq;  // rows of a key head
@@ -146,10 +146,24 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  const int total = before[a.m.B], blocks = min(static_cast<int>(gridDim.x), total);
-  const bool works = static_cast<int>(blockIdx.x) < blocks;
-  const int g0 = works ? static_cast<int>(int64_t(blockIdx.x) * total / blocks) : 0;
-  const int g1 = works ? static_cast<int>(int64_t(blockIdx.x + 1) * total / blocks) : 0;
+  const int total = before[a.m.B], heads = a.m.B * a.m.Hkv;
+  int g0, g1, v0 = 0, v1 = 0;  // the block's tiles, and its heads where they are not cut
+  if (whole) {
+    v0 = static_cast<int>(int64_t(blockIdx.x) * heads / gridDim.x);
+    v1 = static_cast<int>(int64_t(blockIdx.x + 1) * heads / gridDim.x);
+    auto tile_of = [&](int v) -> int {  // head v's first tile
+      const int b = v / a.m.Hkv;
+      return b == a.m.B ? total : before[b] + (v - b * a.m.Hkv) * ((before[b + 1] - before[b]) / a.m.Hkv);
+    };
+    g0 = tile_of(v0);
+    g1 = tile_of(v1);
+  } else {
+    const int blocks = min(static_cast<int>(gridDim.x), total);
+    const bool works = static_cast<int>(blockIdx.x) < blocks;
+    g0 = works ? static_cast<int>(int64_t(blockIdx.x) * total / blocks) : 0;
+    g1 = works ? static_cast<int>(int64_t(blockIdx.x + 1) * total / blocks) : 0;
+    let_next_kernel_start();
+  }
   auto run_at = [&](int g) -> Run {
     int b = 0, top = a.m.B - 1;  // the last entry that starts at g or before and has tiles
     while (b < top) {
@@ -174,11 +188,10 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
     const int t = threadIdx.x;
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     uint32_t c = 0;  // tiles so far
-    for (int g = g0; g < g1;) {
-      const Run x = run_at(g);
-      g += x.n;
-      // The rows, in two terms: RP rows of D / 8 pieces of eight values.  (The last run's products have read the old
-      // ones: its last S is here.)
+    uint32_t runs = 0;
+    // A run's rows, in two terms: RP rows of D / 8 pieces of eight values.  (The last run's products have read the
+    // old ones: its last S is here.)
+    auto prepare = [&](const Run& x, int at) {
       constexpr int kPieces = D / 8;
 #pragma unroll
       for (int f0 = 0; f0 < RP * kPieces; f0 += 128) {
@@ -199,16 +212,28 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
           *reinterpret_cast<uint2*>(smem + C::kQ + rows8_offset<D>(RP + r, p * 8)) = lo;
         }
         if (there && p == 0) {
-          rowf[r] = r < nr ? a.scale_log2 / fac : 0.f;
-          rowhi[r] = r < nr ? row_span(a.m.mask, x.b, qi).hi : 0;
+          rowf[at][r] = r < nr ? a.scale_log2 / fac : 0.f;
+          rowhi[at][r] = r < nr ? row_span(a.m.mask, x.b, qi).hi : 0;
         }
       }
-      if (t < D) nan_at[t] = kNever;
+      if (t < D) nan_at[at][t] = kNever;
       fence_proxy_async_smem();
-      named_barrier(1, 128);
       mbar_arrive(&qfull);
+    };
+    Run x = {}, next = {};
+    if (g0 < g1) {
+      next = run_at(g0);
+      prepare(next, 0);
+      named_barrier(1, 128);
+    }
+    for (int g = g0; g < g1; ++runs) {
+      x = next;
+      g += x.n;
+      const float* rowf_ = rowf[runs & 1];
+      const int* rowhi_ = rowhi[runs & 1];
+      int* nan_at_ = nan_at[runs & 1];
       int least = kNever;
-      for (int r = 0; r < nr; ++r) least = min(least, rowhi[r]);
+      for (int r = 0; r < nr; ++r) least = min(least, rowhi_[r]);
       const int most = keys_of(a, x.b);
       const float* ksc = a.k_scale + int64_t(x.b) * a.k_scales.b + int64_t(x.hk) * a.k_scales.h;
       const float* vsc = a.v_scale + int64_t(x.b) * a.v_scales.b + int64_t(x.hk) * a.v_scales.h;
@@ -246,7 +271,7 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
           }
           tmem_ld_wait();
 #pragma unroll
-          for (int r = 0; r < RP; ++r) y[r] = fmaf(s[r] + s[RP + r], rowf[r] * ks, lv);
+          for (int r = 0; r < RP; ++r) y[r] = fmaf(s[r] + s[RP + r], rowf_[r] * ks, lv);
         }
         if (ks == 0.f) {  // (an empty block's keys are zeros, whatever their codes)
 #pragma unroll
@@ -254,7 +279,7 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
         }
         if (edge) {
 #pragma unroll
-          for (int r = 0; r < RP; ++r) y[r] = key < rowhi[r] ? y[r] : -INFINITY;
+          for (int r = 0; r < RP; ++r) y[r] = key < rowhi_[r] ? y[r] : -INFINITY;
         }
         float u[RP];
         auto weights = [&]() -> bool {  // false: one is too large
@@ -340,7 +365,7 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
               } else if (((e[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) {
                 for (int q = 0; q < 4; ++q)
                   if ((e[i] >> (8 * q) & 127) == 127) {
-                    atomicMin(&nan_at[p * 16 + 4 * i + q], key);
+                    atomicMin(&nan_at_[p * 16 + 4 * i + q], key);
                     e[i] &= ~(255u << (8 * q));
                   }
                 changed = true;
@@ -372,6 +397,10 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
         tc_fence_before();
         mbar_arrive(&pfull[sb]);
       }
+      if (g < g1) {  // its first S is computed beside this run's output
+        next = run_at(g);
+        prepare(next, (runs + 1) & 1);
+      }
       // ---------------------------------------------------------- output: thread = column of d
       mbar_wait(&pdone[(c - 1) & 1], ((c - 1) >> 1) & 1, abort);
 #pragma unroll
@@ -383,10 +412,10 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
       }
       named_barrier(1, 128);
       tc_fence_after();
-      const bool whole = x.n == x.tiles;
+      const bool all = x.n == x.tiles;
       const int64_t slot = int64_t(blockIdx.x) + int64_t(x.b) * a.m.Hkv + x.hk;
       const float unit = fast_exp2(lref);
-      const int nan = t < D ? nan_at[t] : kNever;
+      const int nan = t < D ? nan_at_[t] : kNever;
 #pragma unroll 1
       for (int r0 = 0; r0 < RP; r0 += 8) {
         if (r0 >= nr) break;
@@ -401,10 +430,10 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
           const float sum = (red[0][r] + red[1][r]) + (red[2][r] + red[3][r]);
           float v = __uint_as_float(o[0][i]) + (__uint_as_float(o[1][i]) + __uint_as_float(o[2][i]));
           v = sum == 0.f ? 0.f : v * (unit / sum);
-          if (nan < rowhi[r]) v = __uint_as_float(0x7FC00000u);
+          if (nan < rowhi_[r]) v = __uint_as_float(0x7FC00000u);
           const int qi = r / a.m.R, h = x.hk * a.m.R + r - qi * a.m.R;
           if (t < D) {
-            if (!whole)
+            if (!all)
               a.m.part_o[(slot * nr + r) * D + t] = v;
             else {
               const int64_t at = int64_t(x.b) * a.m.os.b + int64_t(h) * a.m.os.h + int64_t(qi) * a.m.os.n + t;
@@ -416,7 +445,7 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
           }
           if (t == 0) {
             const float lse = sum == 0.f ? -INFINITY : kLn2f * (rowm[r] + log2f(sum));
-            if (!whole)
+            if (!all)
               a.m.part_lse[slot * nr + r] = lse;
             else if (a.m.lse)
               a.m.lse[(int64_t(x.b) * a.m.Hq + h) * a.m.Nq + qi] = lse;
@@ -424,7 +453,20 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
         }
       }
       tc_fence_before();
-      named_barrier(1, 128);  // (the next run writes rowhi, rowm, red and nan_at)
+      named_barrier(1, 128);  // (the next run writes rowm and red, and reads its rows)
+    }
+    for (int v = v0; v < v1; ++v) {  // heads without keys
+      const int b = v / a.m.Hkv, hk = v - b * a.m.Hkv;
+      if (before[b + 1] != before[b]) continue;
+      for (int f = t; f < nr * D; f += 128) {
+        const int r = f / D, qi = r / a.m.R, h = hk * a.m.R + r - qi * a.m.R;
+        const int64_t at = int64_t(b) * a.m.os.b + int64_t(h) * a.m.os.h + int64_t(qi) * a.m.os.n + f % D;
+        if (a.m.out_fp32)
+          static_cast<float*>(a.m.o)[at] = 0.f;
+        else
+          static_cast<uint16_t*>(a.m.o)[at] = 0;
+        if (f % D == 0 && a.m.lse) a.m.lse[(int64_t(b) * a.m.Hq + h) * a.m.Nq + qi] = -INFINITY;
+      }
     }
   } else if (warp == 4) {
     // ------------------------------------------------------------ MMA issue
@@ -591,7 +633,7 @@ cudaError_t launch_f(const Attend8Args& a, int grid, const CUtensorMap& tk, cons
   const int smem = C::kSmemBytes > 120 * 1024 ? C::kSmemBytes : 120 * 1024;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, C::kThreads, smem, st>>>(a, tk, tv);
+  kern<<<grid, C::kThreads, smem, st>>>(a, attend8_whole(a), tk, tv);
   return cudaGetLastError();
 }
 
@@ -601,16 +643,16 @@ cudaError_t launch_d8(const Attend8Args& a, int grid, const CUtensorMap& tk, con
   cudaError_t e = nr <= 8    ? launch_f<D, 8>(a, grid, tk, tv, st)
                   : nr <= 16 ? launch_f<D, 16>(a, grid, tk, tv, st)
                              : launch_f<D, 32>(a, grid, tk, tv, st);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || attend8_whole(a)) return e;
   return launch_early(sa_attend8_join_kernel<D>, dim3(a.m.B * a.m.Hkv * nr), 4 * D, 0, st, a, grid);
 }
 
 }  // namespace
 
-// Blocks of the few-row kernel: one an SM, or a tile each.
+// Blocks of the few-row kernel: one an SM, or a tile (a head, where they are not cut) each.
 int attend8_few_grid(const Attend8Args& a) {
-  const int64_t tiles = int64_t(a.m.B) * a.m.Hkv * ((int64_t(a.m.Nk) + kKeys - 1) / kKeys);
-  return static_cast<int>(std::min<int64_t>(tiles, kAttend8Sms));
+  const int64_t heads = int64_t(a.m.B) * a.m.Hkv, tiles = heads * ((int64_t(a.m.Nk) + kKeys - 1) / kKeys);
+  return static_cast<int>(std::min<int64_t>(attend8_whole(a) ? heads : tiles, kAttend8Sms));
 }
 
 cudaError_t launch_attend8_few(const Attend8Args& a, cudaStream_t st) {

@@ -130,6 +130,7 @@ struct Parts {
   size_t o, lse;
 };
 Parts parts_of(const Attend8Args& a) {
+  if (attend8_few(a) && attend8_whole(a)) return {0, 0};
   const size_t rows = attend8_few(a) ? (size_t(attend8_few_grid(a)) + size_t(a.m.B) * a.m.Hkv) * a.m.R * a.m.Nq
                                      : size_t(a.m.split_units) * a.m.splits * a.m.unit_rows;
   return {(rows * a.m.d * 4 + 255) / 256 * 256, (rows * 4 + 255) / 256 * 256};
@@ -247,7 +248,8 @@ sa_status sparse_attn_cache8_read(const sa_cache8* p, const int32_t* first, int3
   if (st != SA_OK) return st;
   if (n < 1 || (!k_out && !v_out) || (k_out && !ks) || (v_out && !vs) || !aligned(first, 4)) return SA_ERR_INVALID_ARG;
   if (out_dtype != SA_OUT_BF16 && out_dtype != SA_OUT_FP32) return SA_ERR_INVALID_ARG;
-  if (n > (1 << 30) || int64_t(p->B) * p->Hkv * n * (p->d / 16) > (int64_t(1) << 37)) return SA_ERR_UNSUPPORTED;  // grid.x
+  if (n > (1 << 30) || int64_t(p->B) * p->Hkv * 2 * ((int64_t(n) * (p->d / 16) + 511) / 512) >= (int64_t(1) << 31))
+    return SA_ERR_UNSUPPORTED;  // grid.x
   const int esz = out_dtype == SA_OUT_FP32 ? 4 : 2;
   View y[2] = {{k_out, {}, p->B, p->Hkv, n, 0}, {v_out, {}, p->B, p->Hkv, n, 0}};
   for (int i = 0; i < 2; ++i) {

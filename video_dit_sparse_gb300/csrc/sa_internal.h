@@ -248,6 +248,8 @@ struct Attend8Args {
 };
 // Up to 32 rows a key head, and batch entries that its table holds: the few-row kernel.
 inline bool attend8_few(const Attend8Args& a) { return int64_t(a.m.R) * a.m.Nq <= 32 && a.m.B <= kMostEntries; }
+// Short heads are not cut: every block takes whole ones (12 heads of 880 keys: a second kernel and its workspace less).
+inline bool attend8_whole(const Attend8Args& a) { return a.m.Nk <= 8 * 128; }
 int attend8_few_grid(const Attend8Args& a);
 cudaError_t launch_attend8_few(const Attend8Args& a, cudaStream_t stream);
 void attend8_many_plan(Attend8Args* a);
