@@ -191,7 +191,25 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
     uint32_t runs = 0;
     // A run's rows, in two terms: RP rows of D / 8 pieces of eight values.  (The last run's products have read the
     // old ones: its last S is here.)
+    // What else a run needs from memory is asked for ahead of the rows, all at once: one after the other the loads took
+    // longer than the first S.
+    const float *ksc = nullptr, *vsc = nullptr;  // the head's scales
+    int most_next = 0, at_block = 0;             // keys that any row sees; the thread's key's block
+    float s0_next = 0.f, ks_next = 0.f, vs_next = 0.f;
+    const int last_block = (a.m.Nk - 1) >> a.block_log2, block_step = kKeys >> a.block_log2;
+    auto fetch = [&]() {  // (past the cache's end: its last block; no row sees that key)
+      const int at = min(at_block, last_block);
+      ks_next = __ldg(ksc + at);
+      vs_next = __ldg(vsc + at);
+      at_block += block_step;
+    };
     auto prepare = [&](const Run& x, int at) {
+      ksc = a.k_scale + int64_t(x.b) * a.k_scales.b + int64_t(x.hk) * a.k_scales.h;
+      vsc = a.v_scale + int64_t(x.b) * a.v_scales.b + int64_t(x.hk) * a.v_scales.h;
+      s0_next = __ldg(vsc + (x.j0 * kKeys >> a.block_log2));
+      at_block = (x.j0 * kKeys + t) >> a.block_log2;
+      fetch();
+      most_next = keys_of(a, x.b);
       constexpr int kPieces = D / 8;
 #pragma unroll
       for (int f0 = 0; f0 < RP * kPieces; f0 += 128) {
@@ -234,24 +252,17 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
       int* nan_at_ = nan_at[runs & 1];
       int least = kNever;
       for (int r = 0; r < nr; ++r) least = min(least, rowhi_[r]);
-      const int most = keys_of(a, x.b);
-      const float* ksc = a.k_scale + int64_t(x.b) * a.k_scales.b + int64_t(x.hk) * a.k_scales.h;
-      const float* vsc = a.v_scale + int64_t(x.b) * a.v_scales.b + int64_t(x.hk) * a.v_scales.h;
+      const int most = most_next;
       // value scales count from that of the run's first block
-      const float s0 = held_scale(__ldg(vsc + (x.j0 * kKeys >> a.block_log2)));
+      const float s0 = held_scale(s0_next);
       const float lref = s0 > 0.f ? __log2f(s0) : 0.f;
-      auto scale_at = [&](const float* s, int key) -> float { return key < a.m.Nk ? held_scale(__ldg(s + (key >> a.block_log2))) : 0.f; };
       float l[RP];
 #pragma unroll
       for (int r = 0; r < RP; ++r) l[r] = 0.f;
-      float ks_next = scale_at(ksc, x.j0 * kKeys + t), vs_next = scale_at(vsc, x.j0 * kKeys + t);
       for (int j = 0; j < x.n; ++j, ++c) {
         const int k0 = (x.j0 + j) * kKeys, key = k0 + t;
-        const float ks = ks_next, vs = vs_next;
-        if (j + 1 < x.n) {
-          ks_next = scale_at(ksc, key + kKeys);
-          vs_next = scale_at(vsc, key + kKeys);
-        }
+        const float ks = held_scale(ks_next), vs = held_scale(vs_next);
+        if (j + 1 < x.n) fetch();
         const float lv = vs > 0.f ? fminf(fmaxf(__log2f(vs) - lref, -100.f), 100.f) : 0.f, iv = fast_exp2(-lv);
         const uint32_t sb = c & 1;
         const bool edge = k0 + kKeys > least;  // some row does not see the whole tile
@@ -351,27 +362,27 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
           const uint32_t iv_at = (2 * c + 1) % S;
           if (clean) mbar_wait(&full[iv_at], ((2 * c + 1) / S) & 1, abort);
           uint8_t* vt = smem + C::kRing + iv_at * C::kTile;
-#pragma unroll 1
-          for (int p = 0; clean && p < D / 16; ++p) {
-            uint4* at = reinterpret_cast<uint4*>(vt + rows8_offset<D>(t, p * 16));
-            uint4 w = *at;
-            uint32_t* e = reinterpret_cast<uint32_t*>(&w);
-            bool changed = false;
+          auto piece = [&](int p) -> uint4* { return reinterpret_cast<uint4*>(vt + rows8_offset<D>(t, p * 16)); };
+          if (clean && (key >= most || vs == 0.f)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (key >= most || vs == 0.f) {
-                changed |= e[i] != 0;
-                e[i] = 0;
-              } else if (((e[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) {
-                for (int q = 0; q < 4; ++q)
-                  if ((e[i] >> (8 * q) & 127) == 127) {
-                    atomicMin(&nan_at_[p * 16 + 4 * i + q], key);
-                    e[i] &= ~(255u << (8 * q));
-                  }
-                changed = true;
+            for (int p = 0; p < D / 16; ++p) *piece(p) = make_uint4(0, 0, 0, 0);
+          } else if (clean) {
+            uint32_t bad = 0;
+#pragma unroll
+            for (int p = 0; p < D / 16; ++p) {
+              const uint4 w = *piece(p);
+              bad |= ((w.x & 0x7F7F7F7Fu) + 0x01010101u) | ((w.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                     ((w.z & 0x7F7F7F7Fu) + 0x01010101u) | ((w.w & 0x7F7F7F7Fu) + 0x01010101u);
+            }
+            if (bad & 0x80808080u) {
+              for (int q = 0; q < D; ++q) {
+                uint8_t* code = vt + rows8_offset<D>(t, q);
+                if ((*code & 127) == 127) {
+                  atomicMin(&nan_at_[q], key);
+                  *code = 0;
+                }
               }
             }
-            if (changed) *at = w;
           }
         }
 #pragma unroll
@@ -402,7 +413,6 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
         prepare(next, (runs + 1) & 1);
       }
       // ---------------------------------------------------------- output: thread = column of d
-      mbar_wait(&pdone[(c - 1) & 1], ((c - 1) >> 1) & 1, abort);
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
         float v = l[r];
@@ -410,6 +420,7 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
         for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         if (lane == 0) red[warp][r] = v;
       }
+      mbar_wait(&pdone[(c - 1) & 1], ((c - 1) >> 1) & 1, abort);
       named_barrier(1, 128);
       tc_fence_after();
       const bool all = x.n == x.tiles;
