@@ -12,7 +12,7 @@
 // The terms are columns of their own, added up at the end.
 //
 // Work is cut evenly whatever the lengths: the key tiles of all heads of all sequences are one row of tiles, and every
-// block takes an equal run of it.  A run that covers a head in part leaves a normalised fp32 partial result and its
+// block takes an equal part of it.  A run that covers a head in part leaves a normalised fp32 partial result and its
 // lse; a second kernel joins them.
 //
 // The row's reference is that of its run's first tile and moves when a weight passes 2^15 (eight times the first
@@ -45,15 +45,21 @@ struct FCfg {
   static constexpr int kTmemCols = kOCol + kPRows <= 64 ? 64 : kOCol + kPRows <= 128 ? 128 : 256;
   static constexpr int kThreads = 192;  // four softmax warps, one for the MMAs, one for the loads
   static_assert(kSmemBytes <= 220 * 1024, "shared memory");
+  static_assert(kStages <= 32, "a warp makes the ring's barriers");
 };
 
-// What the blocks of a launch share out: tiles of each batch entry's heads, in order.
+// What the blocks of a launch share out: places, of which a head has one for each of its key tiles and kRunCost in
+// front of them (if it has any tiles).  A run's start and output take as long as that many tiles: with tiles alone to go
+// by, the blocks that end one head and begin another came last by a fifth (4 sequences of 24 heads on 6, up to 28160
+// keys).
+constexpr int kRunCost = 6;
 struct Run {
   int b, hk, j0, n, tiles;  // entry, key head, first tile, tiles, tiles of the head
 };
 
 __device__ __forceinline__ int keys_of(const Attend8Args& a, int b) { return row_span(a.m.mask, b, a.m.Nq - 1).hi; }
 __device__ __forceinline__ int tiles_of_entry(const Attend8Args& a, int b) { return (keys_of(a, b) + kKeys - 1) / kKeys; }
+__device__ __forceinline__ int places_of_head(int tiles) { return tiles ? tiles + kRunCost : 0; }
 
 // Any of `count` threads' flags, on hardware barrier `id`.
 __device__ __forceinline__ bool any_of(int id, int count, bool x) {
@@ -97,29 +103,33 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
   __shared__ uint64_t full[S], empty[S], sfull[2], pfull[2], pdone[2], qfull, drain;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
-  __shared__ int before[kMostEntries + 1];  // tiles of the entries ahead of each
+  __shared__ int before[kMostEntries + 1];  // places of the entries ahead of each
   __shared__ float rowf[2][RP], rowm[RP], red[4][RP];  // (two: this run's and the next one's)
   __shared__ int rowhi[2][RP], nan_at[2][D];
   volatile int* abort = &abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nr = a.m.R * a.m.Nq;  // rows of a key head
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], 128);
-      mbar_init(&pdone[i], 1);
-    }
+  if (threadIdx.x < S) {
+    mbar_init(&full[threadIdx.x], 1);
+    mbar_init(&empty[threadIdx.x], 1);
+    fence_mbar_init();
+  } else if (threadIdx.x >= 32 && threadIdx.x < 34) {
+    const int i = threadIdx.x - 32;
+    mbar_init(&sfull[i], 1);
+    mbar_init(&pfull[i], 128);
+    mbar_init(&pdone[i], 1);
+    fence_mbar_init();
+  } else if (threadIdx.x == 64) {
     mbar_init(&qfull, 128);
     mbar_init(&drain, 1);
     abort_flag = 0;
     fence_mbar_init();
+  } else if (threadIdx.x == 160) {
+    prefetch_map(&tm_k);
+    prefetch_map(&tm_v);
   }
-  for (int b = threadIdx.x; b < a.m.B; b += C::kThreads) before[b + 1] = tiles_of_entry(a, b) * a.m.Hkv;
+  for (int b = threadIdx.x; b < a.m.B; b += C::kThreads) before[b + 1] = places_of_head(tiles_of_entry(a, b)) * a.m.Hkv;
   for (int i = threadIdx.x; i < 2 * C::kPBytes / 16; i += C::kThreads)  // (columns that no term fills stay 0)
     reinterpret_cast<uint4*>(smem + C::kP)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
@@ -147,16 +157,16 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   const int total = before[a.m.B], heads = a.m.B * a.m.Hkv;
-  int g0, g1, v0 = 0, v1 = 0;  // the block's tiles, and its heads where they are not cut
+  int g0, g1, v0 = 0, v1 = 0;  // the block's places, and its heads where they are not cut
   if (whole) {
     v0 = static_cast<int>(int64_t(blockIdx.x) * heads / gridDim.x);
     v1 = static_cast<int>(int64_t(blockIdx.x + 1) * heads / gridDim.x);
-    auto tile_of = [&](int v) -> int {  // head v's first tile
+    auto place_of = [&](int v) -> int {  // head v's first place
       const int b = v / a.m.Hkv;
       return b == a.m.B ? total : before[b] + (v - b * a.m.Hkv) * ((before[b + 1] - before[b]) / a.m.Hkv);
     };
-    g0 = tile_of(v0);
-    g1 = tile_of(v1);
+    g0 = place_of(v0);
+    g1 = place_of(v1);
   } else {
     const int blocks = min(static_cast<int>(gridDim.x), total);
     const bool works = static_cast<int>(blockIdx.x) < blocks;
@@ -164,21 +174,27 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
     g1 = works ? static_cast<int>(int64_t(blockIdx.x + 1) * total / blocks) : 0;
     let_next_kernel_start();
   }
-  auto run_at = [&](int g) -> Run {
-    int b = 0, top = a.m.B - 1;  // the last entry that starts at g or before and has tiles
-    while (b < top) {
-      const int mid = (b + top + 1) >> 1;
-      if (before[mid] <= g)
-        b = mid;
-      else
-        top = mid - 1;
+  // The run that begins at place *g or behind it, which moves on; none: n = 0.
+  auto next_run = [&](int* g) -> Run {
+    Run x = {};
+    while (*g < g1 && x.n == 0) {
+      int b = 0, top = a.m.B - 1;  // the last entry that starts there or before and has places
+      while (b < top) {
+        const int mid = (b + top + 1) >> 1;
+        if (before[mid] <= *g)
+          b = mid;
+        else
+          top = mid - 1;
+      }
+      const int per = (before[b + 1] - before[b]) / a.m.Hkv;
+      x.b = b;
+      x.tiles = per - kRunCost;
+      x.hk = (*g - before[b]) / per;
+      const int at = *g - before[b] - x.hk * per, len = min(per - at, g1 - *g);
+      x.j0 = max(at - kRunCost, 0);
+      x.n = max(at + len - kRunCost, 0) - x.j0;
+      *g += len;
     }
-    Run x;
-    x.b = b;
-    x.tiles = (before[b + 1] - before[b]) / a.m.Hkv;
-    x.hk = (g - before[b]) / x.tiles;
-    x.j0 = g - before[b] - x.hk * x.tiles;
-    x.n = min(x.tiles - x.j0, g1 - g);
     return x;
   };
 
@@ -216,6 +232,7 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
         const int f = f0 + t, r = f / kPieces, p = f % kPieces;
         const int qi = r / a.m.R, h = x.hk * a.m.R + r - qi * a.m.R;
         const bool there = RP * kPieces % 128 == 0 || r < RP;
+        const int sees = r < nr ? row_span(a.m.mask, x.b, qi).hi : 0;
         uint4 u = make_uint4(0, 0, 0, 0);
         if (r < nr)
           u = *reinterpret_cast<const uint4*>(a.m.q + int64_t(x.b) * a.m.qs.b + int64_t(h) * a.m.qs.h + int64_t(qi) * a.m.qs.n + p * 8);
@@ -231,22 +248,21 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
         }
         if (there && p == 0) {
           rowf[at][r] = r < nr ? a.scale_log2 / fac : 0.f;
-          rowhi[at][r] = r < nr ? row_span(a.m.mask, x.b, qi).hi : 0;
+          rowhi[at][r] = sees;
         }
       }
       if (t < D) nan_at[at][t] = kNever;
       fence_proxy_async_smem();
       mbar_arrive(&qfull);
     };
-    Run x = {}, next = {};
-    if (g0 < g1) {
-      next = run_at(g0);
+    int g = g0;
+    Run next = next_run(&g);
+    if (next.n) {
       prepare(next, 0);
       named_barrier(1, 128);
     }
-    for (int g = g0; g < g1; ++runs) {
-      x = next;
-      g += x.n;
+    for (; next.n; ++runs) {
+      const Run x = next;
       const float* rowf_ = rowf[runs & 1];
       const int* rowhi_ = rowhi[runs & 1];
       int* nan_at_ = nan_at[runs & 1];
@@ -310,8 +326,8 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
         };
         bool fits = true;
         if (j > 0) fits = weights();
-        if (any_of(2, 128, !fits || (vs == 0.f && key < most)) || j == 0 || edge) {
-          const bool raise = any_of(2, 128, !fits) || j == 0;
+        if (j == 0 || any_of(2, 128, !fits || (vs == 0.f && key < most)) || edge) {
+          const bool raise = j == 0 || any_of(2, 128, !fits);
           if (raise) {
 #pragma unroll
             for (int r = 0; r < RP; ++r) {
@@ -408,10 +424,8 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
         tc_fence_before();
         mbar_arrive(&pfull[sb]);
       }
-      if (g < g1) {  // its first S is computed beside this run's output
-        next = run_at(g);
-        prepare(next, (runs + 1) & 1);
-      }
+      next = next_run(&g);
+      if (next.n) prepare(next, (runs + 1) & 1);  // its first S is computed beside this run's output
       // ---------------------------------------------------------- output: thread = column of d
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
@@ -502,9 +516,9 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
     if (lane == 0) {
       bool ok = true;
       uint32_t c = 0, runs = 0;
-      for (int g = g0; ok && g < g1; ++runs) {
-        const Run x = run_at(g);
-        g += x.n;
+      for (int g = g0; ok; ++runs) {
+        const Run x = next_run(&g);
+        if (!x.n) break;
         if (!(ok = mbar_wait(&qfull, runs & 1, abort)) || !(ok = ready(2 * c))) break;
         tc_fence_after();
         first(c);
@@ -534,9 +548,9 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
     // ------------------------------------------------------------ loads
     uint32_t it = 0;
     bool ok = true;
-    for (int g = g0; ok && g < g1;) {
-      const Run x = run_at(g);
-      g += x.n;
+    for (int g = g0; ok;) {
+      const Run x = next_run(&g);
+      if (!x.n) break;
       for (int f = 0; f < 2 * x.n; ++f, ++it) {
         const uint32_t s = it % S;
         if (!(ok = mbar_wait(&empty[s], ((it / S) & 1) ^ 1, abort))) break;
@@ -564,16 +578,15 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
 }
 
 // A block joins a row's partial results (or writes that it saw nothing): lse = ln sum_p e^(lse_p), o = sum_p
-// e^(lse_p - lse) o_p.  Every column has four threads, each takes every fourth partial result.
+// e^(lse_p - lse) o_p.  Every column has four threads, each takes every fourth partial result, eight at a time.
 template <int D>
 __global__ void __launch_bounds__(4 * D) sa_attend8_join_kernel(const __grid_constant__ Attend8Args a, int grid) {
   __shared__ int sums[2][4 * D / 32];
-  __shared__ float acc[4][D], wsum[4];
-  wait_for_earlier_kernel();
+  __shared__ float s_acc[4][D], s_sum[4], s_mx[4];
   const int nr = a.m.R * a.m.Nq, v = blockIdx.x / nr, r = blockIdx.x - v * nr, b = v / a.m.Hkv, hk = v - b * a.m.Hkv;
-  int ahead = 0, total = 0;  // tiles of the entries ahead of b, and of all
+  int ahead = 0, total = 0;  // places of the entries ahead of b, and of all
   for (int i = threadIdx.x; i < a.m.B; i += 4 * D) {
-    const int n = tiles_of_entry(a, i) * a.m.Hkv;
+    const int n = places_of_head(tiles_of_entry(a, i)) * a.m.Hkv;
     total += n;
     if (i < b) ahead += n;
   }
@@ -591,39 +604,61 @@ __global__ void __launch_bounds__(4 * D) sa_attend8_join_kernel(const __grid_con
     total += sums[1][i];
   }
   const int tiles = tiles_of_entry(a, b), blocks = min(grid, total);
-  const int64_t t0 = ahead + int64_t(hk) * tiles;
   int first = 0, parts = 0;
   if (tiles > 0) {
+    const int64_t t0 = ahead + int64_t(hk) * (tiles + kRunCost) + kRunCost;  // the head's first tile's place
     first = static_cast<int>(((t0 + 1) * blocks - 1) / total);
     parts = static_cast<int>(((t0 + tiles) * blocks - 1) / total) - first + 1;
-    if (parts == 1) return;  // one block did it all
   }
+  // (the partial results are read by plain loads, which stay behind the wait; every block waits)
+  wait_for_earlier_kernel();
+  if (parts == 1) return;  // one block did it all
   const int k = threadIdx.x / D, c = threadIdx.x % D;
   const int64_t row0 = (int64_t(first) + v) * nr + r;
-  float mx = -INFINITY;
-  bool none = false;  // a partial result that is not a number makes the row none (fmaxf drops it)
-#pragma unroll 8
-  for (int p = 0; p < parts; ++p) {
-    const float x = a.m.part_lse[row0 + int64_t(p) * nr];
-    mx = fmaxf(mx, x);
-    none |= x != x;
-  }
-  float sum = 0.f, o = 0.f;
-  if (mx != -INFINITY || none) {
-#pragma unroll 4
-    for (int p = k; p < parts; p += 4) {
+  float mx = -INFINITY, sum = 0.f, o = 0.f;
+  for (int p0 = k; p0 < parts; p0 += 32) {
+    float l[8], f[8], top = mx;
+    bool none = false;  // a partial result that is not a number makes the row none (fmaxf drops it)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int p = p0 + 4 * i;
       const int64_t row = row0 + int64_t(p) * nr;
-      const float w = __expf(a.m.part_lse[row] - mx);
+      l[i] = p < parts ? a.m.part_lse[row] : -INFINITY;
+      f[i] = p < parts ? a.m.part_o[row * D + c] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      top = fmaxf(top, l[i]);
+      none |= l[i] != l[i];
+    }
+    if (top == -INFINITY && !none) continue;
+    const float keep = __expf(mx - top);
+    mx = top;
+    sum *= keep;
+    o *= keep;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float w = __expf(l[i] - mx);
       sum += w;
-      o = fmaf(w, a.m.part_o[row * D + c], o);
+      o = fmaf(w, f[i], o);
     }
   }
-  acc[k][c] = o;
-  if (c == 0) wsum[k] = sum;
+  s_acc[k][c] = o;
+  if (c == 0) {
+    s_sum[k] = sum;
+    s_mx[k] = mx;
+  }
   __syncthreads();
   if (k) return;
-  sum = (wsum[0] + wsum[1]) + (wsum[2] + wsum[3]);
-  o = (acc[0][c] + acc[1][c]) + (acc[2][c] + acc[3][c]);
+  const float all = fmaxf(fmaxf(s_mx[0], s_mx[1]), fmaxf(s_mx[2], s_mx[3]));
+  sum = o = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (s_sum[i] != 0.f) {  // (a NaN is not 0)
+      const float w = __expf(s_mx[i] - all);
+      sum = fmaf(w, s_sum[i], sum);
+      o = fmaf(w, s_acc[i][c], o);
+    }
   o = sum == 0.f ? 0.f : o / sum;
   const int qi = r / a.m.R, h = hk * a.m.R + r - qi * a.m.R;
   const int64_t at = int64_t(b) * a.m.os.b + int64_t(h) * a.m.os.h + int64_t(qi) * a.m.os.n + c;
@@ -631,7 +666,7 @@ __global__ void __launch_bounds__(4 * D) sa_attend8_join_kernel(const __grid_con
     static_cast<float*>(a.m.o)[at] = o;
   else
     static_cast<uint16_t*>(a.m.o)[at] = static_cast<uint16_t>(pack_bf16(o, 0.f));
-  if (c == 0 && a.m.lse) a.m.lse[(int64_t(b) * a.m.Hq + h) * a.m.Nq + qi] = sum == 0.f ? -INFINITY : mx + logf(sum);
+  if (c == 0 && a.m.lse) a.m.lse[(int64_t(b) * a.m.Hq + h) * a.m.Nq + qi] = sum == 0.f ? -INFINITY : all + logf(sum);
 }
 
 namespace {
