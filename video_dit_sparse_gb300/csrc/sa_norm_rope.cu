@@ -22,6 +22,10 @@
 
 namespace sa {
 
+// Heads on their way in the gradient: this one and seven more (a power of two), 128 KB for the one block that an SM has.
+// (24 + 24 heads x 16384 x 128, token-major: 97 us; four heads and two blocks an SM 110; the next head in registers 120.)
+constexpr int kAhead = 8;
+
 struct NormRopeArgs {
   RopeArgs r;           // x: inputs, y: outputs (the gradient's dx)
   const void* g[2];     // the gradient's dy
@@ -213,12 +217,13 @@ __global__ void __launch_bounds__(256, 2) sa_norm_rope_kernel(const __grid_const
 // The gradient.  blockIdx.y: side.  A block takes every blocks[side]-th piece of work: 256 / LANES tokens of a batch
 // entry, `run` heads of them.  BIAS: db is wanted.
 template <int V, int LANES, bool HALF, bool LAYER, bool BIAS>
-__global__ void __launch_bounds__(256, 2) sa_norm_rope_grad_kernel(const __grid_constant__ NormRopeArgs a) {
+__global__ void __launch_bounds__(256, 1) sa_norm_rope_grad_kernel(const __grid_constant__ NormRopeArgs a) {
   constexpr int kTokens = 256 / LANES;
   constexpr int kBytes = V == 8 ? 2 : 4;
   constexpr int kRow = 2 * V * LANES;  // d
   constexpr float kInv = 1.f / kRow;
   __shared__ float sums[8][2][kRow];
+  extern __shared__ uint4 ring[];  // [kAhead][x piece 0, 1, dy piece 0, 1][thread]
   const RopeArgs& r = a.r;
   const int s = blockIdx.y;
   if (static_cast<int>(blockIdx.x) >= a.blocks[s]) return;
@@ -241,25 +246,32 @@ __global__ void __launch_bounds__(256, 2) sa_norm_rope_grad_kernel(const __grid_
     const char* x = static_cast<const char*>(r.x[s]) + (b * r.xs[s].b + n * r.xs[s].n) * kBytes;
     const char* dy = static_cast<const char*>(a.g[s]) + (b * a.gs[s].b + n * a.gs[s].n) * kBytes;
     char* dx = static_cast<char*>(r.y[s]) + (b * r.ys[s].b + n * r.ys[s].n) * kBytes;
-    uint4 ux0, ux1, ug0, ug1;  // the next head's
-    auto load = [&](int h) {
-      const char* at = x + h * r.xs[s].h * kBytes;
-      ux0 = *reinterpret_cast<const uint4*>(at + e0 * kBytes);
-      ux1 = *reinterpret_cast<const uint4*>(at + e1 * kBytes);
-      at = dy + h * a.gs[s].h * kBytes;
-      ug0 = *reinterpret_cast<const uint4*>(at + e0 * kBytes);
-      ug1 = *reinterpret_cast<const uint4*>(at + e1 * kBytes);
+    // The thread's pieces of the next heads are on their way to places of its own in shared memory.
+    auto fetch = [&](int h) {
+      if (h < h1) {
+        const uint32_t to = smem_u32(ring + ((h & (kAhead - 1)) * 4) * 256 + threadIdx.x);
+        const char* at = x + h * r.xs[s].h * kBytes;
+        cp_async16(to, at + e0 * kBytes, 16);
+        cp_async16(to + 4096, at + e1 * kBytes, 16);
+        at = dy + h * a.gs[s].h * kBytes;
+        cp_async16(to + 8192, at + e0 * kBytes, 16);
+        cp_async16(to + 12288, at + e1 * kBytes, 16);
+      }
+      cp_async_commit();
     };
-    load(h0);
+#pragma unroll
+    for (int i = 0; i < kAhead - 1; ++i) fetch(h0 + i);
     Angles<V, HALF> angles;
     angles.load(r, b, n, e0, e1, turns);  // (r.inverse is set: R^-1)
     for (int h = h0; h < h1; ++h) {
       uint64_t v0[V / 2], v1[V / 2], g0[V / 2], g1[V / 2];
-      unpack2<V>(ux0, v0);
-      unpack2<V>(ux1, v1);
-      unpack2<V>(ug0, g0);
-      unpack2<V>(ug1, g1);
-      if (h + 1 < h1) load(h + 1);
+      fetch(h + kAhead - 1);
+      cp_async_wait<kAhead - 1>();
+      const uint4* here = ring + ((h & (kAhead - 1)) * 4) * 256 + threadIdx.x;
+      unpack2<V>(here[0], v0);
+      unpack2<V>(here[256], v1);
+      unpack2<V>(here[512], g0);
+      unpack2<V>(here[768], g1);
       const float k = normalise<V, LANES, LAYER>(v0, v1, a.eps);
       const uint64_t kk = f2(k, k);
       angles.turn(r, e0, e1, turns, part_turns, g0, g1);
@@ -297,6 +309,7 @@ __global__ void __launch_bounds__(256, 2) sa_norm_rope_grad_kernel(const __grid_
       }
     }
   }
+  cp_async_wait<0>();
   if (!a.dw[s] && !a.db[s]) return;
   let_next_kernel_start();
   // the warp's rows, then the block's warps
@@ -366,7 +379,7 @@ cudaError_t launch_n(const NormRopeArgs& a, bool layer, int num_sms, cudaStream_
   return cudaGetLastError();
 }
 
-// Blocks of each side: two an SM for both sides together, by their heads, and no more than there is work for.
+// Blocks of each side: one an SM for both sides together, by their heads, and no more than there is work for.
 // Runs of heads as long as that leaves work for all of them.
 void grad_plan(NormRopeArgs* a, int num_sms) {
   const RopeArgs& r = a->r;
@@ -377,7 +390,7 @@ void grad_plan(NormRopeArgs* a, int num_sms) {
     a->run[s] = 1;
     a->blocks[s] = 0;
     if (!H) continue;
-    const int64_t share = std::max<int64_t>(1, int64_t(num_sms) * 2 * H / (r.H[0] + r.H[1]));
+    const int64_t share = std::max<int64_t>(1, int64_t(num_sms) * H / (r.H[0] + r.H[1]));
     int run = H;
     while (run > 1 && tiles * ((H + run - 1) / run) < share) run = (run + 1) / 2;
     a->run[s] = run;
@@ -390,16 +403,19 @@ cudaError_t launch_g(const NormRopeArgs& a, bool layer, cudaStream_t st) {
   constexpr int D = 2 * V * LANES;
   const dim3 grid(std::max(a.blocks[0], a.blocks[1]), a.r.H[1] ? 2 : 1);
   const bool bias = a.db[0] || a.db[1];
+  constexpr int kSmem = kAhead * 4 * 256 * 16;
+  cudaError_t e = cudaSuccess;
   auto go = [&](auto half, auto lay) {
     constexpr bool kHalf = decltype(half)::value, kLayer = decltype(lay)::value;
-    (bias ? sa_norm_rope_grad_kernel<V, LANES, kHalf, kLayer, true> : sa_norm_rope_grad_kernel<V, LANES, kHalf, kLayer, false>)
-        <<<grid, 256, 0, st>>>(a);
+    auto kern = bias ? sa_norm_rope_grad_kernel<V, LANES, kHalf, kLayer, true> : sa_norm_rope_grad_kernel<V, LANES, kHalf, kLayer, false>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e == cudaSuccess) kern<<<grid, 256, kSmem, st>>>(a);
   };
   if (a.r.half)
     layer ? go(std::true_type(), std::true_type()) : go(std::true_type(), std::false_type());
   else
     layer ? go(std::false_type(), std::true_type()) : go(std::false_type(), std::false_type());
-  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess || !(a.dw[0] || a.dw[1] || a.db[0] || a.db[1])) return e;
   return launch_early(sa_norm_rope_sum_kernel<D>, dim3(2, grid.y), 8 * D, 0, st, a);
 }
