@@ -686,9 +686,7 @@ cudaError_t launch_f(const Attend8Args& a, int grid, const CUtensorMap& tk, cons
 template <int D>
 cudaError_t launch_d8(const Attend8Args& a, int grid, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
   const int nr = a.m.R * a.m.Nq;
-  cudaError_t e = nr <= 8    ? launch_f<D, 8>(a, grid, tk, tv, st)
-                  : nr <= 16 ? launch_f<D, 16>(a, grid, tk, tv, st)
-                             : launch_f<D, 32>(a, grid, tk, tv, st);
+  cudaError_t e = nr <= 8 ? launch_f<D, 8>(a, grid, tk, tv, st) : launch_f<D, 16>(a, grid, tk, tv, st);
   if (e != cudaSuccess || attend8_whole(a)) return e;
   return launch_early(sa_attend8_join_kernel<D>, dim3(a.m.B * a.m.Hkv * nr), 4 * D, 0, st, a, grid);
 }
