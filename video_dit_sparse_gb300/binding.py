@@ -500,6 +500,7 @@ _ATTEND8 = struct.Struct("@2ifi6qiP")
 assert _CACHE8.size == ctypes.sizeof(sa_cache8) and _ATTEND8.size == ctypes.sizeof(sa_attend8)
 _bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
+_BLOCKS = (16, 32, 64, 128)
 _empty, _empty_like = torch.empty, torch.empty_like
 _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
@@ -972,7 +973,9 @@ class Cache8(NamedTuple):
 
 
 def sparse_attn_cache8(B: int, Hk: int, N: int, d: int, *, block: int = 128, device=None) -> Cache8:
-    """An empty cache with room for N tokens of every head."""
+    """An empty cache with room for N tokens of every head, in blocks of 16, 32, 64 or 128 tokens."""
+    if block not in _BLOCKS:
+        raise ValueError("block must be 16, 32, 64 or 128")
     device = torch.device("cuda" if device is None else device)
     k, v = (torch.zeros((B, Hk, N, d), dtype=torch.float8_e4m3fn, device=device) for _ in range(2))
     ks, vs = (torch.zeros((B, Hk, -(-N // block)), dtype=_f32, device=device) for _ in range(2))
@@ -983,6 +986,8 @@ def _cache8_fields(cache, dev):
     """The packed sa_cache8 of a cache on device `dev`, and its B, Hk, N, d."""
     k, v, ks, vs, block = cache
     shape = k.shape
+    if block not in _BLOCKS:
+        raise ValueError("the cache's block must be 16, 32, 64 or 128")
     if k.dtype not in _E4M3 or v.dtype is not k.dtype or dev < 0:
         raise ValueError("the cache's k and v must be CUDA tensors [B, Hk, N, d] of float8_e4m3fn (or uint8)")
     kst, vst = _view(k, k.dtype, "the cache's k", dev), _view(v, v.dtype, "the cache's v", dev)

@@ -559,10 +559,6 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
       uint32_t tc = 0, uc = 0;  // key tiles (of the ring) and units of this tile so far
       uint32_t pc = 0, ts = 0;  // key tiles of this Q tile, steps taken in turns
       auto pass = [&]() { mbar_arrive(&bars.turn[t ^ 1]); };
-      auto free_both = [&](uint64_t* bar) {  // (a tile alone counts for both)
-        mma_commit(bar);
-        if (!two) mma_commit(bar);
-      };
       auto qk = [&](uint32_t c, bool turn) {
         const uint32_t kl = k_lo + (((c % C::kKStages) * C::kTile) >> 4);
         constexpr int kSteps = 2 * (D / 32);
@@ -581,8 +577,14 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
         two = u.two;
         mbar_arrive(&bars.ring_empty[i % kRing]);
         if (!go) break;
-        if (n == 0 || (t && !two)) {
-          tc += n;
+        if (n == 0) continue;
+        if (t && !two) {  // no rows: K and V pass by (tile by tile: a wait for the next unit could outlast its limit)
+          for (int j = 0; ok && j < n; ++j, ++tc) {
+            if (!(ok = mbar_wait(&bars.kfull[tc % C::kKStages], (tc / C::kKStages) & 1, abort))) break;
+            mbar_arrive(&bars.kempty[tc % C::kKStages]);
+            if (!(ok = mbar_wait(&bars.vfull[tc % C::kVStages], (tc / C::kVStages) & 1, abort))) break;
+            mbar_arrive(&bars.vempty[tc % C::kVStages]);
+          }
           continue;
         }
         if (!(ok = mbar_wait(&bars.qfull[t], uc & 1, abort)) ||
@@ -590,7 +592,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
           break;
         tc_fence_after();
         qk(tc, false);
-        free_both(&bars.kempty[tc % C::kKStages]);
+        mma_commit(&bars.kempty[tc % C::kKStages]);
         for (int j = 0; j < n; ++j) {
           const uint32_t c = tc + j, s = ts + j;
           const bool more = j + 1 < n;
@@ -613,8 +615,8 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
           else if (two)
             pass();
           if (!more) mma_commit(&bars.ofull[t]);
-          free_both(&bars.vempty[c % C::kVStages]);
-          if (more) free_both(&bars.kempty[(c + 1) % C::kKStages]);
+          mma_commit(&bars.vempty[c % C::kVStages]);
+          if (more) mma_commit(&bars.kempty[(c + 1) % C::kKStages]);
         }
         tc += n;
         pc += n;
