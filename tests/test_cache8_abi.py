@@ -226,6 +226,17 @@ def test_binding_refusals(sa):
             f()
 
 
+def test_binding_takes_no_position_that_does_not_fit(sa):
+    """A number that a 32-bit argument would wrap around must not end up at another token."""
+    assert sa._tokens(5, "start", 0, 1) == (0, 5) and sa._tokens(-2 ** 31, "start", 0, 1) == (0, -2 ** 31)
+    for at in (2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1):
+        with pytest.raises(ValueError):
+            sa._tokens(at, "start", 0, 1)
+    for block in (0, 8, 48, 256):
+        with pytest.raises(ValueError):
+            sa.sparse_attn_cache8(1, 1, 16, 64, block=block, device="cpu")
+
+
 # ---------------------------------------------------------------- pins of the 64-bit forms
 
 def test_norm_form_against_torch():

@@ -1008,7 +1008,10 @@ def _tokens(at, name, dev, B):
     """A first token given as an int or as int32 [B]: (address, int)."""
     if isinstance(at, torch.Tensor):
         return _flat(at, _i32, name, dev, (B,)), 0
-    return 0, int(at)
+    at = int(at)
+    if not -2 ** 31 <= at < 2 ** 31:
+        raise ValueError(f"{name} must be a 32-bit number")
+    return 0, at
 
 
 def sparse_attn_cache8_append(cache: Cache8, k: torch.Tensor, v: torch.Tensor, start, *,
