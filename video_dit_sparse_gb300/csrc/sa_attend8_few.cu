@@ -117,11 +117,11 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
   } else if (threadIdx.x >= 32 && threadIdx.x < 34) {
     const int i = threadIdx.x - 32;
     mbar_init(&sfull[i], 1);
-    mbar_init(&pfull[i], 128);
+    mbar_init(&pfull[i], 4);
     mbar_init(&pdone[i], 1);
     fence_mbar_init();
   } else if (threadIdx.x == 64) {
-    mbar_init(&qfull, 128);
+    mbar_init(&qfull, 4);
     mbar_init(&drain, 1);
     abort_flag = 0;
     fence_mbar_init();
@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
       }
       if (t < D) nan_at[at][t] = kNever;
       fence_proxy_async_smem();
-      mbar_arrive(&qfull);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qfull);
     };
     int g = g0;
     Run next = next_run(&g);
@@ -403,8 +404,7 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
         }
 #pragma unroll
         for (int r = 0; r < RP; ++r) l[r] = fmaf(u[r], iv, l[r]);
-        // the buffer's last reader
-        if (c >= 2) mbar_wait(&pdone[sb], ((c - 2) >> 1) & 1, abort);
+        // (The buffer's last reader, the product of tile c - 2, was issued ahead of this tile's S and is done with it.)
         uint8_t* sp = smem + C::kP + sb * C::kPBytes;
         auto put = [&](int n, uint32_t code) {
           sp[n * kKeys + ((((t >> 4) ^ (n & 7)) << 4) | (t & 15))] = static_cast<uint8_t>(code);
@@ -422,7 +422,8 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(&pfull[sb]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[sb]);
       }
       next = next_run(&g);
       if (next.n) prepare(next, (runs + 1) & 1);  // its first S is computed beside this run's output
