@@ -105,6 +105,24 @@ def test_ragged_lengths(d, H, Nq, causal):
     check(*run(q, c, causal=causal, lengths=lengths), q, c, causal=causal, lengths=lengths)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq", [1, 4])
+def test_lse_of_one_key_keeps_its_own_precision(d, Nq):
+    """One key, one column that is not 0: lse is the score, however small.  Its roundings (the scale's, its product with
+    log2 e, the score's, its product with ln 2) are 2^-24 of it each, the two constants' 2^-25: below 2^-21 together."""
+    from video_dit_sparse_gb300 import binding as sa
+    c = sa.sparse_attn_cache8(1, 2, 1, d, block=16)
+    k = torch.zeros(1, 2, 1, d)
+    k[..., 5] = 0.7
+    sa.sparse_attn_cache8_append(c, k.to(torch.bfloat16).cuda(), rows(1, 2, 1, d, 1), 0)
+    q = torch.zeros(1, 4, Nq, d)
+    q[..., 5] = torch.tensor([0.01, -0.3, 1.1, 40.0])[None, :, None] * torch.linspace(1, 1.7, Nq)
+    q = q.to(torch.bfloat16).cuda()
+    _, lse = run(q, c, scale=0.3)
+    want = q[..., 5].double().cpu().numpy() * held(c)[0][:, :, 0, 5].repeat(2, 1)[..., None] * 0.3
+    assert (np.abs(lse.double().cpu().numpy() - want) <= 2.0 ** -21 * np.abs(want)).all()
+
+
 @pytest.mark.parametrize("H,Nq", [(2, 1), (2, 40)])
 def test_long_caches_many_splits(H, Nq):
     c = filled(1, 2, 33000, 128, 128, seed=4)

@@ -28,8 +28,10 @@ namespace {
 
 constexpr int kKeys = 128;  // keys of a tile
 constexpr float kLn2f = 0.69314718055994531f;
-constexpr float kTop = 12.f;           // a row's largest weight of its first tile is 2^12
-constexpr float kMostWeight = 32768.f;  // 2^15 (an exponent of 15 and more, as `moved` says it)
+// A row's weights count from the largest of its first tile, so that neither a weight's exponent nor the sum's logarithm
+// carries an offset that its rounding would pay for (2^-20 of lse); the product takes them times 2^12.
+constexpr float kUnit = 4096.f;
+constexpr float kMostWeight = 8.f;  // (2^15 in the product: an exponent of 3 and more, as `moved` says it)
 constexpr int kNever = 0x7FFFFFFF;
 
 template <int D, int RP>
@@ -319,10 +321,10 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
           }
           return top == 0.f;
         };
-        // A row's new reference: it moves if a weight passed 2^15 (each row by itself: its bits do not go by the others).
+        // A row's new reference: it moves if a weight passed 8 (each row by itself: its bits do not go by the others).
         auto moved = [&](int r, float m0, bool start, int rows) -> float {
           const float mx = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r]));
-          const float mn = start || mx - m0 > 15.f ? mx - kTop : m0;
+          const float mn = start || mx - m0 > 3.f ? mx : m0;
           return r >= rows || mn == -INFINITY ? INFINITY : mn;
         };
         bool fits = true;
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
         };
 #pragma unroll
         for (int r = 0; r < RP; r += 2) {
-          uint32_t h = pack_half(u[r], u[r + 1]);
+          uint32_t h = pack_half(u[r] * kUnit, u[r + 1] * kUnit);
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
             const uint32_t e = encode_e5m2(h);
@@ -440,7 +442,7 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
       tc_fence_after();
       const bool all = x.n == x.tiles;
       const int64_t slot = int64_t(blockIdx.x) + int64_t(x.b) * a.m.Hkv + x.hk;
-      const float unit = fast_exp2(lref);
+      const float unit = fast_exp2(lref) * (1.f / kUnit);
       const int nan = t < D ? nan_at_[t] : kNever;
 #pragma unroll 1
       for (int r0 = 0; r0 < RP; r0 += 8) {

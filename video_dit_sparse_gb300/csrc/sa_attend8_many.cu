@@ -33,6 +33,7 @@ constexpr int BN = 128;  // keys of a tile
 constexpr int kRing = 2;  // units in flight
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kTop = 6.f;            // a row's largest weight of its first tile is 2^6
+constexpr float kUnit = 64.f;          // 2^kTop
 constexpr float kMostSum = 32768.f;    // of half a row's weights in a tile
 
 template <int D>
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
         const float inv = l == 0.f ? 0.f : fast_exp2(lref) / l;
         const int64_t prow = int64_t(x.part) * m_.unit_rows + t * 128 + trow;
         if (valid && half == 0) {
-          const float lse = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+          const float lse = l == 0.f ? -INFINITY : kLn2 * ((m + kTop) + log2f(l * (1.f / kUnit)));
           if (x.part >= 0)
             m_.part_lse[prow] = lse;
           else if (m_.lse)
