@@ -835,14 +835,20 @@ def sparse_attn_cache_evict(weights: torch.Tensor, k: torch.Tensor | None, v: to
 
 
 def _norm_vectors(dtype, dev, d, named):
-    """The addresses of the given [d] vectors (0 for None) and whether they are fp32."""
-    kinds = {t.dtype for _, t in named if t is not None}
-    if len(kinds) > 1:
-        raise ValueError("weights and biases must have one dtype")
-    kind = kinds.pop() if kinds else _f32
-    if kind is not _f32 and kind is not dtype:
-        raise ValueError("weights and biases must be float32 or of q's dtype")
-    return [_flat(t, kind, name, dev, (d,)) for name, t in named], _OUT[kind]
+    """The addresses of the given [d] vectors (0 for None) and their dtype's number."""
+    kind, at = None, []
+    for name, t in named:
+        if t is None:
+            at.append(0)
+            continue
+        if kind is None:
+            kind = t.dtype
+            if kind is not _f32 and kind is not dtype:
+                raise ValueError("weights and biases must be float32 or of q's dtype")
+        elif t.dtype is not kind:
+            raise ValueError("weights and biases must have one dtype")
+        at.append(_flat(t, kind, name, dev, (d,)))
+    return at, SA_OUT_FP32 if kind is None else _OUT[kind]
 
 
 def sparse_attn_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, *, norm: str = "rms",
