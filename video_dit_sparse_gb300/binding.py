@@ -1001,13 +1001,16 @@ def _cache8_fields(cache, dev):
         raise ValueError("the cache's v must have its k's shape")
     B, H, N, d = shape
     blocks = -(-N // block)
+    strides = []
     for name, t in (("k_scale", ks), ("v_scale", vs)):
         if t.dtype is not _f32 or t.get_device() != dev or t.dim() != 3 or t.shape != (B, H, blocks):
             raise ValueError(f"the cache's {name} must be float32 [B, Hk, ceil(N / block)] on its k's device")
-        if t.stride(2) != 1 and blocks != 1:
+        sb, sh, sn = t.stride()
+        if sn != 1 and blocks != 1:
             raise ValueError(f"the cache's {name} must have a contiguous last dimension")
+        strides += sb, sh, 1
     return _CACHE8.pack(B, H, N, d, block, k.data_ptr(), v.data_ptr(), *kst, *vst, ks.data_ptr(), vs.data_ptr(),
-                        ks.stride(0), ks.stride(1), 1, vs.stride(0), vs.stride(1), 1), shape
+                        *strides), shape
 
 
 def _tokens(at, name, dev, B):
