@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
     const float* scales = nullptr;
     float ahead = 0.f;
     auto fetch = [&](int k0) -> float {
-      const int key = k0 + (lane < 8 ? col0 + (lane & 3) * W : warp * 8);
-      return lane < 9 && key < m_.Nk ? held_scale(__ldg(scales + (key >> a.block_log2))) : 0.f;
+      const int key = min(k0 + (lane < 8 ? col0 + (lane & 3) * W : warp * 8), m_.Nk - 1);
+      return __ldg(scales + (key >> a.block_log2));  // (as it is: a look at it here would wait for it)
     };
     // The warp's eight keys of a tile's values from codes to fp16.
     uint32_t vc = 0;  // tiles converted so far
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
       auto row_of = [&](int y) -> int { return warp * 8 + r_lane + (D == 128 ? 0 : y * kRows); };
       auto piece_of = [&](int y) -> int { return D == 128 ? p_lane + 4 * y : p_lane; };
       const uint32_t cs = vc % C::kCStages, vs = vc % C::kVStages;
-      const bool filled = __shfl_sync(0xffffffffu, ahead, 8) > 0.f;
+      const bool filled = held_scale(__shfl_sync(0xffffffffu, ahead, 8)) > 0.f;
       const int live = filled ? bars.ring[slot].uhi - k0 : 0;
       if (!mbar_wait(&bars.cfull[cs], (vc / C::kCStages) & 1, abort) ||
           !mbar_wait(&bars.vempty[vs], ((vc / C::kVStages) & 1) ^ 1, abort))
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
       {
         for (int j = 0; j < n; ++j) {
           const int k0 = key0 + j * BN, c0 = k0 + col0;  // the tile's and the warp's first key
-          const float sc = ahead;
+          const float sc = held_scale(ahead);
           if (j + 1 < n) ahead = fetch(k0 + BN);
           auto step = [&]() -> bool {
           const int vb = hi - c0;
