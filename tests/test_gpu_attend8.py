@@ -123,6 +123,26 @@ def test_lse_of_one_key_keeps_its_own_precision(d, Nq):
     assert (np.abs(lse.double().cpu().numpy() - want) <= 2.0 ** -21 * np.abs(want)).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq", [1, 4])
+def test_lse_of_one_key_beside_a_large_query_value(d, Nq):
+    """The column that counts is 2^-10 to 2^-16 of the row's largest, whose key is 0: the row's two terms are off by
+    2^-22 of that largest, what is left as in the test above."""
+    from video_dit_sparse_gb300 import binding as sa
+    c = sa.sparse_attn_cache8(1, 2, 1, d, block=16)
+    k = torch.zeros(1, 2, 1, d)
+    k[..., 5] = 0.7
+    sa.sparse_attn_cache8_append(c, k.to(torch.bfloat16).cuda(), rows(1, 2, 1, d, 1), 0)
+    q = torch.zeros(1, 4, Nq, d)
+    q[..., 9] = 1.9
+    q[..., 5] = torch.tensor([1.3e-3, -7.7e-4, 2.3e-4, 3.1e-5])[None, :, None] * torch.linspace(1, 1.7, Nq)
+    q = q.to(torch.bfloat16).cuda()
+    _, lse = run(q, c, scale=0.3)
+    held_k = held(c)[0][:, :, 0, 5].repeat(2, 1)[..., None]
+    want = q[..., 5].double().cpu().numpy() * held_k * 0.3
+    assert (np.abs(lse.double().cpu().numpy() - want) <= 2.0 ** -21 * np.abs(want) + 2.0 ** -22 * 1.9 * held_k * 0.3).all()
+
+
 @pytest.mark.parametrize("H,Nq", [(2, 1), (2, 40)])
 def test_long_caches_many_splits(H, Nq):
     c = filled(1, 2, 33000, 128, 128, seed=4)

@@ -7,6 +7,8 @@
 // its last of four digits, so what is left is a multiple of bf16's last place of at most four digits: lo holds
 // it exactly, down to e4m3's smallest step of 2^-9.  q f is exact above 2^-10 of the row's largest value and off
 // by 2^-10 (2^-17 of the largest value) below.  Two products at twice the rate cost what one of bf16 does.
+// Where the products of the terms are kept apart, lo is held times 2^5 (it is 8 at most): off by 2^-15, 2^-22 of the
+// largest value.
 #pragma once
 
 #include <cuda.h>
@@ -91,8 +93,8 @@ __device__ __forceinline__ float row_factor(uint32_t top) {
   return __uint_as_float(static_cast<uint32_t>(min(254, 127 + 7 + 127 - e)) << 23);
 }
 
-// Eight bf16 values times f as their two terms.
-__device__ __forceinline__ void two_terms(const uint4& u, float f, uint2* hi, uint2* lo) {
+// Eight bf16 values times f as their two terms, the second one times `lift`.
+__device__ __forceinline__ void two_terms(const uint4& u, float f, float lift, uint2* hi, uint2* lo) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   uint32_t h[4], l[4];
 #pragma unroll
@@ -102,7 +104,7 @@ __device__ __forceinline__ void two_terms(const uint4& u, float f, uint2* hi, ui
     const float x = (a - a) + a * f, y = (b - b) + b * f;
     h[i] = encode2(x, y);
     const uint32_t back = decode2(h[i]);
-    l[i] = encode2(x - half_lo(back), y - half_hi(back));
+    l[i] = encode2((x - half_lo(back)) * lift, (y - half_hi(back)) * lift);
   }
   *hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
   *lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);

@@ -33,6 +33,7 @@ constexpr float kLn2f = 0.69314718055994531f;
 // carries an offset that its rounding would pay for (2^-20 of lse); the product takes them times 2^12.
 constexpr float kUnit = 4096.f;
 constexpr float kMostWeight = 8.f;  // (2^15 in the product: an exponent of 3 and more, as `moved` says it)
+constexpr float kLift = 32.f;  // of a row's second term (its products are columns of their own)
 constexpr int kNever = 0x7FFFFFFF;
 
 template <int D, int RP>
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
         for (int o = kPieces / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float fac = row_factor(top);
         uint2 hi, lo;
-        two_terms(u, fac, &hi, &lo);
+        two_terms(u, fac, kLift, &hi, &lo);
         if (there) {
           *reinterpret_cast<uint2*>(smem + C::kQ + rows8_offset<D>(r, p * 8)) = hi;
           *reinterpret_cast<uint2*>(smem + C::kQ + rows8_offset<D>(RP + r, p * 8)) = lo;
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
           }
           tmem_ld_wait();
 #pragma unroll
-          for (int r = 0; r < RP; ++r) y[r] = fmaf(s[r] + s[RP + r], rowf_[r] * ks, lv);
+          for (int r = 0; r < RP; ++r) y[r] = fmaf(fmaf(s[RP + r], 1.f / kLift, s[r]), rowf_[r] * ks, lv);
         }
         if (ks == 0.f) {  // (an empty block's keys are zeros, whatever their codes)
 #pragma unroll

@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
 #pragma unroll
         for (int p = 0; p < D / 16; p += 2) {
           uint2 h0, l0, h1, l1;
-          two_terms(u[p], f, &h0, &l0);
-          two_terms(u[p + 1], f, &h1, &l1);
+          two_terms(u[p], f, 1.f, &h0, &l0);
+          two_terms(u[p + 1], f, 1.f, &h1, &l1);
           const uint32_t at = rows8_offset<D>(trow, half * (D / 2) + p * 8);
           *reinterpret_cast<uint4*>(sq + at) = make_uint4(h0.x, h0.y, h1.x, h1.y);
           *reinterpret_cast<uint4*>(sq + C::kTile + at) = make_uint4(l0.x, l0.y, l1.x, l1.y);
