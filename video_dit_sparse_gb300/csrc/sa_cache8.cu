@@ -143,8 +143,10 @@ __global__ void __launch_bounds__(256, 4) sa_cache8_append_kernel(const __grid_c
 // 0 where the cache has no such token.  A thread takes twice 16 codes; a.blocks: blocks of a head.
 template <bool WIDE, int PIECES>
 __global__ void __launch_bounds__(256) sa_cache8_read_kernel(const __grid_constant__ Cache8Args a) {
-  constexpr int U = 2;
-  const uint32_t head2 = blockIdx.x / a.blocks, p0 = (blockIdx.x - head2 * a.blocks) * (256 * U) + threadIdx.x;
+  constexpr int U = 2, kTokens = 256 / PIECES;  // tokens that the block's threads have at a time
+  // (a block is a whole number of tokens: pieces of a head, counted through, pass 32 bits from 2^29 tokens of d = 128 on)
+  const uint32_t head2 = blockIdx.x / a.blocks;
+  const int at0 = static_cast<int>(blockIdx.x - head2 * a.blocks) * (kTokens * U) + static_cast<int>(threadIdx.x) / PIECES;
   const bool two = a.y[0] && a.y[1];
   const int which = two ? static_cast<int>(head2 & 1) : a.y[0] ? 0 : 1, bh = static_cast<int>(two ? head2 >> 1 : head2);
   const int b = bh / a.H, h = bh - b * a.H, c = threadIdx.x % PIECES;
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(256) sa_cache8_read_kernel(const __grid_consta
   float s[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const int at = static_cast<int>((p0 + i * 256) / PIECES);
+    const int at = at0 + i * kTokens;
     const int64_t tok = first + at;
     u[i] = make_uint4(0, 0, 0, 0);
     s[i] = 0.f;
@@ -167,7 +169,7 @@ __global__ void __launch_bounds__(256) sa_cache8_read_kernel(const __grid_consta
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const int at = static_cast<int>((p0 + i * 256) / PIECES);
+    const int at = at0 + i * kTokens;
     if (at >= a.n) return;
     if (s[i] == 0.f) u[i] = make_uint4(0, 0, 0, 0);
     const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
