@@ -1023,6 +1023,13 @@ def _tokens(at, name, dev, B):
     return 0, at
 
 
+def _count(n: int) -> int:
+    """A number of tokens, as a 32-bit argument takes it."""
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError("the number of tokens must be a 32-bit number")
+    return n
+
+
 def sparse_attn_cache8_append(cache: Cache8, k: torch.Tensor, v: torch.Tensor, start, *,
                               counts: torch.Tensor | None = None, stream=None) -> Cache8:
     """Writes tokens start[b] .. start[b] + n - 1 of every head into the cache, in place: k, v bf16 views
@@ -1040,7 +1047,7 @@ def sparse_attn_cache8_append(cache: Cache8, k: torch.Tensor, v: torch.Tensor, s
     if k.shape != (B, H, n, d) or v.shape != k.shape:
         raise ValueError("k and v must be [B, Hk, n, d] with the cache's B, Hk and d")
     at, at0 = _tokens(start, "start", dev, B)
-    st = _c_append8(p, n, k.data_ptr(), _STRIDES.pack(*_view(k, _bf16, "k", dev)), v.data_ptr(),
+    st = _c_append8(p, _count(n), k.data_ptr(), _STRIDES.pack(*_view(k, _bf16, "k", dev)), v.data_ptr(),
                     _STRIDES.pack(*_view(v, _bf16, "v", dev)), at, at0, _flat(counts, _i32, "counts", dev, (B,)),
                     _current_stream(dev))
     if st != SA_OK:
@@ -1055,6 +1062,7 @@ def sparse_attn_cache8_read(cache: Cache8, first, n: int, *, out=None, out_dtype
     if dev >= 0 and (stream is not None or dev != _current_device()):
         return _elsewhere(dev, stream, sparse_attn_cache8_read, cache, first, n, out=out, out_dtype=out_dtype)
     p, (B, H, N, d) = _cache8_fields(cache, dev)
+    n = _count(n)
     if out is None:
         device = cache[0].device
         ko, vo = _empty((B, H, n, d), dtype=out_dtype, device=device), _empty((B, H, n, d), dtype=out_dtype, device=device)
