@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
       tc_fence_after();
       const bool all = x.n == x.tiles;
       const int64_t slot = int64_t(blockIdx.x) + int64_t(x.b) * a.m.Hkv + x.hk;
-      const float unit = fast_exp2(lref) * (1.f / kUnit);
+      const float unit = s0 > 0.f ? s0 : 1.f;
       const int nan = t < D ? nan_at_[t] : kNever;
 #pragma unroll 1
       for (int r0 = 0; r0 < RP; r0 += 8) {
@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
           if (r >= nr) continue;
           const float sum = (red[0][r] + red[1][r]) + (red[2][r] + red[3][r]);
           float v = __uint_as_float(o[0][i]) + (__uint_as_float(o[1][i]) + __uint_as_float(o[2][i]));
-          v = sum == 0.f ? 0.f : v * (unit / sum);
+          // (one after the other: the smallest scales by a row's sum are no normal number)
+          v = sum == 0.f ? 0.f : v * ((1.f / kUnit) / sum) * unit;
           if (nan < rowhi_[r]) v = __uint_as_float(0x7FC00000u);
           const int qi = r / a.m.R, h = x.hk * a.m.R + r - qi * a.m.R;
           if (t < D) {

@@ -469,7 +469,8 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
         if (!pair_sync()) goto end;
         l += other()->x;
         ++xn;
-        const float inv = l == 0.f ? 0.f : fast_exp2(lref) / l;
+        // (two factors: the smallest scales by a row's sum are no normal number)
+        const float inv = l == 0.f ? 0.f : 1.f / l, unit = exp2f(lref);
         const int64_t prow = int64_t(x.part) * m_.unit_rows + t * 128 + trow;
         if (valid && half == 0) {
           const float lse = l == 0.f ? -INFINITY : kLn2 * ((m + kTop) + log2f(l * (1.f / kUnit)));
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
           tc_fence_before();
           arrive(&bars.ofree[t]);
 #pragma unroll
-          for (int y = 0; y < D / 2; ++y) v[y] = inv == 0.f ? 0 : __float_as_uint(__uint_as_float(v[y]) * inv);
+          for (int y = 0; y < D / 2; ++y) v[y] = inv == 0.f ? 0 : __float_as_uint(__uint_as_float(v[y]) * inv * unit);
           if (*static_cast<volatile int*>(&bars.nans[i % kRing])) {
             const volatile int* na = nan_at[i % kRing] + half * (D / 2);
 #pragma unroll
