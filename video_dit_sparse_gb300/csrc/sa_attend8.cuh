@@ -110,6 +110,28 @@ __device__ __forceinline__ void two_terms(const uint4& u, float f, float lift, u
   *lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
 }
 
+// Keys of an empty value block add their weights to a row's sum and nothing to its output (their values are cleared).  The
+// row's reference is there for the output, whose weights carry the value scales, any powers of two: as large as the others',
+// an empty block's would push these to the bottom of the second product's 8 or 16 bits.  So they count for the reference
+// less by 2^kEmptyBelow: far enough for blocks 2^100 apart (2^-16 of the reference at least where their weights are as
+// large), near enough for fp32 to hold the sum (2^(84 + 15) a tile, 2^23 tiles); their weights saturate on the way into the
+// product.  As long as a run has seen empty blocks alone they set the reference like any others.
+constexpr float kEmptyBelow = 84.f;
+
+// A pair of weights as fp16; past 65504: 65504.
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ln of 2^m sum.  A sum far from 1 (value scales or empty blocks far from the reference) gives its exponent to m first: added
+// up as logarithms the two would cancel in the digits that fp32 has at their size.
+__device__ __forceinline__ float ln_of(float m, float sum) {
+  const int e = (static_cast<int>(__float_as_uint(sum) >> 23) - 127) / 16 * 16;  // (0 for sums from 2^-15 to 2^16)
+  return 0.69314718055994531f * ((m + e) + log2f(sum * __uint_as_float(static_cast<uint32_t>(127 - e) << 23)));
+}
+
 // Largest finite magnitude (bits) of eight bf16 values.
 __device__ __forceinline__ uint32_t top_of(const uint4& u, uint32_t top) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};

@@ -17,7 +17,7 @@
 // lse; a second kernel joins them.
 //
 // The row's reference is that of its run's first tile and moves when a weight passes 2^15 (eight times the first
-// tile's largest).
+// tile's largest).  Keys of empty value blocks count less for it: sa_attend8.cuh.
 #include <algorithm>
 #include <atomic>
 
@@ -28,7 +28,6 @@ namespace sa {
 namespace {
 
 constexpr int kKeys = 128;  // keys of a tile
-constexpr float kLn2f = 0.69314718055994531f;
 // A row's weights count from the largest of its first tile, so that neither a weight's exponent nor the sum's logarithm
 // carries an offset that its rounding would pay for (2^-20 of lse); the product takes them times 2^12.
 constexpr float kUnit = 4096.f;
@@ -86,11 +85,6 @@ __device__ __forceinline__ uint32_t encode_e5m2(uint32_t pair) {
 __device__ __forceinline__ uint32_t half_sub(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
@@ -274,15 +268,23 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
       int least = kNever;
       for (int r = 0; r < nr; ++r) least = min(least, rowhi_[r]);
       const int most = most_next;
-      // value scales count from that of the run's first block
-      const float s0 = held_scale(s0_next);
-      const float lref = s0 > 0.f ? __log2f(s0) : 0.f;
+      // value scales count from that of the run's first block that holds anything (0: none so far)
+      float s0 = held_scale(s0_next), lref = s0 > 0.f ? __log2f(s0) : 0.f;
       float l[RP];
 #pragma unroll
       for (int r = 0; r < RP; ++r) l[r] = 0.f;
       for (int j = 0; j < x.n; ++j, ++c) {
         const int k0 = (x.j0 + j) * kKeys, key = k0 + t;
         const float ks = held_scale(ks_next), vs = held_scale(vs_next);
+        // (ahead of the next loads, which the loop would wait for; all threads alike)
+        bool first_values = false;  // behind tiles of empty blocks alone
+        if (s0 == 0.f) {
+#pragma unroll 1
+          for (int k = k0; k < min(k0 + kKeys, most) && s0 == 0.f; k += 1 << a.block_log2)
+            s0 = held_scale(__ldg(vsc + (k >> a.block_log2)));
+          if (s0 > 0.f) lref = __log2f(s0);
+          first_values = j > 0 && s0 > 0.f;
+        }
         if (j + 1 < x.n) fetch();
         const float lv = vs > 0.f ? fminf(fmaxf(__log2f(vs) - lref, -100.f), 100.f) : 0.f, iv = fast_exp2(-lv);
         const uint32_t sb = c & 1;
@@ -323,20 +325,23 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
           }
           return top == 0.f;
         };
-        // A row's new reference: it moves if a weight passed 8 (each row by itself: its bits do not go by the others).
+        // A row's new reference: it moves if a weight passed 8 (each row by itself: its bits do not go by the others), and
+        // where empty blocks alone have set it so far.
         auto moved = [&](int r, float m0, bool start, int rows) -> float {
+          if (first_values) m0 -= kEmptyBelow;
           const float mx = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r]));
           const float mn = start || mx - m0 > 3.f ? mx : m0;
           return r >= rows || mn == -INFINITY ? INFINITY : mn;
         };
         bool fits = true;
-        if (j > 0) fits = weights();
+        if (j > 0) fits = weights() && !first_values;
         if (j == 0 || any_of(2, 128, !fits || (vs == 0.f && key < most)) || edge) {
           const bool raise = j == 0 || any_of(2, 128, !fits);
           if (raise) {
+            const float below = vs == 0.f && s0 > 0.f ? kEmptyBelow : 0.f;
 #pragma unroll
             for (int r = 0; r < RP; ++r) {
-              const uint32_t o = __reduce_max_sync(0xffffffffu, y[r] == y[r] ? order_key(y[r]) : 0u);
+              const uint32_t o = __reduce_max_sync(0xffffffffu, y[r] == y[r] ? order_key(y[r] - below) : 0u);
               if (lane == 0) red[warp][r] = o ? key_value(o) : -INFINITY;
             }
             named_barrier(1, 128);
@@ -415,7 +420,7 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
         };
 #pragma unroll
         for (int r = 0; r < RP; r += 2) {
-          uint32_t h = pack_half(u[r] * kUnit, u[r + 1] * kUnit);
+          uint32_t h = pack_weights(u[r] * kUnit, u[r + 1] * kUnit);
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
             const uint32_t e = encode_e5m2(h);
@@ -474,14 +479,14 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
                 static_cast<uint16_t*>(a.m.o)[at] = static_cast<uint16_t>(pack_bf16(v, 0.f));
             }
           }
-          if (t == 0) {
-            const float lse = sum == 0.f ? -INFINITY : kLn2f * (rowm[r] + log2f(sum));
-            if (!all)
-              a.m.part_lse[slot * nr + r] = lse;
-            else if (a.m.lse)
-              a.m.lse[(int64_t(x.b) * a.m.Hq + h) * a.m.Nq + qi] = lse;
-          }
         }
+      }
+      if (t < nr) {
+        const float sum = (red[0][t] + red[1][t]) + (red[2][t] + red[3][t]), lse = sum == 0.f ? -INFINITY : ln_of(rowm[t], sum);
+        if (!all)
+          a.m.part_lse[slot * nr + t] = lse;
+        else if (a.m.lse)
+          a.m.lse[(int64_t(x.b) * a.m.Hq + x.hk * a.m.R + t % a.m.R) * a.m.Nq + t / a.m.R] = lse;
       }
       tc_fence_before();
       named_barrier(1, 128);  // (the next run writes rowm and red, and reads its rows)

@@ -13,7 +13,8 @@
 // one factor a chunk.  P in fp16 keeps eleven digits; its range holds because a row's largest weight starts at 2^6 and
 // the reference m moves before a half row's sum passes 2^15: what is lost lies below 2^-31 of the row's largest.
 //
-// A V tile is cleared where no row of the unit sees it and where a block is empty; a NaN among its codes is cleared
+// A V tile is cleared where no row of the unit sees it and where a block is empty (whose keys count less for the
+// reference: sa_attend8.cuh); a NaN among its codes is cleared
 // too and noted by its column: rows see the first keys of the cache, so a column's first NaN says which rows
 // get one.
 //
@@ -31,10 +32,10 @@ namespace {
 
 constexpr int BN = 128;  // keys of a tile
 constexpr int kRing = 2;  // units in flight
-constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kTop = 6.f;            // a row's largest weight of its first tile is 2^6
 constexpr float kUnit = 64.f;          // 2^kTop
 constexpr float kMostSum = 32768.f;    // of half a row's weights in a tile
+constexpr float kNoScale = INFINITY;   // of a unit that no block with values has shown up in
 
 template <int D>
 struct ACfg {
@@ -71,12 +72,6 @@ struct ABars {
   uint32_t tmem_base;
   int abort;
 };
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 // How many of `count` threads say so, on hardware barrier `id`.
 __device__ __forceinline__ uint32_t count_of(int id, int count, bool x) {
@@ -263,6 +258,16 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
     float rf_next = 0.f, lref_next = 0.f;
     // The next unit's query terms into shared memory, and its first values.  (The last unit's products have read
     // the old terms: its last S is here.)
+    // log2 of the first value scale of a tile of unit x that holds anything (of keys that some row of the unit sees).
+    auto first_scale = [&](const AUnit& x, int k0) -> float {
+      const int key = k0 + (lane << a.block_log2);
+      float s = 0.f;
+      if (lane < BN >> a.block_log2 && key < x.uhi)
+        s = held_scale(__ldg(a.v_scale + int64_t(x.b) * a.v_scales.b + int64_t(x.hk) * a.v_scales.h + (key >> a.block_log2)));
+      const uint32_t has = __ballot_sync(0xffffffffu, s > 0.f);
+      s = __shfl_sync(0xffffffffu, s, has ? __ffs(has) - 1 : 0);
+      return has ? __log2f(s) : kNoScale;
+    };
     auto prepare = [&](uint32_t slot) -> bool {
       const AUnit& x = bars.ring[slot];
       hi_next = 0;
@@ -299,9 +304,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
         }
         fence_proxy_async_smem();
         arrive(&bars.qfull[t]);
-        const float s0 = held_scale(__ldg(a.v_scale + int64_t(x.b) * a.v_scales.b + int64_t(x.hk) * a.v_scales.h +
-                                          (x.key0 >> a.block_log2)));
-        lref_next = s0 > 0.f ? __log2f(s0) : 0.f;
+        lref_next = first_scale(x, x.key0);
       }
       return convert(slot, x.key0);
     };
@@ -311,7 +314,8 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
       const AUnit& x = bars.ring[i % kRing];
       if (!x.go) break;
       const int hi = hi_next;
-      const float rf = rf_next, lref = lref_next;
+      const float rf = rf_next;
+      float lref = lref_next;
       const bool here = t == 0 || x.two;  // the tile has rows
       const int n = x.n, key0 = x.key0;
       const bool valid = in_tile && x.q0 + t * m_.qn + rq < m_.Nq;
@@ -321,11 +325,17 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
         for (int j = 0; j < n; ++j) {
           const int k0 = key0 + j * BN, c0 = k0 + col0;  // the tile's and the warp's first key
           const float sc = held_scale(ahead);
+          // (ahead of the next load, which this one would wait for)
+          bool first_values = false;  // behind tiles of empty blocks alone
+          if (here && lref == kNoScale) {
+            lref = first_scale(x, k0);
+            first_values = j > 0 && lref != kNoScale;
+          }
           if (j + 1 < n) ahead = fetch(k0 + BN);
           auto step = [&]() -> bool {
           const int vb = hi - c0;
           const bool special = __any_sync(0xffffffffu, (valid && vb < H) || (lane < 4 && sc == 0.f));
-          // lanes 4-7: the value scale's exponent and its inverse (0 for an empty block: its values are cleared)
+          // lanes 4-7: the value scale's exponent and its inverse (1 for an empty block)
           const float lv_ = sc > 0.f && lane >= 4 ? fminf(fmaxf(__log2f(sc) - lref, -100.f), 100.f) : 0.f;
           const float iv_ = fast_exp2(-lv_);
           if (!mbar_wait(&bars.sfull[t], (tc + j) & 1, abort)) return false;
@@ -344,12 +354,15 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
               float s[W];
               load(s, base);
               const float ks = __shfl_sync(0xffffffffu, sc, base / W), lv = __shfl_sync(0xffffffffu, lv_, 4 + base / W);
+              const float vs = __shfl_sync(0xffffffffu, sc, 4 + base / W);
+              float top = -INFINITY;
               tmem_ld_wait();
 #pragma unroll
               for (int c = 0; c < W; ++c) {
                 const float y = ks == 0.f ? lv : fmaf(s[c], rf * ks, lv);
-                mx = fmaxf(mx, base + c < vb ? y : -INFINITY);
+                top = fmaxf(top, base + c < vb ? y : -INFINITY);
               }
+              mx = fmaxf(mx, vs == 0.f && lref != kNoScale ? top - kEmptyBelow : top);
             }
             *mine() = make_float2(mx, *over ? 1.f : 0.f);
             if (!pair_sync()) return false;
@@ -391,7 +404,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
                   y1 = base + 2 * c + 1 < vb ? y1 : -INFINITY;
                 }
                 const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
-                p[base / 2 + c] = pack_half2(p0, p1);
+                p[base / 2 + c] = pack_weights(p0, p1);
                 ps[c & 1] = add2(ps[c & 1], f2(p0, p1));
               }
               if ((base + W) % (H / NB) == 0) {
@@ -417,14 +430,14 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
           // A row whose sum is too large in either half moves its reference (the others keep theirs: a row's bits
           // do not go by its neighbours).
           if (j > 0) {
-            bool over = !(ts <= kMostSum);
+            bool over = !(ts <= kMostSum) || first_values;
             const uint32_t asked = meet(__any_sync(0xffffffffu, valid && over));
             if (asked >= 32) return false;
             const bool raise = asked != 0;
             if (raise) {
               float mx;
               if (!row_max(&mx, &over)) return false;
-              const float mn = over ? fmaxf(m, mx) : m;
+              const float mn = over ? fmaxf(first_values ? m - kEmptyBelow : m, mx) : m;
               const float alpha = m == mn ? 1.f : fast_exp2(m - mn);
               m = mn;
               l *= alpha;
@@ -470,10 +483,10 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
         l += other()->x;
         ++xn;
         // (two factors: the smallest scales by a row's sum are no normal number)
-        const float inv = l == 0.f ? 0.f : 1.f / l, unit = exp2f(lref);
+        const float inv = l == 0.f ? 0.f : 1.f / l, unit = lref == kNoScale ? 1.f : exp2f(lref);
         const int64_t prow = int64_t(x.part) * m_.unit_rows + t * 128 + trow;
         if (valid && half == 0) {
-          const float lse = l == 0.f ? -INFINITY : kLn2 * ((m + kTop) + log2f(l * (1.f / kUnit)));
+          const float lse = l == 0.f ? -INFINITY : ln_of(m + kTop, l * (1.f / kUnit));
           if (x.part >= 0)
             m_.part_lse[prow] = lse;
           else if (m_.lse)
