@@ -707,7 +707,7 @@ cudaError_t launch_d8(const Attend8Args& a, int grid, const CUtensorMap& tk, con
 // Blocks of the few-row kernel: one an SM, or a tile (a head, where they are not cut) each.
 int attend8_few_grid(const Attend8Args& a) {
   const int64_t heads = int64_t(a.m.B) * a.m.Hkv, tiles = heads * ((int64_t(a.m.Nk) + kKeys - 1) / kKeys);
-  return static_cast<int>(std::min<int64_t>(attend8_whole(a) ? heads : tiles, kAttend8Sms));
+  return static_cast<int>(std::min<int64_t>(attend8_whole(a) ? heads : tiles, kSms));
 }
 
 cudaError_t launch_attend8_few(const Attend8Args& a, cudaStream_t st) {

@@ -123,6 +123,10 @@ struct MaskDev {
   int32_t Nq, Nk;
 };
 
+// SMs of a GB300.  Plans that decide the order of a sum go by this and not by the device's count, so that the same inputs
+// give the same bits on any part.
+constexpr int kSms = 152;
+
 // Masked forward and cache weights.
 struct MaskedArgs {
   const uint16_t* q;   // bf16 views, element strides, d contiguous
@@ -234,7 +238,6 @@ cudaError_t launch_cache8_append(Cache8Args a, cudaStream_t stream);
 cudaError_t launch_cache8_read(Cache8Args a, bool wide, cudaStream_t stream);
 
 // Attention over an e4m3 cache.  m: q, o, lse, mask, sizes, partial results (ks, vs: the codes' strides).
-constexpr int kAttend8Sms = 152;
 constexpr int kMostEntries = 1024;  // batch entries that the few-row kernel shares out
 struct Attend8Args {
   MaskedArgs m;

@@ -57,7 +57,6 @@ namespace sa {
 namespace {
 
 constexpr int BN = 128;
-constexpr int kSms = 152;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 // P is computed against a row reference m that only moves when a tile's sum

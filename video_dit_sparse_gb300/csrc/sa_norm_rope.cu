@@ -43,9 +43,9 @@ struct NormRopeArgs {
 
 namespace {
 
-// Two fp32 values in each of `P` = V / 2 packed pairs: a lane's piece of V values.
+// A lane's piece of V values is V / 2 packed pairs of fp32.
 
-// The lane's 2 V values of a [d] vector (`none` where it is null).
+// Both of the lane's pieces of a [d] vector (`none` where it is null).
 template <int V>
 __device__ __forceinline__ void load_vector(const void* p, bool wide, int e0, int e1, float none, uint64_t* v0, uint64_t* v1) {
 #pragma unroll
@@ -81,7 +81,7 @@ __device__ __forceinline__ uint4 pack2(const uint64_t* v) {
   return make_uint4(f2lo_bits(v[0]), f2hi_bits(v[0]), f2lo_bits(v[1]), f2hi_bits(v[1]));
 }
 
-// Cosines and sines as `turn2` wants them: HALF: of the pairs (i, i + 1); else pair by pair, in both halves.
+// Cosines and sines as `turn` wants them: HALF: of the pairs (i, i + 1); else pair by pair, in both halves.
 template <int V, bool HALF>
 struct Angles {
   uint64_t cs[V / 2], sn[V / 2];
@@ -379,9 +379,9 @@ cudaError_t launch_n(const NormRopeArgs& a, bool layer, int num_sms, cudaStream_
   return cudaGetLastError();
 }
 
-// Blocks of each side: one an SM for both sides together, by their heads, and no more than there is work for.
-// Runs of heads as long as that leaves work for all of them.
-void grad_plan(NormRopeArgs* a, int num_sms) {
+// Blocks of each side: one an SM (of a GB300, whatever the device) for both sides together, by their heads, and no more
+// than there is work for.  Runs of heads as long as that leaves work for all of them.
+void grad_plan(NormRopeArgs* a) {
   const RopeArgs& r = a->r;
   const int tokens = r.fp32 ? (r.d == 128 ? 16 : 32) : (r.d == 128 ? 32 : 64);
   const int64_t tiles = (int64_t(r.N) + tokens - 1) / tokens * r.B;
@@ -390,7 +390,7 @@ void grad_plan(NormRopeArgs* a, int num_sms) {
     a->run[s] = 1;
     a->blocks[s] = 0;
     if (!H) continue;
-    const int64_t share = std::max<int64_t>(1, int64_t(num_sms) * H / (r.H[0] + r.H[1]));
+    const int64_t share = std::max<int64_t>(1, int64_t(kSms) * H / (r.H[0] + r.H[1]));
     int run = H;
     while (run > 1 && tiles * ((H + run - 1) / run) < share) run = (run + 1) / 2;
     a->run[s] = run;
@@ -434,8 +434,7 @@ sa_status check_norm(const sa_norm_rope* p, int32_t H0, int32_t H1, NormRopeArgs
   return check_rope(&p->rope, H0, H1, &a->r);
 }
 
-// Workspace of the gradient: the blocks' sums, for as many SMs as the GPU can have.
-constexpr int kMostSms = 152;
+// Workspace of the gradient: the blocks' sums.
 size_t grad_workspace(const NormRopeArgs& a) { return size_t(a.blocks[0] + a.blocks[1]) * 2 * a.r.d * 4; }
 
 }  // namespace
@@ -502,7 +501,7 @@ size_t sparse_attn_norm_rope_backward_workspace_size(const sa_norm_rope* p, int3
   if (sa::check_norm(p, H0, H1, &a) != SA_OK) return 0;
   a.r.H[0] = H0;
   a.r.H[1] = H1;
-  sa::grad_plan(&a, sa::kMostSms);
+  sa::grad_plan(&a);
   return sa::grad_workspace(a);
 }
 
@@ -547,7 +546,7 @@ sa_status sparse_attn_norm_rope_backward(const sa_norm_rope* p, const sa_norm_gr
         (!same_view(g[i], y[i]) && views_overlap(g[i], y[i], q.d, esz)))
       return SA_ERR_INVALID_ARG;
   }
-  grad_plan(&a, kMostSms);
+  grad_plan(&a);
   const size_t need = sums ? grad_workspace(a) : 0;
   if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return SA_ERR_INVALID_ARG;
   // Nothing that is written may share memory with anything else of the call.
