@@ -349,20 +349,18 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
           // The row's largest exponent in this tile, over both halves, and whether either half's `over` is set.
           auto row_max = [&](float* res, bool* over) -> bool {
             float mx = -INFINITY;
+            const float lm_ = lane >= 4 && sc == 0.f && lref != kNoScale ? -kEmptyBelow : lv_;
 #pragma unroll 1
             for (int base = 0; base < H; base += W) {
               float s[W];
               load(s, base);
-              const float ks = __shfl_sync(0xffffffffu, sc, base / W), lv = __shfl_sync(0xffffffffu, lv_, 4 + base / W);
-              const float vs = __shfl_sync(0xffffffffu, sc, 4 + base / W);
-              float top = -INFINITY;
+              const float ks = __shfl_sync(0xffffffffu, sc, base / W), lv = __shfl_sync(0xffffffffu, lm_, 4 + base / W);
               tmem_ld_wait();
 #pragma unroll
               for (int c = 0; c < W; ++c) {
                 const float y = ks == 0.f ? lv : fmaf(s[c], rf * ks, lv);
-                top = fmaxf(top, base + c < vb ? y : -INFINITY);
+                mx = fmaxf(mx, base + c < vb ? y : -INFINITY);
               }
-              mx = fmaxf(mx, vs == 0.f && lref != kNoScale ? top - kEmptyBelow : top);
             }
             *mine() = make_float2(mx, *over ? 1.f : 0.f);
             if (!pair_sync()) return false;
