@@ -679,12 +679,20 @@ sa_status sparse_attn_cache8_read(const sa_cache8* cache, const int32_t* first, 
  * clamped to 0 .. N), the query rows are its last positions, and with causal = F > 0 a
  * row sees up to the end of its own frame of F tokens.
  *
- * q bf16, o bf16 or fp32 by out_dtype.  Codes enter the products as they are, a query row in
- * two e4m3 terms (off by 2^-17 of the row's largest value at most); sums are fp32.  What a
- * row does not see never reaches it, whatever its codes and scales.  The value scales of a head
- * may lie up to 2^100 apart.  The workspace (256-byte aligned, may be NULL when its
- * size is 0) holds partial results; calls that may overlap on the GPU need one each.
- * Hq / Hkv <= 128; B Hq <= 2^24.
+ * q bf16, o bf16 or fp32 by out_dtype.  Codes enter the products as they are; scores, sums and o are
+ * fp32.  What is rounded, with o in fp32 too:
+ *  - a query row, held in two e4m3 terms: off by 2^-17 of its largest value at most (2^-22 where
+ *    up to 16 rows, Hq / Hkv Nq, share a key head);
+ *  - a key's weight times its value's scale, held in fp16: off by 2^-11 of it, or by 2^-29 of the row's
+ *    largest such product if that is more.  The weights' sum, which o is divided by and lse comes from, is that
+ *    of the weights before this rounding.
+ *
+ * What a row does not see never reaches it, whatever its codes and scales.  The value scales of a head
+ * may lie up to 2^100 apart, and an empty block costs the others no digits.  The workspace
+ * (256-byte aligned, may be NULL when its size is 0) holds partial results; calls that may overlap on the GPU
+ * need one each.  Hq / Hkv <= 128; B Hq <= 2^24, Hq / Hkv Nq < 2^32, and B Hkv times the tiles of
+ * 128 / (Hq / Hkv) queries, or of 128 tokens, <= 2^30.  Up to 1024 batch entries of up to 16 rows a key head have
+ * a form of their own; with more of them it takes up to twice as long.
  */
 typedef struct {
   int32_t Hq, Nq;

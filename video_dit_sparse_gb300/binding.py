@@ -862,7 +862,9 @@ def sparse_attn_norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, *, nor
 
     norm: "rms" (by the root mean square) or "layer" (by mean and variance).  Weights and biases are [d],
     shared by the heads, fp32 or of q's dtype (None: ones, zeros).  The positions are as in
-    sparse_attn_rope.  out: the output (or a pair of them); it may be the input."""
+    sparse_attn_rope.  out: the output (or a pair of them); it may be the input.
+
+    No autograd graph is recorded, whatever requires a gradient: sparse_attn_norm_rope_backward is the gradient."""
     dtype, dev = q.dtype, q.get_device()
     if dev >= 0 and (stream is not None or dev != _current_device()):
         return _elsewhere(dev, stream, sparse_attn_norm_rope, q, k, norm=norm, q_weight=q_weight, k_weight=k_weight,
@@ -1092,7 +1094,9 @@ def sparse_attn_forward_cache8(q: torch.Tensor, cache: Cache8, *, scale: float |
     Hk).  Returns (o [B, H, Nq, d], lse fp32 [B, H, Nq] or None).
 
     A sequence is the first lengths[b] tokens of the cache (default: all), the rows are its last positions (one new
-    token: Nq = 1), and with `causal` tokens a frame a row sees up to the end of its own frame (1: its own token)."""
+    token: Nq = 1), and with `causal` tokens a frame a row sees up to the end of its own frame (1: its own token).
+
+    Each weight is rounded to fp16 on its way to the values (2^-11 of it, with out_dtype=torch.float32 too)."""
     dev = q.get_device()
     if dev >= 0 and (stream is not None or dev != _current_device()):
         return _elsewhere(dev, stream, sparse_attn_forward_cache8, q, cache, scale=scale, causal=causal, lengths=lengths,

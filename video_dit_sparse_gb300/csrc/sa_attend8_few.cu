@@ -7,9 +7,9 @@
 // of weights stays in the thread until the end, and the mask is a comparison.  The second is
 //     O^T [d x rows] = V^T P^T,
 // with V's codes as the MN-major operand.  Its other operand has 8 bits too: a weight u = 2^12 p vs (vs: the value
-// block's scale; p counts from the row's reference, so that u <= 2^15) is cut into three e5m2 terms, whose exponent
-// reaches from 2^-16 to 2^15: three digits each, eleven bits of fp16 at most, off by 2^-10 of u or by 2^-29 of the
-// row's largest.
+// block's scale; p counts from the row's reference, so that u <= 2^15) is rounded to fp16 and cut into three e5m2 terms,
+// whose exponent reaches from 2^-16 to 2^15: three digits each, which hold an fp16 value exactly from 2^-6 on.  Off by
+// 2^-11 of u, or by 2^-29 of the row's largest.
 // The terms are columns of their own, added up at the end.
 //
 // Work is cut evenly whatever the lengths: the key tiles of all heads of all sequences are one row of tiles, and every
