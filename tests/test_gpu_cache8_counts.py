@@ -24,3 +24,14 @@ def test_counts_fit_32_bits():
     for n in (2 ** 31, 2 ** 32 + 1, -2 ** 31 - 1):
         with pytest.raises(ValueError):
             sa._count(n)
+
+
+def test_tokens_are_whole_numbers():
+    """A first token of 2.5 is not taken for 2."""
+    from video_dit_sparse_gb300 import build
+    build.build()
+    from video_dit_sparse_gb300 import binding as sa
+    assert sa._tokens(3.0, "start", 0, 1) == (0, 3)
+    for at in (2.5, -0.5, "4", float("nan")):
+        with pytest.raises(ValueError):
+            sa._tokens(at, "start", 0, 1)

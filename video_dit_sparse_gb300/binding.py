@@ -1019,10 +1019,10 @@ def _tokens(at, name, dev, B):
     """A first token given as an int or as int32 [B]: (address, int)."""
     if isinstance(at, torch.Tensor):
         return _flat(at, _i32, name, dev, (B,)), 0
-    at = int(at)
-    if not -2 ** 31 <= at < 2 ** 31:
-        raise ValueError(f"{name} must be a 32-bit number")
-    return 0, at
+    token = int(at)
+    if token != at or not -2 ** 31 <= token < 2 ** 31:
+        raise ValueError(f"{name} must be a whole 32-bit number")
+    return 0, token
 
 
 def _count(n: int) -> int:
