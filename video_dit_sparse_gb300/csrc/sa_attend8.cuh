@@ -118,6 +118,15 @@ __device__ __forceinline__ void two_terms(const uint4& u, float f, float lift, u
 // product.  As long as a run has seen empty blocks alone they set the reference like any others.
 constexpr float kEmptyBelow = 84.f;
 
+// The first of a head's scales that holds anything, of the blocks of a tile's `keys` keys from k0 on that begin ahead of
+// `end`; 0: none.  One load a lane, the warp together.
+__device__ __forceinline__ float first_scale(const float* scales, int k0, int keys, int end, int block_log2) {
+  const int lane = threadIdx.x & 31, key = k0 + (lane << block_log2);
+  const float s = lane < (keys >> block_log2) && key < end ? held_scale(__ldg(scales + (key >> block_log2))) : 0.f;
+  const uint32_t has = __ballot_sync(0xffffffffu, s > 0.f);
+  return __shfl_sync(0xffffffffu, s, has ? __ffs(has) - 1 : 0);
+}
+
 // A pair of weights as fp16; past 65504: 65504.
 __device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
   uint32_t r;

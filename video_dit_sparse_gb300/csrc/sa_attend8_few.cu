@@ -276,12 +276,10 @@ __global__ void __launch_bounds__(FCfg<D, RP>::kThreads, 1)
       for (int j = 0; j < x.n; ++j, ++c) {
         const int k0 = (x.j0 + j) * kKeys, key = k0 + t;
         const float ks = held_scale(ks_next), vs = held_scale(vs_next);
-        // (ahead of the next loads, which the loop would wait for; all threads alike)
+        // (ahead of the next loads, which this one would wait for; all threads alike)
         bool first_values = false;  // behind tiles of empty blocks alone
         if (s0 == 0.f) {
-#pragma unroll 1
-          for (int k = k0; k < min(k0 + kKeys, most) && s0 == 0.f; k += 1 << a.block_log2)
-            s0 = held_scale(__ldg(vsc + (k >> a.block_log2)));
+          s0 = first_scale(vsc, k0, kKeys, most, a.block_log2);
           if (s0 > 0.f) lref = __log2f(s0);
           first_values = j > 0 && s0 > 0.f;
         }

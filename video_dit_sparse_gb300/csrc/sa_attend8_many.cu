@@ -14,9 +14,8 @@
 // the reference m moves before a half row's sum passes 2^15: what is lost lies below 2^-31 of the row's largest.
 //
 // A V tile is cleared where no row of the unit sees it and where a block is empty (whose keys count less for the
-// reference: sa_attend8.cuh); a NaN among its codes is cleared
-// too and noted by its column: rows see the first keys of the cache, so a column's first NaN says which rows
-// get one.
+// reference: sa_attend8.cuh); a NaN among its codes is cleared too and noted by its column: rows see the first keys of the
+// cache, so a column's first NaN says which rows get one.
 //
 // Warps: sixteen softmax warps (two a row, 64 columns each), an MMA warp a tile taking turns, one for units and loads.
 // The softmax warps convert V too, a sixteenth of the next tile each behind their P, while they would wait for S
@@ -253,21 +252,16 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
       ++vc;
       return true;
     };
+    // log2 of what value scales count from, as a tile of unit x has it (of keys that some row of the unit sees).
+    auto scale_from = [&](const AUnit& x, int k0) -> float {
+      const float s = first_scale(a.v_scale + int64_t(x.b) * a.v_scales.b + int64_t(x.hk) * a.v_scales.h, k0, BN, x.uhi, a.block_log2);
+      return s > 0.f ? __log2f(s) : kNoScale;
+    };
     // The row of the next unit: keys it sees, its multiplier, what value scales count from.
     int hi_next = 0;
     float rf_next = 0.f, lref_next = 0.f;
     // The next unit's query terms into shared memory, and its first values.  (The last unit's products have read
     // the old terms: its last S is here.)
-    // log2 of the first value scale of a tile of unit x that holds anything (of keys that some row of the unit sees).
-    auto first_scale = [&](const AUnit& x, int k0) -> float {
-      const int key = k0 + (lane << a.block_log2);
-      float s = 0.f;
-      if (lane < BN >> a.block_log2 && key < x.uhi)
-        s = held_scale(__ldg(a.v_scale + int64_t(x.b) * a.v_scales.b + int64_t(x.hk) * a.v_scales.h + (key >> a.block_log2)));
-      const uint32_t has = __ballot_sync(0xffffffffu, s > 0.f);
-      s = __shfl_sync(0xffffffffu, s, has ? __ffs(has) - 1 : 0);
-      return has ? __log2f(s) : kNoScale;
-    };
     auto prepare = [&](uint32_t slot) -> bool {
       const AUnit& x = bars.ring[slot];
       hi_next = 0;
@@ -304,7 +298,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
         }
         fence_proxy_async_smem();
         arrive(&bars.qfull[t]);
-        lref_next = first_scale(x, x.key0);
+        lref_next = scale_from(x, x.key0);
       }
       return convert(slot, x.key0);
     };
@@ -328,7 +322,7 @@ __global__ void __launch_bounds__(ACfg<D>::kThreads, 1)
           // (ahead of the next load, which this one would wait for)
           bool first_values = false;  // behind tiles of empty blocks alone
           if (here && lref == kNoScale) {
-            lref = first_scale(x, k0);
+            lref = scale_from(x, k0);
             first_values = j > 0 && lref != kNoScale;
           }
           if (j + 1 < n) ahead = fetch(k0 + BN);
