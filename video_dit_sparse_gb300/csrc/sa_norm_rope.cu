@@ -164,7 +164,9 @@ __global__ void __launch_bounds__(256, 2) sa_norm_rope_kernel(const __grid_const
   const int c = threadIdx.x % LANES;
   const int64_t tok = int64_t(blockIdx.x) * kTokens + threadIdx.x / LANES;
   const bool valid = tok < r.N;
-  const int64_t n = valid ? tok : r.N - 1;  // (every lane takes part in the sums)
+  // (Every lane takes part in the sums.  Those past the last token read the last row and use none of it: in place it may be
+  // half written.  Returning early spills: 12 + 12 heads of 7040 tokens, pairs by halves, 18.7 -> 20.6 us.)
+  const int64_t n = valid ? tok : r.N - 1;
   const int b = blockIdx.z;
   const int first = blockIdx.y * heads_per_block, last = min(first + heads_per_block, r.H[0] + r.H[1]);
   int e0, e1;
@@ -247,15 +249,17 @@ __global__ void __launch_bounds__(256, 1) sa_norm_rope_grad_kernel(const __grid_
     const char* dy = static_cast<const char*>(a.g[s]) + (b * a.gs[s].b + n * a.gs[s].n) * kBytes;
     char* dx = static_cast<char*>(r.y[s]) + (b * r.ys[s].b + n * r.ys[s].n) * kBytes;
     // The thread's pieces of the next heads are on their way to places of its own in shared memory.
+    // (Past the last token: zeros.  In place, the last row is being written by its own lanes.)
+    const uint32_t bytes = valid ? 16 : 0;
     auto fetch = [&](int h) {
       if (h < h1) {
         const uint32_t to = smem_u32(ring + ((h & (kAhead - 1)) * 4) * 256 + threadIdx.x);
         const char* at = x + h * r.xs[s].h * kBytes;
-        cp_async16(to, at + e0 * kBytes, 16);
-        cp_async16(to + 4096, at + e1 * kBytes, 16);
+        cp_async16(to, at + e0 * kBytes, bytes);
+        cp_async16(to + 4096, at + e1 * kBytes, bytes);
         at = dy + h * a.gs[s].h * kBytes;
-        cp_async16(to + 8192, at + e0 * kBytes, 16);
-        cp_async16(to + 12288, at + e1 * kBytes, 16);
+        cp_async16(to + 8192, at + e0 * kBytes, bytes);
+        cp_async16(to + 12288, at + e1 * kBytes, bytes);
       }
       cp_async_commit();
     };
@@ -280,7 +284,7 @@ __global__ void __launch_bounds__(256, 1) sa_norm_rope_grad_kernel(const __grid_
       for (int e = 0; e < V / 2; ++e) {
         v0[e] = mul2(v0[e], kk);
         v1[e] = mul2(v1[e], kk);
-        if (valid) {  // (a row that is there twice counts once)
+        if (valid) {
           dw0[e] = fma2(g0[e], v0[e], dw0[e]);
           dw1[e] = fma2(g1[e], v1[e], dw1[e]);
           if (BIAS) {
